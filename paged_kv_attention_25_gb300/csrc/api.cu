@@ -10,31 +10,13 @@
 #include <vector>
 
 #include "internal.h"
+#include "pool.h"
 
 using namespace pkv;
-
-namespace pkv {
-int set_last_error(int code, const std::string& msg);
-}
 
 namespace {
 
 thread_local std::string g_err;
-
-int fail(int code, const std::string& msg) {
-  g_err = msg;
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(PKV_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
-#define PKV_CUDA(call, what)                 \
-  do {                                       \
-    cudaError_t e_ = (call);                 \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -53,119 +35,14 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-struct ProfRec {
-  int kernel;
-  cudaEvent_t a, b;
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 
-int pkv::set_last_error(int code, const std::string& msg) { return fail(code, msg); }
-
-struct pkv_pool {
-  int num_blocks = 0, block_size = 0, num_kv_heads = 0, head_dim = 0;
-  int elem_bytes = 2;                 // 2: bf16; 1: fp8 e4m3 codes
-  float k_scale = 1.f, v_scale = 1.f;
-  void* k = nullptr;
-  void* v = nullptr;
-  bool owns = false;
-  unsigned* d_err = nullptr;
-  int device = 0, num_sms = 0;
-  CUtensorMap tmap_k;  // 64-byte aligned by its type
-  CUtensorMap tmap_v;
-  CUtensorMap dmap_k;  // split-KV kernel's maps (FP8, D = 128); copies of tmap_* otherwise
-  CUtensorMap dmap_v;
-  std::mutex mu;
-  Plan plan;
-  // Pinned, double-buffered staging for work-list uploads (allocated at
-  // creation; a work list larger than one slot goes through pageable memory).
-  static constexpr size_t kStagingBytes = size_t(4) << 20;
-  uint8_t* pinned[2] = {nullptr, nullptr};
-  cudaEvent_t pinned_done[2] = {nullptr, nullptr};
-  int pinned_slot = 0;
-  std::vector<uint8_t> staging;
-  // The tensor-core kernel runs on `side`, concurrently with the split-KV
-  // kernel on the caller's stream (fork / join through the two events).
-  cudaStream_t side = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
-  // Recorded after each attention call's kernels: the next call's work-list
-  // upload waits for it before rewriting the work lists.
-  cudaEvent_t ws_free = nullptr;
-  // Device copy of the work lists, owned by the pool (kStagingBytes): the
-  // upload into it runs on the pool's copy stream, ordered after the previous
-  // call's kernels only, so it overlaps the caller's earlier work (the
-  // append, the next step's input copies) and never queues behind it.  The
-  // caller's workspace, whose memory may still be in use by work queued on
-  // the caller's stream, is written only by kernels on that stream.
-  // Two buffers, used by alternate calls (with the pinned staging slots): an
-  // upload then waits only for the call before the previous one, long done,
-  // so it is ready to run when it is submitted and does not queue on the
-  // copy engine behind transfers submitted after it (a serving loop's next
-  // inputs).
-  uint8_t* d_wl[2] = {nullptr, nullptr};
-  cudaEvent_t wl_free[2] = {nullptr, nullptr};
-  cudaStream_t copy = nullptr;
-  cudaEvent_t up_done = nullptr;
-  // Ahead-of-time swap-in: the copy engines bring the blocks into a device
-  // staging buffer on the caller's copy stream (swap_ready), and the pool's
-  // next call scatters them into place on its own stream (staged_free).
-  std::mutex swap_mu;
-  void* swap_staging = nullptr;
-  size_t swap_staging_bytes = 0;
-  cudaEvent_t swap_ready = nullptr, swap_staged_free = nullptr, swap_after = nullptr;
-  bool swap_pending = false;
-  std::vector<int32_t> swap_ids;
-
-  // Test and diagnostic settings (pkv_debug_set).
-  uint64_t wait_ns = 1000000000ull;   // limit of every bounded wait in the kernels
-  int withhold = 0;                   // see AttnArgs::withhold
-  int fused_form = 0;                 // PKV_DEBUG_FUSED_FORM
-
-  // profiling (prof_mode 2: the two attention kernels run one after the other)
-  bool prof_on = false;
-  int prof_mode = 0;
-  std::vector<cudaEvent_t> ev_free;
-  std::vector<ProfRec> pending;
-  pkv_profile totals{};
-
-  PoolView view() const {
-    return PoolView{k, v, num_blocks, num_kv_heads, head_dim, d_err, elem_bytes, k_scale, v_scale};
-  }
-  // Bytes of one physical block of K (or V): all KV heads.
-  size_t block_bytes() const { return static_cast<size_t>(num_kv_heads) * kBlockSize * head_dim * elem_bytes; }
-
-  cudaEvent_t take_event() {
-    if (ev_free.empty()) {
-      cudaEvent_t e;
-      if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
-      return e;
-    }
-    cudaEvent_t e = ev_free.back();
-    ev_free.pop_back();
-    return e;
-  }
-};
+int pkv::set_last_error(int code, const std::string& msg) {
+  g_err = msg;
+  return code;
+}
 
 namespace {
-
-// Launch `fn` on `stream`, bracketed by profiling events when profiling is on.
-template <class F>
-int timed_launch(pkv_pool* pool, int kernel, void* stream, F&& fn) {
-  cudaEvent_t a = nullptr, b = nullptr;
-  if (pool->prof_on) {
-    a = pool->take_event();
-    b = pool->take_event();
-    if (a && b) cudaEventRecord(a, static_cast<cudaStream_t>(stream));
-  }
-  const int rc = fn();
-  if (a && b) {
-    cudaEventRecord(b, static_cast<cudaStream_t>(stream));
-    pool->pending.push_back({kernel, a, b});
-  }
-  return rc;
-}
 
 // swizzle: only for FP8 pools with D = 128 (the split-KV kernel's map, whose
 // 128-byte rows land with 128-byte swizzle); the tensor-core kernel's FP8
@@ -454,11 +331,13 @@ int pkv_pool_kv_ptrs(const pkv_pool* pool, void** k, void** v) {
   return PKV_OK;
 }
 
+}  // extern "C"
+
 // Lands a pending ahead-of-time swap-in on `stream`: waits for its transfer,
 // then scatters the staged blocks into the pool (every block at full HBM
 // rate, on up to one CTA per SM).  Every call that reads or writes the pool
 // starts with this, so the blocks are in place before the call's kernels.
-static int finish_swap_in(pkv_pool* pool, void* stream) {
+int pkv::finish_swap_in(pkv_pool* pool, void* stream) {
   std::lock_guard<std::mutex> lk(pool->swap_mu);
   if (!pool->swap_pending) return PKV_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -472,6 +351,8 @@ static int finish_swap_in(pkv_pool* pool, void* stream) {
   pool->swap_pending = false;
   return PKV_OK;
 }
+
+extern "C" {
 
 int pkv_append(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
                const int32_t* positions, const void* k_new, const void* v_new, int num_tokens, void* stream) {
