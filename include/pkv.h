@@ -89,6 +89,7 @@ extern "C" {
 #define PKV_DEVERR_POSITION 2u   /* a position outside [0, max_blocks*block_size) */
 #define PKV_DEVERR_TIMEOUT 4u    /* a bounded wait inside a kernel gave up */
 #define PKV_DEVERR_INTERNAL 8u   /* a kernel found its launch configuration unusable */
+#define PKV_DEVERR_NO_PAGES 16u  /* pkv_fork found fewer free pages than it needs */
 
 typedef struct pkv_pool pkv_pool; /* opaque */
 
@@ -136,7 +137,9 @@ typedef struct {
                                (a call whose metadata equals the cached plan's builds none) */
 } pkv_plan_stats;
 
-/* Accumulated device time per kernel family while profiling is on. */
+/* Accumulated device time per kernel family while profiling is on.  The tree
+ * attention and the attention over selected blocks count as split-KV, the tree
+ * attention's merge as merge; bounds, selection and pages count as append. */
 typedef struct {
   int launches[5];          /* 0 append, 1 split-KV, 2 tensor-core, 3 merge, 4 swap */
   double total_ms[5];
@@ -293,6 +296,168 @@ int pkv_paged_attn_static(pkv_pool* pool, const void* q, int num_q_heads, const 
                           const int32_t* cu_q_lens, int num_reqs, int num_tokens,
                           const pkv_host_meta* host_meta, float scale, void* o, float* lse,
                           void* stream);
+
+/*
+ * ---- Attention for a tree of drafted tokens over the cache -----------------
+ *
+ * The drafted tokens of a request are appended like any others (pkv_append, at
+ * consecutive slots [prefix_lens[r], ctx_lens[r])), but sibling branches must
+ * not see each other.  Query token t of request r sees key slot j if
+ *   j < prefix_lens[r],  or
+ *   prefix_lens[r] <= j < ctx_lens[r] and bit j - prefix_lens[r] of tree_mask[t],
+ * and with head h, KV head g = h / (num_q_heads / num_kv_heads) and the slots S it sees
+ *   s_j = scale * q[t][h] . K_r[j][g],  m = max_S s_j
+ *   O[t][h]   = sum_S exp(s_j - m) V_r[j][g] / sum_S exp(s_j - m)
+ *   LSE[t][h] = m + ln(sum_S exp(s_j - m));   O = 0 and LSE = -inf if S is empty.
+ *   tree_mask [num_tokens][mask_words] uint32, device: bit i of a row is bit
+ *                i % 32 of word i / 32.  Bits at or beyond ctx - prefix are not
+ *                read as slots, slots at or beyond 32 mask_words are not seen.
+ *                Any pattern is allowed (a token usually sees itself and its
+ *                ancestors); the query tokens need not be all of the drafts
+ *                (a drafting step queries its newest level).
+ *   prefix_lens, ctx_lens, cu_q_lens, block_tables: device.  0 <= prefix <= ctx
+ *                <= max_blocks * 16.  num_tokens may exceed cu_q_lens[num_reqs]
+ *                (a batch padded to a fixed size): rows that belong to no
+ *                request are neither read nor written.
+ * Scores are fp32 (products of the tensor cores' bf16, or f16 for FP8 pools,
+ * operands with fp32 accumulation); P is rounded to bf16 (f16) for its product
+ * with V; O is rounded to bf16 once.  Results do not depend on timing: partial
+ * results are merged in a fixed order.
+ * Values in slots that a token does not see do not reach it, be they infinite
+ * or NaN.  An invalid block id or length is flagged in the error word; the
+ * block's keys are then seen by nobody, a length is cut to its range.
+ *
+ * All metadata is read on the device: the call plans and uploads nothing, can be
+ * captured into a graph and replayed with other lengths, tables and masks, and
+ * runs on `stream` alone (its kernels; a pending ahead-of-time swap-in lands
+ * first).  q and o 16-byte aligned.  workspace: device memory of
+ * pkv_tree_attn_workspace_size() bytes (which grows with num_reqs only), 256-byte
+ * aligned, used by one call at a time: calls that may run at the same time,
+ * graphs that may be replayed at the same time among them, need their own.
+ * num_tokens == 0 is a no-op.  Errors: PKV_EINVAL, PKV_EUNSUPPORTED, PKV_ECUDA.
+ */
+int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, size_t* bytes);
+int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* block_tables, int max_blocks,
+                  const int32_t* ctx_lens, const int32_t* prefix_lens, const int32_t* cu_q_lens, int num_reqs,
+                  int num_tokens, const uint32_t* tree_mask, int mask_words, float scale, void* o, float* lse,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Mask rows from parents: parents[cu_q_lens[r] + i] is the index, within the
+ * request's tree, of node i's parent (below i; -1: a child of the prefix).
+ * Sets bit i and the bits of all ancestors in row cu_q_lens[r] + i of tree_mask,
+ * and clears the others.  A parent outside [-1, i) ends the walk, and a node
+ * index without a word is left out; both set PKV_DEVERR_POSITION.  Rows of
+ * tokens that belong to no request are left as they are. */
+int pkv_tree_mask(pkv_pool* pool, const int32_t* parents, const int32_t* cu_q_lens, int num_reqs, int num_tokens,
+                  uint32_t* tree_mask, int mask_words, void* stream);
+
+/*
+ * ---- Attention over blocks that a cheap score selects ----------------------
+ *
+ * Bounds: for every (physical block, KV head) the largest and smallest value of
+ * each channel over the block's written keys, in 8-bit codes of a power of two:
+ *   codes [num_blocks][num_kv_heads][2][head_dim] int8, exps [num_blocks][num_kv_heads] int8
+ *   codes[..][0][d] = ceil(max_j K_j[d] / 2^e),  codes[..][1][d] = floor(min_j K_j[d] / 2^e)
+ * with e = exps[..] the smallest exponent >= -126 for which every |K_j[d]| <= 127 * 2^e
+ * (FP8 pools: K_j in codes' values, without k_scale).  NaN counts as absent, an
+ * infinity as the largest finite bf16.  The arrays belong to the caller
+ * (device, codes 16-byte aligned).
+ *
+ * pkv_summarize recomputes the bounds of every block that holds one of the
+ * given positions (the arguments of pkv_append, plus ctx_lens: keys at or
+ * beyond ctx_lens[r] are not counted).  Call it after the append with the same
+ * positions; after a swap-in with one position per block.  Tokens that share
+ * a block with the token before them cost nothing.
+ */
+int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
+                  const int32_t* positions, const int32_t* ctx_lens, int num_tokens, int8_t* codes, int8_t* exps,
+                  void* stream);
+
+/*
+ * For every query token t at position p = q_positions[t] and KV head g: the
+ * top_k of the blocks 0 .. p / 16 of its request, in ascending order, -1 beyond them:
+ *   selected [num_tokens][num_kv_heads][top_k] int32 (indexes into the request's block table)
+ * The first `sinks` and the last `recent` blocks come first; then the blocks with the largest
+ *   score(b) = 2^e * sum_d (P_d codes[b][g][0][d] + N_d codes[b][g][1][d]),
+ * ties to the lower index, where P_d = sum_h max(i_hd, 0), N_d = sum_h min(i_hd, 0) over the
+ * group's heads h, i_hd = round-to-even(q_hd / 2^f), f the smallest exponent with
+ * |q_hd| <= floor(32767 / G) * 2^f for the whole group.  The sum is an exact 32-bit
+ * integer, rounded to fp32 once, and the product one of fp32 (exact but for scores
+ * outside its normal range); it bounds sum_h i_h . K_j from above for every key
+ * j of the block.  (q elements that are not finite, and a group whose largest
+ * element is below 2^-100, count as 0.)  So the selection depends on the
+ * inputs alone, not on the order of any sum.
+ * Rows of tokens that belong to no request are left as they are.  A block
+ * without a valid pool block is flagged and not selected; a position outside
+ * the table is flagged and selects nothing.  max_blocks <= 393216 (6.29 M tokens).
+ */
+int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
+                      const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs,
+                      int num_tokens, const int8_t* codes, const int8_t* exps, int top_k, int sinks, int recent,
+                      int32_t* selected, void* stream);
+
+/*
+ * Attention of each query token over the keys j <= p of its selected blocks
+ * (formulas and rounding as above; blocks of one list must be distinct, in any
+ * order; entries below 0 and blocks behind the token are skipped, an entry beyond
+ * the table is flagged and skipped).  A list without a key gives O = 0,
+ * LSE = -inf.  The split over a cluster of CTAs is merged through their shared
+ * memory: no workspace.
+ * Both calls read all metadata on the device, can be captured into a graph and
+ * run on `stream` alone.
+ */
+int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
+                    const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs, int num_tokens,
+                    const int32_t* selected, int top_k, float scale, void* o, float* lse, void* stream);
+
+/*
+ * ---- Pages: sharing, copying, allocating and freeing on the device ----------
+ *
+ * refs [num_blocks] int32 (device, the caller's) counts the owners of every
+ * page (physical block): table rows, or anyone else who raised it; a page with
+ * count 0 is free.  pkv_fork makes the next generation of sequences:
+ *   - old rows tables [num_rows][max_blocks] with lens[r] tokens each, holding
+ *     pages for caps[r] >= lens[r] tokens (ceil(caps[r] / 16) entries);
+ *   - child i continues row parents[i] (-1: an empty sequence) and gets pages for
+ *     max(new_caps[i], tokens it inherits) tokens:
+ *     new_tables [num_children][max_blocks], -1 beyond its pages.
+ * Every old row gives up its pages; each child takes its parent's full pages.
+ * The page that lens[r] fills in part passes to the row's lowest child if no
+ * one else owns it; every other child gets a fresh page with a copy of its
+ * tokens (K, V, and its bounds if codes and exps are given).  Fresh pages are
+ * the lowest-numbered ones without an owner, in the order of children and of
+ * positions; pages freed by this call are among them, except those it copies
+ * from.  Rows without children are thereby freed, num_children = 0 frees all,
+ * num_rows = 0 starts new sequences, one child with a larger cap grows a row.
+ * new_refs receives the counts (new_refs == refs: in place); new_tables must not
+ * overlap tables.  If too few pages are free PKV_DEVERR_NO_PAGES is set and the
+ * entries left over are -1 (their copies do not happen).  Invalid lengths, parents and
+ * page ids are flagged; a bad parent counts as -1, a bad id is not counted.
+ * workspace: pkv_fork_workspace_size() bytes, 16-byte aligned, one call at a time.
+ */
+int pkv_fork_workspace_size(pkv_pool* pool, int num_rows, int num_children, size_t* bytes);
+int pkv_fork(pkv_pool* pool, const int32_t* tables, int num_rows, int max_blocks, const int32_t* lens,
+             const int32_t* caps, const int32_t* parents, const int32_t* new_caps, int num_children,
+             int32_t* new_tables, const int32_t* refs, int32_t* new_refs, int8_t* codes, int8_t* exps, void* workspace,
+             size_t workspace_bytes, void* stream);
+
+/* Copies whole pages src[i] -> dst[i] (device arrays): K, V, and the bounds if
+ * given.  dst ids are distinct and none of them is a source.  An id outside the
+ * pool is flagged and its pair skipped. */
+int pkv_copy_blocks(pkv_pool* pool, const int32_t* src, const int32_t* dst, int n, int8_t* codes, int8_t* exps,
+                    void* stream);
+
+/*
+ * Moves kept tokens together (after a drafted tree has been verified): for
+ * request r the K and V rows at src_positions[cu_keep[r] + i] go to position
+ * dst_starts[r] + i, all KV heads.  Sources ascend strictly and lie at or behind
+ * their targets (the kept nodes of a tree, in order, moved to the prefix's
+ * end); a source that does not is flagged and left where it is.  The requests'
+ * pages at the targets must be their own.  Bounds of the blocks written are
+ * the caller's to recompute (pkv_summarize).  All arrays device.
+ */
+int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_keep,
+                const int32_t* src_positions, const int32_t* dst_starts, int num_kept, void* stream);
 
 /* Statistics of the last plan built on this pool. */
 int pkv_last_plan_stats(const pkv_pool* pool, pkv_plan_stats* out);

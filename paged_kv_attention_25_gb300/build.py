@@ -18,8 +18,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
-SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_append.cu", "attn_static.cu", "swap.cu"]
-HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh"]
+SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_append.cu", "attn_static.cu", "swap.cu",
+           "ops_api.cu", "tree.cu", "sparse.cu", "pages.cu"]
+HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh", "ops.h", "rows.cuh", "sched.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

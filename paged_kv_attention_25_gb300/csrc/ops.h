@@ -1,0 +1,73 @@
+// Launchers of the operators beside the causal paged attention (tree
+// attention, block-selected attention, pages); they return cudaError_t as int.
+#pragma once
+#include "internal.h"
+
+namespace pkv {
+
+struct TreeArgs;
+
+// CTAs of a tree-attention launch at most, and the partial rows of its workspace.
+int tree_ctas(const PoolView& pool, int num_sms);
+size_t tree_part_rows(int ctas);
+// tmk / tmv: the pool's block maps (128-byte swizzle; unused by FP8 pools with head_dim 64).
+int launch_tree(const TreeArgs& a, const void* tmk, const void* tmv, void* stream);
+int launch_tree_merge(const TreeArgs& a, void* stream);
+int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
+                     unsigned* err, void* stream);
+
+// One call over selected blocks (pkv_summarize, pkv_select_blocks, pkv_sparse_attn).
+struct SparseArgs {
+  PoolView pool;
+  const void* q;
+  int num_q_heads, group;
+  const int32_t* positions;
+  const int32_t* block_tables;
+  int max_blocks;
+  const int32_t* cu_q_lens;
+  const int32_t* ctx_lens;
+  int num_reqs, num_tokens;
+  int8_t* codes;     // [blocks][kv heads][2][D]: upper, lower
+  int8_t* exps;      // [blocks][kv heads]
+  int32_t* sel;      // [tokens][kv heads][top_k]
+  int top_k, sinks, recent;
+  float scale_log2;
+  void* o;
+  float* lse;
+  uint64_t wait_ns;
+  int num_sms;
+};
+int launch_summarize(const SparseArgs& a, void* stream);
+// Blocks of a table row that the selection can take (its scores stay in shared memory).
+int select_max_blocks();
+int launch_select(const SparseArgs& a, void* stream);
+int launch_sparse(const SparseArgs& a, const void* tmk, const void* tmv, void* stream);
+
+// pkv_fork.
+struct ForkArgs {
+  PoolView pool;
+  void* kp;
+  void* vp;
+  const int32_t* tables;
+  int num_rows, max_blocks;
+  const int32_t* lens;
+  const int32_t* caps;
+  const int32_t* parents;
+  const int32_t* new_caps;
+  int num_children;
+  int32_t* new_tables;
+  const int32_t* refs;
+  int32_t* new_refs;
+  int8_t* codes;      // summaries to copy along, or nullptr
+  int8_t* exps;
+  int32_t* ws;        // fork_ws_ints() ints
+  int num_sms;
+};
+size_t fork_ws_ints(int num_blocks, int num_rows, int num_children);
+int launch_fork(const ForkArgs& a, void* stream);
+int launch_copy_blocks(const PoolView& pool, void* kp, void* vp, const int32_t* src, const int32_t* dst, int n,
+                       int8_t* codes, int8_t* exps, void* stream);
+int launch_compact(const PoolView& pool, void* kp, void* vp, const int32_t* block_tables, int max_blocks, int num_reqs,
+                   const int32_t* cu_keep, const int32_t* src, const int32_t* dst, int num_kept, void* stream);
+
+}  // namespace pkv

@@ -1,0 +1,341 @@
+// C entry points of the operators beside the causal paged attention: tree
+// attention, block-selected attention, pages.  Their lengths, tables and masks
+// are read on the device alone, so that the calls can be captured in a graph;
+// they take no lock, keep nothing from one call for the next, and run on the
+// caller's stream.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "ops.h"
+#include "pool.h"
+#include "sched.cuh"
+
+using namespace pkv;
+
+namespace {
+
+// Makes the pool's device current for a call's launches.
+class DeviceGuard {
+ public:
+  explicit DeviceGuard(int device) {
+    if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = device;
+    if (prev_ != device) cudaSetDevice(device);
+    device_ = device;
+  }
+  ~DeviceGuard() {
+    if (prev_ != device_) cudaSetDevice(prev_);
+  }
+  DeviceGuard(const DeviceGuard&) = delete;
+  DeviceGuard& operator=(const DeviceGuard&) = delete;
+
+ private:
+  int prev_ = 0, device_ = 0;
+};
+
+int check_tables(int max_blocks, int num_reqs, int num_tokens) {
+  if (num_tokens < 0 || num_reqs < 0) return fail(PKV_EINVAL, "negative size");
+  if (num_tokens == 0) return PKV_OK;
+  if (num_reqs < 1 || max_blocks < 1) return fail(PKV_EINVAL, "num_reqs and max_blocks must be >= 1");
+  if (static_cast<int64_t>(max_blocks) * kBlockSize >= (1ll << 31) - kBlockSize) return fail(PKV_EINVAL, "max_blocks too large");
+  return PKV_OK;
+}
+
+int check_heads(const pkv_pool* pool, int num_q_heads) {
+  if (num_q_heads < 1 || num_q_heads % pool->num_kv_heads)
+    return fail(PKV_EINVAL, "num_q_heads must be a multiple of num_kv_heads");
+  if (num_q_heads / pool->num_kv_heads > kTcRows) return fail(PKV_EUNSUPPORTED, "group size above 128");
+  return PKV_OK;
+}
+
+int check_scale(float scale) {
+  return scale > 0.f && scale <= 3.4e38f ? PKV_OK : fail(PKV_EINVAL, "scale must be positive and finite");
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct TreeWs {
+  size_t offs, part_o, part_lse, total;
+};
+TreeWs tree_ws(const pkv_pool* pool, int num_reqs) {
+  const size_t rows = tree_part_rows(tree_ctas(pool->view(), pool->num_sms));
+  TreeWs w;
+  w.offs = 0;
+  w.part_o = align256((static_cast<size_t>(num_reqs) + 1) * sizeof(int64_t));
+  w.part_lse = w.part_o + align256(rows * pool->head_dim * sizeof(float));
+  w.total = w.part_lse + align256(rows * sizeof(float));
+  return w;
+}
+
+// The maps whose copies land with the 128-byte swizzle that rows.cuh reads.
+const CUtensorMap* rows_map(const pkv_pool* pool, bool v) {
+  return pool->elem_bytes == 1 ? (v ? &pool->dmap_v : &pool->dmap_k) : (v ? &pool->tmap_v : &pool->tmap_k);
+}
+
+int check_summary(const pkv_pool* pool, const void* codes, const void* exps) {
+  (void)pool;
+  if (!codes || !exps) return fail(PKV_EINVAL, "NULL summary arrays");
+  if (!aligned16(codes)) return fail(PKV_EINVAL, "summary codes must be 16-byte aligned");
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_tree_mask(pkv_pool* pool, const int32_t* parents, const int32_t* cu_q_lens, int num_reqs, int num_tokens,
+                  uint32_t* tree_mask, int mask_words, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (num_tokens < 0 || num_reqs < 0) return fail(PKV_EINVAL, "negative size");
+  if (num_tokens == 0) return PKV_OK;
+  if (num_reqs < 1) return fail(PKV_EINVAL, "num_reqs must be >= 1");
+  if (mask_words < 1) return fail(PKV_EINVAL, "mask_words must be >= 1");
+  if (!parents || !cu_q_lens || !tree_mask) return fail(PKV_EINVAL, "NULL device pointer");
+  DeviceGuard guard(pool->device);
+  const int rc = launch_tree_mask(parents, cu_q_lens, num_reqs, num_tokens, tree_mask, mask_words, pool->d_err, stream);
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree mask launch");
+  return PKV_OK;
+}
+
+int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, size_t* bytes) {
+  if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
+  const int rc = check_heads(pool, num_q_heads);
+  if (rc) return rc;
+  if (num_reqs < 0) return fail(PKV_EINVAL, "negative size");
+  *bytes = tree_ws(pool, num_reqs).total;
+  return PKV_OK;
+}
+
+int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* block_tables, int max_blocks,
+                  const int32_t* ctx_lens, const int32_t* prefix_lens, const int32_t* cu_q_lens, int num_reqs,
+                  int num_tokens, const uint32_t* tree_mask, int mask_words, float scale, void* o, float* lse,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc || num_tokens == 0) return rc;
+  if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
+  if (!q || !block_tables || !ctx_lens || !prefix_lens || !cu_q_lens || !tree_mask || !o)
+    return fail(PKV_EINVAL, "NULL device pointer");
+  if (mask_words < 1) return fail(PKV_EINVAL, "mask_words must be >= 1");
+  if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
+  if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
+  const TreeWs w = tree_ws(pool, num_reqs);
+  if (!workspace || workspace_bytes < w.total)
+    return fail(PKV_EINVAL, "workspace missing or smaller than pkv_tree_attn_workspace_size()");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_EINVAL, "workspace must be 256-byte aligned");
+  DeviceGuard guard(pool->device);
+  if ((rc = finish_swap_in(pool, stream))) return rc;
+  TreeArgs a;
+  a.pool = pool->view();
+  a.q = q;
+  a.num_q_heads = num_q_heads;
+  a.group = num_q_heads / pool->num_kv_heads;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = ctx_lens;
+  a.prefix_lens = prefix_lens;
+  a.cu_q_lens = cu_q_lens;
+  a.num_reqs = num_reqs;
+  a.num_tokens = num_tokens;
+  a.mask = tree_mask;
+  a.mask_words = mask_words;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = o;
+  a.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.offs = reinterpret_cast<int64_t*>(ws + w.offs);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  a.ctas = tree_ctas(a.pool, pool->num_sms);
+  a.wait_ns = pool->wait_ns;
+  rc = timed_launch(pool, 1, stream, [&] { return launch_tree(a, rows_map(pool, false), rows_map(pool, true), stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree attention launch");
+  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree merge launch");
+  return PKV_OK;
+}
+
+int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
+                  const int32_t* positions, const int32_t* ctx_lens, int num_tokens, int8_t* codes, int8_t* exps,
+                  void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc || num_tokens == 0) return rc;
+  if (!block_tables || !cu_q_lens || !positions || !ctx_lens) return fail(PKV_EINVAL, "NULL device pointer");
+  if ((rc = check_summary(pool, codes, exps))) return rc;
+  if (static_cast<int64_t>(num_tokens) * pool->num_kv_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many rows");
+  DeviceGuard guard(pool->device);
+  if ((rc = finish_swap_in(pool, stream))) return rc;
+  SparseArgs a{};
+  a.pool = pool->view();
+  a.positions = positions;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.cu_q_lens = cu_q_lens;
+  a.ctx_lens = ctx_lens;
+  a.num_reqs = num_reqs;
+  a.num_tokens = num_tokens;
+  a.codes = codes;
+  a.exps = exps;
+  a.num_sms = pool->num_sms;
+  rc = timed_launch(pool, 0, stream, [&] { return launch_summarize(a, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "summarize launch");
+  return PKV_OK;
+}
+
+int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
+                      const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs,
+                      int num_tokens, const int8_t* codes, const int8_t* exps, int top_k, int sinks, int recent,
+                      int32_t* selected, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc) return rc;
+  if (top_k < 1 || sinks < 0 || recent < 0) return fail(PKV_EINVAL, "need top_k >= 1, sinks >= 0, recent >= 0");
+  if (num_tokens == 0) return PKV_OK;
+  if ((rc = check_heads(pool, num_q_heads))) return rc;
+  if (!q || !q_positions || !block_tables || !cu_q_lens || !selected) return fail(PKV_EINVAL, "NULL device pointer");
+  if (!aligned16(q)) return fail(PKV_EINVAL, "q must be 16-byte aligned");
+  if ((rc = check_summary(pool, codes, exps))) return rc;
+  if (max_blocks > select_max_blocks())
+    return fail(PKV_EUNSUPPORTED, "max_blocks above " + std::to_string(select_max_blocks()));
+  if (static_cast<int64_t>(num_tokens) * pool->num_kv_heads * 8 >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many rows");
+  DeviceGuard guard(pool->device);
+  SparseArgs a{};
+  a.pool = pool->view();
+  a.q = q;
+  a.num_q_heads = num_q_heads;
+  a.group = num_q_heads / pool->num_kv_heads;
+  a.positions = q_positions;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.cu_q_lens = cu_q_lens;
+  a.num_reqs = num_reqs;
+  a.num_tokens = num_tokens;
+  a.codes = const_cast<int8_t*>(codes);
+  a.exps = const_cast<int8_t*>(exps);
+  a.sel = selected;
+  a.top_k = top_k;
+  a.sinks = std::min(sinks, max_blocks);
+  a.recent = std::min(recent, max_blocks);
+  a.num_sms = pool->num_sms;
+  rc = timed_launch(pool, 0, stream, [&] { return launch_select(a, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block selection launch");
+  return PKV_OK;
+}
+
+int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
+                    const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs, int num_tokens,
+                    const int32_t* selected, int top_k, float scale, void* o, float* lse, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc) return rc;
+  if (top_k < 1) return fail(PKV_EINVAL, "top_k must be >= 1");
+  if (num_tokens == 0) return PKV_OK;
+  if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
+  if (!q || !q_positions || !block_tables || !cu_q_lens || !selected || !o) return fail(PKV_EINVAL, "NULL device pointer");
+  if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
+  if (static_cast<int64_t>(num_tokens) * num_q_heads * 8 >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
+  DeviceGuard guard(pool->device);
+  if ((rc = finish_swap_in(pool, stream))) return rc;
+  SparseArgs a{};
+  a.pool = pool->view();
+  a.q = q;
+  a.num_q_heads = num_q_heads;
+  a.group = num_q_heads / pool->num_kv_heads;
+  a.positions = q_positions;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.cu_q_lens = cu_q_lens;
+  a.num_reqs = num_reqs;
+  a.num_tokens = num_tokens;
+  a.sel = const_cast<int32_t*>(selected);
+  a.top_k = top_k;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = o;
+  a.lse = lse;
+  a.wait_ns = pool->wait_ns;
+  a.num_sms = pool->num_sms;
+  rc = timed_launch(pool, 1, stream, [&] { return launch_sparse(a, rows_map(pool, false), rows_map(pool, true), stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected attention launch");
+  return PKV_OK;
+}
+
+int pkv_fork_workspace_size(pkv_pool* pool, int num_rows, int num_children, size_t* bytes) {
+  if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
+  if (num_rows < 0 || num_children < 0) return fail(PKV_EINVAL, "negative size");
+  *bytes = align256(fork_ws_ints(pool->num_blocks, num_rows, num_children) * sizeof(int32_t));
+  return PKV_OK;
+}
+
+int pkv_fork(pkv_pool* pool, const int32_t* tables, int num_rows, int max_blocks, const int32_t* lens,
+             const int32_t* caps, const int32_t* parents, const int32_t* new_caps, int num_children,
+             int32_t* new_tables, const int32_t* refs, int32_t* new_refs, int8_t* codes, int8_t* exps, void* workspace,
+             size_t workspace_bytes, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (num_rows < 0 || num_children < 0) return fail(PKV_EINVAL, "negative size");
+  if (max_blocks < 1 || static_cast<int64_t>(max_blocks) * kBlockSize >= (1ll << 31) - kBlockSize)
+    return fail(PKV_EINVAL, "max_blocks must be >= 1 and leave positions below 2^31");
+  if ((num_rows > 0 && (!tables || !lens || !caps)) || (num_children > 0 && (!parents || !new_caps || !new_tables)) ||
+      !refs || !new_refs)
+    return fail(PKV_EINVAL, "NULL device pointer");
+  if (num_rows > 0 && num_children > 0) {
+    // A child's row is written while other children still read their parent's.
+    const uintptr_t t0 = reinterpret_cast<uintptr_t>(tables), n0 = reinterpret_cast<uintptr_t>(new_tables);
+    const uintptr_t tb = static_cast<uintptr_t>(num_rows) * max_blocks * 4, nb = static_cast<uintptr_t>(num_children) * max_blocks * 4;
+    if (t0 < n0 + nb && n0 < t0 + tb) return fail(PKV_EINVAL, "new_tables must not overlap tables");
+  }
+  if ((codes == nullptr) != (exps == nullptr)) return fail(PKV_EINVAL, "give both summary arrays or neither");
+  if (codes && !aligned16(codes)) return fail(PKV_EINVAL, "summary codes must be 16-byte aligned");
+  const size_t need = fork_ws_ints(pool->num_blocks, num_rows, num_children) * sizeof(int32_t);
+  if (!workspace || workspace_bytes < need)
+    return fail(PKV_EINVAL, "workspace missing or smaller than pkv_fork_workspace_size()");
+  if (reinterpret_cast<uintptr_t>(workspace) & 15u) return fail(PKV_EINVAL, "workspace must be 16-byte aligned");
+  DeviceGuard guard(pool->device);
+  int rc = finish_swap_in(pool, stream);
+  if (rc) return rc;
+  ForkArgs a{pool->view(), pool->k, pool->v, tables, num_rows, max_blocks, lens, caps, parents, new_caps, num_children,
+             new_tables, refs, new_refs, codes, exps, static_cast<int32_t*>(workspace), pool->num_sms};
+  rc = timed_launch(pool, 0, stream, [&] { return launch_fork(a, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "fork launch");
+  return PKV_OK;
+}
+
+int pkv_copy_blocks(pkv_pool* pool, const int32_t* src, const int32_t* dst, int n, int8_t* codes, int8_t* exps,
+                    void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (n < 0) return fail(PKV_EINVAL, "negative count");
+  if (n == 0) return PKV_OK;
+  if (!src || !dst) return fail(PKV_EINVAL, "NULL device pointer");
+  if ((codes == nullptr) != (exps == nullptr)) return fail(PKV_EINVAL, "give both summary arrays or neither");
+  if (codes && !aligned16(codes)) return fail(PKV_EINVAL, "summary codes must be 16-byte aligned");
+  DeviceGuard guard(pool->device);
+  int rc = finish_swap_in(pool, stream);
+  if (rc) return rc;
+  rc = timed_launch(pool, 0, stream, [&] {
+    return launch_copy_blocks(pool->view(), pool->k, pool->v, src, dst, n, codes, exps, stream);
+  });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block copy launch");
+  return PKV_OK;
+}
+
+int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_keep,
+                const int32_t* src_positions, const int32_t* dst_starts, int num_kept, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_kept);
+  if (rc || num_kept == 0) return rc;
+  if (!block_tables || !cu_keep || !src_positions || !dst_starts) return fail(PKV_EINVAL, "NULL device pointer");
+  if (static_cast<int64_t>(num_reqs) * pool->num_kv_heads * pool->head_dim >= (1ll << 31))
+    return fail(PKV_EUNSUPPORTED, "too many rows");
+  DeviceGuard guard(pool->device);
+  if ((rc = finish_swap_in(pool, stream))) return rc;
+  rc = timed_launch(pool, 0, stream, [&] {
+    return launch_compact(pool->view(), pool->k, pool->v, block_tables, max_blocks, num_reqs, cu_keep, src_positions,
+                          dst_starts, num_kept, stream);
+  });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "compact launch");
+  return PKV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,344 @@
+// Attention of up to 16 query rows on the warp-level MMA (mma.sync m16n8k16,
+// fp32 accumulation), one 16-key block of the pool at a time: the core that
+// the tree and the block-selected attention share.
+//
+// One warp holds its rows' queries as A fragments in registers, streams
+// (block, KV head) chunks of K and V from a shared-memory ring that TMA fills,
+// and keeps the rows' online softmax (running max m, sum l, fp32 accumulator
+// o).  Thread t = 4g + c (g = t / 4, c = t % 4) owns rows g and g + 8.
+//
+//   S = Q K^T     16 rows x 16 keys: two n-tiles of 8 keys, D / 16 k-steps
+//   O += P V      D / 8 n-tiles of 8 dims, one k-step of 16 keys
+//
+// bf16 pools: the chunk lands through the pool's tensor map (128-byte lines,
+// 16-byte chunk x of line r at x ^ (r % 8)) and ldmatrix reads the fragments
+// without bank conflicts; P is rounded to bf16 (half a step is 2^-9, and the
+// errors of different keys are independent: smaller than O's own rounding).
+//
+// FP8 pools: operands are f16 (every e4m3 value is an f16 value).  The dims of
+// S's k-steps and of O's n-tiles are permuted so that a thread reads whole
+// 16-byte pieces of codes: k-step s holds dims (D/4) c + 4 s .. + 3, n-tile j's
+// column x is dim (D/8) x + j.  P is rounded to f16.
+//
+// Rows see a 16-bit mask of each block's keys; a block that every row sees
+// whole skips the masks.  A masked key must not reach a row as 0 * inf: where
+// all rows see the same keys (kMaskKeys) the other keys' V rows are read as
+// zero; where rows differ (kMaskRows) V elements that are not finite are read
+// as zero, and the caller adds them to the rows that do see them (see `odd`).
+#pragma once
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace pkv {
+
+constexpr int kRowTile = 16;    // query rows of a warp's tile
+constexpr int kRowWarps = 4;    // warps of a CTA, each with its own blocks and state
+constexpr int kMaskNone = 0, kMaskRows = 1, kMaskKeys = 2;
+
+template <int D, bool F8>
+struct RowsSmem {
+  static constexpr int kStages = F8 ? 4 : 2;                     // per-warp ring depth
+  static constexpr int kChunk = kBlockSize * D * (F8 ? 1 : 2);   // one (block, head) of K or V
+  static constexpr int kStage = 2 * kChunk;
+  static constexpr int kRing = kRowWarps * kStages * kStage;
+  // The warps' states are merged in the ring once it has drained.
+  static constexpr int kMergeRow = D + 4;                        // o, m, l, pad (floats)
+  static constexpr int kMerge = kRowWarps * kRowTile * kMergeRow * 4;
+  static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kTotal = kBuf + kRowWarps * kStages * 8 + 64 + 1024;   // + barriers, flags, alignment
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
+}
+// d += A B, 16 x 8 x 16, fp32 accumulation.
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The pair with elements that are not finite replaced by zero; `odd` is set if there was one.
+template <bool F16>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& odd) {
+  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+  if ((w & kExp) == kExp) { w &= 0xffff0000u; odd = true; }
+  if ((w & (kExp << 16)) == (kExp << 16)) { w &= 0x0000ffffu; odd = true; }
+  return w;
+}
+
+template <int D, bool F8>
+struct RowTile {
+  static constexpr int kSteps = D / 16;    // k-steps of S
+  static constexpr int kTiles = D / 8;     // n-tiles of O
+  uint32_t q[kSteps][4];
+  float o[kTiles][4];
+  float m[2], l[2];    // rows g and g + 8; l is this thread's share of the sum
+  bool odd;            // kMaskRows: a V element that is not finite was left out
+
+  // q0, q1: rows g and g + 8 of the tile ([D] bf16), nullptr for a row that is not there.
+  __device__ __forceinline__ void init(const uint16_t* q0, const uint16_t* q1, int lane) {
+    const int c = lane & 3;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      // Element pairs of the k-step that this thread holds (see the layouts above).
+      const int d0 = F8 ? (D / 4) * c + 4 * s : 16 * s + 2 * c;
+      const int d1 = F8 ? d0 + 2 : d0 + 8;
+      uint32_t w[4];
+      w[0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d0)) : 0u;
+      w[1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d0)) : 0u;
+      w[2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d1)) : 0u;
+      w[3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d1)) : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q[s][i] = F8 ? pack_f16x2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i])) : w[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m[0] = m[1] = -CUDART_INF_F;
+    l[0] = l[1] = 0.f;
+    odd = false;
+  }
+
+  // One block: its K and V chunks at shared addresses kb and vb.  sl2: score
+  // scale times log2(e).  Masked: vis0 / vis1 hold the keys that rows g and
+  // g + 8 see.
+  template <int MASK>
+  __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, float sl2, uint32_t vis0, uint32_t vis1, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    float s[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+    if constexpr (!F8) {
+      // Lane l addresses line (l / 16) * 8 + l % 8, 16-byte chunk 2 s + (l / 8) % 2.
+      const int r8 = lane & 7, key8 = lane >> 4, cx = (lane >> 3) & 1;
+      const uint32_t base = kb + key8 * (D / 64) * 1024 + r8 * 128;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const int ch = 2 * st + cx;
+        uint32_t b0, b1, b2, b3;
+        ldsm4(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), b0, b1, b2, b3);
+        mma16<false>(s[0], q[st], b0, b1);
+        mma16<false>(s[1], q[st], b2, b3);
+      }
+    } else {
+      // Keys g and g + 8: D / 4 codes from dim (D / 4) c.
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          uint4 x;
+          ld_codes(kb, g + 8 * t, (D / 64) * c + u, x);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16x4(w[i], b0, b1);
+            mma16<true>(s[t], q[4 * u + i], b0, b1);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[t][e] *= sl2;
+        if constexpr (MASK != kMaskNone) {
+          const uint32_t v = e < 2 ? vis0 : vis1;
+          if (!((v >> (8 * t + 2 * c + (e & 1))) & 1u)) s[t][e] = -CUDART_INF_F;
+        }
+      }
+    float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+    float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+    }
+    const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
+    if (__any_sync(0xffffffffu, n0 > m[0] || n1 > m[1])) {
+      // A row's max grew: rescale (rows without a visible key so far keep m = -inf and o = 0).
+      const float a0 = n0 == -CUDART_INF_F ? 1.f : fast_exp2(m[0] - n0);
+      const float a1 = n1 == -CUDART_INF_F ? 1.f : fast_exp2(m[1] - n1);
+      l[0] *= a0;
+      l[1] *= a1;
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        o[j][0] *= a0; o[j][1] *= a0;
+        o[j][2] *= a1; o[j][3] *= a1;
+      }
+      m[0] = n0;
+      m[1] = n1;
+    }
+    const float u0 = m[0] == -CUDART_INF_F ? 0.f : m[0], u1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t][0] = fast_exp2(s[t][0] - u0);
+      s[t][1] = fast_exp2(s[t][1] - u0);
+      s[t][2] = fast_exp2(s[t][2] - u1);
+      s[t][3] = fast_exp2(s[t][3] - u1);
+    }
+    l[0] += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
+    l[1] += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+    uint32_t p[4];
+    if constexpr (F8) {
+      p[0] = pack_f16x2(s[0][0], s[0][1]); p[1] = pack_f16x2(s[0][2], s[0][3]);
+      p[2] = pack_f16x2(s[1][0], s[1][1]); p[3] = pack_f16x2(s[1][2], s[1][3]);
+    } else {
+      p[0] = pack_bf16x2(s[0][0], s[0][1]); p[1] = pack_bf16x2(s[0][2], s[0][3]);
+      p[2] = pack_bf16x2(s[1][0], s[1][1]); p[3] = pack_bf16x2(s[1][2], s[1][3]);
+    }
+    // kMaskKeys: the halves of b0 / b1 that hold seen keys (2c, 2c + 1 and 2c + 8, 2c + 9).
+    uint32_t k01 = 0xffffffffu, k89 = 0xffffffffu;
+    if constexpr (MASK == kMaskKeys) {
+      const uint32_t v = vis0 >> (2 * c);
+      k01 = ((v & 1u) ? 0xffffu : 0u) | ((v & 2u) ? 0xffff0000u : 0u);
+      k89 = ((v & 0x100u) ? 0xffffu : 0u) | ((v & 0x200u) ? 0xffff0000u : 0u);
+    }
+    if constexpr (!F8) {
+      // Lane l addresses line ((l / 8) % 2) * 8 + l % 8, chunk j + l / 16; transposed on the way.
+      const int r8 = lane & 7, key8 = (lane >> 3) & 1, cx = lane >> 4;
+      const uint32_t base = vb + key8 * (D / 64) * 1024 + r8 * 128;
+#pragma unroll
+      for (int j = 0; j < kTiles; j += 2) {
+        const int ch = j + cx;
+        uint32_t b0, b1, b2, b3;
+        ldsm4_t(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), b0, b1, b2, b3);
+        if constexpr (MASK == kMaskRows) {
+          b0 = finite_pair<false>(b0, odd); b1 = finite_pair<false>(b1, odd);
+          b2 = finite_pair<false>(b2, odd); b3 = finite_pair<false>(b3, odd);
+        } else if constexpr (MASK == kMaskKeys) {
+          b0 &= k01; b1 &= k89;
+          b2 &= k01; b3 &= k89;
+        }
+        mma16<false>(o[j], p, b0, b1);
+        mma16<false>(o[j + 1], p, b2, b3);
+      }
+    } else {
+      // Keys 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 codes from dim (D / 8) g; a byte
+      // permute pairs two keys' codes of one dim before the conversion.
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = 2 * c + (k & 1) + 8 * (k >> 1);
+        if constexpr (D == 128) {
+          uint4 x;
+          ld_codes(vb, key, g, x);
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1])
+                       : "r"(vb + key * D + 8 * g) : "memory");
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {   // word i: n-tiles 4 i .. 4 i + 3
+        const uint32_t x01 = __byte_perm(v[0][i], v[1][i], 0x5140), y01 = __byte_perm(v[0][i], v[1][i], 0x7362);
+        const uint32_t x89 = __byte_perm(v[2][i], v[3][i], 0x5140), y89 = __byte_perm(v[2][i], v[3][i], 0x7362);
+        uint32_t b[8];
+        e4m3x4_to_f16x4(x01, b[0], b[2]);
+        e4m3x4_to_f16x4(x89, b[1], b[3]);
+        e4m3x4_to_f16x4(y01, b[4], b[6]);
+        e4m3x4_to_f16x4(y89, b[5], b[7]);
+        if constexpr (MASK == kMaskRows) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) b[e] = finite_pair<true>(b[e], odd);
+        } else if constexpr (MASK == kMaskKeys) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) b[e] &= (e & 1) ? k89 : k01;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mma16<true>(o[4 * i + e], p, b[2 * e], b[2 * e + 1]);
+      }
+    }
+  }
+
+  // 16 codes of key `key` from 16-byte chunk x (D = 128: swizzled lines; D = 64: plain rows).
+  __device__ __forceinline__ static void ld_codes(uint32_t base, int key, int x, uint4& v) {
+    const uint32_t a = D == 128 ? base + key * 128 + ((x ^ (key & 7)) << 4) : base + key * D + x * 16;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a) : "memory");
+  }
+
+  // Writes the warp's state to `buf` ([16][D + 4] floats: o unnormalised, m in log2 units, l).
+  __device__ __forceinline__ void store(float* buf, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    float l0 = l[0], l1 = l[1];
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    float* r0 = buf + g * (D + 4);
+    float* r1 = r0 + 8 * (D + 4);
+    if (c == 0) {
+      r0[D] = m[0]; r0[D + 1] = l0;
+      r1[D] = m[1]; r1[D + 1] = l1;
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      if constexpr (F8) {   // columns 2c and 2c + 1 of n-tile j: dims (D/8) 2c + j and (D/8)(2c + 1) + j
+        const int d = (D / 4) * c + j;
+        r0[d] = o[j][0]; r0[d + D / 8] = o[j][1];
+        r1[d] = o[j][2]; r1[d + D / 8] = o[j][3];
+      } else {
+        const int d = 8 * j + 2 * c;
+        *reinterpret_cast<float2*>(r0 + d) = make_float2(o[j][0], o[j][1]);
+        *reinterpret_cast<float2*>(r1 + d) = make_float2(o[j][2], o[j][3]);
+      }
+    }
+  }
+};
+
+// Copies chunk `chunk` (block * kv heads + head) of K and V into a stage; one lane.
+template <int D, bool F8>
+__device__ __forceinline__ void rows_issue(const PoolView& pool, const void* tmk, const void* tmv, uint8_t* dst,
+                                           int64_t chunk, uint64_t* bar) {
+  using S = RowsSmem<D, F8>;
+  // Earlier generic reads of the stage come before the copy's writes.
+  fence_proxy_async_smem();
+  mbar_arrive_expect_tx(bar, 2 * S::kChunk);
+  if constexpr (!F8 && D == 128) {
+    tma_load_4d(dst, tmk, 0, 0, 0, static_cast<int>(2 * chunk), bar);
+    tma_load_4d(dst + S::kChunk, tmv, 0, 0, 0, static_cast<int>(2 * chunk), bar);
+  } else if constexpr (!F8 || D == 128) {
+    tma_load_2d(dst, tmk, 0, static_cast<int>(chunk * kBlockSize), bar);
+    tma_load_2d(dst + S::kChunk, tmv, 0, static_cast<int>(chunk * kBlockSize), bar);
+  } else {
+    bulk_g2s(dst, static_cast<const uint8_t*>(pool.k) + chunk * S::kChunk, S::kChunk, bar);
+    bulk_g2s(dst + S::kChunk, static_cast<const uint8_t*>(pool.v) + chunk * S::kChunk, S::kChunk, bar);
+  }
+}
+
+// Element d of key slot `slot` (block-relative) of chunk `chunk` of V, in the pool's units (codes unscaled).
+template <int D, bool F8>
+__device__ __forceinline__ float pool_v(const PoolView& pool, int64_t chunk, int slot, int d) {
+  const int64_t at = (chunk * kBlockSize + slot) * D + d;
+  if constexpr (F8) {
+    const uint32_t c = static_cast<const uint8_t*>(pool.v)[at];
+    uint32_t h = e4m3x2_lo_to_f16x2(c) & 0xffffu;
+    // f16 -> f32 (NaN stays NaN)
+    float f;
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %1;\n\tcvt.f32.f16 %0, x;\n\t}" : "=f"(f) : "r"(h));
+    return f;
+  } else {
+    return bf16lo_to_f32(static_cast<const uint16_t*>(pool.v)[at]);
+  }
+}
+
+}  // namespace pkv

@@ -1,0 +1,368 @@
+// Attention of drafted tokens over a cache (pkv_tree_attn): token t of request
+// r sees key slot j of its request if j < prefix_r, or if j lies in
+// [prefix_r, ctx_r) and bit j - prefix_r of the token's mask is set.
+//
+//   s_j = scale q . K_j,   O = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),
+//   LSE = m + ln sum_j exp(s_j - m)       over the slots that the token sees;
+//
+// a token that sees none has O = 0 and LSE = -inf.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "internal.h"
+#include "ops.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+#include "sched.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kRowsThreads = 32 * kRowWarps;
+// Rows kernel: 16 query rows a group, one block a unit; a CTA takes at least
+// four blocks a warp.
+using RowsTiling = Tiling<kRowTile, kBlockSize, 16>;
+
+// One segment: blocks [b0, b0 + nb) of one (request, KV head, row tile).
+template <int D, bool F8>
+__global__ void __launch_bounds__(kRowsThreads, 3)
+tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using S = RowsSmem<D, F8>;
+  using T = RowsTiling;
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kBuf);
+  int64_t* scratch = reinterpret_cast<int64_t*>(ring + S::kBuf + kRowWarps * S::kStages * 8);   // kRowWarps + 2
+  __shared__ int s_flags[2];
+  volatile int* s_abort = &s_flags[0];
+  int* s_odd = &s_flags[1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group, Hkv = a.pool.num_kv_heads;
+  const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
+  if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
+  if (tid == 0) {
+    for (int i = 0; i < kRowWarps * S::kStages; ++i) mbar_init(&bars[i], 1);
+    s_flags[0] = s_flags[1] = 0;
+    fence_mbar_init();
+  }
+  int64_t U, u0, u1, off;
+  int C, req;
+  tree_locate<T, kRowsThreads>(a, scratch, U, C, u0, u1, req, off);
+  if (u0 >= u1) return;
+  __syncthreads();
+
+  uint8_t* my_ring = ring + warp * S::kStages * S::kStage;
+  uint64_t* my_bars = bars + warp * S::kStages;
+  const uint32_t my_addr = smem_u32(my_ring);
+  const float sl2 = F8 ? a.scale_log2 * a.pool.k_scale : a.scale_log2;
+  int cnt = 0;   // stages this warp has issued in the launch
+  TreeReq rq = tree_req(a, req);
+  int64_t left = u1 - u0;
+  while (left > 0) {
+    while (off >= T::units(rq, G, Hkv)) {   // next request with work (there is one: left > 0)
+      off -= T::units(rq, G, Hkv);
+      if (++req >= a.num_reqs) return;
+      rq = tree_req(a, req);
+    }
+    const int kblk = T::kblk(rq), ntile = T::tiles(rq, G);
+    const int grp = static_cast<int>(off / kblk);
+    const int b0 = static_cast<int>(off % kblk);
+    const int nb = static_cast<int>(min(static_cast<int64_t>(kblk - b0), left));
+    const int g = grp / ntile, tile = grp % ntile;
+    const int row0 = tile * kRowTile, nrows = min(kRowTile, rq.n * G - row0);
+    // Rows g' and g' + 8 of this thread.
+    const int ra = lane >> 2, rb = ra + 8;
+    auto q_row = [&](int rr) -> const uint16_t* {
+      if (rr >= nrows) return nullptr;
+      const int f = row0 + rr;
+      return static_cast<const uint16_t*>(a.q) +
+             (static_cast<int64_t>(rq.t0 + f / G) * a.num_q_heads + g * G + f % G) * D;
+    };
+    auto mask_row = [&](int rr) {
+      return a.mask + static_cast<int64_t>(rq.t0 + (row0 + min(rr, nrows - 1)) / G) * a.mask_words;
+    };
+    const int end_blk = min(b0 + nb, (rq.ctx + kBlockSize - 1) / kBlockSize);
+    const int live = max(0, end_blk - b0);
+    const int nb_w = live > warp ? (live - warp + kRowWarps - 1) / kRowWarps : 0;
+    const int32_t* bt_row = a.block_tables + static_cast<int64_t>(req) * a.max_blocks;
+    auto load_ids = [&](int base) -> int {
+      const int i = base + lane;
+      if (i >= nb_w) return -1;
+      const int pb = __ldg(bt_row + b0 + warp + kRowWarps * i);
+      if (pb < 0 || pb >= a.pool.num_blocks) {
+        atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
+        return -1;
+      }
+      return pb;
+    };
+    int ids_cur = load_ids(0), ids_next = load_ids(32), win = 0;
+    auto id_of = [&](int j) {   // warp-uniform j
+      return __shfl_sync(0xffffffffu, (j >> 5) == win ? ids_cur : ids_next, j & 31);
+    };
+    auto issue = [&](int j) {
+      const int pb = id_of(j);
+      if (lane == 0) {
+        const int st = (cnt + j) % S::kStages;
+        if (pb >= 0)
+          rows_issue<D, F8>(a.pool, &tmk, &tmv, my_ring + st * S::kStage, static_cast<int64_t>(pb) * Hkv + g,
+                            &my_bars[st]);
+        else
+          mbar_arrive(&my_bars[st]);   // no such block: its keys are seen by no row
+      }
+    };
+    int issued = 0;
+    for (; issued < S::kStages && issued < nb_w; ++issued) issue(issued);
+    RowTile<D, F8> rt;
+    rt.init(q_row(ra), q_row(rb), lane);
+    const uint32_t* m0 = mask_row(ra);
+    const uint32_t* m1 = mask_row(rb);
+    bool ok = true;
+    for (int i = 0; i < nb_w; ++i) {
+      if ((i & 31) == 0 && i > 0) {
+        ids_cur = ids_next;
+        win = i >> 5;
+        ids_next = load_ids(i + 32);
+      }
+      const int st = (cnt + i) % S::kStages;
+      if (!(ok = mbar_wait_warp(&my_bars[st], ((cnt + i) / S::kStages) & 1, s_abort, a.wait_ns))) break;
+      const int key0 = (b0 + warp + kRowWarps * i) * kBlockSize;
+      const uint32_t kb = my_addr + st * S::kStage;
+      if (id_of(i) >= 0) {
+        if (key0 + kBlockSize <= rq.prefix)
+          rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
+        else
+          rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq, m0, a.mask_words, key0),
+                                  tree_sees(rq, m1, a.mask_words, key0), lane);
+      }
+      __syncwarp();
+      if (issued < nb_w) {
+        issue(issued);
+        ++issued;
+      }
+    }
+    if (!ok) {
+      // Gave up: let the copies in flight land, then leave together.
+      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+      *s_abort = 1;
+      for (int j = max(0, issued - S::kStages); j < issued; ++j)
+        (void)mbar_wait(&my_bars[(cnt + j) % S::kStages], ((cnt + j) / S::kStages) & 1, nullptr, a.wait_ns);
+    }
+    cnt += nb_w;
+    if (rt.odd) *s_odd = 1;
+    __syncthreads();   // every warp's ring has drained
+    if (*s_abort) return;
+    // Merge the warps' states: [warp][16][D + 4] floats over the ring.
+    float* mbuf = reinterpret_cast<float*>(ring);
+    rt.store(mbuf + warp * kRowTile * S::kMergeRow, lane);
+    __syncthreads();
+    constexpr int kDims = D / 8;   // dims of a thread's part of a row
+    const int rr = tid >> 3, d0 = (tid & 7) * kDims;
+    if (rr < nrows) {
+      float M = -CUDART_INF_F, L = 0.f, acc[kDims];
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        const float* src = mbuf + (w * kRowTile + rr) * S::kMergeRow;
+        if (src[D + 1] == 0.f) continue;   // the warp saw no key of this row (a NaN score leaves m, not l, as it was)
+        const float f = fast_exp2(src[D] - M);
+        L = fmaf(f, src[D + 1], L);
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) acc[d] = fmaf(f, src[d0 + d], acc[d]);
+      }
+      const float inv = L == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / L;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) acc[d] *= inv;
+      const float lse2 = L == 0.f ? -CUDART_INF_F : M + fast_log2(L);
+      const int f = row0 + rr, t = rq.t0 + f / G, h = g * G + f % G;
+      if (*s_odd) {
+        // V elements that are not finite, for the rows that see them.
+        const uint32_t* mr = a.mask + static_cast<int64_t>(t) * a.mask_words;
+        for (int b = max(b0, rq.prefix / kBlockSize); b < end_blk; ++b) {
+          const uint32_t vis = tree_sees(rq, mr, a.mask_words, b * kBlockSize);
+          const int pb = __ldg(bt_row + b);
+          if (pb < 0 || pb >= a.pool.num_blocks) continue;
+          for (int k = 0; k < kBlockSize; ++k) {
+            if (!((vis >> k) & 1u)) continue;
+            for (int d = 0; d < kDims; ++d) {
+              const float v = pool_v<D, F8>(a.pool, static_cast<int64_t>(pb) * Hkv + g, k, d0 + d);
+              if (!(fabsf(v) < CUDART_INF_F)) acc[d] += v;
+            }
+          }
+        }
+      }
+      if (b0 == 0 && nb == kblk) {   // the whole group: the final result
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
+                                              (static_cast<int64_t>(t) * a.num_q_heads + h) * D + d0);
+#pragma unroll
+        for (int d = 0; d < kDims; d += 8)
+          dst[d / 8] = make_uint4(pack_bf16x2(acc[d], acc[d + 1]), pack_bf16x2(acc[d + 2], acc[d + 3]),
+                                  pack_bf16x2(acc[d + 4], acc[d + 5]), pack_bf16x2(acc[d + 6], acc[d + 7]));
+        if (d0 == 0 && a.lse)
+          a.lse[static_cast<int64_t>(t) * a.num_q_heads + h] = lse2 * 0.69314718055994530942f;
+      } else {
+        const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (b0 == 0 ? 1 : 0)) * kRowTile + rr;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + d0);
+#pragma unroll
+        for (int d = 0; d < kDims; d += 4) dst[d / 4] = make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
+        if (d0 == 0) a.part_lse[slot] = lse2;
+      }
+    }
+    __syncthreads();   // the ring and the flags are free again
+    if (tid == 0) *s_odd = 0;
+    fence_proxy_async_smem();
+    __syncthreads();
+    off += nb;
+    left -= nb;
+  }
+}
+
+// One warp per (token, query head): merges the partials of a group that
+// several CTAs share.  LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c,
+// in CTA order.
+template <int D, class T>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
+  constexpr int kDPL = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the attention kernel's writes
+  if (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT) return;   // the partials may be incomplete
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (w >= static_cast<int64_t>(a.num_tokens) * a.num_q_heads) return;
+  const int t = static_cast<int>(w / a.num_q_heads), h = static_cast<int>(w % a.num_q_heads);
+  // The request that holds token t: the last with cu <= t (tokens past the end belong to none).
+  int lo = 0, hi = a.num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(a.cu_q_lens + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  const TreeReq q = tree_req(a, lo);
+  if (t < q.t0 || t >= q.t0 + q.n) return;
+  const int64_t U = __ldcg(a.offs + a.num_reqs), base = __ldcg(a.offs + lo);
+  if (U <= 0) return;
+  const int C = T::ctas(U, a.ctas);
+  const int kblk = T::kblk(q), ntile = T::tiles(q, a.group);
+  const int g = h / a.group, f = (t - q.t0) * a.group + h % a.group;
+  const int64_t u0 = base + (static_cast<int64_t>(g) * ntile + f / T::kRows) * kblk;
+  const int c0 = T::owner(U, C, u0), c1 = T::owner(U, C, u0 + kblk - 1);
+  if (c0 < 0 || c0 >= c1 || c1 >= C) return;   // one CTA wrote the row
+  const int rr = f % T::kRows;
+  auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * T::kRows + rr; };
+  float M = -CUDART_INF_F;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(a.part_lse + slot(c)));
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float acc[kDPL], sum = 0.f;
+#pragma unroll
+  for (int d = 0; d < kDPL; ++d) acc[d] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float e = __ldcg(a.part_lse + slot(c));
+    if (e == -CUDART_INF_F) continue;   // no key of this row there
+    const float wgt = fast_exp2(e - M);
+    sum += wgt;
+    const float* src = a.part_o + slot(c) * D + lane * kDPL;
+#pragma unroll
+    for (int d = 0; d < kDPL; d += 2) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src + d));
+      acc[d] = fmaf(wgt, v.x, acc[d]);
+      acc[d + 1] = fmaf(wgt, v.y, acc[d + 1]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) +
+                                              (static_cast<int64_t>(t) * a.num_q_heads + h) * D + lane * kDPL);
+#pragma unroll
+  for (int d = 0; d < kDPL; d += 2) dst[d / 2] = pack_bf16x2(acc[d] * inv, acc[d + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[static_cast<int64_t>(t) * a.num_q_heads + h] =
+        sum == 0.f ? -CUDART_INF_F : (M + fast_log2(sum)) * 0.69314718055994530942f;
+}
+
+// Ancestor bits from parents: token i of a request sets its own bit and its
+// ancestors' (parent indexes below its own, -1 for a root; others are flagged
+// and end the walk).  One warp per token; lane l owns words l, l + 32, ...
+__global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restrict__ parents,
+                                                        const int32_t* __restrict__ cu, int num_reqs, int num_tokens,
+                                                        uint32_t* __restrict__ mask, int words, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+  if (t >= num_tokens) return;
+  int lo = 0, hi = num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  const int c0 = __ldg(cu + lo);
+  if (c0 < 0 || t < c0 || t >= __ldg(cu + lo + 1)) return;
+  for (int w0 = 0; w0 < words; w0 += 32) {
+    uint32_t bits = 0;
+    // Parents lie strictly before their children, so the walk ends.
+    for (int i = t - c0; i >= 0;) {
+      if ((i >> 5) == w0 + lane) bits |= 1u << (i & 31);
+      const int p = __ldg(parents + c0 + i);
+      if (p >= i || p < -1) {
+        if (lane == 0) atomicOr(err, PKV_DEVERR_POSITION);
+        break;
+      }
+      i = p;
+    }
+    if (w0 + lane < words) mask[static_cast<int64_t>(t) * words + w0 + lane] = bits;
+  }
+  if (lane == 0 && t - c0 >= words * 32) atomicOr(err, PKV_DEVERR_POSITION);   // its own bit has no word
+}
+
+template <int D, bool F8>
+int launch_rows(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
+  const int smem = RowsSmem<D, F8>::kTotal;
+  cudaError_t e = smem_attr_once<tree_rows_kernel<D, F8>>(smem);
+  if (e != cudaSuccess) return e;
+  tree_rows_kernel<D, F8><<<a.ctas, kRowsThreads, smem, s>>>(a, *tmk, *tmv);
+  return cudaGetLastError();
+}
+
+template <int D, class T>
+int launch_merge_t(const TreeArgs& a, cudaStream_t s) {
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T>, a);
+}
+
+}  // namespace
+
+int tree_ctas(const PoolView&, int num_sms) { return num_sms * 3; }
+
+size_t tree_part_rows(int ctas) { return static_cast<size_t>(2) * ctas * kRowTile; }
+
+int launch_tree(const TreeArgs& a, const void* tmk, const void* tmv, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const CUtensorMap* k = static_cast<const CUtensorMap*>(tmk);
+  const CUtensorMap* v = static_cast<const CUtensorMap*>(tmv);
+  const bool f8 = a.pool.elem_bytes == 1;
+  if (a.pool.head_dim == 128) return f8 ? launch_rows<128, true>(a, k, v, s) : launch_rows<128, false>(a, k, v, s);
+  return f8 ? launch_rows<64, true>(a, k, v, s) : launch_rows<64, false>(a, k, v, s);
+}
+
+int launch_tree_merge(const TreeArgs& a, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a.pool.head_dim == 128 ? launch_merge_t<128, RowsTiling>(a, s) : launch_merge_t<64, RowsTiling>(a, s);
+}
+
+int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
+                     unsigned* err, void* stream) {
+  tree_mask_kernel<<<(num_tokens + 7) / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(parents, cu, num_reqs,
+                                                                                        num_tokens, mask, words, err);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

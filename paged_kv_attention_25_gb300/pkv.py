@@ -32,6 +32,7 @@ PKV_DEVERR_BLOCK_ID = 1
 PKV_DEVERR_POSITION = 2
 PKV_DEVERR_TIMEOUT = 4
 PKV_DEVERR_INTERNAL = 8
+PKV_DEVERR_NO_PAGES = 16
 PKV_DEBUG_WAIT_LIMIT_NS = 1
 PKV_DEBUG_WITHHOLD_COPY = 2
 PKV_DEBUG_FUSED_FORM = 3
@@ -48,6 +49,8 @@ EXPORTED = (
     "pkv_profile_enable", "pkv_profile_read", "pkv_device_sm_count", "pkv_last_error",
     "pkv_version", "pkv_copy_to_device", "pkv_copy_to_host", "pkv_debug_set",
     "pkv_cache_create", "pkv_cache_destroy", "pkv_cache_step", "pkv_cache_release", "pkv_cache_free_blocks",
+    "pkv_tree_mask", "pkv_tree_attn_workspace_size", "pkv_tree_attn", "pkv_summarize", "pkv_select_blocks",
+    "pkv_sparse_attn", "pkv_fork_workspace_size", "pkv_fork", "pkv_copy_blocks", "pkv_compact",
 )
 
 
@@ -139,6 +142,16 @@ def load_library():
             "pkv_cache_step": [P, P, P, I, P, I, P, P, P, ctypes.POINTER(I), P, ctypes.POINTER(I), I],
             "pkv_cache_release": [P, I],
             "pkv_cache_free_blocks": [P, ctypes.POINTER(I), ctypes.POINTER(I)],
+            "pkv_tree_mask": [P, P, P, I, I, P, I, P],
+            "pkv_tree_attn_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_tree_attn": [P, P, I, P, I, P, P, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
+            "pkv_summarize": [P, P, I, I, P, P, P, I, P, P, P],
+            "pkv_select_blocks": [P, P, I, P, P, I, P, I, I, P, P, I, I, I, P, P],
+            "pkv_sparse_attn": [P, P, I, P, P, I, P, I, I, P, I, F, P, P, P],
+            "pkv_fork_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_fork": [P, P, I, I, P, P, P, P, I, P, P, P, P, P, P, ctypes.c_size_t, P],
+            "pkv_copy_blocks": [P, P, P, I, P, P, P],
+            "pkv_compact": [P, P, I, I, P, P, P, I, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -376,6 +389,227 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
                                                 ctx_lens.shape[0], T, ctypes.byref(meta.c), float(scale), _ptr(out),
                                                 _ptr(lse), _stream(stream)))
     return out, lse
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# Tree attention, block-selected attention and pages.  Their metadata is read on the device alone: no HostMeta, and the
+# calls can be captured into a graph.  Tensors live on the pool's device; without `stream` a call runs on that device's
+# current stream.  Outputs and workspaces that are not given are allocated for that stream.
+
+
+def _op_stream(pool: Pool, stream):
+    return torch.cuda.current_stream(pool.k.device) if stream is None else stream
+
+
+def _op_dev(pool: Pool, t, name, dtype, shape=None):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
+    if t.device != pool.k.device:
+        raise ValueError(f"{name} must be on the pool's device")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape))):
+        raise ValueError(f"{name} must have shape {['*' if w is None else w for w in shape]}")
+    return t
+
+
+def _op_heads(pool: Pool, q):
+    _op_dev(pool, q, "q", torch.bfloat16, (None, None, pool.head_dim))
+    return q.shape[0], q.shape[1]
+
+
+def _op_out(pool: Pool, q, out, lse, want_lse, stream):
+    T, Hq, _ = q.shape
+    with torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    _op_dev(pool, out, "out", torch.bfloat16, tuple(q.shape))
+    if lse is not None:
+        _op_dev(pool, lse, "lse", torch.float32, (T, Hq))
+    return out, lse
+
+
+def _op_workspace(pool: Pool, workspace, nbytes, stream):
+    if workspace is None:
+        with torch.cuda.stream(stream):
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.k.device)
+    return _op_dev(pool, workspace, "workspace", torch.uint8, (None,))
+
+
+def pkv_tree_mask(pool: Pool, parents, cu_q_lens, mask_words=None, max_nodes=None, out=None, stream=None):
+    """Mask rows [T, mask_words] (int32 bit patterns) from each node's parent (index in its tree, -1: a root).
+
+    Give mask_words, or max_nodes (the largest tree's size, T if neither is given) to size the rows by."""
+    stream = _op_stream(pool, stream)
+    _op_dev(pool, parents, "parents", torch.int32, (None,))
+    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
+    T = parents.shape[0]
+    if out is None:
+        words = mask_words if mask_words is not None else max(1, ((max_nodes or T) + 31) // 32)
+        with torch.cuda.stream(stream):
+            out = torch.zeros((T, words), dtype=torch.int32, device=parents.device)
+    _op_dev(pool, out, "out", torch.int32, (T, None))
+    _check(load_library().pkv_tree_mask(pool.handle, _ptr(parents), _ptr(cu_q_lens), cu_q_lens.shape[0] - 1, T,
+                                        _ptr(out), out.shape[1], _stream(stream)))
+    return out
+
+
+def pkv_tree_attn_workspace_size(pool: Pool, num_q_heads: int, num_reqs: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().pkv_tree_attn_workspace_size(pool.handle, num_q_heads, num_reqs, ctypes.byref(n)))
+    return n.value
+
+
+def pkv_tree_attn(pool: Pool, q, block_tables, ctx_lens, prefix_lens, cu_q_lens, tree_mask, scale: float, out=None,
+                  lse=None, workspace=None, stream=None, want_lse=True):
+    """Attention of drafted tokens: each sees slots [0, prefix_lens[r]) and the slots prefix_lens[r] + i whose bit i is
+    set in its row of tree_mask [T, words] (int32 bit patterns).  Returns (O [T, Hq, D] bf16, LSE [T, Hq] fp32 or None).
+    """
+    stream = _op_stream(pool, stream)
+    T, Hq = _op_heads(pool, q)
+    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
+    R = cu_q_lens.shape[0] - 1
+    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
+    _op_dev(pool, ctx_lens, "ctx_lens", torch.int32, (R,))
+    _op_dev(pool, prefix_lens, "prefix_lens", torch.int32, (R,))
+    _op_dev(pool, tree_mask, "tree_mask", torch.int32, (T, None))
+    out, lse = _op_out(pool, q, out, lse, want_lse, stream)
+    workspace = _op_workspace(pool, workspace, 0 if workspace is not None
+                              else pkv_tree_attn_workspace_size(pool, Hq, R), stream)
+    _check(load_library().pkv_tree_attn(pool.handle, _ptr(q), Hq, _ptr(block_tables), block_tables.shape[1],
+                                        _ptr(ctx_lens), _ptr(prefix_lens), _ptr(cu_q_lens), R, T, _ptr(tree_mask),
+                                        tree_mask.shape[1], float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                                        workspace.numel(), _stream(stream)))
+    return out, lse
+
+
+class BlockSummary:
+    """Bounds of a pool's blocks: codes [num_blocks, num_kv_heads, 2 (upper, lower), head_dim] int8 in units of
+    2 ** exps [num_blocks, num_kv_heads] (int8).  Kept up to date by pkv_summarize."""
+
+    def __init__(self, pool: Pool, codes=None, exps=None):
+        shape = (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
+        if (codes is None) != (exps is None):
+            raise ValueError("give both codes and exps or neither")
+        if codes is None:
+            codes = torch.zeros(shape, dtype=torch.int8, device=pool.k.device)
+            exps = torch.zeros(shape[:2], dtype=torch.int8, device=pool.k.device)
+        self.codes = _op_dev(pool, codes, "codes", torch.int8, shape)
+        self.exps = _op_dev(pool, exps, "exps", torch.int8, shape[:2])
+
+
+def _op_summary(pool: Pool, summary):
+    shape = (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
+    return (_ptr(_op_dev(pool, summary.codes, "summary.codes", torch.int8, shape)),
+            _ptr(_op_dev(pool, summary.exps, "summary.exps", torch.int8, shape[:2])))
+
+
+def pkv_summarize(pool: Pool, summary: BlockSummary, block_tables, cu_q_lens, positions, ctx_lens, stream=None):
+    """Recompute the bounds of every block that holds one of `positions` (after pkv_append: its own arguments)."""
+    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
+    R = cu_q_lens.shape[0] - 1
+    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
+    _op_dev(pool, positions, "positions", torch.int32, (None,))
+    _op_dev(pool, ctx_lens, "ctx_lens", torch.int32, (R,))
+    codes, exps = _op_summary(pool, summary)
+    _check(load_library().pkv_summarize(pool.handle, _ptr(block_tables), block_tables.shape[1], R, _ptr(cu_q_lens),
+                                        _ptr(positions), _ptr(ctx_lens), positions.shape[0], codes, exps,
+                                        _stream(_op_stream(pool, stream))))
+
+
+def pkv_select_blocks(pool: Pool, summary: BlockSummary, q, q_positions, block_tables, cu_q_lens, top_k: int,
+                      sinks: int = 1, recent: int = 1, out=None, stream=None):
+    """The top_k blocks of each (token, KV head) by the bound on its scores, the first `sinks` and last `recent` always
+    among them: [T, Hkv, top_k] int32 indexes into the block table, ascending, -1 beyond."""
+    stream = _op_stream(pool, stream)
+    T, Hq = _op_heads(pool, q)
+    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
+    R = cu_q_lens.shape[0] - 1
+    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
+    _op_dev(pool, q_positions, "q_positions", torch.int32, (T,))
+    if top_k < 1:
+        raise ValueError("top_k must be >= 1")
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.empty((T, pool.num_kv_heads, top_k), dtype=torch.int32, device=q.device)
+    _op_dev(pool, out, "out", torch.int32, (T, pool.num_kv_heads, top_k))
+    codes, exps = _op_summary(pool, summary)
+    _check(load_library().pkv_select_blocks(pool.handle, _ptr(q), Hq, _ptr(q_positions), _ptr(block_tables),
+                                            block_tables.shape[1], _ptr(cu_q_lens), R, T, codes, exps, int(top_k),
+                                            int(sinks), int(recent), _ptr(out), _stream(stream)))
+    return out
+
+
+def pkv_sparse_attn(pool: Pool, q, q_positions, block_tables, cu_q_lens, selected, scale: float, out=None, lse=None,
+                    stream=None, want_lse=True):
+    """Attention of each token over its selected blocks [T, Hkv, k] (keys up to its position); returns (O, LSE)."""
+    stream = _op_stream(pool, stream)
+    T, Hq = _op_heads(pool, q)
+    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
+    R = cu_q_lens.shape[0] - 1
+    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
+    _op_dev(pool, q_positions, "q_positions", torch.int32, (T,))
+    _op_dev(pool, selected, "selected", torch.int32, (T, pool.num_kv_heads, None))
+    out, lse = _op_out(pool, q, out, lse, want_lse, stream)
+    _check(load_library().pkv_sparse_attn(pool.handle, _ptr(q), Hq, _ptr(q_positions), _ptr(block_tables),
+                                          block_tables.shape[1], _ptr(cu_q_lens), R, T, _ptr(selected),
+                                          selected.shape[2], float(scale), _ptr(out), _ptr(lse), _stream(stream)))
+    return out, lse
+
+
+def pkv_fork_workspace_size(pool: Pool, num_rows: int, num_children: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().pkv_fork_workspace_size(pool.handle, num_rows, num_children, ctypes.byref(n)))
+    return n.value
+
+
+def pkv_fork(pool: Pool, tables, lens, caps, parents, new_caps, refs, out_tables=None, out_refs=None, summary=None,
+             workspace=None, stream=None):
+    """The next generation of sequences: child i continues row parents[i] of `tables` (-1: empty) with pages for
+    new_caps[i] tokens.  Shares full pages, copies partly filled ones where needed, frees what no one owns any more.
+    refs [num_blocks] counts the pages' owners; out_refs defaults to refs (in place).  Returns (new tables, refs)."""
+    stream = _op_stream(pool, stream)
+    i32 = torch.int32
+    _op_dev(pool, tables, "tables", i32, (None, None))
+    R, width = tables.shape
+    _op_dev(pool, lens, "lens", i32, (R,))
+    _op_dev(pool, caps, "caps", i32, (R,))
+    _op_dev(pool, parents, "parents", i32, (None,))
+    N = parents.shape[0]
+    _op_dev(pool, new_caps, "new_caps", i32, (N,))
+    _op_dev(pool, refs, "refs", i32, (pool.num_blocks,))
+    out_refs = refs if out_refs is None else _op_dev(pool, out_refs, "out_refs", i32, (pool.num_blocks,))
+    if out_tables is None:
+        with torch.cuda.stream(stream):
+            out_tables = torch.empty((N, width), dtype=i32, device=tables.device)
+    _op_dev(pool, out_tables, "out_tables", i32, (N, width))
+    codes, exps = (None, None) if summary is None else _op_summary(pool, summary)
+    workspace = _op_workspace(pool, workspace, 0 if workspace is not None else pkv_fork_workspace_size(pool, R, N), stream)
+    _check(load_library().pkv_fork(pool.handle, _ptr(tables), R, width, _ptr(lens), _ptr(caps), _ptr(parents),
+                                   _ptr(new_caps), N, _ptr(out_tables), _ptr(refs), _ptr(out_refs), codes, exps,
+                                   _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out_tables, out_refs
+
+
+def pkv_copy_blocks(pool: Pool, src, dst, summary=None, stream=None):
+    """Copy whole pages src[i] -> dst[i] (int32 device ids): K, V and, if given, the summary's bounds."""
+    _op_dev(pool, src, "src", torch.int32, (None,))
+    _op_dev(pool, dst, "dst", torch.int32, (src.shape[0],))
+    codes, exps = (None, None) if summary is None else _op_summary(pool, summary)
+    _check(load_library().pkv_copy_blocks(pool.handle, _ptr(src), _ptr(dst), src.shape[0], codes, exps,
+                                          _stream(_op_stream(pool, stream))))
+
+
+def pkv_compact(pool: Pool, block_tables, cu_keep, src_positions, dst_starts, stream=None):
+    """Move the K/V rows at src_positions (ascending per request) to dst_starts[r], dst_starts[r] + 1, ..."""
+    _op_dev(pool, cu_keep, "cu_keep", torch.int32, (None,))
+    R = cu_keep.shape[0] - 1
+    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
+    _op_dev(pool, src_positions, "src_positions", torch.int32, (None,))
+    _op_dev(pool, dst_starts, "dst_starts", torch.int32, (R,))
+    _check(load_library().pkv_compact(pool.handle, _ptr(block_tables), block_tables.shape[1], R, _ptr(cu_keep),
+                                      _ptr(src_positions), _ptr(dst_starts), src_positions.shape[0],
+                                      _stream(_op_stream(pool, stream))))
 
 
 def pkv_last_plan_stats(pool: Pool) -> dict:
