@@ -138,8 +138,8 @@ typedef struct {
 } pkv_plan_stats;
 
 /* Accumulated device time per kernel family while profiling is on.  The tree
- * attention and the attention over selected blocks count as split-KV, the tree
- * attention's merge as merge; bounds, selection and pages count as append. */
+ * attention of few rows and the attention over selected blocks count as split-KV, the tree
+ * attention over tiles of 128 rows as tensor-core, its merge as merge; bounds, selection and pages count as append. */
 typedef struct {
   int launches[5];          /* 0 append, 1 split-KV, 2 tensor-core, 3 merge, 4 swap */
   double total_ms[5];
@@ -331,12 +331,11 @@ int pkv_paged_attn_static(pkv_pool* pool, const void* q, int num_q_heads, const 
  * captured into a graph and replayed with other lengths, tables and masks, and
  * runs on `stream` alone (its kernels; a pending ahead-of-time swap-in lands
  * first).  q and o 16-byte aligned.  workspace: device memory of
- * pkv_tree_attn_workspace_size() bytes (which grows with num_reqs only), 256-byte
- * aligned, used by one call at a time: calls that may run at the same time,
+ * pkv_tree_attn_workspace_size() bytes for the same sizes, 256-byte aligned, used by one call at a time: calls that may run at the same time,
  * graphs that may be replayed at the same time among them, need their own.
  * num_tokens == 0 is a no-op.  Errors: PKV_EINVAL, PKV_EUNSUPPORTED, PKV_ECUDA.
  */
-int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, size_t* bytes);
+int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, size_t* bytes);
 int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* block_tables, int max_blocks,
                   const int32_t* ctx_lens, const int32_t* prefix_lens, const int32_t* cu_q_lens, int num_reqs,
                   int num_tokens, const uint32_t* tree_mask, int mask_words, float scale, void* o, float* lse,
@@ -590,10 +589,14 @@ int pkv_check_device_errors(pkv_pool* pool, void* stream, unsigned* flags);
  *     batch (default), 1 = inside the attention launches whenever the pool
  *     allows it, 2 = the append kernel first.  Every form gives the same pool
  *     and the same O and LSE bits.
+ *   PKV_DEBUG_TREE_FORM: which kernel pkv_tree_attn takes: 0 = chosen per batch
+ *     (default), 1 = warp-level MMA on 16 query rows, 2 = tcgen05 on tiles of
+ *     128; set it before asking for the workspace size.
  * Errors: PKV_EINVAL for an unknown setting or a value out of range. */
 #define PKV_DEBUG_WAIT_LIMIT_NS 1
 #define PKV_DEBUG_WITHHOLD_COPY 2
 #define PKV_DEBUG_FUSED_FORM 3
+#define PKV_DEBUG_TREE_FORM 4
 int pkv_debug_set(pkv_pool* pool, int what, int64_t value);
 
 /* Kernel timing with CUDA events recorded around every launch on the launch

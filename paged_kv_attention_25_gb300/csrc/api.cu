@@ -96,11 +96,13 @@ int make_tmap(CUtensorMap* map, void* base, int num_blocks, int hkv, int head_di
   return PKV_OK;
 }
 
+}  // namespace
+
 // Q viewed as [T][Hq][D] (bf16) for the tensor-core kernel's query tiles: a
 // box of 64 columns x G heads (one KV head's group) x the tile's tokens lands
 // as a [row][128 bytes] slab with 128-byte swizzle; tokens past T read zeros.
-int make_q_tmap(CUtensorMap* map, const void* q, int num_tokens, int num_q_heads, int head_dim, int group,
-                int* box_tokens) {
+int pkv::make_q_tmap(CUtensorMap* map, const void* q, int num_tokens, int num_q_heads, int head_dim, int group,
+                     int* box_tokens) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return fail(PKV_ECUDA, "cuTensorMapEncodeTiled unavailable (driver too old?)");
   const int bt = std::min(kTcRows / group, num_tokens);
@@ -116,6 +118,8 @@ int make_q_tmap(CUtensorMap* map, const void* q, int num_tokens, int num_q_heads
   *box_tokens = bt;
   return PKV_OK;
 }
+
+namespace {
 
 // The fused call's new K (or V) rows [T][Hkv][D] (bf16) for the tensor-core
 // kernel: a box of up to 8 tokens of one head lands as one 8-key group of a
@@ -869,6 +873,10 @@ int pkv_debug_set(pkv_pool* pool, int what, int64_t value) {
     case PKV_DEBUG_FUSED_FORM:
       if (value < 0 || value > 2) return fail(PKV_EINVAL, "fused form must be 0, 1 or 2");
       pool->fused_form = static_cast<int>(value);
+      return PKV_OK;
+    case PKV_DEBUG_TREE_FORM:
+      if (value < 0 || value > 2) return fail(PKV_EINVAL, "tree form must be 0, 1 or 2");
+      pool->tree_form = static_cast<int>(value);
       return PKV_OK;
     default:
       return fail(PKV_EINVAL, "unknown debug setting");

@@ -7,12 +7,18 @@ namespace pkv {
 
 struct TreeArgs;
 
-// CTAs of a tree-attention launch at most, and the partial rows of its workspace.
-int tree_ctas(const PoolView& pool, int num_sms);
-size_t tree_part_rows(int ctas);
-// tmk / tmv: the pool's block maps (128-byte swizzle; unused by FP8 pools with head_dim 64).
-int launch_tree(const TreeArgs& a, const void* tmk, const void* tmv, void* stream);
-int launch_tree_merge(const TreeArgs& a, void* stream);
+// The two forms of the tree attention: warp-level MMA on 16 query rows, or
+// tcgen05 on tiles of 128.
+struct TreeForm {
+  bool tensor;
+  int ctas, cuts, slots, slot_rows;
+};
+TreeForm tree_form(bool tensor, int num_sms);
+// tmk / tmv: the pool's block maps (rows form: 128-byte swizzle, unused by FP8
+// pools with head_dim 64); tmq: q viewed as [T][Hq][D] in boxes of one tile.
+int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* stream);
+int launch_tree_tc(const TreeArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream);
+int launch_tree_merge(const TreeArgs& a, const TreeForm& f, void* stream);
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
                      unsigned* err, void* stream);
 

@@ -57,16 +57,23 @@ int check_scale(float scale) {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct TreeWs {
-  size_t offs, part_o, part_lse, total;
+  size_t cuts, part_o, part_lse, total;
 };
-TreeWs tree_ws(const pkv_pool* pool, int num_reqs) {
-  const size_t rows = tree_part_rows(tree_ctas(pool->view(), pool->num_sms));
+TreeWs tree_ws(const pkv_pool* pool, const TreeForm& f) {
+  const size_t rows = static_cast<size_t>(f.slots) * f.slot_rows;
   TreeWs w;
-  w.offs = 0;
-  w.part_o = align256((static_cast<size_t>(num_reqs) + 1) * sizeof(int64_t));
+  w.cuts = 0;
+  w.part_o = align256(f.cuts * sizeof(TreeCut));
   w.part_lse = w.part_o + align256(rows * pool->head_dim * sizeof(float));
   w.total = w.part_lse + align256(rows * sizeof(float));
   return w;
+}
+
+// Which form a batch takes.
+bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens) {
+  if (pool->tree_form != 0) return pool->tree_form == 2;
+  const int64_t rows = static_cast<int64_t>(num_tokens) * (num_q_heads / pool->num_kv_heads);
+  return rows > 24ll * num_reqs;
 }
 
 // The maps whose copies land with the 128-byte swizzle that rows.cuh reads.
@@ -99,12 +106,12 @@ int pkv_tree_mask(pkv_pool* pool, const int32_t* parents, const int32_t* cu_q_le
   return PKV_OK;
 }
 
-int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, size_t* bytes) {
+int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, size_t* bytes) {
   if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
   const int rc = check_heads(pool, num_q_heads);
   if (rc) return rc;
-  if (num_reqs < 0) return fail(PKV_EINVAL, "negative size");
-  *bytes = tree_ws(pool, num_reqs).total;
+  if (num_reqs < 0 || num_tokens < 0) return fail(PKV_EINVAL, "negative size");
+  *bytes = tree_ws(pool, tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens), pool->num_sms)).total;
   return PKV_OK;
 }
 
@@ -121,7 +128,8 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   if (mask_words < 1) return fail(PKV_EINVAL, "mask_words must be >= 1");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
-  const TreeWs w = tree_ws(pool, num_reqs);
+  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens), pool->num_sms);
+  const TreeWs w = tree_ws(pool, form);
   if (!workspace || workspace_bytes < w.total)
     return fail(PKV_EINVAL, "workspace missing or smaller than pkv_tree_attn_workspace_size()");
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_EINVAL, "workspace must be 256-byte aligned");
@@ -145,14 +153,23 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   a.o = o;
   a.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.offs = reinterpret_cast<int64_t*>(ws + w.offs);
+  a.cuts = reinterpret_cast<TreeCut*>(ws + w.cuts);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  a.ctas = tree_ctas(a.pool, pool->num_sms);
+  a.ctas = form.ctas;
+  a.tile_tokens = kTcRows / a.group;
+  a.q_box_tokens = 0;
   a.wait_ns = pool->wait_ns;
-  rc = timed_launch(pool, 1, stream, [&] { return launch_tree(a, rows_map(pool, false), rows_map(pool, true), stream); });
+  if (form.tensor) {
+    CUtensorMap tmap_q;
+    if ((rc = make_q_tmap(&tmap_q, q, num_tokens, num_q_heads, pool->head_dim, a.group, &a.q_box_tokens))) return rc;
+    rc = timed_launch(pool, 2, stream, [&] { return launch_tree_tc(a, &pool->tmap_k, &pool->tmap_v, &tmap_q, stream); });
+  } else {
+    rc = timed_launch(pool, 1, stream,
+                      [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
+  }
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree attention launch");
-  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
+  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, form, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree merge launch");
   return PKV_OK;
 }

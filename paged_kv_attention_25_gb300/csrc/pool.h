@@ -89,6 +89,7 @@ struct pkv_pool {
   uint64_t wait_ns = 1000000000ull;   // limit of every bounded wait in the kernels
   int withhold = 0;                   // see AttnArgs::withhold
   int fused_form = 0;                 // PKV_DEBUG_FUSED_FORM
+  int tree_form = 0;                  // PKV_DEBUG_TREE_FORM
 
   // profiling (prof_mode 2: the two attention kernels run one after the other)
   bool prof_on = false;
@@ -138,5 +139,9 @@ int timed_launch(pkv_pool* pool, int kernel, void* stream, F&& fn) {
 // then scatters the staged blocks into the pool.  Every call that reads or
 // writes the pool starts with this.
 int finish_swap_in(pkv_pool* pool, void* stream);
+
+// Q viewed as [T][Hq][D] in boxes of one tile of kTcRows / group tokens (at most num_tokens: *box_tokens).
+int make_q_tmap(CUtensorMap* map, const void* q, int num_tokens, int num_q_heads, int head_dim, int group,
+                int* box_tokens);
 
 }  // namespace pkv

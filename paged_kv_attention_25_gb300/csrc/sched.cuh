@@ -1,13 +1,14 @@
 // Work split of an attention call whose lengths live on the device.
 //
-// The work of request r is groups (KV head, tile of query rows) of kblk key
-// units each; all requests' units form one line of U units, and CTA c of C
-// takes [c U / C, (c + 1) U / C): equal shares whatever the lengths, no plan
-// on the host, nothing to upload, and a captured call follows the lengths it
-// finds.  A group that falls into several CTAs is merged by log-sum-exp
-// afterwards: of a CTA's share only the first and the last group can be cut,
-// so a CTA has two partial slots, 2 c (a group that began before its share)
-// and 2 c + 1 (a group that ends after it).
+// The work of request r is groups (KV head, tile of query rows) of a number of
+// key units each; all requests' units form one line of U units, and worker w
+// of C takes [w U / C, (w + 1) U / C): equal shares whatever the lengths, no
+// plan on the host, nothing to upload, and a captured call follows the lengths
+// it finds.  A group that falls into several shares is merged by log-sum-exp
+// afterwards.  Of a worker's share only the first and the last group can be
+// cut, so it has two partial slots: 0 for a group that began before its share,
+// 1 for one that ends after it; the worker that begins a cut group leaves a
+// record of it for the merge.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -31,13 +32,26 @@ struct TreeArgs {
   float scale_log2;
   void* o;
   float* lse;
-  // Workspace: unit offset of each request (num_reqs + 1), partial slots.
-  int64_t* offs;
-  float* part_o;     // [2 C][tile rows][D]
-  float* part_lse;   // [2 C][tile rows], log2 units
-  int ctas;          // C at most
+  // Workspace: the cut groups, their partial rows.
+  struct TreeCut* cuts;
+  float* part_o;     // [slots][slot rows][D]
+  float* part_lse;   // [slots][slot rows], log2 units
+  int ctas;          // CTAs of the attention launch
+  int tile_tokens;   // tensor-core form: tokens of a tile of 128 rows
+  int q_box_tokens;  // ... and of a copy of its query map
   uint64_t wait_ns;
 };
+
+// A group that several workers share: rows [0, rows_a) and [128, 128 + rows_b)
+// of its slots; row i belongs to token tok + (f0 + i) / G and head
+// g G + (f0 + i) % G.  Its partials are slot `first` and slots
+// next, next + stride, ... (count - 1 of them).
+struct alignas(16) TreeCut {
+  int count, first, next, stride;
+  int tok_a, rows_a, tok_b, rows_b;
+  int f0, g, pad0, pad1;
+};
+static_assert(sizeof(TreeCut) == 48, "TreeCut layout: three 16-byte loads");
 
 // A request's lengths, made safe: whatever the device arrays hold, tokens stay
 // inside [0, num_tokens) and keys inside the block table's row.
@@ -58,38 +72,32 @@ __device__ __forceinline__ TreeReq tree_req(const TreeArgs& a, int r) {
   return q;
 }
 
-// Tiling of a kernel: TileRows query rows per group, KeyUnit keys per unit, at least MinUnits units a CTA.
-template <int TileRows_, int KeyUnit_, int MinUnits_>
-struct Tiling {
-  static constexpr int kRows = TileRows_, kKeys = KeyUnit_, kMin = MinUnits_;
-  __device__ static int tiles(const TreeReq& q, int group) {
-    return static_cast<int>((static_cast<int64_t>(q.n) * group + kRows - 1) / kRows);
-  }
-  // A request without keys keeps one (empty) unit a group: its rows are written too.
-  __device__ static int kblk(const TreeReq& q) { return max(1, (q.ctx + kKeys - 1) / kKeys); }
-  __device__ static int64_t units(const TreeReq& q, int group, int hkv) {
-    return static_cast<int64_t>(tiles(q, group)) * hkv * kblk(q);
-  }
-  // CTAs that share U units.
-  __device__ static int ctas(int64_t U, int most) {
+// Shares of U units among `most` workers at most, kMin units each at least.
+template <int kMin>
+struct Share {
+  __device__ static int workers(int64_t U, int most) {
     const int64_t want = (U + kMin - 1) / kMin;
     return static_cast<int>(want < 1 ? 1 : want > most ? most : want);
   }
-  __device__ static int64_t begin(int64_t U, int C, int c) { return U * c / C; }
-  // The CTA whose share holds unit u.
+  __device__ static int64_t begin(int64_t U, int C, int w) { return U * w / C; }
+  // The worker whose share holds unit u.
   __device__ static int owner(int64_t U, int C, int64_t u) { return static_cast<int>(((u + 1) * C - 1) / U); }
 };
 
-// Block-wide: the total number of units, and the request that holds the first
-// unit of this CTA's share with the unit's offset inside it.  CTA 0 writes the
-// requests' offsets for the merge.  scratch: one int64 per warp, plus two.
-template <class T, int Threads>
-__device__ __forceinline__ void tree_locate(const TreeArgs& a, int64_t* scratch, int64_t& U, int& C, int64_t& u0,
-                                            int64_t& u1, int& req, int64_t& off) {
+// A worker's share of a line: units [u, end) of U, the first of them unit
+// `off` of request `req`.
+struct TreeShare {
+  int64_t U, u, end, off;
+  int workers, req;
+};
+
+// Block-wide: worker w's share of the line in which request r has
+// units(tree_req(a, r)) units.  scratch: one int64 per warp and two more.
+template <class S, int Threads, class F>
+__device__ __forceinline__ TreeShare tree_share(const TreeArgs& a, int64_t* scratch, int w, int most, F&& units) {
   constexpr int kW = Threads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hkv = a.pool.num_kv_heads;
-  U = 0;
+  TreeShare sh{0, 0, 0, 0, 1, 0};
   for (int pass = 0; pass < 2; ++pass) {
     int64_t run = 0;
     for (int base = 0; base < a.num_reqs; base += Threads) {
@@ -97,7 +105,7 @@ __device__ __forceinline__ void tree_locate(const TreeArgs& a, int64_t* scratch,
       int64_t n = 0;
       if (r < a.num_reqs) {
         const TreeReq q = tree_req(a, r);
-        n = T::units(q, a.group, hkv);
+        n = units(q);
         if (pass == 0 && q.bad && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
       }
       int64_t inc = n;
@@ -110,38 +118,31 @@ __device__ __forceinline__ void tree_locate(const TreeArgs& a, int64_t* scratch,
       __syncthreads();
       int64_t before = run, total = run;
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        if (w < warp) before += scratch[w];
-        total += scratch[w];
+      for (int v = 0; v < kW; ++v) {
+        if (v < warp) before += scratch[v];
+        total += scratch[v];
       }
       const int64_t excl = before + inc - n;
-      if (pass == 0) {
-        if (blockIdx.x == 0 && r < a.num_reqs) a.offs[r] = excl;
-      } else if (n > 0 && excl <= u0 && u0 < excl + n) {
+      if (pass == 1 && n > 0 && excl <= sh.u && sh.u < excl + n) {
         scratch[kW] = r;
-        scratch[kW + 1] = u0 - excl;
+        scratch[kW + 1] = sh.u - excl;
       }
       run = total;
       __syncthreads();
-      if (pass == 1 && run > u0) break;   // block-uniform
+      if (pass == 1 && run > sh.u) break;   // block-uniform
     }
     if (pass == 0) {
-      U = run;
-      if (blockIdx.x == 0 && tid == 0) a.offs[a.num_reqs] = U;
-      C = T::ctas(U, a.ctas);
-      if (U == 0 || static_cast<int>(blockIdx.x) >= C) {
-        u0 = u1 = 0;
-        req = 0;
-        off = 0;
-        return;
-      }
-      u0 = T::begin(U, C, blockIdx.x);
-      u1 = T::begin(U, C, blockIdx.x + 1);
+      sh.U = run;
+      sh.workers = S::workers(run, most);
+      if (run == 0 || w >= sh.workers) return sh;
+      sh.u = S::begin(run, sh.workers, w);
+      sh.end = S::begin(run, sh.workers, w + 1);
     }
   }
-  req = static_cast<int>(scratch[kW]);
-  off = scratch[kW + 1];
+  sh.req = static_cast<int>(scratch[kW]);
+  sh.off = scratch[kW + 1];
   __syncthreads();
+  return sh;
 }
 
 // Bits [x0, x0 + 32) of a token's tree mask (bits outside the row's words are

@@ -20,16 +20,20 @@ namespace pkv {
 namespace {
 
 constexpr int kRowsThreads = 32 * kRowWarps;
-// Rows kernel: 16 query rows a group, one block a unit; a CTA takes at least
-// four blocks a warp.
-using RowsTiling = Tiling<kRowTile, kBlockSize, 16>;
+// Rows kernel: a group has 16 query rows and one KV head, a unit is one block;
+// a CTA takes at least four blocks a warp.  A request without keys keeps one
+// (empty) unit a group: its rows are written too.
+using RowsShare = Share<4 * kRowWarps>;
+__device__ __forceinline__ int rows_tiles(const TreeReq& q, int group) {
+  return static_cast<int>((static_cast<int64_t>(q.n) * group + kRowTile - 1) / kRowTile);
+}
+__device__ __forceinline__ int rows_blocks(const TreeReq& q) { return max(1, (q.ctx + kBlockSize - 1) / kBlockSize); }
 
 // One segment: blocks [b0, b0 + nb) of one (request, KV head, row tile).
 template <int D, bool F8>
 __global__ void __launch_bounds__(kRowsThreads, 3)
 tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using S = RowsSmem<D, F8>;
-  using T = RowsTiling;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kBuf);
@@ -40,16 +44,16 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, Hkv = a.pool.num_kv_heads;
   const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
+  if (tid == 0) a.cuts[blockIdx.x].count = 0;
   if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
   if (tid == 0) {
     for (int i = 0; i < kRowWarps * S::kStages; ++i) mbar_init(&bars[i], 1);
     s_flags[0] = s_flags[1] = 0;
     fence_mbar_init();
   }
-  int64_t U, u0, u1, off;
-  int C, req;
-  tree_locate<T, kRowsThreads>(a, scratch, U, C, u0, u1, req, off);
-  if (u0 >= u1) return;
+  auto units = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv * rows_blocks(q); };
+  TreeShare sh = tree_share<RowsShare, kRowsThreads>(a, scratch, blockIdx.x, a.ctas, units);
+  if (sh.u >= sh.end) return;
   __syncthreads();
 
   uint8_t* my_ring = ring + warp * S::kStages * S::kStage;
@@ -57,18 +61,18 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
   const uint32_t my_addr = smem_u32(my_ring);
   const float sl2 = F8 ? a.scale_log2 * a.pool.k_scale : a.scale_log2;
   int cnt = 0;   // stages this warp has issued in the launch
+  int req = sh.req;
   TreeReq rq = tree_req(a, req);
-  int64_t left = u1 - u0;
-  while (left > 0) {
-    while (off >= T::units(rq, G, Hkv)) {   // next request with work (there is one: left > 0)
-      off -= T::units(rq, G, Hkv);
+  while (sh.u < sh.end) {
+    for (int64_t n = units(rq); sh.off >= n; n = units(rq)) {   // the next request with work (there is one)
+      sh.off -= n;
       if (++req >= a.num_reqs) return;
       rq = tree_req(a, req);
     }
-    const int kblk = T::kblk(rq), ntile = T::tiles(rq, G);
-    const int grp = static_cast<int>(off / kblk);
-    const int b0 = static_cast<int>(off % kblk);
-    const int nb = static_cast<int>(min(static_cast<int64_t>(kblk - b0), left));
+    const int kblk = rows_blocks(rq), ntile = rows_tiles(rq, G);
+    const int grp = static_cast<int>(sh.off / kblk);
+    const int b0 = static_cast<int>(sh.off % kblk);
+    const int nb = static_cast<int>(min(static_cast<int64_t>(kblk - b0), sh.end - sh.u));
     const int g = grp / ntile, tile = grp % ntile;
     const int row0 = tile * kRowTile, nrows = min(kRowTile, rq.n * G - row0);
     // Rows g' and g' + 8 of this thread.
@@ -215,55 +219,55 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
     if (tid == 0) *s_odd = 0;
     fence_proxy_async_smem();
     __syncthreads();
-    off += nb;
-    left -= nb;
+    if (b0 == 0 && nb < kblk && tid == 0) {   // the group's first part: its other owners follow
+      const int c1 = RowsShare::owner(sh.U, sh.workers, sh.u + kblk - 1);
+      TreeCut& cut = a.cuts[blockIdx.x];
+      cut.first = 2 * blockIdx.x + 1;
+      cut.next = 2 * (blockIdx.x + 1);
+      cut.stride = 2;
+      cut.tok_a = rq.t0;
+      cut.rows_a = nrows;
+      cut.tok_b = cut.rows_b = 0;
+      cut.f0 = row0;
+      cut.g = g;
+      cut.count = c1 - static_cast<int>(blockIdx.x) + 1;
+    }
+    sh.off += nb;
+    sh.u += nb;
   }
 }
 
-// One warp per (token, query head): merges the partials of a group that
-// several CTAs share.  LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c,
-// in CTA order.
-template <int D, class T>
+// One warp per row of a cut group: merges its partials in the workers' order.
+// LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c.
+template <int D, int SlotRows>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kDPL = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the attention kernel's writes
-  if (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT) return;   // the partials may be incomplete
   const int lane = threadIdx.x & 31;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= static_cast<int64_t>(a.num_tokens) * a.num_q_heads) return;
-  const int t = static_cast<int>(w / a.num_q_heads), h = static_cast<int>(w % a.num_q_heads);
-  // The request that holds token t: the last with cu <= t (tokens past the end belong to none).
-  int lo = 0, hi = a.num_reqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.cu_q_lens + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  const TreeReq q = tree_req(a, lo);
-  if (t < q.t0 || t >= q.t0 + q.n) return;
-  const int64_t U = __ldcg(a.offs + a.num_reqs), base = __ldcg(a.offs + lo);
-  if (U <= 0) return;
-  const int C = T::ctas(U, a.ctas);
-  const int kblk = T::kblk(q), ntile = T::tiles(q, a.group);
-  const int g = h / a.group, f = (t - q.t0) * a.group + h % a.group;
-  const int64_t u0 = base + (static_cast<int64_t>(g) * ntile + f / T::kRows) * kblk;
-  const int c0 = T::owner(U, C, u0), c1 = T::owner(U, C, u0 + kblk - 1);
-  if (c0 < 0 || c0 >= c1 || c1 >= C) return;   // one CTA wrote the row
-  const int rr = f % T::kRows;
-  auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * T::kRows + rr; };
+  const int row = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5);
+  const int4* rec = reinterpret_cast<const int4*>(a.cuts + blockIdx.x);
+  const int4 s = __ldcg(rec);
+  if (s.x < 2 || (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT)) return;   // (partials may be incomplete)
+  const int4 tk = __ldcg(rec + 1), fg = __ldcg(rec + 2);
+  const int tok = row < 128 ? tk.x : tk.z, i = row & 127;
+  if (i >= (row < 128 ? tk.y : tk.w)) return;
+  auto slot_row = [&](int c) {
+    return static_cast<int64_t>(c == 0 ? s.y : s.z + (c - 1) * s.w) * SlotRows + row;
+  };
   float M = -CUDART_INF_F;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(a.part_lse + slot(c)));
+  for (int c = lane; c < s.x; c += 32) M = fmaxf(M, __ldcg(a.part_lse + slot_row(c)));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float acc[kDPL], sum = 0.f;
 #pragma unroll
   for (int d = 0; d < kDPL; ++d) acc[d] = 0.f;
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float e = __ldcg(a.part_lse + slot(c));
+  for (int c = 0; c < s.x; ++c) {
+    const float e = __ldcg(a.part_lse + slot_row(c));
     if (e == -CUDART_INF_F) continue;   // no key of this row there
     const float wgt = fast_exp2(e - M);
     sum += wgt;
-    const float* src = a.part_o + slot(c) * D + lane * kDPL;
+    const float* src = a.part_o + slot_row(c) * D + lane * kDPL;
 #pragma unroll
     for (int d = 0; d < kDPL; d += 2) {
       const float2 v = __ldcg(reinterpret_cast<const float2*>(src + d));
@@ -272,13 +276,12 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) +
-                                              (static_cast<int64_t>(t) * a.num_q_heads + h) * D + lane * kDPL);
+  const int f = fg.x + i;
+  const int64_t at = static_cast<int64_t>(tok + f / a.group) * a.num_q_heads + fg.y * a.group + f % a.group;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at * D + lane * kDPL);
 #pragma unroll
   for (int d = 0; d < kDPL; d += 2) dst[d / 2] = pack_bf16x2(acc[d] * inv, acc[d + 1] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[static_cast<int64_t>(t) * a.num_q_heads + h] =
-        sum == 0.f ? -CUDART_INF_F : (M + fast_log2(sum)) * 0.69314718055994530942f;
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (M + fast_log2(sum)) * 0.69314718055994530942f;
 }
 
 // Ancestor bits from parents: token i of a request sets its own bit and its
@@ -323,11 +326,10 @@ int launch_rows(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tm
   return cudaGetLastError();
 }
 
-template <int D, class T>
-int launch_merge_t(const TreeArgs& a, cudaStream_t s) {
-  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+template <int D, int SlotRows>
+int launch_merge_t(const TreeArgs& a, int cuts, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.gridDim = dim3(cuts, SlotRows / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -335,16 +337,22 @@ int launch_merge_t(const TreeArgs& a, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T>, a);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, SlotRows>, a);
 }
 
 }  // namespace
 
-int tree_ctas(const PoolView&, int num_sms) { return num_sms * 3; }
+TreeForm tree_form(bool tensor, int num_sms) {
+  TreeForm f;
+  f.tensor = tensor;
+  f.ctas = tensor ? num_sms : 3 * num_sms;
+  f.cuts = tensor ? 2 * f.ctas : f.ctas;             // the tensor-core form has two lines of work
+  f.slot_rows = tensor ? 256 : kRowTile;
+  f.slots = 2 * f.cuts;
+  return f;
+}
 
-size_t tree_part_rows(int ctas) { return static_cast<size_t>(2) * ctas * kRowTile; }
-
-int launch_tree(const TreeArgs& a, const void* tmk, const void* tmv, void* stream) {
+int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const CUtensorMap* k = static_cast<const CUtensorMap*>(tmk);
   const CUtensorMap* v = static_cast<const CUtensorMap*>(tmv);
@@ -353,9 +361,11 @@ int launch_tree(const TreeArgs& a, const void* tmk, const void* tmv, void* strea
   return f8 ? launch_rows<64, true>(a, k, v, s) : launch_rows<64, false>(a, k, v, s);
 }
 
-int launch_tree_merge(const TreeArgs& a, void* stream) {
+int launch_tree_merge(const TreeArgs& a, const TreeForm& f, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return a.pool.head_dim == 128 ? launch_merge_t<128, RowsTiling>(a, s) : launch_merge_t<64, RowsTiling>(a, s);
+  if (f.tensor)
+    return a.pool.head_dim == 128 ? launch_merge_t<128, 256>(a, f.cuts, s) : launch_merge_t<64, 256>(a, f.cuts, s);
+  return a.pool.head_dim == 128 ? launch_merge_t<128, kRowTile>(a, f.cuts, s) : launch_merge_t<64, kRowTile>(a, f.cuts, s);
 }
 
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,

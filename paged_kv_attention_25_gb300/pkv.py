@@ -36,6 +36,7 @@ PKV_DEVERR_NO_PAGES = 16
 PKV_DEBUG_WAIT_LIMIT_NS = 1
 PKV_DEBUG_WITHHOLD_COPY = 2
 PKV_DEBUG_FUSED_FORM = 3
+PKV_DEBUG_TREE_FORM = 4
 
 KERNELS = ("append", "split_kv", "tensor_core", "merge", "swap")
 
@@ -143,7 +144,7 @@ def load_library():
             "pkv_cache_release": [P, I],
             "pkv_cache_free_blocks": [P, ctypes.POINTER(I), ctypes.POINTER(I)],
             "pkv_tree_mask": [P, P, P, I, I, P, I, P],
-            "pkv_tree_attn_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_tree_attn_workspace_size": [P, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
             "pkv_tree_attn": [P, P, I, P, I, P, P, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
             "pkv_summarize": [P, P, I, I, P, P, P, I, P, P, P],
             "pkv_select_blocks": [P, P, I, P, P, I, P, I, I, P, P, I, I, I, P, P],
@@ -454,9 +455,10 @@ def pkv_tree_mask(pool: Pool, parents, cu_q_lens, mask_words=None, max_nodes=Non
     return out
 
 
-def pkv_tree_attn_workspace_size(pool: Pool, num_q_heads: int, num_reqs: int) -> int:
+def pkv_tree_attn_workspace_size(pool: Pool, num_q_heads: int, num_reqs: int, num_tokens: int) -> int:
     n = ctypes.c_size_t()
-    _check(load_library().pkv_tree_attn_workspace_size(pool.handle, num_q_heads, num_reqs, ctypes.byref(n)))
+    _check(load_library().pkv_tree_attn_workspace_size(pool.handle, num_q_heads, num_reqs, num_tokens,
+                                                       ctypes.byref(n)))
     return n.value
 
 
@@ -475,7 +477,7 @@ def pkv_tree_attn(pool: Pool, q, block_tables, ctx_lens, prefix_lens, cu_q_lens,
     _op_dev(pool, tree_mask, "tree_mask", torch.int32, (T, None))
     out, lse = _op_out(pool, q, out, lse, want_lse, stream)
     workspace = _op_workspace(pool, workspace, 0 if workspace is not None
-                              else pkv_tree_attn_workspace_size(pool, Hq, R), stream)
+                              else pkv_tree_attn_workspace_size(pool, Hq, R, T), stream)
     _check(load_library().pkv_tree_attn(pool.handle, _ptr(q), Hq, _ptr(block_tables), block_tables.shape[1],
                                         _ptr(ctx_lens), _ptr(prefix_lens), _ptr(cu_q_lens), R, T, _ptr(tree_mask),
                                         tree_mask.shape[1], float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -759,8 +761,9 @@ def pkv_profile_enable(pool: Pool, on=True):
 
 
 def pkv_debug_set(pool: Pool, what: int, value: int):
-    """Test settings: PKV_DEBUG_WAIT_LIMIT_NS (bounded-wait limit), PKV_DEBUG_WITHHOLD_COPY (0, 1, 2) or
-    PKV_DEBUG_FUSED_FORM (0 per batch, 1 in-kernel append, 2 append first)."""
+    """Test settings: PKV_DEBUG_WAIT_LIMIT_NS (bounded-wait limit), PKV_DEBUG_WITHHOLD_COPY (0, 1, 2),
+    PKV_DEBUG_FUSED_FORM (0 per batch, 1 in-kernel append, 2 append first) or PKV_DEBUG_TREE_FORM (0 per batch, 1 rows
+    of 16, 2 tiles of 128)."""
     _check(load_library().pkv_debug_set(pool.handle, int(what), int(value)))
 
 

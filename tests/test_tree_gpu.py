@@ -16,6 +16,12 @@ def built():
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
 
 
+@pytest.fixture(params=[1, 2], ids=["rows", "tiles"], autouse=True)
+def form(request):
+    """Every test runs with both kernels: on 16 rows, and on tiles of 128."""
+    Case.form = request.param
+
+
 class Case:
     """A batch of drafted trees over a pool of random values."""
 
@@ -32,6 +38,7 @@ class Case:
         nblk = sum((int(c) + 15) // 16 for c in self.ctx) + 5
         kw = dict(dtype=dtype, k_scale=scales[0], v_scale=scales[1]) if dtype != "bf16" else {}
         self.pool = ref.random_pool(pkv.Pool(nblk, hkv, d, **kw), seed)
+        pkv.pkv_debug_set(self.pool, pkv.PKV_DEBUG_TREE_FORM, self.form)
         self.bt = ref.tables(rng, self.ctx, nblk)
         self.words = max(1, (max(drafts + [1]) + 31) // 32) if words is None else words
         self.bits = np.zeros((self.T, self.words * 32), bool)
@@ -189,7 +196,7 @@ def test_runs_are_repeatable_and_lse_is_optional():
 
 def test_other_stream_and_own_workspace():
     c = Case(19, [(700, 33), (90, 12)], 8, 2, 128)
-    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, 2), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, 2, c.T), dtype=torch.uint8, device="cuda")
     ws.fill_(0xFF)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -203,7 +210,7 @@ def test_captured_call_follows_lengths_tables_and_masks():
     bt, ctx, pre, cu, mask = (
         ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.prefix), ref.dev(c.cu), c.mask())
     out, lse = torch.zeros_like(c.q), torch.zeros((c.T, 8), device="cuda")
-    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, 3), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, 3, c.T), dtype=torch.uint8, device="cuda")
 
     def call():
         pkv.pkv_tree_attn(c.pool, c.q, bt, ctx, pre, cu, mask, c.scale, out=out, lse=lse, workspace=ws)
@@ -227,6 +234,14 @@ def test_captured_call_follows_lengths_tables_and_masks():
         torch.cuda.synchronize()
         c.check(out, lse)
     assert pkv.pkv_check_device_errors(c.pool) == 0
+
+
+def test_trees_of_many_tiles():
+    """1 to 9 tiles of 128 rows, ragged last ones, over contexts that are cut between workers."""
+    Case(22, [(200, 9), (1000, 130), (77, 65), (300, 40), (2000, 33), (64, 17), (5, 50), (129, 1)], 64, 8, 64).run_check()
+    Case(23, [(3000, 100), (10, 51), (500, 26)], 15, 3, 128).run_check()
+    Case(24, [(1500, 9), (20, 4), (130, 1)], 128, 1, 128).run_check()
+    Case(25, [(700, 290)], 16, 4, 128, "fp8_e4m3").run_check()
 
 
 def test_large_logits():
