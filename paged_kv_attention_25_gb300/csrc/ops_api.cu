@@ -159,6 +159,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   a.ctas = form.ctas;
   a.tile_tokens = kTcRows / a.group;
   a.q_box_tokens = 0;
+  a.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   a.wait_ns = pool->wait_ns;
   if (form.tensor) {
     CUtensorMap tmap_q;

@@ -39,6 +39,7 @@ struct TreeArgs {
   int ctas;          // CTAs of the attention launch
   int tile_tokens;   // tensor-core form: tokens of a tile of 128 rows
   int q_box_tokens;  // ... and of a copy of its query map
+  int o_align32;     // o is 32-byte aligned
   uint64_t wait_ns;
 };
 
@@ -91,58 +92,94 @@ struct TreeShare {
   int workers, req;
 };
 
-// Block-wide: worker w's share of the line in which request r has
-// units(tree_req(a, r)) units.  scratch: one int64 per warp and two more.
-template <class S, int Threads, class F>
-__device__ __forceinline__ TreeShare tree_share(const TreeArgs& a, int64_t* scratch, int w, int most, F&& units) {
+// Block-wide: the shares of worker w[i] of most[i] in NL lines, request r
+// having units(tree_req(a, r), i) units in line i.  One pass over the requests
+// (kept in registers) when there are no more of them than threads, two
+// otherwise.  scratch: NL * (warps + 2) int64.
+template <class S, int Threads, int NL, class F>
+__device__ __forceinline__ void tree_shares(const TreeArgs& a, int64_t* scratch, const int (&w)[NL],
+                                            const int (&most)[NL], TreeShare (&sh)[NL], F&& units) {
   constexpr int kW = Threads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  TreeShare sh{0, 0, 0, 0, 1, 0};
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t run = 0;
-    for (int base = 0; base < a.num_reqs; base += Threads) {
-      const int r = base + tid;
-      int64_t n = 0;
-      if (r < a.num_reqs) {
-        const TreeReq q = tree_req(a, r);
-        n = units(q);
-        if (pass == 0 && q.bad && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
-      }
-      int64_t inc = n;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) sh[i] = TreeShare{0, 0, 0, 0, 1, 0};
+  int64_t run[NL], n[NL], excl[NL];
+  auto scan = [&](int base, bool check) {   // units and exclusive offset of request base + tid; run: total so far
+    const int r = base + tid;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) n[i] = 0;
+    if (r < a.num_reqs) {
+      const TreeReq q = tree_req(a, r);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) n[i] = units(q, i);
+      if (check && q.bad && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      int64_t inc = n[i];
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, inc, x);
         if (lane >= x) inc += y;
       }
-      if (lane == 31) scratch[warp] = inc;
-      __syncthreads();
-      int64_t before = run, total = run;
+      if (lane == 31) scratch[i * (kW + 2) + warp] = inc;
+      excl[i] = inc - n[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      int64_t total = run[i];
+      excl[i] += run[i];
 #pragma unroll
       for (int v = 0; v < kW; ++v) {
-        if (v < warp) before += scratch[v];
-        total += scratch[v];
+        const int64_t x = scratch[i * (kW + 2) + v];
+        if (v < warp) excl[i] += x;
+        total += x;
       }
-      const int64_t excl = before + inc - n;
-      if (pass == 1 && n > 0 && excl <= sh.u && sh.u < excl + n) {
-        scratch[kW] = r;
-        scratch[kW + 1] = sh.u - excl;
-      }
-      run = total;
-      __syncthreads();
-      if (pass == 1 && run > sh.u) break;   // block-uniform
+      run[i] = total;
     }
-    if (pass == 0) {
-      sh.U = run;
-      sh.workers = S::workers(run, most);
-      if (run == 0 || w >= sh.workers) return sh;
-      sh.u = S::begin(run, sh.workers, w);
-      sh.end = S::begin(run, sh.workers, w + 1);
+  };
+  auto find = [&](int base) {   // leaves the request that holds the share's first unit, and the unit's offset in it
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (n[i] > 0 && sh[i].u < sh[i].end && excl[i] <= sh[i].u && sh[i].u < excl[i] + n[i]) {
+        scratch[i * (kW + 2) + kW] = base + tid;
+        scratch[i * (kW + 2) + kW + 1] = sh[i].u - excl[i];
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < NL; ++i) run[i] = 0;
+  for (int base = 0; base < a.num_reqs; base += Threads) {
+    scan(base, true);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    sh[i].U = run[i];
+    sh[i].workers = S::workers(run[i], most[i]);
+    if (run[i] > 0 && w[i] < sh[i].workers) {
+      sh[i].u = S::begin(run[i], sh[i].workers, w[i]);
+      sh[i].end = S::begin(run[i], sh[i].workers, w[i] + 1);
     }
   }
-  sh.req = static_cast<int>(scratch[kW]);
-  sh.off = scratch[kW + 1];
+  if (a.num_reqs <= Threads) {
+    find(0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) run[i] = 0;
+    for (int base = 0; base < a.num_reqs; base += Threads) {
+      scan(base, false);
+      find(base);
+      __syncthreads();
+    }
+  }
   __syncthreads();
-  return sh;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    sh[i].req = static_cast<int>(scratch[i * (kW + 2) + kW]);
+    sh[i].off = scratch[i * (kW + 2) + kW + 1];
+  }
+  __syncthreads();
 }
 
 // Bits [x0, x0 + 32) of a token's tree mask (bits outside the row's words are
@@ -159,10 +196,10 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
 // The lowest n bits (n <= 0: none, n >= 32: all).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// Keys [key0, key0 + 32) that a token of request q sees, as bits.
-__device__ __forceinline__ uint32_t tree_sees(const TreeReq& q, const uint32_t* row, int words, int key0) {
-  const uint32_t tree = tree_bits(row, words, key0 - q.prefix) & ~low_bits(q.prefix - key0);
-  return (low_bits(q.prefix - key0) | tree) & low_bits(q.ctx - key0);
+// Keys [key0, key0 + 32) that a token of a request sees, as bits.
+__device__ __forceinline__ uint32_t tree_sees(int prefix, int ctx, const uint32_t* row, int words, int key0) {
+  const uint32_t tree = tree_bits(row, words, key0 - prefix) & ~low_bits(prefix - key0);
+  return (low_bits(prefix - key0) | tree) & low_bits(ctx - key0);
 }
 
 }  // namespace pkv

@@ -44,6 +44,7 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, Hkv = a.pool.num_kv_heads;
   const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
+  griddep_launch();   // the merge may take its place and wait
   if (tid == 0) a.cuts[blockIdx.x].count = 0;
   if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
   if (tid == 0) {
@@ -52,7 +53,11 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
     fence_mbar_init();
   }
   auto units = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv * rows_blocks(q); };
-  TreeShare sh = tree_share<RowsShare, kRowsThreads>(a, scratch, blockIdx.x, a.ctas, units);
+  const int worker[1] = {static_cast<int>(blockIdx.x)}, most[1] = {a.ctas};
+  TreeShare shares[1];
+  tree_shares<RowsShare, kRowsThreads, 1>(a, scratch, worker, most, shares,
+                                          [&](const TreeReq& q, int) { return units(q); });
+  TreeShare& sh = shares[0];
   if (sh.u >= sh.end) return;
   __syncthreads();
 
@@ -136,8 +141,8 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
         if (key0 + kBlockSize <= rq.prefix)
           rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
         else
-          rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq, m0, a.mask_words, key0),
-                                  tree_sees(rq, m1, a.mask_words, key0), lane);
+          rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
+                                  tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
       }
       __syncwarp();
       if (issued < nb_w) {
@@ -186,7 +191,7 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
         // V elements that are not finite, for the rows that see them.
         const uint32_t* mr = a.mask + static_cast<int64_t>(t) * a.mask_words;
         for (int b = max(b0, rq.prefix / kBlockSize); b < end_blk; ++b) {
-          const uint32_t vis = tree_sees(rq, mr, a.mask_words, b * kBlockSize);
+          const uint32_t vis = tree_sees(rq.prefix, rq.ctx, mr, a.mask_words, b * kBlockSize);
           const int pb = __ldg(bt_row + b);
           if (pb < 0 || pb >= a.pool.num_blocks) continue;
           for (int k = 0; k < kBlockSize; ++k) {
@@ -237,51 +242,86 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
   }
 }
 
-// One warp per row of a cut group: merges its partials in the workers' order.
-// LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c.
+// One warp per kRows rows of a cut group: merges their partials in the workers'
+// order.  LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c.  The
+// rows' loads are independent, so that a warp has kRows of them in flight:
+// with one row a warp the kernel waited for its loads (28 us against 9 for 190
+// groups of 256 rows, two to three partials each).
 template <int D, int SlotRows>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kDPL = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the attention kernel's writes
+  constexpr int kRows = SlotRows >= 128 ? 4 : 2;
+  griddep_wait();   // the attention kernel's writes
   const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5);
+  const int row0 = (static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5)) * kRows;
   const int4* rec = reinterpret_cast<const int4*>(a.cuts + blockIdx.x);
   const int4 s = __ldcg(rec);
-  if (s.x < 2 || (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT)) return;   // (partials may be incomplete)
   const int4 tk = __ldcg(rec + 1), fg = __ldcg(rec + 2);
-  const int tok = row < 128 ? tk.x : tk.z, i = row & 127;
-  if (i >= (row < 128 ? tk.y : tk.w)) return;
+  if (s.x < 2 || (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT)) return;   // (partials may be incomplete)
+  // The rows of a warp lie in one tile (kRows divides 128).
+  const int tok = row0 < 128 ? tk.x : tk.z, rows = row0 < 128 ? tk.y : tk.w, i0 = row0 & 127;
+  if (i0 >= rows) return;
   auto slot_row = [&](int c) {
-    return static_cast<int64_t>(c == 0 ? s.y : s.z + (c - 1) * s.w) * SlotRows + row;
+    return static_cast<int64_t>(c == 0 ? s.y : s.z + (c - 1) * s.w) * SlotRows + row0;
   };
-  float M = -CUDART_INF_F;
-  for (int c = lane; c < s.x; c += 32) M = fmaxf(M, __ldcg(a.part_lse + slot_row(c)));
+  float M[kRows], sum[kRows], acc[kRows][kDPL];
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float acc[kDPL], sum = 0.f;
+  for (int k = 0; k < kRows; ++k) {
+    M[k] = -CUDART_INF_F;
+    sum[k] = 0.f;
 #pragma unroll
-  for (int d = 0; d < kDPL; ++d) acc[d] = 0.f;
-#pragma unroll 4
+    for (int d = 0; d < kDPL; ++d) acc[k][d] = 0.f;
+  }
+  for (int c = lane; c < s.x; c += 32) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (i0 + k < rows) M[k] = fmaxf(M[k], __ldcg(a.part_lse + slot_row(c) + k));
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], x));
+#pragma unroll 2
   for (int c = 0; c < s.x; ++c) {
-    const float e = __ldcg(a.part_lse + slot_row(c));
-    if (e == -CUDART_INF_F) continue;   // no key of this row there
-    const float wgt = fast_exp2(e - M);
-    sum += wgt;
-    const float* src = a.part_o + slot_row(c) * D + lane * kDPL;
+    const int64_t at = slot_row(c);
+    float e[kRows], v[kRows][kDPL];
 #pragma unroll
-    for (int d = 0; d < kDPL; d += 2) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(src + d));
-      acc[d] = fmaf(wgt, v.x, acc[d]);
-      acc[d + 1] = fmaf(wgt, v.y, acc[d + 1]);
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = at + (i0 + k < rows ? k : 0);
+      e[k] = __ldcg(a.part_lse + r);
+      const float* src = a.part_o + r * D + lane * kDPL;
+      if constexpr (kDPL == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        v[k][0] = x.x; v[k][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (e[k] == -CUDART_INF_F) continue;   // no key of this row there
+      const float wgt = fast_exp2(e[k] - M[k]);
+      sum[k] += wgt;
+#pragma unroll
+      for (int d = 0; d < kDPL; ++d) acc[k][d] = fmaf(wgt, v[k][d], acc[k][d]);
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int f = fg.x + i;
-  const int64_t at = static_cast<int64_t>(tok + f / a.group) * a.num_q_heads + fg.y * a.group + f % a.group;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at * D + lane * kDPL);
 #pragma unroll
-  for (int d = 0; d < kDPL; d += 2) dst[d / 2] = pack_bf16x2(acc[d] * inv, acc[d + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (M + fast_log2(sum)) * 0.69314718055994530942f;
+  for (int k = 0; k < kRows; ++k) {
+    if (i0 + k >= rows) break;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+    const int f = fg.x + i0 + k;
+    const int64_t at = static_cast<int64_t>(tok + f / a.group) * a.num_q_heads + fg.y * a.group + f % a.group;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at * D + lane * kDPL);
+    if constexpr (kDPL == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv),
+                                                  pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv));
+    else
+      *dst = pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv);
+    if (lane == 0 && a.lse)
+      a.lse[at] = sum[k] == 0.f ? -CUDART_INF_F : (M[k] + fast_log2(sum[k])) * 0.69314718055994530942f;
+  }
 }
 
 // Ancestor bits from parents: token i of a request sets its own bit and its
@@ -329,7 +369,7 @@ int launch_rows(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tm
 template <int D, int SlotRows>
 int launch_merge_t(const TreeArgs& a, int cuts, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(cuts, SlotRows / 8);
+  cfg.gridDim = dim3(cuts, SlotRows >= 128 ? SlotRows / 32 : 1);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at{};

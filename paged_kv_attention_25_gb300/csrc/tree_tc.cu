@@ -3,8 +3,10 @@
 //
 // One CTA per SM with the warp roles of the prefill kernel (K and V producers
 // that gather blocks by TMA, one MMA issuer, two softmax warpgroups A and B,
-// scores, P and O in TMEM), but no work list: lengths are read on the device
-// and every role walks the CTA's share of the work by the same arithmetic.
+// scores, P and O in TMEM), but no work list: lengths are read on the device,
+// and a twelfth warp walks the CTA's share of the work and hands segments to
+// the others through a ring in shared memory, ahead of their use (each role
+// walking by itself cost 3 to 6 us a segment, most of it instruction misses).
 //
 // A request's query rows form tiles of 128 (whole tokens).  Two warpgroups keep
 // the tensor pipe busy when there is something for both, so a step takes
@@ -14,10 +16,11 @@
 //   pair    two tiles on one CTA;
 //   single  one tile: A takes the even key tiles, B the odd ones, and A joins
 //           B's state (read from its TMEM columns) at the end.
-// Quads form one line of work, shared out over pairs of CTAs in units of 128
-// keys; pairs (128 keys) and singles (256 keys) form a second one over CTAs: a
-// unit is the same tensor work everywhere (two S = Q K^T and two O += P V
-// products of 128 x 128 x D a CTA).
+// Quads form one line of work, shared out over pairs of CTAs; pairs and singles
+// form a second one over CTAs.  A key tile of a quad or a pair costs a CTA two S
+// and two PV products (three units), one of a single half of that but the same
+// copies (two units); every group costs kGroupUnits besides, for its start and
+// its epilogue.
 //
 // Masks: key tiles that end at or before the prefix are seen whole.  In the others
 // each row's thread forms its 128 visibility bits from its mask words.  The V
@@ -39,10 +42,13 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kBlkPerTile = kNK / kBlockSize;   // 8
-constexpr int kSegRing = 8;                     // segments the V producer may be ahead
-using TcShare = Share<2>;
+constexpr int kSegSlots = 4;                    // segments handed out ahead
+constexpr int kSegRing = 8;                     // V producer's reports (it is at most kSegSlots + 1 ahead)
+constexpr int kSegReaders = 11;                 // warps that read a segment
+constexpr int kPairUnits = 3, kSingleUnits = 2, kGroupUnits = 6;
+using TcShare = Share<kPairUnits + kGroupUnits>;
 
 template <int KS, int VS>
 struct TreeBars {
@@ -59,8 +65,19 @@ struct TreeBars {
   static constexpr int kJoined = kT + 13;   // single: A has read it (128 arrivals)
   static constexpr int kDrain = kT + 14;
   static constexpr int kVDone = kT + 15;    // + segment % kSegRing: its V tiles are all handed over
-  static constexpr int kCount = kT + 15 + kSegRing;
+  static constexpr int kSegFull = kT + 15 + kSegRing;               // + segment % kSegSlots: published
+  static constexpr int kSegEmpty = kSegFull + kSegSlots;            // + segment % kSegSlots: read by every role
+  static constexpr int kCount = kSegEmpty + kSegSlots;
 };
+
+// What one CTA does with one group: key tiles [kt0, kt1) of a request.
+struct alignas(16) Seg {
+  int req, g, prefix, ctx;
+  int tok0, tok1, rows0, rows1;   // query tiles (rows1 = 0: single)
+  int kt0, kt1, slot, flags;
+};
+static_assert(sizeof(Seg) == 48, "Seg layout: three 16-byte loads");
+constexpr int kSegSingle = 1, kSegWhole = 2, kSegMissing = 4, kSegEnd = 8;
 
 template <int D>
 struct TreeSmem {
@@ -68,106 +85,117 @@ struct TreeSmem {
   using B = TreeBars<S::kKSt, S::kVSt>;
   static constexpr int kOffBar = S::kOffBar;
   static constexpr int kOffMl = kOffBar + ((B::kCount * 8 + 15) / 16) * 16;   // float2 [128]: B's m, l
-  static constexpr int kOffMisc = kOffMl + kTcRows * 8;
-  static constexpr int kTotal = kOffMisc + 64 + 2 * static_cast<int>(sizeof(TreeShare));
+  static constexpr int kOffSeg = kOffMl + kTcRows * 8;
+  static constexpr int kOffMisc = kOffSeg + kSegSlots * static_cast<int>(sizeof(Seg));
+  static constexpr int kTotal = kOffMisc + 64;
 };
 static_assert(TreeSmem<128>::kTotal <= 232448, "shared memory of the D = 128 kernel");
-
-// What one CTA does with one group: key tiles [kt0, kt1) of a request.
-struct Seg {
-  TreeReq rq;
-  int req, g;
-  int tok0, tok1, rows0, rows1;   // query tiles (rows1 = 0: single)
-  int kt0, kt1;
-  bool single, whole, opens;      // whole: the group's result is final; opens: begins the group
-  int line, worker_units;         // line; units of the group from this segment's first on
-};
 
 __device__ __forceinline__ int key_tiles(const TreeReq& q) { return max(1, (q.ctx + kNK - 1) / kNK); }
 __device__ __forceinline__ int query_tiles(const TreeReq& q, int tile_tokens) {
   return (q.n + tile_tokens - 1) / tile_tokens;
 }
 __device__ __forceinline__ int64_t quad_units(const TreeReq& q, int tile_tokens, int hkv) {
-  return static_cast<int64_t>(query_tiles(q, tile_tokens) / 4) * hkv * key_tiles(q);
+  return static_cast<int64_t>(query_tiles(q, tile_tokens) / 4) * hkv * (kPairUnits * key_tiles(q) + kGroupUnits);
 }
 __device__ __forceinline__ int64_t rest_units(const TreeReq& q, int tile_tokens, int hkv) {
   const int rem = query_tiles(q, tile_tokens) % 4, kt = key_tiles(q);
-  return static_cast<int64_t>(hkv) * ((rem >> 1) * kt + (rem & 1) * ((kt + 1) / 2));
+  return static_cast<int64_t>(hkv) * ((rem >> 1) * (kPairUnits * kt + kGroupUnits) +
+                                      (rem & 1) * (kSingleUnits * kt + kGroupUnits));
 }
 
-// Walks a CTA's two shares: the quads, then the rest.
+// Walks a CTA's two shares: the quads, then the rest.  Key tile k of a group
+// that begins at unit 0 belongs to the worker that holds unit k * cost; the
+// group's fixed units follow its last tile.
 struct Walk {
   TreeShare sh[2];
   TreeReq rq;
   int line, req;
   bool fresh;   // rq is not the current request's yet
 
-  __device__ __forceinline__ void start(const TreeShare* s) {
-    sh[0] = s[0];
-    sh[1] = s[1];
-    line = 0;
-    fresh = true;
-  }
-  __device__ __forceinline__ bool next(const TreeArgs& a, Seg& s) {
+  // The next segment with key tiles.  cut: the record of a group that this CTA begins and others go on with.
+  __device__ __forceinline__ bool next(const TreeArgs& a, Seg& s, TreeCut& cut) {
     const int hkv = a.pool.num_kv_heads, tt = a.tile_tokens;
-    TreeShare* h = &sh[0];
-    if (line == 0 && sh[0].u >= sh[0].end) {
-      line = 1;
-      fresh = true;
-    }
-    if (line == 1) h = &sh[1];
-    if (h->u >= h->end) return false;
-    if (fresh) {
-      req = h->req;
-      rq = tree_req(a, req);
-      fresh = false;
-    }
     for (;;) {
-      const int64_t n = line == 0 ? quad_units(rq, tt, hkv) : rest_units(rq, tt, hkv);
-      if (h->off < n) break;
-      h->off -= n;
-      if (++req >= a.num_reqs) return false;
-      rq = tree_req(a, req);
-    }
-    const int kt = key_tiles(rq), nt = query_tiles(rq, tt), quads = nt / 4;
-    const int64_t left = h->end - h->u;
-    int k0, glen, tile;
-    s.single = false;
-    if (line == 0) {
-      const int grp = static_cast<int>(h->off / kt);
-      k0 = static_cast<int>(h->off % kt);
-      glen = kt;
-      s.g = grp / quads;
-      tile = (grp % quads) * 4 + 2 * (blockIdx.x & 1);
-    } else {
-      const int rem = nt % 4, w = (rem >> 1) * kt + (rem & 1) * ((kt + 1) / 2);
-      s.g = static_cast<int>(h->off / w);
-      k0 = static_cast<int>(h->off % w);
-      tile = quads * 4;
-      glen = kt;
-      if (k0 >= (rem >> 1) * kt) {
-        k0 -= (rem >> 1) * kt;
-        tile += rem & 2;
-        glen = (kt + 1) / 2;
-        s.single = true;
+      if (line == 0 && sh[0].u >= sh[0].end) {
+        line = 1;
+        fresh = true;
       }
+      TreeShare h = line == 0 ? sh[0] : sh[1];
+      if (h.u >= h.end) return false;
+      if (fresh) {
+        req = h.req;
+        rq = tree_req(a, req);
+        fresh = false;
+      }
+      for (;;) {
+        const int64_t n = line == 0 ? quad_units(rq, tt, hkv) : rest_units(rq, tt, hkv);
+        if (h.off < n) break;
+        h.off -= n;
+        if (++req >= a.num_reqs) return false;
+        rq = tree_req(a, req);
+      }
+      const int kt = key_tiles(rq), nt = query_tiles(rq, tt), quads = nt / 4;
+      const int pair_len = kPairUnits * kt + kGroupUnits;
+      int x, tile, cost = kPairUnits, glen = pair_len;   // x: unit within the group
+      bool single = false;
+      if (line == 0) {
+        const int64_t grp = h.off / pair_len;
+        x = static_cast<int>(h.off - grp * pair_len);
+        s.g = static_cast<int>(grp) / quads;
+        tile = (static_cast<int>(grp) % quads) * 4 + 2 * (blockIdx.x & 1);
+      } else {
+        const int rem = nt % 4, pairs = rem >> 1;
+        const int single_len = kSingleUnits * kt + kGroupUnits;
+        const int w = pairs * pair_len + (rem & 1) * single_len;
+        s.g = static_cast<int>(h.off / w);
+        x = static_cast<int>(h.off - static_cast<int64_t>(s.g) * w);
+        tile = quads * 4;
+        if (x >= pairs * pair_len) {
+          x -= pairs * pair_len;
+          tile += rem & 2;
+          cost = kSingleUnits;
+          glen = single_len;
+          single = true;
+        }
+      }
+      const int len = static_cast<int>(min(static_cast<int64_t>(glen - x), h.end - h.u));
+      const int kt0 = min(kt, (x + cost - 1) / cost), kt1 = min(kt, (x + len + cost - 1) / cost);
+      const int64_t gbegin = h.u - x;
+      h.u += len;
+      h.off += len;
+      if (line == 0) sh[0] = h; else sh[1] = h;
+      if (kt0 >= kt1) continue;   // the group's fixed units only
+      s.req = req;
+      s.prefix = rq.prefix;
+      s.ctx = rq.ctx;
+      s.tok0 = rq.t0 + tile * tt;
+      s.rows0 = min(tt, rq.n - tile * tt) * a.group;
+      s.tok1 = s.tok0 + tt;
+      s.rows1 = single ? 0 : min(tt, rq.n - (tile + 1) * tt) * a.group;
+      s.kt0 = kt0;
+      s.kt1 = kt1;
+      s.slot = (static_cast<int>(blockIdx.x) * 2 + line) * 2 + (kt0 == 0 ? 1 : 0);
+      s.flags = (single ? kSegSingle : 0) | (kt0 == 0 && kt1 == kt ? kSegWhole : 0);
+      cut.count = 0;
+      if (kt0 == 0 && kt1 < kt) {
+        // The last tile's first unit names the last worker; the workers between each have a tile (a share is
+        // longer than a tile).
+        const int per = line ? 1 : 2;   // CTAs a worker
+        const int wk = static_cast<int>(blockIdx.x) / per;
+        cut.count = TcShare::owner(h.U, h.workers, gbegin + static_cast<int64_t>(kt - 1) * cost) - wk + 1;
+        cut.first = s.slot;
+        cut.next = ((static_cast<int>(blockIdx.x) + per) * 2 + line) * 2;
+        cut.stride = per * 4;
+        cut.tok_a = s.tok0;
+        cut.rows_a = s.rows0;
+        cut.tok_b = s.tok1;
+        cut.rows_b = s.rows1;
+        cut.f0 = 0;
+        cut.g = s.g;
+      }
+      return true;
     }
-    const int len = static_cast<int>(min(static_cast<int64_t>(glen - k0), left));
-    s.rq = rq;
-    s.req = req;
-    s.kt0 = s.single ? 2 * k0 : k0;
-    s.kt1 = min(kt, s.single ? 2 * (k0 + len) : k0 + len);
-    s.opens = k0 == 0;
-    s.whole = k0 == 0 && len == glen;
-    s.line = line;
-    s.worker_units = glen - k0;
-    s.tok0 = rq.t0 + tile * tt;
-    s.rows0 = min(tt, rq.n - tile * tt) * a.group;
-    s.tok1 = s.tok0 + tt;
-    s.rows1 = s.single ? 0 : min(tt, rq.n - (tile + 1) * tt) * a.group;
-    h->off += len;
-    h->u += len;
-    return true;
   }
 };
 
@@ -177,12 +205,12 @@ template <int D, bool F8>
 __device__ __noinline__ void add_odd(const TreeArgs& a, const Seg& s, const uint32_t* mrow, uint16_t* o, float* part) {
   const int64_t Hkv = a.pool.num_kv_heads;
   const int32_t* bt = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
-  const int b0 = max(s.kt0, s.rq.prefix / kNK) * kBlkPerTile;
-  const int b1 = min(s.kt1 * kBlkPerTile, (s.rq.ctx + kBlockSize - 1) / kBlockSize);
+  const int b0 = max(s.kt0 * kBlkPerTile, s.prefix / kBlockSize);
+  const int b1 = min(s.kt1 * kBlkPerTile, (s.ctx + kBlockSize - 1) / kBlockSize);
   for (int b = b0; b < b1; ++b) {
     const int pb = __ldg(bt + b);
     if (pb < 0 || pb >= a.pool.num_blocks) continue;
-    const uint32_t vis = tree_sees(s.rq, mrow, a.mask_words, b * kBlockSize);
+    const uint32_t vis = tree_sees(s.prefix, s.ctx, mrow, a.mask_words, b * kBlockSize) & ~low_bits(s.prefix - b * kBlockSize);
     for (int k = 0; k < kBlockSize; ++k) {
       if (!((vis >> k) & 1u)) continue;
       for (int d = 0; d < D; ++d) {
@@ -204,6 +232,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
   using B = typename M::B;
   constexpr int kKSt = S::kKSt, kVSt = S::kVSt;
   extern __shared__ __align__(1024) uint8_t smem[];
+  griddep_launch();   // the merge may take its place and wait
   if (threadIdx.x < 2) a.cuts[2 * blockIdx.x + threadIdx.x].count = 0;
   if ((smem_u32(smem) & 1023u) != 0) {   // swizzle atoms need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_INTERNAL);
@@ -216,24 +245,22 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + M::kOffMisc + 8);
   volatile int* s_odd = reinterpret_cast<volatile int*>(smem + M::kOffMisc + 16);   // [kSegRing]
-  TreeShare* s_share = reinterpret_cast<TreeShare*>(smem + M::kOffMisc + 64);       // [2]
+  Seg* s_seg = reinterpret_cast<Seg*>(smem + M::kOffSeg);   // [kSegSlots]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.group, Hkv = a.pool.num_kv_heads;
+  Walk walk;
   {
     // The CTA's shares (scratch in the query buffer, before its first copy).
-    int64_t* scratch = reinterpret_cast<int64_t*>(smem);
-    const TreeShare q = tree_share<TcShare, kThreads>(a, scratch, blockIdx.x >> 1, a.ctas / 2, [&](const TreeReq& r) {
-      return quad_units(r, a.tile_tokens, Hkv);
-    });
-    const TreeShare r = tree_share<TcShare, kThreads>(a, scratch, blockIdx.x, a.ctas, [&](const TreeReq& x) {
-      return rest_units(x, a.tile_tokens, Hkv);
-    });
-    if (q.u >= q.end && r.u >= r.end) return;   // block-uniform
-    if (threadIdx.x == 0) {
-      s_share[0] = q;
-      s_share[1] = r;
-    }
+    TreeShare (&sh)[2] = walk.sh;
+    const int worker[2] = {static_cast<int>(blockIdx.x >> 1), static_cast<int>(blockIdx.x)};
+    const int most[2] = {a.ctas / 2, a.ctas};
+    tree_shares<TcShare, kThreads, 2>(a, reinterpret_cast<int64_t*>(smem), worker, most, sh,
+                                      [&](const TreeReq& q, int line) {
+                                        return line == 0 ? quad_units(q, a.tile_tokens, Hkv)
+                                                         : rest_units(q, a.tile_tokens, Hkv);
+                                      });
+    if (sh[0].u >= sh[0].end && sh[1].u >= sh[1].end) return;   // block-uniform
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKSt; ++i) {
@@ -258,6 +285,10 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
     mbar_init(&bars[B::kJoined], 128);
     mbar_init(&bars[B::kDrain], 1);
     for (int i = 0; i < kSegRing; ++i) mbar_init(&bars[B::kVDone + i], 1);
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(&bars[B::kSegFull + i], 1);
+      mbar_init(&bars[B::kSegEmpty + i], kSegReaders);
+    }
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -279,9 +310,18 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
   const uint32_t sQ = smem_u32(smem + S::kOffQ);
   const uint32_t sK = smem_u32(smem + S::kOffK);
   const uint32_t sV = smem_u32(smem + S::kOffV);
-  Walk walk;
-  walk.start(s_share);
+  // The CTA's r-th segment: waits until it is published, reads it and frees its slot.  false: gave up, or no more (`ok`
+  // tells which).
   Seg sg;
+  bool ok = true;
+  auto take = [&](int r) -> bool {
+    const int slot = r % kSegSlots;
+    if (!(ok = mbar_wait_warp(&bars[B::kSegFull + slot], (r / kSegSlots) & 1, s_abort, a.wait_ns))) return false;
+    sg = s_seg[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[B::kSegEmpty + slot]);
+    return (sg.flags & kSegEnd) == 0;
+  };
 
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------ producers: warp 8 K (and Q), warp 10 V
@@ -295,8 +335,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
     int fin = 0;      // FP8: tiles widened and handed over
     int nq = 0;       // segments whose query tiles have been issued
     uint32_t landed_par = 0;
-    bool ok = true;
-    for (int r = 0; ok && walk.next(a, sg); ++r) {
+    for (int r = 0; ok && take(r); ++r) {
       if (is_k) {
         for (int t = 0; t < 2 && ok; ++t) {
           if (!(ok = mbar_wait_warp(&bars[B::kQEmpty + t], (r & 1) ^ 1, s_abort, a.wait_ns))) break;
@@ -318,26 +357,21 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
         nq = r + 1;
       }
       const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
-      const int nblk = (sg.rq.ctx + kBlockSize - 1) / kBlockSize;
+      const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
       // Lane l holds block 32 w + l of the segment (window w: four key tiles), the next window in flight.
       auto load_window = [&](int w) -> int {
         const int b = sg.kt0 * kBlkPerTile + w * 32 + lane;
         return b < nblk && b < sg.kt1 * kBlkPerTile ? __ldg(bt_row + b) : -1;
       };
-      auto check_window = [&](int w, int pb) -> int {
-        if (pb >= 0 && pb < a.pool.num_blocks) return pb;
-        const int b = sg.kt0 * kBlkPerTile + w * 32 + lane;
-        if (b < nblk && b < sg.kt1 * kBlkPerTile) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
-        return -1;
-      };
+      auto check_window = [&](int pb) -> int { return pb >= 0 && pb < a.pool.num_blocks ? pb : -1; };
       int win = 0;
-      int ids_cur = check_window(0, load_window(0)), ids_next = load_window(1);
+      int ids_cur = check_window(load_window(0)), ids_next = load_window(1);
       // Lane l < 8: chunk index of key tile j's block l, or -1.
       auto block_chunk = [&](int j) -> int {
         const int rel = j - sg.kt0;
         if ((rel >> 2) != win) {
           win = rel >> 2;
-          ids_cur = check_window(win, ids_next);
+          ids_cur = check_window(ids_next);
           ids_next = load_window(win + 1);
         }
         const int pb = __shfl_sync(0xffffffffu, ids_cur, (rel & 3) * kBlkPerTile + (lane & 7));
@@ -345,20 +379,24 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
       };
       int seg_odd = 0;
       // V tiles that some row does not see whole: clear the rows without a key
-      // (past the context, or of a block that is not there) and elements that
-      // are not finite.  have: blocks of the tile that were copied.
+      // (past the context, or of a block that is not there) and, behind the
+      // prefix, elements that are not finite.  have: blocks that were copied.
       auto clean_v = [&](uint8_t* stage, int j, uint32_t have) {
         constexpr int kCh = S::kHalves * 8;   // 16-byte chunks of a key's row
         const int ch = lane % kCh;
         uint8_t* col = stage + (ch / 8) * S::kHS;
-        const int live = sg.rq.ctx - j * kNK;
+        const int live = sg.ctx - j * kNK;
+        const int first = have == 0xffu ? max(0, sg.prefix - j * kNK) & ~(32 / kCh - 1) : 0;
+        const int pre = sg.prefix - j * kNK;
         bool odd = false;
-        for (int key = lane / kCh; key < kNK; key += 32 / kCh) {
+#pragma unroll 4
+        for (int key = first + lane / kCh; key < kNK; key += 32 / kCh) {
           uint4* p = reinterpret_cast<uint4*>(col + (key / 8) * S::kGS + (key % 8) * 128 + (((ch % 8) ^ (key % 8)) * 16));
           if (key >= live || !((have >> (key / kBlockSize)) & 1u)) {
             *p = make_uint4(0, 0, 0, 0);
             continue;
           }
+          if (key < pre) continue;
           uint4 v = *p;
           bool any = false;
           v.x = finite_pair<F8>(v.x, any);
@@ -373,7 +411,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
         if (__any_sync(0xffffffffu, odd)) seg_odd = 1;
       };
       // Which tiles need it: a tile that ends behind the prefix, or lacks a block.
-      auto needs_clean = [&](int j, uint32_t have) { return (j + 1) * kNK > sg.rq.prefix || have != 0xffu; };
+      auto needs_clean = [&](int j, uint32_t have) { return (j + 1) * kNK > sg.prefix || have != 0xffu; };
       if constexpr (!F8) {
         for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
           const int y = block_chunk(j);
@@ -505,7 +543,6 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
     constexpr int kQReady = F8 ? B::kQc : B::kQFull;
     int kc = 0, vc = 0;          // K / V tiles consumed
     uint32_t pc0 = 0, pc1 = 0;   // P phases of group A / B waited so far
-    bool ok = true;
     auto wait_k = [&] { return mbar_wait_warp(&bars[B::kKFull + kc % kKSt], (kc / kKSt) & 1, s_abort, a.wait_ns); };
     auto wait_v = [&] { return mbar_wait_warp(&bars[B::kVFull + vc % kVSt], (vc / kVSt) & 1, s_abort, a.wait_ns); };
     auto wait_p = [&](int t) {
@@ -513,12 +550,12 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
       if (t) ++pc1; else ++pc0;
       return o;
     };
-    for (int r = 0; ok && walk.next(a, sg); ++r) {
+    for (int r = 0; ok && take(r); ++r) {
       const int n = sg.kt1 - sg.kt0;   // >= 1
       if (!(ok = mbar_wait_warp(&bars[kQReady], r & 1, s_abort, a.wait_ns) &&
                  mbar_wait_warp(&bars[kQReady + 1], r & 1, s_abort, a.wait_ns)))
         break;
-      if (!sg.single) {
+      if (!(sg.flags & kSegSingle)) {
         // Both groups use every key tile: PV_A(j) S_A(j+1) PV_B(j) S_B(j+1).
         if (!(ok = wait_k())) break;
         tc_fence_after();
@@ -589,6 +626,44 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
     // Drain: every MMA issued has completed before TMEM is released.
     release(B::kDrain);
     (void)mbar_wait_warp(&bars[B::kDrain], 0, nullptr, a.wait_ns);
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ scheduler
+    walk.line = 0;
+    walk.fresh = true;
+    for (int r = 0;; ++r) {
+      Seg s;
+      TreeCut cut;
+      const bool more = walk.next(a, s, cut);
+      if (more) {
+        if (cut.count > 0 && lane == 0) a.cuts[2 * blockIdx.x + walk.line] = cut;
+        // Blocks that are not there: flagged here, and only then looked for by the softmax warps.
+        const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
+        const int end = min(s.kt1 * kBlkPerTile, (s.ctx + kBlockSize - 1) / kBlockSize);
+        bool gone = false;
+        for (int b = s.kt0 * kBlkPerTile + lane; b < end; b += 32) {
+          const int pb = __ldg(bt_row + b);
+          gone |= pb < 0 || pb >= a.pool.num_blocks;
+        }
+        if (__any_sync(0xffffffffu, gone)) {
+          s.flags |= kSegMissing;
+          if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
+        }
+      } else {
+        s.flags = kSegEnd;
+      }
+      const int slot = r % kSegSlots;
+      if (!(ok = mbar_wait_warp(&bars[B::kSegEmpty + slot], ((r / kSegSlots) & 1) ^ 1, s_abort, a.wait_ns))) break;
+      if (lane == 0) {
+        s_seg[slot] = s;
+        mbar_arrive(&bars[B::kSegFull + slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+      *s_abort = 1;
+    }
   } else {
     // ------------------------------------------------------------ softmax / epilogue of group X
     const int X = (warp >> 2) & 1;
@@ -597,18 +672,18 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
     const uint32_t colS = X * kNK, colO = kColO + X * 128;
     const float sl2 = F8 ? a.scale_log2 * a.pool.k_scale : a.scale_log2;
     uint32_t sc = 0, pvc = 0, joins = 0;      // phases waited so far
-    bool ok = true;
-    for (int r = 0; ok && walk.next(a, sg); ++r) {
+    for (int r = 0; ok && take(r); ++r) {
       const int g = sg.g;
-      const bool mine = X == 0 || !sg.single;            // stores its rows
-      const int nrows = X && !sg.single ? sg.rows1 : sg.rows0;
-      const int tok = X && !sg.single ? sg.tok1 : sg.tok0;
+      const bool single = (sg.flags & kSegSingle) != 0, whole = (sg.flags & kSegWhole) != 0;
+      const bool mine = X == 0 || !single;               // stores its rows
+      const int nrows = X && !single ? sg.rows1 : sg.rows0;
+      const int tok = X && !single ? sg.tok1 : sg.tok0;
       const bool valid = row < nrows;
       const int t_row = tok + (valid ? row / G : 0);
       const uint32_t* mrow = a.mask + static_cast<int64_t>(t_row) * a.mask_words;
-      const int step = sg.single ? 2 : 1;
+      const int step = single ? 2 : 1;
       const int n = sg.kt1 - sg.kt0;
-      const int nt = sg.single ? (n + 1 - X) / 2 : n;    // key tiles of this group
+      const int nt = single ? (n + 1 - X) / 2 : n;    // key tiles of this group
       if constexpr (F8) {
         // Operands of one MMA share a type: this thread's Q row to f16, in place (exact within f16's range).
         ok = mbar_wait_warp(&bars[B::kQFull + X], r & 1, s_abort, a.wait_ns);
@@ -633,7 +708,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
       }
       // Blocks that are not there, as bits: window of 32 blocks (four key tiles) at a time.
       const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
-      const int nblk = (sg.rq.ctx + kBlockSize - 1) / kBlockSize;
+      const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
       auto missing_of = [&](int w) -> uint32_t {
         const int b = sg.kt0 * kBlkPerTile + w * 32 + lane;
         bool gone = false;
@@ -643,12 +718,24 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
         }
         return __ballot_sync(0xffffffffu, gone);
       };
-      uint32_t missing = missing_of(0);
+      const bool any_missing = (sg.flags & kSegMissing) != 0;
+      uint32_t missing = any_missing ? missing_of(0) : 0u;
       float m = -CUDART_INF_F, l = 0.f;
       for (int i = 0; ok && i < nt; ++i) {
-        const int rel = sg.single ? 2 * i + X : i;
+        const int rel = single ? 2 * i + X : i;
         const int key0 = (sg.kt0 + rel) * kNK;
-        if (rel > 0 && (rel & 3) < step) missing = missing_of(rel >> 2);
+        if (any_missing && rel > 0 && (rel & 3) < step) missing = missing_of(rel >> 2);
+        const uint32_t gone = (missing >> ((rel & 3) * kBlkPerTile)) & 0xffu;
+        const bool masked = key0 + kNK > sg.prefix || gone != 0;
+        uint32_t vis[4];
+        if (masked) {   // the mask words are on their way while the scores are computed
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            vis[w] = tree_sees(sg.prefix, sg.ctx, mrow, a.mask_words, key0 + 32 * w);
+            if ((gone >> (2 * w)) & 1u) vis[w] &= 0xffff0000u;
+            if ((gone >> (2 * w)) & 2u) vis[w] &= 0x0000ffffu;
+          }
+        }
         if (!(ok = mbar_wait_warp(&bars[B::kS + X], sc & 1, s_abort, a.wait_ns))) break;
         ++sc;
         tc_fence_after();
@@ -656,16 +743,11 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
 #pragma unroll
         for (int c = 0; c < kNK; c += 16) tmem_ld16(tmem + lane_base + colS + c, s + c);
         tmem_wait_ld();
-        const uint32_t gone = (missing >> ((rel & 3) * kBlkPerTile)) & 0xffu;
-        if (key0 + kNK > sg.rq.prefix || gone != 0) {
+        if (masked) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t vis = tree_sees(sg.rq, mrow, a.mask_words, key0 + 32 * w);
-            if ((gone >> (2 * w)) & 1u) vis &= 0xffff0000u;
-            if ((gone >> (2 * w)) & 2u) vis &= 0x0000ffffu;
+          for (int w = 0; w < 4; ++w)
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[32 * w + c] = (vis >> c) & 1u ? s[32 * w + c] : -CUDART_INF_F;
-          }
+            for (int c = 0; c < 32; ++c) s[32 * w + c] = (vis[w] >> c) & 1u ? s[32 * w + c] : -CUDART_INF_F;
         }
         float mx8[8];
 #pragma unroll
@@ -722,7 +804,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
       }
       float wa = 1.f, wb = 0.f;   // weights of A's and B's accumulators
       bool join = false;
-      if (sg.single) {
+      if (single) {
         if (X == 1) {
           s_ml[row] = make_float2(m, l);
           tc_fence_before();
@@ -757,8 +839,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
       const float inv = l == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / l;
       const float lse2 = l == 0.f ? -CUDART_INF_F : m + fast_log2(l);
       const int h = g * G + row % G;
-      const int slot = (static_cast<int>(blockIdx.x) * 2 + sg.line) * 2 + (sg.opens ? 1 : 0);
-      const int64_t prow = static_cast<int64_t>(slot) * 256 + X * 128 + row;
+      const int64_t prow = static_cast<int64_t>(sg.slot) * 256 + X * 128 + row;
       const int64_t orow = static_cast<int64_t>(t_row) * a.num_q_heads + h;
       uint4* dst_o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * D);
       float4* dst_p = reinterpret_cast<float4*>(a.part_o + prow * D);
@@ -787,7 +868,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
           for (int e = 0; e < 32; ++e) ob[e] = 0.f;
         }
         if (valid) {
-          if (sg.whole) {
+          if (whole) {
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
               uint4 w0, w1;
@@ -795,21 +876,29 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
               w0.z = pack_bf16x2(ob[e + 4], ob[e + 5]);   w0.w = pack_bf16x2(ob[e + 6], ob[e + 7]);
               w1.x = pack_bf16x2(ob[e + 8], ob[e + 9]);   w1.y = pack_bf16x2(ob[e + 10], ob[e + 11]);
               w1.z = pack_bf16x2(ob[e + 12], ob[e + 13]); w1.w = pack_bf16x2(ob[e + 14], ob[e + 15]);
-              dst_o[(c0 + e) / 8] = w0;
-              dst_o[(c0 + e) / 8 + 1] = w1;
+              // A thread writes its own row: 32 bytes a store, a whole sector, where o allows it.
+              if (a.o_align32) {
+                st_global_v8(dst_o + (c0 + e) / 8, w0, w1);
+              } else {
+                dst_o[(c0 + e) / 8] = w0;
+                dst_o[(c0 + e) / 8 + 1] = w1;
+              }
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) dst_p[(c0 + e) / 4] = make_float4(ob[e], ob[e + 1], ob[e + 2], ob[e + 3]);
+            for (int e = 0; e < 32; e += 8) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(ob + e);
+              st_global_v8(dst_p + (c0 + e) / 4, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+            }
           }
         }
       }
-      if (sg.single) {
+      if (single) {
         tc_fence_before();
         mbar_arrive(&bars[B::kJoined]);   // B's columns have been read
       }
       if (valid) {
-        if (sg.whole) {
+        if (whole) {
           if (a.lse) a.lse[orow] = lse2 * 0.69314718055994530942f;
         } else {
           a.part_lse[prow] = lse2;
@@ -817,27 +906,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
       }
       if (!(ok = mbar_wait_warp(&bars[B::kVDone + r % kSegRing], (r / kSegRing) & 1, s_abort, a.wait_ns))) break;
       if (s_odd[r % kSegRing] && valid)
-        add_odd<D, F8>(a, sg, mrow, static_cast<uint16_t*>(a.o) + orow * D, sg.whole ? nullptr : a.part_o + prow * D);
-      if (threadIdx.x == 0 && sg.opens && !sg.whole) {
-        // This CTA begins a group that others go on with.
-        const TreeShare& sh = s_share[sg.line];
-        const int64_t end = walk.sh[sg.line].u;              // one past this segment's units: the share's end
-        const int wk = sg.line ? blockIdx.x : blockIdx.x >> 1;
-        const int64_t gend = end - (static_cast<int64_t>(sg.single ? (n + 1) / 2 : n)) + sg.worker_units;
-        const int c1 = TcShare::owner(sh.U, sh.workers, gend - 1);
-        TreeCut& cut = a.cuts[2 * blockIdx.x + sg.line];
-        const int per = sg.line ? 1 : 2;                     // CTAs a worker
-        cut.first = slot;
-        cut.next = ((blockIdx.x + per) * 2 + sg.line) * 2;
-        cut.stride = per * 4;
-        cut.tok_a = sg.tok0;
-        cut.rows_a = sg.rows0;
-        cut.tok_b = sg.tok1;
-        cut.rows_b = sg.rows1;
-        cut.f0 = 0;
-        cut.g = g;
-        cut.count = c1 - wk + 1;
-      }
+        add_odd<D, F8>(a, sg, mrow, static_cast<uint16_t*>(a.o) + orow * D, whole ? nullptr : a.part_o + prow * D);
     }
     if (!ok) {
       if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
