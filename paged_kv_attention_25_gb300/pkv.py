@@ -104,6 +104,8 @@ _lock = threading.Lock()
 def load_library():
     """Load libpkv.so (built by paged_kv_attention_25_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -255,6 +257,8 @@ class Pool:
             _check(lib.pkv_pool_create(ctypes.byref(desc), ctypes.byref(h)))
         self.handle = h
         self._ws = None
+        self.device_index = self.k.get_device()
+        self._op_ws = {}     # workspace sizes of the calls below, by their sizes
 
     def close(self):
         if getattr(self, "handle", None):
@@ -395,63 +399,100 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
 # ---------------------------------------------------------------------------------------------------------------------
 # Tree attention, block-selected attention and pages.  Their metadata is read on the device alone: no HostMeta, and the
 # calls can be captured into a graph.  Tensors live on the pool's device; without `stream` a call runs on that device's
-# current stream.  Outputs and workspaces that are not given are allocated for that stream.
+# current stream.  Outputs and workspaces that are not given are allocated for that stream, the workspace afresh for
+# each call (a captured graph keeps its own).
+
+_I32, _I8, _BF16, _F32, _U8 = torch.int32, torch.int8, torch.bfloat16, torch.float32, torch.uint8
 
 
-def _op_stream(pool: Pool, stream):
-    return torch.cuda.current_stream(pool.k.device) if stream is None else stream
+def _op_stream(pool: Pool, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(pool.device_index)
+    return stream.cuda_stream
 
 
-def _op_dev(pool: Pool, t, name, dtype, shape=None):
+def _op_dims(t, name, n):
+    """The tensor's shape, which has n dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions")
+    return shape
+
+
+def _op_ptr(pool: Pool, t, name, dtype, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on the pool's device."""
+    try:
+        if t.dtype is dtype and t.get_device() == pool.device_index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
-    if t.device != pool.k.device:
+    if t.get_device() != pool.device_index:
         raise ValueError(f"{name} must be on the pool's device")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape))):
-        raise ValueError(f"{name} must have shape {['*' if w is None else w for w in shape]}")
-    return t
+    raise ValueError(f"{name} must have shape {tuple(shape)}")
 
 
-def _op_heads(pool: Pool, q):
-    _op_dev(pool, q, "q", torch.bfloat16, (None, None, pool.head_dim))
-    return q.shape[0], q.shape[1]
-
-
-def _op_out(pool: Pool, q, out, lse, want_lse, stream):
-    T, Hq, _ = q.shape
+def _op_new(pool: Pool, shape, dtype, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=pool.k.device)
     with torch.cuda.stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    _op_dev(pool, out, "out", torch.bfloat16, tuple(q.shape))
-    if lse is not None:
-        _op_dev(pool, lse, "lse", torch.float32, (T, Hq))
-    return out, lse
+        return torch.empty(shape, dtype=dtype, device=pool.k.device)
 
 
-def _op_workspace(pool: Pool, workspace, nbytes, stream):
+def _op_workspace(pool: Pool, workspace, key, size, stream):
+    """(the tensor, its bytes); key: what the size depends on."""
     if workspace is None:
-        with torch.cuda.stream(stream):
-            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.k.device)
-    return _op_dev(pool, workspace, "workspace", torch.uint8, (None,))
+        n = pool._op_ws.get(key)
+        if n is None:
+            n = pool._op_ws[key] = size(pool, *key[1:])
+        return _op_new(pool, (n,), _U8, stream), n
+    n = _op_dims(workspace, "workspace", 1)[0]
+    _op_ptr(pool, workspace, "workspace", _U8, (n,))
+    return workspace, n
+
+
+def _op_batch(pool: Pool, block_tables, cu_q_lens):
+    """(requests, table width, table pointer, cu pointer)"""
+    R = _op_dims(cu_q_lens, "cu_q_lens", 1)[0] - 1
+    if R < 0:
+        raise ValueError("cu_q_lens must hold num_reqs + 1 entries")
+    width = _op_dims(block_tables, "block_tables", 2)[1]
+    return (R, width, _op_ptr(pool, block_tables, "block_tables", _I32, (R, width)),
+            _op_ptr(pool, cu_q_lens, "cu_q_lens", _I32, (R + 1,)))
+
+
+def _op_query(pool: Pool, q, out, lse, want_lse, stream):
+    """(T, Hq, q pointer, O, LSE or None)"""
+    T, Hq, _ = _op_dims(q, "q", 3)
+    qp = _op_ptr(pool, q, "q", _BF16, (T, Hq, pool.head_dim))
+    if out is None:
+        out = _op_new(pool, (T, Hq, pool.head_dim), _BF16, stream)
+    else:
+        _op_ptr(pool, out, "out", _BF16, q.shape)
+    if lse is not None:
+        _op_ptr(pool, lse, "lse", _F32, (T, Hq))
+    elif want_lse:
+        lse = _op_new(pool, (T, Hq), _F32, stream)
+    return T, Hq, qp, out, lse
 
 
 def pkv_tree_mask(pool: Pool, parents, cu_q_lens, mask_words=None, max_nodes=None, out=None, stream=None):
     """Mask rows [T, mask_words] (int32 bit patterns) from each node's parent (index in its tree, -1: a root).
 
     Give mask_words, or max_nodes (the largest tree's size, T if neither is given) to size the rows by."""
-    stream = _op_stream(pool, stream)
-    _op_dev(pool, parents, "parents", torch.int32, (None,))
-    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
-    T = parents.shape[0]
+    T = _op_dims(parents, "parents", 1)[0]
+    pp = _op_ptr(pool, parents, "parents", _I32, (T,))
+    R = _op_dims(cu_q_lens, "cu_q_lens", 1)[0] - 1
+    cp = _op_ptr(pool, cu_q_lens, "cu_q_lens", _I32, (R + 1,))
     if out is None:
         words = mask_words if mask_words is not None else max(1, ((max_nodes or T) + 31) // 32)
-        with torch.cuda.stream(stream):
-            out = torch.zeros((T, words), dtype=torch.int32, device=parents.device)
-    _op_dev(pool, out, "out", torch.int32, (T, None))
-    _check(load_library().pkv_tree_mask(pool.handle, _ptr(parents), _ptr(cu_q_lens), cu_q_lens.shape[0] - 1, T,
-                                        _ptr(out), out.shape[1], _stream(stream)))
+        out = _op_new(pool, (T, words), _I32, stream)
+    words = _op_dims(out, "out", 2)[1]
+    op = _op_ptr(pool, out, "out", _I32, (T, words))
+    _check(load_library().pkv_tree_mask(pool.handle, pp, cp, R, T, op, words, _op_stream(pool, stream)))
     return out
 
 
@@ -467,21 +508,16 @@ def pkv_tree_attn(pool: Pool, q, block_tables, ctx_lens, prefix_lens, cu_q_lens,
     """Attention of drafted tokens: each sees slots [0, prefix_lens[r]) and the slots prefix_lens[r] + i whose bit i is
     set in its row of tree_mask [T, words] (int32 bit patterns).  Returns (O [T, Hq, D] bf16, LSE [T, Hq] fp32 or None).
     """
-    stream = _op_stream(pool, stream)
-    T, Hq = _op_heads(pool, q)
-    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
-    R = cu_q_lens.shape[0] - 1
-    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
-    _op_dev(pool, ctx_lens, "ctx_lens", torch.int32, (R,))
-    _op_dev(pool, prefix_lens, "prefix_lens", torch.int32, (R,))
-    _op_dev(pool, tree_mask, "tree_mask", torch.int32, (T, None))
-    out, lse = _op_out(pool, q, out, lse, want_lse, stream)
-    workspace = _op_workspace(pool, workspace, 0 if workspace is not None
-                              else pkv_tree_attn_workspace_size(pool, Hq, R, T), stream)
-    _check(load_library().pkv_tree_attn(pool.handle, _ptr(q), Hq, _ptr(block_tables), block_tables.shape[1],
-                                        _ptr(ctx_lens), _ptr(prefix_lens), _ptr(cu_q_lens), R, T, _ptr(tree_mask),
-                                        tree_mask.shape[1], float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-                                        workspace.numel(), _stream(stream)))
+    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
+    T, Hq, qp, out, lse = _op_query(pool, q, out, lse, want_lse, stream)
+    words = _op_dims(tree_mask, "tree_mask", 2)[1]
+    ctx = _op_ptr(pool, ctx_lens, "ctx_lens", _I32, (R,))
+    pre = _op_ptr(pool, prefix_lens, "prefix_lens", _I32, (R,))
+    mask = _op_ptr(pool, tree_mask, "tree_mask", _I32, (T, words))
+    ws, n = _op_workspace(pool, workspace, ("tree", Hq, R, T), pkv_tree_attn_workspace_size, stream)
+    _check(load_library().pkv_tree_attn(pool.handle, qp, Hq, bt, width, ctx, pre, cu, R, T, mask, words, scale,
+                                        out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), n,
+                                        _op_stream(pool, stream)))
     return out, lse
 
 
@@ -496,66 +532,56 @@ class BlockSummary:
         if codes is None:
             codes = torch.zeros(shape, dtype=torch.int8, device=pool.k.device)
             exps = torch.zeros(shape[:2], dtype=torch.int8, device=pool.k.device)
-        self.codes = _op_dev(pool, codes, "codes", torch.int8, shape)
-        self.exps = _op_dev(pool, exps, "exps", torch.int8, shape[:2])
+        self.codes, self.exps = codes, exps
+        _op_summary(pool, self)
 
 
 def _op_summary(pool: Pool, summary):
     shape = (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
-    return (_ptr(_op_dev(pool, summary.codes, "summary.codes", torch.int8, shape)),
-            _ptr(_op_dev(pool, summary.exps, "summary.exps", torch.int8, shape[:2])))
+    return (_op_ptr(pool, summary.codes, "summary.codes", _I8, shape),
+            _op_ptr(pool, summary.exps, "summary.exps", _I8, shape[:2]))
 
 
 def pkv_summarize(pool: Pool, summary: BlockSummary, block_tables, cu_q_lens, positions, ctx_lens, stream=None):
     """Recompute the bounds of every block that holds one of `positions` (after pkv_append: its own arguments)."""
-    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
-    R = cu_q_lens.shape[0] - 1
-    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
-    _op_dev(pool, positions, "positions", torch.int32, (None,))
-    _op_dev(pool, ctx_lens, "ctx_lens", torch.int32, (R,))
+    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
+    T = _op_dims(positions, "positions", 1)[0]
+    pos = _op_ptr(pool, positions, "positions", _I32, (T,))
+    ctx = _op_ptr(pool, ctx_lens, "ctx_lens", _I32, (R,))
     codes, exps = _op_summary(pool, summary)
-    _check(load_library().pkv_summarize(pool.handle, _ptr(block_tables), block_tables.shape[1], R, _ptr(cu_q_lens),
-                                        _ptr(positions), _ptr(ctx_lens), positions.shape[0], codes, exps,
-                                        _stream(_op_stream(pool, stream))))
+    _check(load_library().pkv_summarize(pool.handle, bt, width, R, cu, pos, ctx, T, codes, exps,
+                                        _op_stream(pool, stream)))
 
 
 def pkv_select_blocks(pool: Pool, summary: BlockSummary, q, q_positions, block_tables, cu_q_lens, top_k: int,
                       sinks: int = 1, recent: int = 1, out=None, stream=None):
     """The top_k blocks of each (token, KV head) by the bound on its scores, the first `sinks` and last `recent` always
     among them: [T, Hkv, top_k] int32 indexes into the block table, ascending, -1 beyond."""
-    stream = _op_stream(pool, stream)
-    T, Hq = _op_heads(pool, q)
-    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
-    R = cu_q_lens.shape[0] - 1
-    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
-    _op_dev(pool, q_positions, "q_positions", torch.int32, (T,))
+    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
+    T, Hq, _ = _op_dims(q, "q", 3)
+    qp = _op_ptr(pool, q, "q", _BF16, (T, Hq, pool.head_dim))
+    pos = _op_ptr(pool, q_positions, "q_positions", _I32, (T,))
     if top_k < 1:
         raise ValueError("top_k must be >= 1")
     if out is None:
-        with torch.cuda.stream(stream):
-            out = torch.empty((T, pool.num_kv_heads, top_k), dtype=torch.int32, device=q.device)
-    _op_dev(pool, out, "out", torch.int32, (T, pool.num_kv_heads, top_k))
+        out = _op_new(pool, (T, pool.num_kv_heads, top_k), _I32, stream)
+    op = _op_ptr(pool, out, "out", _I32, (T, pool.num_kv_heads, top_k))
     codes, exps = _op_summary(pool, summary)
-    _check(load_library().pkv_select_blocks(pool.handle, _ptr(q), Hq, _ptr(q_positions), _ptr(block_tables),
-                                            block_tables.shape[1], _ptr(cu_q_lens), R, T, codes, exps, int(top_k),
-                                            int(sinks), int(recent), _ptr(out), _stream(stream)))
+    _check(load_library().pkv_select_blocks(pool.handle, qp, Hq, pos, bt, width, cu, R, T, codes, exps, top_k, sinks,
+                                            recent, op, _op_stream(pool, stream)))
     return out
 
 
 def pkv_sparse_attn(pool: Pool, q, q_positions, block_tables, cu_q_lens, selected, scale: float, out=None, lse=None,
                     stream=None, want_lse=True):
     """Attention of each token over its selected blocks [T, Hkv, k] (keys up to its position); returns (O, LSE)."""
-    stream = _op_stream(pool, stream)
-    T, Hq = _op_heads(pool, q)
-    _op_dev(pool, cu_q_lens, "cu_q_lens", torch.int32, (None,))
-    R = cu_q_lens.shape[0] - 1
-    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
-    _op_dev(pool, q_positions, "q_positions", torch.int32, (T,))
-    _op_dev(pool, selected, "selected", torch.int32, (T, pool.num_kv_heads, None))
-    out, lse = _op_out(pool, q, out, lse, want_lse, stream)
-    _check(load_library().pkv_sparse_attn(pool.handle, _ptr(q), Hq, _ptr(q_positions), _ptr(block_tables),
-                                          block_tables.shape[1], _ptr(cu_q_lens), R, T, _ptr(selected),
-                                          selected.shape[2], float(scale), _ptr(out), _ptr(lse), _stream(stream)))
+    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
+    T, Hq, qp, out, lse = _op_query(pool, q, out, lse, want_lse, stream)
+    pos = _op_ptr(pool, q_positions, "q_positions", _I32, (T,))
+    k = _op_dims(selected, "selected", 3)[2]
+    sel = _op_ptr(pool, selected, "selected", _I32, (T, pool.num_kv_heads, k))
+    _check(load_library().pkv_sparse_attn(pool.handle, qp, Hq, pos, bt, width, cu, R, T, sel, k, scale, out.data_ptr(),
+                                          None if lse is None else lse.data_ptr(), _op_stream(pool, stream)))
     return out, lse
 
 
@@ -570,48 +596,42 @@ def pkv_fork(pool: Pool, tables, lens, caps, parents, new_caps, refs, out_tables
     """The next generation of sequences: child i continues row parents[i] of `tables` (-1: empty) with pages for
     new_caps[i] tokens.  Shares full pages, copies partly filled ones where needed, frees what no one owns any more.
     refs [num_blocks] counts the pages' owners; out_refs defaults to refs (in place).  Returns (new tables, refs)."""
-    stream = _op_stream(pool, stream)
-    i32 = torch.int32
-    _op_dev(pool, tables, "tables", i32, (None, None))
-    R, width = tables.shape
-    _op_dev(pool, lens, "lens", i32, (R,))
-    _op_dev(pool, caps, "caps", i32, (R,))
-    _op_dev(pool, parents, "parents", i32, (None,))
-    N = parents.shape[0]
-    _op_dev(pool, new_caps, "new_caps", i32, (N,))
-    _op_dev(pool, refs, "refs", i32, (pool.num_blocks,))
-    out_refs = refs if out_refs is None else _op_dev(pool, out_refs, "out_refs", i32, (pool.num_blocks,))
+    R, width = _op_dims(tables, "tables", 2)
+    N = _op_dims(parents, "parents", 1)[0]
+    tp = _op_ptr(pool, tables, "tables", _I32, (R, width))
+    lp = _op_ptr(pool, lens, "lens", _I32, (R,))
+    cp = _op_ptr(pool, caps, "caps", _I32, (R,))
+    pp = _op_ptr(pool, parents, "parents", _I32, (N,))
+    np_ = _op_ptr(pool, new_caps, "new_caps", _I32, (N,))
+    rp = _op_ptr(pool, refs, "refs", _I32, (pool.num_blocks,))
+    if out_refs is None:
+        out_refs = refs
+    orp = _op_ptr(pool, out_refs, "out_refs", _I32, (pool.num_blocks,))
     if out_tables is None:
-        with torch.cuda.stream(stream):
-            out_tables = torch.empty((N, width), dtype=i32, device=tables.device)
-    _op_dev(pool, out_tables, "out_tables", i32, (N, width))
+        out_tables = _op_new(pool, (N, width), _I32, stream)
+    otp = _op_ptr(pool, out_tables, "out_tables", _I32, (N, width))
     codes, exps = (None, None) if summary is None else _op_summary(pool, summary)
-    workspace = _op_workspace(pool, workspace, 0 if workspace is not None else pkv_fork_workspace_size(pool, R, N), stream)
-    _check(load_library().pkv_fork(pool.handle, _ptr(tables), R, width, _ptr(lens), _ptr(caps), _ptr(parents),
-                                   _ptr(new_caps), N, _ptr(out_tables), _ptr(refs), _ptr(out_refs), codes, exps,
-                                   _ptr(workspace), workspace.numel(), _stream(stream)))
+    ws, n = _op_workspace(pool, workspace, ("fork", R, N), pkv_fork_workspace_size, stream)
+    _check(load_library().pkv_fork(pool.handle, tp, R, width, lp, cp, pp, np_, N, otp, rp, orp, codes, exps,
+                                   ws.data_ptr(), n, _op_stream(pool, stream)))
     return out_tables, out_refs
 
 
 def pkv_copy_blocks(pool: Pool, src, dst, summary=None, stream=None):
     """Copy whole pages src[i] -> dst[i] (int32 device ids): K, V and, if given, the summary's bounds."""
-    _op_dev(pool, src, "src", torch.int32, (None,))
-    _op_dev(pool, dst, "dst", torch.int32, (src.shape[0],))
+    n = _op_dims(src, "src", 1)[0]
+    sp, dp = _op_ptr(pool, src, "src", _I32, (n,)), _op_ptr(pool, dst, "dst", _I32, (n,))
     codes, exps = (None, None) if summary is None else _op_summary(pool, summary)
-    _check(load_library().pkv_copy_blocks(pool.handle, _ptr(src), _ptr(dst), src.shape[0], codes, exps,
-                                          _stream(_op_stream(pool, stream))))
+    _check(load_library().pkv_copy_blocks(pool.handle, sp, dp, n, codes, exps, _op_stream(pool, stream)))
 
 
 def pkv_compact(pool: Pool, block_tables, cu_keep, src_positions, dst_starts, stream=None):
     """Move the K/V rows at src_positions (ascending per request) to dst_starts[r], dst_starts[r] + 1, ..."""
-    _op_dev(pool, cu_keep, "cu_keep", torch.int32, (None,))
-    R = cu_keep.shape[0] - 1
-    _op_dev(pool, block_tables, "block_tables", torch.int32, (R, None))
-    _op_dev(pool, src_positions, "src_positions", torch.int32, (None,))
-    _op_dev(pool, dst_starts, "dst_starts", torch.int32, (R,))
-    _check(load_library().pkv_compact(pool.handle, _ptr(block_tables), block_tables.shape[1], R, _ptr(cu_keep),
-                                      _ptr(src_positions), _ptr(dst_starts), src_positions.shape[0],
-                                      _stream(_op_stream(pool, stream))))
+    R, width, bt, cu = _op_batch(pool, block_tables, cu_keep)
+    n = _op_dims(src_positions, "src_positions", 1)[0]
+    sp = _op_ptr(pool, src_positions, "src_positions", _I32, (n,))
+    dp = _op_ptr(pool, dst_starts, "dst_starts", _I32, (R,))
+    _check(load_library().pkv_compact(pool.handle, bt, width, R, cu, sp, dp, n, _op_stream(pool, stream)))
 
 
 def pkv_last_plan_stats(pool: Pool) -> dict:
@@ -765,6 +785,7 @@ def pkv_debug_set(pool: Pool, what: int, value: int):
     PKV_DEBUG_FUSED_FORM (0 per batch, 1 in-kernel append, 2 append first) or PKV_DEBUG_TREE_FORM (0 per batch, 1 rows
     of 16, 2 tiles of 128)."""
     _check(load_library().pkv_debug_set(pool.handle, int(what), int(value)))
+    pool._op_ws.clear()   # sizes may depend on it
 
 
 def pkv_profile_read(pool: Pool, reset: bool = False) -> dict:

@@ -38,20 +38,34 @@ class FakePool:
     def __init__(self):
         self.k = torch.zeros(1)
         self.num_blocks, self.num_kv_heads, self.head_dim = 8, 2, 64
-        self.handle = None
+        self.handle, self.device_index = None, 0
+
+
+I1, I2, Q = torch.zeros(3, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32), torch.zeros((2, 2, 64), dtype=torch.bfloat16)
 
 
 @pytest.mark.parametrize("call", [
-    lambda p, t: pkv.pkv_tree_attn(p, t, t, t, t, t, t, 1.0, stream=object()),
-    lambda p, t: pkv.pkv_tree_mask(p, t, t, stream=object()),
-    lambda p, t: pkv.pkv_select_blocks(p, None, t, t, t, t, 4, stream=object()),
-    lambda p, t: pkv.pkv_sparse_attn(p, t, t, t, t, t, 1.0, stream=object()),
-    lambda p, t: pkv.pkv_summarize(p, None, t, t, t, t, stream=object()),
-    lambda p, t: pkv.pkv_fork(p, t, t, t, t, t, t, stream=object()),
-    lambda p, t: pkv.pkv_copy_blocks(p, t, t, stream=object()),
-    lambda p, t: pkv.pkv_compact(p, t, t, t, t, stream=object()),
-    lambda p, t: pkv.BlockSummary(p, t, t),
+    lambda p: pkv.pkv_tree_attn(p, Q, I2, I1, I1, I1, I2, 1.0),
+    lambda p: pkv.pkv_tree_mask(p, I1, I1),
+    lambda p: pkv.pkv_select_blocks(p, None, Q, I1, I2, I1, 4),
+    lambda p: pkv.pkv_sparse_attn(p, Q, I1, I2, I1, Q, 1.0),
+    lambda p: pkv.pkv_summarize(p, None, I2, I1, I1, I1),
+    lambda p: pkv.pkv_fork(p, I2, I1, I1, I1, I1, I1),
+    lambda p: pkv.pkv_copy_blocks(p, I1, I1),
+    lambda p: pkv.pkv_compact(p, I2, I1, I1, I1),
+    lambda p: pkv.BlockSummary(p, Q, Q),
+    lambda p: pkv.pkv_compact(p, [[0]], [0, 1], [0], [0]),
 ])
-def test_cpu_tensors_are_refused(call):
+def test_tensors_that_are_not_on_the_device_are_refused(call):
     with pytest.raises(TypeError, match="CUDA tensor"):
-        call(FakePool(), torch.zeros((2, 2, 64), dtype=torch.int32))
+        call(FakePool())
+
+
+@pytest.mark.parametrize("call", [
+    lambda p: pkv.pkv_tree_attn(p, Q, I1, I1, I1, I1, I2, 1.0),
+    lambda p: pkv.pkv_fork(p, I1, I1, I1, I1, I1, I1),
+    lambda p: pkv.pkv_copy_blocks(p, I2, I1),
+])
+def test_wrong_dimensions_are_refused(call):
+    with pytest.raises(ValueError, match="dimensions"):
+        call(FakePool())
