@@ -400,14 +400,16 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
  * (formulas and rounding as above; blocks of one list must be distinct, in any
  * order; entries below 0 and blocks behind the token are skipped, an entry beyond
  * the table is flagged and skipped).  A list without a key gives O = 0,
- * LSE = -inf.  The split over a cluster of CTAs is merged through their shared
- * memory: no workspace.
+ * LSE = -inf.  workspace: pkv_sparse_attn_workspace_size() bytes (a constant of
+ * the pool), 256-byte aligned, used by one call at a time as for pkv_tree_attn.
  * Both calls read all metadata on the device, can be captured into a graph and
  * run on `stream` alone.
  */
+int pkv_sparse_attn_workspace_size(pkv_pool* pool, size_t* bytes);
 int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
                     const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs, int num_tokens,
-                    const int32_t* selected, int top_k, float scale, void* o, float* lse, void* stream);
+                    const int32_t* selected, int top_k, float scale, void* o, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /*
  * ---- Pages: sharing, copying, allocating and freeing on the device ----------

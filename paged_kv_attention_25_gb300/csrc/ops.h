@@ -16,13 +16,14 @@ struct TreeForm {
 TreeForm tree_form(bool tensor, int num_sms);
 // tmk / tmv: the pool's block maps (rows form: 128-byte swizzle, unused by FP8
 // pools with head_dim 64); tmq: q viewed as [T][Hq][D] in boxes of one tile.
+// (launch_tree_rows also runs the attention over selected blocks.)
 int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* stream);
 int launch_tree_tc(const TreeArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream);
 int launch_tree_merge(const TreeArgs& a, const TreeForm& f, void* stream);
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
                      unsigned* err, void* stream);
 
-// One call over selected blocks (pkv_summarize, pkv_select_blocks, pkv_sparse_attn).
+// One call of pkv_summarize or pkv_select_blocks.
 struct SparseArgs {
   PoolView pool;
   const void* q;
@@ -37,17 +38,12 @@ struct SparseArgs {
   int8_t* exps;      // [blocks][kv heads]
   int32_t* sel;      // [tokens][kv heads][top_k]
   int top_k, sinks, recent;
-  float scale_log2;
-  void* o;
-  float* lse;
-  uint64_t wait_ns;
   int num_sms;
 };
 int launch_summarize(const SparseArgs& a, void* stream);
 // Blocks of a table row that the selection can take (its scores stay in shared memory).
 int select_max_blocks();
 int launch_select(const SparseArgs& a, void* stream);
-int launch_sparse(const SparseArgs& a, const void* tmk, const void* tmv, void* stream);
 
 // pkv_fork.
 struct ForkArgs {

@@ -69,6 +69,24 @@ TreeWs tree_ws(const pkv_pool* pool, const TreeForm& f) {
   return w;
 }
 
+TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, void* workspace) {
+  TreeArgs a{};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.pool = pool->view();
+  a.cuts = reinterpret_cast<TreeCut*>(ws + w.cuts);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  a.ctas = f.ctas;
+  a.wait_ns = pool->wait_ns;
+  return a;
+}
+
+int check_workspace(const void* workspace, size_t have, size_t need, const char* size_fn) {
+  if (!workspace || have < need) return fail(PKV_EINVAL, std::string("workspace missing or smaller than ") + size_fn);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_EINVAL, "workspace must be 256-byte aligned");
+  return PKV_OK;
+}
+
 // Which form a batch takes.
 bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens) {
   if (pool->tree_form != 0) return pool->tree_form == 2;
@@ -130,13 +148,10 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
   const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens), pool->num_sms);
   const TreeWs w = tree_ws(pool, form);
-  if (!workspace || workspace_bytes < w.total)
-    return fail(PKV_EINVAL, "workspace missing or smaller than pkv_tree_attn_workspace_size()");
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_EINVAL, "workspace must be 256-byte aligned");
+  if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_tree_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
   if ((rc = finish_swap_in(pool, stream))) return rc;
-  TreeArgs a;
-  a.pool = pool->view();
+  TreeArgs a = tree_args(pool, form, w, workspace);
   a.q = q;
   a.num_q_heads = num_q_heads;
   a.group = num_q_heads / pool->num_kv_heads;
@@ -152,15 +167,8 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o;
   a.lse = lse;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.cuts = reinterpret_cast<TreeCut*>(ws + w.cuts);
-  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
-  a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  a.ctas = form.ctas;
   a.tile_tokens = kTcRows / a.group;
-  a.q_box_tokens = 0;
   a.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  a.wait_ns = pool->wait_ns;
   if (form.tensor) {
     CUtensorMap tmap_q;
     if ((rc = make_q_tmap(&tmap_q, q, num_tokens, num_q_heads, pool->head_dim, a.group, &a.q_box_tokens))) return rc;
@@ -243,9 +251,16 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
   return PKV_OK;
 }
 
+int pkv_sparse_attn_workspace_size(pkv_pool* pool, size_t* bytes) {
+  if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
+  *bytes = tree_ws(pool, tree_form(false, pool->num_sms)).total;
+  return PKV_OK;
+}
+
 int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
                     const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs, int num_tokens,
-                    const int32_t* selected, int top_k, float scale, void* o, float* lse, void* stream) {
+                    const int32_t* selected, int top_k, float scale, void* o, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
   int rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
@@ -254,11 +269,12 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
   if (!q || !q_positions || !block_tables || !cu_q_lens || !selected || !o) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
-  if (static_cast<int64_t>(num_tokens) * num_q_heads * 8 >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
+  const TreeForm form = tree_form(false, pool->num_sms);
+  const TreeWs w = tree_ws(pool, form);
+  if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_sparse_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
   if ((rc = finish_swap_in(pool, stream))) return rc;
-  SparseArgs a{};
-  a.pool = pool->view();
+  TreeArgs a = tree_args(pool, form, w, workspace);
   a.q = q;
   a.num_q_heads = num_q_heads;
   a.group = num_q_heads / pool->num_kv_heads;
@@ -268,15 +284,16 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   a.cu_q_lens = cu_q_lens;
   a.num_reqs = num_reqs;
   a.num_tokens = num_tokens;
-  a.sel = const_cast<int32_t*>(selected);
+  a.sel = selected;
   a.top_k = top_k;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o;
   a.lse = lse;
-  a.wait_ns = pool->wait_ns;
-  a.num_sms = pool->num_sms;
-  rc = timed_launch(pool, 1, stream, [&] { return launch_sparse(a, rows_map(pool, false), rows_map(pool, true), stream); });
+  rc = timed_launch(pool, 1, stream,
+                    [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected attention launch");
+  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, form, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected merge launch");
   return PKV_OK;
 }
 

@@ -16,7 +16,8 @@
 
 namespace pkv {
 
-// One tree-attention call (pkv_tree_attn).
+// One call of the tree attention (pkv_tree_attn), or of the attention over
+// selected blocks (pkv_sparse_attn: `sel` is not nullptr).
 struct TreeArgs {
   PoolView pool;
   const void* q;
@@ -29,6 +30,9 @@ struct TreeArgs {
   int num_reqs, num_tokens;
   const uint32_t* mask;
   int mask_words;
+  const int32_t* positions;   // selected blocks: the tokens' positions,
+  const int32_t* sel;         // their lists [tokens][kv heads][top_k]
+  int top_k;
   float scale_log2;
   void* o;
   float* lse;
@@ -53,6 +57,21 @@ struct alignas(16) TreeCut {
   int f0, g, pad0, pad1;
 };
 static_assert(sizeof(TreeCut) == 48, "TreeCut layout: three 16-byte loads");
+
+// The request of token t (the last with cu <= t), or -1 for a token that
+// belongs to none.  A whole warp: each round narrows the range 32-fold.
+__device__ __forceinline__ int req_of_warp(const int32_t* cu, int num_reqs, int t, int lane) {
+  int lo = 0, n = num_reqs;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && __ldg(cu + at) <= t);
+    const int k = max(0, __popc(le) - 1);
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
+}
 
 // A request's lengths, made safe: whatever the device arrays hold, tokens stay
 // inside [0, num_tokens) and keys inside the block table's row.

@@ -23,7 +23,7 @@
 #include "internal.h"
 #include "ops.h"
 #include "ptx.cuh"
-#include "rows.cuh"
+#include "sched.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SparseArgs a)
   const int rank = CS > 1 ? static_cast<int>(blockIdx.x % CS) : 0;
   const int64_t th = blockIdx.x / CS;
   const int g = static_cast<int>(th % Hkv), t = static_cast<int>(th / Hkv);
-  const int r = req_of(a.cu_q_lens, a.num_reqs, t);
+  const int r = req_of_warp(a.cu_q_lens, a.num_reqs, t, lane);
   if (r < 0) return;   // cluster-uniform
   const int p = __ldg(a.positions + t);
   int32_t* out = a.sel + th * a.top_k;
@@ -242,40 +242,59 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SparseArgs a)
 #pragma unroll
     for (int w = 0; w < 8; ++w) qq[i][w] = reinterpret_cast<const int*>(s_q)[(i * 4 + sub) * 8 + w];
   const int32_t* bt_row = a.block_tables + static_cast<int64_t>(r) * a.max_blocks;
-  for (int base = b0 + warp * 8; base < b1; base += kSelThreads / 4) {
-    const int b = base + (lane >> 2);
-    int pb = -1;
-    if (b < b1) {
-      pb = __ldg(bt_row + b);
-      if (pb < 0 || pb >= a.pool.num_blocks) {
-        if (sub == 0) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
-        pb = -1;
-      }
-    }
-    int s = 0, e = 0;
-    if (pb >= 0) {
+  // Two iterations' codes in flight, their block ids one more ahead.
+  constexpr int kStep = kSelThreads / 4;
+  const int first = b0 + warp * 8 + (lane >> 2);
+  auto load_id = [&](int b) -> int { return b < b1 ? __ldg(bt_row + b) : -1; };
+  struct Codes { uint4 c[kPieces]; int e; };
+  auto load_codes = [&](int pb, Codes& k) {
+    k.e = 0;
+    if (pb >= 0 && pb < a.pool.num_blocks) {
       const int64_t chunk = static_cast<int64_t>(pb) * Hkv + g;
       const uint4* src = reinterpret_cast<const uint4*>(a.codes + chunk * 2 * D) + sub;
-      uint4 c[kPieces];
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) c[i] = __ldg(src + i * 4);
-      e = __ldg(a.exps + chunk);
+      for (int i = 0; i < kPieces; ++i) k.c[i] = __ldg(src + i * 4);
+      k.e = __ldg(a.exps + chunk);
+    } else {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int w[4] = {static_cast<int>(c[i].x), static_cast<int>(c[i].y), static_cast<int>(c[i].z),
-                          static_cast<int>(c[i].w)};
+      for (int i = 0; i < kPieces; ++i) k.c[i] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto score = [&](int b, int pb, const Codes& k) {
+    int s = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s = __dp2a_lo(qq[i][2 * x], w[x], s);
-          s = __dp2a_hi(qq[i][2 * x + 1], w[x], s);
-        }
+    for (int i = 0; i < kPieces; ++i) {
+      const int w[4] = {static_cast<int>(k.c[i].x), static_cast<int>(k.c[i].y), static_cast<int>(k.c[i].z),
+                        static_cast<int>(k.c[i].w)};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        s = __dp2a_lo(qq[i][2 * x], w[x], s);
+        s = __dp2a_hi(qq[i][2 * x + 1], w[x], s);
       }
     }
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     if (sub == 0 && b < b1) {
+      const bool there = pb >= 0 && pb < a.pool.num_blocks;
+      if (!there) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
       const bool forced = b < a.sinks || b >= n - a.recent;
-      keys[b - b0] = pb < 0 ? 0u : forced ? 0xffffffffu : key_of(__int2float_rn(s) * pow2f(max(-126, e)));
+      keys[b - b0] = !there ? 0u : forced ? 0xffffffffu : key_of(__int2float_rn(s) * pow2f(max(-126, k.e)));
+    }
+  };
+  {
+    const int iters = b1 > b0 + warp * 8 ? (b1 - b0 - warp * 8 + kStep - 1) / kStep : 0;   // warp-uniform
+    int id0 = load_id(first), id1 = load_id(first + kStep), id2 = load_id(first + 2 * kStep);
+    Codes k0, k1;
+    load_codes(id0, k0);
+    for (int i = 0; i < iters; i += 2) {
+      load_codes(id1, k1);
+      const int id3 = load_id(first + (i + 3) * kStep);
+      score(first + i * kStep, id0, k0);
+      id0 = id2;
+      load_codes(id0, k0);
+      id2 = load_id(first + (i + 4) * kStep);
+      if (i + 1 < iters) score(first + (i + 1) * kStep, id1, k1);
+      id1 = id3;
     }
   }
   __syncthreads();
@@ -367,185 +386,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SparseArgs a)
   if constexpr (CS > 1) cg::this_cluster().sync();   // no CTA leaves while another reads its shared memory
 }
 
-// ---------------------------------------------------------------- attention
-constexpr int kSpThreads = 32 * kRowWarps;
-
-template <int D, bool F8>
-struct SparseSmem {
-  using R = RowsSmem<D, F8>;
-  static constexpr int kState = kRowTile * R::kMergeRow * 4;   // the CTA's merged state, behind the warps'
-  static_assert(R::kMerge + kState <= R::kRing, "the merge fits the drained ring");
-};
-
-// One cluster of CS CTAs per (token, KV head, tile of 16 heads of the group):
-// CTA i streams the i-th part of the token's list, its warps round-robin; the
-// warps' states are merged in shared memory and the CTAs' through the
-// cluster's distributed shared memory, in a fixed order.
-template <int D, bool F8, int CS>
-__global__ void __launch_bounds__(kSpThreads, 3)
-sparse_kernel(const SparseArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-  using S = RowsSmem<D, F8>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kBuf);
-  __shared__ int s_abort_flag;
-  volatile int* s_abort = &s_abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.group, Hkv = a.pool.num_kv_heads;
-  const int rtiles = (G + kRowTile - 1) / kRowTile;
-  const int rank = CS > 1 ? static_cast<int>(blockIdx.x % CS) : 0;
-  int64_t x = blockIdx.x / CS;
-  const int tile = static_cast<int>(x % rtiles);
-  x /= rtiles;
-  const int g = static_cast<int>(x % Hkv), t = static_cast<int>(x / Hkv);
-  const int r = req_of(a.cu_q_lens, a.num_reqs, t);
-  if (r < 0) return;   // cluster-uniform
-  if (tid == 0) {
-    for (int i = 0; i < kRowWarps * S::kStages; ++i) mbar_init(&bars[i], 1);
-    s_abort_flag = 0;
-    fence_mbar_init();
-  }
-  const int p = __ldg(a.positions + t);
-  const int h0 = tile * kRowTile, nrows = min(kRowTile, G - h0);
-  const int32_t* list = a.sel + (static_cast<int64_t>(t) * Hkv + g) * a.top_k;
-  const int32_t* bt_row = a.block_tables + static_cast<int64_t>(r) * a.max_blocks;
-  const int per = (a.top_k + CS - 1) / CS;
-  const int i0 = min(a.top_k, rank * per), i1 = min(a.top_k, i0 + per);
-  const int nb_w = i1 - i0 > warp ? (i1 - i0 - warp + kRowWarps - 1) / kRowWarps : 0;
-  __syncthreads();
-
-  uint8_t* my_ring = ring + warp * S::kStages * S::kStage;
-  uint64_t* my_bars = bars + warp * S::kStages;
-  const uint32_t my_addr = smem_u32(my_ring);
-  const float sl2 = F8 ? a.scale_log2 * a.pool.k_scale : a.scale_log2;
-  // Lane l: listed block and its place in the pool (-1: none) of iteration base + l.
-  auto load_ids = [&](int base, int& blk) -> int {
-    const int i = base + lane;
-    blk = -1;
-    if (i >= nb_w) return -1;
-    blk = __ldg(list + i0 + warp + kRowWarps * i);
-    if (blk < 0 || p < 0 || blk > (p >> 4)) return -1;   // padding, or a block that the token does not see
-    if (blk >= a.max_blocks) {
-      atomicOr(a.pool.err, PKV_DEVERR_POSITION);
-      return -1;
-    }
-    const int pb = __ldg(bt_row + blk);
-    if (pb < 0 || pb >= a.pool.num_blocks) {
-      atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
-      return -1;
-    }
-    return pb;
-  };
-  int blk_cur, blk_next, win = 0;
-  int ids_cur = load_ids(0, blk_cur), ids_next = load_ids(32, blk_next);
-  auto issue = [&](int j) {
-    const int pb = __shfl_sync(0xffffffffu, (j >> 5) == win ? ids_cur : ids_next, j & 31);
-    if (lane == 0) {
-      const int st = j % S::kStages;
-      if (pb >= 0)
-        rows_issue<D, F8>(a.pool, &tmk, &tmv, my_ring + st * S::kStage, static_cast<int64_t>(pb) * Hkv + g, &my_bars[st]);
-      else
-        mbar_arrive(&my_bars[st]);
-    }
-  };
-  int issued = 0;
-  for (; issued < S::kStages && issued < nb_w; ++issued) issue(issued);
-  RowTile<D, F8> rt;
-  const uint16_t* q0 = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(t) * a.num_q_heads + g * G + h0) * D;
-  const int ra = lane >> 2;
-  rt.init(ra < nrows ? q0 + ra * D : nullptr, ra + 8 < nrows ? q0 + (ra + 8) * D : nullptr, lane);
-  bool ok = true;
-  for (int i = 0; i < nb_w; ++i) {
-    if ((i & 31) == 0 && i > 0) {
-      ids_cur = ids_next;
-      blk_cur = blk_next;
-      win = i >> 5;
-      ids_next = load_ids(i + 32, blk_next);
-    }
-    const int st = i % S::kStages;
-    if (!(ok = mbar_wait_warp(&my_bars[st], (i / S::kStages) & 1, s_abort, a.wait_ns))) break;
-    const uint32_t kb = my_addr + st * S::kStage;
-    if (__shfl_sync(0xffffffffu, ids_cur, i & 31) >= 0) {
-      const int seen = p - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1;   // keys of the block up to p
-      if (seen >= kBlockSize)
-        rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
-      else
-        rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
-    }
-    __syncwarp();
-    if (issued < nb_w) {
-      issue(issued);
-      ++issued;
-    }
-  }
-  if (!ok) {
-    if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
-    *s_abort = 1;
-    for (int j = max(0, issued - S::kStages); j < issued; ++j)
-      (void)mbar_wait(&my_bars[j % S::kStages], (j / S::kStages) & 1, nullptr, a.wait_ns);
-  }
-  __syncthreads();   // every warp's ring has drained
-  float* mbuf = reinterpret_cast<float*>(ring);
-  float* state = reinterpret_cast<float*>(ring + S::kMerge);
-  rt.store(mbuf + warp * kRowTile * S::kMergeRow, lane);
-  __syncthreads();
-  constexpr int kDims = D / 8;
-  const int rr = tid >> 3, d0 = (tid & 7) * kDims;
-  {
-    float M = -CUDART_INF_F, L = 0.f, acc[kDims];
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-      const float* src = mbuf + (w * kRowTile + rr) * S::kMergeRow;
-      if (src[D + 1] == 0.f) continue;   // the warp saw no key (a NaN score leaves m, not l, as it was)
-      const float f = fast_exp2(src[D] - M);
-      L = fmaf(f, src[D + 1], L);
-#pragma unroll
-      for (int d = 0; d < kDims; ++d) acc[d] = fmaf(f, src[d0 + d], acc[d]);
-    }
-    float* dst = state + rr * S::kMergeRow;
-#pragma unroll
-    for (int d = 0; d < kDims; d += 4)
-      *reinterpret_cast<float4*>(dst + d0 + d) = make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
-    if (d0 == 0) { dst[D] = M; dst[D + 1] = L; }
-  }
-  if constexpr (CS > 1) cg::this_cluster().sync(); else __syncthreads();
-  // Rows (in pieces of 4 dims) shared out over the cluster's threads.
-  for (int i = rank * kSpThreads + tid; i < nrows * (D / 4); i += CS * kSpThreads) {
-    const int row = i / (D / 4), d = (i % (D / 4)) * 4;
-    float M = -CUDART_INF_F, m[CS];
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      const float* st = state + row * S::kMergeRow;
-      if constexpr (CS > 1) st = cg::this_cluster().map_shared_rank(st, c);
-      m[c] = st[D];
-      M = fmaxf(M, m[c]);
-    }
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      const float* st = state + row * S::kMergeRow;
-      if constexpr (CS > 1) st = cg::this_cluster().map_shared_rank(st, c);
-      if (st[D + 1] == 0.f) continue;
-      const float f = fast_exp2(m[c] - M);
-      L = fmaf(f, st[D + 1], L);
-      const float4 v = *reinterpret_cast<const float4*>(st + d);
-      acc[0] = fmaf(f, v.x, acc[0]); acc[1] = fmaf(f, v.y, acc[1]);
-      acc[2] = fmaf(f, v.z, acc[2]); acc[3] = fmaf(f, v.w, acc[3]);
-    }
-    const float inv = L == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / L;
-    const int64_t row_at = static_cast<int64_t>(t) * a.num_q_heads + g * G + h0 + row;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row_at * D + d) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    if (d == 0 && a.lse)
-      a.lse[row_at] = L == 0.f ? -CUDART_INF_F : (M + fast_log2(L)) * 0.69314718055994530942f;
-  }
-  if constexpr (CS > 1) cg::this_cluster().sync();   // no CTA leaves while another reads its state
-}
-
 // Launches a kernel with clusters of CS CTAs.
 template <class K, class... Args>
 cudaError_t launch_cluster(K kernel, int cs, int64_t grid, int threads, int smem, cudaStream_t s, Args... args) {
@@ -589,30 +429,6 @@ int launch_select_d(const SparseArgs& a, cudaStream_t s) {
   }
 }
 
-template <int D, bool F8, int CS>
-int launch_sparse_t(const SparseArgs& a, const CUtensorMap* k, const CUtensorMap* v, cudaStream_t s) {
-  (void)sizeof(SparseSmem<D, F8>);
-  const int smem = RowsSmem<D, F8>::kTotal;
-  cudaError_t e = smem_attr_once<sparse_kernel<D, F8, CS>>(smem);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(a.num_tokens) * a.pool.num_kv_heads * ((a.group + kRowTile - 1) / kRowTile) * CS;
-  return launch_cluster(sparse_kernel<D, F8, CS>, CS, grid, kSpThreads, smem, s, a, *k, *v);
-}
-
-template <int D, bool F8>
-int launch_sparse_d(const SparseArgs& a, const CUtensorMap* k, const CUtensorMap* v, cudaStream_t s) {
-  const int64_t units = static_cast<int64_t>(a.num_tokens) * a.pool.num_kv_heads * ((a.group + kRowTile - 1) / kRowTile);
-  // Enough CTAs for three a SM, each with four blocks at least.
-  int cs = 1;
-  while (cs < 8 && units * cs < 3 * a.num_sms && a.top_k / (2 * cs) >= kRowWarps) cs *= 2;
-  switch (cs) {
-    case 1: return launch_sparse_t<D, F8, 1>(a, k, v, s);
-    case 2: return launch_sparse_t<D, F8, 2>(a, k, v, s);
-    case 4: return launch_sparse_t<D, F8, 4>(a, k, v, s);
-    default: return launch_sparse_t<D, F8, 8>(a, k, v, s);
-  }
-}
-
 template <int D, bool F8>
 int launch_summarize_d(const SparseArgs& a, cudaStream_t s) {
   // A warp of 16 tokens finds about one new block in a prompt; a batch of
@@ -641,15 +457,6 @@ int select_max_blocks() { return 8 * kSelMost; }
 int launch_select(const SparseArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return a.pool.head_dim == 128 ? launch_select_d<128>(a, s) : launch_select_d<64>(a, s);
-}
-
-int launch_sparse(const SparseArgs& a, const void* tmk, const void* tmv, void* stream) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const CUtensorMap* k = static_cast<const CUtensorMap*>(tmk);
-  const CUtensorMap* v = static_cast<const CUtensorMap*>(tmv);
-  const bool f8 = a.pool.elem_bytes == 1;
-  if (a.pool.head_dim == 128) return f8 ? launch_sparse_d<128, true>(a, k, v, s) : launch_sparse_d<128, false>(a, k, v, s);
-  return f8 ? launch_sparse_d<64, true>(a, k, v, s) : launch_sparse_d<64, false>(a, k, v, s);
 }
 
 }  // namespace pkv

@@ -1,6 +1,8 @@
 // Attention of drafted tokens over a cache (pkv_tree_attn): token t of request
 // r sees key slot j of its request if j < prefix_r, or if j lies in
 // [prefix_r, ctx_r) and bit j - prefix_r of the token's mask is set.
+// Attention of tokens over listed blocks (pkv_sparse_attn): token t at position
+// p sees the keys j <= p of the blocks of its list.
 //
 //   s_j = scale q . K_j,   O = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),
 //   LSE = m + ln sum_j exp(s_j - m)       over the slots that the token sees;
@@ -20,8 +22,8 @@ namespace pkv {
 namespace {
 
 constexpr int kRowsThreads = 32 * kRowWarps;
-// Rows kernel: a group has 16 query rows and one KV head, a unit is one block;
-// a CTA takes at least four blocks a warp.  A request without keys keeps one
+// Rows kernel: a group has 16 query rows and one KV head, a unit is one block
+// (or one entry of a list); a CTA takes at least four blocks a warp.  A request without keys keeps one
 // (empty) unit a group: its rows are written too.
 using RowsShare = Share<4 * kRowWarps>;
 __device__ __forceinline__ int rows_tiles(const TreeReq& q, int group) {
@@ -29,10 +31,15 @@ __device__ __forceinline__ int rows_tiles(const TreeReq& q, int group) {
 }
 __device__ __forceinline__ int rows_blocks(const TreeReq& q) { return max(1, (q.ctx + kBlockSize - 1) / kBlockSize); }
 
-// One segment: blocks [b0, b0 + nb) of one (request, KV head, row tile).
-template <int D, bool F8>
+// A CTA walks its share of the line, segment by segment: blocks (list entries)
+// [b0, b0 + nb) of one group.  Its four warps take them in turn, each with its
+// own ring of copies and its own state, and merge at the segment's end.
+// Bound by the reads of K and V; the split in equal shares matters more than
+// the work per block (lists of 128 blocks for 256 groups: 62 us in clusters of
+// two CTAs, whose 512 CTAs leave a second, nearly empty wave; 4x us here).
+template <int D, bool F8, bool LIST>
 __global__ void __launch_bounds__(kRowsThreads, 3)
-tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using S = RowsSmem<D, F8>;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -53,11 +60,25 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
     fence_mbar_init();
   }
   auto units = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv * rows_blocks(q); };
-  const int worker[1] = {static_cast<int>(blockIdx.x)}, most[1] = {a.ctas};
-  TreeShare shares[1];
-  tree_shares<RowsShare, kRowsThreads, 1>(a, scratch, worker, most, shares,
-                                          [&](const TreeReq& q, int) { return units(q); });
-  TreeShare& sh = shares[0];
+  const int rtiles = (G + kRowTile - 1) / kRowTile;   // LIST: row tiles of a token's group
+  TreeShare sh;
+  if constexpr (LIST) {
+    // Every token of the requests has top_k units a group.
+    const int tokens = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
+    sh.U = static_cast<int64_t>(tokens) * Hkv * rtiles * a.top_k;
+    sh.workers = RowsShare::workers(sh.U, a.ctas);
+    sh.u = sh.end = 0;
+    if (sh.U > 0 && static_cast<int>(blockIdx.x) < sh.workers) {
+      sh.u = RowsShare::begin(sh.U, sh.workers, blockIdx.x);
+      sh.end = RowsShare::begin(sh.U, sh.workers, blockIdx.x + 1);
+    }
+  } else {
+    const int worker[1] = {static_cast<int>(blockIdx.x)}, most[1] = {a.ctas};
+    TreeShare shares[1];
+    tree_shares<RowsShare, kRowsThreads, 1>(a, scratch, worker, most, shares,
+                                            [&](const TreeReq& q, int) { return units(q); });
+    sh = shares[0];
+  }
   if (sh.u >= sh.end) return;
   __syncthreads();
 
@@ -66,20 +87,43 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
   const uint32_t my_addr = smem_u32(my_ring);
   const float sl2 = F8 ? a.scale_log2 * a.pool.k_scale : a.scale_log2;
   int cnt = 0;   // stages this warp has issued in the launch
-  int req = sh.req;
-  TreeReq rq = tree_req(a, req);
+  int req = LIST ? 0 : sh.req;
+  TreeReq rq{0, 0, 0, 0, false};
+  if constexpr (!LIST) rq = tree_req(a, req);
   while (sh.u < sh.end) {
-    for (int64_t n = units(rq); sh.off >= n; n = units(rq)) {   // the next request with work (there is one)
-      sh.off -= n;
-      if (++req >= a.num_reqs) return;
-      rq = tree_req(a, req);
+    int kblk, b0, g, row0, nrows, pos = 0;   // units of the group, its first unit here, its rows
+    const int32_t* list = nullptr;
+    if constexpr (LIST) {
+      kblk = a.top_k;
+      const int64_t grp = sh.u / kblk;
+      b0 = static_cast<int>(sh.u - grp * kblk);
+      const int64_t th = grp / rtiles;
+      row0 = static_cast<int>(grp - th * rtiles) * kRowTile;
+      g = static_cast<int>(th % Hkv);
+      rq.t0 = static_cast<int>(th / Hkv);
+      nrows = min(kRowTile, G - row0);
+      req = req_of_warp(a.cu_q_lens, a.num_reqs, rq.t0, lane);
+      pos = __ldg(a.positions + rq.t0);
+      list = a.sel + th * a.top_k;
+    } else {
+      for (int64_t n = units(rq); sh.off >= n; n = units(rq)) {   // the next request with work (there is one)
+        sh.off -= n;
+        if (++req >= a.num_reqs) return;
+        rq = tree_req(a, req);
+      }
+      kblk = rows_blocks(rq);
+      const int grp = static_cast<int>(sh.off / kblk);
+      b0 = static_cast<int>(sh.off - static_cast<int64_t>(grp) * kblk);
+      const int ntile = rows_tiles(rq, G);
+      g = grp / ntile;
+      row0 = (grp - g * ntile) * kRowTile;
+      nrows = min(kRowTile, rq.n * G - row0);
     }
-    const int kblk = rows_blocks(rq), ntile = rows_tiles(rq, G);
-    const int grp = static_cast<int>(sh.off / kblk);
-    const int b0 = static_cast<int>(sh.off % kblk);
     const int nb = static_cast<int>(min(static_cast<int64_t>(kblk - b0), sh.end - sh.u));
-    const int g = grp / ntile, tile = grp % ntile;
-    const int row0 = tile * kRowTile, nrows = min(kRowTile, rq.n * G - row0);
+    if (LIST && req < 0) {   // a token that belongs to no request: its rows are left alone
+      sh.u += nb;
+      continue;
+    }
     // Rows g' and g' + 8 of this thread.
     const int ra = lane >> 2, rb = ra + 8;
     auto q_row = [&](int rr) -> const uint16_t* {
@@ -91,21 +135,33 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
     auto mask_row = [&](int rr) {
       return a.mask + static_cast<int64_t>(rq.t0 + (row0 + min(rr, nrows - 1)) / G) * a.mask_words;
     };
-    const int end_blk = min(b0 + nb, (rq.ctx + kBlockSize - 1) / kBlockSize);
+    const int end_blk = LIST ? b0 + nb : min(b0 + nb, (rq.ctx + kBlockSize - 1) / kBlockSize);
     const int live = max(0, end_blk - b0);
     const int nb_w = live > warp ? (live - warp + kRowWarps - 1) / kRowWarps : 0;
     const int32_t* bt_row = a.block_tables + static_cast<int64_t>(req) * a.max_blocks;
-    auto load_ids = [&](int base) -> int {
+    // Lane l: the pool block (-1: none) of the warp's iteration base + l, and the block's index in the request.
+    auto load_ids = [&](int base, int& blk) -> int {
       const int i = base + lane;
+      blk = -1;
       if (i >= nb_w) return -1;
-      const int pb = __ldg(bt_row + b0 + warp + kRowWarps * i);
+      blk = b0 + warp + kRowWarps * i;
+      if constexpr (LIST) {
+        blk = __ldg(list + blk);
+        if (blk < 0 || pos < 0 || blk > (pos >> 4)) return -1;   // padding, or a block that the token does not see
+        if (blk >= a.max_blocks) {
+          atomicOr(a.pool.err, PKV_DEVERR_POSITION);
+          return -1;
+        }
+      }
+      const int pb = __ldg(bt_row + blk);
       if (pb < 0 || pb >= a.pool.num_blocks) {
         atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
         return -1;
       }
       return pb;
     };
-    int ids_cur = load_ids(0), ids_next = load_ids(32), win = 0;
+    int blk_cur, blk_next, win = 0;
+    int ids_cur = load_ids(0, blk_cur), ids_next = load_ids(32, blk_next);
     auto id_of = [&](int j) {   // warp-uniform j
       return __shfl_sync(0xffffffffu, (j >> 5) == win ? ids_cur : ids_next, j & 31);
     };
@@ -124,25 +180,35 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
     for (; issued < S::kStages && issued < nb_w; ++issued) issue(issued);
     RowTile<D, F8> rt;
     rt.init(q_row(ra), q_row(rb), lane);
-    const uint32_t* m0 = mask_row(ra);
-    const uint32_t* m1 = mask_row(rb);
+    const uint32_t* m0 = LIST ? nullptr : mask_row(ra);
+    const uint32_t* m1 = LIST ? nullptr : mask_row(rb);
     bool ok = true;
     for (int i = 0; i < nb_w; ++i) {
       if ((i & 31) == 0 && i > 0) {
         ids_cur = ids_next;
+        blk_cur = blk_next;
         win = i >> 5;
-        ids_next = load_ids(i + 32);
+        ids_next = load_ids(i + 32, blk_next);
       }
       const int st = (cnt + i) % S::kStages;
       if (!(ok = mbar_wait_warp(&my_bars[st], ((cnt + i) / S::kStages) & 1, s_abort, a.wait_ns))) break;
-      const int key0 = (b0 + warp + kRowWarps * i) * kBlockSize;
       const uint32_t kb = my_addr + st * S::kStage;
-      if (id_of(i) >= 0) {
-        if (key0 + kBlockSize <= rq.prefix)
-          rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
-        else
-          rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
-                                  tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
+      if (__shfl_sync(0xffffffffu, ids_cur, i & 31) >= 0) {
+        if constexpr (LIST) {
+          const int seen = pos - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1;   // keys up to the position
+          if (seen >= kBlockSize)
+            rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
+          else
+            rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
+        } else {
+          const int key0 = (b0 + warp + kRowWarps * i) * kBlockSize;
+          if (key0 + kBlockSize <= rq.prefix)
+            rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
+          else
+            rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2,
+                                         tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
+                                         tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
+        }
       }
       __syncwarp();
       if (issued < nb_w) {
@@ -158,7 +224,7 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
         (void)mbar_wait(&my_bars[(cnt + j) % S::kStages], ((cnt + j) / S::kStages) & 1, nullptr, a.wait_ns);
     }
     cnt += nb_w;
-    if (rt.odd) *s_odd = 1;
+    if (!LIST && rt.odd) *s_odd = 1;
     __syncthreads();   // every warp's ring has drained
     if (*s_abort) return;
     // Merge the warps' states: [warp][16][D + 4] floats over the ring.
@@ -187,7 +253,7 @@ tree_rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, cons
       for (int d = 0; d < kDims; ++d) acc[d] *= inv;
       const float lse2 = L == 0.f ? -CUDART_INF_F : M + fast_log2(L);
       const int f = row0 + rr, t = rq.t0 + f / G, h = g * G + f % G;
-      if (*s_odd) {
+      if (!LIST && *s_odd) {
         // V elements that are not finite, for the rows that see them.
         const uint32_t* mr = a.mask + static_cast<int64_t>(t) * a.mask_words;
         for (int b = max(b0, rq.prefix / kBlockSize); b < end_blk; ++b) {
@@ -357,13 +423,18 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restric
   if (lane == 0 && t - c0 >= words * 32) atomicOr(err, PKV_DEVERR_POSITION);   // its own bit has no word
 }
 
+template <int D, bool F8, bool LIST>
+int launch_rows_l(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
+  const int smem = RowsSmem<D, F8>::kTotal;
+  cudaError_t e = smem_attr_once<rows_kernel<D, F8, LIST>>(smem);
+  if (e != cudaSuccess) return e;
+  rows_kernel<D, F8, LIST><<<a.ctas, kRowsThreads, smem, s>>>(a, *tmk, *tmv);
+  return cudaGetLastError();
+}
+
 template <int D, bool F8>
 int launch_rows(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
-  const int smem = RowsSmem<D, F8>::kTotal;
-  cudaError_t e = smem_attr_once<tree_rows_kernel<D, F8>>(smem);
-  if (e != cudaSuccess) return e;
-  tree_rows_kernel<D, F8><<<a.ctas, kRowsThreads, smem, s>>>(a, *tmk, *tmv);
-  return cudaGetLastError();
+  return a.sel ? launch_rows_l<D, F8, true>(a, tmk, tmv, s) : launch_rows_l<D, F8, false>(a, tmk, tmv, s);
 }
 
 template <int D, int SlotRows>

@@ -51,7 +51,7 @@ EXPORTED = (
     "pkv_version", "pkv_copy_to_device", "pkv_copy_to_host", "pkv_debug_set",
     "pkv_cache_create", "pkv_cache_destroy", "pkv_cache_step", "pkv_cache_release", "pkv_cache_free_blocks",
     "pkv_tree_mask", "pkv_tree_attn_workspace_size", "pkv_tree_attn", "pkv_summarize", "pkv_select_blocks",
-    "pkv_sparse_attn", "pkv_fork_workspace_size", "pkv_fork", "pkv_copy_blocks", "pkv_compact",
+    "pkv_sparse_attn_workspace_size", "pkv_sparse_attn", "pkv_fork_workspace_size", "pkv_fork", "pkv_copy_blocks", "pkv_compact",
 )
 
 
@@ -150,7 +150,8 @@ def load_library():
             "pkv_tree_attn": [P, P, I, P, I, P, P, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
             "pkv_summarize": [P, P, I, I, P, P, P, I, P, P, P],
             "pkv_select_blocks": [P, P, I, P, P, I, P, I, I, P, P, I, I, I, P, P],
-            "pkv_sparse_attn": [P, P, I, P, P, I, P, I, I, P, I, F, P, P, P],
+            "pkv_sparse_attn_workspace_size": [P, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_sparse_attn": [P, P, I, P, P, I, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
             "pkv_fork_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
             "pkv_fork": [P, P, I, I, P, P, P, P, I, P, P, P, P, P, P, ctypes.c_size_t, P],
             "pkv_copy_blocks": [P, P, P, I, P, P, P],
@@ -572,16 +573,24 @@ def pkv_select_blocks(pool: Pool, summary: BlockSummary, q, q_positions, block_t
     return out
 
 
+def pkv_sparse_attn_workspace_size(pool: Pool) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().pkv_sparse_attn_workspace_size(pool.handle, ctypes.byref(n)))
+    return n.value
+
+
 def pkv_sparse_attn(pool: Pool, q, q_positions, block_tables, cu_q_lens, selected, scale: float, out=None, lse=None,
-                    stream=None, want_lse=True):
+                    workspace=None, stream=None, want_lse=True):
     """Attention of each token over its selected blocks [T, Hkv, k] (keys up to its position); returns (O, LSE)."""
     R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
     T, Hq, qp, out, lse = _op_query(pool, q, out, lse, want_lse, stream)
     pos = _op_ptr(pool, q_positions, "q_positions", _I32, (T,))
     k = _op_dims(selected, "selected", 3)[2]
     sel = _op_ptr(pool, selected, "selected", _I32, (T, pool.num_kv_heads, k))
+    ws, n = _op_workspace(pool, workspace, ("sparse",), pkv_sparse_attn_workspace_size, stream)
     _check(load_library().pkv_sparse_attn(pool.handle, qp, Hq, pos, bt, width, cu, R, T, sel, k, scale, out.data_ptr(),
-                                          None if lse is None else lse.data_ptr(), _op_stream(pool, stream)))
+                                          None if lse is None else lse.data_ptr(), ws.data_ptr(), n,
+                                          _op_stream(pool, stream)))
     return out, lse
 
 
