@@ -275,15 +275,59 @@ struct RowTile {
                  : "r"(a) : "memory");
   }
 
-  // Writes the warp's state to `buf` ([16][D + 4] floats: o unnormalised, m in log2 units, l).
-  __device__ __forceinline__ void store(float* buf, int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    float l0 = l[0], l1 = l[1];
+  // Sums l over the threads that share a row.
+  __device__ __forceinline__ void total_l(float& l0, float& l1) const {
+    l0 = l[0];
+    l1 = l[1];
 #pragma unroll
     for (int x = 1; x < 4; x <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, x);
       l1 += __shfl_xor_sync(0xffffffffu, l1, x);
     }
+  }
+
+  // Stores row g (i = 0) or g + 8 (i = 1), scaled, as bf16 or as floats.
+  __device__ __forceinline__ void put_bf16(uint16_t* row, int i, float f, int lane) const {
+    const int c = lane & 3;
+    if constexpr (F8) {   // dims (D/4) c .. (D/4)(c + 1) - 1, in two runs of D / 8
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < kTiles; j += 8) {
+          uint4 w;
+          w.x = pack_bf16x2(o[j][2 * i + e] * f, o[j + 1][2 * i + e] * f);
+          w.y = pack_bf16x2(o[j + 2][2 * i + e] * f, o[j + 3][2 * i + e] * f);
+          w.z = pack_bf16x2(o[j + 4][2 * i + e] * f, o[j + 5][2 * i + e] * f);
+          w.w = pack_bf16x2(o[j + 6][2 * i + e] * f, o[j + 7][2 * i + e] * f);
+          *reinterpret_cast<uint4*>(row + (D / 4) * c + (D / 8) * e + j) = w;
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+        *reinterpret_cast<uint32_t*>(row + 8 * j + 2 * c) = pack_bf16x2(o[j][2 * i] * f, o[j][2 * i + 1] * f);
+    }
+  }
+  __device__ __forceinline__ void put_f32(float* row, int i, float f, int lane) const {
+    const int c = lane & 3;
+    if constexpr (F8) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < kTiles; j += 4)
+          *reinterpret_cast<float4*>(row + (D / 4) * c + (D / 8) * e + j) =
+              make_float4(o[j][2 * i + e] * f, o[j + 1][2 * i + e] * f, o[j + 2][2 * i + e] * f, o[j + 3][2 * i + e] * f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+        *reinterpret_cast<float2*>(row + 8 * j + 2 * c) = make_float2(o[j][2 * i] * f, o[j][2 * i + 1] * f);
+    }
+  }
+
+  // Writes the warp's state to `buf` ([16][D + 4] floats: o unnormalised, m in log2 units, l).
+  __device__ __forceinline__ void store(float* buf, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    float l0, l1;
+    total_l(l0, l1);
     float* r0 = buf + g * (D + 4);
     float* r1 = r0 + 8 * (D + 4);
     if (c == 0) {

@@ -111,19 +111,20 @@ struct TreeShare {
   int workers, req;
 };
 
-// Block-wide: the shares of worker w[i] of most[i] in NL lines, request r
-// having units(tree_req(a, r), i) units in line i.  One pass over the requests
-// (kept in registers) when there are no more of them than threads, two
-// otherwise.  scratch: NL * (warps + 2) int64.
-template <class S, int Threads, int NL, class F>
-__device__ __forceinline__ void tree_shares(const TreeArgs& a, int64_t* scratch, const int (&w)[NL],
-                                            const int (&most)[NL], TreeShare (&sh)[NL], F&& units) {
+// Block-wide: the lengths U[i] of NL lines in which request r has
+// units(tree_req(a, r), i) units, and for each of NP probes the request that
+// holds a unit and the unit's offset in it.  probe(U, p, line, unit), called
+// once U is known, names probe p's line and unit (-1: none); the answers are
+// req[p] and off[p].  One pass over the requests (kept in registers) when there
+// are no more of them than threads, two otherwise.
+// scratch: max(NL * warps, 2 * NP) int64.
+template <int Threads, int NL, int NP, class F, class P>
+__device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, int64_t (&U)[NL], int (&req)[NP],
+                                          int64_t (&off)[NP], F&& units, P&& probe) {
   constexpr int kW = Threads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-#pragma unroll
-  for (int i = 0; i < NL; ++i) sh[i] = TreeShare{0, 0, 0, 0, 1, 0};
-  int64_t run[NL], n[NL], excl[NL];
-  auto scan = [&](int base, bool check) {   // units and exclusive offset of request base + tid; run: total so far
+  int64_t n[NL], excl[NL];
+  auto scan = [&](int base, bool check) {   // units and exclusive offset of request base + tid; U: total so far
     const int r = base + tid;
 #pragma unroll
     for (int i = 0; i < NL; ++i) n[i] = 0;
@@ -141,64 +142,75 @@ __device__ __forceinline__ void tree_shares(const TreeArgs& a, int64_t* scratch,
         const int64_t y = __shfl_up_sync(0xffffffffu, inc, x);
         if (lane >= x) inc += y;
       }
-      if (lane == 31) scratch[i * (kW + 2) + warp] = inc;
+      if (lane == 31) scratch[i * kW + warp] = inc;
       excl[i] = inc - n[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      int64_t total = run[i];
-      excl[i] += run[i];
+      int64_t total = U[i];
+      excl[i] += U[i];
 #pragma unroll
       for (int v = 0; v < kW; ++v) {
-        const int64_t x = scratch[i * (kW + 2) + v];
+        const int64_t x = scratch[i * kW + v];
         if (v < warp) excl[i] += x;
         total += x;
       }
-      run[i] = total;
+      U[i] = total;
     }
-  };
-  auto find = [&](int base) {   // leaves the request that holds the share's first unit, and the unit's offset in it
-#pragma unroll
-    for (int i = 0; i < NL; ++i)
-      if (n[i] > 0 && sh[i].u < sh[i].end && excl[i] <= sh[i].u && sh[i].u < excl[i] + n[i]) {
-        scratch[i * (kW + 2) + kW] = base + tid;
-        scratch[i * (kW + 2) + kW + 1] = sh[i].u - excl[i];
-      }
+    __syncthreads();
   };
 #pragma unroll
-  for (int i = 0; i < NL; ++i) run[i] = 0;
+  for (int i = 0; i < NL; ++i) U[i] = 0;
+  for (int base = 0; base < a.num_reqs; base += Threads) scan(base, true);
+  int line[NP];
+  int64_t unit[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    probe(U, p, line[p], unit[p]);
+    req[p] = 0;
+    off[p] = 0;
+  }
+  const bool kept = a.num_reqs <= Threads;
+  int64_t total[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    total[i] = U[i];
+    if (!kept) U[i] = 0;
+  }
   for (int base = 0; base < a.num_reqs; base += Threads) {
-    scan(base, true);
+    if (!kept) scan(base, false);
+    bool here[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      int64_t e = excl[0], m = n[0];
+#pragma unroll
+      for (int i = 1; i < NL; ++i)
+        if (line[p] == i) { e = excl[i]; m = n[i]; }
+      here[p] = unit[p] >= 0 && e <= unit[p] && unit[p] < e + m;
+      if (here[p]) {
+        scratch[2 * p] = base + tid;
+        scratch[2 * p + 1] = unit[p] - e;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      // (the chunk that holds the probe's unit: its total has passed it)
+      int64_t end = U[0];
+#pragma unroll
+      for (int i = 1; i < NL; ++i)
+        if (line[p] == i) end = U[i];
+      if (unit[p] >= 0 && unit[p] < end) {
+        req[p] = static_cast<int>(scratch[2 * p]);
+        off[p] = scratch[2 * p + 1];
+        unit[p] = -1;
+      }
+    }
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    sh[i].U = run[i];
-    sh[i].workers = S::workers(run[i], most[i]);
-    if (run[i] > 0 && w[i] < sh[i].workers) {
-      sh[i].u = S::begin(run[i], sh[i].workers, w[i]);
-      sh[i].end = S::begin(run[i], sh[i].workers, w[i] + 1);
-    }
-  }
-  if (a.num_reqs <= Threads) {
-    find(0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) run[i] = 0;
-    for (int base = 0; base < a.num_reqs; base += Threads) {
-      scan(base, false);
-      find(base);
-      __syncthreads();
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    sh[i].req = static_cast<int>(scratch[i * (kW + 2) + kW]);
-    sh[i].off = scratch[i * (kW + 2) + kW + 1];
-  }
-  __syncthreads();
+  for (int i = 0; i < NL; ++i) U[i] = total[i];
 }
 
 // Bits [x0, x0 + 32) of a token's tree mask (bits outside the row's words are

@@ -22,21 +22,53 @@ namespace pkv {
 namespace {
 
 constexpr int kRowsThreads = 32 * kRowWarps;
-// Rows kernel: a group has 16 query rows and one KV head, a unit is one block
-// (or one entry of a list); a CTA takes at least four blocks a warp.  A request without keys keeps one
-// (empty) unit a group: its rows are written too.
-using RowsShare = Share<4 * kRowWarps>;
+// Rows kernel: a group has 16 query rows and one KV head; a unit is one block
+// (or one entry of a list), and a group has kGroupUnits besides, for its start
+// and end.  A request without keys keeps one empty block: its rows are written
+// too.
+//
+// Two ways to share the line, chosen by the number of groups:
+//   many groups   a worker is one warp: it walks its share alone, nothing waits
+//                 for another warp, and a group has a few owners (kManyGroups
+//                 groups a CTA: eight at most);
+//   few groups    a worker is a CTA, whose four warps take a segment's blocks in
+//                 turn and merge their states in shared memory: a quarter of the
+//                 partials of long groups.
+constexpr int kGroupUnits = 2;
+using RowsShare = Share<4 * kRowWarps>;   // few groups: four blocks a warp at least
+using WarpShare = Share<4>;
 __device__ __forceinline__ int rows_tiles(const TreeReq& q, int group) {
   return static_cast<int>((static_cast<int64_t>(q.n) * group + kRowTile - 1) / kRowTile);
 }
 __device__ __forceinline__ int rows_blocks(const TreeReq& q) { return max(1, (q.ctx + kBlockSize - 1) / kBlockSize); }
 
-// A CTA walks its share of the line, segment by segment: blocks (list entries)
-// [b0, b0 + nb) of one group.  Its four warps take them in turn, each with its
-// own ring of copies and its own state, and merge at the segment's end.
-// Bound by the reads of K and V; the split in equal shares matters more than
-// the work per block (lists of 128 blocks for 256 groups: 62 us in clusters of
-// two CTAs, whose 512 CTAs leave a second, nearly empty wave; 4x us here).
+// V elements that are not finite, added to a stored row that sees them (they
+// were left out of the products); D / 32 dims a lane.
+template <int D, bool F8>
+__device__ __noinline__ void rows_add_odd(const TreeArgs& a, const int32_t* bt_row, int g, int prefix, int ctx, int b0,
+                                          int end_blk, const uint32_t* mrow, uint16_t* o, float* part, int lane) {
+  const int64_t Hkv = a.pool.num_kv_heads;
+  for (int b = max(b0, prefix / kBlockSize); b < end_blk; ++b) {
+    const uint32_t vis = tree_sees(prefix, ctx, mrow, a.mask_words, b * kBlockSize);
+    const int pb = __ldg(bt_row + b);
+    if (pb < 0 || pb >= a.pool.num_blocks) continue;
+    for (int k = 0; k < kBlockSize; ++k) {
+      if (!((vis >> k) & 1u)) continue;
+      for (int d = lane; d < D; d += 32) {
+        const float v = pool_v<D, F8>(a.pool, pb * Hkv + g, k, d);
+        if (fabsf(v) < CUDART_INF_F) continue;
+        if (part) part[d] += v;
+        else o[d] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(o[d]) + v, 0.f) & 0xffffu);
+      }
+    }
+  }
+}
+
+// A worker walks its share of the line, segment by segment: blocks (list
+// entries) [b0, b1) of one group.  Every warp has its own ring of copies and its
+// own state.  Bound by the reads of K and V; equal shares matter more than the
+// work per block (lists of 128 blocks for 256 groups took 62 us in clusters of
+// two CTAs: 512 CTAs leave a second, nearly empty wave).
 template <int D, bool F8, bool LIST>
 __global__ void __launch_bounds__(kRowsThreads, 3)
 rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
@@ -44,7 +76,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kBuf);
-  int64_t* scratch = reinterpret_cast<int64_t*>(ring + S::kBuf + kRowWarps * S::kStages * 8);   // kRowWarps + 2
+  __shared__ int64_t scratch[2 * kRowWarps];
   __shared__ int s_flags[2];
   volatile int* s_abort = &s_flags[0];
   int* s_odd = &s_flags[1];
@@ -52,36 +84,69 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   const int G = a.group, Hkv = a.pool.num_kv_heads;
   const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
   griddep_launch();   // the merge may take its place and wait
-  if (tid == 0) a.cuts[blockIdx.x].count = 0;
+  if (tid < kRowWarps) a.cuts[blockIdx.x * kRowWarps + tid].count = 0;
   if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
   if (tid == 0) {
     for (int i = 0; i < kRowWarps * S::kStages; ++i) mbar_init(&bars[i], 1);
     s_flags[0] = s_flags[1] = 0;
     fence_mbar_init();
   }
-  auto units = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv * rows_blocks(q); };
   const int rtiles = (G + kRowTile - 1) / kRowTile;   // LIST: row tiles of a token's group
+  auto groups = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
+  auto units = [&](const TreeReq& q) { return groups(q) * (rows_blocks(q) + kGroupUnits); };
+  // The shares: of this warp if there are many groups, of the CTA otherwise.
+  const int warp_id = static_cast<int>(blockIdx.x) * kRowWarps + warp, many_from = a.ctas / 2;
   TreeShare sh;
+  bool solo;
   if constexpr (LIST) {
     // Every token of the requests has top_k units a group.
     const int tokens = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
-    sh.U = static_cast<int64_t>(tokens) * Hkv * rtiles * a.top_k;
-    sh.workers = RowsShare::workers(sh.U, a.ctas);
-    sh.u = sh.end = 0;
-    if (sh.U > 0 && static_cast<int>(blockIdx.x) < sh.workers) {
-      sh.u = RowsShare::begin(sh.U, sh.workers, blockIdx.x);
-      sh.end = RowsShare::begin(sh.U, sh.workers, blockIdx.x + 1);
+    const int64_t n = static_cast<int64_t>(tokens) * Hkv * rtiles;
+    sh = TreeShare{n * (a.top_k + kGroupUnits), 0, 0, 0, 1, 0};
+    solo = n >= many_from;
+    sh.workers = solo ? WarpShare::workers(sh.U, a.ctas * kRowWarps) : RowsShare::workers(sh.U, a.ctas);
+    const int w = solo ? warp_id : static_cast<int>(blockIdx.x);
+    if (sh.U > 0 && w < sh.workers) {
+      sh.u = RowsShare::begin(sh.U, sh.workers, w);
+      sh.end = RowsShare::begin(sh.U, sh.workers, w + 1);
     }
   } else {
-    const int worker[1] = {static_cast<int>(blockIdx.x)}, most[1] = {a.ctas};
-    TreeShare shares[1];
-    tree_shares<RowsShare, kRowsThreads, 1>(a, scratch, worker, most, shares,
-                                            [&](const TreeReq& q, int) { return units(q); });
-    sh = shares[0];
+    // Line 0: units; line 1: groups (for their number alone).  Probe p: where warp p's share begins.
+    int64_t U[2], off[kRowWarps];
+    int reqs[kRowWarps];
+    auto share = [&](const int64_t (&len)[2], int p, TreeShare& t) {
+      const bool alone = len[1] >= many_from;
+      t.U = len[0];
+      t.workers = alone ? WarpShare::workers(len[0], a.ctas * kRowWarps) : RowsShare::workers(len[0], a.ctas);
+      const int w = alone ? static_cast<int>(blockIdx.x) * kRowWarps + p : static_cast<int>(blockIdx.x);
+      t.u = t.end = 0;
+      if (len[0] > 0 && w < t.workers) {
+        t.u = RowsShare::begin(len[0], t.workers, w);
+        t.end = RowsShare::begin(len[0], t.workers, w + 1);
+      }
+    };
+    tree_scan<kRowsThreads, 2, kRowWarps>(
+        a, scratch, U, reqs, off, [&](const TreeReq& q, int line) { return line == 0 ? units(q) : groups(q); },
+        [&](const int64_t (&len)[2], int p, int& line, int64_t& unit) {
+          TreeShare t;
+          share(len, p, t);
+          line = 0;
+          unit = t.u < t.end ? t.u : -1;
+        });
+    solo = U[1] >= many_from;
+    share(U, warp, sh);
+#pragma unroll
+    for (int p = 0; p < kRowWarps; ++p)
+      if (warp == p) {
+        sh.req = reqs[p];
+        sh.off = off[p];
+      }
   }
-  if (sh.u >= sh.end) return;
-  __syncthreads();
+  __syncthreads();   // barriers initialised
+  if (sh.u >= sh.end) return;   // a warp's (solo) or the CTA's
 
+  const int worker = solo ? warp_id : static_cast<int>(blockIdx.x);
+  const int wi = solo ? 0 : warp, wn = solo ? 1 : kRowWarps;   // this warp's place among those of the segment
   uint8_t* my_ring = ring + warp * S::kStages * S::kStage;
   uint64_t* my_bars = bars + warp * S::kStages;
   const uint32_t my_addr = smem_u32(my_ring);
@@ -91,12 +156,12 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   TreeReq rq{0, 0, 0, 0, false};
   if constexpr (!LIST) rq = tree_req(a, req);
   while (sh.u < sh.end) {
-    int kblk, b0, g, row0, nrows, pos = 0;   // units of the group, its first unit here, its rows
+    int kblk, x, g, row0, nrows, pos = 0;   // blocks of the group, its first unit here, its rows
     const int32_t* list = nullptr;
     if constexpr (LIST) {
       kblk = a.top_k;
-      const int64_t grp = sh.u / kblk;
-      b0 = static_cast<int>(sh.u - grp * kblk);
+      const int64_t grp = sh.u / (kblk + kGroupUnits);
+      x = static_cast<int>(sh.u - grp * (kblk + kGroupUnits));
       const int64_t th = grp / rtiles;
       row0 = static_cast<int>(grp - th * rtiles) * kRowTile;
       g = static_cast<int>(th % Hkv);
@@ -112,18 +177,21 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
         rq = tree_req(a, req);
       }
       kblk = rows_blocks(rq);
-      const int grp = static_cast<int>(sh.off / kblk);
-      b0 = static_cast<int>(sh.off - static_cast<int64_t>(grp) * kblk);
+      const int glen = kblk + kGroupUnits;
+      const int grp = static_cast<int>(sh.off / glen);
+      x = static_cast<int>(sh.off - static_cast<int64_t>(grp) * glen);
       const int ntile = rows_tiles(rq, G);
       g = grp / ntile;
       row0 = (grp - g * ntile) * kRowTile;
       nrows = min(kRowTile, rq.n * G - row0);
     }
-    const int nb = static_cast<int>(min(static_cast<int64_t>(kblk - b0), sh.end - sh.u));
-    if (LIST && req < 0) {   // a token that belongs to no request: its rows are left alone
-      sh.u += nb;
-      continue;
-    }
+    const int len = static_cast<int>(min(static_cast<int64_t>(kblk + kGroupUnits - x), sh.end - sh.u));
+    const int64_t gbegin = sh.u - x;
+    sh.u += len;
+    sh.off += len;
+    const int b0 = x, b1 = min(x + len, kblk);
+    // The group's fixed units only, or a token that belongs to no request (its rows are left alone).
+    if (b0 >= b1 || (LIST && req < 0)) continue;
     // Rows g' and g' + 8 of this thread.
     const int ra = lane >> 2, rb = ra + 8;
     auto q_row = [&](int rr) -> const uint16_t* {
@@ -135,16 +203,16 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
     auto mask_row = [&](int rr) {
       return a.mask + static_cast<int64_t>(rq.t0 + (row0 + min(rr, nrows - 1)) / G) * a.mask_words;
     };
-    const int end_blk = LIST ? b0 + nb : min(b0 + nb, (rq.ctx + kBlockSize - 1) / kBlockSize);
+    const int end_blk = LIST ? b1 : min(b1, (rq.ctx + kBlockSize - 1) / kBlockSize);
     const int live = max(0, end_blk - b0);
-    const int nb_w = live > warp ? (live - warp + kRowWarps - 1) / kRowWarps : 0;
+    const int nb_w = live > wi ? (live - wi + wn - 1) / wn : 0;
     const int32_t* bt_row = a.block_tables + static_cast<int64_t>(req) * a.max_blocks;
     // Lane l: the pool block (-1: none) of the warp's iteration base + l, and the block's index in the request.
     auto load_ids = [&](int base, int& blk) -> int {
       const int i = base + lane;
       blk = -1;
       if (i >= nb_w) return -1;
-      blk = b0 + warp + kRowWarps * i;
+      blk = b0 + wi + wn * i;
       if constexpr (LIST) {
         blk = __ldg(list + blk);
         if (blk < 0 || pos < 0 || blk > (pos >> 4)) return -1;   // padding, or a block that the token does not see
@@ -201,7 +269,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
           else
             rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
         } else {
-          const int key0 = (b0 + warp + kRowWarps * i) * kBlockSize;
+          const int key0 = (b0 + wi + wn * i) * kBlockSize;
           if (key0 + kBlockSize <= rq.prefix)
             rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
           else
@@ -217,94 +285,117 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
       }
     }
     if (!ok) {
-      // Gave up: let the copies in flight land, then leave together.
+      // Gave up: let the copies in flight land, then leave.
       if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
       *s_abort = 1;
       for (int j = max(0, issued - S::kStages); j < issued; ++j)
         (void)mbar_wait(&my_bars[(cnt + j) % S::kStages], ((cnt + j) / S::kStages) & 1, nullptr, a.wait_ns);
+      if (solo) return;
     }
     cnt += nb_w;
-    if (!LIST && rt.odd) *s_odd = 1;
-    __syncthreads();   // every warp's ring has drained
-    if (*s_abort) return;
-    // Merge the warps' states: [warp][16][D + 4] floats over the ring.
-    float* mbuf = reinterpret_cast<float*>(ring);
-    rt.store(mbuf + warp * kRowTile * S::kMergeRow, lane);
-    __syncthreads();
-    constexpr int kDims = D / 8;   // dims of a thread's part of a row
-    const int rr = tid >> 3, d0 = (tid & 7) * kDims;
-    if (rr < nrows) {
-      float M = -CUDART_INF_F, L = 0.f, acc[kDims];
+    const bool whole = b0 == 0 && b1 == kblk;
+    const int64_t slot = (2 * static_cast<int64_t>(worker) + (b0 == 0 ? 1 : 0)) * kRowTile;
+    auto out_row = [&](int rr) {   // row index of O and LSE
+      const int f = row0 + rr;
+      return static_cast<int64_t>(rq.t0 + f / G) * a.num_q_heads + g * G + f % G;
+    };
+    if (solo) {
+      float l0, l1;
+      rt.total_l(l0, l1);
 #pragma unroll
-      for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
-#pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
-        const float* src = mbuf + (w * kRowTile + rr) * S::kMergeRow;
-        if (src[D + 1] == 0.f) continue;   // the warp saw no key of this row (a NaN score leaves m, not l, as it was)
-        const float f = fast_exp2(src[D] - M);
-        L = fmaf(f, src[D + 1], L);
-#pragma unroll
-        for (int d = 0; d < kDims; ++d) acc[d] = fmaf(f, src[d0 + d], acc[d]);
-      }
-      const float inv = L == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / L;
-#pragma unroll
-      for (int d = 0; d < kDims; ++d) acc[d] *= inv;
-      const float lse2 = L == 0.f ? -CUDART_INF_F : M + fast_log2(L);
-      const int f = row0 + rr, t = rq.t0 + f / G, h = g * G + f % G;
-      if (!LIST && *s_odd) {
-        // V elements that are not finite, for the rows that see them.
-        const uint32_t* mr = a.mask + static_cast<int64_t>(t) * a.mask_words;
-        for (int b = max(b0, rq.prefix / kBlockSize); b < end_blk; ++b) {
-          const uint32_t vis = tree_sees(rq.prefix, rq.ctx, mr, a.mask_words, b * kBlockSize);
-          const int pb = __ldg(bt_row + b);
-          if (pb < 0 || pb >= a.pool.num_blocks) continue;
-          for (int k = 0; k < kBlockSize; ++k) {
-            if (!((vis >> k) & 1u)) continue;
-            for (int d = 0; d < kDims; ++d) {
-              const float v = pool_v<D, F8>(a.pool, static_cast<int64_t>(pb) * Hkv + g, k, d0 + d);
-              if (!(fabsf(v) < CUDART_INF_F)) acc[d] += v;
-            }
+      for (int i = 0; i < 2; ++i) {
+        const int rr = i ? rb : ra;
+        const float L = i ? l1 : l0;
+        const float f = L == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / L;
+        const float lse2 = L == 0.f ? -CUDART_INF_F : rt.m[i] + fast_log2(L);
+        if (rr < nrows) {
+          if (whole) {
+            const int64_t at = out_row(rr);
+            rt.put_bf16(static_cast<uint16_t*>(a.o) + at * D, i, f, lane);
+            if ((lane & 3) == 0 && a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
+          } else {
+            rt.put_f32(a.part_o + (slot + rr) * D, i, f, lane);
+            if ((lane & 3) == 0) a.part_lse[slot + rr] = lse2;
           }
         }
       }
-      if (b0 == 0 && nb == kblk) {   // the whole group: the final result
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
-                                              (static_cast<int64_t>(t) * a.num_q_heads + h) * D + d0);
-#pragma unroll
-        for (int d = 0; d < kDims; d += 8)
-          dst[d / 8] = make_uint4(pack_bf16x2(acc[d], acc[d + 1]), pack_bf16x2(acc[d + 2], acc[d + 3]),
-                                  pack_bf16x2(acc[d + 4], acc[d + 5]), pack_bf16x2(acc[d + 6], acc[d + 7]));
-        if (d0 == 0 && a.lse)
-          a.lse[static_cast<int64_t>(t) * a.num_q_heads + h] = lse2 * 0.69314718055994530942f;
-      } else {
-        const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (b0 == 0 ? 1 : 0)) * kRowTile + rr;
-        float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + d0);
-#pragma unroll
-        for (int d = 0; d < kDims; d += 4) dst[d / 4] = make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
-        if (d0 == 0) a.part_lse[slot] = lse2;
+      if (!LIST && __any_sync(0xffffffffu, rt.odd)) {
+        __syncwarp();
+        for (int rr = 0; rr < nrows; ++rr)
+          rows_add_odd<D, F8>(a, bt_row, g, rq.prefix, rq.ctx, b0, end_blk, mask_row(rr),
+                              static_cast<uint16_t*>(a.o) + out_row(rr) * D,
+                              whole ? nullptr : a.part_o + (slot + rr) * D, lane);
       }
+    } else {
+      if (!LIST && rt.odd) *s_odd = 1;
+      __syncthreads();   // every warp's ring has drained
+      if (*s_abort) return;
+      // Merge the warps' states: [warp][16][D + 4] floats over the ring.
+      float* mbuf = reinterpret_cast<float*>(ring);
+      rt.store(mbuf + warp * kRowTile * S::kMergeRow, lane);
+      __syncthreads();
+      constexpr int kDims = D / 8;   // dims of a thread's part of a row
+      const int rr = tid >> 3, d0 = (tid & 7) * kDims;
+      if (rr < nrows) {
+        float M = -CUDART_INF_F, L = 0.f, acc[kDims];
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+          const float* src = mbuf + (w * kRowTile + rr) * S::kMergeRow;
+          if (src[D + 1] == 0.f) continue;   // the warp saw no key of this row (a NaN score leaves m, not l, as it was)
+          const float f = fast_exp2(src[D] - M);
+          L = fmaf(f, src[D + 1], L);
+#pragma unroll
+          for (int d = 0; d < kDims; ++d) acc[d] = fmaf(f, src[d0 + d], acc[d]);
+        }
+        const float inv = L == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / L;
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) acc[d] *= inv;
+        const float lse2 = L == 0.f ? -CUDART_INF_F : M + fast_log2(L);
+        if (whole) {
+          const int64_t at = out_row(rr);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at * D + d0);
+#pragma unroll
+          for (int d = 0; d < kDims; d += 8)
+            dst[d / 8] = make_uint4(pack_bf16x2(acc[d], acc[d + 1]), pack_bf16x2(acc[d + 2], acc[d + 3]),
+                                    pack_bf16x2(acc[d + 4], acc[d + 5]), pack_bf16x2(acc[d + 6], acc[d + 7]));
+          if (d0 == 0 && a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + (slot + rr) * D + d0);
+#pragma unroll
+          for (int d = 0; d < kDims; d += 4) dst[d / 4] = make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
+          if (d0 == 0) a.part_lse[slot + rr] = lse2;
+        }
+      }
+      __syncthreads();   // the ring and the flags are free again, the rows stored
+      if (!LIST && *s_odd) {
+        for (int r2 = warp; r2 < nrows; r2 += kRowWarps)
+          rows_add_odd<D, F8>(a, bt_row, g, rq.prefix, rq.ctx, b0, end_blk, mask_row(r2),
+                              static_cast<uint16_t*>(a.o) + out_row(r2) * D,
+                              whole ? nullptr : a.part_o + (slot + r2) * D, lane);
+        __syncthreads();
+        if (tid == 0) *s_odd = 0;
+      }
+      fence_proxy_async_smem();
+      __syncthreads();
     }
-    __syncthreads();   // the ring and the flags are free again
-    if (tid == 0) *s_odd = 0;
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (b0 == 0 && nb < kblk && tid == 0) {   // the group's first part: its other owners follow
-      const int c1 = RowsShare::owner(sh.U, sh.workers, sh.u + kblk - 1);
-      TreeCut& cut = a.cuts[blockIdx.x];
-      cut.first = 2 * blockIdx.x + 1;
-      cut.next = 2 * (blockIdx.x + 1);
+    if (b0 == 0 && b1 < kblk && lane == 0 && (solo || warp == 0)) {   // the group's first part: its other owners follow
+      // (the last block names the last owner; those between each have a block, a share being longer than the fixed units)
+      const int c1 = RowsShare::owner(sh.U, sh.workers, gbegin + kblk - 1);
+      TreeCut& cut = a.cuts[worker];
+      cut.first = 2 * worker + 1;
+      cut.next = 2 * (worker + 1);
       cut.stride = 2;
       cut.tok_a = rq.t0;
       cut.rows_a = nrows;
       cut.tok_b = cut.rows_b = 0;
       cut.f0 = row0;
       cut.g = g;
-      cut.count = c1 - static_cast<int>(blockIdx.x) + 1;
+      cut.count = c1 - worker + 1;
     }
-    sh.off += nb;
-    sh.u += nb;
   }
 }
 
@@ -457,7 +548,7 @@ TreeForm tree_form(bool tensor, int num_sms) {
   TreeForm f;
   f.tensor = tensor;
   f.ctas = tensor ? num_sms : 3 * num_sms;
-  f.cuts = tensor ? 2 * f.ctas : f.ctas;             // the tensor-core form has two lines of work
+  f.cuts = tensor ? 2 * f.ctas : kRowWarps * f.ctas;   // two lines of work, or a share a warp
   f.slot_rows = tensor ? 256 : kRowTile;
   f.slots = 2 * f.cuts;
   return f;

@@ -253,13 +253,34 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
   {
     // The CTA's shares (scratch in the query buffer, before its first copy).
     TreeShare (&sh)[2] = walk.sh;
-    const int worker[2] = {static_cast<int>(blockIdx.x >> 1), static_cast<int>(blockIdx.x)};
-    const int most[2] = {a.ctas / 2, a.ctas};
-    tree_shares<TcShare, kThreads, 2>(a, reinterpret_cast<int64_t*>(smem), worker, most, sh,
-                                      [&](const TreeReq& q, int line) {
-                                        return line == 0 ? quad_units(q, a.tile_tokens, Hkv)
-                                                         : rest_units(q, a.tile_tokens, Hkv);
-                                      });
+    int64_t U[2], off[2];
+    int reqs[2];
+    auto share = [&](const int64_t (&len)[2], int line) {   // line 0: of this CTA's pair, line 1: of the CTA
+      TreeShare& t = sh[line];
+      t.U = len[line];
+      t.workers = TcShare::workers(t.U, line ? a.ctas : a.ctas / 2);
+      const int w = line ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x >> 1);
+      t.u = t.end = 0;
+      if (t.U > 0 && w < t.workers) {
+        t.u = TcShare::begin(t.U, t.workers, w);
+        t.end = TcShare::begin(t.U, t.workers, w + 1);
+      }
+    };
+    tree_scan<kThreads, 2, 2>(
+        a, reinterpret_cast<int64_t*>(smem), U, reqs, off,
+        [&](const TreeReq& q, int line) {
+          return line == 0 ? quad_units(q, a.tile_tokens, Hkv) : rest_units(q, a.tile_tokens, Hkv);
+        },
+        [&](const int64_t (&len)[2], int p, int& line, int64_t& unit) {
+          share(len, p);
+          line = p;
+          unit = sh[p].u < sh[p].end ? sh[p].u : -1;
+        });
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sh[i].req = reqs[i];
+      sh[i].off = off[i];
+    }
     if (sh[0].u >= sh[0].end && sh[1].u >= sh[1].end) return;   // block-uniform
   }
   if (threadIdx.x == 0) {
