@@ -388,12 +388,16 @@ int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, i
  * inputs alone, not on the order of any sum.
  * Rows of tokens that belong to no request are left as they are.  A block
  * without a valid pool block is flagged and not selected; a position outside
- * the table is flagged and selects nothing.  max_blocks <= 393216 (6.29 M tokens).
+ * the table is flagged and selects nothing.  num_kv_heads <= 256.  workspace:
+ * pkv_select_blocks_workspace_size() bytes for the same sizes (the scores of up
+ * to 64 MB of tokens at a time), 256-byte aligned, used by one call at a time as
+ * for pkv_tree_attn.
  */
+int pkv_select_blocks_workspace_size(pkv_pool* pool, int max_blocks, int num_tokens, size_t* bytes);
 int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
                       const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs,
                       int num_tokens, const int8_t* codes, const int8_t* exps, int top_k, int sinks, int recent,
-                      int32_t* selected, void* stream);
+                      int32_t* selected, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Attention of each query token over the keys j <= p of its selected blocks

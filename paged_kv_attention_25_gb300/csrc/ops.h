@@ -7,6 +7,26 @@ namespace pkv {
 
 struct TreeArgs;
 
+// Launches a kernel that may be scheduled before the one ahead of it in the
+// stream ends: it begins with griddep_wait().
+#ifdef __CUDACC__
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // The two forms of the tree attention: warp-level MMA on 16 query rows, or
 // tcgen05 on tiles of 128.
 struct TreeForm {
@@ -39,10 +59,15 @@ struct SparseArgs {
   int32_t* sel;      // [tokens][kv heads][top_k]
   int top_k, sinks, recent;
   int num_sms;
+  // Selection: the keys [tokens of a part][kv heads][max_blocks] (workspace) of
+  // tokens [tok_first, tok_first + tok_count), tok_most tokens a part.
+  uint32_t* keys;
+  int tok_first, tok_count, tok_most;
 };
 int launch_summarize(const SparseArgs& a, void* stream);
-// Blocks of a table row that the selection can take (its scores stay in shared memory).
-int select_max_blocks();
+// KV heads that the selection can take (their queries stay in shared memory), and the tokens of a part.
+constexpr int kSelectMaxHeads = 256;
+int select_part(int num_tokens, int max_blocks, int num_kv_heads);
 int launch_select(const SparseArgs& a, void* stream);
 
 // pkv_fork.

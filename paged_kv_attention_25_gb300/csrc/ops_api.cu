@@ -99,6 +99,11 @@ const CUtensorMap* rows_map(const pkv_pool* pool, bool v) {
   return pool->elem_bytes == 1 ? (v ? &pool->dmap_v : &pool->dmap_k) : (v ? &pool->tmap_v : &pool->tmap_k);
 }
 
+size_t select_ws(const pkv_pool* pool, int max_blocks, int num_tokens) {
+  return align256(static_cast<size_t>(select_part(num_tokens, max_blocks, pool->num_kv_heads)) * max_blocks *
+                  pool->num_kv_heads * sizeof(uint32_t));
+}
+
 int check_summary(const pkv_pool* pool, const void* codes, const void* exps) {
   (void)pool;
   if (!codes || !exps) return fail(PKV_EINVAL, "NULL summary arrays");
@@ -211,22 +216,32 @@ int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, i
   return PKV_OK;
 }
 
+int pkv_select_blocks_workspace_size(pkv_pool* pool, int max_blocks, int num_tokens, size_t* bytes) {
+  if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
+  const int rc = check_tables(max_blocks, 1, num_tokens);
+  if (rc) return rc;
+  *bytes = num_tokens == 0 ? 256 : select_ws(pool, max_blocks, num_tokens);
+  return PKV_OK;
+}
+
 int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
                       const int32_t* block_tables, int max_blocks, const int32_t* cu_q_lens, int num_reqs,
                       int num_tokens, const int8_t* codes, const int8_t* exps, int top_k, int sinks, int recent,
-                      int32_t* selected, void* stream) {
+                      int32_t* selected, void* workspace, size_t workspace_bytes, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
   int rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
   if (top_k < 1 || sinks < 0 || recent < 0) return fail(PKV_EINVAL, "need top_k >= 1, sinks >= 0, recent >= 0");
   if (num_tokens == 0) return PKV_OK;
   if ((rc = check_heads(pool, num_q_heads))) return rc;
+  if (pool->num_kv_heads > kSelectMaxHeads)
+    return fail(PKV_EUNSUPPORTED, "num_kv_heads above " + std::to_string(kSelectMaxHeads));
   if (!q || !q_positions || !block_tables || !cu_q_lens || !selected) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q)) return fail(PKV_EINVAL, "q must be 16-byte aligned");
   if ((rc = check_summary(pool, codes, exps))) return rc;
-  if (max_blocks > select_max_blocks())
-    return fail(PKV_EUNSUPPORTED, "max_blocks above " + std::to_string(select_max_blocks()));
-  if (static_cast<int64_t>(num_tokens) * pool->num_kv_heads * 8 >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many rows");
+  if ((rc = check_workspace(workspace, workspace_bytes, select_ws(pool, max_blocks, num_tokens),
+                            "pkv_select_blocks_workspace_size()")))
+    return rc;
   DeviceGuard guard(pool->device);
   SparseArgs a{};
   a.pool = pool->view();
@@ -246,6 +261,8 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
   a.sinks = std::min(sinks, max_blocks);
   a.recent = std::min(recent, max_blocks);
   a.num_sms = pool->num_sms;
+  a.keys = static_cast<uint32_t*>(workspace);
+  a.tok_most = select_part(num_tokens, max_blocks, pool->num_kv_heads);
   rc = timed_launch(pool, 0, stream, [&] { return launch_select(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block selection launch");
   return PKV_OK;

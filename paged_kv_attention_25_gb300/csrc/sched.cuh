@@ -111,29 +111,23 @@ struct TreeShare {
   int workers, req;
 };
 
-// Block-wide: the lengths U[i] of NL lines in which request r has
-// units(tree_req(a, r), i) units, and for each of NP probes the request that
-// holds a unit and the unit's offset in it.  probe(U, p, line, unit), called
-// once U is known, names probe p's line and unit (-1: none); the answers are
-// req[p] and off[p].  One pass over the requests (kept in registers) when there
-// are no more of them than threads, two otherwise.
-// scratch: max(NL * warps, 2 * NP) int64.
+// Block-wide: the lengths U[i] of NL lines in which item r of `items` has n[i]
+// units, units(r, n) filling n, and for each of NP probes the item that holds a
+// unit and the unit's offset in it.  probe(U, p, line, unit), called once U is
+// known, names probe p's line and unit (-1: none); the answers are req[p] and
+// off[p].  One pass over the items (kept in registers) when there are no more of
+// them than threads, two otherwise.  scratch: max(NL * warps, 2 * NP) int64.
 template <int Threads, int NL, int NP, class F, class P>
-__device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, int64_t (&U)[NL], int (&req)[NP],
+__device__ __forceinline__ void line_scan(int items, int64_t* scratch, int64_t (&U)[NL], int (&req)[NP],
                                           int64_t (&off)[NP], F&& units, P&& probe) {
   constexpr int kW = Threads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int64_t n[NL], excl[NL];
-  auto scan = [&](int base, bool check) {   // units and exclusive offset of request base + tid; U: total so far
+  auto scan = [&](int base) {   // units and exclusive offset of item base + tid; U: total so far
     const int r = base + tid;
 #pragma unroll
     for (int i = 0; i < NL; ++i) n[i] = 0;
-    if (r < a.num_reqs) {
-      const TreeReq q = tree_req(a, r);
-#pragma unroll
-      for (int i = 0; i < NL; ++i) n[i] = units(q, i);
-      if (check && q.bad && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
-    }
+    if (r < items) units(r, n);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       int64_t inc = n[i];
@@ -162,7 +156,7 @@ __device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, i
   };
 #pragma unroll
   for (int i = 0; i < NL; ++i) U[i] = 0;
-  for (int base = 0; base < a.num_reqs; base += Threads) scan(base, true);
+  for (int base = 0; base < items; base += Threads) scan(base);
   int line[NP];
   int64_t unit[NP];
 #pragma unroll
@@ -171,15 +165,15 @@ __device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, i
     req[p] = 0;
     off[p] = 0;
   }
-  const bool kept = a.num_reqs <= Threads;
+  const bool kept = items <= Threads;
   int64_t total[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     total[i] = U[i];
     if (!kept) U[i] = 0;
   }
-  for (int base = 0; base < a.num_reqs; base += Threads) {
-    if (!kept) scan(base, false);
+  for (int base = 0; base < items; base += Threads) {
+    if (!kept) scan(base);
     bool here[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -211,6 +205,21 @@ __device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, i
   }
 #pragma unroll
   for (int i = 0; i < NL; ++i) U[i] = total[i];
+}
+
+// The lines of a tree-attention call: request r has units(tree_req(a, r), i) units in line i.
+template <int Threads, int NL, int NP, class F, class P>
+__device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, int64_t (&U)[NL], int (&req)[NP],
+                                          int64_t (&off)[NP], F&& units, P&& probe) {
+  line_scan<Threads, NL, NP>(
+      a.num_reqs, scratch, U, req, off,
+      [&](int r, int64_t (&n)[NL]) {
+        const TreeReq q = tree_req(a, r);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) n[i] = units(q, i);
+        if (q.bad && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
+      },
+      probe);
 }
 
 // Bits [x0, x0 + 32) of a token's tree mask (bits outside the row's words are

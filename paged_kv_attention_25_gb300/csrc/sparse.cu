@@ -15,17 +15,16 @@
 // each of at most 128 channels, codes of at most 127: below 2^30), rounded to fp32 once and scaled by
 // 2^e exactly: the order of the blocks, ties included, does not depend on the
 // order of any sum.
-#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "ops.h"
 #include "ptx.cuh"
 #include "sched.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace pkv {
 namespace {
@@ -160,169 +159,319 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 256;
-constexpr int kSelMost = 49152;   // scores a CTA keeps (192 KB)
+// Two kernels.  score_kernel reads the bounds once, all heads of a block
+// together, in equal shares of the line (token, block), and leaves a 32-bit key
+// for every (token, block, head); pick_kernel finds each (token, head)'s
+// threshold and writes its list.  (One kernel a (token, head), clusters or not,
+// left the memory idle while it looked for thresholds and took as long as the
+// longest context on the fullest SM: 35 us against 2x for 32 requests of 9 to 32
+// thousand tokens.)
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreStages = 3;    // warp iterations of bounds in flight
+constexpr int kTokenUnits = 8;     // blocks that a token's start costs
+using ScoreShare = Share<16>;
 
-// Order-preserving key of a score: larger score, larger key.  0 is below every score.
+// Order-preserving key of a score: larger score, larger key.  0 (no block) is
+// below every score, 0xffffffff (taken in any case) above.
 __device__ __forceinline__ uint32_t key_of(float f) {
   f += 0.f;   // -0 counts as 0
   const uint32_t u = __float_as_uint(f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// One cluster of CS CTAs per (token, KV head); CTA i scores the i-th part of
-// the token's blocks into shared memory, then the cluster finds the top_k-th
-// key with four 8-bit radix passes and writes the chosen blocks in order.
-template <int D, int CS>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SparseArgs a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ __align__(16) int16_t s_q[2 * D];   // P, then N
-  __shared__ uint32_t s_hist[4][256];  // one histogram a pass
-  __shared__ float s_red[8];
-  __shared__ int s_cnt[2];             // keys above the threshold, equal to it
-  __shared__ int s_scan[2][8];
-  __shared__ int s_pick[2];            // radix pass: bin, keys above it
+// A warp's view of one iteration: eight groups of four lanes; group i takes
+// head 8 o + i of one block (more than 8 heads), or head i % Hkv of block i / Hkv
+// (up to 8 heads: 8 / Hkv blocks an iteration).  Lane s of a group takes the
+// 16-byte pieces s, s + 4, ... of the head's 2 D codes, and copies them itself
+// into its own places of the ring, so that it waits for nothing but its copies.
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const SparseArgs a) {
+  constexpr int kPieces = 2 * D / 64;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t scratch[kScoreWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hkv = a.pool.num_kv_heads, G = a.group;
-  const int rank = CS > 1 ? static_cast<int>(blockIdx.x % CS) : 0;
-  const int64_t th = blockIdx.x / CS;
-  const int g = static_cast<int>(th % Hkv), t = static_cast<int>(th / Hkv);
-  const int r = req_of_warp(a.cu_q_lens, a.num_reqs, t, lane);
-  if (r < 0) return;   // cluster-uniform
-  const int p = __ldg(a.positions + t);
-  int32_t* out = a.sel + th * a.top_k;
-  if (p < 0 || p >= a.max_blocks * kBlockSize) {
-    if (rank == 0) {
-      if (tid == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
-      for (int i = tid; i < a.top_k; i += kSelThreads) out[i] = -1;
-    }
-    return;
-  }
-  const int n = (p >> 4) + 1;
-  const int per = (n + CS - 1) / CS;
-  const int b0 = min(n, rank * per), b1 = min(n, b0 + per);
+  int16_t* s_q = reinterpret_cast<int16_t*>(smem);                       // [Hkv][P: D, N: D]
+  const uint32_t slot = smem_u32(smem) + Hkv * (4 * D) + tid * 16;       // ring: [stage][piece][thread] 16 bytes
+  griddep_wait();
+  griddep_launch();
 
-  // Whole-number queries: unit 2^f, the smallest with |q| <= most 2^f, most = floor(32767 / G).
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(t) * a.num_q_heads + g * G) * D;
-  float amax = 0.f;
-  for (int i = tid; i < G * D; i += kSelThreads) {
-    const float x = fabsf(bf16lo_to_f32(__ldg(q + i)));
-    if (x < CUDART_INF_F) amax = fmaxf(amax, x);   // values that are not finite count as 0
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
-  if (lane == 0) s_red[warp] = amax;
-  for (int i = tid; i < 4 * 256; i += kSelThreads) (&s_hist[0][0])[i] = 0;
-  if (tid < 2) s_cnt[tid] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) amax = fmaxf(amax, s_red[w]);
-  const float most = static_cast<float>(32767 / G);
-  // Tiny queries (below 2^-100) count as 0: the unit stays a normal number.
-  const bool none = !(amax >= 7.8886e-31f);
-  const int f = none ? 0 : exp_of(amax) - exp_of(most) + (mant_of(amax) <= mant_of(most) ? 0 : 1);
-  for (int d = tid; d < D; d += kSelThreads) {
-    int P = 0, N = 0;
-    for (int h = 0; h < G && !none; ++h) {
-      const float x = bf16lo_to_f32(__ldg(q + h * D + d));
-      // x 2^-f in two exact steps (2^-f alone may exceed the normal range)
-      const int i = fabsf(x) < CUDART_INF_F ? static_cast<int>(rintf(x * pow2f(-f / 2) * pow2f(-(f - f / 2)))) : 0;
-      if (i > 0) P += i; else N += i;
-    }
-    s_q[d] = static_cast<int16_t>(P);
-    s_q[D + d] = static_cast<int16_t>(N);
-  }
-  __syncthreads();
-  // Scores: four lanes a block, lane s of them the 16-byte pieces s, s + 4, ... of the 2 D codes.
-  constexpr int kPieces = 2 * D / 64;
-  const int sub = lane & 3;
-  int qq[kPieces][8];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-    for (int w = 0; w < 8; ++w) qq[i][w] = reinterpret_cast<const int*>(s_q)[(i * 4 + sub) * 8 + w];
-  const int32_t* bt_row = a.block_tables + static_cast<int64_t>(r) * a.max_blocks;
-  // Two iterations' codes in flight, their block ids one more ahead.
-  constexpr int kStep = kSelThreads / 4;
-  const int first = b0 + warp * 8 + (lane >> 2);
-  auto load_id = [&](int b) -> int { return b < b1 ? __ldg(bt_row + b) : -1; };
-  struct Codes { uint4 c[kPieces]; int e; };
-  auto load_codes = [&](int pb, Codes& k) {
-    k.e = 0;
-    if (pb >= 0 && pb < a.pool.num_blocks) {
-      const int64_t chunk = static_cast<int64_t>(pb) * Hkv + g;
-      const uint4* src = reinterpret_cast<const uint4*>(a.codes + chunk * 2 * D) + sub;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) k.c[i] = __ldg(src + i * 4);
-      k.e = __ldg(a.exps + chunk);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) k.c[i] = make_uint4(0, 0, 0, 0);
-    }
+  // The share: token t (of this launch's) has a unit for each block up to its position, and kTokenUnits.
+  const int end_tok = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
+  const int tokens = max(0, min(a.tok_count, end_tok - a.tok_first));
+  const int most = a.max_blocks * kBlockSize;
+  auto token_blocks = [&](int t) -> int {   // 0 for a position outside the table
+    const int p = __ldg(a.positions + t);
+    return p >= 0 && p < most ? (p >> 4) + 1 : 0;
   };
-  auto score = [&](int b, int pb, const Codes& k) {
-    int s = 0;
+  int64_t U[1], off[1];
+  int at[1];
+  int64_t u = 0, end = 0;
+  line_scan<kScoreThreads, 1, 1>(
+      tokens, scratch, U, at, off,
+      [&](int i, int64_t (&n)[1]) {
+        const int b = token_blocks(a.tok_first + i);
+        n[0] = b + kTokenUnits;
+        if (b == 0 && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
+      },
+      [&](const int64_t (&len)[1], int, int& line, int64_t& unit) {
+        const int C = ScoreShare::workers(len[0], gridDim.x);
+        if (len[0] > 0 && static_cast<int>(blockIdx.x) < C) {
+          u = ScoreShare::begin(len[0], C, blockIdx.x);
+          end = ScoreShare::begin(len[0], C, blockIdx.x + 1);
+        }
+        line = 0;
+        unit = u < end ? u : -1;
+      });
+  if (u >= end) return;
+
+  const int grp = lane >> 2, sub = lane & 3;
+  const int bpw = Hkv >= 8 ? 1 : 8 / Hkv;               // blocks of a warp iteration
+  const int octets = Hkv > 8 ? (Hkv + 7) / 8 : 1;
+  const int my_blk = Hkv >= 8 ? 0 : grp / Hkv;
+  const bool lane_on = Hkv >= 8 || grp < bpw * Hkv;
+  const float mostq = static_cast<float>(32767 / G);
+  int tok = a.tok_first + at[0];
+  int64_t x = off[0];
+  for (; u < end; ++tok, x = 0) {
+    const int n = token_blocks(tok);
+    const int len = static_cast<int>(min(n + kTokenUnits - x, end - u));
+    const int b0 = static_cast<int>(x), b1 = static_cast<int>(min(x + len, static_cast<int64_t>(n)));
+    u += len;
+    if (b0 >= b1) continue;   // block-uniform
+    const int r = req_of_warp(a.cu_q_lens, a.num_reqs, tok, lane);
+    if (r < 0) continue;
+    const int32_t* bt_row = a.block_tables + static_cast<int64_t>(r) * a.max_blocks;
+    // Iteration k of this warp: octet k / per, blocks b0 + ((k % per) * warps + warp) * bpw ...
+    const int per = (b1 - b0 + kScoreWarps * bpw - 1) / (kScoreWarps * bpw);
+    const int iters = octets * per;
+    auto block_of = [&](int k) { return b0 + ((k % per) * kScoreWarps + warp) * bpw + my_blk; };
+    auto load_id = [&](int k) -> int {
+      if (k >= iters) return -1;
+      const int b = block_of(k);
+      return b < b1 ? __ldg(bt_row + b) : -1;
+    };
+    int ids[kScoreStages], ex[kScoreStages];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int w[4] = {static_cast<int>(k.c[i].x), static_cast<int>(k.c[i].y), static_cast<int>(k.c[i].z),
-                        static_cast<int>(k.c[i].w)};
+    for (int v = 0; v < kScoreStages; ++v) ids[v] = load_id(v);
+    int next = load_id(kScoreStages);
+    auto copy = [&](int st, int k, int pb, int& e) {
+      e = 0;
+      const int h = Hkv >= 8 ? (k / per) * 8 + grp : grp % Hkv;
+      if (pb >= 0 && pb < a.pool.num_blocks && lane_on && h < Hkv) {
+        const int64_t chunk = static_cast<int64_t>(pb) * Hkv + h;
+        const int8_t* src = a.codes + chunk * 2 * D + sub * 16;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        s = __dp2a_lo(qq[i][2 * x], w[x], s);
-        s = __dp2a_hi(qq[i][2 * x + 1], w[x], s);
+        for (int i = 0; i < kPieces; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                       ::"r"(slot + (st * kPieces + i) * (kScoreThreads * 16)), "l"(src + i * 64) : "memory");
+        if (sub == 0) e = __ldg(a.exps + chunk);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int v = 0; v < kScoreStages; ++v) copy(v, v, ids[v], ex[v]);
+
+    // Whole-number queries of every head, while the first copies are under way: unit 2^f, the smallest with
+    // |q| <= most 2^f, most = floor(32767 / G).  A warp a head, D / 32 channels a lane.
+    __syncthreads();   // the previous token's are no longer read
+    constexpr int kDPL = D / 32;
+    for (int h = warp; h < Hkv; h += kScoreWarps) {
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                          (static_cast<int64_t>(tok) * a.num_q_heads + h * G) * D + lane * kDPL;
+      auto channels = [&](int i, float (&v)[kDPL]) {   // head i of the group; values that are not finite count as 0
+        uint32_t w[2];
+        if constexpr (kDPL == 4) {
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(q + i * D));
+          w[0] = y.x; w[1] = y.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(q + i * D));
+        }
+#pragma unroll
+        for (int d = 0; d < kDPL; ++d) {
+          const float f = (d & 1) ? bf16hi_to_f32(w[d >> 1]) : bf16lo_to_f32(w[d >> 1]);
+          v[d] = fabsf(f) < CUDART_INF_F ? f : 0.f;
+        }
+      };
+      float amax = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < G; ++i) {
+        float v[kDPL];
+        channels(i, v);
+#pragma unroll
+        for (int d = 0; d < kDPL; ++d) amax = fmaxf(amax, fabsf(v[d]));
+      }
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
+      // Tiny queries (below 2^-100) count as 0: the unit stays a normal number.
+      const bool none = !(amax >= 7.8886090522101181e-31f);
+      const int f = none ? 0 : exp_of(amax) - exp_of(mostq) + (mant_of(amax) <= mant_of(mostq) ? 0 : 1);
+      // x 2^-f in two exact steps (2^-f alone may exceed the normal range)
+      const float f1 = none ? 0.f : pow2f(-f / 2), f2 = pow2f(-(f - f / 2));
+      int P[kDPL], N[kDPL];
+#pragma unroll
+      for (int d = 0; d < kDPL; ++d) P[d] = N[d] = 0;
+#pragma unroll 8
+      for (int i = 0; i < G; ++i) {
+        float v[kDPL];
+        channels(i, v);
+#pragma unroll
+        for (int d = 0; d < kDPL; ++d) {
+          const int w = static_cast<int>(rintf(v[d] * f1 * f2));
+          P[d] += max(w, 0);
+          N[d] += min(w, 0);
+        }
+      }
+      int16_t* dst = s_q + h * 2 * D + lane * kDPL;
+#pragma unroll
+      for (int d = 0; d < kDPL; ++d) {
+        dst[d] = static_cast<int16_t>(P[d]);
+        dst[D + d] = static_cast<int16_t>(N[d]);
       }
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if (sub == 0 && b < b1) {
-      const bool there = pb >= 0 && pb < a.pool.num_blocks;
-      if (!there) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
-      const bool forced = b < a.sinks || b >= n - a.recent;
-      keys[b - b0] = !there ? 0u : forced ? 0xffffffffu : key_of(__int2float_rn(s) * pow2f(max(-126, k.e)));
+    __syncthreads();
+
+    int qq[kPieces][8], octet = -1, h = 0;
+    uint32_t* out = a.keys + static_cast<int64_t>(tok - a.tok_first) * Hkv * a.max_blocks;
+    for (int k0 = 0; k0 < iters; k0 += kScoreStages) {
+#pragma unroll
+      for (int v = 0; v < kScoreStages; ++v) {
+        const int k = k0 + v;
+        if (k < iters) {
+          if (k / per != octet) {   // warp-uniform
+            octet = k / per;
+            h = Hkv >= 8 ? octet * 8 + grp : grp % Hkv;
+            const int* src = reinterpret_cast<const int*>(s_q + min(h, Hkv - 1) * 2 * D);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+              for (int w = 0; w < 8; ++w) qq[i][w] = src[(i * 4 + sub) * 8 + w];
+          }
+          asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
+          int s = 0;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(slot + (v * kPieces + i) * (kScoreThreads * 16)) : "memory");
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              s = __dp2a_lo(qq[i][2 * y], static_cast<int>(w[y]), s);
+              s = __dp2a_hi(qq[i][2 * y + 1], static_cast<int>(w[y]), s);
+            }
+          }
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          const int b = block_of(k);
+          if (sub == 0 && b < b1 && lane_on && h < Hkv) {
+            uint32_t key = 0u;
+            if (ids[v] < 0 || ids[v] >= a.pool.num_blocks) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
+            else if (b < a.sinks || b >= n - a.recent) key = 0xffffffffu;
+            else key = key_of(__int2float_rn(s) * pow2f(max(-126, ex[v])));
+            out[static_cast<int64_t>(h) * a.max_blocks + b] = key;
+          }
+          ids[v] = next;
+          copy(v, k + kScoreStages, ids[v], ex[v]);
+          next = load_id(k + kScoreStages + 1);
+        }
+      }
     }
-  };
-  {
-    const int iters = b1 > b0 + warp * 8 ? (b1 - b0 - warp * 8 + kStep - 1) / kStep : 0;   // warp-uniform
-    int id0 = load_id(first), id1 = load_id(first + kStep), id2 = load_id(first + 2 * kStep);
-    Codes k0, k1;
-    load_codes(id0, k0);
-    for (int i = 0; i < iters; i += 2) {
-      load_codes(id1, k1);
-      const int id3 = load_id(first + (i + 3) * kStep);
-      score(first + i * kStep, id0, k0);
-      id0 = id2;
-      load_codes(id0, k0);
-      id2 = load_id(first + (i + 4) * kStep);
-      if (i + 1 < iters) score(first + (i + 1) * kStep, id1, k1);
-      id1 = id3;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+}
+
+// One CTA per (token, KV head).  Keys of up to kPickKeys blocks stay in shared
+// memory, more are read again from L2.  The radix passes run on key - lo, shifted
+// until the largest uses all 32 bits, so that the first 8-bit pass spreads the
+// keys over its bins (as they are they share their top byte, and hundreds of
+// additions to one counter take a microsecond), and stop as soon as the
+// threshold's bin is taken whole.
+constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickKeys = 8192;
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SparseArgs a) {
+  __shared__ uint32_t s_keys[kPickKeys];
+  __shared__ uint32_t s_hist[4][256];
+  __shared__ uint32_t s_lohi[2];
+  __shared__ int s_count[2];           // forced, ordinary
+  __shared__ int s_scan[2][kPickWarps];
+  __shared__ int s_pick[3];            // radix pass: bin, keys above it, keys in it
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int Hkv = a.pool.num_kv_heads;
+  const int g = static_cast<int>(blockIdx.x % Hkv), i_tok = static_cast<int>(blockIdx.x / Hkv);
+  const int t = a.tok_first + i_tok;
+  for (int i = tid; i < 4 * 256; i += kPickThreads) (&s_hist[0][0])[i] = 0;
+  if (tid == 0) {
+    s_lohi[0] = 0xffffffffu;
+    s_lohi[1] = 0u;
+    s_count[0] = s_count[1] = 0;
+  }
+  griddep_wait();
+  griddep_launch();
+  if (req_of_warp(a.cu_q_lens, a.num_reqs, t, lane) < 0) return;   // block-uniform
+  const int p = __ldg(a.positions + t);
+  int32_t* out = a.sel + (static_cast<int64_t>(t) * Hkv + g) * a.top_k;
+  const int n = p >= 0 && p < a.max_blocks * kBlockSize ? (p >> 4) + 1 : 0;
+  const uint32_t* src = a.keys + (static_cast<int64_t>(i_tok) * Hkv + g) * a.max_blocks;
+  const bool kept = n <= kPickKeys;
+  __syncthreads();
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  int forced = 0, ordinary = 0;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kPickThreads) {
+    const uint32_t k = __ldcg(src + i);
+    if (kept) s_keys[i] = k;
+    if (k == 0xffffffffu) {
+      ++forced;
+    } else if (k != 0u) {
+      lo = min(lo, k);
+      hi = max(hi, k);
+      ++ordinary;
     }
   }
+  auto key = [&](int i) { return kept ? s_keys[i] : __ldcg(src + i); };
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  ordinary = __reduce_add_sync(0xffffffffu, ordinary);
+  if (lane == 0) {
+    atomicMin(&s_lohi[0], lo);
+    atomicMax(&s_lohi[1], hi);
+    atomicAdd(&s_count[0], forced);
+    atomicAdd(&s_count[1], ordinary);
+  }
   __syncthreads();
-  // The top_k-th largest key, 8 bits at a time.
-  const int cnt = b1 - b0;
+  lo = s_lohi[0];
+  hi = s_lohi[1];
+  forced = s_count[0];
+  ordinary = s_count[1];
+  // Ordinary keys in the passes' form: key - lo, shifted up.  Taken are the forced keys, the ordinary ones above
+  // `thr`, and the first `need` equal to it.
+  const int shift0 = hi > lo ? __clz(hi - lo) : 0;
+  auto form = [&](uint32_t k) { return (k - lo) << shift0; };
+  const bool forced_only = forced >= a.top_k;   // the first top_k of the forced ones
+  bool all = false;                             // every ordinary key
   uint32_t thr = 0;
-  int need = min(a.top_k, n);       // keys still to be found at or below the current prefix
-  if (n > a.top_k) {
+  int need = forced_only ? a.top_k : min(a.top_k - forced, ordinary);
+  if (!forced_only && need == ordinary) {
+    all = true;
+  } else if (!forced_only && hi > lo) {
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
-      for (int i = tid; i < cnt; i += kSelThreads) {
-        const uint32_t k = keys[i];
-        if (pass == 0 || (k >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&s_hist[pass][(k >> shift) & 255u], 1u);
+      for (int i = tid; i < n; i += kPickThreads) {
+        const uint32_t k = key(i), v = form(k);
+        if (k != 0u && k != 0xffffffffu && (pass == 0 || (v >> (shift + 8)) == (thr >> (shift + 8))))
+          atomicAdd(&s_hist[pass][(v >> shift) & 255u], 1u);
       }
-      if constexpr (CS > 1) cg::this_cluster().sync(); else __syncthreads();
-      // Thread i: bin 255 - i over the whole cluster, then an inclusive scan from the top bin.
-      int c = 0;
-#pragma unroll
-      for (int x = 0; x < CS; ++x) {
-        const uint32_t* h = &s_hist[pass][255 - tid];
-        if constexpr (CS > 1) h = cg::this_cluster().map_shared_rank(h, x);
-        c += static_cast<int>(*h);
-      }
+      __syncthreads();
+      // Thread i < 256: bin 255 - i, then an inclusive scan from the top bin.
+      const int c = tid < 256 ? static_cast<int>(s_hist[pass][255 - tid]) : 0;
       int inc = c;
 #pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, x);
-        if (lane >= x) inc += y;
+      for (int y = 1; y < 32; y <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, inc, y);
+        if (lane >= y) inc += z;
       }
       if (lane == 31) s_scan[0][warp] = inc;
       __syncthreads();
@@ -330,103 +479,85 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SparseArgs a)
       if (inc >= need && inc - c < need) {
         s_pick[0] = 255 - tid;
         s_pick[1] = inc - c;
+        s_pick[2] = c;
       }
       __syncthreads();
       thr |= static_cast<uint32_t>(s_pick[0]) << shift;
       need -= s_pick[1];
+      if (need == s_pick[2]) {   // everything from the bin on: thr > 0, or every ordinary key would be taken
+        thr -= 1u;
+        need = 0;
+        break;
+      }
       __syncthreads();
     }
   }
-  if (thr == 0u) need = 0;   // all are taken but the entries without a block (key 0)
-  // Count, then write in order: keys above thr, and the first `need` equal to it.
+  // 2: taken, 1: equal to the threshold, 0: not taken.
+  auto kind = [&](uint32_t k) -> int {
+    if (k == 0u) return 0;
+    if (k == 0xffffffffu) return forced_only ? 1 : 2;
+    if (forced_only) return 0;
+    if (all) return 2;
+    const uint32_t v = form(k);
+    return v > thr ? 2 : v == thr && need > 0 ? 1 : 0;
+  };
+  // Each warp writes the entries of its own stretch of the blocks, in order: first every warp counts.
+  const int per = ((n + kPickWarps - 1) / kPickWarps + 31) / 32 * 32;
+  const int w0 = min(n, warp * per), w1 = min(n, w0 + per);
   int gt = 0, eq = 0;
-  for (int i = tid; i < cnt; i += kSelThreads) {
-    gt += keys[i] > thr;
-    eq += keys[i] == thr;
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const int x = kind(key(i));
+    gt += x == 2;
+    eq += x == 1;
   }
-  if (gt) atomicAdd(&s_cnt[0], gt);
-  if (eq) atomicAdd(&s_cnt[1], eq);
-  if constexpr (CS > 1) cg::this_cluster().sync(); else __syncthreads();
-  int eq_before = 0, at = 0, total = 0, eq_left = 0;
-#pragma unroll
-  for (int x = 0; x < CS; ++x) {
-    const int* c = s_cnt;
-    if constexpr (CS > 1) c = cg::this_cluster().map_shared_rank(c, x);
-    const int cgt = c[0], ceq = c[1];
-    const int take = min(max(need - eq_before, 0), ceq);
-    if (x < rank) at += cgt + take;
-    if (x == rank) eq_left = max(need - eq_before, 0);   // equal keys that this CTA may take
-    total += cgt + take;
-    eq_before += ceq;
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  __syncthreads();   // s_scan is free
+  if (lane == 0) {
+    s_scan[0][warp] = eq;
+    s_scan[1][warp] = gt;
   }
-  for (int base = 0; base < cnt; base += kSelThreads) {
-    const int i = base + tid;
-    const uint32_t k = i < cnt ? keys[i] : 0u;
-    const bool is_eq = i < cnt && k == thr, is_gt = i < cnt && k > thr;
-    const uint32_t beq = __ballot_sync(0xffffffffu, is_eq), bgt = __ballot_sync(0xffffffffu, is_gt);
-    if (lane == 0) { s_scan[0][warp] = __popc(beq); s_scan[1][warp] = __popc(bgt); }
-    __syncthreads();
-    int weq = 0, wgt = 0, teq = 0, tgt = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) { weq += s_scan[0][w]; wgt += s_scan[1][w]; }
-      teq += s_scan[0][w];
-      tgt += s_scan[1][w];
+  __syncthreads();
+  int at = 0, left = need, total = 0;   // where the warp writes, equal keys that it and later ones may take
+  for (int w = 0, l = need; w < kPickWarps; ++w) {
+    const int take = min(l, s_scan[0][w]);
+    if (w < warp) {
+      at += s_scan[1][w] + take;
+      left -= take;
     }
-    const uint32_t below = (1u << lane) - 1u;
-    const int peq = weq + __popc(beq & below), pgt = wgt + __popc(bgt & below);
-    const bool take = is_gt || (is_eq && peq < eq_left);
-    if (take) out[at + pgt + min(peq, eq_left)] = b0 + i;
-    at += tgt + min(eq_left, teq);
-    eq_left -= min(eq_left, teq);
-    __syncthreads();
+    l -= take;
+    total += s_scan[1][w] + take;
   }
-  if (rank == 0)
-    for (int i = total + tid; i < a.top_k; i += kSelThreads) out[i] = -1;
-  if constexpr (CS > 1) cg::this_cluster().sync();   // no CTA leaves while another reads its shared memory
-}
-
-// Launches a kernel with clusters of CS CTAs.
-template <class K, class... Args>
-cudaError_t launch_cluster(K kernel, int cs, int64_t grid, int threads, int smem, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <int D, int CS>
-int launch_select_t(const SparseArgs& a, cudaStream_t s) {
-  cudaError_t e = smem_attr_once<select_kernel<D, CS>>(kSelMost * 4);
-  if (e != cudaSuccess) return e;
-  const int smem = (a.max_blocks + CS - 1) / CS * 4;
-  return launch_cluster(select_kernel<D, CS>, CS, static_cast<int64_t>(a.num_tokens) * a.pool.num_kv_heads * CS,
-                        kSelThreads, smem, s, a);
+  for (int base = w0; base < w1; base += 32) {
+    const int i = base + lane;
+    const int x = i < w1 ? kind(key(i)) : 0;
+    const uint32_t beq = __ballot_sync(0xffffffffu, x == 1), bgt = __ballot_sync(0xffffffffu, x == 2);
+    const uint32_t below = (1u << lane) - 1u;
+    const int peq = __popc(beq & below), pgt = __popc(bgt & below);
+    if (x == 2 || (x == 1 && peq < left)) out[at + pgt + min(peq, left)] = i;
+    const int teq = min(left, __popc(beq));
+    at += __popc(bgt) + teq;
+    left -= teq;
+  }
+  for (int i = total + tid; i < a.top_k; i += kPickThreads) out[i] = -1;
 }
 
 template <int D>
-int launch_select_d(const SparseArgs& a, cudaStream_t s) {
-  // The larger the cluster, the more of the machine a small batch uses; a
-  // part has 256 blocks at least, and a CTA's scores have to fit.
-  const int64_t th = static_cast<int64_t>(a.num_tokens) * a.pool.num_kv_heads;
-  int cs = 1;
-  while (cs < 8 && ((th * cs < 2 * a.num_sms && a.max_blocks / (2 * cs) >= 256) ||
-                    (a.max_blocks + cs - 1) / cs > kSelMost))
-    cs *= 2;
-  switch (cs) {
-    case 1: return launch_select_t<D, 1>(a, s);
-    case 2: return launch_select_t<D, 2>(a, s);
-    case 4: return launch_select_t<D, 4>(a, s);
-    default: return launch_select_t<D, 8>(a, s);
+int launch_select_d(SparseArgs a, cudaStream_t s) {
+  const int ring = kScoreStages * kScoreThreads * (2 * D / 64) * 16;
+  const int smem = a.pool.num_kv_heads * 4 * D + ring;
+  cudaError_t e = smem_attr_once<score_kernel<D>>(kSelectMaxHeads * 4 * D + ring);
+  if (e != cudaSuccess) return e;
+  // Tokens in parts whose keys fit the workspace.
+  for (int t = 0; t < a.num_tokens; t += a.tok_most) {
+    a.tok_first = t;
+    a.tok_count = std::min(a.tok_most, a.num_tokens - t);
+    e = launch_dependent(score_kernel<D>, dim3(3 * a.num_sms), kScoreThreads, smem, s, a);
+    if (e == cudaSuccess)
+      e = launch_dependent(pick_kernel, dim3(static_cast<unsigned>(a.tok_count) * a.pool.num_kv_heads), kPickThreads, 0, s, a);
+    if (e != cudaSuccess) return e;
   }
+  return cudaSuccess;
 }
 
 template <int D, bool F8>
@@ -452,7 +583,11 @@ int launch_summarize(const SparseArgs& a, void* stream) {
   return f8 ? launch_summarize_d<64, true>(a, s) : launch_summarize_d<64, false>(a, s);
 }
 
-int select_max_blocks() { return 8 * kSelMost; }
+// Keys of as many tokens as fit 64 MB, of one at least.
+int select_part(int num_tokens, int max_blocks, int num_kv_heads) {
+  const int64_t one = static_cast<int64_t>(max_blocks) * num_kv_heads * 4;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_tokens, (64ll << 20) / one)));
+}
 
 int launch_select(const SparseArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);

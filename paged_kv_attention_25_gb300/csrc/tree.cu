@@ -82,8 +82,9 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   int* s_odd = &s_flags[1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, Hkv = a.pool.num_kv_heads;
-  const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
+  griddep_wait();
   griddep_launch();   // the merge may take its place and wait
+  const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
   if (tid < kRowWarps) a.cuts[blockIdx.x * kRowWarps + tid].count = 0;
   if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
   if (tid == 0) {
@@ -400,14 +401,14 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
 }
 
 // One warp per kRows rows of a cut group: merges their partials in the workers'
-// order.  LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c.  The
-// rows' loads are independent, so that a warp has kRows of them in flight:
-// with one row a warp the kernel waited for its loads (28 us against 9 for 190
-// groups of 256 rows, two to three partials each).
+// order with a running maximum, kBatch partials of each row in flight.
+//   M = max LSE_c, LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c
+// Bound by the latency of its loads (the record, then the partials).
 template <int D, int SlotRows>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kDPL = D / 32;
   constexpr int kRows = SlotRows >= 128 ? 4 : 2;
+  constexpr int kBatch = SlotRows >= 128 ? 2 : 4;
   griddep_wait();   // the attention kernel's writes
   const int lane = threadIdx.x & 31;
   const int row0 = (static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5)) * kRows;
@@ -429,39 +430,48 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
 #pragma unroll
     for (int d = 0; d < kDPL; ++d) acc[k][d] = 0.f;
   }
-  for (int c = lane; c < s.x; c += 32) {
+  for (int c0 = 0; c0 < s.x; c0 += kBatch) {
+    float e[kBatch][kRows], v[kBatch][kRows][kDPL];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (i0 + k < rows) M[k] = fmaxf(M[k], __ldcg(a.part_lse + slot_row(c) + k));
-  }
+    for (int c = 0; c < kBatch; ++c) {
+      const int64_t at = slot_row(min(c0 + c, s.x - 1));
 #pragma unroll
-  for (int k = 0; k < kRows; ++k)
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], x));
-#pragma unroll 2
-  for (int c = 0; c < s.x; ++c) {
-    const int64_t at = slot_row(c);
-    float e[kRows], v[kRows][kDPL];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int64_t r = at + (i0 + k < rows ? k : 0);
-      e[k] = __ldcg(a.part_lse + r);
-      const float* src = a.part_o + r * D + lane * kDPL;
-      if constexpr (kDPL == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        v[k][0] = x.x; v[k][1] = x.y;
+      for (int k = 0; k < kRows; ++k) {
+        const int64_t r = at + (i0 + k < rows ? k : 0);
+        e[c][k] = __ldcg(a.part_lse + r);
+        const float* src = a.part_o + r * D + lane * kDPL;
+        if constexpr (kDPL == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          v[c][k][0] = x.x; v[c][k][1] = x.y; v[c][k][2] = x.z; v[c][k][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[c][k][0] = x.x; v[c][k][1] = x.y;
+        }
       }
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      if (e[k] == -CUDART_INF_F) continue;   // no key of this row there
-      const float wgt = fast_exp2(e[k] - M[k]);
-      sum[k] += wgt;
+      float m = M[k];
 #pragma unroll
-      for (int d = 0; d < kDPL; ++d) acc[k][d] = fmaf(wgt, v[k][d], acc[k][d]);
+      for (int c = 0; c < kBatch; ++c) {
+        if (c0 + c >= s.x) e[c][k] = -CUDART_INF_F;
+        m = fmaxf(m, e[c][k]);
+      }
+      if (m > M[k]) {
+        const float f = M[k] == -CUDART_INF_F ? 1.f : fast_exp2(M[k] - m);   // (nothing, or NaN, summed so far)
+        sum[k] *= f;
+#pragma unroll
+        for (int d = 0; d < kDPL; ++d) acc[k][d] *= f;
+        M[k] = m;
+      }
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        if (e[c][k] == -CUDART_INF_F) continue;   // no key of this row there
+        const float wgt = fast_exp2(e[c][k] - M[k]);
+        sum[k] += wgt;
+#pragma unroll
+        for (int d = 0; d < kDPL; ++d) acc[k][d] = fmaf(wgt, v[c][k][d], acc[k][d]);
+      }
     }
   }
 #pragma unroll
@@ -519,8 +529,7 @@ int launch_rows_l(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* 
   const int smem = RowsSmem<D, F8>::kTotal;
   cudaError_t e = smem_attr_once<rows_kernel<D, F8, LIST>>(smem);
   if (e != cudaSuccess) return e;
-  rows_kernel<D, F8, LIST><<<a.ctas, kRowsThreads, smem, s>>>(a, *tmk, *tmv);
-  return cudaGetLastError();
+  return launch_dependent(rows_kernel<D, F8, LIST>, dim3(a.ctas), kRowsThreads, smem, s, a, *tmk, *tmv);
 }
 
 template <int D, bool F8>
@@ -530,16 +539,7 @@ int launch_rows(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tm
 
 template <int D, int SlotRows>
 int launch_merge_t(const TreeArgs& a, int cuts, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(cuts, SlotRows >= 128 ? SlotRows / 32 : 1);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, SlotRows>, a);
+  return launch_dependent(tree_merge_kernel<D, SlotRows>, dim3(cuts, SlotRows >= 128 ? SlotRows / 32 : 1), 256, 0, s, a);
 }
 
 }  // namespace

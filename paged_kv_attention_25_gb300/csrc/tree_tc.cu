@@ -232,6 +232,7 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
   using B = typename M::B;
   constexpr int kKSt = S::kKSt, kVSt = S::kVSt;
   extern __shared__ __align__(1024) uint8_t smem[];
+  griddep_wait();
   griddep_launch();   // the merge may take its place and wait
   if (threadIdx.x < 2) a.cuts[2 * blockIdx.x + threadIdx.x].count = 0;
   if ((smem_u32(smem) & 1023u) != 0) {   // swizzle atoms need 1024-byte alignment
@@ -947,8 +948,7 @@ int launch_t(const TreeArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, co
   const int smem = TreeSmem<D>::kTotal;
   cudaError_t e = smem_attr_once<tree_tc_kernel<D, F8>>(smem);
   if (e != cudaSuccess) return e;
-  tree_tc_kernel<D, F8><<<a.ctas, kThreads, smem, s>>>(a, *tk, *tv, *tq);
-  return cudaGetLastError();
+  return launch_dependent(tree_tc_kernel<D, F8>, dim3(a.ctas), kThreads, smem, s, a, *tk, *tv, *tq);
 }
 
 }  // namespace

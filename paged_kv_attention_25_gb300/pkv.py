@@ -50,7 +50,8 @@ EXPORTED = (
     "pkv_profile_enable", "pkv_profile_read", "pkv_device_sm_count", "pkv_last_error",
     "pkv_version", "pkv_copy_to_device", "pkv_copy_to_host", "pkv_debug_set",
     "pkv_cache_create", "pkv_cache_destroy", "pkv_cache_step", "pkv_cache_release", "pkv_cache_free_blocks",
-    "pkv_tree_mask", "pkv_tree_attn_workspace_size", "pkv_tree_attn", "pkv_summarize", "pkv_select_blocks",
+    "pkv_tree_mask", "pkv_tree_attn_workspace_size", "pkv_tree_attn", "pkv_summarize", "pkv_select_blocks_workspace_size",
+    "pkv_select_blocks",
     "pkv_sparse_attn_workspace_size", "pkv_sparse_attn", "pkv_fork_workspace_size", "pkv_fork", "pkv_copy_blocks", "pkv_compact",
 )
 
@@ -149,7 +150,8 @@ def load_library():
             "pkv_tree_attn_workspace_size": [P, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
             "pkv_tree_attn": [P, P, I, P, I, P, P, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
             "pkv_summarize": [P, P, I, I, P, P, P, I, P, P, P],
-            "pkv_select_blocks": [P, P, I, P, P, I, P, I, I, P, P, I, I, I, P, P],
+            "pkv_select_blocks_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_select_blocks": [P, P, I, P, P, I, P, I, I, P, P, I, I, I, P, P, ctypes.c_size_t, P],
             "pkv_sparse_attn_workspace_size": [P, ctypes.POINTER(ctypes.c_size_t)],
             "pkv_sparse_attn": [P, P, I, P, P, I, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
             "pkv_fork_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
@@ -554,8 +556,14 @@ def pkv_summarize(pool: Pool, summary: BlockSummary, block_tables, cu_q_lens, po
                                         _op_stream(pool, stream)))
 
 
+def pkv_select_blocks_workspace_size(pool: Pool, max_blocks: int, num_tokens: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().pkv_select_blocks_workspace_size(pool.handle, max_blocks, num_tokens, ctypes.byref(n)))
+    return n.value
+
+
 def pkv_select_blocks(pool: Pool, summary: BlockSummary, q, q_positions, block_tables, cu_q_lens, top_k: int,
-                      sinks: int = 1, recent: int = 1, out=None, stream=None):
+                      sinks: int = 1, recent: int = 1, out=None, workspace=None, stream=None):
     """The top_k blocks of each (token, KV head) by the bound on its scores, the first `sinks` and last `recent` always
     among them: [T, Hkv, top_k] int32 indexes into the block table, ascending, -1 beyond."""
     R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
@@ -568,8 +576,9 @@ def pkv_select_blocks(pool: Pool, summary: BlockSummary, q, q_positions, block_t
         out = _op_new(pool, (T, pool.num_kv_heads, top_k), _I32, stream)
     op = _op_ptr(pool, out, "out", _I32, (T, pool.num_kv_heads, top_k))
     codes, exps = _op_summary(pool, summary)
+    ws, n = _op_workspace(pool, workspace, ("select", width, T), pkv_select_blocks_workspace_size, stream)
     _check(load_library().pkv_select_blocks(pool.handle, qp, Hq, pos, bt, width, cu, R, T, codes, exps, top_k, sinks,
-                                            recent, op, _op_stream(pool, stream)))
+                                            recent, op, ws.data_ptr(), n, _op_stream(pool, stream)))
     return out
 
 

@@ -21,7 +21,8 @@ def test_null_pool(lib):
     assert lib.pkv_tree_attn(None, None, 8, None, 1, None, None, None, 1, 1, None, 1, 1.0, None, None, None, 0,
                              None) == pkv.PKV_EINVAL
     assert lib.pkv_summarize(None, None, 1, 1, None, None, None, 1, None, None, None) == pkv.PKV_EINVAL
-    assert lib.pkv_select_blocks(None, None, 8, None, None, 1, None, 1, 1, None, None, 1, 0, 0, None,
+    assert lib.pkv_select_blocks_workspace_size(None, 1, 1, ctypes.byref(n)) == pkv.PKV_EINVAL
+    assert lib.pkv_select_blocks(None, None, 8, None, None, 1, None, 1, 1, None, None, 1, 0, 0, None, None, 0,
                                  None) == pkv.PKV_EINVAL
     assert lib.pkv_sparse_attn_workspace_size(None, ctypes.byref(n)) == pkv.PKV_EINVAL
     assert lib.pkv_sparse_attn(None, None, 8, None, None, 1, None, 1, 1, None, 1, 1.0, None, None, None, 0,
