@@ -91,31 +91,39 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
     const int64_t chunk = static_cast<int64_t>(pb) * Hkv + g;
     const uint8_t* src = static_cast<const uint8_t*>(a.pool.k) + chunk * kBlockSize * D * (F8 ? 1 : 2) +
                          lane * kDPL * (F8 ? 1 : 2);
+    // All rows' loads first (past the written keys: the last one again), so that they are in flight together.
+    uint32_t raw[kBlockSize][F8 ? 1 : kDPL / 2];
+#pragma unroll
+    for (int j = 0; j < kBlockSize; ++j) {
+      const uint8_t* row = src + min(j, n - 1) * D * (F8 ? 1 : 2);
+      if constexpr (F8) {
+        if constexpr (kDPL == 4) raw[j][0] = __ldg(reinterpret_cast<const uint32_t*>(row));
+        else raw[j][0] = __ldg(reinterpret_cast<const uint16_t*>(row));
+      } else if constexpr (kDPL == 4) {
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(row));
+        raw[j][0] = y.x;
+        raw[j][1] = y.y;
+      } else {
+        raw[j][0] = __ldg(reinterpret_cast<const uint32_t*>(row));
+      }
+    }
     float hi[kDPL], lo[kDPL];
 #pragma unroll
     for (int d = 0; d < kDPL; ++d) { hi[d] = -CUDART_INF_F; lo[d] = CUDART_INF_F; }
 #pragma unroll
-    for (int j = 0; j < kBlockSize; ++j) {   // past the written keys: the last one again
+    for (int j = 0; j < kBlockSize; ++j) {
       float x[kDPL];
-      const uint8_t* row = src + min(j, n - 1) * D * (F8 ? 1 : 2);
       if constexpr (F8) {
         uint32_t h[2];
-        if constexpr (kDPL == 4) e4m3x4_to_f16x4(__ldg(reinterpret_cast<const uint32_t*>(row)), h[0], h[1]);
-        else h[0] = e4m3x2_lo_to_f16x2(__ldg(reinterpret_cast<const uint16_t*>(row)));
+        if constexpr (kDPL == 4) e4m3x4_to_f16x4(raw[j][0], h[0], h[1]);
+        else h[0] = e4m3x2_lo_to_f16x2(raw[j][0]);
 #pragma unroll
         for (int d = 0; d < kDPL; d += 2)
           asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
               : "=f"(x[d]), "=f"(x[d + 1]) : "r"(h[d / 2]));
       } else {
-        uint32_t v[2];
-        if constexpr (kDPL == 4) {
-          const uint2 y = __ldg(reinterpret_cast<const uint2*>(row));
-          v[0] = y.x; v[1] = y.y;
-        } else {
-          v[0] = __ldg(reinterpret_cast<const uint32_t*>(row));
-        }
 #pragma unroll
-        for (int d = 0; d < kDPL; d += 2) { x[d] = bf16lo_to_f32(v[d / 2]); x[d + 1] = bf16hi_to_f32(v[d / 2]); }
+        for (int d = 0; d < kDPL; d += 2) { x[d] = bf16lo_to_f32(raw[j][d / 2]); x[d + 1] = bf16hi_to_f32(raw[j][d / 2]); }
       }
 #pragma unroll
       for (int d = 0; d < kDPL; ++d) {   // NaN: no change (fmaxf and fminf return the other operand)

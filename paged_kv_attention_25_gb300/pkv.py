@@ -261,7 +261,8 @@ class Pool:
         self.handle = h
         self._ws = None
         self.device_index = self.k.get_device()
-        self._op_ws = {}     # workspace sizes of the calls below, by their sizes
+        self._op_ws = {}     # workspace sizes of the device-metadata calls, by their sizes
+        self._op_buf = {}    # their workspace of each stream
 
     def close(self):
         if getattr(self, "handle", None):
@@ -402,8 +403,9 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
 # ---------------------------------------------------------------------------------------------------------------------
 # Tree attention, block-selected attention and pages.  Their metadata is read on the device alone: no HostMeta, and the
 # calls can be captured into a graph.  Tensors live on the pool's device; without `stream` a call runs on that device's
-# current stream.  Outputs and workspaces that are not given are allocated for that stream, the workspace afresh for
-# each call (a captured graph keeps its own).
+# current stream.  Outputs and workspaces that are not given are allocated for that stream.  The workspace of calls on a
+# current stream is kept with the pool, one for each stream: calls on one stream follow one another.  A call that is
+# being captured, or that names another stream, gets one of its own (a captured graph keeps it).
 
 _I32, _I8, _BF16, _F32, _U8 = torch.int32, torch.int8, torch.bfloat16, torch.float32, torch.uint8
 
@@ -447,14 +449,20 @@ def _op_new(pool: Pool, shape, dtype, stream):
 
 def _op_workspace(pool: Pool, workspace, key, size, stream):
     """(the tensor, its bytes); key: what the size depends on."""
-    if workspace is None:
-        n = pool._op_ws.get(key)
-        if n is None:
-            n = pool._op_ws[key] = size(pool, *key[1:])
+    if workspace is not None:
+        n = _op_dims(workspace, "workspace", 1)[0]
+        _op_ptr(pool, workspace, "workspace", _U8, (n,))
+        return workspace, n
+    n = pool._op_ws.get(key)
+    if n is None:
+        n = pool._op_ws[key] = size(pool, *key[1:])
+    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
         return _op_new(pool, (n,), _U8, stream), n
-    n = _op_dims(workspace, "workspace", 1)[0]
-    _op_ptr(pool, workspace, "workspace", _U8, (n,))
-    return workspace, n
+    raw = torch._C._cuda_getCurrentRawStream(pool.device_index)
+    buf = pool._op_buf.get(raw)
+    if buf is None or buf.numel() < n:
+        buf = pool._op_buf[raw] = _op_new(pool, (n,), _U8, None)
+    return buf, n
 
 
 def _op_batch(pool: Pool, block_tables, cu_q_lens):
