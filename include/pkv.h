@@ -335,7 +335,8 @@ int pkv_paged_attn_static(pkv_pool* pool, const void* q, int num_q_heads, const 
  * graphs that may be replayed at the same time among them, need their own.
  * num_tokens == 0 is a no-op.  Errors: PKV_EINVAL, PKV_EUNSUPPORTED, PKV_ECUDA.
  */
-int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, size_t* bytes);
+int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_blocks, int num_reqs, int num_tokens,
+                                 size_t* bytes);
 int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* block_tables, int max_blocks,
                   const int32_t* ctx_lens, const int32_t* prefix_lens, const int32_t* cu_q_lens, int num_reqs,
                   int num_tokens, const uint32_t* tree_mask, int mask_words, float scale, void* o, float* lse,

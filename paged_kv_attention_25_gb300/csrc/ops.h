@@ -32,6 +32,11 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, 
 struct TreeForm {
   bool tensor;
   int ctas, cuts, slots, slot_rows;
+  int many_groups;   // rows form: from so many groups on, a share a warp
+  void shrink(int n) {
+    cuts = cuts / ctas * n;
+    ctas = n;
+  }
 };
 TreeForm tree_form(bool tensor, int num_sms);
 // tmk / tmv: the pool's block maps (rows form: 128-byte swizzle, unused by FP8
@@ -39,7 +44,7 @@ TreeForm tree_form(bool tensor, int num_sms);
 // (launch_tree_rows also runs the attention over selected blocks.)
 int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* stream);
 int launch_tree_tc(const TreeArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream);
-int launch_tree_merge(const TreeArgs& a, const TreeForm& f, void* stream);
+int launch_tree_merge(const TreeArgs& a, void* stream);
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
                      unsigned* err, void* stream);
 

@@ -76,9 +76,19 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
   a.cuts = reinterpret_cast<TreeCut*>(ws + w.cuts);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  a.form = f;
   a.ctas = f.ctas;
   a.wait_ns = pool->wait_ns;
   return a;
+}
+
+// Launches as many CTAs as `units` (an upper bound of the call's blocks or key
+// tiles) can occupy: 16 a CTA of the rows form, one of the tiles form (an even
+// number: quads go to pairs of CTAs).
+void fit_ctas(TreeArgs& a, int64_t units) {
+  const int64_t want = a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
+  a.form.shrink(static_cast<int>(std::min<int64_t>(want < 2 ? 2 : want, a.form.ctas)));
+  a.ctas = a.form.ctas;
 }
 
 int check_workspace(const void* workspace, size_t have, size_t need, const char* size_fn) {
@@ -87,11 +97,22 @@ int check_workspace(const void* workspace, size_t have, size_t need, const char*
   return PKV_OK;
 }
 
-// Which form a batch takes.
-bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens) {
+// Which form a batch takes, by its mean number of query rows a (request, KV
+// head).  The rows form reads K and V once for every 16 rows, the tiles form once
+// for 128 (or 256), but has more to start and, for FP8 pools, to widen.  Measured
+// (rows / tiles, us): bf16, D = 128, 12 requests of 1.5 to 20 thousand tokens, 8
+// KV heads: 16 rows 66 / 68, 24 rows 91 / 69, 64 rows 116 / 72; D = 64, 32 requests
+// of 1 to 3 thousand: 32 rows 41 / 45, 48 rows 53 / 46; FP8, D = 128: 32 rows
+// 77 / 84, 48 rows 95 / 85; 40 KV heads: 32 rows 149 / 212, 64 rows 281 / 233.
+// A batch that gives every CTA of the rows form 16 blocks at most stays there
+// (one request of 240 tokens, 128 rows: 15.6 / 16.4).
+bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks) {
   if (pool->tree_form != 0) return pool->tree_form == 2;
+  if (num_reqs < 1) return false;
   const int64_t rows = static_cast<int64_t>(num_tokens) * (num_q_heads / pool->num_kv_heads);
-  return rows > 24ll * num_reqs;
+  const int64_t most = pool->elem_bytes == 1 ? 44 : pool->head_dim == 64 ? 40 : 20;
+  const int64_t work = (rows / 16 + num_reqs) * pool->num_kv_heads * max_blocks;   // at most
+  return rows > most * num_reqs && work > 16ll * 3 * pool->num_sms;
 }
 
 // The maps whose copies land with the 128-byte swizzle that rows.cuh reads.
@@ -129,12 +150,13 @@ int pkv_tree_mask(pkv_pool* pool, const int32_t* parents, const int32_t* cu_q_le
   return PKV_OK;
 }
 
-int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, size_t* bytes) {
+int pkv_tree_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_blocks, int num_reqs, int num_tokens,
+                                 size_t* bytes) {
   if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
   const int rc = check_heads(pool, num_q_heads);
   if (rc) return rc;
-  if (num_reqs < 0 || num_tokens < 0) return fail(PKV_EINVAL, "negative size");
-  *bytes = tree_ws(pool, tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens), pool->num_sms)).total;
+  if (num_reqs < 0 || num_tokens < 0 || max_blocks < 0) return fail(PKV_EINVAL, "negative size");
+  *bytes = tree_ws(pool, tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms)).total;
   return PKV_OK;
 }
 
@@ -151,7 +173,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   if (mask_words < 1) return fail(PKV_EINVAL, "mask_words must be >= 1");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
-  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens), pool->num_sms);
+  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
   const TreeWs w = tree_ws(pool, form);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_tree_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
@@ -173,6 +195,10 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   a.o = o;
   a.lse = lse;
   a.tile_tokens = kTcRows / a.group;
+  // No more CTAs than the largest batch of these sizes can use.
+  const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / (form.tensor ? kTcRows : 16) + num_reqs) *
+                         pool->num_kv_heads;
+  fit_ctas(a, groups * (form.tensor ? static_cast<int64_t>(max_blocks) / 8 + 1 : max_blocks + 1) + groups);
   a.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   if (form.tensor) {
     CUtensorMap tmap_q;
@@ -183,7 +209,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
                       [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
   }
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree attention launch");
-  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, form, stream); });
+  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree merge launch");
   return PKV_OK;
 }
@@ -303,13 +329,14 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   a.num_tokens = num_tokens;
   a.sel = selected;
   a.top_k = top_k;
+  fit_ctas(a, static_cast<int64_t>(num_tokens) * pool->num_kv_heads * ((a.group + 15) / 16) * (static_cast<int64_t>(top_k) + 2));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o;
   a.lse = lse;
   rc = timed_launch(pool, 1, stream,
                     [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected attention launch");
-  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, form, stream); });
+  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected merge launch");
   return PKV_OK;
 }

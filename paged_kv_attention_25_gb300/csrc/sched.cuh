@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "ops.h"
 
 namespace pkv {
 
@@ -40,6 +41,7 @@ struct TreeArgs {
   struct TreeCut* cuts;
   float* part_o;     // [slots][slot rows][D]
   float* part_lse;   // [slots][slot rows], log2 units
+  TreeForm form;
   int ctas;          // CTAs of the attention launch
   int tile_tokens;   // tensor-core form: tokens of a tile of 128 rows
   int q_box_tokens;  // ... and of a copy of its query map

@@ -560,7 +560,10 @@ int launch_select_d(SparseArgs a, cudaStream_t s) {
   for (int t = 0; t < a.num_tokens; t += a.tok_most) {
     a.tok_first = t;
     a.tok_count = std::min(a.tok_most, a.num_tokens - t);
-    e = launch_dependent(score_kernel<D>, dim3(3 * a.num_sms), kScoreThreads, smem, s, a);
+    // No more CTAs than there can be shares of 16 units.
+    const int64_t units = static_cast<int64_t>(a.tok_count) * (a.max_blocks + kTokenUnits);
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(3 * a.num_sms, (units + 15) / 16));
+    e = launch_dependent(score_kernel<D>, dim3(ctas), kScoreThreads, smem, s, a);
     if (e == cudaSuccess)
       e = launch_dependent(pick_kernel, dim3(static_cast<unsigned>(a.tok_count) * a.pool.num_kv_heads), kPickThreads, 0, s, a);
     if (e != cudaSuccess) return e;

@@ -96,7 +96,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   auto groups = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
   auto units = [&](const TreeReq& q) { return groups(q) * (rows_blocks(q) + kGroupUnits); };
   // The shares: of this warp if there are many groups, of the CTA otherwise.
-  const int warp_id = static_cast<int>(blockIdx.x) * kRowWarps + warp, many_from = a.ctas / 2;
+  const int warp_id = static_cast<int>(blockIdx.x) * kRowWarps + warp, many_from = a.form.many_groups;
   TreeShare sh;
   bool solo;
   if constexpr (LIST) {
@@ -551,6 +551,7 @@ TreeForm tree_form(bool tensor, int num_sms) {
   f.cuts = tensor ? 2 * f.ctas : kRowWarps * f.ctas;   // two lines of work, or a share a warp
   f.slot_rows = tensor ? 256 : kRowTile;
   f.slots = 2 * f.cuts;
+  f.many_groups = f.ctas / 2;
   return f;
 }
 
@@ -563,11 +564,12 @@ int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* 
   return f8 ? launch_rows<64, true>(a, k, v, s) : launch_rows<64, false>(a, k, v, s);
 }
 
-int launch_tree_merge(const TreeArgs& a, const TreeForm& f, void* stream) {
+int launch_tree_merge(const TreeArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (f.tensor)
-    return a.pool.head_dim == 128 ? launch_merge_t<128, 256>(a, f.cuts, s) : launch_merge_t<64, 256>(a, f.cuts, s);
-  return a.pool.head_dim == 128 ? launch_merge_t<128, kRowTile>(a, f.cuts, s) : launch_merge_t<64, kRowTile>(a, f.cuts, s);
+  const int n = a.form.cuts;
+  if (a.form.tensor)
+    return a.pool.head_dim == 128 ? launch_merge_t<128, 256>(a, n, s) : launch_merge_t<64, 256>(a, n, s);
+  return a.pool.head_dim == 128 ? launch_merge_t<128, kRowTile>(a, n, s) : launch_merge_t<64, kRowTile>(a, n, s);
 }
 
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,

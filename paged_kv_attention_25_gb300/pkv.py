@@ -147,7 +147,7 @@ def load_library():
             "pkv_cache_release": [P, I],
             "pkv_cache_free_blocks": [P, ctypes.POINTER(I), ctypes.POINTER(I)],
             "pkv_tree_mask": [P, P, P, I, I, P, I, P],
-            "pkv_tree_attn_workspace_size": [P, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_tree_attn_workspace_size": [P, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
             "pkv_tree_attn": [P, P, I, P, I, P, P, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P],
             "pkv_summarize": [P, P, I, I, P, P, P, I, P, P, P],
             "pkv_select_blocks_workspace_size": [P, I, I, ctypes.POINTER(ctypes.c_size_t)],
@@ -507,9 +507,9 @@ def pkv_tree_mask(pool: Pool, parents, cu_q_lens, mask_words=None, max_nodes=Non
     return out
 
 
-def pkv_tree_attn_workspace_size(pool: Pool, num_q_heads: int, num_reqs: int, num_tokens: int) -> int:
+def pkv_tree_attn_workspace_size(pool: Pool, num_q_heads: int, max_blocks: int, num_reqs: int, num_tokens: int) -> int:
     n = ctypes.c_size_t()
-    _check(load_library().pkv_tree_attn_workspace_size(pool.handle, num_q_heads, num_reqs, num_tokens,
+    _check(load_library().pkv_tree_attn_workspace_size(pool.handle, num_q_heads, max_blocks, num_reqs, num_tokens,
                                                        ctypes.byref(n)))
     return n.value
 
@@ -525,7 +525,7 @@ def pkv_tree_attn(pool: Pool, q, block_tables, ctx_lens, prefix_lens, cu_q_lens,
     ctx = _op_ptr(pool, ctx_lens, "ctx_lens", _I32, (R,))
     pre = _op_ptr(pool, prefix_lens, "prefix_lens", _I32, (R,))
     mask = _op_ptr(pool, tree_mask, "tree_mask", _I32, (T, words))
-    ws, n = _op_workspace(pool, workspace, ("tree", Hq, R, T), pkv_tree_attn_workspace_size, stream)
+    ws, n = _op_workspace(pool, workspace, ("tree", Hq, width, R, T), pkv_tree_attn_workspace_size, stream)
     _check(load_library().pkv_tree_attn(pool.handle, qp, Hq, bt, width, ctx, pre, cu, R, T, mask, words, scale,
                                         out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), n,
                                         _op_stream(pool, stream)))

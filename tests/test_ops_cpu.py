@@ -17,7 +17,7 @@ def lib():
 def test_null_pool(lib):
     n = ctypes.c_size_t()
     assert lib.pkv_tree_mask(None, None, None, 1, 1, None, 1, None) == pkv.PKV_EINVAL
-    assert lib.pkv_tree_attn_workspace_size(None, 8, 1, 1, ctypes.byref(n)) == pkv.PKV_EINVAL
+    assert lib.pkv_tree_attn_workspace_size(None, 8, 1, 1, 1, ctypes.byref(n)) == pkv.PKV_EINVAL
     assert lib.pkv_tree_attn(None, None, 8, None, 1, None, None, None, 1, 1, None, 1, 1.0, None, None, None, 0,
                              None) == pkv.PKV_EINVAL
     assert lib.pkv_summarize(None, None, 1, 1, None, None, None, 1, None, None, None) == pkv.PKV_EINVAL

@@ -196,7 +196,7 @@ def test_runs_are_repeatable_and_lse_is_optional():
 
 def test_other_stream_and_own_workspace():
     c = Case(19, [(700, 33), (90, 12)], 8, 2, 128)
-    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, 2, c.T), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, c.bt.shape[1], 2, c.T), dtype=torch.uint8, device="cuda")
     ws.fill_(0xFF)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -210,7 +210,7 @@ def test_captured_call_follows_lengths_tables_and_masks():
     bt, ctx, pre, cu, mask = (
         ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.prefix), ref.dev(c.cu), c.mask())
     out, lse = torch.zeros_like(c.q), torch.zeros((c.T, 8), device="cuda")
-    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, 3, c.T), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkv.pkv_tree_attn_workspace_size(c.pool, 8, c.bt.shape[1], 3, c.T), dtype=torch.uint8, device="cuda")
 
     def call():
         pkv.pkv_tree_attn(c.pool, c.q, bt, ctx, pre, cu, mask, c.scale, out=out, lse=lse, workspace=ws)
