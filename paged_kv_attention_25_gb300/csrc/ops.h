@@ -33,12 +33,14 @@ struct TreeForm {
   bool tensor;
   int ctas, cuts, slots, slot_rows;
   int many_groups;   // rows form: from so many groups on, a share a warp
+  int whole;         // rows form: CTAs take whole groups, nothing is merged
   void shrink(int n) {
     cuts = cuts / ctas * n;
     ctas = n;
   }
 };
 TreeForm tree_form(bool tensor, int num_sms);
+constexpr int kWholeBlocks = 32;   // blocks of a group up to which it stays whole
 // tmk / tmv: the pool's block maps (rows form: 128-byte swizzle, unused by FP8
 // pools with head_dim 64); tmq: q viewed as [T][Hq][D] in boxes of one tile.
 // (launch_tree_rows also runs the attention over selected blocks.)

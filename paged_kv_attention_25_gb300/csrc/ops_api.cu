@@ -82,11 +82,13 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
   return a;
 }
 
-// Launches as many CTAs as `units` (an upper bound of the call's blocks or key
-// tiles) can occupy: 16 a CTA of the rows form, one of the tiles form (an even
-// number: quads go to pairs of CTAs).
-void fit_ctas(TreeArgs& a, int64_t units) {
-  const int64_t want = a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
+// Launches as many CTAs as `groups` groups of `blocks` blocks (key tiles) can
+// occupy, both upper bounds: 16 blocks a CTA of the rows form, a tile a CTA of the
+// tiles form (an even number: quads go to pairs of CTAs).
+void fit_ctas(TreeArgs& a, int64_t groups, int blocks) {
+  const int64_t units = groups * (static_cast<int64_t>(blocks) + 2);
+  a.form.whole = !a.form.tensor && blocks <= kWholeBlocks && groups <= a.form.ctas;
+  const int64_t want = a.form.whole ? groups : a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
   a.form.shrink(static_cast<int>(std::min<int64_t>(want < 2 ? 2 : want, a.form.ctas)));
   a.ctas = a.form.ctas;
 }
@@ -198,7 +200,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   // No more CTAs than the largest batch of these sizes can use.
   const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / (form.tensor ? kTcRows : 16) + num_reqs) *
                          pool->num_kv_heads;
-  fit_ctas(a, groups * (form.tensor ? static_cast<int64_t>(max_blocks) / 8 + 1 : max_blocks + 1) + groups);
+  fit_ctas(a, groups, form.tensor ? max_blocks / 8 + 1 : max_blocks);
   a.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   if (form.tensor) {
     CUtensorMap tmap_q;
@@ -209,6 +211,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
                       [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
   }
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree attention launch");
+  if (a.form.whole) return PKV_OK;
   rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree merge launch");
   return PKV_OK;
@@ -329,13 +332,14 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   a.num_tokens = num_tokens;
   a.sel = selected;
   a.top_k = top_k;
-  fit_ctas(a, static_cast<int64_t>(num_tokens) * pool->num_kv_heads * ((a.group + 15) / 16) * (static_cast<int64_t>(top_k) + 2));
+  fit_ctas(a, static_cast<int64_t>(num_tokens) * pool->num_kv_heads * ((a.group + 15) / 16), top_k);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o;
   a.lse = lse;
   rc = timed_launch(pool, 1, stream,
                     [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected attention launch");
+  if (a.form.whole) return PKV_OK;
   rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected merge launch");
   return PKV_OK;

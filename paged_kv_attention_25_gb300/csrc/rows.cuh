@@ -115,63 +115,75 @@ struct RowTile {
     odd = false;
   }
 
-  // One block: its K and V chunks at shared addresses kb and vb.  sl2: score
-  // scale times log2(e).  Masked: vis0 / vis1 hold the keys that rows g and
-  // g + 8 see.
-  template <int MASK>
-  __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, float sl2, uint32_t vis0, uint32_t vis1, int lane) {
+  // NB blocks: the first one's K and V chunks at shared addresses kb and vb, the
+  // second one's at kb1 and vb1.  sl2: score scale times log2(e).  Masked (one
+  // block): vis0 / vis1 hold the keys that rows g and g + 8 see.
+  template <int MASK, int NB = 1>
+  __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, float sl2, uint32_t vis0, uint32_t vis1, int lane,
+                                        uint32_t kb1 = 0, uint32_t vb1 = 0) {
+    static_assert(NB == 1 || MASK == kMaskNone, "masks are those of one block");
     const int g = lane >> 2, c = lane & 3;
-    float s[2][4];
+    float s[NB][2][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[n][t][0] = s[n][t][1] = s[n][t][2] = s[n][t][3] = 0.f;
     if constexpr (!F8) {
       // Lane l addresses line (l / 16) * 8 + l % 8, 16-byte chunk 2 s + (l / 8) % 2.
       const int r8 = lane & 7, key8 = lane >> 4, cx = (lane >> 3) & 1;
-      const uint32_t base = kb + key8 * (D / 64) * 1024 + r8 * 128;
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const int ch = 2 * st + cx;
-        uint32_t b0, b1, b2, b3;
-        ldsm4(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), b0, b1, b2, b3);
-        mma16<false>(s[0], q[st], b0, b1);
-        mma16<false>(s[1], q[st], b2, b3);
+      for (int n = 0; n < NB; ++n) {
+        const uint32_t base = (n ? kb1 : kb) + key8 * (D / 64) * 1024 + r8 * 128;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          const int ch = 2 * st + cx;
+          uint32_t b0, b1, b2, b3;
+          ldsm4(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), b0, b1, b2, b3);
+          mma16<false>(s[n][0], q[st], b0, b1);
+          mma16<false>(s[n][1], q[st], b2, b3);
+        }
       }
     } else {
       // Keys g and g + 8: D / 4 codes from dim (D / 4) c.
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int u = 0; u < D / 64; ++u) {
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) {
-          uint4 x;
-          ld_codes(kb, g + 8 * t, (D / 64) * c + u, x);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16x4(w[i], b0, b1);
-            mma16<true>(s[t], q[4 * u + i], b0, b1);
+          for (int t = 0; t < 2; ++t) {
+            uint4 x;
+            ld_codes(n ? kb1 : kb, g + 8 * t, (D / 64) * c + u, x);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16x4(w[i], b0, b1);
+              mma16<true>(s[n][t], q[4 * u + i], b0, b1);
+            }
           }
-        }
       }
     }
+    if constexpr (MASK != kMaskNone) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[t][e] *= sl2;
-        if constexpr (MASK != kMaskNone) {
+        for (int e = 0; e < 4; ++e) {
           const uint32_t v = e < 2 ? vis0 : vis1;
-          if (!((v >> (8 * t + 2 * c + (e & 1))) & 1u)) s[t][e] = -CUDART_INF_F;
+          if (!((v >> (8 * t + 2 * c + (e & 1))) & 1u)) s[0][t][e] = -CUDART_INF_F;
         }
-      }
-    float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+    }
+    float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mx0 = fmaxf(mx0, fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][1][0], s[n][1][1])));
+      mx1 = fmaxf(mx1, fmaxf(fmaxf(s[n][0][2], s[n][0][3]), fmaxf(s[n][1][2], s[n][1][3])));
+    }
 #pragma unroll
     for (int x = 1; x < 4; x <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
     }
-    const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
+    const float n0 = fmaxf(m[0], mx0 * sl2), n1 = fmaxf(m[1], mx1 * sl2);   // sl2 > 0
     if (__any_sync(0xffffffffu, n0 > m[0] || n1 > m[1])) {
       // A row's max grew: rescale (rows without a visible key so far keep m = -inf and o = 0).
       const float a0 = n0 == -CUDART_INF_F ? 1.f : fast_exp2(m[0] - n0);
@@ -186,23 +198,26 @@ struct RowTile {
       m[0] = n0;
       m[1] = n1;
     }
-    const float u0 = m[0] == -CUDART_INF_F ? 0.f : m[0], u1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+    const float u0 = m[0] == -CUDART_INF_F ? 0.f : -m[0], u1 = m[1] == -CUDART_INF_F ? 0.f : -m[1];
+    uint32_t p[NB][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t][0] = fast_exp2(s[t][0] - u0);
-      s[t][1] = fast_exp2(s[t][1] - u0);
-      s[t][2] = fast_exp2(s[t][2] - u1);
-      s[t][3] = fast_exp2(s[t][3] - u1);
-    }
-    l[0] += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-    l[1] += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
-    uint32_t p[4];
-    if constexpr (F8) {
-      p[0] = pack_f16x2(s[0][0], s[0][1]); p[1] = pack_f16x2(s[0][2], s[0][3]);
-      p[2] = pack_f16x2(s[1][0], s[1][1]); p[3] = pack_f16x2(s[1][2], s[1][3]);
-    } else {
-      p[0] = pack_bf16x2(s[0][0], s[0][1]); p[1] = pack_bf16x2(s[0][2], s[0][3]);
-      p[2] = pack_bf16x2(s[1][0], s[1][1]); p[3] = pack_bf16x2(s[1][2], s[1][3]);
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        s[n][t][0] = fast_exp2(fmaf(s[n][t][0], sl2, u0));
+        s[n][t][1] = fast_exp2(fmaf(s[n][t][1], sl2, u0));
+        s[n][t][2] = fast_exp2(fmaf(s[n][t][2], sl2, u1));
+        s[n][t][3] = fast_exp2(fmaf(s[n][t][3], sl2, u1));
+        if constexpr (F8) {
+          p[n][2 * t] = pack_f16x2(s[n][t][0], s[n][t][1]);
+          p[n][2 * t + 1] = pack_f16x2(s[n][t][2], s[n][t][3]);
+        } else {
+          p[n][2 * t] = pack_bf16x2(s[n][t][0], s[n][t][1]);
+          p[n][2 * t + 1] = pack_bf16x2(s[n][t][2], s[n][t][3]);
+        }
+      }
+      l[0] += (s[n][0][0] + s[n][0][1]) + (s[n][1][0] + s[n][1][1]);
+      l[1] += (s[n][0][2] + s[n][0][3]) + (s[n][1][2] + s[n][1][3]);
     }
     // kMaskKeys: the halves of b0 / b1 that hold seen keys (2c, 2c + 1 and 2c + 8, 2c + 9).
     uint32_t k01 = 0xffffffffu, k89 = 0xffffffffu;
@@ -214,56 +229,62 @@ struct RowTile {
     if constexpr (!F8) {
       // Lane l addresses line ((l / 8) % 2) * 8 + l % 8, chunk j + l / 16; transposed on the way.
       const int r8 = lane & 7, key8 = (lane >> 3) & 1, cx = lane >> 4;
-      const uint32_t base = vb + key8 * (D / 64) * 1024 + r8 * 128;
 #pragma unroll
-      for (int j = 0; j < kTiles; j += 2) {
-        const int ch = j + cx;
-        uint32_t b0, b1, b2, b3;
-        ldsm4_t(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), b0, b1, b2, b3);
-        if constexpr (MASK == kMaskRows) {
-          b0 = finite_pair<false>(b0, odd); b1 = finite_pair<false>(b1, odd);
-          b2 = finite_pair<false>(b2, odd); b3 = finite_pair<false>(b3, odd);
-        } else if constexpr (MASK == kMaskKeys) {
-          b0 &= k01; b1 &= k89;
-          b2 &= k01; b3 &= k89;
+      for (int n = 0; n < NB; ++n) {
+        const uint32_t base = (n ? vb1 : vb) + key8 * (D / 64) * 1024 + r8 * 128;
+#pragma unroll
+        for (int j = 0; j < kTiles; j += 2) {
+          const int ch = j + cx;
+          uint32_t b0, b1, b2, b3;
+          ldsm4_t(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), b0, b1, b2, b3);
+          if constexpr (MASK == kMaskRows) {
+            b0 = finite_pair<false>(b0, odd); b1 = finite_pair<false>(b1, odd);
+            b2 = finite_pair<false>(b2, odd); b3 = finite_pair<false>(b3, odd);
+          } else if constexpr (MASK == kMaskKeys) {
+            b0 &= k01; b1 &= k89;
+            b2 &= k01; b3 &= k89;
+          }
+          mma16<false>(o[j], p[n], b0, b1);
+          mma16<false>(o[j + 1], p[n], b2, b3);
         }
-        mma16<false>(o[j], p, b0, b1);
-        mma16<false>(o[j + 1], p, b2, b3);
       }
     } else {
       // Keys 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 codes from dim (D / 8) g; a byte
       // permute pairs two keys' codes of one dim before the conversion.
-      uint32_t v[4][D / 32];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = 2 * c + (k & 1) + 8 * (k >> 1);
-        if constexpr (D == 128) {
-          uint4 x;
-          ld_codes(vb, key, g, x);
-          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-        } else {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1])
-                       : "r"(vb + key * D + 8 * g) : "memory");
-        }
-      }
+      for (int n = 0; n < NB; ++n) {
+        uint32_t v[4][D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {   // word i: n-tiles 4 i .. 4 i + 3
-        const uint32_t x01 = __byte_perm(v[0][i], v[1][i], 0x5140), y01 = __byte_perm(v[0][i], v[1][i], 0x7362);
-        const uint32_t x89 = __byte_perm(v[2][i], v[3][i], 0x5140), y89 = __byte_perm(v[2][i], v[3][i], 0x7362);
-        uint32_t b[8];
-        e4m3x4_to_f16x4(x01, b[0], b[2]);
-        e4m3x4_to_f16x4(x89, b[1], b[3]);
-        e4m3x4_to_f16x4(y01, b[4], b[6]);
-        e4m3x4_to_f16x4(y89, b[5], b[7]);
-        if constexpr (MASK == kMaskRows) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) b[e] = finite_pair<true>(b[e], odd);
-        } else if constexpr (MASK == kMaskKeys) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) b[e] &= (e & 1) ? k89 : k01;
+        for (int k = 0; k < 4; ++k) {
+          const int key = 2 * c + (k & 1) + 8 * (k >> 1);
+          if constexpr (D == 128) {
+            uint4 x;
+            ld_codes(n ? vb1 : vb, key, g, x);
+            v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+          } else {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1])
+                         : "r"((n ? vb1 : vb) + key * D + 8 * g) : "memory");
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mma16<true>(o[4 * i + e], p, b[2 * e], b[2 * e + 1]);
+        for (int i = 0; i < D / 32; ++i) {   // word i: n-tiles 4 i .. 4 i + 3
+          const uint32_t x01 = __byte_perm(v[0][i], v[1][i], 0x5140), y01 = __byte_perm(v[0][i], v[1][i], 0x7362);
+          const uint32_t x89 = __byte_perm(v[2][i], v[3][i], 0x5140), y89 = __byte_perm(v[2][i], v[3][i], 0x7362);
+          uint32_t b[8];
+          e4m3x4_to_f16x4(x01, b[0], b[2]);
+          e4m3x4_to_f16x4(x89, b[1], b[3]);
+          e4m3x4_to_f16x4(y01, b[4], b[6]);
+          e4m3x4_to_f16x4(y89, b[5], b[7]);
+          if constexpr (MASK == kMaskRows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = finite_pair<true>(b[e], odd);
+          } else if constexpr (MASK == kMaskKeys) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] &= (e & 1) ? k89 : k01;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma16<true>(o[4 * i + e], p[n], b[2 * e], b[2 * e + 1]);
+        }
       }
     }
   }

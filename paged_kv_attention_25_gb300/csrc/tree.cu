@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <cstdint>
+
 #include "internal.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -34,6 +36,9 @@ constexpr int kRowsThreads = 32 * kRowWarps;
 //   few groups    a worker is a CTA, whose four warps take a segment's blocks in
 //                 turn and merge their states in shared memory: a quarter of the
 //                 partials of long groups.
+// Where no group can have more than kWholeBlocks blocks and there are no more
+// groups than CTAs, CTAs take whole groups and there is nothing to merge: one launch less (one request, 28 rows, 15
+// blocks: 11 us and two launches against 8 and one).
 constexpr int kGroupUnits = 2;
 using RowsShare = Share<4 * kRowWarps>;   // few groups: four blocks a warp at least
 using WarpShare = Share<4>;
@@ -99,7 +104,37 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   const int warp_id = static_cast<int>(blockIdx.x) * kRowWarps + warp, many_from = a.form.many_groups;
   TreeShare sh;
   bool solo;
-  if constexpr (LIST) {
+  int64_t left = 0;   // whole groups: how many the CTA still has to do
+  if (a.form.whole) {
+    int64_t n[1], off[1];
+    int reqs[1];
+    auto share = [&](int64_t len, int64_t& first) {
+      const int C = static_cast<int>(min(len, static_cast<int64_t>(a.ctas)));
+      const bool has = static_cast<int>(blockIdx.x) < C;
+      first = has ? RowsShare::begin(len, C, blockIdx.x) : 0;
+      left = has ? RowsShare::begin(len, C, blockIdx.x + 1) - first : 0;
+    };
+    sh = TreeShare{0, 0, 0, 0, 1, 0};
+    solo = false;
+    int64_t first;
+    if constexpr (LIST) {
+      const int tokens = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
+      share(static_cast<int64_t>(tokens) * Hkv * rtiles, first);
+      sh.u = first * (a.top_k + kGroupUnits);
+    } else {
+      tree_scan<kRowsThreads, 1, 1>(
+          a, scratch, n, reqs, off, [&](const TreeReq& q, int) { return groups(q); },
+          [&](const int64_t (&len)[1], int, int& line, int64_t& unit) {
+            share(len[0], first);
+            line = 0;
+            unit = left > 0 ? first : -1;
+          });
+      sh.req = reqs[0];
+      if (left > 0) sh.off = off[0] * (rows_blocks(tree_req(a, sh.req)) + kGroupUnits);
+    }
+    sh.end = left > 0 ? INT64_MAX : 0;
+    if (left == 0) sh.u = 0;
+  } else if constexpr (LIST) {
     // Every token of the requests has top_k units a group.
     const int tokens = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
     const int64_t n = static_cast<int64_t>(tokens) * Hkv * rtiles;
@@ -156,7 +191,8 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   int req = LIST ? 0 : sh.req;
   TreeReq rq{0, 0, 0, 0, false};
   if constexpr (!LIST) rq = tree_req(a, req);
-  while (sh.u < sh.end) {
+  for (; sh.u < sh.end; ) {
+    if (a.form.whole && left-- <= 0) return;
     int kblk, x, g, row0, nrows, pos = 0;   // blocks of the group, its first unit here, its rows
     const int32_t* list = nullptr;
     if constexpr (LIST) {
@@ -252,6 +288,12 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
     const uint32_t* m0 = LIST ? nullptr : mask_row(ra);
     const uint32_t* m1 = LIST ? nullptr : mask_row(rb);
     bool ok = true;
+    // Keys of the warp's iteration i that the rows see: whole blocks, or masked ones.
+    auto whole_block = [&](int i) -> bool {   // there, and seen whole by every row
+      if (__shfl_sync(0xffffffffu, ids_cur, i & 31) < 0) return false;
+      if constexpr (LIST) return pos - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1 >= kBlockSize;
+      else return (b0 + wi + wn * i + 1) * kBlockSize <= rq.prefix;
+    };
     for (int i = 0; i < nb_w; ++i) {
       if ((i & 31) == 0 && i > 0) {
         ids_cur = ids_next;
@@ -262,21 +304,30 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
       const int st = (cnt + i) % S::kStages;
       if (!(ok = mbar_wait_warp(&my_bars[st], ((cnt + i) / S::kStages) & 1, s_abort, a.wait_ns))) break;
       const uint32_t kb = my_addr + st * S::kStage;
-      if (__shfl_sync(0xffffffffu, ids_cur, i & 31) >= 0) {
+      const bool plain = whole_block(i);
+      if (F8 && plain && (i & 31) != 31 && i + 1 < nb_w && whole_block(i + 1)) {
+        // FP8: two blocks at once.  Half the shuffles and votes, and two chains of products and conversions to
+        // interleave (the warps waited for fixed latencies most of the time): 100 -> 9x us for FP8 trees.
+        const int st1 = (cnt + i + 1) % S::kStages;
+        if (!(ok = mbar_wait_warp(&my_bars[st1], ((cnt + i + 1) / S::kStages) & 1, s_abort, a.wait_ns))) break;
+        const uint32_t kb1 = my_addr + st1 * S::kStage;
+        rt.template block<kMaskNone, 2>(kb, kb + S::kChunk, sl2, 0u, 0u, lane, kb1, kb1 + S::kChunk);
+        ++i;
+        __syncwarp();
+        if (issued < nb_w) {
+          issue(issued);
+          ++issued;
+        }
+      } else if (plain) {
+        rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
+      } else if (__shfl_sync(0xffffffffu, ids_cur, i & 31) >= 0) {
         if constexpr (LIST) {
           const int seen = pos - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1;   // keys up to the position
-          if (seen >= kBlockSize)
-            rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
-          else
-            rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
+          rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
         } else {
           const int key0 = (b0 + wi + wn * i) * kBlockSize;
-          if (key0 + kBlockSize <= rq.prefix)
-            rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
-          else
-            rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2,
-                                         tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
-                                         tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
+          rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
+                                       tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
         }
       }
       __syncwarp();
@@ -552,6 +603,7 @@ TreeForm tree_form(bool tensor, int num_sms) {
   f.slot_rows = tensor ? 256 : kRowTile;
   f.slots = 2 * f.cuts;
   f.many_groups = f.ctas / 2;
+  f.whole = 0;
   return f;
 }
 
