@@ -84,10 +84,14 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
 
 // Launches as many CTAs as `groups` groups of `blocks` blocks (key tiles) can
 // occupy, both upper bounds: 16 blocks a CTA of the rows form, a tile a CTA of the
-// tiles form (an even number: quads go to pairs of CTAs).
-void fit_ctas(TreeArgs& a, int64_t groups, int blocks) {
+// tiles form (an even number: quads go to pairs of CTAs).  Whole groups, a CTA
+// each, need no merge: taken where groups are short (kWholeBlocks), and for lists,
+// which are all equally long, where there are enough of them to keep the memory
+// busy (256 groups of 128 blocks: 91 us for selection and attention with shares,
+// 8x with whole groups).
+void fit_ctas(TreeArgs& a, int64_t groups, int blocks, int num_sms) {
   const int64_t units = groups * (static_cast<int64_t>(blocks) + 2);
-  a.form.whole = !a.form.tensor && blocks <= kWholeBlocks && groups <= a.form.ctas;
+  a.form.whole = !a.form.tensor && groups <= a.form.ctas && (blocks <= kWholeBlocks || (a.sel && groups >= num_sms));
   const int64_t want = a.form.whole ? groups : a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
   a.form.shrink(static_cast<int>(std::min<int64_t>(want < 2 ? 2 : want, a.form.ctas)));
   a.ctas = a.form.ctas;
@@ -200,7 +204,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   // No more CTAs than the largest batch of these sizes can use.
   const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / (form.tensor ? kTcRows : 16) + num_reqs) *
                          pool->num_kv_heads;
-  fit_ctas(a, groups, form.tensor ? max_blocks / 8 + 1 : max_blocks);
+  fit_ctas(a, groups, form.tensor ? max_blocks / 8 + 1 : max_blocks, pool->num_sms);
   a.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   if (form.tensor) {
     CUtensorMap tmap_q;
@@ -332,7 +336,7 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   a.num_tokens = num_tokens;
   a.sel = selected;
   a.top_k = top_k;
-  fit_ctas(a, static_cast<int64_t>(num_tokens) * pool->num_kv_heads * ((a.group + 15) / 16), top_k);
+  fit_ctas(a, static_cast<int64_t>(num_tokens) * pool->num_kv_heads * ((a.group + 15) / 16), top_k, pool->num_sms);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o;
   a.lse = lse;
