@@ -367,7 +367,8 @@ int pkv_tree_mask(pkv_pool* pool, const int32_t* parents, const int32_t* cu_q_le
  * given positions (the arguments of pkv_append, plus ctx_lens: keys at or
  * beyond ctx_lens[r] are not counted).  Call it after the append with the same
  * positions; after a swap-in with one position per block.  Tokens that share
- * a block with the token before them cost nothing.
+ * a block with the token before them cost nothing.  A block that two of the
+ * requests hold must be full for both (their bounds are then the same).
  */
 int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
                   const int32_t* positions, const int32_t* ctx_lens, int num_tokens, int8_t* codes, int8_t* exps,
@@ -389,7 +390,8 @@ int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, i
  * inputs alone, not on the order of any sum.
  * Rows of tokens that belong to no request are left as they are.  A block
  * without a valid pool block is flagged and not selected; a position outside
- * the table is flagged and selects nothing.  num_kv_heads <= 256.  workspace:
+ * the table is flagged and selects nothing.  1 <= top_k <= 2^27 (it may exceed
+ * the table), num_kv_heads <= 256.  workspace:
  * pkv_select_blocks_workspace_size() bytes for the same sizes (the scores of up
  * to 64 MB of tokens at a time), 256-byte aligned, used by one call at a time as
  * for pkv_tree_attn.
@@ -402,8 +404,8 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
 
 /*
  * Attention of each query token over the keys j <= p of its selected blocks
- * (formulas and rounding as above; blocks of one list must be distinct, in any
- * order; entries below 0 and blocks behind the token are skipped, an entry beyond
+ * (formulas and rounding as above; all keys of a block up to p have been
+ * written; blocks of one list must be distinct, in any order; entries below 0 and blocks behind the token are skipped, an entry beyond
  * the table is flagged and skipped).  A list without a key gives O = 0,
  * LSE = -inf.  workspace: pkv_sparse_attn_workspace_size() bytes (a constant of
  * the pool), 256-byte aligned, used by one call at a time as for pkv_tree_attn.
@@ -591,7 +593,8 @@ int pkv_check_device_errors(pkv_pool* pool, void* stream, unsigned* flags);
  *     (tensor-core) kernel never issues its first K copy, so that the wait for
  *     it runs out: the kernel records PKV_DEVERR_TIMEOUT, drains its copies,
  *     frees what it holds and returns, and that call's outputs are undefined;
- *     0 = off (default);
+ *     0 = off (default).  1 (2) acts on the rows (tiles) form of pkv_tree_attn
+ *     in the same way, 1 on pkv_sparse_attn;
  *   PKV_DEBUG_FUSED_FORM: how pkv_append_paged_attn appends: 0 = chosen per
  *     batch (default), 1 = inside the attention launches whenever the pool
  *     allows it, 2 = the append kernel first.  Every form gives the same pool

@@ -1,12 +1,15 @@
 // C entry points of the operators beside the causal paged attention: tree
 // attention, block-selected attention, pages.  Their lengths, tables and masks
 // are read on the device alone, so that the calls can be captured in a graph;
-// they take no lock, keep nothing from one call for the next, and run on the
-// caller's stream.
+// they keep nothing from one call for the next and run on the caller's stream.
+// A call of several kernels holds the pool's lock while it launches them, so that
+// calls from two threads on one stream, which may share a workspace, follow one
+// another.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "internal.h"
 #include "ops.h"
@@ -54,6 +57,10 @@ int check_scale(float scale) {
   return scale > 0.f && scale <= 3.4e38f ? PKV_OK : fail(PKV_EINVAL, "scale must be positive and finite");
 }
 
+int check_top_k(int top_k) {
+  return top_k >= 1 && top_k <= (1 << 27) ? PKV_OK : fail(PKV_EINVAL, "top_k must be in 1 .. 2^27");
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct TreeWs {
@@ -79,6 +86,7 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
   a.form = f;
   a.ctas = f.ctas;
   a.wait_ns = pool->wait_ns;
+  a.withhold = pool->withhold;
   return a;
 }
 
@@ -88,7 +96,7 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
 // each, need no merge: taken where groups are short (kWholeBlocks), and for lists,
 // which are all equally long, where there are enough of them to keep the memory
 // busy (256 groups of 128 blocks: 91 us for selection and attention with shares,
-// 8x with whole groups).
+// 85 with whole groups).
 void fit_ctas(TreeArgs& a, int64_t groups, int blocks, int num_sms) {
   const int64_t units = groups * (static_cast<int64_t>(blocks) + 2);
   a.form.whole = !a.form.tensor && groups <= a.form.ctas && (blocks <= kWholeBlocks || (a.sel && groups >= num_sms));
@@ -184,6 +192,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
   if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_tree_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
   if ((rc = finish_swap_in(pool, stream))) return rc;
+  std::lock_guard<std::mutex> lk(pool->mu);
   TreeArgs a = tree_args(pool, form, w, workspace);
   a.q = q;
   a.num_q_heads = num_q_heads;
@@ -264,7 +273,8 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
   int rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
-  if (top_k < 1 || sinks < 0 || recent < 0) return fail(PKV_EINVAL, "need top_k >= 1, sinks >= 0, recent >= 0");
+  if ((rc = check_top_k(top_k))) return rc;
+  if (sinks < 0 || recent < 0) return fail(PKV_EINVAL, "need sinks >= 0, recent >= 0");
   if (num_tokens == 0) return PKV_OK;
   if ((rc = check_heads(pool, num_q_heads))) return rc;
   if (pool->num_kv_heads > kSelectMaxHeads)
@@ -294,6 +304,7 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
   a.sinks = std::min(sinks, max_blocks);
   a.recent = std::min(recent, max_blocks);
   a.num_sms = pool->num_sms;
+  std::lock_guard<std::mutex> lk(pool->mu);
   a.keys = static_cast<uint32_t*>(workspace);
   a.tok_most = select_part(num_tokens, max_blocks, pool->num_kv_heads);
   rc = timed_launch(pool, 0, stream, [&] { return launch_select(a, stream); });
@@ -314,7 +325,7 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
   int rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
-  if (top_k < 1) return fail(PKV_EINVAL, "top_k must be >= 1");
+  if ((rc = check_top_k(top_k))) return rc;
   if (num_tokens == 0) return PKV_OK;
   if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
   if (!q || !q_positions || !block_tables || !cu_q_lens || !selected || !o) return fail(PKV_EINVAL, "NULL device pointer");
@@ -324,6 +335,7 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_sparse_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
   if ((rc = finish_swap_in(pool, stream))) return rc;
+  std::lock_guard<std::mutex> lk(pool->mu);
   TreeArgs a = tree_args(pool, form, w, workspace);
   a.q = q;
   a.num_q_heads = num_q_heads;
@@ -382,6 +394,7 @@ int pkv_fork(pkv_pool* pool, const int32_t* tables, int num_rows, int max_blocks
   DeviceGuard guard(pool->device);
   int rc = finish_swap_in(pool, stream);
   if (rc) return rc;
+  std::lock_guard<std::mutex> lk(pool->mu);
   ForkArgs a{pool->view(), pool->k, pool->v, tables, num_rows, max_blocks, lens, caps, parents, new_caps, num_children,
              new_tables, refs, new_refs, codes, exps, static_cast<int32_t*>(workspace), pool->num_sms};
   rc = timed_launch(pool, 0, stream, [&] { return launch_fork(a, stream); });

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
 // for every (token, block, head); pick_kernel finds each (token, head)'s
 // threshold and writes its list.  (One kernel a (token, head), clusters or not,
 // left the memory idle while it looked for thresholds and took as long as the
-// longest context on the fullest SM: 35 us against 2x for 32 requests of 9 to 32
+// longest context on the fullest SM: 35 us against 30 for 32 requests of 9 to 32
 // thousand tokens.)
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;

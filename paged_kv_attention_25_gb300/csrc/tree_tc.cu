@@ -440,6 +440,8 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
           const int st = cnt % nst;
           const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
           if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
+          // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
+          if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
           const bool clean = !is_k && needs_clean(j, have);
           uint64_t* bar = &bars[(clean ? bar_landed : bar_full) + st];
           if (lane == 0)
@@ -479,9 +481,10 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
             const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
             have_ring = (have_ring & ~(0xffu << (8 * st))) | (have << (8 * st));
             uint64_t* bar = &bars[bar_landed + st];
-            if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D));
+            const bool withheld = a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0;   // test hook (above)
+            if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D));
             __syncwarp();
-            if (y >= 0)
+            if (y >= 0 && !withheld)
               tma_load_2d(stages + st * S::kKV + S::kKV / 2 + lane * (kBlockSize * D), tm, 0, y * kBlockSize, bar);
             ++cnt;
             ++jl;

@@ -351,3 +351,81 @@ def test_drafting_step_end_to_end():
                     ref.assert_close(oo[:, g * 4:g * 4 + 4].float().cpu().numpy().reshape(-1, d), want, to, "O")
                     ref.assert_close(ll[:, g * 4:g * 4 + 4].cpu().numpy().reshape(-1), wl, tl, "LSE")
     assert pkv.pkv_check_device_errors(pool) == 0
+
+
+def test_refusals():
+    w = World(13, 32)
+    w.step([-1, -1], [20, 30])
+    t = ref.dev
+    tables, lens, caps, refs = t(w.tables), t(w.lens), t(w.caps), t(w.refs)
+    one = t(np.array([0], np.int32))
+    with pytest.raises(pkv.PkvError, match="overlap"):
+        pkv.pkv_fork(w.pool, tables, lens, caps, t(np.array([0, 1], np.int32)), t(np.array([30, 30], np.int32)), refs,
+                     out_tables=tables)
+    with pytest.raises(pkv.PkvError, match="workspace"):
+        pkv.pkv_fork(w.pool, tables, lens, caps, one, one, refs, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    for kw in (dict(lens=lens[:1]), dict(refs=refs[:5].contiguous()), dict(new_caps=t(np.zeros(2, np.int32)))):
+        args = dict(tables=tables, lens=lens, caps=caps, parents=one, new_caps=one, refs=refs)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            pkv.pkv_fork(w.pool, **args)
+    with pytest.raises(TypeError):
+        pkv.pkv_fork(w.pool, tables.long(), lens, caps, one, one, refs)
+    with pytest.raises(ValueError):
+        pkv.pkv_copy_blocks(w.pool, one, t(np.zeros(2, np.int32)))
+    with pytest.raises(ValueError):
+        pkv.pkv_compact(w.pool, tables, one, one, one)
+    lib = pkv.load_library()
+    p = refs.data_ptr()
+    assert lib.pkv_copy_blocks(w.pool.handle, p, p, 1, p, None, None) == pkv.PKV_EINVAL      # half a summary
+    assert lib.pkv_copy_blocks(w.pool.handle, p, None, 1, None, None, None) == pkv.PKV_EINVAL
+    assert lib.pkv_copy_blocks(w.pool.handle, p, p, -1, None, None, None) == pkv.PKV_EINVAL
+    assert lib.pkv_compact(w.pool.handle, p, 1 << 28, 1, p, p, p, 1, None) == pkv.PKV_EINVAL
+    assert np.array_equal(refs.cpu().numpy(), w.refs)
+
+
+def test_nothing_to_do():
+    w = World(14, 32)
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    pkv.pkv_copy_blocks(w.pool, e, e)
+    pkv.pkv_compact(w.pool, e.view(0, 3), torch.zeros(1, dtype=torch.int32, device="cuda"), e, e)
+    assert pkv.pkv_check_device_errors(w.pool) == 0
+
+
+def test_rows_around_the_limit_of_the_small_kernel():
+    for rows, kids in ((1024, 1024), (1025, 3), (3, 1025), (1024, 1)):
+        w = World(rows + kids, 6000, hkv=1, width=6)
+        w.step([-1] * rows, w.rng.integers(1, 33, rows))
+        w.grow(w.rng.integers(0, 33, rows))
+        parents = w.rng.integers(-1, rows, kids)
+        w.step(parents, w.rng.integers(1, 50, kids), in_place=False)
+
+
+def test_pages_beyond_4_gb():
+    nb = 600_000
+    pool = pkv.Pool(nb, 2, 128)
+    pool.k[-40:] = torch.randn((40, 2, 16, 128), device="cuda").to(torch.bfloat16)
+    pool.v[-40:] = torch.randn((40, 2, 16, 128), device="cuda").to(torch.bfloat16)
+    k, v = pool.k[-40:].clone(), pool.v[-40:].clone()
+    refs = torch.ones(nb, dtype=torch.int32, device="cuda")
+    refs[-30:] = 0                                           # the free pages are the last thirty
+    base = nb - 40
+    bt = np.array([[base, base + 1, -1]], np.int32)
+    args = [bt, np.array([20], np.int32), np.array([32], np.int32), np.array([0, 0], np.int32), np.array([33, 33], np.int32)]
+    want, want_refs, moves, short = fork_ref(*args, refs.cpu().numpy())
+    assert want.tolist() == [[base, base + 1, base + 10], [base, base + 11, base + 12]] and not short
+    assert moves == [(base + 1, base + 11, 4)]
+    two, _ = pkv.pkv_fork(pool, *(ref.dev(x) for x in args), refs)
+    assert np.array_equal(two.cpu().numpy(), want) and np.array_equal(refs.cpu().numpy(), want_refs)
+    k[11, :, :4], v[11, :, :4] = k[1, :, :4], v[1, :, :4]
+    pkv.pkv_copy_blocks(pool, ref.dev(np.array([base + 3], np.int32)), ref.dev(np.array([base + 20], np.int32)))
+    k[20], v[20] = k[3], v[3]
+    pkv.pkv_compact(pool, ref.dev(want[1:]), ref.dev(np.array([0, 2], np.int32)), ref.dev(np.array([19, 33], np.int32)),
+                    ref.dev(np.array([16], np.int32)))
+    for x in (k, v):
+        a, b = x[11, :, 3].clone(), x[12, :, 1].clone()
+        x[11, :, 0], x[11, :, 1] = a, b
+    torch.cuda.synchronize()
+    assert torch.equal(pool.k[-40:], k) and torch.equal(pool.v[-40:], v)
+    assert pkv.pkv_check_device_errors(pool) == 0
+    pool.close()

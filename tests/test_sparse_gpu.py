@@ -338,3 +338,110 @@ def test_all_blocks_selected_equals_the_causal_attention():
     po, pl = pkv.pkv_paged_attn(c.pool, c.q, ref.dev(c.pos), ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.cu), meta, c.scale)
     torch.cuda.synchronize()
     c.check_attend(sel, po, pl)
+
+
+def test_wait_that_runs_out_is_reported_and_the_pool_recovers():
+    c = Case(43, [(2000, [1999]), (700, [699])], 8, 2, 128)
+    c.summarize()
+    sel = c.select(48, 1, 1)
+    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 2_000_000)
+    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WITHHOLD_COPY, 1)
+    c.attend(sel)
+    assert pkv.pkv_check_device_errors(c.pool) & pkv.PKV_DEVERR_TIMEOUT
+    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WITHHOLD_COPY, 0)
+    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
+    o, lse = c.attend(sel)
+    c.check_attend(sel, o, lse)
+
+
+def test_refusals():
+    c = Case(44, [(100, [99])], 8, 2, 64)
+    pos, bt, cu = ref.dev(c.pos), ref.dev(c.bt), ref.dev(c.cu)
+    sel = c.select(4, 1, 1)
+    with pytest.raises(ValueError):
+        c.select(0, 1, 1)
+    for sinks, recent in ((-1, 0), (0, -1)):
+        with pytest.raises(pkv.PkvError) as e:
+            c.select(4, sinks, recent)
+        assert e.value.code == pkv.PKV_EINVAL
+    p, lib = c.q.data_ptr(), pkv.load_library()
+    for k in (0, -1, (1 << 27) + 1):
+        assert lib.pkv_select_blocks(c.pool.handle, p, 8, p, p, 7, p, 1, 1, p, p, k, 1, 1, p, p, 1 << 30, None) == pkv.PKV_EINVAL
+        assert lib.pkv_sparse_attn(c.pool.handle, p, 8, p, p, 7, p, 1, 1, p, k, 0.1, p, None, p, 1 << 30, None) == pkv.PKV_EINVAL
+    c.scale = 0.0
+    with pytest.raises(pkv.PkvError, match="scale"):
+        c.attend(sel)
+    c.scale = 0.1
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pkv.PkvError, match="workspace"):
+        c.attend(sel, workspace=small)
+    with pytest.raises(ValueError):
+        pkv.BlockSummary(c.pool, codes=c.sum.codes)
+    with pytest.raises(ValueError):
+        pkv.BlockSummary(c.pool, c.sum.codes[:, :1].contiguous(), c.sum.exps)
+    with pytest.raises(TypeError):
+        pkv.BlockSummary(c.pool, c.sum.codes.float(), c.sum.exps)
+    for kw in (dict(q_positions=ref.dev(np.zeros(2, np.int32))), dict(block_tables=torch.cat([bt, bt])),
+               dict(selected=sel[:, :1].contiguous())):
+        args = dict(q_positions=pos, block_tables=bt, cu_q_lens=cu, selected=sel)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            pkv.pkv_sparse_attn(c.pool, c.q, scale=0.1, **args)
+    heads = pkv.Pool(2, 300, 64)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.pkv_select_blocks(heads, pkv.BlockSummary(heads), torch.zeros((1, 300, 64), dtype=torch.bfloat16, device="cuda"),
+                              pos, bt, cu, 2)
+    assert e.value.code == pkv.PKV_EUNSUPPORTED
+
+
+def test_no_tokens_is_nothing_to_do():
+    c = Case(45, [(100, [99])], 8, 2, 64)
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.pkv_summarize(c.pool, c.sum, e.view(0, 3), zero, e, e)
+    sel = pkv.pkv_select_blocks(c.pool, c.sum, c.q[:0], e, e.view(0, 3), zero, 5)
+    o, lse = pkv.pkv_sparse_attn(c.pool, c.q[:0], e, e.view(0, 3), zero, sel, 0.1)
+    assert sel.shape == (0, 2, 5) and o.shape == (0, 8, 64) and lse.shape == (0, 8)
+    assert pkv.pkv_check_device_errors(c.pool) == 0
+
+
+def test_tokens_in_parts():
+    """More tokens than the workspace holds the scores of at a time."""
+    c = Case(46, [(300, list(range(100, 300)))], 2, 2, 64, width=100_000)     # 80 tokens a part
+    c.bt[:, 19:] = -1
+    c.whole(6, 1, 1)
+
+
+def test_heads_that_fill_no_octet():
+    for hkv in (3, 5, 7, 9, 12, 20):
+        Case(hkv, [(700, [699]), (90, [89, 5])], hkv * 2, hkv, 64 if hkv % 2 else 128).whole(9, 1, 1)
+
+
+def test_many_groups_and_long_lists():
+    rng = np.random.default_rng(47)
+    reqs = [(int(n), [int(n) - 1]) for n in rng.integers(600, 2500, 70)]
+    Case(47, reqs, 16, 8, 64, "fp8_e4m3").whole(40, 1, 1)        # a share a warp
+    Case(48, reqs[:25], 16, 8, 64).whole(40, 1, 1)               # a CTA a group
+    Case(49, reqs[:3], 16, 8, 128).whole(90, 1, 1)               # shares of CTAs
+
+
+def test_blocks_beyond_4_gb():
+    c = Case(50, [(700, [699]), (40, [20])], 8, 2, 128)
+    nb, small = 600_000, c.pool
+    pool = pkv.Pool(nb, 2, 128)
+    pool.k[nb - small.num_blocks:] = small.k
+    pool.v[nb - small.num_blocks:] = small.v
+    low, low_bt = c.sum, c.bt
+    c.pool, c.sum = pool, pkv.BlockSummary(pool)
+    c.bt = np.where(c.bt >= 0, c.bt + nb - small.num_blocks, -1).astype(np.int32)
+    c.summarize()
+    sel = c.select(11, 1, 1)
+    o, lse = c.attend(sel)
+    torch.cuda.synchronize()
+    assert pkv.pkv_check_device_errors(pool) == 0
+    tail = pkv.BlockSummary(small, c.sum.codes[nb - small.num_blocks:].contiguous(), c.sum.exps[nb - small.num_blocks:].contiguous())
+    c.pool, c.sum, c.bt = small, tail, low_bt
+    c.check_bounds()
+    c.check_select(sel, 11, 1, 1)
+    c.check_attend(sel, o, lse)
+    pool.close()

@@ -279,3 +279,140 @@ def test_mask_from_parents(words):
     pkv.pkv_tree_mask(pool, ref.dev(parents), ref.dev(cu), out=out)
     torch.cuda.synchronize()
     assert pkv.pkv_check_device_errors(pool) == pkv.PKV_DEVERR_POSITION
+
+
+def test_wait_that_runs_out_is_reported_and_the_pool_recovers():
+    for dtype in ("bf16", "fp8_e4m3"):
+        c = Case(30, [(3000, 20), (500, 33), (40, 3)], 8, 2, 128, dtype)
+        pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 2_000_000)
+        pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WITHHOLD_COPY, Case.form)
+        c.run()
+        assert pkv.pkv_check_device_errors(c.pool) & pkv.PKV_DEVERR_TIMEOUT
+        pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WITHHOLD_COPY, 0)
+        pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
+        c.run_check()
+
+
+def test_refusals():
+    c = Case(31, [(20, 5)], 8, 2, 64)
+    bt, ctx, pre, cu, mask = ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.prefix), ref.dev(c.cu), c.mask()
+
+    def call(q=c.q, bt=bt, ctx=ctx, pre=pre, cu=cu, mask=mask, scale=0.1, **kw):
+        return pkv.pkv_tree_attn(c.pool, q, bt, ctx, pre, cu, mask, scale, **kw)
+
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(pkv.PkvError) as e:
+            call(scale=scale)
+        assert e.value.code == pkv.PKV_EINVAL
+    odd = torch.zeros(c.q.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view(c.q.shape)
+    for kw in (dict(q=odd), dict(out=odd)):
+        with pytest.raises(pkv.PkvError, match="aligned"):
+            call(**kw)
+    with pytest.raises(pkv.PkvError, match="workspace"):
+        call(workspace=torch.empty(512, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(pkv.PkvError, match="aligned"):
+        n = pkv.pkv_tree_attn_workspace_size(c.pool, 8, c.bt.shape[1], 1, c.T)
+        call(workspace=torch.empty(n + 512, dtype=torch.uint8, device="cuda")[8:])
+    q3 = torch.zeros((c.T, 3, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(pkv.PkvError, match="multiple"):
+        call(q=q3)
+    with pytest.raises(pkv.PkvError) as e:
+        call(q=torch.zeros((c.T, 2 * 129, 64), dtype=torch.bfloat16, device="cuda"))
+    assert e.value.code == pkv.PKV_EUNSUPPORTED
+    with pytest.raises(TypeError):
+        call(q=c.q.float())
+    with pytest.raises(TypeError):
+        call(q=torch.zeros((c.T, 64, 8), dtype=torch.bfloat16, device="cuda").transpose(1, 2))
+    with pytest.raises(TypeError):
+        call(mask=mask.long())
+    for kw in (dict(ctx=torch.cat([ctx, ctx])), dict(pre=pre[:0]), dict(mask=mask[:-1].contiguous()),
+               dict(bt=torch.cat([bt, bt])), dict(lse=torch.zeros(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**kw)
+
+
+def test_no_tokens_is_nothing_to_do():
+    c = Case(32, [(20, 5)], 8, 2, 64)
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = c.q[:0]
+    o, lse = pkv.pkv_tree_attn(c.pool, q, e.view(0, 3), e, e, zero, e.view(0, 1), 0.1)
+    assert o.shape == (0, 8, 64) and lse.shape == (0, 8)
+    # requests without query tokens beside a padded batch: nothing is written
+    out = torch.full_like(c.q, 7.0)
+    pkv.pkv_tree_attn(c.pool, c.q, ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.prefix), torch.cat([zero, zero]), c.mask(),
+                      0.1, out=out)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and pkv.pkv_check_device_errors(c.pool) == 0
+
+
+def test_output_at_an_odd_multiple_of_16_bytes():
+    c = Case(33, [(600, 40), (33, 7)], 8, 2, 128)
+    out = torch.zeros(c.q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(c.q.shape)
+    o, lse = c.run(out=out)
+    c.check(o, lse)
+
+
+def test_two_threads_and_two_streams_at_once():
+    """Calls of one pool from two threads: on one stream (they share the pool's workspace) and on two."""
+    import threading
+    cases = [Case(34, [(3000, 20), (100, 9)], 8, 2, 128), Case(35, [(2500, 33), (700, 5)], 8, 2, 128)]
+    cases[1].pool.close()
+    cases[1].pool = cases[0].pool
+    nb = cases[0].pool.num_blocks
+    rng = np.random.default_rng(1)
+    for c in cases:                       # tables that may share blocks: the pool is only read
+        c.bt = np.where(c.bt >= 0, rng.integers(0, nb, c.bt.shape), -1).astype(np.int32)
+    for streams in ((None, None), (torch.cuda.Stream(), torch.cuda.Stream())):
+        got = [None, None]
+        args = [(c.pool, c.q, ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.prefix), ref.dev(c.cu), c.mask(), c.scale) for c in cases]
+        torch.cuda.synchronize()
+
+        def work(i):
+            for _ in range(30):
+                got[i] = pkv.pkv_tree_attn(*args[i], stream=streams[i])
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for c, (o, lse) in zip(cases, got):
+            c.check(o, lse)
+
+
+def test_graph_with_its_own_workspace_beside_eager_calls():
+    c = Case(36, [(900, 20), (40, 20)], 8, 2, 64)
+    args = (c.pool, c.q, ref.dev(c.bt), ref.dev(c.ctx), ref.dev(c.prefix), ref.dev(c.cu), c.mask(), c.scale)
+    pkv.pkv_tree_attn(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = pkv.pkv_tree_attn(*args)
+    s = torch.cuda.Stream()
+    for _ in range(5):                    # the replay on one stream, eager calls on another, at the same time
+        with torch.cuda.stream(s):
+            graph.replay()
+        o2, lse2 = pkv.pkv_tree_attn(*args)
+    torch.cuda.synchronize()
+    c.check(o, lse)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_blocks_beyond_4_gb():
+    """Offsets above 2^32 bytes: a pool of 4.9 GB of K, its requests in the last blocks."""
+    if Case.form == 1:
+        c = Case(37, [(700, 20), (40, 7)], 8, 2, 128)
+    else:
+        c = Case(37, [(700, 40), (40, 7)], 8, 2, 128)
+    nb, small = 600_000, c.pool
+    pool = pkv.Pool(nb, 2, 128)
+    pkv.pkv_debug_set(pool, pkv.PKV_DEBUG_TREE_FORM, Case.form)
+    pool.k[nb - small.num_blocks:] = small.k
+    pool.v[nb - small.num_blocks:] = small.v
+    o, lse = pkv.pkv_tree_attn(pool, c.q, ref.dev(np.where(c.bt >= 0, c.bt + nb - small.num_blocks, -1).astype(np.int32)),
+                               ref.dev(c.ctx), ref.dev(c.prefix), ref.dev(c.cu), c.mask(), c.scale)
+    c.check(o, lse)
+    assert pkv.pkv_check_device_errors(pool) == 0
+    pool.close()
