@@ -361,7 +361,7 @@ int pkv_tree_mask(pkv_pool* pool, const int32_t* parents, const int32_t* cu_q_le
  * with e = exps[..] the smallest exponent >= -126 for which every |K_j[d]| <= 127 * 2^e
  * (FP8 pools: K_j in codes' values, without k_scale).  NaN counts as absent, an
  * infinity as the largest finite bf16.  The arrays belong to the caller
- * (device, codes 16-byte aligned).
+ * (device, codes 16-byte aligned; exps is read in whole aligned 4-byte words).
  *
  * pkv_summarize recomputes the bounds of every block that holds one of the
  * given positions (the arguments of pkv_append, plus ctx_lens: keys at or
