@@ -189,6 +189,62 @@ __device__ __forceinline__ uint32_t key_of(float f) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// P and N of a group's queries ([G][D]) as whole numbers: unit 2^f, the smallest
+// with |q| <= most 2^f, most = floor(32767 / G).  One warp, D / 32 channels a lane.
+template <int D>
+__device__ __forceinline__ void whole_queries(const uint16_t* q, int G, int16_t* dst, int lane) {
+  constexpr int kDPL = D / 32;
+  const float mostq = static_cast<float>(32767 / G);
+  auto channels = [&](int r, float (&v)[kDPL]) {   // row r of the group; values that are not finite count as 0
+    uint32_t w[2];
+    if constexpr (kDPL == 4) {
+      const uint2 y = *reinterpret_cast<const uint2*>(q + r * D + lane * kDPL);
+      w[0] = y.x; w[1] = y.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(q + r * D + lane * kDPL);
+    }
+#pragma unroll
+    for (int d = 0; d < kDPL; ++d) {
+      const float f = (d & 1) ? bf16hi_to_f32(w[d >> 1]) : bf16lo_to_f32(w[d >> 1]);
+      v[d] = fabsf(f) < CUDART_INF_F ? f : 0.f;
+    }
+  };
+  float amax = 0.f;
+#pragma unroll 8
+  for (int r = 0; r < G; ++r) {
+    float v[kDPL];
+    channels(r, v);
+#pragma unroll
+    for (int d = 0; d < kDPL; ++d) amax = fmaxf(amax, fabsf(v[d]));
+  }
+#pragma unroll
+  for (int y = 16; y > 0; y >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
+  // Tiny queries (below 2^-100) count as 0: the unit stays a normal number.
+  const bool none = !(amax >= 7.8886090522101181e-31f);
+  const int f = none ? 0 : exp_of(amax) - exp_of(mostq) + (mant_of(amax) <= mant_of(mostq) ? 0 : 1);
+  // x 2^-f in two exact steps (2^-f alone may exceed the normal range)
+  const float f1 = none ? 0.f : pow2f(-f / 2), f2 = pow2f(-(f - f / 2));
+  int P[kDPL], N[kDPL];
+#pragma unroll
+  for (int d = 0; d < kDPL; ++d) P[d] = N[d] = 0;
+#pragma unroll 8
+  for (int r = 0; r < G; ++r) {
+    float v[kDPL];
+    channels(r, v);
+#pragma unroll
+    for (int d = 0; d < kDPL; ++d) {
+      const int w = static_cast<int>(rintf(v[d] * f1 * f2));
+      P[d] += max(w, 0);
+      N[d] += min(w, 0);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < kDPL; ++d) {
+    dst[lane * kDPL + d] = static_cast<int16_t>(P[d]);
+    dst[D + lane * kDPL + d] = static_cast<int16_t>(N[d]);
+  }
+}
+
 // A warp's view of one iteration: eight groups of four lanes; group i takes
 // head 8 o + i of one block (more than 8 heads), or head i % Hkv of block i / Hkv
 // (up to 8 heads: 8 / Hkv blocks an iteration).  Lane s of a group takes the
@@ -278,7 +334,6 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
   const int octets = Hkv > 8 ? (Hkv + 7) / 8 : 1;
   const int my_blk = Hkv >= 8 ? 0 : grp / Hkv;
   const bool lane_on = Hkv >= 8 || grp < bpw * Hkv;
-  const float mostq = static_cast<float>(32767 / G);
   int tok = a.tok_first + at[0];
   int64_t x = off[0];
   for (; u < end; ++tok, x = 0) {
@@ -362,64 +417,14 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
     asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - S::kRawStages) : "memory");
     __syncthreads();
 
-    // Whole-number queries of every head, while the first copies are under way: unit 2^f, the smallest with
-    // |q| <= most 2^f, most = floor(32767 / G).  A warp a (head, token), D / 32 channels a lane.
-    constexpr int kDPL = D / 32;
+    // Whole-number queries of every head, while the first copies are under way: a warp a (head, token).
     for (int i = warp; i < Hkv * NT; i += kScoreWarps) {
       const int h = i / NT, j = i % NT;
       if (nt[j] == 0) continue;   // no second token (its sums are not used)
       const uint16_t* q = h < raw_heads
-          ? reinterpret_cast<const uint16_t*>(smem + raw_at) + (j * S::kRawRows + h * G) * D + lane * kDPL
-          : static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(tok + j) * a.num_q_heads + h * G) * D + lane * kDPL;
-      auto channels = [&](int r, float (&v)[kDPL]) {   // row r of the group; values that are not finite count as 0
-        uint32_t w[2];
-        if constexpr (kDPL == 4) {
-          const uint2 y = *reinterpret_cast<const uint2*>(q + r * D);
-          w[0] = y.x; w[1] = y.y;
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(q + r * D);
-        }
-#pragma unroll
-        for (int d = 0; d < kDPL; ++d) {
-          const float f = (d & 1) ? bf16hi_to_f32(w[d >> 1]) : bf16lo_to_f32(w[d >> 1]);
-          v[d] = fabsf(f) < CUDART_INF_F ? f : 0.f;
-        }
-      };
-      float amax = 0.f;
-#pragma unroll 8
-      for (int r = 0; r < G; ++r) {
-        float v[kDPL];
-        channels(r, v);
-#pragma unroll
-        for (int d = 0; d < kDPL; ++d) amax = fmaxf(amax, fabsf(v[d]));
-      }
-#pragma unroll
-      for (int y = 16; y > 0; y >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-      // Tiny queries (below 2^-100) count as 0: the unit stays a normal number.
-      const bool none = !(amax >= 7.8886090522101181e-31f);
-      const int f = none ? 0 : exp_of(amax) - exp_of(mostq) + (mant_of(amax) <= mant_of(mostq) ? 0 : 1);
-      // x 2^-f in two exact steps (2^-f alone may exceed the normal range)
-      const float f1 = none ? 0.f : pow2f(-f / 2), f2 = pow2f(-(f - f / 2));
-      int P[kDPL], N[kDPL];
-#pragma unroll
-      for (int d = 0; d < kDPL; ++d) P[d] = N[d] = 0;
-#pragma unroll 8
-      for (int r = 0; r < G; ++r) {
-        float v[kDPL];
-        channels(r, v);
-#pragma unroll
-        for (int d = 0; d < kDPL; ++d) {
-          const int w = static_cast<int>(rintf(v[d] * f1 * f2));
-          P[d] += max(w, 0);
-          N[d] += min(w, 0);
-        }
-      }
-      int16_t* dst = reinterpret_cast<int16_t*>(smem + h * S::kQuery) + j * 2 * D + lane * kDPL;
-#pragma unroll
-      for (int d = 0; d < kDPL; ++d) {
-        dst[d] = static_cast<int16_t>(P[d]);
-        dst[D + d] = static_cast<int16_t>(N[d]);
-      }
+          ? reinterpret_cast<const uint16_t*>(smem + raw_at) + (j * S::kRawRows + h * G) * D
+          : static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(tok + j) * a.num_q_heads + h * G) * D;
+      whole_queries<D>(q, G, reinterpret_cast<int16_t*>(smem + h * S::kQuery) + j * 2 * D, lane);
     }
     __syncthreads();
 #pragma unroll
@@ -502,6 +507,60 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
   }
 }
 
+constexpr int kPickThreads = 512;
+// Few short lists: a CTA of pick_kernel scores its (token, head)'s blocks itself,
+// which saves a launch and the way through the workspace.  Four lanes a block,
+// 16-byte pieces as above; the first blocks' codes are on their way while a warp
+// makes the whole-number query.
+template <int D>
+__device__ __forceinline__ void alone_keys(const SparseArgs& a, int t, int g, int req, int n, uint32_t* s_keys) {
+  constexpr int kPieces = 2 * D / 64, kRound = kPickThreads / 4;
+  __shared__ __align__(16) int16_t s_q[2 * D];
+  const int tid = threadIdx.x, sub = tid & 3;
+  const int32_t* bt_row = a.block_tables + static_cast<int64_t>(req) * a.max_blocks;
+  int qq[kPieces][8];
+  for (int base = 0; base < n; base += kRound) {
+    const int b = base + (tid >> 2), pb = b < n ? __ldg(bt_row + b) : 0;
+    const bool there = b < n && static_cast<unsigned>(pb) < static_cast<unsigned>(a.pool.num_blocks);
+    const int64_t chunk = static_cast<int64_t>(pb) * a.pool.num_kv_heads + g;
+    uint4 w[kPieces];
+    int e = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      w[i] = there ? __ldg(reinterpret_cast<const uint4*>(a.codes + chunk * 2 * D + sub * 16 + i * 64)) : make_uint4(0, 0, 0, 0);
+    if (there) e = __ldg(a.exps + chunk);
+    if (base == 0) {
+      if (tid < 32)
+        whole_queries<D>(static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(t) * a.num_q_heads + g * a.group) * D,
+                         a.group, s_q, tid);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+        for (int y = 0; y < 8; ++y) qq[i][y] = reinterpret_cast<const int*>(s_q)[(i * 4 + sub) * 8 + y];
+    }
+    int s = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        s = __dp2a_lo(qq[i][2 * y], static_cast<int>(x[y]), s);
+        s = __dp2a_hi(qq[i][2 * y + 1], static_cast<int>(x[y]), s);
+      }
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (sub == 0 && b < n) {
+      uint32_t key = 0u;
+      if (!there) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
+      else if (b < a.sinks || b >= n - a.recent) key = 0xffffffffu;
+      else key = key_of(__int2float_rn(s) * pow2f(max(-126, e)));
+      s_keys[b] = key;
+    }
+  }
+}
+
 // One CTA per (token, KV head).  Keys of up to kPickKeys blocks stay in shared
 // memory, more are read again from L2.  The radix passes run on key - lo, shifted
 // until the largest uses all 32 bits, so that the first 8-bit pass spreads the
@@ -509,11 +568,18 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
 // additions to one counter take a microsecond), and stop as soon as the
 // threshold's bin is taken whole, or holds so few keys that ranking them against
 // each other is shorter than another pass (for 190 blocks 18.4 -> 16.6 us of a
-// selection and attention).
-constexpr int kPickThreads = 512;
+// selection and attention).  Bound by the latency of these steps: 8 us for 256 lists
+// of 1500 blocks.
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickKeys = 8192;
 constexpr int kPickRank = 64;
+// pick_kernel alone up to kAloneBlocks blocks a list and kAloneLists lists an SM
+// (selection and attention, us, both kernels / alone; 190 blocks: 2 lists 16.5 / 14.5,
+// 64 lists 20.6 / 16.5, 256 lists 26.7 / 22.1, 1024 lists 65.7 / 74.1; 500 blocks: 64
+// lists 20.6 / 18.6, 512 lists 49.9 / 50.7; 8 lists of 940 blocks 19.4 / 20.6, of 1900
+// 20.6 / 27.0).
+constexpr int kAloneBlocks = 512, kAloneLists = 3;
+template <int D, bool ALONE>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SparseArgs a) {
   __shared__ uint32_t s_keys[kPickKeys];
   __shared__ uint32_t s_hist[4][256];
@@ -535,19 +601,23 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SparseArgs a) 
   }
   griddep_wait();
   griddep_launch();
-  if (req_of_warp(a.cu_q_lens, a.num_reqs, t, lane) < 0) return;   // block-uniform
+  const int req = req_of_warp(a.cu_q_lens, a.num_reqs, t, lane);
   const int p = __ldg(a.positions + t);
+  if (ALONE && g == 0 && tid == 0 && t < __ldg(a.cu_q_lens + a.num_reqs) && (p < 0 || p >= a.max_blocks * kBlockSize))
+    atomicOr(a.pool.err, PKV_DEVERR_POSITION);
+  if (req < 0) return;   // block-uniform
   int32_t* out = a.sel + (static_cast<int64_t>(t) * Hkv + g) * a.top_k;
   const int n = p >= 0 && p < a.max_blocks * kBlockSize ? (p >> 4) + 1 : 0;
   const uint32_t* src = a.keys + (static_cast<int64_t>(i_tok) * Hkv + g) * a.max_blocks;
-  const bool kept = n <= kPickKeys;
+  const bool kept = ALONE || n <= kPickKeys;
+  if constexpr (ALONE) alone_keys<D>(a, t, g, req, n, s_keys);
   __syncthreads();
   uint32_t lo = 0xffffffffu, hi = 0u;
   int forced = 0, ordinary = 0;
 #pragma unroll 4
   for (int i = tid; i < n; i += kPickThreads) {
-    const uint32_t k = __ldcg(src + i);
-    if (kept) s_keys[i] = k;
+    const uint32_t k = ALONE ? s_keys[i] : __ldcg(src + i);
+    if (!ALONE && kept) s_keys[i] = k;
     if (k == 0xffffffffu) {
       ++forced;
     } else if (k != 0u) {
@@ -708,10 +778,18 @@ int launch_select_d(SparseArgs a, cudaStream_t s) {
     const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(S::kCtas * a.num_sms, (units + 15) / 16));
     e = launch_dependent(score_kernel<D, NT>, dim3(ctas), kScoreThreads, smem, s, a);
     if (e == cudaSuccess)
-      e = launch_dependent(pick_kernel, dim3(static_cast<unsigned>(a.tok_count) * a.pool.num_kv_heads), kPickThreads, 0, s, a);
+      e = launch_dependent(pick_kernel<0, false>, dim3(static_cast<unsigned>(a.tok_count) * a.pool.num_kv_heads), kPickThreads, 0, s, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+template <int D>
+int launch_alone_d(SparseArgs a, cudaStream_t s) {
+  a.tok_first = 0;
+  a.tok_count = a.num_tokens;
+  return launch_dependent(pick_kernel<D, true>, dim3(static_cast<unsigned>(a.num_tokens) * a.pool.num_kv_heads), kPickThreads,
+                          0, s, a);
 }
 
 template <int D, bool F8>
@@ -745,6 +823,8 @@ int select_part(int num_tokens, int max_blocks, int num_kv_heads) {
 
 int launch_select(const SparseArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.max_blocks <= kAloneBlocks && static_cast<int64_t>(a.num_tokens) * a.pool.num_kv_heads <= kAloneLists * static_cast<int64_t>(a.num_sms))
+    return a.pool.head_dim == 128 ? launch_alone_d<128>(a, s) : launch_alone_d<64>(a, s);
   const bool pairs = a.num_tokens / 2 >= a.num_reqs && a.pool.num_kv_heads <= kPairMaxHeads;
   if (a.pool.head_dim == 128) return pairs ? launch_select_d<128, 2>(a, s) : launch_select_d<128, 1>(a, s);
   return pairs ? launch_select_d<64, 2>(a, s) : launch_select_d<64, 1>(a, s);

@@ -445,3 +445,21 @@ def test_blocks_beyond_4_gb():
     c.check_select(sel, 11, 1, 1)
     c.check_attend(sel, o, lse)
     pool.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(2, 2, 64, "bf16"), (8, 2, 128, "bf16"), (24, 3, 64, "bf16"), (5, 5, 128, "fp8_e4m3"),
+                                            (16, 8, 128, "bf16"), (12, 12, 64, "fp8_e4m3"), (128, 1, 128, "bf16"),
+                                            (80, 20, 128, "fp8_e4m3")])
+def test_small_batches_in_wide_tables(hq, hkv, d, dtype):
+    """The kernels of large batches on the sizes of small ones: as pairs of tokens, and one by one."""
+    Case(51, SMALL, hq, hkv, d, dtype, width=600).whole(7, 1, 1)
+    Case(52, [(40, [39]), (700, [699]), (17, [16]), (300, [299, 298, 297])], hq, hkv, d, dtype, width=600).whole(7, 1, 1)
+
+
+def test_more_heads_than_pairs_take():
+    Case(53, [(300, list(range(290, 300))), (40, [39, 38])], 130, 65, 64, width=600).whole(6, 1, 1)
+
+
+def test_query_heads_beyond_the_staging_rows():
+    Case(54, [(300, [299, 298]), (40, [39, 38])], 200, 40, 64, width=600).whole(6, 1, 1)      # 13 of 40 heads staged
+    Case(55, [(300, [299]), (40, [39])], 200, 2, 64, width=600).whole(6, 1, 1)                # none
