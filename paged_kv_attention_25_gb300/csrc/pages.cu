@@ -111,7 +111,8 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {   //
 // reads (children, rows, tables, counts), so that each link keeps as many reads
 // under way as there are: a warp takes kRowBatch rows at a time (one row at a
 // time took 12 of 19 us for 240 rows of 60 pages), and a row with one child
-// skips the full pages, whose counts do not change.
+// skips the full pages, whose counts do not change.  (1500 rows of 16 pages: 39 us
+// with the fill, 4000 rows of 8: 95.)
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a) {
   __shared__ int s_warp[32];
   __shared__ int s_kids[kPlanRows], s_first[kPlanRows];
@@ -252,7 +253,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
 
 // The same for up to kPlanThreads rows and children: thread i has row i and
 // child i in registers, so that the chain is three reads long: lengths and
-// parents, tables, counts.
+// parents, tables, counts.  4 rows of 8 pages: 8.3 us with the fill (the general
+// kernel: 10); 240 rows of up to 130: 14.4 (19); 1024 rows of 16: 21.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const ForkArgs a) {
   __shared__ int s_warp[32];
   __shared__ int s_kids[kPlanThreads], s_first[kPlanThreads], s_keeper[kPlanThreads];
@@ -373,8 +375,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
   }
 }
 
-// One CTA per child: its table row, and the copy of its parent's partly filled page, kCopyBatch chunks a thread at a
-// time.
+// One CTA per child: its table row, and the copy of its parent's partly filled
+// page, kCopyBatch chunks a thread at a time.  Bound by latency: its record, the
+// fresh page's id, the page (4 children 4.2 us by itself, 240 children 5.6).
 constexpr int kCopyBatch = 4;
 __global__ void __launch_bounds__(256) fork_fill_kernel(const ForkArgs a) {
   const int i = blockIdx.x, tid = threadIdx.x;
@@ -423,7 +426,9 @@ __global__ void __launch_bounds__(256) fork_fill_kernel(const ForkArgs a) {
   }
 }
 
-// One CTA per pair: the whole page.
+// A CTA copies kCopyBatch chunks a thread of a pair's page (K, then V), all loads
+// before the stores.  Bound by HBM: 1024 pages of 64 KB in 23 us, 5.9 TB/s (a CTA a
+// page with one load under way a thread: 31 us), 8192 in 166, 6.5 TB/s; 64 pages 4.3 us.
 __global__ void __launch_bounds__(256) copy_blocks_kernel(const PoolView pool, uint4* kp, uint4* vp,
                                                           const int32_t* __restrict__ src,
                                                           const int32_t* __restrict__ dst, int8_t* codes,
@@ -436,11 +441,18 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const PoolView pool, u
   }
   if (s == d) return;
   const int64_t page = static_cast<int64_t>(pool.num_kv_heads) * kBlockSize * pool.head_dim * pool.elem_bytes / 16;
-  for (int64_t e = tid; e < page; e += 256) {
-    kp[d * page + e] = kp[s * page + e];
-    vp[d * page + e] = vp[s * page + e];
+  uint4 v[kCopyBatch];
+#pragma unroll
+  for (int k = 0; k < kCopyBatch; ++k) {
+    const int64_t e = (static_cast<int64_t>(blockIdx.y) * kCopyBatch + k) * 256 + tid;
+    if (e < 2 * page) v[k] = e < page ? kp[s * page + e] : vp[s * page + e - page];
   }
-  if (codes) {
+#pragma unroll
+  for (int k = 0; k < kCopyBatch; ++k) {
+    const int64_t e = (static_cast<int64_t>(blockIdx.y) * kCopyBatch + k) * 256 + tid;
+    if (e < 2 * page) (e < page ? kp[d * page + e] : vp[d * page + e - page]) = v[k];
+  }
+  if (codes && blockIdx.y == 0) {
     const int64_t n = static_cast<int64_t>(pool.num_kv_heads) * 2 * pool.head_dim / 16;
     uint4* c = reinterpret_cast<uint4*>(codes);
     for (int64_t e = tid; e < n; e += 256) c[d * n + e] = c[s * n + e];
@@ -453,6 +465,8 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const PoolView pool, u
 // of the request's kept tokens, kMoveBatch at a time, all loads before the
 // stores.  Sources ascend and lie at or behind their targets, so a store never
 // reaches a row that is still to be read: no two threads touch one column.
+// Bound by latency: positions, table, rows, a batch after another (one request,
+// 6 kept tokens: 6.2 us; 128 requests of up to 14, 8 heads: 8.3).
 constexpr int kMoveBatch = 8;
 __global__ void __launch_bounds__(256) compact_kernel(const PoolView pool, uint4* kp, uint4* vp,
                                                       const int32_t* __restrict__ bt, int max_blocks, int num_reqs,
@@ -527,7 +541,9 @@ int launch_fork(const ForkArgs& a, void* stream) {
 
 int launch_copy_blocks(const PoolView& pool, void* kp, void* vp, const int32_t* src, const int32_t* dst, int n,
                        int8_t* codes, int8_t* exps, void* stream) {
-  copy_blocks_kernel<<<n, 256, 0, static_cast<cudaStream_t>(stream)>>>(pool, static_cast<uint4*>(kp),
+  const int64_t chunks = static_cast<int64_t>(2) * pool.num_kv_heads * kBlockSize * pool.head_dim * pool.elem_bytes / 16;
+  const dim3 grid(n, static_cast<unsigned>((chunks + 256 * kCopyBatch - 1) / (256 * kCopyBatch)));
+  copy_blocks_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(pool, static_cast<uint4*>(kp),
                                                                        static_cast<uint4*>(vp), src, dst, codes, exps);
   return cudaGetLastError();
 }

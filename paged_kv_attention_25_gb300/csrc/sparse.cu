@@ -50,7 +50,10 @@ __device__ __forceinline__ float mant_of(float x) {
 // ---------------------------------------------------------------- bounds
 // One warp per TOK consecutive tokens and KV head: it handles the blocks that
 // these tokens open (the first of the request's consecutive tokens in a
-// block).  Lane l holds channels [l D/32, (l + 1) D/32).
+// block).  Lane l holds channels [l D/32, (l + 1) D/32).  Bound by the latency of a
+// chain of reads (request and position, table, keys): 96 single tokens 6.2 us, 25
+// thousand tokens of prompts, 8 heads, 12.4 us warm (51 MB of keys, 4.1 TB/s) and 20
+// from HBM.  (32 tokens a warp: the same; four heads a warp: 16 us.)
 template <int D, bool F8, int TOK>
 __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
   constexpr int kDPL = D / 32;
