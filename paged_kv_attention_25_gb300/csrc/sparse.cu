@@ -602,10 +602,12 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SparseArgs a) 
     s_lohi[1] = 0u;
     s_count[0] = s_count[1] = s_cands = 0;
   }
-  griddep_wait();
-  griddep_launch();
+  // (After the scores' kernel the caller's arrays are complete already: every CTA of it waited before it let this one start.)
+  if constexpr (ALONE) griddep_wait();
   const int req = req_of_warp(a.cu_q_lens, a.num_reqs, t, lane);
   const int p = __ldg(a.positions + t);
+  if constexpr (!ALONE) griddep_wait();
+  griddep_launch();
   if (ALONE && g == 0 && tid == 0 && t < __ldg(a.cu_q_lens + a.num_reqs) && (p < 0 || p >= a.max_blocks * kBlockSize))
     atomicOr(a.pool.err, PKV_DEVERR_POSITION);
   if (req < 0) return;   // block-uniform
