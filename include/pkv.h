@@ -391,7 +391,7 @@ int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, i
  * Rows of tokens that belong to no request are left as they are.  A block
  * without a valid pool block is flagged and not selected; a position outside
  * the table is flagged and selects nothing.  1 <= top_k <= 2^27 (it may exceed
- * the table), num_kv_heads <= 256.  workspace:
+ * the table).  workspace:
  * pkv_select_blocks_workspace_size() bytes for the same sizes (the scores of up
  * to 64 MB of tokens at a time), 256-byte aligned, used by one call at a time as
  * for pkv_tree_attn.

@@ -72,8 +72,7 @@ struct SparseArgs {
   int tok_first, tok_count, tok_most;
 };
 int launch_summarize(const SparseArgs& a, void* stream);
-// KV heads that the selection can take (their queries stay in shared memory), and the tokens of a part.
-constexpr int kSelectMaxHeads = 256;
+// The tokens of a part.
 int select_part(int num_tokens, int max_blocks, int num_kv_heads);
 int launch_select(const SparseArgs& a, void* stream);
 

@@ -277,8 +277,6 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
   if (sinks < 0 || recent < 0) return fail(PKV_EINVAL, "need sinks >= 0, recent >= 0");
   if (num_tokens == 0) return PKV_OK;
   if ((rc = check_heads(pool, num_q_heads))) return rc;
-  if (pool->num_kv_heads > kSelectMaxHeads)
-    return fail(PKV_EUNSUPPORTED, "num_kv_heads above " + std::to_string(kSelectMaxHeads));
   if (!q || !q_positions || !block_tables || !cu_q_lens || !selected) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q)) return fail(PKV_EINVAL, "q must be 16-byte aligned");
   if ((rc = check_summary(pool, codes, exps))) return rc;

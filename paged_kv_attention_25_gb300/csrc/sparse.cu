@@ -170,18 +170,19 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
 }
 
 // ---------------------------------------------------------------- selection
-// Two kernels.  score_kernel reads the bounds once, all heads of a block
-// together, in equal shares of the line (token, block), and leaves a 32-bit key
-// for every (token, block, head); pick_kernel finds each (token, head)'s
+// Two kernels.  score_kernel reads the bounds once, eight heads of a block
+// together, in equal shares of the line (token, heads, block), and leaves a 32-bit
+// key for every (token, block, head); pick_kernel finds each (token, head)'s
 // threshold and writes its list.  (One kernel a (token, head), clusters or not,
 // left the memory idle while it looked for thresholds and took as long as the
 // longest context on the fullest SM: 35 us against 30 for 32 requests of 9 to 32
-// thousand tokens; now 19 + 8.)
+// thousand tokens; now 18 + 8.)
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-// Blocks that a token's start costs (about 40 KB of bounds and a bit).
-__host__ __device__ inline int token_units(int num_kv_heads) { return 4 + 160 / num_kv_heads; }
-constexpr int kPairMaxHeads = 64;  // KV heads whose whole-number queries of two tokens leave room for two CTAs an SM
+// Heads go in octets (all heads if there are no more than eight): an item of the line is a token's octet.
+__host__ __device__ inline int octets_of(int num_kv_heads) { return num_kv_heads > 8 ? (num_kv_heads + 7) / 8 : 1; }
+// Blocks that an item's start costs (about 40 KB of bounds and a bit).
+__host__ __device__ inline int start_units(int num_kv_heads) { return 4 + 160 / (num_kv_heads < 8 ? num_kv_heads : 8); }
 using ScoreShare = Share<16>;
 
 // Order-preserving key of a score: larger score, larger key.  0 (no block) is
@@ -248,20 +249,22 @@ __device__ __forceinline__ void whole_queries(const uint16_t* q, int G, int16_t*
   }
 }
 
-// A warp's view of one iteration: eight groups of four lanes; group i takes
-// head 8 o + i of one block (more than 8 heads), or head i % Hkv of block i / Hkv
-// (up to 8 heads: 8 / Hkv blocks an iteration).  Lane s of a group takes the
+// A warp's view of one iteration: eight groups of four lanes; group i takes head i
+// of the octet of one block, or head i % Hkv of block i / Hkv (fewer than 8 heads:
+// 8 / Hkv blocks an iteration).  Lane s of a group takes the
 // 16-byte pieces s, s + 4, ... of the head's 2 D codes, and copies them itself
 // into its own places of the ring, so that it waits for nothing but its copies.
 // Bound by HBM: 105 MB of bounds (32 contexts of 9 to 40 thousand tokens, 8 heads)
-// in 19 us, of which 5 are the start (positions, block ids, queries).
+// in 18 us, of which 5 are the start (positions, block ids, queries).  All heads of a
+// token as one item, their queries made at its start by every CTA, took 99 us instead
+// of 93 for the 7 tokens below.
 //
 // NT = 2: the tokens of a request go in pairs, which read its bounds once.  A
 // pair is an item of the line at its first token, its second token has no units.
-// Taken from two tokens a request on (selection and attention, us, single / pairs;
-// 40 heads, 5 contexts of 60 to 131 thousand tokens: 1.4 tokens each 99 / 102, 4 tokens
-// 195 / 168; 8 heads, 32 contexts of 9 to 40 thousand: 2 tokens 137 / 136, 4 tokens
-// 241 / 234; 2 x 256 tokens of 8 thousand: 172 / 158).
+// Taken where there are more tokens than requests (selection and attention, us,
+// single / pairs; 40 heads, 5 contexts of 60 to 131 thousand tokens: 7 tokens in all
+// 100 / 93, 4 each 197 / 162; 8 heads, 32 contexts of 9 to 40 thousand: 2 each 138 /
+// 135, 4 each 237 / 232; 2 x 256 tokens of 8 thousand: 167 / 156).
 template <int D, int NT>
 struct ScoreShape {
   static constexpr int kStages = NT == 1 ? 3 : 4;   // warp iterations of bounds in flight
@@ -273,6 +276,8 @@ struct ScoreShape {
   static constexpr int kRawRows = 64;               // rows of each token that fit
   static_assert(kRawStages * kPieces * 16 * kScoreThreads >= NT * kRawRows * D * 2, "query rows fit their stages");
   static constexpr int kQuery = NT * 4 * D + 16;    // bytes a KV head (heads 16 bytes apart in the banks)
+  static constexpr int kRingAt = 8 * kQuery;
+  static constexpr int kTotal = kRingAt + kRing;
 };
 template <int D, int NT>
 __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score_kernel(const SparseArgs a) {
@@ -282,13 +287,14 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
   __shared__ int64_t scratch[kScoreWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hkv = a.pool.num_kv_heads, G = a.group;
-  // smem: [Hkv][NT][P: D, N: D] 16-bit whole-number queries, then the ring
-  const uint32_t slot = smem_u32(smem) + Hkv * S::kQuery + tid * 16;     // ring: [stage][piece][thread] 16 bytes,
-  const uint32_t slot_e = smem_u32(smem) + Hkv * S::kQuery + kScoreStages * kScoreThreads * kPieces * 16 + tid * 4;
+  // smem: [8 heads][NT][P: D, N: D] 16-bit whole-number queries; ring: [stage][piece][thread] 16 bytes, [stage][thread] 4
+  const uint32_t slot = smem_u32(smem) + S::kRingAt + tid * 16;
+  const uint32_t slot_e = smem_u32(smem) + S::kRingAt + kScoreStages * kScoreThreads * kPieces * 16 + tid * 4;
   griddep_wait();
   griddep_launch();
 
-  // The share: token t (of this launch's) has a unit for each block up to its position, and some for its start.
+  // The share: each octet of token t (of this launch's) has a unit for each block up to its position, and some for
+  // its start.
   const int end_tok = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
   const int tokens = max(0, min(a.tok_count, end_tok - a.tok_first));
   const int most = a.max_blocks * kBlockSize;
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
     n1 = t + 1 < min(__ldg(a.cu_q_lens + r + 1), a.tok_first + tokens) ? token_blocks(t + 1) : 0;
     return true;
   };
-  const int start = token_units(Hkv);
+  const int start = start_units(Hkv), octets = octets_of(Hkv);
   int64_t U[1], off[1];
   int at[1];
   int64_t u = 0, end = 0;
@@ -314,10 +320,12 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
       [&](int i, int64_t (&n)[1]) {
         const int t = a.tok_first + i, b = token_blocks(t);
         if constexpr (NT == 1) {
-          n[0] = b + start;
+          n[0] = static_cast<int64_t>(octets) * (b + start);
         } else {
           int n0, n1;
-          n[0] = pair_blocks(t, req_of(a.cu_q_lens, a.num_reqs, t), n0, n1) ? max(n0, n1) + start : 0;
+          n[0] = pair_blocks(t, req_of(a.cu_q_lens, a.num_reqs, t), n0, n1)
+                     ? static_cast<int64_t>(octets) * (max(n0, n1) + start)
+                     : 0;
         }
         if (b == 0 && blockIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
       },
@@ -334,48 +342,57 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
 
   const int grp = lane >> 2, sub = lane & 3;
   const int bpw = Hkv >= 8 ? 1 : 8 / Hkv;               // blocks of a warp iteration
-  const int octets = Hkv > 8 ? (Hkv + 7) / 8 : 1;
   const int my_blk = Hkv >= 8 ? 0 : grp / Hkv;
   const bool lane_on = Hkv >= 8 || grp < bpw * Hkv;
   int tok = a.tok_first + at[0];
-  int64_t x = off[0];
-  for (; u < end; ++tok, x = 0) {
+  int64_t x = off[0];   // unit within the token
+  while (u < end) {
     int nt[NT], r = -1;   // blocks of each token
+    bool opens = true;
     if constexpr (NT == 1) {
       nt[0] = token_blocks(tok);
     } else {
       r = req_of_warp(a.cu_q_lens, a.num_reqs, tok, lane);
-      if (!pair_blocks(tok, r, nt[0], nt[1])) continue;   // (no units)
+      opens = pair_blocks(tok, r, nt[0], nt[1]);   // (otherwise it has no units)
     }
-    const int n = max(nt[0], nt[NT - 1]);
-    const int len = static_cast<int>(min(n + start - x, end - u));
-    const int b0 = static_cast<int>(x), b1 = static_cast<int>(min(x + len, static_cast<int64_t>(n)));
+    const int n = opens ? max(nt[0], nt[NT - 1]) : 0, span = n + start;
+    const int octet = static_cast<int>(x / span);
+    if (!opens || octet >= octets) {
+      ++tok;
+      x = 0;
+      continue;
+    }
+    const int b0 = static_cast<int>(x - static_cast<int64_t>(octet) * span);
+    const int len = static_cast<int>(min(static_cast<int64_t>(span - b0), end - u));
+    const int b1 = min(b0 + len, n);
     u += len;
+    x += len;
     if (b0 >= b1) continue;   // block-uniform
     if constexpr (NT == 1) {
       r = req_of_warp(a.cu_q_lens, a.num_reqs, tok, lane);
       if (r < 0) continue;
     }
+    const int head0 = octet * 8, heads = min(8, Hkv - head0);
     const int32_t* bt_row = a.block_tables + static_cast<int64_t>(r) * a.max_blocks;
-    // Iterations of this warp: octet by octet, blocks first, first + step, ... (`per` of them).  Everything that is
-    // read comes through copies in flight, but for the block ids: lane l holds the id of the warp's block base + l,
-    // and the next 32 are on their way.  (A load into a register, consumed iterations later, waits for the newest
-    // such load: exponents read so made every iteration as long as a read of DRAM.)
+    // Iterations of this warp: blocks first, first + step, ... (`per` of them).  Everything that is read comes
+    // through copies in flight, but for the block ids: lane l holds the id of the warp's block base + l, and the next
+    // 32 are on their way.  (A load into a register, consumed iterations later, waits for the newest such load:
+    // exponents read so made every iteration as long as a read of DRAM.)
     const int step = kScoreWarps * bpw, first = b0 + warp * bpw + my_blk;
-    const int per = (b1 - b0 + step - 1) / step, iters = octets * per;
-    const int h0 = Hkv >= 8 ? grp : grp % Hkv;
+    const int per = (b1 - b0 + step - 1) / step;
+    const int h = head0 + (Hkv >= 8 ? grp : grp % Hkv);   // this lane's
+    const bool on = lane_on && h < Hkv;
     const int own = per * bpw;   // the warp's blocks
     auto load_ids = [&](int base) -> int {
       const int i = base + lane, b = b0 + (i / bpw * kScoreWarps + warp) * bpw + i % bpw;
       return i < own && b < b1 ? __ldg(bt_row + b) : -1;
     };
-    int id_cur = load_ids(0), id_next = load_ids(own > 32 ? 32 : 0);
-    int id_at = 0, id_o = 0;   // the copies' cursor: the warp's block, octet
+    int id_cur = load_ids(0), id_next = load_ids(32);
+    int id_at = 0;   // the copies' cursor
     int ids[kScoreStages];
     auto copy = [&](int st) {   // the next iteration's
       int pb = __shfl_sync(0xffffffffu, id_cur, (id_at & 31) + my_blk);
-      const int h = h0 + 8 * id_o;
-      if (id_o >= octets || !lane_on || h >= Hkv) pb = -1;
+      if (id_at >= own || !on) pb = -1;
       ids[st] = pb;
       if (static_cast<unsigned>(pb) < static_cast<unsigned>(a.pool.num_blocks)) {
         const int64_t chunk = static_cast<int64_t>(pb) * Hkv + h;
@@ -391,25 +408,21 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       id_at += bpw;
-      const bool wrap = id_at >= own;
-      if (wrap) {
-        id_at = 0;
-        ++id_o;
-      }
-      if (own > 32 && (id_at & 31) == 0) {   // on to the next 32 (after the last come the first again)
+      if ((id_at & 31) == 0) {
         id_cur = id_next;
-        id_next = load_ids(id_at + 32 < own ? id_at + 32 : 0);
+        id_next = load_ids(id_at + 32);
       }
     };
     // The queries of the first heads (of up to kRawRows rows) are asked for before the first bounds, into the ring's
     // last stages: behind three stages of bounds they took 4 us to come.
-    const int raw_heads = min(Hkv, S::kRawRows / G);
-    const int raw_at = Hkv * S::kQuery + (kScoreStages - S::kRawStages) * kPieces * kScoreThreads * 16;
+    const int raw_heads = min(heads, S::kRawRows / G);
+    const int raw_at = S::kRingAt + (kScoreStages - S::kRawStages) * kPieces * kScoreThreads * 16;
     __syncthreads();   // the previous token's queries and bounds are no longer read
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int chunks = nt[j] == 0 ? 0 : raw_heads * G * (D / 8);
-      const uint8_t* src = static_cast<const uint8_t*>(a.q) + static_cast<int64_t>(tok + j) * a.num_q_heads * D * 2;
+      const uint8_t* src = static_cast<const uint8_t*>(a.q) +
+                           (static_cast<int64_t>(tok + j) * a.num_q_heads + head0 * G) * D * 2;
       const uint32_t dst = smem_u32(smem) + raw_at + j * (S::kRawRows * D * 2);
       for (int i = tid; i < chunks; i += kScoreThreads)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 16), "l"(src + i * 16) : "memory");
@@ -420,43 +433,38 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
     asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - S::kRawStages) : "memory");
     __syncthreads();
 
-    // Whole-number queries of every head, while the first copies are under way: a warp a (head, token).
-    for (int i = warp; i < Hkv * NT; i += kScoreWarps) {
-      const int h = i / NT, j = i % NT;
+    // Whole-number queries of the heads, while the first copies are under way: a warp a (head, token).
+    for (int i = warp; i < heads * NT; i += kScoreWarps) {
+      const int hh = i / NT, j = i % NT;
       if (nt[j] == 0) continue;   // no second token (its sums are not used)
-      const uint16_t* q = h < raw_heads
-          ? reinterpret_cast<const uint16_t*>(smem + raw_at) + (j * S::kRawRows + h * G) * D
-          : static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(tok + j) * a.num_q_heads + h * G) * D;
-      whole_queries<D>(q, G, reinterpret_cast<int16_t*>(smem + h * S::kQuery) + j * 2 * D, lane);
+      const uint16_t* q = hh < raw_heads
+          ? reinterpret_cast<const uint16_t*>(smem + raw_at) + (j * S::kRawRows + hh * G) * D
+          : static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(tok + j) * a.num_q_heads + (head0 + hh) * G) * D;
+      whole_queries<D>(q, G, reinterpret_cast<int16_t*>(smem + hh * S::kQuery) + j * 2 * D, lane);
     }
     __syncthreads();
 #pragma unroll
     for (int v = kScoreStages - S::kRawStages; v < kScoreStages; ++v) copy(v);
 
-    int qq[NT][kPieces][8], octet = -1, h = 0, b = first + per * step;
-    uint32_t* out = a.keys + static_cast<int64_t>(tok - a.tok_first) * Hkv * a.max_blocks;
-    uint32_t* row = out;   // this lane's head and token
+    int qq[NT][kPieces][8];
+    {
+      const int* src = reinterpret_cast<const int*>(smem + min(h - head0, heads - 1) * S::kQuery);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+          for (int w = 0; w < 8; ++w) qq[j][i][w] = src[j * D + (i * 4 + sub) * 8 + w];
+    }
+    // This lane's head and token.
+    uint32_t* row = a.keys + (static_cast<int64_t>(tok - a.tok_first + sub) * Hkv + h) * a.max_blocks;
     const int n_tok = NT == 1 || sub == 0 ? nt[0] : nt[NT - 1];
-    const int most_b = min(b1, n_tok);   // blocks whose keys this lane writes
-    bool writes = false;
-    for (int k0 = 0; k0 < iters; k0 += kScoreStages) {
+    const int most_b = on && sub < NT ? min(b1, n_tok) : 0;   // blocks whose keys this lane writes
+    int b = first;
+    for (int k0 = 0; k0 < per; k0 += kScoreStages) {
 #pragma unroll
       for (int v = 0; v < kScoreStages; ++v) {
-        if (k0 + v < iters) {
-          if (b - first >= per * step) {   // warp-uniform: the next octet
-            b = first;
-            ++octet;
-            h = h0 + 8 * octet;
-            const int* src = reinterpret_cast<const int*>(smem + min(h, Hkv - 1) * S::kQuery);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-                for (int w = 0; w < 8; ++w) qq[j][i][w] = src[j * D + (i * 4 + sub) * 8 + w];
-            writes = sub < NT && lane_on && h < Hkv;
-            row = out + (static_cast<int64_t>(sub) * Hkv + h) * a.max_blocks;
-          }
+        if (k0 + v < per) {
           asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
           int part[NT][kPieces] = {};   // (short chains: a warp waits for fixed latencies otherwise)
 #pragma unroll
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
             s += __shfl_xor_sync(0xffffffffu, s, 1);
           }
           s += __shfl_xor_sync(0xffffffffu, s, 2);
-          if (writes && b < most_b) {
+          if (b < most_b) {
             uint32_t key = 0u;
             if (static_cast<unsigned>(ids[v]) >= static_cast<unsigned>(a.pool.num_blocks))
               atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
@@ -771,17 +779,17 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SparseArgs a) 
 template <int D, int NT>
 int launch_select_d(SparseArgs a, cudaStream_t s) {
   using S = ScoreShape<D, NT>;
-  const int smem = a.pool.num_kv_heads * S::kQuery + S::kRing;
-  cudaError_t e = smem_attr_once<score_kernel<D, NT>>((NT == 1 ? kSelectMaxHeads : kPairMaxHeads) * S::kQuery + S::kRing);
+  cudaError_t e = smem_attr_once<score_kernel<D, NT>>(S::kTotal);
   if (e != cudaSuccess) return e;
   // Tokens in parts whose keys fit the workspace.
   for (int t = 0; t < a.num_tokens; t += a.tok_most) {
     a.tok_first = t;
     a.tok_count = std::min(a.tok_most, a.num_tokens - t);
     // No more CTAs than there can be shares of 16 units.
-    const int64_t units = static_cast<int64_t>(a.tok_count) * (a.max_blocks + token_units(a.pool.num_kv_heads));
+    const int64_t units = static_cast<int64_t>(a.tok_count) * octets_of(a.pool.num_kv_heads) *
+                          (a.max_blocks + start_units(a.pool.num_kv_heads));
     const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(S::kCtas * a.num_sms, (units + 15) / 16));
-    e = launch_dependent(score_kernel<D, NT>, dim3(ctas), kScoreThreads, smem, s, a);
+    e = launch_dependent(score_kernel<D, NT>, dim3(ctas), kScoreThreads, S::kTotal, s, a);
     if (e == cudaSuccess)
       e = launch_dependent(pick_kernel<0, false>, dim3(static_cast<unsigned>(a.tok_count) * a.pool.num_kv_heads), kPickThreads, 0, s, a);
     if (e != cudaSuccess) return e;
@@ -830,7 +838,7 @@ int launch_select(const SparseArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.max_blocks <= kAloneBlocks && static_cast<int64_t>(a.num_tokens) * a.pool.num_kv_heads <= kAloneLists * static_cast<int64_t>(a.num_sms))
     return a.pool.head_dim == 128 ? launch_alone_d<128>(a, s) : launch_alone_d<64>(a, s);
-  const bool pairs = a.num_tokens / 2 >= a.num_reqs && a.pool.num_kv_heads <= kPairMaxHeads;
+  const bool pairs = a.num_tokens > a.num_reqs;
   if (a.pool.head_dim == 128) return pairs ? launch_select_d<128, 2>(a, s) : launch_select_d<128, 1>(a, s);
   return pairs ? launch_select_d<64, 2>(a, s) : launch_select_d<64, 1>(a, s);
 }

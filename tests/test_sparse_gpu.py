@@ -387,11 +387,6 @@ def test_refusals():
         args.update(kw)
         with pytest.raises(ValueError):
             pkv.pkv_sparse_attn(c.pool, c.q, scale=0.1, **args)
-    heads = pkv.Pool(2, 300, 64)
-    with pytest.raises(pkv.PkvError) as e:
-        pkv.pkv_select_blocks(heads, pkv.BlockSummary(heads), torch.zeros((1, 300, 64), dtype=torch.bfloat16, device="cuda"),
-                              pos, bt, cu, 2)
-    assert e.value.code == pkv.PKV_EUNSUPPORTED
 
 
 def test_no_tokens_is_nothing_to_do():
@@ -456,8 +451,10 @@ def test_small_batches_in_wide_tables(hq, hkv, d, dtype):
     Case(52, [(40, [39]), (700, [699]), (17, [16]), (300, [299, 298, 297])], hq, hkv, d, dtype, width=600).whole(7, 1, 1)
 
 
-def test_more_heads_than_pairs_take():
+def test_many_heads():
     Case(53, [(300, list(range(290, 300))), (40, [39, 38])], 130, 65, 64, width=600).whole(6, 1, 1)
+    Case(56, [(100, [99])], 301, 301, 64, width=600).whole(3, 1, 1)
+    Case(57, [(100, [99, 98])], 600, 300, 64).whole(3, 1, 1)
 
 
 def test_query_heads_beyond_the_staging_rows():
