@@ -63,7 +63,7 @@ def gather(vals, row, ctx, g):
     nb = (ctx + 15) // 16
     ids = row[:nb]
     good = (ids >= 0) & (ids < vals.shape[0])
-    x = vals[np.where(good, ids, 0), g].reshape(nb * 16, -1)[:ctx]
+    x = vals[np.where(good, ids, 0), g].reshape(nb * 16, vals.shape[-1])[:ctx]
     return x, np.repeat(good, 16)[:ctx]
 
 

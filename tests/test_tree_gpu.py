@@ -416,3 +416,42 @@ def test_blocks_beyond_4_gb():
     c.check(o, lse)
     assert pkv.pkv_check_device_errors(pool) == 0
     pool.close()
+
+
+def test_query_tokens_over_an_empty_cache():
+    c = Case(38, [(0, 4), (30, 6), (0, 40)], 8, 2, 128)
+    c.ctx[:] = [0, 36, 0]
+    c.prefix[:] = [0, 30, 0]
+    o, lse = c.run()
+    torch.cuda.synchronize()
+    assert pkv.pkv_check_device_errors(c.pool) == 0
+    for a, b in ((0, 4), (10, 50)):
+        assert (o[a:b] == 0).all() and (lse[a:b] == float("-inf")).all()
+    c.check(o, lse)
+
+
+def test_prefixes_out_of_range_are_flagged():
+    for prefix in (-1, 200):
+        c = Case(39, [(20, 5), (40, 3)], 8, 2, 64)
+        c.prefix[0] = prefix
+        o, lse = c.run()
+        torch.cuda.synchronize()
+        assert pkv.pkv_check_device_errors(c.pool) == pkv.PKV_DEVERR_POSITION
+        c.prefix[0] = min(max(prefix, 0), c.ctx[0])          # cut to its range
+        c.check(o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("reqs", [[(3000, 90), (1700, 200)], [(600, 20)] * 30, [(1000, 150)] * 4], ids=["long", "many", "several"])
+def test_infinite_values_that_some_rows_see_in_groups_of_every_sharing(dtype, reqs):
+    """V of NaN or infinities in tree slots, in groups that are whole, cut between CTAs, or shared out over warps."""
+    c = Case(40, reqs, 16, 8, 128, dtype, kind="random")
+    rng = np.random.default_rng(41)
+    for r in range(len(reqs)):
+        for slot in rng.integers(c.prefix[r], c.ctx[r], 3):
+            row = c.pool.v[int(c.bt[r, slot // 16]), int(rng.integers(0, 8)), int(slot) % 16]
+            if dtype == "bf16":
+                row[int(rng.integers(0, 128))] = float(rng.choice([np.inf, -np.inf, np.nan]))
+            else:
+                row[int(rng.integers(0, 128))] = 0x7F
+    c.run_check()
