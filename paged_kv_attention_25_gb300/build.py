@@ -1,4 +1,5 @@
-"""Compile the CUDA library (libpkv.so) in-tree for sm_103a.
+"""Compile the CUDA library (libpkv.so) in-tree for sm_103a, and the native
+part of the Python binding (pkv_binding.so, host code against torch's headers).
 
 Each translation unit is compiled by its own nvcc process (in parallel), then
 linked into one shared library with the CUDA runtime linked statically, so
@@ -22,6 +23,8 @@ SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_
            "ops_api.cu", "tree.cu", "tree_tc.cu", "sparse.cu", "pages.cu"]
 HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh", "ops.h", "rows.cuh", "sched.cuh",
            "tc.cuh"]
+BINDING = os.path.join(BUILD, "pkv_binding.so")
+BINDING_SOURCE = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,17 +36,43 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING_SOURCE]]
     files.append(os.path.join(ROOT, "include", "pkv.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _compile_binding():
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj,
+           "-isystem", os.path.join(home, "include"), "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_path("include"), "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           "-I", os.path.join(ROOT, "include"), f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{BINDING_SOURCE} failed:\n{r.stderr}")
+    return obj, os.path.join(home, "lib")
+
+
+def _link_binding(obj, torch_lib):
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-shared", obj, "-o", tmp, "-L", torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding link failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -65,14 +94,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, "-shared", "-cudart", "static"] + ARCH + objs + ["-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(*binding)
     return LIB
 
 

@@ -12,6 +12,7 @@ missing, every call raises RuntimeError: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -171,6 +172,26 @@ def load_library():
         return lib
 
 
+_binding = None
+
+
+def _load_binding():
+    """The native part of the binding (pkv_binding.so), for the calls that read their metadata on the device."""
+    global _binding
+    if _binding is None:
+        load_library()
+        path = os.path.join(os.path.dirname(LIB_PATH), "pkv_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"Python binding not built: {path} is missing "
+                               "(run `python -c \"import __graft_entry__ as g; g.build()\"`)")
+        spec = importlib.util.spec_from_file_location("pkv_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.set_error(PkvError)
+        _binding = mod
+    return _binding
+
+
 def pkv_last_error() -> str:
     return load_library().pkv_last_error().decode()
 
@@ -261,11 +282,11 @@ class Pool:
         self.handle = h
         self._ws = None
         self.device_index = self.k.get_device()
-        self._op_ws = {}     # workspace sizes of the device-metadata calls, by their sizes
-        self._op_buf = {}    # their workspace of each stream
 
     def close(self):
         if getattr(self, "handle", None):
+            if hasattr(self, "_ops"):
+                self._ops.close()
             load_library().pkv_pool_destroy(self.handle)
             self.handle = None
 
@@ -405,106 +426,24 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
 # calls can be captured into a graph.  Tensors live on the pool's device; without `stream` a call runs on that device's
 # current stream.  Outputs and workspaces that are not given are allocated for that stream.  The workspace of calls on a
 # current stream is kept with the pool, one for each stream: calls on one stream follow one another.  A call that is
-# being captured, or that names another stream, gets one of its own (a captured graph keeps it).
-
-_I32, _I8, _BF16, _F32, _U8 = torch.int32, torch.int8, torch.bfloat16, torch.float32, torch.uint8
-
-
-def _op_stream(pool: Pool, stream) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(pool.device_index)
-    return stream.cuda_stream
+# being captured, or that names another stream, gets one of its own (a captured graph keeps it).  The checks and the
+# marshalling are native code (csrc/binding.cpp).
 
 
-def _op_dims(t, name, n):
-    """The tensor's shape, which has n dimensions."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if len(shape) != n:
-        raise ValueError(f"{name} must have {n} dimensions")
-    return shape
-
-
-def _op_ptr(pool: Pool, t, name, dtype, shape) -> int:
-    """The address of a contiguous tensor of this type and shape on the pool's device."""
+def _ops(pool: Pool):
     try:
-        if t.dtype is dtype and t.get_device() == pool.device_index and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
+        return pool._ops
     except AttributeError:
-        pass
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
-    if t.get_device() != pool.device_index:
-        raise ValueError(f"{name} must be on the pool's device")
-    raise ValueError(f"{name} must have shape {tuple(shape)}")
-
-
-def _op_new(pool: Pool, shape, dtype, stream):
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=pool.k.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=pool.k.device)
-
-
-def _op_workspace(pool: Pool, workspace, key, size, stream):
-    """(the tensor, its bytes); key: what the size depends on."""
-    if workspace is not None:
-        n = _op_dims(workspace, "workspace", 1)[0]
-        _op_ptr(pool, workspace, "workspace", _U8, (n,))
-        return workspace, n
-    n = pool._op_ws.get(key)
-    if n is None:
-        n = pool._op_ws[key] = size(pool, *key[1:])
-    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
-        return _op_new(pool, (n,), _U8, stream), n
-    raw = torch._C._cuda_getCurrentRawStream(pool.device_index)
-    buf = pool._op_buf.get(raw)
-    if buf is None or buf.numel() < n:
-        buf = pool._op_buf[raw] = _op_new(pool, (n,), _U8, None)
-    return buf, n
-
-
-def _op_batch(pool: Pool, block_tables, cu_q_lens):
-    """(requests, table width, table pointer, cu pointer)"""
-    R = _op_dims(cu_q_lens, "cu_q_lens", 1)[0] - 1
-    if R < 0:
-        raise ValueError("cu_q_lens must hold num_reqs + 1 entries")
-    width = _op_dims(block_tables, "block_tables", 2)[1]
-    return (R, width, _op_ptr(pool, block_tables, "block_tables", _I32, (R, width)),
-            _op_ptr(pool, cu_q_lens, "cu_q_lens", _I32, (R + 1,)))
-
-
-def _op_query(pool: Pool, q, out, lse, want_lse, stream):
-    """(T, Hq, q pointer, O, LSE or None)"""
-    T, Hq, _ = _op_dims(q, "q", 3)
-    qp = _op_ptr(pool, q, "q", _BF16, (T, Hq, pool.head_dim))
-    if out is None:
-        out = _op_new(pool, (T, Hq, pool.head_dim), _BF16, stream)
-    else:
-        _op_ptr(pool, out, "out", _BF16, q.shape)
-    if lse is not None:
-        _op_ptr(pool, lse, "lse", _F32, (T, Hq))
-    elif want_lse:
-        lse = _op_new(pool, (T, Hq), _F32, stream)
-    return T, Hq, qp, out, lse
+        h = pool.handle.value if isinstance(pool.handle, ctypes.c_void_p) else pool.handle
+        pool._ops = _load_binding().Pool(h or 0, pool.device_index, pool.num_blocks, pool.num_kv_heads, pool.head_dim)
+        return pool._ops
 
 
 def pkv_tree_mask(pool: Pool, parents, cu_q_lens, mask_words=None, max_nodes=None, out=None, stream=None):
     """Mask rows [T, mask_words] (int32 bit patterns) from each node's parent (index in its tree, -1: a root).
 
     Give mask_words, or max_nodes (the largest tree's size, T if neither is given) to size the rows by."""
-    T = _op_dims(parents, "parents", 1)[0]
-    pp = _op_ptr(pool, parents, "parents", _I32, (T,))
-    R = _op_dims(cu_q_lens, "cu_q_lens", 1)[0] - 1
-    cp = _op_ptr(pool, cu_q_lens, "cu_q_lens", _I32, (R + 1,))
-    if out is None:
-        words = mask_words if mask_words is not None else max(1, ((max_nodes or T) + 31) // 32)
-        out = _op_new(pool, (T, words), _I32, stream)
-    words = _op_dims(out, "out", 2)[1]
-    op = _op_ptr(pool, out, "out", _I32, (T, words))
-    _check(load_library().pkv_tree_mask(pool.handle, pp, cp, R, T, op, words, _op_stream(pool, stream)))
-    return out
+    return _ops(pool).tree_mask(parents, cu_q_lens, mask_words, max_nodes, out, stream)
 
 
 def pkv_tree_attn_workspace_size(pool: Pool, num_q_heads: int, max_blocks: int, num_reqs: int, num_tokens: int) -> int:
@@ -519,17 +458,8 @@ def pkv_tree_attn(pool: Pool, q, block_tables, ctx_lens, prefix_lens, cu_q_lens,
     """Attention of drafted tokens: each sees slots [0, prefix_lens[r]) and the slots prefix_lens[r] + i whose bit i is
     set in its row of tree_mask [T, words] (int32 bit patterns).  Returns (O [T, Hq, D] bf16, LSE [T, Hq] fp32 or None).
     """
-    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
-    T, Hq, qp, out, lse = _op_query(pool, q, out, lse, want_lse, stream)
-    words = _op_dims(tree_mask, "tree_mask", 2)[1]
-    ctx = _op_ptr(pool, ctx_lens, "ctx_lens", _I32, (R,))
-    pre = _op_ptr(pool, prefix_lens, "prefix_lens", _I32, (R,))
-    mask = _op_ptr(pool, tree_mask, "tree_mask", _I32, (T, words))
-    ws, n = _op_workspace(pool, workspace, ("tree", Hq, width, R, T), pkv_tree_attn_workspace_size, stream)
-    _check(load_library().pkv_tree_attn(pool.handle, qp, Hq, bt, width, ctx, pre, cu, R, T, mask, words, scale,
-                                        out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), n,
-                                        _op_stream(pool, stream)))
-    return out, lse
+    return _ops(pool).tree_attn(q, block_tables, ctx_lens, prefix_lens, cu_q_lens, tree_mask, scale, out, lse, workspace,
+                                stream, bool(want_lse))
 
 
 class BlockSummary:
@@ -544,24 +474,16 @@ class BlockSummary:
             codes = torch.zeros(shape, dtype=torch.int8, device=pool.k.device)
             exps = torch.zeros(shape[:2], dtype=torch.int8, device=pool.k.device)
         self.codes, self.exps = codes, exps
-        _op_summary(pool, self)
+        _ops(pool).check_summary(codes, exps)
 
 
-def _op_summary(pool: Pool, summary):
-    shape = (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
-    return (_op_ptr(pool, summary.codes, "summary.codes", _I8, shape),
-            _op_ptr(pool, summary.exps, "summary.exps", _I8, shape[:2]))
+def _bounds(summary):
+    return (None, None) if summary is None else (summary.codes, summary.exps)
 
 
 def pkv_summarize(pool: Pool, summary: BlockSummary, block_tables, cu_q_lens, positions, ctx_lens, stream=None):
     """Recompute the bounds of every block that holds one of `positions` (after pkv_append: its own arguments)."""
-    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
-    T = _op_dims(positions, "positions", 1)[0]
-    pos = _op_ptr(pool, positions, "positions", _I32, (T,))
-    ctx = _op_ptr(pool, ctx_lens, "ctx_lens", _I32, (R,))
-    codes, exps = _op_summary(pool, summary)
-    _check(load_library().pkv_summarize(pool.handle, bt, width, R, cu, pos, ctx, T, codes, exps,
-                                        _op_stream(pool, stream)))
+    _ops(pool).summarize(*_bounds(summary), block_tables, cu_q_lens, positions, ctx_lens, stream)
 
 
 def pkv_select_blocks_workspace_size(pool: Pool, max_blocks: int, num_tokens: int) -> int:
@@ -574,20 +496,8 @@ def pkv_select_blocks(pool: Pool, summary: BlockSummary, q, q_positions, block_t
                       sinks: int = 1, recent: int = 1, out=None, workspace=None, stream=None):
     """The top_k blocks of each (token, KV head) by the bound on its scores, the first `sinks` and last `recent` always
     among them: [T, Hkv, top_k] int32 indexes into the block table, ascending, -1 beyond."""
-    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
-    T, Hq, _ = _op_dims(q, "q", 3)
-    qp = _op_ptr(pool, q, "q", _BF16, (T, Hq, pool.head_dim))
-    pos = _op_ptr(pool, q_positions, "q_positions", _I32, (T,))
-    if top_k < 1:
-        raise ValueError("top_k must be >= 1")
-    if out is None:
-        out = _op_new(pool, (T, pool.num_kv_heads, top_k), _I32, stream)
-    op = _op_ptr(pool, out, "out", _I32, (T, pool.num_kv_heads, top_k))
-    codes, exps = _op_summary(pool, summary)
-    ws, n = _op_workspace(pool, workspace, ("select", width, T), pkv_select_blocks_workspace_size, stream)
-    _check(load_library().pkv_select_blocks(pool.handle, qp, Hq, pos, bt, width, cu, R, T, codes, exps, top_k, sinks,
-                                            recent, op, ws.data_ptr(), n, _op_stream(pool, stream)))
-    return out
+    return _ops(pool).select_blocks(*_bounds(summary), q, q_positions, block_tables, cu_q_lens, top_k, sinks, recent, out,
+                                    workspace, stream)
 
 
 def pkv_sparse_attn_workspace_size(pool: Pool) -> int:
@@ -599,16 +509,8 @@ def pkv_sparse_attn_workspace_size(pool: Pool) -> int:
 def pkv_sparse_attn(pool: Pool, q, q_positions, block_tables, cu_q_lens, selected, scale: float, out=None, lse=None,
                     workspace=None, stream=None, want_lse=True):
     """Attention of each token over its selected blocks [T, Hkv, k] (keys up to its position); returns (O, LSE)."""
-    R, width, bt, cu = _op_batch(pool, block_tables, cu_q_lens)
-    T, Hq, qp, out, lse = _op_query(pool, q, out, lse, want_lse, stream)
-    pos = _op_ptr(pool, q_positions, "q_positions", _I32, (T,))
-    k = _op_dims(selected, "selected", 3)[2]
-    sel = _op_ptr(pool, selected, "selected", _I32, (T, pool.num_kv_heads, k))
-    ws, n = _op_workspace(pool, workspace, ("sparse",), pkv_sparse_attn_workspace_size, stream)
-    _check(load_library().pkv_sparse_attn(pool.handle, qp, Hq, pos, bt, width, cu, R, T, sel, k, scale, out.data_ptr(),
-                                          None if lse is None else lse.data_ptr(), ws.data_ptr(), n,
-                                          _op_stream(pool, stream)))
-    return out, lse
+    return _ops(pool).sparse_attn(q, q_positions, block_tables, cu_q_lens, selected, scale, out, lse, workspace, stream,
+                                  bool(want_lse))
 
 
 def pkv_fork_workspace_size(pool: Pool, num_rows: int, num_children: int) -> int:
@@ -622,42 +524,18 @@ def pkv_fork(pool: Pool, tables, lens, caps, parents, new_caps, refs, out_tables
     """The next generation of sequences: child i continues row parents[i] of `tables` (-1: empty) with pages for
     new_caps[i] tokens.  Shares full pages, copies partly filled ones where needed, frees what no one owns any more.
     refs [num_blocks] counts the pages' owners; out_refs defaults to refs (in place).  Returns (new tables, refs)."""
-    R, width = _op_dims(tables, "tables", 2)
-    N = _op_dims(parents, "parents", 1)[0]
-    tp = _op_ptr(pool, tables, "tables", _I32, (R, width))
-    lp = _op_ptr(pool, lens, "lens", _I32, (R,))
-    cp = _op_ptr(pool, caps, "caps", _I32, (R,))
-    pp = _op_ptr(pool, parents, "parents", _I32, (N,))
-    np_ = _op_ptr(pool, new_caps, "new_caps", _I32, (N,))
-    rp = _op_ptr(pool, refs, "refs", _I32, (pool.num_blocks,))
-    if out_refs is None:
-        out_refs = refs
-    orp = _op_ptr(pool, out_refs, "out_refs", _I32, (pool.num_blocks,))
-    if out_tables is None:
-        out_tables = _op_new(pool, (N, width), _I32, stream)
-    otp = _op_ptr(pool, out_tables, "out_tables", _I32, (N, width))
-    codes, exps = (None, None) if summary is None else _op_summary(pool, summary)
-    ws, n = _op_workspace(pool, workspace, ("fork", R, N), pkv_fork_workspace_size, stream)
-    _check(load_library().pkv_fork(pool.handle, tp, R, width, lp, cp, pp, np_, N, otp, rp, orp, codes, exps,
-                                   ws.data_ptr(), n, _op_stream(pool, stream)))
-    return out_tables, out_refs
+    return _ops(pool).fork(tables, lens, caps, parents, new_caps, refs, out_tables, out_refs, *_bounds(summary), workspace,
+                           stream)
 
 
 def pkv_copy_blocks(pool: Pool, src, dst, summary=None, stream=None):
     """Copy whole pages src[i] -> dst[i] (int32 device ids): K, V and, if given, the summary's bounds."""
-    n = _op_dims(src, "src", 1)[0]
-    sp, dp = _op_ptr(pool, src, "src", _I32, (n,)), _op_ptr(pool, dst, "dst", _I32, (n,))
-    codes, exps = (None, None) if summary is None else _op_summary(pool, summary)
-    _check(load_library().pkv_copy_blocks(pool.handle, sp, dp, n, codes, exps, _op_stream(pool, stream)))
+    _ops(pool).copy_blocks(src, dst, *_bounds(summary), stream)
 
 
 def pkv_compact(pool: Pool, block_tables, cu_keep, src_positions, dst_starts, stream=None):
     """Move the K/V rows at src_positions (ascending per request) to dst_starts[r], dst_starts[r] + 1, ..."""
-    R, width, bt, cu = _op_batch(pool, block_tables, cu_keep)
-    n = _op_dims(src_positions, "src_positions", 1)[0]
-    sp = _op_ptr(pool, src_positions, "src_positions", _I32, (n,))
-    dp = _op_ptr(pool, dst_starts, "dst_starts", _I32, (R,))
-    _check(load_library().pkv_compact(pool.handle, bt, width, R, cu, sp, dp, n, _op_stream(pool, stream)))
+    _ops(pool).compact(block_tables, cu_keep, src_positions, dst_starts, stream)
 
 
 def pkv_last_plan_stats(pool: Pool) -> dict:
@@ -811,7 +689,6 @@ def pkv_debug_set(pool: Pool, what: int, value: int):
     PKV_DEBUG_FUSED_FORM (0 per batch, 1 in-kernel append, 2 append first) or PKV_DEBUG_TREE_FORM (0 per batch, 1 rows
     of 16, 2 tiles of 128)."""
     _check(load_library().pkv_debug_set(pool.handle, int(what), int(value)))
-    pool._op_ws.clear()   # sizes may depend on it
 
 
 def pkv_profile_read(pool: Pool, reset: bool = False) -> dict:

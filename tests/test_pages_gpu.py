@@ -429,3 +429,31 @@ def test_pages_beyond_4_gb():
     assert torch.equal(pool.k[-40:], k) and torch.equal(pool.v[-40:], v)
     assert pkv.pkv_check_device_errors(pool) == 0
     pool.close()
+
+
+def test_a_closed_pool_is_refused():
+    w = World(15, 32)
+    t = ref.dev(np.zeros(1, np.int32))
+    pkv.pkv_copy_blocks(w.pool, t, t)
+    w.pool.close()
+    never = pkv.Pool(4, 1, 64)
+    never.close()
+    for pool in (w.pool, never):
+        with pytest.raises(pkv.PkvError, match="pool is NULL") as e:
+            pkv.pkv_copy_blocks(pool, t, t)
+        assert e.value.code == pkv.PKV_EINVAL
+
+
+def test_arguments_of_other_types():
+    w = World(16, 32)
+    t = ref.dev(np.zeros(1, np.int32))
+    with pytest.raises(AttributeError):
+        pkv.pkv_copy_blocks(w.pool, t, t, stream=3)
+    with pytest.raises(TypeError):
+        pkv.pkv_copy_blocks(w.pool, t, None)
+    with pytest.raises(TypeError):
+        pkv.pkv_tree_mask(w.pool, t, ref.dev(np.array([0, 1], np.int32)), mask_words="two")
+    with pytest.raises(ValueError):
+        pkv.pkv_tree_mask(w.pool, t, ref.dev(np.array([0, 1], np.int32)), mask_words=1 << 40)
+    with pytest.raises(pkv.PkvError):
+        pkv.pkv_tree_mask(w.pool, t, ref.dev(np.array([0, 1], np.int32)), mask_words=0)
