@@ -34,6 +34,7 @@ struct TreeForm {
   int ctas, cuts, slots, slot_rows;
   int many_groups;   // rows form: from so many groups on, a share a warp
   int whole;         // rows form: CTAs take whole groups, nothing is merged
+  int warps;         // rows form: warps of a CTA (4; whole groups 4, 6 or 12)
   void shrink(int n) {
     cuts = cuts / ctas * n;
     ctas = n;

@@ -93,16 +93,27 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
 // Launches as many CTAs as `groups` groups of `blocks` blocks (key tiles) can
 // occupy, both upper bounds: 16 blocks a CTA of the rows form, a tile a CTA of the
 // tiles form (an even number: quads go to pairs of CTAs).  Whole groups, a CTA
-// each, need no merge: taken where groups are short (kWholeBlocks), and for lists,
-// which are all equally long, where there are enough of them to keep the memory
-// busy (256 groups of 128 blocks: 91 us for selection and attention with shares,
-// 85 with whole groups).
+// each, need no merge.  They are taken
+//   - where groups are short (kWholeBlocks);
+//   - where a CTA of twelve warps on every SM is no more than six blocks a warp
+//     behind equal shares (with the groups' 2 heads a row, D = 128, us, shares /
+//     whole: 8 groups of 38 blocks 18.5 / 14.4, of 250 20.6 / 30.8; 32 lists of 64
+//     24.7 / 22.7, of 128 26.7 / 28.7, of 256 28.9 / 37.9; 64 groups of 126 26.5 /
+//     22.6, FP8 30.7 / 24.7; 120 lists of 128 45.7 / 41.4);
+//   - for lists, which are all equally long, where there are enough of them to keep
+//     the memory busy (256 of 128 blocks: 91 us for selection and attention with
+//     shares, 85 with whole groups).
+// An SM holds twelve warps of this kernel: as one CTA, two or three, by the number
+// of groups (two up to 64 blocks: 256 lists of 16, 22.1 us with three and 20.6 with
+// two, 280 FP8 lists of 64 92.9 and 89.7, but 256 of 128 blocks 78.3 and 79.9).
 void fit_ctas(TreeArgs& a, int64_t groups, int blocks, int num_sms) {
   const int64_t units = groups * (static_cast<int64_t>(blocks) + 2);
-  a.form.whole = !a.form.tensor && groups <= a.form.ctas && (blocks <= kWholeBlocks || (a.sel && groups >= num_sms));
+  const bool near = groups <= num_sms && blocks <= 74 + std::max<int64_t>(48, groups * blocks / num_sms);
+  a.form.whole = !a.form.tensor && groups <= a.form.ctas && (blocks <= kWholeBlocks || near || (a.sel && groups >= num_sms));
   const int64_t want = a.form.whole ? groups : a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
   a.form.shrink(static_cast<int>(std::min<int64_t>(want < 2 ? 2 : want, a.form.ctas)));
   a.ctas = a.form.ctas;
+  if (a.form.whole) a.form.warps = groups <= num_sms ? 12 : groups <= 2 * num_sms && blocks <= 64 ? 6 : 4;
 }
 
 int check_workspace(const void* workspace, size_t have, size_t need, const char* size_fn) {

@@ -35,20 +35,20 @@
 namespace pkv {
 
 constexpr int kRowTile = 16;    // query rows of a warp's tile
-constexpr int kRowWarps = 4;    // warps of a CTA, each with its own blocks and state
+constexpr int kRowWarps = 4;    // warps of a CTA, each with its own blocks and state (whole groups: up to 12)
 constexpr int kMaskNone = 0, kMaskRows = 1, kMaskKeys = 2;
 
-template <int D, bool F8>
+template <int D, bool F8, int W = kRowWarps>
 struct RowsSmem {
   static constexpr int kStages = F8 ? 4 : 2;                     // per-warp ring depth
   static constexpr int kChunk = kBlockSize * D * (F8 ? 1 : 2);   // one (block, head) of K or V
   static constexpr int kStage = 2 * kChunk;
-  static constexpr int kRing = kRowWarps * kStages * kStage;
+  static constexpr int kRing = W * kStages * kStage;
   // The warps' states are merged in the ring once it has drained.
   static constexpr int kMergeRow = D + 4;                        // o, m, l, pad (floats)
-  static constexpr int kMerge = kRowWarps * kRowTile * kMergeRow * 4;
+  static constexpr int kMerge = W * kRowTile * kMergeRow * 4;
   static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kTotal = kBuf + kRowWarps * kStages * 8 + 64 + 1024;   // + barriers, flags, alignment
+  static constexpr int kTotal = kBuf + W * kStages * 8 + 64 + 1024;   // + barriers, flags, alignment
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {

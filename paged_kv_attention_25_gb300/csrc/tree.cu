@@ -23,7 +23,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kRowsThreads = 32 * kRowWarps;
 // Rows kernel: a group has 16 query rows and one KV head; a unit is one block
 // (or one entry of a list), and a group has kGroupUnits besides, for its start
 // and end.  A request without keys keeps one empty block: its rows are written
@@ -36,10 +35,9 @@ constexpr int kRowsThreads = 32 * kRowWarps;
 //   few groups    a worker is a CTA, whose four warps take a segment's blocks in
 //                 turn and merge their states in shared memory: a quarter of the
 //                 partials of long groups.
-// Where no group can have more than kWholeBlocks blocks and there are no more
-// groups than CTAs, CTAs take whole groups and there is nothing to merge: one launch
-// less (one request, 28 rows, 15
-// blocks: 10.3 us against 11.2 with shares and a merge).
+// Where groups are short, or about as many as there are SMs, CTAs of W warps take
+// whole groups and there is nothing to merge: one launch less (one request, 28 rows,
+// 15 blocks: 9.8 us with W = 12, 10.2 with 4, 11.2 with shares and a merge).
 constexpr int kGroupUnits = 2;
 using RowsShare = Share<4 * kRowWarps>;   // few groups: four blocks a warp at least
 using WarpShare = Share<4>;
@@ -78,14 +76,15 @@ __device__ __noinline__ void rows_add_odd(const TreeArgs& a, const int32_t* bt_r
 // from HBM, 100 MB of them the second row tiles'); equal shares matter more than the
 // work per block (lists of 128 blocks for 256 groups took 62 us in clusters of
 // two CTAs: 512 CTAs leave a second, nearly empty wave; 46 us here).
-template <int D, bool F8, bool LIST>
-__global__ void __launch_bounds__(kRowsThreads, 3)
+template <int D, bool F8, bool LIST, int W>
+__global__ void __launch_bounds__(32 * W, 12 / W)
 rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-  using S = RowsSmem<D, F8>;
+  using S = RowsSmem<D, F8, W>;
+  constexpr bool kAlways = W != kRowWarps;   // always whole groups
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kBuf);
-  __shared__ int64_t scratch[2 * kRowWarps];
+  __shared__ int64_t scratch[2 * W];
   __shared__ int s_flags[2];
   volatile int* s_abort = &s_flags[0];
   int* s_odd = &s_flags[1];
@@ -94,10 +93,10 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   griddep_wait();
   griddep_launch();   // the merge may take its place and wait
   const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
-  if (tid < kRowWarps) a.cuts[blockIdx.x * kRowWarps + tid].count = 0;
+  if (!kAlways && tid < W) a.cuts[blockIdx.x * W + tid].count = 0;
   if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
   if (tid == 0) {
-    for (int i = 0; i < kRowWarps * S::kStages; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < W * S::kStages; ++i) mbar_init(&bars[i], 1);
     s_flags[0] = s_flags[1] = 0;
     fence_mbar_init();
   }
@@ -105,11 +104,12 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   auto groups = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
   auto units = [&](const TreeReq& q) { return groups(q) * (rows_blocks(q) + kGroupUnits); };
   // The shares: of this warp if there are many groups, of the CTA otherwise.
-  const int warp_id = static_cast<int>(blockIdx.x) * kRowWarps + warp, many_from = a.form.many_groups;
+  const int warp_id = static_cast<int>(blockIdx.x) * W + warp, many_from = a.form.many_groups;
   TreeShare sh;
   bool solo;
   int64_t left = 0;   // whole groups: how many the CTA still has to do
-  if (a.form.whole) {
+  const bool all_whole = kAlways || a.form.whole;
+  if (all_whole) {
     int64_t n[1], off[1];
     int reqs[1];
     auto share = [&](int64_t len, int64_t& first) {
@@ -126,7 +126,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
       share(static_cast<int64_t>(tokens) * Hkv * rtiles, first);
       sh.u = first * (a.top_k + kGroupUnits);
     } else {
-      tree_scan<kRowsThreads, 1, 1>(
+      tree_scan<32 * W, 1, 1>(
           a, scratch, n, reqs, off, [&](const TreeReq& q, int) { return groups(q); },
           [&](const int64_t (&len)[1], int, int& line, int64_t& unit) {
             share(len[0], first);
@@ -138,13 +138,14 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
     }
     sh.end = left > 0 ? INT64_MAX : 0;
     if (left == 0) sh.u = 0;
+  } else if constexpr (kAlways) {
   } else if constexpr (LIST) {
     // Every token of the requests has top_k units a group.
     const int tokens = min(max(__ldg(a.cu_q_lens + a.num_reqs), 0), a.num_tokens);
     const int64_t n = static_cast<int64_t>(tokens) * Hkv * rtiles;
     sh = TreeShare{n * (a.top_k + kGroupUnits), 0, 0, 0, 1, 0};
     solo = n >= many_from;
-    sh.workers = solo ? WarpShare::workers(sh.U, a.ctas * kRowWarps) : RowsShare::workers(sh.U, a.ctas);
+    sh.workers = solo ? WarpShare::workers(sh.U, a.ctas * W) : RowsShare::workers(sh.U, a.ctas);
     const int w = solo ? warp_id : static_cast<int>(blockIdx.x);
     if (sh.U > 0 && w < sh.workers) {
       sh.u = RowsShare::begin(sh.U, sh.workers, w);
@@ -152,20 +153,20 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
     }
   } else {
     // Line 0: units; line 1: groups (for their number alone).  Probe p: where warp p's share begins.
-    int64_t U[2], off[kRowWarps];
-    int reqs[kRowWarps];
+    int64_t U[2], off[W];
+    int reqs[W];
     auto share = [&](const int64_t (&len)[2], int p, TreeShare& t) {
       const bool alone = len[1] >= many_from;
       t.U = len[0];
-      t.workers = alone ? WarpShare::workers(len[0], a.ctas * kRowWarps) : RowsShare::workers(len[0], a.ctas);
-      const int w = alone ? static_cast<int>(blockIdx.x) * kRowWarps + p : static_cast<int>(blockIdx.x);
+      t.workers = alone ? WarpShare::workers(len[0], a.ctas * W) : RowsShare::workers(len[0], a.ctas);
+      const int w = alone ? static_cast<int>(blockIdx.x) * W + p : static_cast<int>(blockIdx.x);
       t.u = t.end = 0;
       if (len[0] > 0 && w < t.workers) {
         t.u = RowsShare::begin(len[0], t.workers, w);
         t.end = RowsShare::begin(len[0], t.workers, w + 1);
       }
     };
-    tree_scan<kRowsThreads, 2, kRowWarps>(
+    tree_scan<32 * W, 2, W>(
         a, scratch, U, reqs, off, [&](const TreeReq& q, int line) { return line == 0 ? units(q) : groups(q); },
         [&](const int64_t (&len)[2], int p, int& line, int64_t& unit) {
           TreeShare t;
@@ -176,7 +177,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
     solo = U[1] >= many_from;
     share(U, warp, sh);
 #pragma unroll
-    for (int p = 0; p < kRowWarps; ++p)
+    for (int p = 0; p < W; ++p)
       if (warp == p) {
         sh.req = reqs[p];
         sh.off = off[p];
@@ -186,7 +187,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   if (sh.u >= sh.end) return;   // a warp's (solo) or the CTA's
 
   const int worker = solo ? warp_id : static_cast<int>(blockIdx.x);
-  const int wi = solo ? 0 : warp, wn = solo ? 1 : kRowWarps;   // this warp's place among those of the segment
+  const int wi = solo ? 0 : warp, wn = solo ? 1 : W;   // this warp's place among those of the segment
   uint8_t* my_ring = ring + warp * S::kStages * S::kStage;
   uint64_t* my_bars = bars + warp * S::kStages;
   const uint32_t my_addr = smem_u32(my_ring);
@@ -196,7 +197,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
   TreeReq rq{0, 0, 0, 0, false};
   if constexpr (!LIST) rq = tree_req(a, req);
   for (; sh.u < sh.end; ) {
-    if (a.form.whole && left-- <= 0) return;
+    if (all_whole && left-- <= 0) return;
     int kblk, x, g, row0, nrows, pos = 0;   // blocks of the group, its first unit here, its rows
     const int32_t* list = nullptr;
     if constexpr (LIST) {
@@ -399,9 +400,9 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
 #pragma unroll
         for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
+        for (int w = 0; w < W; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float* src = mbuf + (w * kRowTile + rr) * S::kMergeRow;
           if (src[D + 1] == 0.f) continue;   // the warp saw no key of this row (a NaN score leaves m, not l, as it was)
           const float f = fast_exp2(src[D] - M);
@@ -430,7 +431,7 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
       }
       __syncthreads();   // the ring and the flags are free again, the rows stored
       if (!LIST && *s_odd) {
-        for (int r2 = warp; r2 < nrows; r2 += kRowWarps)
+        for (int r2 = warp; r2 < nrows; r2 += W)
           rows_add_odd<D, F8>(a, bt_row, g, rq.prefix, rq.ctx, b0, end_blk, mask_row(r2),
                               static_cast<uint16_t*>(a.o) + out_row(r2) * D,
                               whole ? nullptr : a.part_o + (slot + r2) * D, lane);
@@ -584,12 +585,20 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restric
   if (lane == 0 && t - c0 >= words * 32) atomicOr(err, PKV_DEVERR_POSITION);   // its own bit has no word
 }
 
+template <int D, bool F8, bool LIST, int W>
+int launch_rows_w(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
+  const int smem = RowsSmem<D, F8, W>::kTotal;
+  static_assert(RowsSmem<D, F8, W>::kTotal <= 232448, "shared memory of a CTA");
+  cudaError_t e = smem_attr_once<rows_kernel<D, F8, LIST, W>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(rows_kernel<D, F8, LIST, W>, dim3(a.ctas), 32 * W, smem, s, a, *tmk, *tmv);
+}
+
 template <int D, bool F8, bool LIST>
 int launch_rows_l(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
-  const int smem = RowsSmem<D, F8>::kTotal;
-  cudaError_t e = smem_attr_once<rows_kernel<D, F8, LIST>>(smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(rows_kernel<D, F8, LIST>, dim3(a.ctas), kRowsThreads, smem, s, a, *tmk, *tmv);
+  if (a.form.warps == 12) return launch_rows_w<D, F8, LIST, 12>(a, tmk, tmv, s);
+  if (a.form.warps == 6) return launch_rows_w<D, F8, LIST, 6>(a, tmk, tmv, s);
+  return launch_rows_w<D, F8, LIST, kRowWarps>(a, tmk, tmv, s);
 }
 
 template <int D, bool F8>
@@ -613,6 +622,7 @@ TreeForm tree_form(bool tensor, int num_sms) {
   f.slots = 2 * f.cuts;
   f.many_groups = f.ctas / 2;
   f.whole = 0;
+  f.warps = kRowWarps;
   return f;
 }
 

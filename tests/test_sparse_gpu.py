@@ -416,7 +416,10 @@ def test_many_groups_and_long_lists():
     rng = np.random.default_rng(47)
     reqs = [(int(n), [int(n) - 1]) for n in rng.integers(600, 2500, 70)]
     Case(47, reqs, 16, 8, 64, "fp8_e4m3").whole(40, 1, 1)        # a share a warp
-    Case(48, reqs[:25], 16, 8, 64).whole(40, 1, 1)               # a CTA a group
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("fp8_e4m3", 64), ("fp8_e4m3", 128)):
+        Case(48, reqs[:25], 16, 8, d, dtype).whole(40, 1, 1)     # a CTA of six warps a group
+        Case(48, reqs[:9], 16, 8, d, dtype).whole(40, 1, 1)      # of twelve
+    Case(48, reqs[:25], 16, 8, 64).whole(70, 1, 1)               # of four
     Case(49, reqs[:3], 16, 8, 128).whole(90, 1, 1)               # shares of CTAs
 
 

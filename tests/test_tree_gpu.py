@@ -455,3 +455,13 @@ def test_infinite_values_that_some_rows_see_in_groups_of_every_sharing(dtype, re
             else:
                 row[int(rng.integers(0, 128))] = 0x7F
     c.run_check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_whole_groups_of_six_and_twelve_warps(dtype, d):
+    rng = np.random.default_rng(42)
+    reqs = [(int(rng.integers(0, 480)), int(rng.integers(0, 9))) for _ in range(25)]
+    Case(43, reqs, 8, 8, d, dtype).run_check()               # at most 248 groups of 31 blocks
+    Case(44, reqs[:5] + [(1000, 12)], 8, 8, d, dtype, kind="random").run_check()
+    Case(45, [(1800, 9), (1700, 16), (900, 1)], 16, 16, d, dtype).run_check()   # 48 of 114
