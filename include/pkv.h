@@ -593,8 +593,8 @@ int pkv_check_device_errors(pkv_pool* pool, void* stream, unsigned* flags);
  *     (tensor-core) kernel never issues its first K copy, so that the wait for
  *     it runs out: the kernel records PKV_DEVERR_TIMEOUT, drains its copies,
  *     frees what it holds and returns, and that call's outputs are undefined;
- *     0 = off (default).  1 (2) acts on the rows (tiles) form of pkv_tree_attn
- *     in the same way, 1 on pkv_sparse_attn;
+ *     0 = off (default).  2 acts on the tiles form of pkv_tree_attn in the same
+ *     way (its rows form, pkv_sparse_attn and the calls below wait on no barrier);
  *   PKV_DEBUG_FUSED_FORM: how pkv_append_paged_attn appends: 0 = chosen per
  *     batch (default), 1 = inside the attention launches whenever the pool
  *     allows it, 2 = the append kernel first.  Every form gives the same pool

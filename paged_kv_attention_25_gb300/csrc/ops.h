@@ -42,10 +42,9 @@ struct TreeForm {
 };
 TreeForm tree_form(bool tensor, int num_sms);
 constexpr int kWholeBlocks = 32;   // blocks of a group up to which it stays whole
-// tmk / tmv: the pool's block maps (rows form: 128-byte swizzle, unused by FP8
-// pools with head_dim 64); tmq: q viewed as [T][Hq][D] in boxes of one tile.
+// tmk / tmv: the pool's block maps; tmq: q viewed as [T][Hq][D] in boxes of one tile.
 // (launch_tree_rows also runs the attention over selected blocks.)
-int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* stream);
+int launch_tree_rows(const TreeArgs& a, void* stream);
 int launch_tree_tc(const TreeArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream);
 int launch_tree_merge(const TreeArgs& a, void* stream);
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,

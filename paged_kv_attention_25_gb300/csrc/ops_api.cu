@@ -140,11 +140,6 @@ bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_to
   return rows > most * num_reqs && work > 16ll * 3 * pool->num_sms;
 }
 
-// The maps whose copies land with the 128-byte swizzle that rows.cuh reads.
-const CUtensorMap* rows_map(const pkv_pool* pool, bool v) {
-  return pool->elem_bytes == 1 ? (v ? &pool->dmap_v : &pool->dmap_k) : (v ? &pool->tmap_v : &pool->tmap_k);
-}
-
 size_t select_ws(const pkv_pool* pool, int max_blocks, int num_tokens) {
   return align256(static_cast<size_t>(select_part(num_tokens, max_blocks, pool->num_kv_heads)) * max_blocks *
                   pool->num_kv_heads * sizeof(uint32_t));
@@ -232,7 +227,7 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
     rc = timed_launch(pool, 2, stream, [&] { return launch_tree_tc(a, &pool->tmap_k, &pool->tmap_v, &tmap_q, stream); });
   } else {
     rc = timed_launch(pool, 1, stream,
-                      [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
+                      [&] { return launch_tree_rows(a, stream); });
   }
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "tree attention launch");
   if (a.form.whole) return PKV_OK;
@@ -362,7 +357,7 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
   a.o = o;
   a.lse = lse;
   rc = timed_launch(pool, 1, stream,
-                    [&] { return launch_tree_rows(a, rows_map(pool, false), rows_map(pool, true), stream); });
+                    [&] { return launch_tree_rows(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block-selected attention launch");
   if (a.form.whole) return PKV_OK;
   rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });

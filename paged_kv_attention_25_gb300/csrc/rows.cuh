@@ -3,15 +3,15 @@
 // the tree and the block-selected attention share.
 //
 // One warp holds its rows' queries as A fragments in registers, streams
-// (block, KV head) chunks of K and V from a shared-memory ring that TMA fills,
-// and keeps the rows' online softmax (running max m, sum l, fp32 accumulator
+// (block, KV head) chunks of K and V through a shared-memory ring that it fills
+// with asynchronous copies, and keeps the rows' online softmax (running max m, sum l, fp32 accumulator
 // o).  Thread t = 4g + c (g = t / 4, c = t % 4) owns rows g and g + 8.
 //
 //   S = Q K^T     16 rows x 16 keys: two n-tiles of 8 keys, D / 16 k-steps
 //   O += P V      D / 8 n-tiles of 8 dims, one k-step of 16 keys
 //
-// bf16 pools: the chunk lands through the pool's tensor map (128-byte lines,
-// 16-byte chunk x of line r at x ^ (r % 8)) and ldmatrix reads the fragments
+// bf16 pools: the chunk lies in 128-byte lines, 16-byte piece x of line r at
+// x ^ (r % 8), and ldmatrix reads the fragments
 // without bank conflicts; P is rounded to bf16 (half a step is 2^-9, and the
 // errors of different keys are independent: smaller than O's own rounding).
 //
@@ -48,7 +48,7 @@ struct RowsSmem {
   static constexpr int kMergeRow = D + 4;                        // o, m, l, pad (floats)
   static constexpr int kMerge = W * kRowTile * kMergeRow * 4;
   static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kTotal = kBuf + W * kStages * 8 + 64 + 1024;   // + barriers, flags, alignment
+  static constexpr int kTotal = kBuf + 1024;                     // + alignment
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
@@ -92,21 +92,26 @@ struct RowTile {
   bool odd;            // kMaskRows: a V element that is not finite was left out
 
   // q0, q1: rows g and g + 8 of the tile ([D] bf16), nullptr for a row that is not there.
-  __device__ __forceinline__ void init(const uint16_t* q0, const uint16_t* q1, int lane) {
+  __device__ __forceinline__ void load(const uint16_t* q0, const uint16_t* q1, int lane) {
     const int c = lane & 3;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       // Element pairs of the k-step that this thread holds (see the layouts above).
       const int d0 = F8 ? (D / 4) * c + 4 * s : 16 * s + 2 * c;
       const int d1 = F8 ? d0 + 2 : d0 + 8;
-      uint32_t w[4];
-      w[0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d0)) : 0u;
-      w[1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d0)) : 0u;
-      w[2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d1)) : 0u;
-      w[3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d1)) : 0u;
+      q[s][0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d0)) : 0u;
+      q[s][1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d0)) : 0u;
+      q[s][2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d1)) : 0u;
+      q[s][3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d1)) : 0u;
+    }
+  }
+  // The loaded queries as operands, and an empty state.
+  __device__ __forceinline__ void start() {
+    if constexpr (F8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[s][i] = F8 ? pack_f16x2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i])) : w[i];
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[s][i] = pack_f16x2(bf16lo_to_f32(q[s][i]), bf16hi_to_f32(q[s][i]));
     }
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -370,23 +375,35 @@ struct RowTile {
   }
 };
 
-// Copies chunk `chunk` (block * kv heads + head) of K and V into a stage; one lane.
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Copies chunk `chunk` (block * kv heads + head) of K and V into the stage at shared
+// address dst; a whole warp, 512 bytes an instruction.  (One lane's tensor copies,
+// with the barriers around them, took 1200 of a warp's 3900 cycles for two FP8
+// blocks, and boxes of 2 KB arrive at 26 bytes a clock and SM at most.)
 template <int D, bool F8>
-__device__ __forceinline__ void rows_issue(const PoolView& pool, const void* tmk, const void* tmv, uint8_t* dst,
-                                           int64_t chunk, uint64_t* bar) {
-  using S = RowsSmem<D, F8>;
-  // Earlier generic reads of the stage come before the copy's writes.
-  fence_proxy_async_smem();
-  mbar_arrive_expect_tx(bar, 2 * S::kChunk);
-  if constexpr (!F8 && D == 128) {
-    tma_load_4d(dst, tmk, 0, 0, 0, static_cast<int>(2 * chunk), bar);
-    tma_load_4d(dst + S::kChunk, tmv, 0, 0, 0, static_cast<int>(2 * chunk), bar);
-  } else if constexpr (!F8 || D == 128) {
-    tma_load_2d(dst, tmk, 0, static_cast<int>(chunk * kBlockSize), bar);
-    tma_load_2d(dst + S::kChunk, tmv, 0, static_cast<int>(chunk * kBlockSize), bar);
-  } else {
-    bulk_g2s(dst, static_cast<const uint8_t*>(pool.k) + chunk * S::kChunk, S::kChunk, bar);
-    bulk_g2s(dst + S::kChunk, static_cast<const uint8_t*>(pool.v) + chunk * S::kChunk, S::kChunk, bar);
+__device__ __forceinline__ void rows_copy(const PoolView& pool, uint32_t dst, int chunk, int lane) {
+  constexpr int kBytes = RowsSmem<D, F8>::kChunk;
+  constexpr int kRow = D * (F8 ? 1 : 2);   // bytes of a key's row
+  const int64_t at = static_cast<int64_t>(chunk) * kBytes + lane * 16;
+  const uint8_t* k = static_cast<const uint8_t*>(pool.k) + at;
+  const uint8_t* v = static_cast<const uint8_t*>(pool.v) + at;
+  // Where the lane's 16 bytes go: rows of 64 bytes as they are; of 128, chunk c of row r at c ^ (r % 8); of 256 in
+  // two halves of that kind, eight rows of each together.
+  uint32_t to;
+  if constexpr (kRow == 64) to = lane * 16;
+  else if constexpr (kRow == 128) to = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+  else to = ((lane & 15) >> 3) * 1024 + (lane >> 4) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+#pragma unroll
+  for (int i = 0; i < kBytes / 512; ++i) {
+    uint32_t off;
+    if constexpr (kRow == 64) off = to + i * 512;
+    else if constexpr (kRow == 128) off = (to ^ ((i & 1) * 64)) + i * 512;
+    else off = (to ^ (((2 * i) & 7) << 4)) + (i >> 2) * 2048 + ((2 * i) & 7) * 128;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + off), "l"(k + i * 512) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + kBytes + off), "l"(v + i * 512) : "memory");
   }
 }
 

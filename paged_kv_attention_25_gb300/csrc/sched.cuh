@@ -47,7 +47,7 @@ struct TreeArgs {
   int q_box_tokens;  // ... and of a copy of its query map
   int o_align32;     // o is 32-byte aligned
   uint64_t wait_ns;
-  int withhold;      // test hook: 1 / 2 = CTA 0 of the rows / tiles form skips its first (K) copy
+  int withhold;      // test hook: 2 = CTA 0 of the tiles form skips its first K copy
 };
 
 // A group that several workers share: rows [0, rows_a) and [128, 128 + rows_b)

@@ -8,7 +8,6 @@
 //   LSE = m + ln sum_j exp(s_j - m)       over the slots that the token sees;
 //
 // a token that sees none has O = 0 and LSE = -inf.
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -78,28 +77,19 @@ __device__ __noinline__ void rows_add_odd(const TreeArgs& a, const int32_t* bt_r
 // two CTAs: 512 CTAs leave a second, nearly empty wave; 46 us here).
 template <int D, bool F8, bool LIST, int W>
 __global__ void __launch_bounds__(32 * W, 12 / W)
-rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+rows_kernel(const TreeArgs a) {
   using S = RowsSmem<D, F8, W>;
   constexpr bool kAlways = W != kRowWarps;   // always whole groups
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kBuf);
   __shared__ int64_t scratch[2 * W];
-  __shared__ int s_flags[2];
-  volatile int* s_abort = &s_flags[0];
-  int* s_odd = &s_flags[1];
+  __shared__ int s_odd;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, Hkv = a.pool.num_kv_heads;
   griddep_wait();
   griddep_launch();   // the merge may take its place and wait
-  const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
   if (!kAlways && tid < W) a.cuts[blockIdx.x * W + tid].count = 0;
-  if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
-  if (tid == 0) {
-    for (int i = 0; i < W * S::kStages; ++i) mbar_init(&bars[i], 1);
-    s_flags[0] = s_flags[1] = 0;
-    fence_mbar_init();
-  }
+  if (tid == 0) s_odd = 0;
   const int rtiles = (G + kRowTile - 1) / kRowTile;   // LIST: row tiles of a token's group
   auto groups = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
   auto units = [&](const TreeReq& q) { return groups(q) * (rows_blocks(q) + kGroupUnits); };
@@ -183,16 +173,13 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
         sh.off = off[p];
       }
   }
-  __syncthreads();   // barriers initialised
+  __syncthreads();   // s_odd, and scratch is free
   if (sh.u >= sh.end) return;   // a warp's (solo) or the CTA's
 
   const int worker = solo ? warp_id : static_cast<int>(blockIdx.x);
   const int wi = solo ? 0 : warp, wn = solo ? 1 : W;   // this warp's place among those of the segment
-  uint8_t* my_ring = ring + warp * S::kStages * S::kStage;
-  uint64_t* my_bars = bars + warp * S::kStages;
-  const uint32_t my_addr = smem_u32(my_ring);
+  const uint32_t my_ring = smem_u32(ring) + warp * S::kStages * S::kStage;
   const float sl2 = F8 ? a.scale_log2 * a.pool.k_scale : a.scale_log2;
-  int cnt = 0;   // stages this warp has issued in the launch
   int req = LIST ? 0 : sh.req;
   TreeReq rq{0, 0, 0, 0, false};
   if constexpr (!LIST) rq = tree_req(a, req);
@@ -249,7 +236,9 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
     const int live = max(0, end_blk - b0);
     const int nb_w = live > wi ? (live - wi + wn - 1) / wn : 0;
     const int32_t* bt_row = a.block_tables + static_cast<int64_t>(req) * a.max_blocks;
-    // Lane l: the pool block (-1: none) of the warp's iteration base + l, and the block's index in the request.
+    // Windows of 32 iterations: lane l holds the chunk of iteration base + l (-1: no such block) and the block's index
+    // in the request; `there` and `plain` are the window's iterations that have a block, and those whose block every
+    // row sees whole, as bits.  (A shuffle for each of these in every iteration took 300 of a pair's 3900 cycles.)
     auto load_ids = [&](int base, int& blk) -> int {
       const int i = base + lane;
       blk = -1;
@@ -268,90 +257,71 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
         atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
         return -1;
       }
-      return pb;
+      return pb * Hkv + g;
     };
     int blk_cur, blk_next, win = 0;
-    int ids_cur = load_ids(0, blk_cur), ids_next = load_ids(32, blk_next);
-    auto id_of = [&](int j) {   // warp-uniform j
-      return __shfl_sync(0xffffffffu, (j >> 5) == win ? ids_cur : ids_next, j & 31);
+    int chunk_cur = load_ids(0, blk_cur), chunk_next = load_ids(32, blk_next);
+    uint32_t there, plain;
+    auto look = [&] {
+      const bool has = chunk_cur >= 0;
+      there = __ballot_sync(0xffffffffu, has);
+      const int blk = LIST ? blk_cur : b0 + wi + wn * (32 * win + lane);
+      plain = __ballot_sync(0xffffffffu, has && (LIST ? pos - blk * kBlockSize + 1 >= kBlockSize
+                                                      : (blk + 1) * kBlockSize <= rq.prefix));
     };
-    auto issue = [&](int j) {
-      const int pb = id_of(j);
-      // Test hook: CTA 0's first warp never issues its first copy, so that its bounded wait for it runs out.
-      const bool withheld = a.withhold == 1 && blockIdx.x == 0 && warp == 0 && cnt + j == 0;
-      if (lane == 0 && !withheld) {
-        const int st = (cnt + j) % S::kStages;
-        if (pb >= 0)
-          rows_issue<D, F8>(a.pool, &tmk, &tmv, my_ring + st * S::kStage, static_cast<int64_t>(pb) * Hkv + g,
-                            &my_bars[st]);
-        else
-          mbar_arrive(&my_bars[st]);   // no such block: its keys are seen by no row
-      }
-    };
-    int issued = 0;
-    for (; issued < S::kStages && issued < nb_w; ++issued) issue(issued);
+    look();
     RowTile<D, F8> rt;
-    rt.init(q_row(ra), q_row(rb), lane);
+    rt.load(q_row(ra), q_row(rb), lane);   // asked for before the first blocks
+    // One group of copies an iteration (an empty one for a block that is not there, and behind the last).
+    auto copy = [&](int j) {
+      const int chunk = __shfl_sync(0xffffffffu, (j >> 5) == win ? chunk_cur : chunk_next, j & 31);
+      if (j < nb_w && chunk >= 0)
+        rows_copy<D, F8>(a.pool, my_ring + static_cast<uint32_t>(j) % S::kStages * S::kStage, chunk, lane);
+      cp_commit();
+    };
+    for (int j = 0; j < S::kStages; ++j) copy(j);
+    rt.start();
     const uint32_t* m0 = LIST ? nullptr : mask_row(ra);
     const uint32_t* m1 = LIST ? nullptr : mask_row(rb);
-    bool ok = true;
-    // Keys of the warp's iteration i that the rows see: whole blocks, or masked ones.
-    auto whole_block = [&](int i) -> bool {   // there, and seen whole by every row
-      if (__shfl_sync(0xffffffffu, ids_cur, i & 31) < 0) return false;
-      if constexpr (LIST) return pos - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1 >= kBlockSize;
-      else return (b0 + wi + wn * i + 1) * kBlockSize <= rq.prefix;
-    };
     for (int i = 0; i < nb_w; ++i) {
       if ((i & 31) == 0 && i > 0) {
-        ids_cur = ids_next;
+        chunk_cur = chunk_next;
         blk_cur = blk_next;
         win = i >> 5;
-        ids_next = load_ids(i + 32, blk_next);
+        look();
+        chunk_next = load_ids(i + 32, blk_next);
       }
-      const int st = (cnt + i) % S::kStages;
-      if (!(ok = mbar_wait_warp(&my_bars[st], ((cnt + i) / S::kStages) & 1, s_abort, a.wait_ns))) break;
-      const uint32_t kb = my_addr + st * S::kStage;
-      const bool plain = whole_block(i);
-      if (F8 && plain && (i & 31) != 31 && i + 1 < nb_w && whole_block(i + 1)) {
-        // FP8: two blocks at once.  Half the shuffles and votes, and two chains of products and conversions to
-        // interleave (the warps wait for fixed latencies most of the time): 101 -> 99 us for FP8 trees.
-        const int st1 = (cnt + i + 1) % S::kStages;
-        if (!(ok = mbar_wait_warp(&my_bars[st1], ((cnt + i + 1) / S::kStages) & 1, s_abort, a.wait_ns))) break;
-        const uint32_t kb1 = my_addr + st1 * S::kStage;
-        rt.template block<kMaskNone, 2>(kb, kb + S::kChunk, sl2, 0u, 0u, lane, kb1, kb1 + S::kChunk);
-        ++i;
+      const uint32_t bit = 1u << (i & 31);
+      const uint32_t kb = my_ring + static_cast<uint32_t>(i) % S::kStages * S::kStage;
+      // FP8: two blocks at once where both are seen whole.  Half the shuffles and votes, and two chains of products
+      // and conversions to interleave (the warps wait for fixed latencies most of the time).
+      if (F8 && (plain & bit) && (plain & (bit << 1)) && i + 1 < nb_w) {
+        cp_wait<S::kStages - 2>();
         __syncwarp();
-        if (issued < nb_w) {
-          issue(issued);
-          ++issued;
+        const uint32_t kb1 = my_ring + static_cast<uint32_t>(i + 1) % S::kStages * S::kStage;
+        rt.template block<kMaskNone, 2>(kb, kb + S::kChunk, sl2, 0u, 0u, lane, kb1, kb1 + S::kChunk);
+        __syncwarp();   // the stages have been read
+        copy(i + S::kStages);
+        ++i;
+      } else {
+        cp_wait<S::kStages - 1>();
+        __syncwarp();
+        if (plain & bit) {
+          rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
+        } else if (there & bit) {
+          if constexpr (LIST) {
+            const int seen = pos - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1;   // keys up to the position
+            rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
+          } else {
+            const int key0 = (b0 + wi + wn * i) * kBlockSize;
+            rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
+                                         tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
+          }
         }
-      } else if (plain) {
-        rt.template block<kMaskNone>(kb, kb + S::kChunk, sl2, 0u, 0u, lane);
-      } else if (__shfl_sync(0xffffffffu, ids_cur, i & 31) >= 0) {
-        if constexpr (LIST) {
-          const int seen = pos - __shfl_sync(0xffffffffu, blk_cur, i & 31) * kBlockSize + 1;   // keys up to the position
-          rt.template block<kMaskKeys>(kb, kb + S::kChunk, sl2, (1u << seen) - 1u, (1u << seen) - 1u, lane);
-        } else {
-          const int key0 = (b0 + wi + wn * i) * kBlockSize;
-          rt.template block<kMaskRows>(kb, kb + S::kChunk, sl2, tree_sees(rq.prefix, rq.ctx, m0, a.mask_words, key0),
-                                       tree_sees(rq.prefix, rq.ctx, m1, a.mask_words, key0), lane);
-        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (issued < nb_w) {
-        issue(issued);
-        ++issued;
-      }
+      copy(i + S::kStages);
     }
-    if (!ok) {
-      // Gave up: let the copies in flight land, then leave.
-      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
-      *s_abort = 1;
-      for (int j = max(0, issued - S::kStages); j < issued; ++j)
-        (void)mbar_wait(&my_bars[(cnt + j) % S::kStages], ((cnt + j) / S::kStages) & 1, nullptr, a.wait_ns);
-      if (solo) return;
-    }
-    cnt += nb_w;
     const bool whole = b0 == 0 && b1 == kblk;
     const int64_t slot = (2 * static_cast<int64_t>(worker) + (b0 == 0 ? 1 : 0)) * kRowTile;
     auto out_row = [&](int rr) {   // row index of O and LSE
@@ -386,9 +356,8 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
                               whole ? nullptr : a.part_o + (slot + rr) * D, lane);
       }
     } else {
-      if (!LIST && rt.odd) *s_odd = 1;
+      if (!LIST && rt.odd) s_odd = 1;
       __syncthreads();   // every warp's ring has drained
-      if (*s_abort) return;
       // Merge the warps' states: [warp][16][D + 4] floats over the ring.
       float* mbuf = reinterpret_cast<float*>(ring);
       rt.store(mbuf + warp * kRowTile * S::kMergeRow, lane);
@@ -430,15 +399,14 @@ rows_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __g
         }
       }
       __syncthreads();   // the ring and the flags are free again, the rows stored
-      if (!LIST && *s_odd) {
+      if (!LIST && s_odd) {
         for (int r2 = warp; r2 < nrows; r2 += W)
           rows_add_odd<D, F8>(a, bt_row, g, rq.prefix, rq.ctx, b0, end_blk, mask_row(r2),
                               static_cast<uint16_t*>(a.o) + out_row(r2) * D,
                               whole ? nullptr : a.part_o + (slot + r2) * D, lane);
         __syncthreads();
-        if (tid == 0) *s_odd = 0;
+        if (tid == 0) s_odd = 0;
       }
-      fence_proxy_async_smem();
       __syncthreads();
     }
     if (b0 == 0 && b1 < kblk && lane == 0 && (solo || warp == 0)) {   // the group's first part: its other owners follow
@@ -474,7 +442,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   const int4* rec = reinterpret_cast<const int4*>(a.cuts + blockIdx.x);
   const int4 s = __ldcg(rec);
   const int4 tk = __ldcg(rec + 1), fg = __ldcg(rec + 2);
-  if (s.x < 2 || (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT)) return;   // (partials may be incomplete)
+  if (s.x < 2) return;
+  if (SlotRows >= 128 && (__ldcg(a.pool.err) & PKV_DEVERR_TIMEOUT)) return;   // (partials may be incomplete)
   // The rows of a warp lie in one tile (kRows divides 128).
   const int tok = row0 < 128 ? tk.x : tk.z, rows = row0 < 128 ? tk.y : tk.w, i0 = row0 & 127;
   if (i0 >= rows) return;
@@ -586,24 +555,24 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restric
 }
 
 template <int D, bool F8, bool LIST, int W>
-int launch_rows_w(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
+int launch_rows_w(const TreeArgs& a, cudaStream_t s) {
   const int smem = RowsSmem<D, F8, W>::kTotal;
   static_assert(RowsSmem<D, F8, W>::kTotal <= 232448, "shared memory of a CTA");
   cudaError_t e = smem_attr_once<rows_kernel<D, F8, LIST, W>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(rows_kernel<D, F8, LIST, W>, dim3(a.ctas), 32 * W, smem, s, a, *tmk, *tmv);
+  return launch_dependent(rows_kernel<D, F8, LIST, W>, dim3(a.ctas), 32 * W, smem, s, a);
 }
 
 template <int D, bool F8, bool LIST>
-int launch_rows_l(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
-  if (a.form.warps == 12) return launch_rows_w<D, F8, LIST, 12>(a, tmk, tmv, s);
-  if (a.form.warps == 6) return launch_rows_w<D, F8, LIST, 6>(a, tmk, tmv, s);
-  return launch_rows_w<D, F8, LIST, kRowWarps>(a, tmk, tmv, s);
+int launch_rows_l(const TreeArgs& a, cudaStream_t s) {
+  if (a.form.warps == 12) return launch_rows_w<D, F8, LIST, 12>(a, s);
+  if (a.form.warps == 6) return launch_rows_w<D, F8, LIST, 6>(a, s);
+  return launch_rows_w<D, F8, LIST, kRowWarps>(a, s);
 }
 
 template <int D, bool F8>
-int launch_rows(const TreeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s) {
-  return a.sel ? launch_rows_l<D, F8, true>(a, tmk, tmv, s) : launch_rows_l<D, F8, false>(a, tmk, tmv, s);
+int launch_rows(const TreeArgs& a, cudaStream_t s) {
+  return a.sel ? launch_rows_l<D, F8, true>(a, s) : launch_rows_l<D, F8, false>(a, s);
 }
 
 template <int D, int SlotRows>
@@ -626,13 +595,11 @@ TreeForm tree_form(bool tensor, int num_sms) {
   return f;
 }
 
-int launch_tree_rows(const TreeArgs& a, const void* tmk, const void* tmv, void* stream) {
+int launch_tree_rows(const TreeArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const CUtensorMap* k = static_cast<const CUtensorMap*>(tmk);
-  const CUtensorMap* v = static_cast<const CUtensorMap*>(tmv);
   const bool f8 = a.pool.elem_bytes == 1;
-  if (a.pool.head_dim == 128) return f8 ? launch_rows<128, true>(a, k, v, s) : launch_rows<128, false>(a, k, v, s);
-  return f8 ? launch_rows<64, true>(a, k, v, s) : launch_rows<64, false>(a, k, v, s);
+  if (a.pool.head_dim == 128) return f8 ? launch_rows<128, true>(a, s) : launch_rows<128, false>(a, s);
+  return f8 ? launch_rows<64, true>(a, s) : launch_rows<64, false>(a, s);
 }
 
 int launch_tree_merge(const TreeArgs& a, void* stream) {

@@ -340,20 +340,6 @@ def test_all_blocks_selected_equals_the_causal_attention():
     c.check_attend(sel, po, pl)
 
 
-def test_wait_that_runs_out_is_reported_and_the_pool_recovers():
-    c = Case(43, [(2000, [1999]), (700, [699])], 8, 2, 128)
-    c.summarize()
-    sel = c.select(48, 1, 1)
-    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 2_000_000)
-    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WITHHOLD_COPY, 1)
-    c.attend(sel)
-    assert pkv.pkv_check_device_errors(c.pool) & pkv.PKV_DEVERR_TIMEOUT
-    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WITHHOLD_COPY, 0)
-    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
-    o, lse = c.attend(sel)
-    c.check_attend(sel, o, lse)
-
-
 def test_refusals():
     c = Case(44, [(100, [99])], 8, 2, 64)
     pos, bt, cu = ref.dev(c.pos), ref.dev(c.bt), ref.dev(c.cu)

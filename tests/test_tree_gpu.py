@@ -282,6 +282,8 @@ def test_mask_from_parents(words):
 
 
 def test_wait_that_runs_out_is_reported_and_the_pool_recovers():
+    if Case.form == 1:
+        return                                            # the rows form waits on no barrier
     for dtype in ("bf16", "fp8_e4m3"):
         c = Case(30, [(3000, 20), (500, 33), (40, 3)], 8, 2, 128, dtype)
         pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_WAIT_LIMIT_NS, 2_000_000)
