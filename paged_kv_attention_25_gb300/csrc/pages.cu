@@ -434,6 +434,8 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const PoolView pool, u
                                                           const int32_t* __restrict__ dst, int8_t* codes,
                                                           int8_t* exps) {
   const int tid = threadIdx.x;
+  griddep_wait();
+  griddep_launch();
   const int s = __ldg(src + blockIdx.x), d = __ldg(dst + blockIdx.x);
   if (s < 0 || s >= pool.num_blocks || d < 0 || d >= pool.num_blocks) {
     if (tid == 0) atomicOr(pool.err, PKV_DEVERR_BLOCK_ID);
@@ -476,6 +478,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const PoolView pool, uint4
   const int cols = 2 * pool.num_kv_heads * cpr;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int r = static_cast<int>(e / cols);
+  griddep_wait();
+  griddep_launch();
   if (r >= num_reqs) return;
   const int col = static_cast<int>(e % cols);
   const int ch = col % cpr, g = (col / cpr) % pool.num_kv_heads;
@@ -543,19 +547,17 @@ int launch_copy_blocks(const PoolView& pool, void* kp, void* vp, const int32_t* 
                        int8_t* codes, int8_t* exps, void* stream) {
   const int64_t chunks = static_cast<int64_t>(2) * pool.num_kv_heads * kBlockSize * pool.head_dim * pool.elem_bytes / 16;
   const dim3 grid(n, static_cast<unsigned>((chunks + 256 * kCopyBatch - 1) / (256 * kCopyBatch)));
-  copy_blocks_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(pool, static_cast<uint4*>(kp),
-                                                                       static_cast<uint4*>(vp), src, dst, codes, exps);
-  return cudaGetLastError();
+  return launch_dependent(copy_blocks_kernel, grid, 256, 0, static_cast<cudaStream_t>(stream), pool,
+                          static_cast<uint4*>(kp), static_cast<uint4*>(vp), src, dst, codes, exps);
 }
 
 int launch_compact(const PoolView& pool, void* kp, void* vp, const int32_t* block_tables, int max_blocks, int num_reqs,
                    const int32_t* cu_keep, const int32_t* src, const int32_t* dst, int num_kept, void* stream) {
   const int64_t cols = static_cast<int64_t>(2) * pool.num_kv_heads * (pool.head_dim * pool.elem_bytes / 16);
   const int64_t grid = (cols * num_reqs + 255) / 256;
-  compact_kernel<<<static_cast<unsigned>(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-      pool, static_cast<uint4*>(kp), static_cast<uint4*>(vp), block_tables, max_blocks, num_reqs, cu_keep, src, dst,
-      num_kept);
-  return cudaGetLastError();
+  return launch_dependent(compact_kernel, dim3(static_cast<unsigned>(grid)), 256, 0, static_cast<cudaStream_t>(stream), pool,
+                          static_cast<uint4*>(kp), static_cast<uint4*>(vp), block_tables, max_blocks, num_reqs, cu_keep,
+                          src, dst, num_kept);
 }
 
 }  // namespace pkv

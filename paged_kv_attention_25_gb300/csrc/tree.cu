@@ -529,6 +529,8 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restric
                                                         uint32_t* __restrict__ mask, int words, unsigned* err) {
   const int lane = threadIdx.x & 31;
   const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+  griddep_wait();
+  griddep_launch();
   if (t >= num_tokens) return;
   int lo = 0, hi = num_reqs - 1;
   while (lo < hi) {
@@ -612,9 +614,8 @@ int launch_tree_merge(const TreeArgs& a, void* stream) {
 
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
                      unsigned* err, void* stream) {
-  tree_mask_kernel<<<(num_tokens + 7) / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(parents, cu, num_reqs,
-                                                                                        num_tokens, mask, words, err);
-  return cudaGetLastError();
+  return launch_dependent(tree_mask_kernel, dim3((num_tokens + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream), parents,
+                          cu, num_reqs, num_tokens, mask, words, err);
 }
 
 }  // namespace pkv

@@ -457,3 +457,59 @@ def test_arguments_of_other_types():
         pkv.pkv_tree_mask(w.pool, t, ref.dev(np.array([0, 1], np.int32)), mask_words=1 << 40)
     with pytest.raises(pkv.PkvError):
         pkv.pkv_tree_mask(w.pool, t, ref.dev(np.array([0, 1], np.int32)), mask_words=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
+def test_calls_that_follow_one_another_see_what_the_last_one_wrote(dtype):
+    """Moves, copies, forks, bounds, selections and attention without a wait between them, and with one: the same bits."""
+    got = []
+    for wait in (False, True):
+        torch.manual_seed(17)                             # (the bounds that World makes up)
+        w = World(17, 200, 8, 128, dtype, width=24)
+        w.step([-1] * 6, [300] * 6)
+        w.grow([300] * 6)
+        rng = np.random.default_rng(18)
+        bt, lens, caps, refs = ref.dev(w.tables), ref.dev(w.lens), ref.dev(w.caps), ref.dev(w.refs)
+        tabs, counts = [bt, torch.zeros_like(bt)], [refs, torch.zeros_like(refs)]
+        cu = ref.dev(np.arange(7).astype(np.int32))
+        pos = ref.dev(np.full(6, 299, np.int32))
+        same = ref.dev(np.arange(6).astype(np.int32))
+        every = ref.dev(np.tile(np.arange(0, 300, 16), 6).astype(np.int32))
+        every_cu = ref.dev((np.arange(7) * 19).astype(np.int32))
+        q = torch.randn((6, 16, 128), generator=torch.Generator().manual_seed(19)).to(torch.bfloat16).cuda()
+        mask = torch.full((6, 1), -1, dtype=torch.int32, device="cuda")
+        prefix = ref.dev(np.full(6, 290, np.int32))
+        moves = []
+        for _ in range(20):
+            src = np.concatenate([np.sort(rng.choice(np.arange(100, 300), 40, replace=False)) for _ in range(6)]).astype(np.int32)
+            moves.append((ref.dev((np.arange(7) * 40).astype(np.int32)), ref.dev(src),
+                          ref.dev(rng.integers(0, 100, 6).astype(np.int32))))
+        torch.cuda.synchronize()
+        outs = []
+
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+
+        for k, (mcu, src, dst) in enumerate(moves):
+            t, r = tabs[k % 2], counts[k % 2]
+            pkv.pkv_compact(w.pool, t, mcu, src, dst)
+            done()
+            pkv.pkv_summarize(w.pool, w.sum, t, every_cu, every, lens)
+            done()
+            sel = pkv.pkv_select_blocks(w.pool, w.sum, q, pos, t, cu, 6)
+            done()
+            outs += [sel, *pkv.pkv_sparse_attn(w.pool, q, pos, t, cu, sel, 0.1)]
+            done()
+            outs += list(pkv.pkv_tree_attn(w.pool, q, t, lens, prefix, cu, mask, 0.1))
+            done()
+            pkv.pkv_fork(w.pool, t, lens, caps, same, lens, r, out_tables=tabs[(k + 1) % 2], out_refs=counts[(k + 1) % 2],
+                         summary=w.sum)
+            done()
+            pkv.pkv_copy_blocks(w.pool, same + 190, same + 180, summary=w.sum)
+            done()
+        torch.cuda.synchronize()
+        assert pkv.pkv_check_device_errors(w.pool) == 0
+        got.append([x.view(torch.uint8).clone() for x in outs + [w.pool.k, w.pool.v, w.sum.codes, w.sum.exps] + tabs + counts])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
