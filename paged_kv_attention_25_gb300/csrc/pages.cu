@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
 // The same for up to kPlanThreads rows and children: thread i has row i and
 // child i in registers, so that the chain is three reads long: lengths and
 // parents, tables, counts.  4 rows of 8 pages: 8.3 us with the fill (the general
-// kernel: 10); 240 rows of up to 130: 14.4 (19); 1024 rows of 16: 21.
+// kernel: 10); 240 rows of up to 130: 14.4 (19), of which the additions to 7 thousand
+// counts, from one SM, are 4 and the first read behind them 2; 1024 rows of 16: 21.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const ForkArgs a) {
   __shared__ int s_warp[32];
   __shared__ int s_kids[kPlanThreads], s_first[kPlanThreads], s_keeper[kPlanThreads];
