@@ -46,6 +46,13 @@ struct TreeForm {
 };
 TreeForm tree_form(bool tensor, int num_sms);
 constexpr int kWholeBlocks = 32;   // blocks of a group up to which it stays whole
+// Rows form: the record of a group that CTA `block` of W warps (`solo`: its warp
+// `warp` by itself) begins and others go on with.  It is one of the CTA's own W
+// records, which the CTA clears when it starts: no other CTA writes them.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int cut_record(int block, int W, bool solo, int warp) { return block * W + (solo ? warp : 0); }
 // tmk / tmv: the pool's block maps; tmq: q viewed as [T][Hq][D] in boxes of one tile.
 // (launch_tree_rows also runs the attention over selected blocks.)
 int launch_tree_rows(const TreeArgs& a, void* stream);

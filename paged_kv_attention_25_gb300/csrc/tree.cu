@@ -88,7 +88,7 @@ rows_kernel(const TreeArgs a) {
   const int G = a.group, Hkv = a.pool.num_kv_heads;
   griddep_wait();
   griddep_launch();   // the merge may take its place and wait
-  if (!kAlways && tid < W) a.cuts[blockIdx.x * W + tid].count = 0;
+  if (!kAlways && tid < W) a.cuts[cut_record(blockIdx.x, W, true, tid)].count = 0;
   if (tid == 0) s_odd = 0;
   const int rtiles = (G + kRowTile - 1) / kRowTile;   // LIST: row tiles of a token's group
   auto groups = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
@@ -412,7 +412,7 @@ rows_kernel(const TreeArgs a) {
     if (b0 == 0 && b1 < kblk && lane == 0 && (solo || warp == 0)) {   // the group's first part: its other owners follow
       // (the last block names the last owner; those between each have a block, a share being longer than the fixed units)
       const int c1 = RowsShare::owner(sh.U, sh.workers, gbegin + kblk - 1);
-      TreeCut& cut = a.cuts[worker];
+      TreeCut& cut = a.cuts[cut_record(blockIdx.x, W, solo, warp)];
       cut.first = 2 * worker + 1;
       cut.next = 2 * (worker + 1);
       cut.stride = 2;
