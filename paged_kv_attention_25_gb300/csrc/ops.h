@@ -8,11 +8,14 @@ namespace pkv {
 struct TreeArgs;
 
 // Launches a kernel that may be scheduled before the one ahead of it in the
-// stream ends: it begins with griddep_wait().  What the one ahead may have read
-// and then written must not be read through the non-coherent path (__ldg): pool
-// values are read by copies that bypass L1, TMA or plain loads, results of the
-// kernel ahead with __ldcg.  (summarize_kernel, which reads keys with __ldg, is
-// launched without this.)
+// stream ends: it begins with griddep_wait().  What a kernel that releases its
+// dependents early (griddep_launch) writes must not be read through the
+// non-coherent path (__ldg) by the next: queries (they may be an output), mask
+// words, lists, bounds, owners' counts and pool values are read with plain loads,
+// __ldcg, cp.async or TMA, which see the writes behind griddep_wait().  Tables,
+// lengths, positions and ids may be read with __ldg: of these calls only the
+// fork's fill writes any (tables), and it lets nothing start before it ends.
+// (summarize_kernel, which reads keys with __ldg, is launched without this.)
 #ifdef __CUDACC__
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s,

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
     first[r] = 0x7fffffff;
   }
   if (a.new_refs != a.refs)
-    for (int i = tid; i < nb; i += kPlanThreads) a.new_refs[i] = __ldg(a.refs + i);
+    for (int i = tid; i < nb; i += kPlanThreads) a.new_refs[i] = __ldcg(a.refs + i);   // (a fork ahead may have written them)
   __syncthreads();
   for (int i = tid; i < a.num_children; i += kPlanThreads) {
     const int p = __ldg(a.parents + i);
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
   int parent = is_child ? __ldg(a.parents + tid) : -1;
   const int new_cap = is_child ? __ldg(a.new_caps + tid) : 0;
   if (a.new_refs != a.refs)
-    for (int i = tid; i < nb; i += kPlanThreads) a.new_refs[i] = __ldg(a.refs + i);
+    for (int i = tid; i < nb; i += kPlanThreads) a.new_refs[i] = __ldcg(a.refs + i);   // (a fork ahead may have written them)
   const ForkRow x = fork_row_of(a, len, cap);
   int last = -1;   // the page that the row's tokens fill in part
   if (is_row && x.part > 0) {

@@ -91,7 +91,8 @@ struct RowTile {
   float m[2], l[2];    // rows g and g + 8; l is this thread's share of the sum
   bool odd;            // kMaskRows: a V element that is not finite was left out
 
-  // q0, q1: rows g and g + 8 of the tile ([D] bf16), nullptr for a row that is not there.
+  // q0, q1: rows g and g + 8 of the tile ([D] bf16), nullptr for a row that is not there.  (Plain loads: the queries may
+  // be what the kernel ahead wrote.)
   __device__ __forceinline__ void load(const uint16_t* q0, const uint16_t* q1, int lane) {
     const int c = lane & 3;
 #pragma unroll
@@ -99,10 +100,10 @@ struct RowTile {
       // Element pairs of the k-step that this thread holds (see the layouts above).
       const int d0 = F8 ? (D / 4) * c + 4 * s : 16 * s + 2 * c;
       const int d1 = F8 ? d0 + 2 : d0 + 8;
-      q[s][0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d0)) : 0u;
-      q[s][1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d0)) : 0u;
-      q[s][2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d1)) : 0u;
-      q[s][3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d1)) : 0u;
+      q[s][0] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + d0) : 0u;
+      q[s][1] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + d0) : 0u;
+      q[s][2] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + d1) : 0u;
+      q[s][3] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + d1) : 0u;
     }
   }
   // The loaded queries as operands, and an empty state.

@@ -226,13 +226,13 @@ __device__ __forceinline__ void tree_scan(const TreeArgs& a, int64_t* scratch, i
 }
 
 // Bits [x0, x0 + 32) of a token's tree mask (bits outside the row's words are
-// 0; x0 may be negative).
+// 0; x0 may be negative).  Plain loads: the kernel ahead may have written the mask.
 __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int x0) {
   if (x0 <= -32) return 0u;
-  if (x0 < 0) return (words > 0 ? __ldg(row) : 0u) << (-x0);
+  if (x0 < 0) return (words > 0 ? row[0] : 0u) << (-x0);
   const int w = x0 >> 5;
-  const uint32_t lo = w < words ? __ldg(row + w) : 0u;
-  const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+  const uint32_t lo = w < words ? row[w] : 0u;
+  const uint32_t hi = w + 1 < words ? row[w + 1] : 0u;
   return __funnelshift_r(lo, hi, x0 & 31);
 }
 

@@ -522,7 +522,8 @@ constexpr int kPickThreads = 512;
 // Few short lists: a CTA of pick_kernel scores its (token, head)'s blocks itself,
 // which saves a launch and the way through the workspace.  Four lanes a block,
 // 16-byte pieces as above; the first blocks' codes are on their way while a warp
-// makes the whole-number query.
+// makes the whole-number query.  (Bounds are read from L2: the kernel ahead may be a
+// copy of pages that has read and written them.)
 template <int D>
 __device__ __forceinline__ void alone_keys(const SparseArgs& a, int t, int g, int req, int n, uint32_t* s_keys) {
   constexpr int kPieces = 2 * D / 64, kRound = kPickThreads / 4;
@@ -538,8 +539,8 @@ __device__ __forceinline__ void alone_keys(const SparseArgs& a, int t, int g, in
     int e = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-      w[i] = there ? __ldg(reinterpret_cast<const uint4*>(a.codes + chunk * 2 * D + sub * 16 + i * 64)) : make_uint4(0, 0, 0, 0);
-    if (there) e = __ldg(a.exps + chunk);
+      w[i] = there ? __ldcg(reinterpret_cast<const uint4*>(a.codes + chunk * 2 * D + sub * 16 + i * 64)) : make_uint4(0, 0, 0, 0);
+    if (there) e = __ldcg(reinterpret_cast<const signed char*>(a.exps) + chunk);
     if (base == 0) {
       if (tid < 32)
         whole_queries<D>(static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(t) * a.num_q_heads + g * a.group) * D,

@@ -245,7 +245,7 @@ rows_kernel(const TreeArgs a) {
       if (i >= nb_w) return -1;
       blk = b0 + wi + wn * i;
       if constexpr (LIST) {
-        blk = __ldg(list + blk);
+        blk = __ldcg(list + blk);   // (the kernel ahead may have picked it)
         if (blk < 0 || pos < 0 || blk > (pos >> 4)) return -1;   // padding, or a block that the token does not see
         if (blk >= a.max_blocks) {
           atomicOr(a.pool.err, PKV_DEVERR_POSITION);
