@@ -86,7 +86,8 @@ extern "C" {
 
 /* Bits of the device error word (pkv_check_device_errors). */
 #define PKV_DEVERR_BLOCK_ID 1u   /* a block-table entry outside [0, num_blocks) */
-#define PKV_DEVERR_POSITION 2u   /* a position outside [0, max_blocks*block_size) */
+#define PKV_DEVERR_POSITION 2u   /* a position outside [0, max_blocks*block_size), or a length, parent, node
+                                  * or token range (cu_q_lens, cu_keep) out of its own */
 #define PKV_DEVERR_TIMEOUT 4u    /* a bounded wait inside a kernel gave up */
 #define PKV_DEVERR_INTERNAL 8u   /* a kernel found its launch configuration unusable */
 #define PKV_DEVERR_NO_PAGES 16u  /* pkv_fork found fewer free pages than it needs */

@@ -12,6 +12,7 @@
 #include "internal.h"
 #include "ops.h"
 #include "ptx.cuh"
+#include "sched.cuh"
 
 namespace pkv {
 namespace {
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const PoolView pool, uint4
   const int r = static_cast<int>(e / cols);
   griddep_wait();
   griddep_launch();
+  if (e == 0) check_cu(cu, num_reqs, num_kept, pool.err);
   if (r >= num_reqs) return;
   const int col = static_cast<int>(e % cols);
   const int ch = col % cpr, g = (col / cpr) % pool.num_kv_heads;

@@ -61,6 +61,11 @@ struct alignas(16) TreeCut {
 };
 static_assert(sizeof(TreeCut) == 48, "TreeCut layout: three 16-byte loads");
 
+// Flags token ranges that reach outside [0, num_tokens); the kernels cut them.  One thread of a launch.
+__device__ __forceinline__ void check_cu(const int32_t* cu, int num_reqs, int num_tokens, unsigned* err) {
+  if (__ldg(cu) < 0 || __ldg(cu + num_reqs) > num_tokens) atomicOr(err, PKV_DEVERR_POSITION);
+}
+
 // The request of token t (the last with cu <= t), or -1 for a token that
 // belongs to none.  A whole warp: each round narrows the range 32-fold.
 __device__ __forceinline__ int req_of_warp(const int32_t* cu, int num_reqs, int t, int lane) {

@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
   const int Hkv = a.pool.num_kv_heads;
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int groups = (a.num_tokens + TOK - 1) / TOK;
+  if (blockIdx.x == 0 && threadIdx.x == 0) check_cu(a.cu_q_lens, a.num_reqs, a.num_tokens, a.pool.err);
   if (w >= static_cast<int64_t>(groups) * Hkv) return;
   const int g = static_cast<int>(w % Hkv), t0 = static_cast<int>(w / Hkv) * TOK;
   // Lane i: token t0 + i's request, and whether it opens a block.
@@ -69,7 +70,8 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SparseArgs a) {
   bool opens = false;
   if (lane < TOK && mine < a.num_tokens) {
     my_req = req_of(a.cu_q_lens, a.num_reqs, mine);
-    opens = my_req >= 0 && (mine == __ldg(a.cu_q_lens + my_req) ||
+    // (no token lies before the first, wherever its request begins)
+    opens = my_req >= 0 && (mine == 0 || mine == __ldg(a.cu_q_lens + my_req) ||
                             (__ldg(a.positions + mine) >> 4) != (__ldg(a.positions + mine - 1) >> 4));
   }
   uint32_t todo = __ballot_sync(0xffffffffu, opens);
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreShape<D, NT>::kCtas) score
   const uint32_t slot_e = smem_u32(smem) + S::kRingAt + kScoreStages * kScoreThreads * kPieces * 16 + tid * 4;
   griddep_wait();
   griddep_launch();
+  if (blockIdx.x == 0 && tid == 0) check_cu(a.cu_q_lens, a.num_reqs, a.num_tokens, a.pool.err);
 
   // The share: each octet of token t (of this launch's) has a unit for each block up to its position, and some for
   // its start.
@@ -617,6 +620,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SparseArgs a) 
   const int p = __ldg(a.positions + t);
   if constexpr (!ALONE) griddep_wait();
   griddep_launch();
+  if (ALONE && blockIdx.x == 0 && tid == 0) check_cu(a.cu_q_lens, a.num_reqs, a.num_tokens, a.pool.err);
   if (ALONE && g == 0 && tid == 0 && t < __ldg(a.cu_q_lens + a.num_reqs) && (p < 0 || p >= a.max_blocks * kBlockSize))
     atomicOr(a.pool.err, PKV_DEVERR_POSITION);
   if (req < 0) return;   // block-uniform

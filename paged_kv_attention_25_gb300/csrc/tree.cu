@@ -90,6 +90,7 @@ rows_kernel(const TreeArgs a) {
   griddep_launch();   // the merge may take its place and wait
   if (!kAlways && tid < W) a.cuts[cut_record(blockIdx.x, W, true, tid)].count = 0;
   if (tid == 0) s_odd = 0;
+  if (LIST && blockIdx.x == 0 && tid == 0) check_cu(a.cu_q_lens, a.num_reqs, a.num_tokens, a.pool.err);
   const int rtiles = (G + kRowTile - 1) / kRowTile;   // LIST: row tiles of a token's group
   auto groups = [&](const TreeReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
   auto units = [&](const TreeReq& q) { return groups(q) * (rows_blocks(q) + kGroupUnits); };
@@ -531,6 +532,7 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restric
   const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
   griddep_wait();
   griddep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) check_cu(cu, num_reqs, num_tokens, err);
   if (t >= num_tokens) return;
   int lo = 0, hi = num_reqs - 1;
   while (lo < hi) {
