@@ -787,8 +787,10 @@ tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k, con
         for (int c = 16; c < kNK; c += 2) mx8[(c >> 1) & 7] = max3f(mx8[(c >> 1) & 7], s[c], s[c + 1]);
         const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         // Lazy rescaling: a row keeps its reference while the tile's maximum
-        // stays within 2^kRescaleLog2 of it.
-        const float m_tile = mx * sl2;
+        // stays within 2^kRescaleLog2 of it.  (Rows of the tile that are not the
+        // segment's, other requests' or whatever the buffer held, have no say:
+        // they would move the warp's references, and with them roundings.)
+        const float m_tile = valid ? mx * sl2 : -CUDART_INF_F;
         const bool grow = __any_sync(0xffffffffu, m_tile > m + kRescaleLog2);
         const float m_new = grow ? fmaxf(m, m_tile) : m;
         const float neg_m = m_new == -CUDART_INF_F ? 0.f : -m_new;
