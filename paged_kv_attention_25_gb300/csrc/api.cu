@@ -885,16 +885,33 @@ int pkv_debug_set(pkv_pool* pool, int what, int64_t value) {
 
 int pkv_profile_read(pkv_pool* pool, pkv_profile* out, int reset) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
-  for (auto& r : pool->pending) {
-    PKV_CUDA(cudaEventSynchronize(r.b), "cudaEventSynchronize");
-    float ms = 0.f;
-    PKV_CUDA(cudaEventElapsedTime(&ms, r.a, r.b), "cudaEventElapsedTime");
-    pool->totals.launches[r.kernel] += 1;
-    pool->totals.total_ms[r.kernel] += ms;
-    pool->ev_free.push_back(r.a);
-    pool->ev_free.push_back(r.b);
+  std::vector<ProfRec> recs;   // those there are now; calls may add more meanwhile
+  {
+    std::lock_guard<std::mutex> lk(pool->prof_mu);
+    recs.swap(pool->pending);
   }
-  pool->pending.clear();
+  cudaError_t e = cudaSuccess;
+  size_t n = 0;
+  double ms[5] = {};
+  int launches[5] = {};
+  for (; n < recs.size(); ++n) {
+    const ProfRec& r = recs[n];
+    float t = 0.f;
+    if ((e = cudaEventSynchronize(r.b)) != cudaSuccess || (e = cudaEventElapsedTime(&t, r.a, r.b)) != cudaSuccess) break;
+    launches[r.kernel] += 1;
+    ms[r.kernel] += t;
+  }
+  std::lock_guard<std::mutex> lk(pool->prof_mu);
+  for (size_t i = 0; i < n; ++i) {
+    pool->ev_free.push_back(recs[i].a);
+    pool->ev_free.push_back(recs[i].b);
+  }
+  pool->pending.insert(pool->pending.begin(), recs.begin() + static_cast<std::ptrdiff_t>(n), recs.end());
+  for (int k = 0; k < 5; ++k) {
+    pool->totals.launches[k] += launches[k];
+    pool->totals.total_ms[k] += ms[k];
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "profiling events");
   if (out) *out = pool->totals;
   if (reset) pool->totals = pkv_profile{};
   return PKV_OK;

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -91,9 +92,11 @@ struct pkv_pool {
   int fused_form = 0;                 // PKV_DEBUG_FUSED_FORM
   int tree_form = 0;                  // PKV_DEBUG_TREE_FORM
 
-  // profiling (prof_mode 2: the two attention kernels run one after the other)
-  bool prof_on = false;
-  int prof_mode = 0;
+  // profiling (prof_mode 2: the two attention kernels run one after the other).
+  // Not every call that launches holds `mu`: the lists have a lock of their own.
+  std::atomic<bool> prof_on{false};
+  std::atomic<int> prof_mode{0};
+  std::mutex prof_mu;
   std::vector<cudaEvent_t> ev_free;
   std::vector<pkv::ProfRec> pending;
   pkv_profile totals{};
@@ -104,7 +107,7 @@ struct pkv_pool {
   // Bytes of one physical block of K (or V): all KV heads.
   size_t block_bytes() const { return static_cast<size_t>(num_kv_heads) * pkv::kBlockSize * head_dim * elem_bytes; }
 
-  cudaEvent_t take_event() {
+  cudaEvent_t take_event() {   // prof_mu held
     if (ev_free.empty()) {
       cudaEvent_t e;
       if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
@@ -123,13 +126,17 @@ template <class F>
 int timed_launch(pkv_pool* pool, int kernel, void* stream, F&& fn) {
   cudaEvent_t a = nullptr, b = nullptr;
   if (pool->prof_on) {
-    a = pool->take_event();
-    b = pool->take_event();
+    {
+      std::lock_guard<std::mutex> lk(pool->prof_mu);
+      a = pool->take_event();
+      b = pool->take_event();
+    }
     if (a && b) cudaEventRecord(a, static_cast<cudaStream_t>(stream));
   }
   const int rc = fn();
   if (a && b) {
     cudaEventRecord(b, static_cast<cudaStream_t>(stream));
+    std::lock_guard<std::mutex> lk(pool->prof_mu);
     pool->pending.push_back({kernel, a, b});
   }
   return rc;
