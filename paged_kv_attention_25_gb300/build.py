@@ -8,10 +8,12 @@ CUDA error instead of the load failing).
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +26,7 @@ SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_
 HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh", "ops.h", "rows.cuh", "sched.cuh",
            "tc.cuh"]
 BINDING = os.path.join(BUILD, "pkv_binding.so")
+BINDING_STAMP = os.path.join(BUILD, "pkv_binding.stamp")   # binding_key()
 BINDING_SOURCE = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -35,23 +38,38 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING_SOURCE]]
-    files.append(os.path.join(ROOT, "include", "pkv.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _newer(files, than) -> bool:
+    files = list(files) + [os.path.join(ROOT, "include", "pkv.h"), os.path.abspath(__file__)]
+    return not os.path.exists(than) or any(os.path.getmtime(f) > os.path.getmtime(than) for f in files)
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+def _lib_stale() -> bool:
+    return _newer((os.path.join(CSRC, s) for s in SOURCES + HEADERS), LIB)
+
+
+def binding_key() -> str:
+    """What the binding is compiled against: the installed torch ("" if there is none) and this interpreter."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return ""
+    return f"torch {torch} {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def built_for():
+    """The binding_key() of the last build; None before the first."""
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read().strip()
+    except OSError:
+        return None
+
+
+def _binding_stale() -> bool:
+    return built_for() != binding_key() or _newer([os.path.join(CSRC, BINDING_SOURCE)], BINDING)
 
 
 def _compile_binding():
-    import sysconfig
-
     import torch
     home = os.path.dirname(torch.__file__)
     obj = os.path.join(BUILD, "binding.o")
@@ -76,7 +94,8 @@ def _link_binding(obj, torch_lib):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    lib, binding = force or _lib_stale(), force or _binding_stale()
+    if not (lib or binding):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -95,16 +114,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, "-shared", "-cudart", "static"] + ARCH + objs + ["-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(*binding)
+        compiled = ex.submit(_compile_binding) if binding else None
+        if lib:
+            objs = list(ex.map(compile_one, SOURCES))
+        compiled = compiled and compiled.result()
+        if lib:
+            tmp = LIB + f".tmp{os.getpid()}"
+            r = subprocess.run([cc, "-shared", "-cudart", "static"] + ARCH + objs + ["-o", tmp], capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr}")
+            os.replace(tmp, LIB)
+    if binding:
+        _link_binding(*compiled)
+        tmp = BINDING_STAMP + f".tmp{os.getpid()}"
+        with open(tmp, "w") as f:
+            f.write(binding_key() + "\n")
+        os.replace(tmp, BINDING_STAMP)
     return LIB
 
 

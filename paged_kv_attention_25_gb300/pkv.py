@@ -19,6 +19,8 @@ import threading
 import numpy as np
 import torch
 
+from . import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpkv.so")
 
@@ -181,9 +183,11 @@ def _load_binding():
     if _binding is None:
         load_library()
         path = os.path.join(os.path.dirname(LIB_PATH), "pkv_binding.so")
+        how = "(run `python -c \"import __graft_entry__ as g; g.build()\"`)"
         if not os.path.exists(path):
-            raise RuntimeError(f"Python binding not built: {path} is missing "
-                               "(run `python -c \"import __graft_entry__ as g; g.build()\"`)")
+            raise RuntimeError(f"Python binding not built: {path} is missing {how}")
+        if build.built_for() != build.binding_key():
+            raise RuntimeError(f"Python binding built for another torch or interpreter than {build.binding_key()} {how}")
         spec = importlib.util.spec_from_file_location("pkv_binding", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
