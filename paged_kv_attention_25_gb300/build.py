@@ -26,7 +26,7 @@ SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_
 HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh", "ops.h", "rows.cuh", "sched.cuh",
            "tc.cuh"]
 BINDING = os.path.join(BUILD, "pkv_binding.so")
-BINDING_STAMP = os.path.join(BUILD, "pkv_binding.stamp")   # binding_key()
+BINDING_STAMP = os.path.join(BUILD, "pkv_binding.stamp")   # binding_key(), and "built" or "left out"
 BINDING_SOURCE = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -57,20 +57,32 @@ def binding_key() -> str:
 
 
 def built_for():
-    """The binding_key() of the last build; None before the first."""
+    """The binding_key() of the last build and whether it made a binding; None before the first."""
     try:
         with open(BINDING_STAMP) as f:
-            return f.read().strip()
-    except OSError:
+            key, made = f.read().splitlines()
+    except (OSError, ValueError):
         return None
+    return key, made == "built"
 
 
 def _binding_stale() -> bool:
-    return built_for() != binding_key() or _newer([os.path.join(CSRC, BINDING_SOURCE)], BINDING)
+    last = built_for()
+    if last is None or last[0] != binding_key():
+        return True
+    return last[1] and _newer([os.path.join(CSRC, BINDING_SOURCE)], BINDING)
 
 
-def _compile_binding():
-    import torch
+def _torch():
+    """torch, if there is one with CUDA to compile the binding against."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch if torch.version.cuda else None
+
+
+def _compile_binding(torch):
     home = os.path.dirname(torch.__file__)
     obj = os.path.join(BUILD, "binding.o")
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj,
@@ -79,7 +91,7 @@ def _compile_binding():
            "-I", os.path.join(ROOT, "include"), f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{BINDING_SOURCE} failed:\n{r.stderr}")
+        raise RuntimeError(f"{BINDING_SOURCE} failed (the C library is built):\n{r.stderr}")
     return obj, os.path.join(home, "lib")
 
 
@@ -89,17 +101,20 @@ def _link_binding(obj, torch_lib):
            "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"binding link failed:\n{r.stderr}")
+        raise RuntimeError(f"binding link failed (the C library is built):\n{r.stderr}")
     os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The C library, for which nvcc is enough, and then the binding, for which there has to be a torch with CUDA: without
+    one it is left out, and the calls that need it say so."""
     lib, binding = force or _lib_stale(), force or _binding_stale()
     if not (lib or binding):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), "-lineinfo"]
+    torch = _torch() if binding else None
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
@@ -114,21 +129,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        compiled = ex.submit(_compile_binding) if binding else None
+        compiled = ex.submit(_compile_binding, torch) if torch else None
         if lib:
             objs = list(ex.map(compile_one, SOURCES))
-        compiled = compiled and compiled.result()
-        if lib:
             tmp = LIB + f".tmp{os.getpid()}"
             r = subprocess.run([cc, "-shared", "-cudart", "static"] + ARCH + objs + ["-o", tmp], capture_output=True, text=True)
             if r.returncode != 0:
                 raise RuntimeError(f"link failed:\n{r.stderr}")
             os.replace(tmp, LIB)
     if binding:
-        _link_binding(*compiled)
+        if compiled:
+            _link_binding(*compiled.result())
+        elif verbose:
+            sys.stderr.write("no torch with CUDA: the Python binding is left out\n")
         tmp = BINDING_STAMP + f".tmp{os.getpid()}"
         with open(tmp, "w") as f:
-            f.write(binding_key() + "\n")
+            f.write(f"{binding_key()}\n{'built' if compiled else 'left out'}\n")
         os.replace(tmp, BINDING_STAMP)
     return LIB
 

@@ -183,10 +183,10 @@ def _load_binding():
     if _binding is None:
         load_library()
         path = os.path.join(os.path.dirname(LIB_PATH), "pkv_binding.so")
-        how = "(run `python -c \"import __graft_entry__ as g; g.build()\"`)"
+        how = "(run `python -c \"import __graft_entry__ as g; g.build()\"` with a torch that has CUDA)"
         if not os.path.exists(path):
             raise RuntimeError(f"Python binding not built: {path} is missing {how}")
-        if build.built_for() != build.binding_key():
+        if build.built_for() != (build.binding_key(), True):
             raise RuntimeError(f"Python binding built for another torch or interpreter than {build.binding_key()} {how}")
         spec = importlib.util.spec_from_file_location("pkv_binding", path)
         mod = importlib.util.module_from_spec(spec)
