@@ -50,6 +50,27 @@ void check(int rc) {
   throw Raised{};
 }
 
+// A library call, without the interpreter's lock: it may wait for the pool's (another thread's plan of a batch).
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+template <class... P, class... A>
+void run(int (*call)(P...), A... args) {   // (the arguments are made, and refused, with the lock)
+  int rc;
+  {
+    const Unlocked unlocked;
+    rc = call(args...);
+  }
+  check(rc);
+}
+
 struct Pool {
   PyObject_HEAD
   pkv_pool* handle;
@@ -83,13 +104,13 @@ class Call {
   }
 
   // `size` bytes: the caller's tensor (any size: the library checks it), the pool's, or a new one.
-  const at::Tensor& workspace(PyObject* given, size_t size);
+  // (Held by the call: another thread's may replace the pool's while this one runs.)
+  at::Tensor workspace(PyObject* given, size_t size);
 
  private:
   Pool* pool_;
   bool given_;
   cudaStream_t stream_ = nullptr;
-  at::Tensor own_;
 };
 
 const at::Tensor& tensor(PyObject* o, const char* name, int64_t dims) {
@@ -126,7 +147,7 @@ T* address(const Pool* pool, PyObject* o, const char* name, at::ScalarType type,
   return static_cast<T*>(t.data_ptr());
 }
 
-const at::Tensor& Call::workspace(PyObject* given, size_t size) {
+at::Tensor Call::workspace(PyObject* given, size_t size) {
   if (given != Py_None) {
     const at::Tensor& t = tensor(given, "workspace", 1);
     address(pool_, given, "workspace", at::kByte, t.sizes());
@@ -138,10 +159,7 @@ const at::Tensor& Call::workspace(PyObject* given, size_t size) {
     const cudaError_t e = cudaStreamIsCapturing(stream_, &capturing);
     if (e != cudaSuccess) raise(PyExc_RuntimeError, std::string("cudaStreamIsCapturing: ") + cudaGetErrorString(e));
   }
-  if (given_ || capturing != cudaStreamCaptureStatusNone) {
-    own_ = make({n}, at::kByte);
-    return own_;
-  }
+  if (given_ || capturing != cudaStreamCaptureStatusNone) return make({n}, at::kByte);
   at::Tensor& t = (*pool_->buf)[stream_];
   if (!t.defined() || t.numel() < n) t = make({n}, at::kByte);
   return t;
@@ -263,8 +281,8 @@ PyObject* tree_mask(Pool* p, Args a) {
   }
   if (words < 0) raise(PyExc_ValueError, "mask_words must be >= 0");
   Table out(p, call, a[4], "out", {T, words});
-  check(pkv_tree_mask(p->handle, parents, cu, count(R), count(T), reinterpret_cast<uint32_t*>(out.at), count(words),
-                      call.stream()));
+  run(pkv_tree_mask, p->handle, parents, cu, count(R), count(T), reinterpret_cast<uint32_t*>(out.at), count(words),
+      call.stream());
   return out.result();
 }
 
@@ -281,10 +299,10 @@ PyObject* tree_attn(Pool* p, Args a) {
   Output out(p, call, q, a[7], a[8], a[11] == Py_True);
   size_t size = 0;
   check(pkv_tree_attn_workspace_size(p->handle, count(q.heads), count(b.width), count(b.reqs), count(q.tokens), &size));
-  const at::Tensor& ws = call.workspace(a[9], size);
-  check(pkv_tree_attn(p->handle, q.q, count(q.heads), b.tables, count(b.width), ctx, prefix, b.cu, count(b.reqs),
-                      count(q.tokens), reinterpret_cast<const uint32_t*>(mask), count(words), scale, out.o, out.lse,
-                      ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream()));
+  const at::Tensor ws = call.workspace(a[9], size);
+  run(pkv_tree_attn, p->handle, q.q, count(q.heads), b.tables, count(b.width), ctx, prefix, b.cu, count(b.reqs),
+      count(q.tokens), reinterpret_cast<const uint32_t*>(mask), count(words), scale, out.o, out.lse, ws.data_ptr(),
+      static_cast<size_t>(ws.numel()), call.stream());
   return out.result();
 }
 
@@ -296,8 +314,8 @@ PyObject* summarize(Pool* p, Args a) {
   const int32_t* ctx = address<int32_t>(p, a[5], "ctx_lens", at::kInt, {b.reqs});
   const Summary s(p, a[0], a[1]);
   const Call call(p, a[6]);
-  check(pkv_summarize(p->handle, b.tables, count(b.width), count(b.reqs), b.cu, pos, ctx, count(T), s.codes, s.exps,
-                      call.stream()));
+  run(pkv_summarize, p->handle, b.tables, count(b.width), count(b.reqs), b.cu, pos, ctx, count(T), s.codes, s.exps,
+      call.stream());
   Py_RETURN_NONE;
 }
 
@@ -313,10 +331,10 @@ PyObject* select_blocks(Pool* p, Args a) {
   Table out(p, call, a[9], "out", {q.tokens, p->num_kv_heads, top_k});
   size_t size = 0;
   check(pkv_select_blocks_workspace_size(p->handle, count(b.width), count(q.tokens), &size));
-  const at::Tensor& ws = call.workspace(a[10], size);
-  check(pkv_select_blocks(p->handle, q.q, count(q.heads), pos, b.tables, count(b.width), b.cu, count(b.reqs),
-                          count(q.tokens), s.codes, s.exps, top_k, sinks, recent, out.at, ws.data_ptr(),
-                          static_cast<size_t>(ws.numel()), call.stream()));
+  const at::Tensor ws = call.workspace(a[10], size);
+  run(pkv_select_blocks, p->handle, q.q, count(q.heads), pos, b.tables, count(b.width), b.cu, count(b.reqs),
+      count(q.tokens), s.codes, s.exps, top_k, sinks, recent, out.at, ws.data_ptr(), static_cast<size_t>(ws.numel()),
+      call.stream());
   return out.result();
 }
 
@@ -332,10 +350,10 @@ PyObject* sparse_attn(Pool* p, Args a) {
   Output out(p, call, q, a[6], a[7], a[10] == Py_True);
   size_t size = 0;
   check(pkv_sparse_attn_workspace_size(p->handle, &size));
-  const at::Tensor& ws = call.workspace(a[8], size);
-  check(pkv_sparse_attn(p->handle, q.q, count(q.heads), pos, b.tables, count(b.width), b.cu, count(b.reqs),
-                        count(q.tokens), sel, count(k), scale, out.o, out.lse, ws.data_ptr(),
-                        static_cast<size_t>(ws.numel()), call.stream()));
+  const at::Tensor ws = call.workspace(a[8], size);
+  run(pkv_sparse_attn, p->handle, q.q, count(q.heads), pos, b.tables, count(b.width), b.cu, count(b.reqs),
+      count(q.tokens), sel, count(k), scale, out.o, out.lse, ws.data_ptr(), static_cast<size_t>(ws.numel()),
+      call.stream());
   return out.result();
 }
 
@@ -357,10 +375,10 @@ PyObject* fork(Pool* p, Args a) {
   Table out(p, call, a[6], "out_tables", {N, width});
   size_t size = 0;
   check(pkv_fork_workspace_size(p->handle, count(R), count(N), &size));
-  const at::Tensor& ws = call.workspace(a[10], size);
-  check(pkv_fork(p->handle, tables, count(R), count(width), lens, caps, parents, new_caps, count(N), out.at, refs,
-                 out_refs, s ? s->codes : nullptr, s ? s->exps : nullptr, ws.data_ptr(),
-                 static_cast<size_t>(ws.numel()), call.stream()));
+  const at::Tensor ws = call.workspace(a[10], size);
+  run(pkv_fork, p->handle, tables, count(R), count(width), lens, caps, parents, new_caps, count(N), out.at, refs,
+      out_refs, s ? s->codes : nullptr, s ? s->exps : nullptr, ws.data_ptr(), static_cast<size_t>(ws.numel()),
+      call.stream());
   PyObject* made = out.result();
   if (!made) return nullptr;
   PyObject* r = PyTuple_Pack(2, made, refs_out);
@@ -376,7 +394,7 @@ PyObject* copy_blocks(Pool* p, Args a) {
   std::optional<Summary> s;
   if (a[2] != Py_None || a[3] != Py_None) s.emplace(p, a[2], a[3]);
   const Call call(p, a[4]);
-  check(pkv_copy_blocks(p->handle, src, dst, count(n), s ? s->codes : nullptr, s ? s->exps : nullptr, call.stream()));
+  run(pkv_copy_blocks, p->handle, src, dst, count(n), s ? s->codes : nullptr, s ? s->exps : nullptr, call.stream());
   Py_RETURN_NONE;
 }
 
@@ -387,7 +405,7 @@ PyObject* compact(Pool* p, Args a) {
   const int32_t* src = address<int32_t>(p, a[2], "src_positions", at::kInt, {n});
   const int32_t* dst = address<int32_t>(p, a[3], "dst_starts", at::kInt, {b.reqs});
   const Call call(p, a[4]);
-  check(pkv_compact(p->handle, b.tables, count(b.width), count(b.reqs), b.cu, src, dst, count(n), call.stream()));
+  run(pkv_compact, p->handle, b.tables, count(b.width), count(b.reqs), b.cu, src, dst, count(n), call.stream());
   Py_RETURN_NONE;
 }
 
