@@ -9,7 +9,9 @@
 // workspace of calls on a current stream is kept with the pool, one for each
 // stream, as calls on one stream follow one another.  A call that is being
 // captured, or that names a stream, gets a workspace of its own (a captured
-// graph keeps it).
+// graph keeps it), and so does one on a stream that torch does not own: such a
+// stream may be destroyed while its work runs, and another come back under its
+// handle.
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -90,7 +92,10 @@ class Call {
       Py_DECREF(raw);
       if (PyErr_Occurred()) throw Raised{};
     } else {
-      stream_ = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(pool->device)).stream();
+      const c10::cuda::CUDAStream s = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(pool->device));
+      stream_ = s.stream();
+      // (torch's own have small ids, others their handle for an id)
+      foreign_ = stream_ && static_cast<uint64_t>(s.id()) == reinterpret_cast<uintptr_t>(stream_);
     }
   }
   void* stream() const { return stream_; }
@@ -109,7 +114,7 @@ class Call {
 
  private:
   Pool* pool_;
-  bool given_;
+  bool given_, foreign_ = false;
   cudaStream_t stream_ = nullptr;
 };
 
@@ -155,11 +160,12 @@ at::Tensor Call::workspace(PyObject* given, size_t size) {
   }
   const int64_t n = static_cast<int64_t>(size);
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (!given_) {
+  const bool kept = !given_ && !foreign_;
+  if (kept) {
     const cudaError_t e = cudaStreamIsCapturing(stream_, &capturing);
     if (e != cudaSuccess) raise(PyExc_RuntimeError, std::string("cudaStreamIsCapturing: ") + cudaGetErrorString(e));
   }
-  if (given_ || capturing != cudaStreamCaptureStatusNone) return make({n}, at::kByte);
+  if (!kept || capturing != cudaStreamCaptureStatusNone) return make({n}, at::kByte);
   at::Tensor& t = (*pool_->buf)[stream_];
   if (!t.defined() || t.numel() < n) t = make({n}, at::kByte);
   return t;

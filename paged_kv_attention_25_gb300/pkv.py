@@ -430,8 +430,8 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
 # calls can be captured into a graph.  Tensors live on the pool's device; without `stream` a call runs on that device's
 # current stream.  Outputs and workspaces that are not given are allocated for that stream.  The workspace of calls on a
 # current stream is kept with the pool, one for each stream: calls on one stream follow one another.  A call that is
-# being captured, or that names another stream, gets one of its own (a captured graph keeps it).  The checks and the
-# marshalling are native code (csrc/binding.cpp).
+# being captured, that names another stream, or whose current stream is not one of torch's own (ExternalStream) gets one
+# of its own (a captured graph keeps it).  The checks and the marshalling are native code (csrc/binding.cpp).
 
 
 def _ops(pool: Pool):
