@@ -407,7 +407,8 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
  * Attention of each query token over the keys j <= p of its selected blocks
  * (formulas and rounding as above; all keys of a block up to p have been
  * written; blocks of one list must be distinct, in any order; entries below 0 and blocks behind the token are skipped, an entry beyond
- * the table is flagged and skipped).  A list without a key gives O = 0,
+ * the table is flagged and skipped; so is a position outside the table, below 0
+ * without keys, beyond it with all keys of its blocks).  A list without a key gives O = 0,
  * LSE = -inf.  workspace: pkv_sparse_attn_workspace_size() bytes (a constant of
  * the pool), 256-byte aligned, used by one call at a time as for pkv_tree_attn.
  * Both calls read all metadata on the device, can be captured into a graph and

@@ -199,6 +199,7 @@ rows_kernel(const TreeArgs a) {
       nrows = min(kRowTile, G - row0);
       req = req_of_warp(a.cu_q_lens, a.num_reqs, rq.t0, lane);
       pos = __ldg(a.positions + rq.t0);
+      if (lane == 0 && req >= 0 && (pos < 0 || pos >= a.max_blocks * kBlockSize)) atomicOr(a.pool.err, PKV_DEVERR_POSITION);
       list = a.sel + th * a.top_k;
     } else {
       for (int64_t n = units(rq); sh.off >= n; n = units(rq)) {   // the next request with work (there is one)
@@ -267,7 +268,7 @@ rows_kernel(const TreeArgs a) {
       const bool has = chunk_cur >= 0;
       there = __ballot_sync(0xffffffffu, has);
       const int blk = LIST ? blk_cur : b0 + wi + wn * (32 * win + lane);
-      plain = __ballot_sync(0xffffffffu, has && (LIST ? pos - blk * kBlockSize + 1 >= kBlockSize
+      plain = __ballot_sync(0xffffffffu, has && (LIST ? pos - blk * kBlockSize >= kBlockSize - 1
                                                       : (blk + 1) * kBlockSize <= rq.prefix));
     };
     look();
