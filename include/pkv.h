@@ -500,10 +500,13 @@ int pkv_swap_in(pkv_pool* pool, const int32_t* block_ids, int n, const void* hos
  * `stream` before this call (for instance the swap-out that filled
  * host_buf), so it takes no SMs and overlaps whatever the caller queues next.
  * The blocks land in the pool at the start of the pool's next call that reads
- * or writes it (pkv_append, pkv_paged_attn, pkv_swap_out, pkv_swap_in,
- * another pkv_swap_in_ahead) or at pkv_swap_in_finish: that call's stream
- * waits for the transfer, and a kernel scatters the staged blocks into
- * block_ids.  Until then the pool's blocks keep their old contents, so calls
+ * or writes it (pkv_append, pkv_paged_attn, pkv_tree_attn, pkv_sparse_attn,
+ * pkv_summarize, pkv_fork, pkv_copy_blocks, pkv_compact, pkv_swap_out,
+ * pkv_swap_in, another pkv_swap_in_ahead) or at pkv_swap_in_finish: that
+ * call's stream waits for the transfer, and a kernel scatters the staged
+ * blocks into block_ids.  A replayed graph lands nothing, and a call that is
+ * being captured is refused (PKV_EINVAL) while a swap-in is pending: call
+ * pkv_swap_in_finish before a replay or a capture.  Until then the pool's blocks keep their old contents, so calls
  * take effect in call order; read the storage from pkv_pool_kv_ptrs only
  * after pkv_swap_in_finish.
  * Layer pipelining: with one pool per model layer, issue every layer's

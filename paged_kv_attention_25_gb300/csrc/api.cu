@@ -345,6 +345,11 @@ int pkv::finish_swap_in(pkv_pool* pool, void* stream) {
   std::lock_guard<std::mutex> lk(pool->swap_mu);
   if (!pool->swap_pending) return PKV_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // (A capture cannot wait for a transfer that is not part of it, and trying to would end it.)
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  PKV_CUDA(cudaStreamIsCapturing(s, &capturing), "swap-in capture status");
+  if (capturing != cudaStreamCaptureStatusNone)
+    return fail(PKV_EINVAL, "a swap-in is pending: call pkv_swap_in_finish before the capture");
   PKV_CUDA(cudaStreamWaitEvent(s, pool->swap_ready, 0), "swap-in wait");
   const int rc = timed_launch(pool, 4, stream, [&] {
     return launch_swap(pool->view(), pool->k, pool->v, pool->swap_staging, pool->swap_ids.data(),

@@ -431,7 +431,8 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
 # current stream.  Outputs and workspaces that are not given are allocated for that stream.  The workspace of calls on a
 # current stream is kept with the pool, one for each stream: calls on one stream follow one another.  A call that is
 # being captured, that names another stream, or whose current stream is not one of torch's own (ExternalStream) gets one
-# of its own (a captured graph keeps it).  The checks and the marshalling are native code (csrc/binding.cpp).
+# of its own (a captured graph keeps it).  A replay lands no pending swap-in: pkv_swap_in_finish comes before it, and
+# before a capture.  The checks and the marshalling are native code (csrc/binding.cpp).
 
 
 def _ops(pool: Pool):
