@@ -443,6 +443,11 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
  * overlap tables.  If too few pages are free PKV_DEVERR_NO_PAGES is set and the
  * entries left over are -1 (their copies do not happen).  Invalid lengths, parents and
  * page ids are flagged; a bad parent counts as -1, a bad id is not counted.
+ * A cache of several pools (one a layer) under one set of tables is forked by one
+ * call a pool with the same inputs: tables and counts follow from the inputs
+ * alone, so that every call makes the same, and each copies its own pool's pages.
+ * All calls but the last take a new_refs other than refs (a later call that found
+ * changed counts would take other pages); new_tables may be one array for all.
  * workspace: pkv_fork_workspace_size() bytes, 16-byte aligned, one call at a time.
  */
 int pkv_fork_workspace_size(pkv_pool* pool, int num_rows, int num_children, size_t* bytes);

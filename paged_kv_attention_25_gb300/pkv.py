@@ -528,7 +528,9 @@ def pkv_fork(pool: Pool, tables, lens, caps, parents, new_caps, refs, out_tables
              workspace=None, stream=None):
     """The next generation of sequences: child i continues row parents[i] of `tables` (-1: empty) with pages for
     new_caps[i] tokens.  Shares full pages, copies partly filled ones where needed, frees what no one owns any more.
-    refs [num_blocks] counts the pages' owners; out_refs defaults to refs (in place).  Returns (new tables, refs)."""
+    refs [num_blocks] counts the pages' owners; out_refs defaults to refs (in place).  Returns (new tables, refs).
+    Several pools (one a layer) under one set of tables: one call each with the same inputs, all but the last with an
+    out_refs other than refs, so that every call starts from the same counts and takes the same pages."""
     return _ops(pool).fork(tables, lens, caps, parents, new_caps, refs, out_tables, out_refs, *_bounds(summary), workspace,
                            stream)
 
