@@ -96,19 +96,27 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
 // each, need no merge.  They are taken
 //   - where groups are short (kWholeBlocks);
 //   - where a CTA of twelve warps on every SM is no more than six blocks a warp
-//     behind equal shares (with the groups' 2 heads a row, D = 128, us, shares /
-//     whole: 8 groups of 38 blocks 18.5 / 14.4, of 250 20.6 / 30.8; 32 lists of 64
-//     24.7 / 22.7, of 128 26.7 / 28.7, of 256 28.9 / 37.9; 64 groups of 126 26.5 /
-//     22.6, FP8 30.7 / 24.7; 120 lists of 128 45.7 / 41.4);
+//     behind equal shares, if all groups are equally long (lists, one request; D =
+//     128, us, shares / whole: 8 groups of 38 blocks 18.5 / 14.4, of 250 20.6 /
+//     30.8; 32 lists of 64 24.7 / 22.7, of 128 26.7 / 28.7, of 256 28.9 / 37.9; 120
+//     lists of 128 45.7 / 41.4);
+//   - up to kNearBlocks blocks and a CTA an SM, if requests may differ: a longer
+//     table may be that of one request of many, whose groups are then waited for (12
+//     requests of 97 to 1236 blocks, 422 on average, 8 KV heads, a row tile each: bf16
+//     64.6 / 103.5, FP8 48.0 / 94.6; 6 of 23 to 147: 24.8 / 22.8, 28.3 / 24.6; equally
+//     long ones: 16 groups of 128 20.3 / 20.7, of 192 22.7 / 26.0; 64 of 96 24.7 /
+//     18.6, of 128 25.1 / 22.6, of 256 41.8 / 36.9; 144 of 256 64.8 / 57.5);
 //   - for lists, which are all equally long, where there are enough of them to keep
 //     the memory busy (256 of 128 blocks: 91 us for selection and attention with
 //     shares, 85 with whole groups).
 // An SM holds twelve warps of this kernel: as one CTA, two or three, by the number
 // of groups (two up to 64 blocks: 256 lists of 16, 22.1 us with three and 20.6 with
 // two, 280 FP8 lists of 64 92.9 and 89.7, but 256 of 128 blocks 78.3 and 79.9).
+constexpr int kNearBlocks = 160;
 void fit_ctas(TreeArgs& a, int64_t groups, int blocks, int num_sms) {
+  const bool equal = a.sel || a.num_reqs == 1;
   const int64_t units = groups * (static_cast<int64_t>(blocks) + 2);
-  const bool near = groups <= num_sms && blocks <= 74 + std::max<int64_t>(48, groups * blocks / num_sms);
+  const bool near = groups <= num_sms && blocks <= (equal ? 74 + std::max<int64_t>(48, groups * blocks / num_sms) : kNearBlocks);
   a.form.whole = !a.form.tensor && groups <= a.form.ctas && (blocks <= kWholeBlocks || near || (a.sel && groups >= num_sms));
   const int64_t want = a.form.whole ? groups : a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
   a.form.shrink(static_cast<int>(std::min<int64_t>(want < 2 ? 2 : want, a.form.ctas)));
