@@ -109,9 +109,11 @@ TreeArgs tree_args(const pkv_pool* pool, const TreeForm& f, const TreeWs& w, voi
 //   - for lists, which are all equally long, where there are enough of them to keep
 //     the memory busy (256 of 128 blocks: 91 us for selection and attention with
 //     shares, 85 with whole groups).
-// An SM holds twelve warps of this kernel: as one CTA, two or three, by the number
-// of groups (two up to 64 blocks: 256 lists of 16, 22.1 us with three and 20.6 with
-// two, 280 FP8 lists of 64 92.9 and 89.7, but 256 of 128 blocks 78.3 and 79.9).
+// An SM holds twelve warps of this kernel: as one CTA, two or three, so that all
+// groups are under way (selection and attention, us, three CTAs / two; 256 lists of
+// 16 41.4 / 41.1, of 64 60.0 / 59.3, of 128 80.8 / 79.9, of 512 194 / 193, of 1024
+// 328 / 324; 160 of 128 63.0 / 59.9, of 1024 257 / 229; 304 of 128 90.2 / 89.3, of 1024
+// 378 / 379; FP8: 280 of 64 53.5 / 50.8, of 128 65.8 / 63.5, of 1024 242 / 198).
 constexpr int kNearBlocks = 160;
 void fit_ctas(TreeArgs& a, int64_t groups, int blocks, int num_sms) {
   const bool equal = a.sel || a.num_reqs == 1;
@@ -121,7 +123,7 @@ void fit_ctas(TreeArgs& a, int64_t groups, int blocks, int num_sms) {
   const int64_t want = a.form.whole ? groups : a.form.tensor ? (units + 1) / 2 * 2 : (units + 15) / 16;
   a.form.shrink(static_cast<int>(std::min<int64_t>(want < 2 ? 2 : want, a.form.ctas)));
   a.ctas = a.form.ctas;
-  if (a.form.whole) a.form.warps = groups <= num_sms ? 12 : groups <= 2 * num_sms && blocks <= 64 ? 6 : 4;
+  if (a.form.whole) a.form.warps = groups <= num_sms ? 12 : groups <= 2 * num_sms ? 6 : 4;
 }
 
 int check_workspace(const void* workspace, size_t have, size_t need, const char* size_fn) {
