@@ -108,7 +108,6 @@ struct ForkArgs {
   int8_t* codes;      // summaries to copy along, or nullptr
   int8_t* exps;
   int32_t* ws;        // fork_ws_ints() ints
-  int num_sms;
 };
 size_t fork_ws_ints(int num_blocks, int num_rows, int num_children);
 int launch_fork(const ForkArgs& a, void* stream);

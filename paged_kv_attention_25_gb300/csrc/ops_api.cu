@@ -155,8 +155,7 @@ size_t select_ws(const pkv_pool* pool, int max_blocks, int num_tokens) {
                   pool->num_kv_heads * sizeof(uint32_t));
 }
 
-int check_summary(const pkv_pool* pool, const void* codes, const void* exps) {
-  (void)pool;
+int check_summary(const void* codes, const void* exps) {
   if (!codes || !exps) return fail(PKV_EINVAL, "NULL summary arrays");
   if (!aligned16(codes)) return fail(PKV_EINVAL, "summary codes must be 16-byte aligned");
   return PKV_OK;
@@ -253,7 +252,7 @@ int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, i
   int rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc || num_tokens == 0) return rc;
   if (!block_tables || !cu_q_lens || !positions || !ctx_lens) return fail(PKV_EINVAL, "NULL device pointer");
-  if ((rc = check_summary(pool, codes, exps))) return rc;
+  if ((rc = check_summary(codes, exps))) return rc;
   if (static_cast<int64_t>(num_tokens) * pool->num_kv_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many rows");
   DeviceGuard guard(pool->device);
   if ((rc = finish_swap_in(pool, stream))) return rc;
@@ -295,7 +294,7 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
   if ((rc = check_heads(pool, num_q_heads))) return rc;
   if (!q || !q_positions || !block_tables || !cu_q_lens || !selected) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q)) return fail(PKV_EINVAL, "q must be 16-byte aligned");
-  if ((rc = check_summary(pool, codes, exps))) return rc;
+  if ((rc = check_summary(codes, exps))) return rc;
   if ((rc = check_workspace(workspace, workspace_bytes, select_ws(pool, max_blocks, num_tokens),
                             "pkv_select_blocks_workspace_size()")))
     return rc;
@@ -410,7 +409,7 @@ int pkv_fork(pkv_pool* pool, const int32_t* tables, int num_rows, int max_blocks
   if (rc) return rc;
   std::lock_guard<std::mutex> lk(pool->mu);
   ForkArgs a{pool->view(), pool->k, pool->v, tables, num_rows, max_blocks, lens, caps, parents, new_caps, num_children,
-             new_tables, refs, new_refs, codes, exps, static_cast<int32_t*>(workspace), pool->num_sms};
+             new_tables, refs, new_refs, codes, exps, static_cast<int32_t*>(workspace)};
   rc = timed_launch(pool, 0, stream, [&] { return launch_fork(a, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "fork launch");
   return PKV_OK;

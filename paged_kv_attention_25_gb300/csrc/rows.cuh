@@ -12,8 +12,9 @@
 //
 // bf16 pools: the chunk lies in 128-byte lines, 16-byte piece x of line r at
 // x ^ (r % 8), and ldmatrix reads the fragments
-// without bank conflicts; P is rounded to bf16 (half a step is 2^-9, and the
-// errors of different keys are independent: smaller than O's own rounding).
+// without bank conflicts; P is rounded to bf16, each p by at most 2^-8 of itself, as
+// much as O's own rounding: for a row that one or a few keys dominate the two add up,
+// over many keys the roundings of P average out.
 //
 // FP8 pools: operands are f16 (every e4m3 value is an f16 value).  The dims of
 // S's k-steps and of O's n-tiles are permuted so that a thread reads whole

@@ -66,8 +66,17 @@ __device__ __forceinline__ void check_cu(const int32_t* cu, int num_reqs, int nu
   if (__ldg(cu) < 0 || __ldg(cu + num_reqs) > num_tokens) atomicOr(err, PKV_DEVERR_POSITION);
 }
 
-// The request of token t (the last with cu <= t), or -1 for a token that
-// belongs to none.  A whole warp: each round narrows the range 32-fold.
+// The request of token t (the last with cu <= t), or -1 for a token that belongs to none.
+__device__ __forceinline__ int req_of(const int32_t* cu, int num_reqs, int t) {
+  int lo = 0, hi = num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
+}
+
+// The same by a whole warp: each round narrows the range 32-fold.
 __device__ __forceinline__ int req_of_warp(const int32_t* cu, int num_reqs, int t, int lane) {
   int lo = 0, n = num_reqs;
   while (n > 1) {

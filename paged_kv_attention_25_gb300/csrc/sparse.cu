@@ -29,16 +29,6 @@
 namespace pkv {
 namespace {
 
-// The request of token t (the last with cu <= t), or -1 for a token that belongs to none.
-__device__ __forceinline__ int req_of(const int32_t* cu, int num_reqs, int t) {
-  int lo = 0, hi = num_reqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
-}
-
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
 // x = m 2^e with m in [0.5, 1), for a normal x > 0.

@@ -535,13 +535,8 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(const int32_t* __restric
   griddep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) check_cu(cu, num_reqs, num_tokens, err);
   if (t >= num_tokens) return;
-  int lo = 0, hi = num_reqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  const int c0 = __ldg(cu + lo);
-  if (c0 < 0 || t < c0 || t >= __ldg(cu + lo + 1)) return;
+  const int r = req_of(cu, num_reqs, t), c0 = r >= 0 ? __ldg(cu + r) : -1;
+  if (c0 < 0) return;
   for (int w0 = 0; w0 < words; w0 += 32) {
     uint32_t bits = 0;
     // Parents lie strictly before their children, so the walk ends.
