@@ -136,11 +136,13 @@ int check_workspace(const void* workspace, size_t have, size_t need, const char*
 // head).  The rows form reads K and V once for every 16 rows, the tiles form once
 // for 128 (or 256), but has more to start and, for FP8 pools, to widen.  Measured
 // (rows / tiles, us): bf16, D = 128, 12 requests of 1.5 to 20 thousand tokens, 8
-// KV heads: 16 rows 66 / 68, 24 rows 91 / 69, 64 rows 116 / 72; D = 64, 32 requests
-// of 1 to 3 thousand: 32 rows 41 / 45, 48 rows 53 / 46; FP8, D = 128: 32 rows
-// 77 / 84, 48 rows 95 / 85; 40 KV heads: 32 rows 149 / 212, 64 rows 281 / 233.
+// KV heads: 16 rows 67 / 68, 24 rows 90 / 68, 64 rows 118 / 70; D = 64, 32 requests
+// of 1 to 3 thousand, 8 KV heads: 32 rows 39 / 45, 48 rows 49 / 45; FP8, D = 128, the
+// same 12 requests: 32 rows 66 / 85, 48 rows 80 / 86, 64 rows 96 / 87; 24 requests of
+// 300 to 4000 tokens, 40 KV heads: 32 rows 136 / 216, 64 rows 256 / 235.
 // A batch that gives every CTA of the rows form 16 blocks at most stays there
-// (one request of 240 tokens, 128 rows: 15.6 / 16.4).
+// (one request of 240 tokens, 2 KV heads, D = 64, 128 rows: 8.9 / 13.8).  The table's
+// width stands for the contexts' lengths, which only the device knows.
 bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks) {
   if (pool->tree_form != 0) return pool->tree_form == 2;
   if (num_reqs < 1) return false;

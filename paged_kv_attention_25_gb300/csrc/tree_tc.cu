@@ -25,8 +25,9 @@
 // Bound by the steps' order, not by one unit: a key tile of a pair takes 1.4 us, of
 // which the MMAs are 1.23 at the clock under load (scores, exponentials and P of one
 // group run while the other's products do).  12 requests of 1.5 to 40 thousand
-// tokens, 40 to 64 nodes, 64 query and 8 KV heads, D = 128: 234 us, 1.15 PFLOP/s, and
-// 16 for the merge.
+// tokens, 40 to 64 nodes, 64 query and 8 KV heads, D = 128: 228 us, 1.18 PFLOP/s, and
+// 16 for the merge.  Of these the shares' key tiles (391 units a CTA, a third of a
+// pair's 1.4 us each) are 182; tiles filled in part are in them (1.16 times the rows).
 //
 // Masks: key tiles that end at or before the prefix are seen whole.  In the others
 // each row's thread forms its 128 visibility bits from its mask words.  The V
