@@ -625,7 +625,7 @@ int pkv_debug_set(pkv_pool* pool, int what, int64_t value);
  * that each kernel's events bracket its own execution alone.  Enabling adds
  * one event pair per launch.  pkv_profile_read synchronises the recorded
  * events, adds their durations into *out and, if reset != 0, clears the
- * totals. */
+ * totals.  Launches of a call that is being captured are not timed. */
 int pkv_profile_enable(pkv_pool* pool, int on);
 int pkv_profile_read(pkv_pool* pool, pkv_profile* out, int reset);
 

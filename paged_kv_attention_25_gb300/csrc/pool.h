@@ -121,11 +121,14 @@ struct pkv_pool {
 
 namespace pkv {
 
-// Launch `fn` on `stream`, bracketed by profiling events when profiling is on.
+// Launch `fn` on `stream`, bracketed by profiling events when profiling is on (not in a capture: its events have no
+// times, and would be in the way of those that do).
 template <class F>
 int timed_launch(pkv_pool* pool, int kernel, void* stream, F&& fn) {
   cudaEvent_t a = nullptr, b = nullptr;
-  if (pool->prof_on) {
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (pool->prof_on && cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capturing) == cudaSuccess &&
+      capturing == cudaStreamCaptureStatusNone) {
     {
       std::lock_guard<std::mutex> lk(pool->prof_mu);
       a = pool->take_event();
