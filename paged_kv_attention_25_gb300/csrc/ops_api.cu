@@ -42,7 +42,8 @@ int check_tables(int max_blocks, int num_reqs, int num_tokens) {
   if (num_tokens < 0 || num_reqs < 0) return fail(PKV_EINVAL, "negative size");
   if (num_tokens == 0) return PKV_OK;
   if (num_reqs < 1 || max_blocks < 1) return fail(PKV_EINVAL, "num_reqs and max_blocks must be >= 1");
-  if (static_cast<int64_t>(max_blocks) * kBlockSize >= (1ll << 31) - kBlockSize) return fail(PKV_EINVAL, "max_blocks too large");
+  // (Key positions, rounded up to a tile, stay below 2^31.)
+  if (static_cast<int64_t>(max_blocks) * kBlockSize > (1ll << 31) - 1 - kTcKeys) return fail(PKV_EINVAL, "max_blocks too large");
   return PKV_OK;
 }
 
@@ -389,7 +390,7 @@ int pkv_fork(pkv_pool* pool, const int32_t* tables, int num_rows, int max_blocks
              size_t workspace_bytes, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
   if (num_rows < 0 || num_children < 0) return fail(PKV_EINVAL, "negative size");
-  if (max_blocks < 1 || static_cast<int64_t>(max_blocks) * kBlockSize >= (1ll << 31) - kBlockSize)
+  if (max_blocks < 1 || static_cast<int64_t>(max_blocks) * kBlockSize > (1ll << 31) - 1 - kTcKeys)
     return fail(PKV_EINVAL, "max_blocks must be >= 1 and leave positions below 2^31");
   if ((num_rows > 0 && (!tables || !lens || !caps)) || (num_children > 0 && (!parents || !new_caps || !new_tables)) ||
       !refs || !new_refs)
