@@ -509,11 +509,12 @@ int pkv_swap_in(pkv_pool* pool, const int32_t* block_ids, int n, const void* hos
  * pkv_summarize, pkv_fork, pkv_copy_blocks, pkv_compact, pkv_swap_out,
  * pkv_swap_in, another pkv_swap_in_ahead) or at pkv_swap_in_finish: that
  * call's stream waits for the transfer, and a kernel scatters the staged
- * blocks into block_ids.  A replayed graph lands nothing, and a call that is
- * being captured is refused (PKV_EINVAL) while a swap-in is pending: call
- * pkv_swap_in_finish before a replay or a capture.  Until then the pool's blocks keep their old contents, so calls
- * take effect in call order; read the storage from pkv_pool_kv_ptrs only
- * after pkv_swap_in_finish.
+ * blocks into block_ids.  A replayed graph lands nothing but what was both
+ * started and landed in its capture, and a call that is being captured is
+ * refused (PKV_EINVAL) while another swap-in is pending: call
+ * pkv_swap_in_finish before a replay or a capture.  Until a swap-in lands the
+ * pool's blocks keep their old contents, so calls take effect in call order;
+ * read the storage from pkv_pool_kv_ptrs only after pkv_swap_in_finish.
  * Layer pipelining: with one pool per model layer, issue every layer's
  * pkv_swap_in_ahead on one copy stream at the start of a step, then the
  * layers' attention in order on the compute stream; layer l then waits only

@@ -337,6 +337,14 @@ int pkv_pool_kv_ptrs(const pkv_pool* pool, void** k, void** v) {
 
 }  // extern "C"
 
+// The capture that `s` is part of, 0 if none.
+static int capture_of(cudaStream_t s, unsigned long long* id) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  PKV_CUDA(cudaStreamGetCaptureInfo(s, &status, id), "capture status");
+  if (status == cudaStreamCaptureStatusNone) *id = 0;
+  return PKV_OK;
+}
+
 // Lands a pending ahead-of-time swap-in on `stream`: waits for its transfer,
 // then scatters the staged blocks into the pool (every block at full HBM
 // rate, on up to one CTA per SM).  Every call that reads or writes the pool
@@ -346,9 +354,9 @@ int pkv::finish_swap_in(pkv_pool* pool, void* stream) {
   if (!pool->swap_pending) return PKV_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // (A capture cannot wait for a transfer that is not part of it, and trying to would end it.)
-  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  PKV_CUDA(cudaStreamIsCapturing(s, &capturing), "swap-in capture status");
-  if (capturing != cudaStreamCaptureStatusNone)
+  unsigned long long capture = 0;
+  if (int rc = capture_of(s, &capture)) return rc;
+  if (capture != 0 && capture != pool->swap_capture)
     return fail(PKV_EINVAL, "a swap-in is pending: call pkv_swap_in_finish before the capture");
   PKV_CUDA(cudaStreamWaitEvent(s, pool->swap_ready, 0), "swap-in wait");
   const int rc = timed_launch(pool, 4, stream, [&] {
@@ -814,6 +822,7 @@ int pkv_swap_in_ahead(pkv_pool* pool, const int32_t* block_ids, int n, const voi
   PKV_CUDA(cudaEventRecord(pool->swap_after, static_cast<cudaStream_t>(stream)), "swap-in order");
   PKV_CUDA(cudaStreamWaitEvent(cs, pool->swap_after, 0), "swap-in order");
   PKV_CUDA(cudaStreamWaitEvent(cs, pool->swap_staged_free, 0), "swap-in staging wait");
+  if ((rc = capture_of(cs, &pool->swap_capture))) return rc;
   PKV_CUDA(cudaMemcpyAsync(pool->swap_staging, host_buf, bytes, cudaMemcpyHostToDevice, cs), "swap-in transfer");
   PKV_CUDA(cudaEventRecord(pool->swap_ready, cs), "swap-in record");
   pool->swap_ids.assign(block_ids, block_ids + n);

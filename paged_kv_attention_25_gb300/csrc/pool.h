@@ -84,6 +84,7 @@ struct pkv_pool {
   size_t swap_staging_bytes = 0;
   cudaEvent_t swap_ready = nullptr, swap_staged_free = nullptr, swap_after = nullptr;
   bool swap_pending = false;
+  unsigned long long swap_capture = 0;   // the capture that the pending transfer is part of (0: none)
   std::vector<int32_t> swap_ids;
 
   // Test and diagnostic settings (pkv_debug_set).

@@ -63,3 +63,27 @@ def test_a_swap_in_is_finished_before_a_capture_and_before_a_replay():
     assert torch.equal(o, want) and torch.equal(lse, wl)
     assert torch.equal(pool.k[torch.as_tensor(ids).long().cuda()].cpu(), host.flip(0)[:, 0])
     pool.close()
+
+
+def test_a_swap_in_that_is_started_and_landed_in_one_capture():
+    pool = ref.random_pool(pkv.Pool(20, 2, 64), 3)
+    bt, cu = ref.dev(np.arange(10, dtype=np.int32)[None]), ref.dev(np.array([0, 1], np.int32))
+    pos = ref.dev(np.array([149], np.int32))
+    sel = ref.dev(np.tile(np.arange(10, dtype=np.int32), (1, 2, 1)))
+    q = torch.randn((1, 4, 64), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    pkv.pkv_sparse_attn(pool, q, pos, bt, cu, sel, 0.1)
+    host = torch.randn((3, 2, 2, 16, 64), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).pin_memory()
+    ids = np.array([2, 5, 9], np.int32)
+    copy = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):       # (the staging buffer is allocated here)
+        pkv.pkv_swap_in_ahead(pool, ids, host, copy)
+        o, lse = pkv.pkv_sparse_attn(pool, q, pos, bt, cu, sel, 0.1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(pool.k[torch.as_tensor(ids).long().cuda()].cpu(), host[:, 0])
+    want, wl = pkv.pkv_sparse_attn(pool, q, pos, bt, cu, sel, 0.1)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+    pool.close()
