@@ -155,3 +155,49 @@ def test_a_fork_behind_one_without_children_sees_its_counts():
     both_ways(steps)
     assert pkv.pkv_check_device_errors(pool) == 0
     pool.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("form", [1, 2], ids=["rows", "tiles"])
+def test_an_attention_behind_moved_rows_and_copied_pages_sees_them(form, dtype):
+    """Compactions and page copies of the tables' own pages, each followed at once by the tree's and the lists' attention."""
+    rng = np.random.default_rng(6)
+    kw = dict(dtype=dtype, k_scale=0.02, v_scale=0.5) if dtype != "bf16" else {}
+    pool = ref.random_pool(pkv.Pool(200, 2, 128, **kw), 6)
+    pkv.pkv_debug_set(pool, pkv.PKV_DEBUG_TREE_FORM, form)
+    ctx = np.array([700, 90, 1100], np.int32)
+    tables = ref.tables(rng, ctx, 200)
+    bt, lens, cu = ref.dev(tables), ref.dev(ctx), ref.dev(np.array([0, 20, 40, 60], np.int32))
+    pos = ref.dev(np.concatenate([np.arange(c - 20, c) for c in ctx]).astype(np.int32))
+    prefix, mask = ref.dev(ctx - 20), torch.full((60, 1), 0xFFFFF, dtype=torch.int32, device="cuda")
+    q = torch.randn((60, 16, 128), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    sel = ref.dev(np.tile(np.arange(tables.shape[1], dtype=np.int32), (60, 2, 1)))
+    used = np.unique(tables[tables >= 0])
+    free = np.setdiff1d(np.arange(200), used)
+    moves = []
+    for _ in range(12):
+        src = np.concatenate([np.sort(rng.choice(np.arange(40, c), 30, replace=False)) for c in ctx]).astype(np.int32)
+        to = rng.permutation(used)[:40].astype(np.int32)
+        moves.append((ref.dev(np.array([0, 30, 60, 90], np.int32)), ref.dev(src), ref.dev(rng.integers(0, 10, 3).astype(np.int32)),
+                      ref.dev(rng.choice(free, 40).astype(np.int32)), ref.dev(to)))
+    k0, v0 = pool.k.clone(), pool.v.clone()
+
+    def steps(done):
+        pool.k.copy_(k0)
+        pool.v.copy_(v0)
+        outs = []
+        for mcu, src, dst, frm, to in moves:
+            for change in (lambda: pkv.pkv_compact(pool, bt, mcu, src, dst), lambda: pkv.pkv_copy_blocks(pool, frm, to)):
+                change()
+                done()
+                outs += list(pkv.pkv_tree_attn(pool, q, bt, lens, prefix, cu, mask, 0.1))
+                done()
+                change()
+                done()
+                outs += list(pkv.pkv_sparse_attn(pool, q, pos, bt, cu, sel, 0.1))
+                done()
+        return outs
+
+    both_ways(steps)
+    assert pkv.pkv_check_device_errors(pool) == 0
+    pool.close()
