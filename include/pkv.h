@@ -83,6 +83,16 @@ extern "C" {
  * |q| within f16's range, below 65504).  Q, O and the new K/V given to
  * pkv_append stay bf16. */
 #define PKV_DTYPE_FP8_E4M3 1
+/* Int8 KV cache with an exponent for each block and KV head: K and V stored as
+ * 8-bit integers, [num_blocks][num_kv_heads][block_size][head_dim], and K and V
+ * exponents, [num_blocks][num_kv_heads] int8: the value of a code c is c * 2^e
+ * with the exponent of its (block, KV head), |c| <= 127, -126 <= e <= 121 (other
+ * exponents, in pages never written, are read as the nearer of these).  Every
+ * value is a bf16 value.  Written by pkv_append_int8, read by pkv_score_attn and
+ * pkv_read_rows, shared and copied with their exponents by pkv_fork and
+ * pkv_copy_blocks; the other calls on the pool's K and V return
+ * PKV_EUNSUPPORTED. */
+#define PKV_DTYPE_INT8 2
 
 /* Bits of the device error word (pkv_check_device_errors). */
 #define PKV_DEVERR_BLOCK_ID 1u   /* a block-table entry outside [0, num_blocks) */
@@ -91,6 +101,7 @@ extern "C" {
 #define PKV_DEVERR_TIMEOUT 4u    /* a bounded wait inside a kernel gave up */
 #define PKV_DEVERR_INTERNAL 8u   /* a kernel found its launch configuration unusable */
 #define PKV_DEVERR_NO_PAGES 16u  /* pkv_fork found fewer free pages than it needs */
+#define PKV_DEVERR_VALUE 32u     /* pkv_append_int8 met a value that is infinite or NaN */
 
 typedef struct pkv_pool pkv_pool; /* opaque */
 
@@ -99,16 +110,21 @@ typedef struct {
   int block_size;   /* tokens per block; must be 16 */
   int num_kv_heads; /* >= 1 */
   int head_dim;     /* 64 or 128 */
-  int dtype;        /* PKV_DTYPE_BF16 or PKV_DTYPE_FP8_E4M3 */
+  int dtype;        /* PKV_DTYPE_BF16, PKV_DTYPE_FP8_E4M3 or PKV_DTYPE_INT8 */
   /* Optional caller-owned device storage for the two pools (each
    * num_blocks*num_kv_heads*block_size*head_dim*E bytes, E = 2 for bf16 and 1
-   * for fp8, 16-byte aligned).  NULL: the library allocates (and zero-fills)
+   * for fp8 and int8, 16-byte aligned).  NULL: the library allocates (and zero-fills)
    * the storage itself. */
   void* k_storage;
   void* v_storage;
   /* PKV_DTYPE_FP8_E4M3 only: dequantisation scales (finite, > 0). */
   float k_scale;
   float v_scale;
+  /* PKV_DTYPE_INT8 only: the caller's exponent arrays (device,
+   * num_blocks*num_kv_heads bytes each), given if and only if k_storage and
+   * v_storage are. */
+  int8_t* k_exps;
+  int8_t* v_exps;
 } pkv_pool_desc;
 
 /* Host copies of the batch metadata, used to plan the work split.
@@ -160,6 +176,8 @@ int pkv_pool_destroy(pkv_pool* pool);
 
 /* Device addresses of the K and V pools (for tests and host gathers). */
 int pkv_pool_kv_ptrs(const pkv_pool* pool, void** k, void** v);
+/* Device addresses of an int8 pool's exponents (PKV_EINVAL for other pools). */
+int pkv_pool_exps(const pkv_pool* pool, int8_t** k_exps, int8_t** v_exps);
 
 /*
  * Paged KV append ("LLM上下文缓存与状态复用机制的分析和探索" section 3.1; the new
@@ -473,6 +491,47 @@ int pkv_copy_blocks(pkv_pool* pool, const int32_t* src, const int32_t* dst, int 
  */
 int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_keep,
                 const int32_t* src_positions, const int32_t* dst_starts, int num_kept, void* stream);
+
+/*
+ * ---- An 8-bit cache with an exponent for each block: writing and reading ----
+ *
+ * pkv_append_int8 quantises the new rows into an int8 pool's blocks.  The rows
+ * x of the call that fall into one block (positions as for pkv_append) set, for
+ * each KV head, for K and for V by itself:
+ *   e  = max(e_old, the smallest e' in [-126, 121] with |x| <= 127 * 2^e' for all of them),
+ *        without e_old if the block holds no tokens;
+ *   c  = round-to-even(x / 2^e) for the new rows,
+ *   c' = round-to-even(c * 2^(e_old - e)) for the codes of the tokens it holds.
+ * held_lens[r]: the tokens that request r holds before the call: slots at
+ * positions below it keep their values (but for that rounding) unless the call
+ * writes them, and a block with such slots holds tokens.  What other slots of a
+ * written block hold is not kept.  A new conversation, or a page taken anew, has
+ * held_lens 0 there: what an earlier owner left has no say.
+ * Magnitudes above 127 * 2^121 count as that, infinities among them; NaN counts
+ * as 0; infinities and NaN set PKV_DEVERR_VALUE.
+ * Precondition: tokens of one block follow one another in the batch (as ascending
+ * positions do); of several tokens at one position the last one counts.  No two
+ * requests of the call write one block.  Rows of tokens that belong to no request
+ * are not read; a position or block id out of range is flagged and skipped.
+ * Reads its metadata on the device (all arrays device), can be captured into a
+ * graph, runs on `stream` alone; k_new and v_new 16-byte aligned.
+ */
+int pkv_append_int8(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
+                    const int32_t* positions, const int32_t* held_lens, const void* k_new, const void* v_new,
+                    int num_tokens, void* stream);
+
+/*
+ * Reads rows of a cache back: for every token t of request r (rows
+ * [cu_lens[r], cu_lens[r + 1])) the K and V rows at positions[t], all KV heads, as
+ *   k_out, v_out [num_tokens][num_kv_heads][head_dim] bf16 (16-byte aligned)
+ * from a pool of any type: bf16 rows as they are, int8 values exactly, FP8 codes
+ * times their scale, rounded once.  Positions in any order, repeated or not.  A
+ * position or block id out of range is flagged and its rows are zero; rows of
+ * tokens that belong to no request are left as they are.  All arrays device; can
+ * be captured, runs on `stream` alone.
+ */
+int pkv_read_rows(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_lens,
+                  const int32_t* positions, int num_tokens, void* k_out, void* v_out, void* stream);
 
 /* Statistics of the last plan built on this pool. */
 int pkv_last_plan_stats(const pkv_pool* pool, pkv_plan_stats* out);

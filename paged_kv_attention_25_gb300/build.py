@@ -22,12 +22,13 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
 SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_append.cu", "attn_static.cu", "swap.cu",
-           "ops_api.cu", "tree.cu", "tree_tc.cu", "sparse.cu", "pages.cu"]
+           "ops_api.cu", "tree.cu", "tree_tc.cu", "sparse.cu", "pages.cu", "int8.cu"]
 HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh", "ops.h", "rows.cuh", "sched.cuh",
-           "tc.cuh"]
+           "tc.cuh", "int8.cuh"]
 BINDING = os.path.join(BUILD, "pkv_binding.so")
 BINDING_STAMP = os.path.join(BUILD, "pkv_binding.stamp")   # binding_key(), and "built" or "left out"
 BINDING_SOURCE = "binding.cpp"
+BINDING_HEADERS = ["binding_score.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -70,7 +71,7 @@ def _binding_stale() -> bool:
     last = built_for()
     if last is None or last[0] != binding_key():
         return True
-    return last[1] and _newer([os.path.join(CSRC, BINDING_SOURCE)], BINDING)
+    return last[1] and _newer((os.path.join(CSRC, s) for s in [BINDING_SOURCE] + BINDING_HEADERS), BINDING)
 
 
 def _torch():

@@ -177,15 +177,19 @@ int pkv_pool_create(const pkv_pool_desc* desc, pkv_pool** out) {
   if (desc->num_blocks < 1 || desc->num_kv_heads < 1) return fail(PKV_EINVAL, "num_blocks and num_kv_heads must be >= 1");
   if (desc->block_size != kBlockSize) return fail(PKV_EUNSUPPORTED, "block_size must be 16");
   if (desc->head_dim != 64 && desc->head_dim != 128) return fail(PKV_EUNSUPPORTED, "head_dim must be 64 or 128");
-  if (desc->dtype != PKV_DTYPE_BF16 && desc->dtype != PKV_DTYPE_FP8_E4M3)
-    return fail(PKV_EUNSUPPORTED, "dtype must be PKV_DTYPE_BF16 or PKV_DTYPE_FP8_E4M3");
-  const bool fp8 = desc->dtype == PKV_DTYPE_FP8_E4M3;
+  if (desc->dtype != PKV_DTYPE_BF16 && desc->dtype != PKV_DTYPE_FP8_E4M3 && desc->dtype != PKV_DTYPE_INT8)
+    return fail(PKV_EUNSUPPORTED, "dtype must be PKV_DTYPE_BF16, PKV_DTYPE_FP8_E4M3 or PKV_DTYPE_INT8");
+  const bool fp8 = desc->dtype == PKV_DTYPE_FP8_E4M3, int8 = desc->dtype == PKV_DTYPE_INT8;
   if (fp8 && !(desc->k_scale > 0.f && desc->k_scale <= 3.4e38f && desc->v_scale > 0.f && desc->v_scale <= 3.4e38f))
     return fail(PKV_EINVAL, "fp8 pools need finite k_scale and v_scale > 0");
   if ((desc->k_storage == nullptr) != (desc->v_storage == nullptr))
     return fail(PKV_EINVAL, "give both k_storage and v_storage or neither");
   if (desc->k_storage && (!aligned16(desc->k_storage) || !aligned16(desc->v_storage)))
     return fail(PKV_EINVAL, "pool storage must be 16-byte aligned");
+  if (int8) {
+    if ((desc->k_exps == nullptr) != (desc->v_exps == nullptr) || (desc->k_exps == nullptr) != (desc->k_storage == nullptr))
+      return fail(PKV_EINVAL, "int8 pools: give k_storage, v_storage, k_exps and v_exps, or none of them");
+  }
   auto* p = new pkv_pool();
   p->num_blocks = desc->num_blocks;
   p->block_size = desc->block_size;
@@ -196,10 +200,13 @@ int pkv_pool_create(const pkv_pool_desc* desc, pkv_pool** out) {
     p->k_scale = desc->k_scale;
     p->v_scale = desc->v_scale;
   }
+  if (int8) p->elem_bytes = 1;
   auto cleanup = [p](int rc) {
     if (p->owns) {
       cudaFree(p->k);
       cudaFree(p->v);
+      cudaFree(p->k_exps);
+      cudaFree(p->v_exps);
     }
     if (p->d_err) cudaFree(p->d_err);
     for (int i = 0; i < 2; ++i) {
@@ -227,12 +234,23 @@ int pkv_pool_create(const pkv_pool_desc* desc, pkv_pool** out) {
   if (desc->k_storage) {
     p->k = desc->k_storage;
     p->v = desc->v_storage;
+    if (int8) {
+      p->k_exps = desc->k_exps;
+      p->v_exps = desc->v_exps;
+    }
   } else {
     p->owns = true;
     if (cudaMalloc(&p->k, bytes) != cudaSuccess) { p->k = nullptr; return cleanup(fail(PKV_ENOMEM, "cudaMalloc K pool")); }
     if (cudaMalloc(&p->v, bytes) != cudaSuccess) { p->v = nullptr; return cleanup(fail(PKV_ENOMEM, "cudaMalloc V pool")); }
     if (cudaMemset(p->k, 0, bytes) != cudaSuccess || cudaMemset(p->v, 0, bytes) != cudaSuccess)
       return cleanup(fail(PKV_ECUDA, "cudaMemset pool"));
+    if (int8) {
+      const size_t n = static_cast<size_t>(desc->num_blocks) * desc->num_kv_heads;
+      for (int8_t** x : {&p->k_exps, &p->v_exps}) {
+        if (cudaMalloc(x, n) != cudaSuccess) { *x = nullptr; return cleanup(fail(PKV_ENOMEM, "cudaMalloc exponents")); }
+        if (cudaMemset(*x, 0, n) != cudaSuccess) return cleanup(fail(PKV_ECUDA, "cudaMemset exponents"));
+      }
+    }
   }
   if (cudaMalloc(&p->d_err, sizeof(unsigned)) != cudaSuccess) { p->d_err = nullptr; return cleanup(fail(PKV_ENOMEM, "cudaMalloc error word")); }
   if (cudaMemset(p->d_err, 0, sizeof(unsigned)) != cudaSuccess) return cleanup(fail(PKV_ECUDA, "cudaMemset error word"));
@@ -274,9 +292,9 @@ int pkv_pool_create(const pkv_pool_desc* desc, pkv_pool** out) {
 
   // The attention kernels' block maps.
   {
-    int rc = make_tmap(&p->tmap_k, p->k, p->num_blocks, p->num_kv_heads, p->head_dim, fp8);
+    int rc = make_tmap(&p->tmap_k, p->k, p->num_blocks, p->num_kv_heads, p->head_dim, fp8 || int8);
     if (rc) return cleanup(rc);
-    rc = make_tmap(&p->tmap_v, p->v, p->num_blocks, p->num_kv_heads, p->head_dim, fp8);
+    rc = make_tmap(&p->tmap_v, p->v, p->num_blocks, p->num_kv_heads, p->head_dim, fp8 || int8);
     if (rc) return cleanup(rc);
     p->dmap_k = p->tmap_k;
     p->dmap_v = p->tmap_v;
@@ -299,6 +317,8 @@ int pkv_pool_destroy(pkv_pool* pool) {
   if (pool->owns) {
     cudaFree(pool->k);
     cudaFree(pool->v);
+    cudaFree(pool->k_exps);
+    cudaFree(pool->v_exps);
   }
   cudaFree(pool->d_err);
   for (int i = 0; i < 2; ++i) {
@@ -332,6 +352,14 @@ int pkv_pool_kv_ptrs(const pkv_pool* pool, void** k, void** v) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
   if (k) *k = pool->k;
   if (v) *v = pool->v;
+  return PKV_OK;
+}
+
+int pkv_pool_exps(const pkv_pool* pool, int8_t** k_exps, int8_t** v_exps) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (!pool->k_exps) return fail(PKV_EINVAL, "the pool is not an int8 pool");
+  if (k_exps) *k_exps = pool->k_exps;
+  if (v_exps) *v_exps = pool->v_exps;
   return PKV_OK;
 }
 
@@ -374,6 +402,7 @@ extern "C" {
 int pkv_append(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
                const int32_t* positions, const void* k_new, const void* v_new, int num_tokens, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (int rc = refuse_int8(pool, "pkv_append (pkv_append_int8 does)")) return rc;
   if (num_tokens < 0 || num_reqs < 0) return fail(PKV_EINVAL, "negative size");
   if (num_tokens == 0) return PKV_OK;
   if (num_reqs < 1 || max_blocks < 1) return fail(PKV_EINVAL, "num_reqs and max_blocks must be >= 1");
@@ -407,6 +436,7 @@ static int plan_for(pkv_pool* pool, int num_q_heads, int num_reqs, int num_token
 int pkv_paged_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens,
                                   const pkv_host_meta* host_meta, size_t* bytes) {
   if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
+  if (int rc = refuse_int8(pool, "pkv_paged_attn (pkv_score_attn does)")) return rc;
   if (num_q_heads < 1 || num_q_heads % pool->num_kv_heads) return fail(PKV_EINVAL, "num_q_heads must be a multiple of num_kv_heads");
   if (num_reqs < 0 || num_tokens < 0) return fail(PKV_EINVAL, "negative size");
   std::lock_guard<std::mutex> lk(pool->mu);
@@ -420,6 +450,7 @@ int pkv_paged_attn_workspace_size(pkv_pool* pool, int num_q_heads, int num_reqs,
 
 int pkv::paged_attn_call(pkv_pool* pool, const AttnCall& c) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (int rc = refuse_int8(pool, "the causal paged attention (pkv_score_attn does)")) return rc;
   if (c.num_tokens < 0 || c.num_reqs < 0) return fail(PKV_EINVAL, "negative size");
   if (c.num_tokens == 0) return PKV_OK;
   if (c.num_q_heads < 1 || c.num_q_heads % pool->num_kv_heads)
@@ -734,6 +765,7 @@ int pkv_last_plan_stats(const pkv_pool* pool, pkv_plan_stats* out) {
 
 static int swap_impl(pkv_pool* pool, const int32_t* ids, int n, void* host, bool out, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (int rc = refuse_int8(pool, out ? "pkv_swap_out" : "pkv_swap_in")) return rc;
   if (n < 0) return fail(PKV_EINVAL, "negative count");
   if (n == 0) return PKV_OK;
   if (!ids || !host) return fail(PKV_EINVAL, "NULL block_ids or host buffer");
@@ -784,6 +816,7 @@ int pkv_swap_in(pkv_pool* pool, const int32_t* block_ids, int n, const void* hos
 int pkv_swap_in_ahead(pkv_pool* pool, const int32_t* block_ids, int n, const void* host_buf, void* copy_stream,
                       void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (int rc = refuse_int8(pool, "pkv_swap_in_ahead")) return rc;
   if (n < 0) return fail(PKV_EINVAL, "negative count");
   if (n == 0) return PKV_OK;
   if (!block_ids || !host_buf) return fail(PKV_EINVAL, "NULL block_ids or host buffer");

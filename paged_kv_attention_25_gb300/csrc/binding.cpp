@@ -255,14 +255,18 @@ struct Output {
 struct Table {
   at::Tensor made;
   PyObject* given;
-  int32_t* at;
-  Table(const Pool* pool, const Call& call, PyObject* o, const char* name, at::IntArrayRef shape) : given(o) {
+  void* data;
+  int32_t* at;   // data as int32
+  Table(const Pool* pool, const Call& call, PyObject* o, const char* name, at::IntArrayRef shape,
+        at::ScalarType type = at::kInt)
+      : given(o) {
     if (o == Py_None) {
-      made = call.make(shape, at::kInt);
-      at = static_cast<int32_t*>(made.data_ptr());
+      made = call.make(shape, type);
+      data = made.data_ptr();
     } else {
-      at = address<int32_t>(pool, o, name, at::kInt, shape);
+      data = address(pool, o, name, type, shape);
     }
+    at = static_cast<int32_t*>(data);
   }
   PyObject* result() { return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(given); }
 };
@@ -415,6 +419,8 @@ PyObject* compact(Pool* p, Args a) {
   Py_RETURN_NONE;
 }
 
+#include "binding_score.h"
+
 // codes, exps
 PyObject* check_summary(Pool* p, Args a) {
   const Summary s(p, a[0], a[1]);
@@ -454,6 +460,7 @@ PyMethodDef kMethods[] = {entry<tree_mask, 6>("tree_mask"),         entry<tree_a
                           entry<sparse_attn, 11>("sparse_attn"),    entry<fork, 12>("fork"),
                           entry<copy_blocks, 5>("copy_blocks"),     entry<compact, 5>("compact"),
                           entry<check_summary, 2>("check_summary"), entry<close, 0>("close"),
+                          entry<append_int8, 7>("append_int8"),     entry<read_rows, 6>("read_rows"),
                           {nullptr, nullptr, 0, nullptr}};
 
 // Pool(handle, device, num_blocks, num_kv_heads, head_dim)

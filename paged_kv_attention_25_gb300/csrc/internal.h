@@ -124,8 +124,10 @@ struct PoolView {
   const void* v;
   int num_blocks, num_kv_heads, head_dim;
   unsigned* err;     // device error word
-  int elem_bytes;    // 2: bf16 pool; 1: fp8 e4m3 codes
+  int elem_bytes;    // 2: bf16 pool; 1: fp8 e4m3 (or int8) codes
   float k_scale, v_scale;   // fp8 dequantisation scales (1 for bf16)
+  int8_t* k_exps;    // int8 pool: exponents [num_blocks][num_kv_heads] (else nullptr; its elem_bytes is 1, too)
+  int8_t* v_exps;
 };
 
 // Block ids of one swap launch, passed by value as a kernel parameter.

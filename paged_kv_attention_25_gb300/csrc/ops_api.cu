@@ -197,7 +197,9 @@ int pkv_tree_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t*
                   int num_tokens, const uint32_t* tree_mask, int mask_words, float scale, void* o, float* lse,
                   void* workspace, size_t workspace_bytes, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
-  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  int rc = refuse_int8(pool, "pkv_tree_attn");
+  if (rc) return rc;
+  rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc || num_tokens == 0) return rc;
   if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
   if (!q || !block_tables || !ctx_lens || !prefix_lens || !cu_q_lens || !tree_mask || !o)
@@ -252,7 +254,9 @@ int pkv_summarize(pkv_pool* pool, const int32_t* block_tables, int max_blocks, i
                   const int32_t* positions, const int32_t* ctx_lens, int num_tokens, int8_t* codes, int8_t* exps,
                   void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
-  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  int rc = refuse_int8(pool, "pkv_summarize");
+  if (rc) return rc;
+  rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc || num_tokens == 0) return rc;
   if (!block_tables || !cu_q_lens || !positions || !ctx_lens) return fail(PKV_EINVAL, "NULL device pointer");
   if ((rc = check_summary(codes, exps))) return rc;
@@ -289,7 +293,9 @@ int pkv_select_blocks(pkv_pool* pool, const void* q, int num_q_heads, const int3
                       int num_tokens, const int8_t* codes, const int8_t* exps, int top_k, int sinks, int recent,
                       int32_t* selected, void* workspace, size_t workspace_bytes, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
-  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  int rc = refuse_int8(pool, "pkv_select_blocks");
+  if (rc) return rc;
+  rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
   if ((rc = check_top_k(top_k))) return rc;
   if (sinks < 0 || recent < 0) return fail(PKV_EINVAL, "need sinks >= 0, recent >= 0");
@@ -339,7 +345,9 @@ int pkv_sparse_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_
                     const int32_t* selected, int top_k, float scale, void* o, float* lse, void* workspace,
                     size_t workspace_bytes, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
-  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  int rc = refuse_int8(pool, "pkv_sparse_attn");
+  if (rc) return rc;
+  rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
   if ((rc = check_top_k(top_k))) return rc;
   if (num_tokens == 0) return PKV_OK;
@@ -436,10 +444,49 @@ int pkv_copy_blocks(pkv_pool* pool, const int32_t* src, const int32_t* dst, int 
   return PKV_OK;
 }
 
+int pkv_append_int8(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_q_lens,
+                    const int32_t* positions, const int32_t* held_lens, const void* k_new, const void* v_new,
+                    int num_tokens, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  if (!pool->k_exps) return fail(PKV_EINVAL, "pkv_append_int8 needs an int8 pool");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc || num_tokens == 0) return rc;
+  if (!block_tables || !cu_q_lens || !positions || !held_lens || !k_new || !v_new)
+    return fail(PKV_EINVAL, "NULL device pointer");
+  if (!aligned16(k_new) || !aligned16(v_new)) return fail(PKV_EINVAL, "k_new / v_new must be 16-byte aligned");
+  DeviceGuard guard(pool->device);
+  rc = timed_launch(pool, 0, stream, [&] {
+    return launch_append_int8(pool->view(), pool->k, pool->v, block_tables, max_blocks, num_reqs, cu_q_lens, positions,
+                              held_lens, k_new, v_new, num_tokens, pool->num_sms, stream);
+  });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "int8 append launch");
+  return PKV_OK;
+}
+
+int pkv_read_rows(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_lens,
+                  const int32_t* positions, int num_tokens, void* k_out, void* v_out, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc || num_tokens == 0) return rc;
+  if (!block_tables || !cu_lens || !positions || !k_out || !v_out) return fail(PKV_EINVAL, "NULL device pointer");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(PKV_EINVAL, "k_out / v_out must be 16-byte aligned");
+  if (2ll * 16 * pool->num_kv_heads * pool->head_dim >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many KV heads");
+  DeviceGuard guard(pool->device);
+  if ((rc = finish_swap_in(pool, stream))) return rc;
+  rc = timed_launch(pool, 0, stream, [&] {
+    return launch_read_rows(pool->view(), block_tables, max_blocks, num_reqs, cu_lens, positions, num_tokens, k_out,
+                            v_out, pool->num_sms, stream);
+  });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "row read launch");
+  return PKV_OK;
+}
+
 int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int num_reqs, const int32_t* cu_keep,
                 const int32_t* src_positions, const int32_t* dst_starts, int num_kept, void* stream) {
   if (!pool) return fail(PKV_EINVAL, "pool is NULL");
-  int rc = check_tables(max_blocks, num_reqs, num_kept);
+  int rc = refuse_int8(pool, "pkv_compact");
+  if (rc) return rc;
+  rc = check_tables(max_blocks, num_reqs, num_kept);
   if (rc || num_kept == 0) return rc;
   if (!block_tables || !cu_keep || !src_positions || !dst_starts) return fail(PKV_EINVAL, "NULL device pointer");
   if (static_cast<int64_t>(num_reqs) * pool->num_kv_heads * pool->head_dim >= (1ll << 31))

@@ -419,6 +419,14 @@ __global__ void __launch_bounds__(256) fork_fill_kernel(const ForkArgs a) {
     for (int k = 0; k < kCopyBatch; ++k)
       if (e0 + 256 * k < chunks) pool[k][dst * page + at[k]] = v[k];
   }
+  if (a.pool.k_exps) {   // int8: the copied codes' exponents
+    const int hkv = a.pool.num_kv_heads;
+    for (int e = tid; e < 2 * hkv; e += 256) {
+      int8_t* x = e < hkv ? a.pool.k_exps : a.pool.v_exps;
+      const int g = e < hkv ? e : e - hkv;
+      x[static_cast<int64_t>(dst) * hkv + g] = x[static_cast<int64_t>(src) * hkv + g];
+    }
+  }
   if (a.codes) {
     const int n = a.pool.num_kv_heads * 2 * a.pool.head_dim / 16;
     uint4* codes = reinterpret_cast<uint4*>(a.codes);
@@ -455,6 +463,14 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const PoolView pool, u
   for (int k = 0; k < kCopyBatch; ++k) {
     const int64_t e = (static_cast<int64_t>(blockIdx.y) * kCopyBatch + k) * 256 + tid;
     if (e < 2 * page) (e < page ? kp[d * page + e] : vp[d * page + e - page]) = v[k];
+  }
+  if (pool.k_exps && blockIdx.y == 0) {   // int8: the copied codes' exponents
+    const int hkv = pool.num_kv_heads;
+    for (int e = tid; e < 2 * hkv; e += 256) {
+      int8_t* x = e < hkv ? pool.k_exps : pool.v_exps;
+      const int g = e < hkv ? e : e - hkv;
+      x[static_cast<int64_t>(d) * hkv + g] = x[static_cast<int64_t>(s) * hkv + g];
+    }
   }
   if (codes && blockIdx.y == 0) {
     const int64_t n = static_cast<int64_t>(pool.num_kv_heads) * 2 * pool.head_dim / 16;

@@ -34,8 +34,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 struct pkv_pool {
   int num_blocks = 0, block_size = 0, num_kv_heads = 0, head_dim = 0;
-  int elem_bytes = 2;                 // 2: bf16; 1: fp8 e4m3 codes
+  int elem_bytes = 2;                 // 2: bf16; 1: fp8 e4m3 or int8 codes
   float k_scale = 1.f, v_scale = 1.f;
+  int8_t* k_exps = nullptr;           // int8 pools (elem_bytes 1): exponents [num_blocks][num_kv_heads]
+  int8_t* v_exps = nullptr;
   void* k = nullptr;
   void* v = nullptr;
   bool owns = false;
@@ -103,7 +105,7 @@ struct pkv_pool {
   pkv_profile totals{};
 
   pkv::PoolView view() const {
-    return pkv::PoolView{k, v, num_blocks, num_kv_heads, head_dim, d_err, elem_bytes, k_scale, v_scale};
+    return pkv::PoolView{k, v, num_blocks, num_kv_heads, head_dim, d_err, elem_bytes, k_scale, v_scale, k_exps, v_exps};
   }
   // Bytes of one physical block of K (or V): all KV heads.
   size_t block_bytes() const { return static_cast<size_t>(num_kv_heads) * pkv::kBlockSize * head_dim * elem_bytes; }
@@ -121,6 +123,12 @@ struct pkv_pool {
 };
 
 namespace pkv {
+
+// For calls that have no form for int8 pools.
+inline int refuse_int8(const pkv_pool* pool, const char* call) {
+  if (!pool->k_exps) return PKV_OK;
+  return fail(PKV_EUNSUPPORTED, std::string(call) + " does not support int8 pools");
+}
 
 // Launch `fn` on `stream`, bracketed by profiling events when profiling is on (not in a capture: its events have no
 // times, and would be in the way of those that do).

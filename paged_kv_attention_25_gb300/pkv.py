@@ -36,6 +36,7 @@ PKV_DEVERR_POSITION = 2
 PKV_DEVERR_TIMEOUT = 4
 PKV_DEVERR_INTERNAL = 8
 PKV_DEVERR_NO_PAGES = 16
+PKV_DEVERR_VALUE = 32
 PKV_DEBUG_WAIT_LIMIT_NS = 1
 PKV_DEBUG_WITHHOLD_COPY = 2
 PKV_DEBUG_FUSED_FORM = 3
@@ -56,6 +57,7 @@ EXPORTED = (
     "pkv_tree_mask", "pkv_tree_attn_workspace_size", "pkv_tree_attn", "pkv_summarize", "pkv_select_blocks_workspace_size",
     "pkv_select_blocks",
     "pkv_sparse_attn_workspace_size", "pkv_sparse_attn", "pkv_fork_workspace_size", "pkv_fork", "pkv_copy_blocks", "pkv_compact",
+    "pkv_pool_exps", "pkv_append_int8", "pkv_read_rows",
 )
 
 
@@ -67,12 +69,14 @@ class PkvError(RuntimeError):
 
 PKV_DTYPE_BF16 = 0
 PKV_DTYPE_FP8_E4M3 = 1
+PKV_DTYPE_INT8 = 2
 
 
 class pkv_pool_desc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int), ("block_size", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("k_storage", ctypes.c_void_p),
-                ("v_storage", ctypes.c_void_p), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+                ("v_storage", ctypes.c_void_p), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("k_exps", ctypes.c_void_p), ("v_exps", ctypes.c_void_p)]
 
 
 class pkv_host_meta(ctypes.Structure):
@@ -161,6 +165,9 @@ def load_library():
             "pkv_fork": [P, P, I, I, P, P, P, P, I, P, P, P, P, P, P, ctypes.c_size_t, P],
             "pkv_copy_blocks": [P, P, P, I, P, P, P],
             "pkv_compact": [P, P, I, I, P, P, P, I, P],
+            "pkv_pool_exps": [P, ctypes.POINTER(P), ctypes.POINTER(P)],
+            "pkv_append_int8": [P, P, I, I, P, P, P, P, P, I, P],
+            "pkv_read_rows": [P, P, I, I, P, P, I, P, P, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -250,36 +257,55 @@ class HostMeta:
                                None if self.q_positions is None else self.q_positions.ctypes.data)
 
 
+_STORAGE = {"bf16": (PKV_DTYPE_BF16, torch.bfloat16), "fp8_e4m3": (PKV_DTYPE_FP8_E4M3, torch.uint8),
+            "int8": (PKV_DTYPE_INT8, torch.int8)}
+
+
 class Pool:
     """A KV block pool: K and V storage [num_blocks, num_kv_heads, 16, head_dim] in torch memory, bf16
-    (dtype "bf16") or E4M3 codes as uint8 (dtype "fp8_e4m3", values code * k_scale / code * v_scale)."""
+    (dtype "bf16"), E4M3 codes as uint8 (dtype "fp8_e4m3", values code * k_scale / code * v_scale), or int8 codes
+    with an exponent for each block and KV head (dtype "int8", values code * 2 ** k_exps / v_exps
+    [num_blocks, num_kv_heads] int8)."""
 
     def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, block_size: int = 16,
                  device=None, k_storage: torch.Tensor | None = None, v_storage: torch.Tensor | None = None,
-                 dtype: str = "bf16", k_scale: float = 1.0, v_scale: float = 1.0):
+                 dtype: str = "bf16", k_scale: float = 1.0, v_scale: float = 1.0,
+                 k_exps: torch.Tensor | None = None, v_exps: torch.Tensor | None = None):
         lib = load_library()
-        if dtype not in ("bf16", "fp8_e4m3"):
-            raise ValueError("dtype must be 'bf16' or 'fp8_e4m3'")
-        fp8 = dtype == "fp8_e4m3"
-        tdtype = torch.uint8 if fp8 else torch.bfloat16
+        if dtype not in _STORAGE:
+            raise ValueError("dtype must be 'bf16', 'fp8_e4m3' or 'int8'")
+        code, tdtype = _STORAGE[dtype]
         if device is None:
             device = torch.device("cuda", torch.cuda.current_device())
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
+        if dtype == "int8":
+            if len({x is None for x in (k_storage, v_storage, k_exps, v_exps)}) != 1:
+                raise ValueError("int8 pools: give k_storage, v_storage, k_exps and v_exps, or none of them")
+        elif k_exps is not None or v_exps is not None:
+            raise ValueError("k_exps and v_exps are those of int8 pools")
         if k_storage is None:
             k_storage = torch.zeros(shape, dtype=tdtype, device=device)
             v_storage = torch.zeros(shape, dtype=tdtype, device=device)
+            if dtype == "int8":
+                k_exps = torch.zeros(shape[:2], dtype=torch.int8, device=device)
+                v_exps = torch.zeros(shape[:2], dtype=torch.int8, device=device)
         for t, n in ((k_storage, "k_storage"), (v_storage, "v_storage")):
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == tdtype and t.is_contiguous()):
                 raise TypeError(f"{n} must be a contiguous {tdtype} CUDA tensor")
             if tuple(t.shape) != shape:
                 raise ValueError(f"{n} must have shape {shape}")
-        self.k, self.v = k_storage, v_storage
+        if dtype == "int8":
+            for t, n in ((k_exps, "k_exps"), (v_exps, "v_exps")):
+                if not (isinstance(t, torch.Tensor) and t.dtype == torch.int8 and t.is_contiguous()):
+                    raise TypeError(f"{n} must be a contiguous int8 CUDA tensor")
+                if tuple(t.shape) != shape[:2] or t.device != k_storage.device:
+                    raise ValueError(f"{n} must have shape {shape[:2]} and be on the storage's device")
+        self.k, self.v, self.k_exps, self.v_exps = k_storage, v_storage, k_exps, v_exps
         self.num_blocks, self.num_kv_heads, self.head_dim, self.block_size = num_blocks, num_kv_heads, head_dim, block_size
-        self.dtype, self.elem_bytes = dtype, (1 if fp8 else 2)
+        self.dtype, self.elem_bytes = dtype, (2 if dtype == "bf16" else 1)
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
-        desc = pkv_pool_desc(num_blocks, block_size, num_kv_heads, head_dim,
-                             PKV_DTYPE_FP8_E4M3 if fp8 else PKV_DTYPE_BF16, self.k.data_ptr(), self.v.data_ptr(),
-                             self.k_scale, self.v_scale)
+        desc = pkv_pool_desc(num_blocks, block_size, num_kv_heads, head_dim, code, self.k.data_ptr(), self.v.data_ptr(),
+                             self.k_scale, self.v_scale, _ptr(k_exps), _ptr(v_exps))
         h = ctypes.c_void_p()
         with torch.cuda.device(self.k.device):
             _check(lib.pkv_pool_create(ctypes.byref(desc), ctypes.byref(h)))
@@ -426,7 +452,7 @@ def pkv_paged_attn_static(pool: Pool, q, q_positions, block_tables, ctx_lens, cu
 
 
 # ---------------------------------------------------------------------------------------------------------------------
-# Tree attention, block-selected attention and pages.  Their metadata is read on the device alone: no HostMeta, and the
+# Tree attention, block-selected attention, pages, the 8-bit cache and attention with modified scores.  Their metadata is read on the device alone: no HostMeta, and the
 # calls can be captured into a graph.  Tensors live on the pool's device; without `stream` a call runs on that device's
 # current stream.  Outputs and workspaces that are not given are allocated for that stream.  The workspace of calls on a
 # current stream is kept with the pool, one for each stream: calls on one stream follow one another.  A call that is
@@ -543,6 +569,17 @@ def pkv_copy_blocks(pool: Pool, src, dst, summary=None, stream=None):
 def pkv_compact(pool: Pool, block_tables, cu_keep, src_positions, dst_starts, stream=None):
     """Move the K/V rows at src_positions (ascending per request) to dst_starts[r], dst_starts[r] + 1, ..."""
     _ops(pool).compact(block_tables, cu_keep, src_positions, dst_starts, stream)
+
+
+def pkv_append_int8(pool: Pool, block_tables, cu_q_lens, positions, held_lens, k_new, v_new, stream=None):
+    """Quantise k_new / v_new [T, Hkv, D] (bf16) into an int8 pool.  held_lens [R]: the tokens each request holds before the
+    call; their codes follow a block's exponent when the new rows raise it."""
+    _ops(pool).append_int8(block_tables, cu_q_lens, positions, held_lens, k_new, v_new, stream)
+
+
+def pkv_read_rows(pool: Pool, block_tables, cu_lens, positions, k_out=None, v_out=None, stream=None):
+    """The K and V rows at `positions` of each request's cache: (k, v), [T, Hkv, D] bf16, from a pool of any dtype."""
+    return _ops(pool).read_rows(block_tables, cu_lens, positions, k_out, v_out, stream)
 
 
 def pkv_last_plan_stats(pool: Pool) -> dict:
