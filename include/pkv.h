@@ -493,6 +493,60 @@ int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int
                 const int32_t* src_positions, const int32_t* dst_starts, int num_kept, void* stream);
 
 /*
+ * ---- Attention with modified scores, over a pool of any type ----------------
+ *
+ * Query token t of request r at position p = q_positions[t] sees key j < ctx_lens[r] if
+ *   j < prefix_lens[r],  or
+ *   first_keys[t] <= j <= p  and  (window == 0 or j > p - window),
+ * and with head h, KV head g = h / (num_q_heads / num_kv_heads) and the keys S it sees
+ *   x_j = scale * q[t][h] . K_r[j][g];   x_j = softcap * tanh(x_j / softcap)  if softcap > 0;
+ *   x_j = x_j - slopes[h] * |p - j|      if there are slopes;   m = max_S x_j
+ *   O[t][h]   = sum_S exp(x_j - m) V_r[j][g] / sum_S exp(x_j - m)
+ *   LSE[t][h] = m + ln(sum_S exp(x_j - m));   O = 0 and LSE = -inf if S is empty.
+ * So first_keys holds where a token's document begins, prefix_lens the keys that
+ * all tokens of a request see whatever their positions (a prefix seen both ways,
+ * or the first few keys beside a window).  With no descriptor (NULL), or one of
+ * zeros, this is the causal attention of pkv_paged_attn, for callers whose
+ * lengths are on the device, and for int8 pools.
+ *   prefix_lens [num_reqs], first_keys [num_tokens], slopes [num_q_heads]: device
+ *   arrays, or NULL (0; 0; none).  0 <= prefix <= ctx <= max_blocks * 16; negative
+ *   first_keys count as 0.  Positions and first_keys of a request in any order.
+ * Scores are fp32 as for pkv_tree_attn (int8 pools: bf16 operands), tanh and the
+ * bias are taken in fp32; P is rounded to bf16 (f16 for FP8 pools), O once.  Results
+ * do not depend on timing.  Keys that a token does not see do not reach it, be
+ * their values infinite or NaN.  Blocks that no token of a request sees (before
+ * a window or a document, behind the last position) are not read.  A request of
+ * many tokens and others of few may share a call.
+ * Invalid block ids are flagged where they would be read and their keys seen by
+ * nobody; lengths out of range are flagged and cut; positions outside the table
+ * are flagged (below 0: the prefix is seen; beyond: all keys that the masks leave).
+ * num_tokens may exceed cu_q_lens[num_reqs]: rows that belong to no request are
+ * neither read nor written.
+ *
+ * All metadata but the descriptor itself is read on the device: the call can be
+ * captured into a graph and replayed with other lengths, tables and masks, and
+ * runs on `stream` alone (a pending ahead-of-time swap-in lands first).  q and o
+ * 16-byte aligned.  workspace: device memory of pkv_score_attn_workspace_size()
+ * bytes for the same sizes, 256-byte aligned, used by one call at a time as for
+ * pkv_tree_attn.  num_tokens == 0 is a no-op.
+ * Errors: PKV_EINVAL (softcap neither 0 nor in 2^-30 .. 2^30, window < 0, bad shapes, a
+ * workspace that is too small), PKV_EUNSUPPORTED, PKV_ECUDA.
+ */
+typedef struct {
+  float softcap;              /* 0: none */
+  int window;                 /* 0: none */
+  const float* slopes;        /* device, or NULL */
+  const int32_t* first_keys;  /* device, or NULL */
+  const int32_t* prefix_lens; /* device, or NULL */
+} pkv_score_desc;
+int pkv_score_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_blocks, int num_reqs, int num_tokens,
+                                  size_t* bytes);
+int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
+                   const int32_t* block_tables, int max_blocks, const int32_t* ctx_lens, const int32_t* cu_q_lens,
+                   int num_reqs, int num_tokens, const pkv_score_desc* score, float scale, void* o, float* lse,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * ---- An 8-bit cache with an exponent for each block: writing and reading ----
  *
  * pkv_append_int8 quantises the new rows into an int8 pool's blocks.  The rows

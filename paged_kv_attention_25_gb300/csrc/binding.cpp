@@ -461,6 +461,7 @@ PyMethodDef kMethods[] = {entry<tree_mask, 6>("tree_mask"),         entry<tree_a
                           entry<copy_blocks, 5>("copy_blocks"),     entry<compact, 5>("compact"),
                           entry<check_summary, 2>("check_summary"), entry<close, 0>("close"),
                           entry<append_int8, 7>("append_int8"),     entry<read_rows, 6>("read_rows"),
+                          entry<score_attn, 16>("score_attn"),
                           {nullptr, nullptr, 0, nullptr}};
 
 // Pool(handle, device, num_blocks, num_kv_heads, head_dim)

@@ -28,3 +28,26 @@ PyObject* read_rows(Pool* p, Args a) {
   Py_XDECREF(y);
   return r;
 }
+
+// q, q_positions, block_tables, ctx_lens, cu_q_lens, scale, softcap, window, slopes, first_keys, prefix_lens, out, lse,
+// workspace, stream, want_lse
+PyObject* score_attn(Pool* p, Args a) {
+  const Batch b(p, a[2], a[4], "cu_q_lens");
+  const Query q(p, a[0]);
+  const int32_t* pos = address<int32_t>(p, a[1], "q_positions", at::kInt, {q.tokens});
+  const int32_t* ctx = address<int32_t>(p, a[3], "ctx_lens", at::kInt, {b.reqs});
+  const float scale = number(a[5]);
+  pkv_score_desc d{number(a[6]), integer(a[7]), nullptr, nullptr, nullptr};
+  if (a[8] != Py_None) d.slopes = address<float>(p, a[8], "slopes", at::kFloat, {q.heads});
+  if (a[9] != Py_None) d.first_keys = address<int32_t>(p, a[9], "first_keys", at::kInt, {q.tokens});
+  if (a[10] != Py_None) d.prefix_lens = address<int32_t>(p, a[10], "prefix_lens", at::kInt, {b.reqs});
+  Call call(p, a[14]);
+  Output out(p, call, q, a[11], a[12], a[15] == Py_True);
+  size_t size = 0;
+  check(pkv_score_attn_workspace_size(p->handle, count(q.heads), count(b.width), count(b.reqs), count(q.tokens), &size));
+  const at::Tensor ws = call.workspace(a[13], size);
+  run(pkv_score_attn, p->handle, q.q, count(q.heads), pos, b.tables, count(b.width), ctx, b.cu, count(b.reqs),
+      count(q.tokens), static_cast<const pkv_score_desc*>(&d), scale, out.o, out.lse, ws.data_ptr(),
+      static_cast<size_t>(ws.numel()), call.stream());
+  return out.result();
+}

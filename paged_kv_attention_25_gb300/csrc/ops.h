@@ -115,6 +115,10 @@ int launch_copy_blocks(const PoolView& pool, void* kp, void* vp, const int32_t* 
                        int8_t* codes, int8_t* exps, void* stream);
 int launch_compact(const PoolView& pool, void* kp, void* vp, const int32_t* block_tables, int max_blocks, int num_reqs,
                    const int32_t* cu_keep, const int32_t* src, const int32_t* dst, int num_kept, void* stream);
+// pkv_score_attn: the form for few query rows, the form on tiles of 128.
+struct ScoreArgs;
+int launch_score_rows(const ScoreArgs& a, void* stream);
+
 // pkv_append_int8 (int8 pools), pkv_read_rows (any).
 int launch_append_int8(const PoolView& pool, void* kp, void* vp, const int32_t* bt, int max_blocks, int num_reqs,
                        const int32_t* cu, const int32_t* pos, const int32_t* held, const void* k_new, const void* v_new,

@@ -15,6 +15,7 @@
 #include "ops.h"
 #include "pool.h"
 #include "sched.cuh"
+#include "score.cuh"
 
 using namespace pkv;
 
@@ -441,6 +442,76 @@ int pkv_copy_blocks(pkv_pool* pool, const int32_t* src, const int32_t* dst, int 
     return launch_copy_blocks(pool->view(), pool->k, pool->v, src, dst, n, codes, exps, stream);
   });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "block copy launch");
+  return PKV_OK;
+}
+
+int pkv_score_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_blocks, int num_reqs, int num_tokens,
+                                  size_t* bytes) {
+  if (!pool || !bytes) return fail(PKV_EINVAL, "pool/bytes is NULL");
+  const int rc = check_heads(pool, num_q_heads);
+  if (rc) return rc;
+  if (num_reqs < 0 || num_tokens < 0 || max_blocks < 0) return fail(PKV_EINVAL, "negative size");
+  *bytes = tree_ws(pool, tree_form(false, pool->num_sms)).total;
+  return PKV_OK;
+}
+
+int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t* q_positions,
+                   const int32_t* block_tables, int max_blocks, const int32_t* ctx_lens, const int32_t* cu_q_lens,
+                   int num_reqs, int num_tokens, const pkv_score_desc* score, float scale, void* o, float* lse,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!pool) return fail(PKV_EINVAL, "pool is NULL");
+  int rc = check_tables(max_blocks, num_reqs, num_tokens);
+  if (rc) return rc;
+  const pkv_score_desc d = score ? *score : pkv_score_desc{};
+  // (So that scale / softcap times a product of q and K stays in fp32's range.)
+  if (!(d.softcap == 0.f || (d.softcap >= 0x1p-30f && d.softcap <= 0x1p30f)))
+    return fail(PKV_EINVAL, "softcap must be 0 or in 2^-30 .. 2^30");
+  if (d.window < 0) return fail(PKV_EINVAL, "window must be >= 0");
+  if (num_tokens == 0) return PKV_OK;
+  if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
+  if (!q || !q_positions || !block_tables || !ctx_lens || !cu_q_lens || !o) return fail(PKV_EINVAL, "NULL device pointer");
+  if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
+  if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
+  const TreeForm form = tree_form(false, pool->num_sms);
+  const TreeWs w = tree_ws(pool, form);
+  if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_score_attn_workspace_size()"))) return rc;
+  DeviceGuard guard(pool->device);
+  if ((rc = finish_swap_in(pool, stream))) return rc;
+  std::lock_guard<std::mutex> lk(pool->mu);
+  ScoreArgs s{};
+  s.t = tree_args(pool, form, w, workspace);
+  TreeArgs& a = s.t;
+  a.q = q;
+  a.num_q_heads = num_q_heads;
+  a.group = num_q_heads / pool->num_kv_heads;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = ctx_lens;
+  a.prefix_lens = d.prefix_lens;
+  a.cu_q_lens = cu_q_lens;
+  a.num_reqs = num_reqs;
+  a.num_tokens = num_tokens;
+  a.positions = q_positions;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = o;
+  a.lse = lse;
+  if (d.softcap > 0.f) {
+    s.cap_in = scale / d.softcap;
+    s.cap_out = d.softcap * 1.4426950408889634f;
+  }
+  s.slopes = d.slopes;
+  s.window = d.window;
+  s.first_keys = d.first_keys;
+  const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / 16 + num_reqs) * pool->num_kv_heads;
+  // (A window alone bounds what a single token reads, whatever the table's width.)
+  int blocks = max_blocks;
+  if (d.window > 0 && !d.prefix_lens) blocks = static_cast<int>(std::min<int64_t>(blocks, d.window / kBlockSize + 2));
+  fit_ctas(a, groups, blocks, pool->num_sms);
+  rc = timed_launch(pool, 1, stream, [&] { return launch_score_rows(s, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "score attention launch");
+  if (a.form.whole) return PKV_OK;
+  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
+  if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "score attention merge launch");
   return PKV_OK;
 }
 

@@ -1,0 +1,81 @@
+// What the two forms of the attention with modified scores (pkv_score_attn)
+// share: which keys a token sees, and what becomes of a score.
+//
+// Token t at position p of request r sees key j < ctx_r if
+//   j < prefix_r,  or  first_t <= j <= p and (window = 0 or j > p - window),
+// and its score is
+//   x = scale q . K_j,   x = cap tanh(x / cap) if cap > 0,   x -= slope_h |p - j| if there are slopes.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "int8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "sched.cuh"
+
+namespace pkv {
+
+constexpr int kPoolBf16 = 0, kPoolFp8 = 1, kPoolInt8 = 2;
+
+struct ScoreItem;
+
+// One call.  t.prefix_lens may be nullptr; t.positions holds the queries' positions; t.mask, t.sel are not used.
+struct ScoreArgs {
+  TreeArgs t;
+  float cap_in, cap_out;      // scale / cap, cap * log2 e (0: no cap)
+  const float* slopes;        // [num_q_heads], or nullptr
+  int window;                 // 0: none
+  const int32_t* first_keys;  // [num_tokens], or nullptr
+  ScoreItem* items;           // tiles form: its plan (workspace)
+  int max_items;
+};
+
+// The keys behind the prefix that a token sees: [lo, hi] (hi < lo: none).
+struct KeySpan {
+  int lo, hi;
+};
+__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int ctx) {
+  const int p = max(__ldg(a.t.positions + t), -1);
+  KeySpan s{a.first_keys ? max(__ldg(a.first_keys + t), 0) : 0, min(p, ctx - 1)};
+  if (a.window > 0) s.lo = max(s.lo, p - a.window + 1);
+  return s;
+}
+// Keys [key0, key0 + 32) that a token sees, as bits.
+__device__ __forceinline__ uint32_t span_bits(int prefix, KeySpan s, int key0) {
+  return low_bits(prefix - key0) | (low_bits(s.hi + 1 - key0) & ~low_bits(s.lo - key0));
+}
+
+// A request's lengths, made safe.
+struct ScoreReq {
+  int t0, n, ctx, prefix;
+  bool bad;
+};
+__device__ __forceinline__ ScoreReq score_req(const ScoreArgs& a, int r) {
+  ScoreReq q;
+  const int c0 = __ldg(a.t.cu_q_lens + r), c1 = __ldg(a.t.cu_q_lens + r + 1);
+  const int ctx = __ldg(a.t.ctx_lens + r), pre = a.t.prefix_lens ? __ldg(a.t.prefix_lens + r) : 0;
+  q.t0 = min(max(c0, 0), a.t.num_tokens);
+  q.n = min(max(c1, q.t0), a.t.num_tokens) - q.t0;
+  q.ctx = min(max(ctx, 0), a.t.max_blocks * kBlockSize);
+  q.prefix = min(max(pre, 0), q.ctx);
+  q.bad = c0 < 0 || c1 < c0 || c1 > a.t.num_tokens || q.ctx != ctx || q.prefix != pre;
+  return q;
+}
+
+// tanh(y), off by 2^-23 of it for |y| < 1/2 and by about 2^-22 above.  Below 1/2
+// an odd polynomial of degree 9, interpolated at Chebyshev nodes of y^2 in [0, 1/4];
+// above, (1 - e) / (1 + e) with e = exp(-2 |y|).
+__device__ __forceinline__ float tanh_small(float y) {
+  const float z = y * y;
+  float r = fmaf(z, 0.017131345f, -0.052984238f);
+  r = fmaf(r, z, 0.13324751f);
+  r = fmaf(r, z, -0.33333068f);
+  r = fmaf(r, z, 0.99999999f);
+  return r * y;
+}
+__device__ __forceinline__ float tanh_large(float y) {
+  const float e = fast_exp2(fabsf(y) * -2.8853900817779268f);
+  return copysignf(__fdividef(1.f - e, 1.f + e), y);
+}
+
+}  // namespace pkv

@@ -58,6 +58,7 @@ EXPORTED = (
     "pkv_select_blocks",
     "pkv_sparse_attn_workspace_size", "pkv_sparse_attn", "pkv_fork_workspace_size", "pkv_fork", "pkv_copy_blocks", "pkv_compact",
     "pkv_pool_exps", "pkv_append_int8", "pkv_read_rows",
+    "pkv_score_attn_workspace_size", "pkv_score_attn",
 )
 
 
@@ -81,6 +82,11 @@ class pkv_pool_desc(ctypes.Structure):
 
 class pkv_host_meta(ctypes.Structure):
     _fields_ = [("cu_q_lens", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("q_positions", ctypes.c_void_p)]
+
+
+class pkv_score_desc(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int), ("slopes", ctypes.c_void_p),
+                ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
 class pkv_plan_stats(ctypes.Structure):
@@ -165,6 +171,8 @@ def load_library():
             "pkv_fork": [P, P, I, I, P, P, P, P, I, P, P, P, P, P, P, ctypes.c_size_t, P],
             "pkv_copy_blocks": [P, P, P, I, P, P, P],
             "pkv_compact": [P, P, I, I, P, P, P, I, P],
+            "pkv_score_attn_workspace_size": [P, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "pkv_score_attn": [P, P, I, P, P, I, P, P, I, I, ctypes.POINTER(pkv_score_desc), F, P, P, P, ctypes.c_size_t, P],
             "pkv_pool_exps": [P, ctypes.POINTER(P), ctypes.POINTER(P)],
             "pkv_append_int8": [P, P, I, I, P, P, P, P, P, I, P],
             "pkv_read_rows": [P, P, I, I, P, P, I, P, P, P],
@@ -569,6 +577,24 @@ def pkv_copy_blocks(pool: Pool, src, dst, summary=None, stream=None):
 def pkv_compact(pool: Pool, block_tables, cu_keep, src_positions, dst_starts, stream=None):
     """Move the K/V rows at src_positions (ascending per request) to dst_starts[r], dst_starts[r] + 1, ..."""
     _ops(pool).compact(block_tables, cu_keep, src_positions, dst_starts, stream)
+
+
+def pkv_score_attn_workspace_size(pool: Pool, num_q_heads: int, max_blocks: int, num_reqs: int, num_tokens: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().pkv_score_attn_workspace_size(pool.handle, num_q_heads, max_blocks, num_reqs, num_tokens,
+                                                        ctypes.byref(n)))
+    return n.value
+
+
+def pkv_score_attn(pool: Pool, q, q_positions, block_tables, ctx_lens, cu_q_lens, scale: float, softcap: float = 0.0,
+                   window: int = 0, slopes=None, first_keys=None, prefix_lens=None, out=None, lse=None, workspace=None,
+                   stream=None, want_lse=True):
+    """Attention over a pool of any dtype.  Each token sees the keys j < prefix_lens[r] and those with
+    first_keys[t] <= j <= position (window > 0: and j > position - window); scores are scale * q . k, capped to
+    softcap * tanh(score / softcap), less slopes[h] * |position - j| (slopes [Hq] fp32).  Returns (O [T, Hq, D] bf16,
+    LSE [T, Hq] fp32 or None)."""
+    return _ops(pool).score_attn(q, q_positions, block_tables, ctx_lens, cu_q_lens, scale, softcap, window, slopes,
+                                 first_keys, prefix_lens, out, lse, workspace, stream, bool(want_lse))
 
 
 def pkv_append_int8(pool: Pool, block_tables, cu_q_lens, positions, held_lens, k_new, v_new, stream=None):

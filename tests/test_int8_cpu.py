@@ -36,7 +36,7 @@ def test_binding_calls_let_go_of_the_interpreter():
     csrc = os.path.join(os.path.dirname(pkv.__file__), "csrc")
     with open(os.path.join(csrc, "binding_score.h")) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
-    names = {"append_int8", "read_rows"}
+    names = {"append_int8", "read_rows", "score_attn"}
     assert set(re.findall(r"run\(pkv_(\w+), p->handle", text)) == names
     assert not names & set(re.findall(r"pkv_(\w+)\(", text))
 
