@@ -717,13 +717,13 @@ int pkv_check_device_errors(pkv_pool* pool, void* stream, unsigned* flags);
  *     (tensor-core) kernel never issues its first K copy, so that the wait for
  *     it runs out: the kernel records PKV_DEVERR_TIMEOUT, drains its copies,
  *     frees what it holds and returns, and that call's outputs are undefined;
- *     0 = off (default).  2 acts on the tiles form of pkv_tree_attn in the same
+ *     0 = off (default).  2 acts on the tiles form of pkv_tree_attn and pkv_score_attn in the same
  *     way (its rows form, pkv_sparse_attn and the calls below wait on no barrier);
  *   PKV_DEBUG_FUSED_FORM: how pkv_append_paged_attn appends: 0 = chosen per
  *     batch (default), 1 = inside the attention launches whenever the pool
  *     allows it, 2 = the append kernel first.  Every form gives the same pool
  *     and the same O and LSE bits.
- *   PKV_DEBUG_TREE_FORM: which kernel pkv_tree_attn takes: 0 = chosen per batch
+ *   PKV_DEBUG_TREE_FORM: which kernel pkv_tree_attn and pkv_score_attn take: 0 = chosen per batch
  *     (default), 1 = warp-level MMA on 16 query rows, 2 = tcgen05 on tiles of
  *     128; set it before asking for the workspace size.
  * Errors: PKV_EINVAL for an unknown setting or a value out of range. */

@@ -118,6 +118,8 @@ int launch_compact(const PoolView& pool, void* kp, void* vp, const int32_t* bloc
 // pkv_score_attn: the form for few query rows, the form on tiles of 128.
 struct ScoreArgs;
 int launch_score_rows(const ScoreArgs& a, void* stream);
+template <int D>
+int launch_score_tc(const ScoreArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream);
 
 // pkv_append_int8 (int8 pools), pkv_read_rows (any).
 int launch_append_int8(const PoolView& pool, void* kp, void* vp, const int32_t* bt, int max_blocks, int num_reqs,

@@ -154,6 +154,25 @@ bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_to
   return rows > most * num_reqs && work > 16ll * 3 * pool->num_sms;
 }
 
+// The plan of pkv_score_attn's tiles form, behind the workspace of the form itself.
+struct ScoreWs {
+  TreeWs tree;
+  size_t items, cum, first, total;
+  int most;
+};
+ScoreWs score_ws(const pkv_pool* pool, const TreeForm& f, int num_q_heads, int num_reqs, int num_tokens) {
+  ScoreWs w{tree_ws(pool, f), 0, 0, 0, 0, 0};
+  w.total = w.tree.total;
+  if (!f.tensor) return w;
+  const int pair = 2 * (kTcRows / (num_q_heads / pool->num_kv_heads));   // tokens
+  w.most = num_tokens / pair + num_reqs;
+  w.items = w.tree.total;
+  w.cum = w.items + align256(static_cast<size_t>(w.most) * sizeof(ScoreItem));
+  w.first = w.cum + align256((static_cast<size_t>(w.most) + 2) * sizeof(int64_t));
+  w.total = w.first + align256(static_cast<size_t>(num_reqs) * sizeof(int));
+  return w;
+}
+
 size_t select_ws(const pkv_pool* pool, int max_blocks, int num_tokens) {
   return align256(static_cast<size_t>(select_part(num_tokens, max_blocks, pool->num_kv_heads)) * max_blocks *
                   pool->num_kv_heads * sizeof(uint32_t));
@@ -451,7 +470,8 @@ int pkv_score_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_block
   const int rc = check_heads(pool, num_q_heads);
   if (rc) return rc;
   if (num_reqs < 0 || num_tokens < 0 || max_blocks < 0) return fail(PKV_EINVAL, "negative size");
-  *bytes = tree_ws(pool, tree_form(false, pool->num_sms)).total;
+  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
+  *bytes = score_ws(pool, form, num_q_heads, num_reqs, num_tokens).total;
   return PKV_OK;
 }
 
@@ -472,14 +492,14 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   if (!q || !q_positions || !block_tables || !ctx_lens || !cu_q_lens || !o) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
-  const TreeForm form = tree_form(false, pool->num_sms);
-  const TreeWs w = tree_ws(pool, form);
+  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
+  const ScoreWs w = score_ws(pool, form, num_q_heads, num_reqs, num_tokens);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_score_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
   if ((rc = finish_swap_in(pool, stream))) return rc;
   std::lock_guard<std::mutex> lk(pool->mu);
   ScoreArgs s{};
-  s.t = tree_args(pool, form, w, workspace);
+  s.t = tree_args(pool, form, w.tree, workspace);
   TreeArgs& a = s.t;
   a.q = q;
   a.num_q_heads = num_q_heads;
@@ -492,22 +512,47 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   a.num_reqs = num_reqs;
   a.num_tokens = num_tokens;
   a.positions = q_positions;
-  a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o;
   a.lse = lse;
+  s.base = scale * (pool->k_exps || pool->elem_bytes == 2 ? 1.f : pool->k_scale);
   if (d.softcap > 0.f) {
-    s.cap_in = scale / d.softcap;
+    s.base /= d.softcap;
     s.cap_out = d.softcap * 1.4426950408889634f;
+    // cap_out tanh(base x) = x Q(x^2); where the powers of base leave fp32's range nothing counts as small.
+    if (s.base >= 0x1p-15f && s.base <= 0x1p15f) {
+      s.cap_small = 0.5f / s.base;
+      const double c[5] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4};
+      double f = static_cast<double>(s.base) * s.cap_out;
+      for (int i = 0; i < 5; ++i, f *= static_cast<double>(s.base) * s.base) s.cap_q[i] = static_cast<float>(c[i] * f);
+    }
+  } else {
+    s.base *= 1.4426950408889634f;
   }
   s.slopes = d.slopes;
   s.window = d.window;
   s.first_keys = d.first_keys;
-  const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / 16 + num_reqs) * pool->num_kv_heads;
+  a.tile_tokens = kTcRows / a.group;
+  const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / (form.tensor ? kTcRows : 16) + num_reqs) *
+                         pool->num_kv_heads;
   // (A window alone bounds what a single token reads, whatever the table's width.)
   int blocks = max_blocks;
-  if (d.window > 0 && !d.prefix_lens) blocks = static_cast<int>(std::min<int64_t>(blocks, d.window / kBlockSize + 2));
-  fit_ctas(a, groups, blocks, pool->num_sms);
-  rc = timed_launch(pool, 1, stream, [&] { return launch_score_rows(s, stream); });
+  if (!form.tensor && d.window > 0 && !d.prefix_lens)
+    blocks = static_cast<int>(std::min<int64_t>(blocks, d.window / kBlockSize + 2));
+  fit_ctas(a, groups, form.tensor ? blocks / 8 + 1 : blocks, pool->num_sms);
+  a.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  if (form.tensor) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    s.plan = ScorePlan{reinterpret_cast<ScoreItem*>(ws + w.items), reinterpret_cast<int64_t*>(ws + w.cum),
+                       reinterpret_cast<int*>(ws + w.first), w.most};
+    CUtensorMap tmap_q;
+    if ((rc = make_q_tmap(&tmap_q, q, num_tokens, num_q_heads, pool->head_dim, a.group, &a.q_box_tokens))) return rc;
+    rc = timed_launch(pool, 2, stream, [&] {
+      return pool->head_dim == 128 ? launch_score_tc<128>(s, &pool->tmap_k, &pool->tmap_v, &tmap_q, stream)
+                                   : launch_score_tc<64>(s, &pool->tmap_k, &pool->tmap_v, &tmap_q, stream);
+    });
+  } else {
+    rc = timed_launch(pool, 1, stream, [&] { return launch_score_rows(s, stream); });
+  }
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "score attention launch");
   if (a.form.whole) return PKV_OK;
   rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });

@@ -459,9 +459,7 @@ score_rows_kernel(const ScoreArgs a) {
   const int worker = solo ? warp_id : static_cast<int>(blockIdx.x);
   const int wi = solo ? 0 : warp, wn = solo ? 1 : W;   // this warp's place among those of the segment
   const uint32_t my_ring = smem_u32(ring) + warp * S::kStages * S::kStage;
-  // Raw products to log2 units, or to the cap's argument.
   const bool cap = a.cap_out != 0.f;
-  const float base = (cap ? a.cap_in : t.scale_log2) * (KIND == kPoolFp8 ? t.pool.k_scale : 1.f);
   int req = sh.req;
   RowsReq rq = rows_req_warp(a, req, lane);
   if (all_whole) sh.off *= rq.blocks + kGroupUnits;
@@ -560,7 +558,7 @@ score_rows_kernel(const ScoreArgs a) {
     for (int j = 0; j < S::kStages; ++j) copy(j);
     rt.begin();
     auto factor = [&](int i) {
-      BlockFactor f{base, 1.f};
+      BlockFactor f{a.base, 1.f};
       if constexpr (KIND == kPoolInt8) {
         const int e = __shfl_sync(0xffffffffu, exps_cur, i & 31);
         f.score *= exp_f32(static_cast<int16_t>(e & 0xffff));

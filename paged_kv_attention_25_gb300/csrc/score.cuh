@@ -17,17 +17,33 @@ namespace pkv {
 
 constexpr int kPoolBf16 = 0, kPoolFp8 = 1, kPoolInt8 = 2;
 
-struct ScoreItem;
+// Two neighbouring query tiles of a request (rows1 = 0: one), of the tiles form's
+// plan: key tiles 0 .. ktiles - 1, of which those below pre_tiles hold the prefix
+// and the others lie `gap` tiles further on; every row sees the keys [all_lo, all_hi].
+struct alignas(16) ScoreItem {
+  int req, tok0, rows0, rows1;
+  int pre_tiles, gap, ktiles, prefix;
+  int ctx, all_lo, all_hi, pad;
+};
+static_assert(sizeof(ScoreItem) == 48, "ScoreItem layout: three 16-byte loads");
+// The plan in the workspace, for `most` items at most.
+struct ScorePlan {
+  ScoreItem* items;   // [most]
+  int64_t* cum;       // [most + 2]: units of a head's line before each item; total; number of items
+  int* first;         // [num_reqs]: items before each request's
+  int most;
+};
 
 // One call.  t.prefix_lens may be nullptr; t.positions holds the queries' positions; t.mask, t.sel are not used.
 struct ScoreArgs {
   TreeArgs t;
-  float cap_in, cap_out;      // scale / cap, cap * log2 e (0: no cap)
+  float base;                 // raw products to log2 units, or to the cap's argument (FP8: with k_scale)
+  float cap_out;              // cap * log2 e (0: no cap)
+  float cap_small, cap_q[5];  // products below cap_small: x Q(x^2) is the capped score in log2 units
   const float* slopes;        // [num_q_heads], or nullptr
   int window;                 // 0: none
   const int32_t* first_keys;  // [num_tokens], or nullptr
-  ScoreItem* items;           // tiles form: its plan (workspace)
-  int max_items;
+  ScorePlan plan;             // tiles form
 };
 
 // The keys behind the prefix that a token sees: [lo, hi] (hi < lo: none).
@@ -38,6 +54,7 @@ __device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int ctx) 
   const int p = max(__ldg(a.t.positions + t), -1);
   KeySpan s{a.first_keys ? max(__ldg(a.first_keys + t), 0) : 0, min(p, ctx - 1)};
   if (a.window > 0) s.lo = max(s.lo, p - a.window + 1);
+  s.lo = min(s.lo, ctx);
   return s;
 }
 // Keys [key0, key0 + 32) that a token sees, as bits.
@@ -65,12 +82,14 @@ __device__ __forceinline__ ScoreReq score_req(const ScoreArgs& a, int r) {
 // tanh(y), off by 2^-23 of it for |y| < 1/2 and by about 2^-22 above.  Below 1/2
 // an odd polynomial of degree 9, interpolated at Chebyshev nodes of y^2 in [0, 1/4];
 // above, (1 - e) / (1 + e) with e = exp(-2 |y|).
+constexpr float kTanh0 = 0.99999999f, kTanh1 = -0.33333068f, kTanh2 = 0.13324751f, kTanh3 = -0.052984238f,
+                kTanh4 = 0.017131345f;
 __device__ __forceinline__ float tanh_small(float y) {
   const float z = y * y;
-  float r = fmaf(z, 0.017131345f, -0.052984238f);
-  r = fmaf(r, z, 0.13324751f);
-  r = fmaf(r, z, -0.33333068f);
-  r = fmaf(r, z, 0.99999999f);
+  float r = fmaf(z, kTanh4, kTanh3);
+  r = fmaf(r, z, kTanh2);
+  r = fmaf(r, z, kTanh1);
+  r = fmaf(r, z, kTanh0);
   return r * y;
 }
 __device__ __forceinline__ float tanh_large(float y) {

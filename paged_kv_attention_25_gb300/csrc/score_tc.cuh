@@ -1,0 +1,1183 @@
+// Attention with modified scores and masks (pkv_score_attn), the form on the
+// tcgen05 tensor cores for batches that bring many query rows per KV head.
+//
+// The warp roles are those of the tree attention on tiles (K and V producers that
+// gather blocks by TMA, one MMA issuer, two softmax warpgroups A and B, scores, P
+// and O in TMEM, a scheduler that hands out segments ahead of their use).  What
+// differs is the work: a tile of 128 query rows sees keys from the first that its
+// window or document leaves up to its last position, so that tiles of one request
+// differ in length.  A plan kernel of one CTA lists them first:
+//   item    two neighbouring tiles of a request (A and B share every K/V tile), or
+//           its odd last one (A takes the even key tiles, B the odd ones, and A
+//           joins B's state at the end); the key tiles that hold the prefix, then
+//           those from the first key that any row sees to the last;
+//   line    the items of one KV head after another's, a key tile of a pair three
+//           units, of a single tile two, and kGroupUnits for start and epilogue.
+// A CTA takes an equal share of the line; a group that several share is merged by
+// log-sum-exp.
+//
+// Masks: in key tiles that some row does not see whole each row's thread forms its
+// 128 visibility bits from its span of keys.  The V producer reads those tiles once
+// in shared memory and clears elements that are not finite (a masked key must not
+// reach a row as 0 * inf) and the rows past the context; rows that do see such an
+// element get it added after their result is stored.  Int8 values are finite.
+//
+// Scores: tanh on the FMA pipe, as x Q(x^2) with the polynomial of tanh_small and
+// the scales in its coefficients, five paired operations for two scores, while
+// every |x| of the warp's rows stays below half the cap; tanh_large otherwise.
+//
+// Int8 pools: the producers widen a stage's codes to bf16 times the block's power
+// of two, exactly; the MMAs are those of bf16 pools.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <climits>
+
+#include "internal.h"
+#include "ops.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+#include "sched.cuh"
+#include "score.cuh"
+#include "tc.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kBlkPerTile = kNK / kBlockSize;   // 8
+constexpr int kSegSlots = 4;                    // segments handed out ahead
+constexpr int kSegRing = 8;                     // V producer's reports (it is at most kSegSlots + 1 ahead)
+constexpr int kSegReaders = 11;                 // warps that read a segment
+constexpr int kPairUnits = 3, kSingleUnits = 2, kGroupUnits = 6;
+using TcShare = Share<kPairUnits + kGroupUnits>;
+
+template <int KS, int VS>
+struct ScoreBars {
+  static constexpr int kKFull = 0, kKEmpty = KS, kKLanded = 2 * KS;
+  static constexpr int kVFull = 3 * KS, kVEmpty = 3 * KS + VS, kVLanded = 3 * KS + 2 * VS;
+  static constexpr int kT = 3 * KS + 3 * VS;
+  static constexpr int kS = kT;             // + group: S of its next key tile in TMEM
+  static constexpr int kP = kT + 2;         // + group: P written, O rescaled (128 arrivals)
+  static constexpr int kPv = kT + 4;        // + group: its last PV of the segment done
+  static constexpr int kQFull = kT + 6;     // + tile
+  static constexpr int kQEmpty = kT + 8;    // + tile
+  static constexpr int kQc = kT + 10;       // + tile: FP8: Q rows converted to f16 (128 arrivals)
+  static constexpr int kMl = kT + 12;       // single: B's state is final (128 arrivals)
+  static constexpr int kJoined = kT + 13;   // single: A has read it (128 arrivals)
+  static constexpr int kDrain = kT + 14;
+  static constexpr int kVDone = kT + 15;    // + segment % kSegRing: its V tiles are all handed over
+  static constexpr int kSegFull = kT + 15 + kSegRing;               // + segment % kSegSlots: published
+  static constexpr int kSegEmpty = kSegFull + kSegSlots;            // + segment % kSegSlots: read by every role
+  static constexpr int kCount = kSegEmpty + kSegSlots;
+};
+
+// What one CTA does with one group: key tiles [kt0, kt1) of an item, numbered from
+// 0: those below pre_tiles lie at their number, the others `gap` further on.
+struct alignas(16) Seg {
+  int req, g, prefix, ctx;
+  int tok0, tok1, rows0, rows1;   // query tiles (rows1 = 0: single)
+  int kt0, kt1, slot, flags;
+  int pre_tiles, gap, all_lo, all_hi;   // every row sees the keys [all_lo, all_hi]
+};
+static_assert(sizeof(Seg) == 64, "Seg layout: four 16-byte loads");
+constexpr int kSegSingle = 1, kSegWhole = 2, kSegMissing = 4, kSegEnd = 8;
+
+template <int D>
+struct ScoreSmem {
+  using S = TcSmem<D>;
+  using B = ScoreBars<S::kKSt, S::kVSt>;
+  static constexpr int kOffBar = S::kOffBar;
+  static constexpr int kOffMl = kOffBar + ((B::kCount * 8 + 15) / 16) * 16;   // float2 [128]: B's m, l
+  static constexpr int kOffSeg = kOffMl + kTcRows * 8;
+  static constexpr int kOffMisc = kOffSeg + kSegSlots * static_cast<int>(sizeof(Seg));
+  static constexpr int kTotal = kOffMisc + 64;
+};
+static_assert(ScoreSmem<128>::kTotal <= 232448, "shared memory of the D = 128 kernel");
+
+// Key tile j of a segment's (or an item's) numbering, as a tile of the context.
+__device__ __forceinline__ int tile_at(int j, int pre_tiles, int gap) { return j < pre_tiles ? j : j + gap; }
+
+// Whether every row of the segment sees the whole key tile that begins at key0.
+__device__ __forceinline__ bool seen_whole(const Seg& s, int key0) {
+  return key0 + kNK <= s.prefix || (key0 >= s.all_lo && key0 + kNK - 1 <= s.all_hi);
+}
+
+// Walks a CTA's share of the line.  Key tile k of a group that begins at unit 0
+// belongs to the worker that holds unit k * cost; the group's fixed units follow
+// its last tile.
+struct Walk {
+  int64_t U, total, u, end;   // all heads' units, one head's, the share
+  int workers, n_items, g, idx;
+  bool fresh;                 // `it` is not item idx yet
+  ScoreItem it;
+  int64_t at;                 // units of the head's line before it
+  int glen;
+
+  // Every thread; false: the CTA has no share.
+  __device__ __forceinline__ bool begin(const ScoreArgs& a) {
+    total = __ldcg(a.plan.cum + a.plan.most);
+    n_items = static_cast<int>(__ldcg(a.plan.cum + a.plan.most + 1));
+    U = total * a.t.pool.num_kv_heads;
+    workers = TcShare::workers(U, a.t.ctas);
+    if (U == 0 || static_cast<int>(blockIdx.x) >= workers) return false;
+    u = TcShare::begin(U, workers, blockIdx.x);
+    end = TcShare::begin(U, workers, blockIdx.x + 1);
+    return true;
+  }
+  // The warp that walks: the item that holds the share's first unit.
+  __device__ __forceinline__ void find(const ScoreArgs& a, int lane) {
+    g = static_cast<int>(u / total);
+    const int64_t rem = u - g * total;
+    int lo = 0, n = n_items;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && __ldcg(a.plan.cum + lo + min(lane * step, n - 1)) <= rem);
+      const int k = max(0, __popc(le) - 1);
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+    idx = lo;
+    fresh = true;
+  }
+  // The next segment with key tiles.  cut: the record of a group that this CTA begins and others go on with.
+  __device__ __forceinline__ bool next(const ScoreArgs& a, Seg& s, TreeCut& cut) {
+    for (;;) {
+      if (u >= end) return false;
+      if (fresh) {
+        const int4* p = reinterpret_cast<const int4*>(a.plan.items + idx);
+        const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
+        it = ScoreItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+        at = __ldcg(a.plan.cum + idx);
+        fresh = false;
+      }
+      const bool single = it.rows1 == 0;
+      const int cost = single ? kSingleUnits : kPairUnits;
+      glen = cost * it.ktiles + kGroupUnits;
+      const int x = static_cast<int>(u - g * total - at);
+      const int len = static_cast<int>(min(static_cast<int64_t>(glen - x), end - u));
+      const int kt = it.ktiles, kt0 = min(kt, (x + cost - 1) / cost), kt1 = min(kt, (x + len + cost - 1) / cost);
+      const int64_t gbegin = u - x;
+      s.g = g;
+      u += len;
+      if (x + len == glen) {
+        if (++idx == n_items) {
+          idx = 0;
+          ++g;
+        }
+        fresh = true;
+      }
+      if (kt0 >= kt1) continue;   // the group's fixed units only
+      s.req = it.req;
+      s.prefix = it.prefix;
+      s.ctx = it.ctx;
+      s.tok0 = it.tok0;
+      s.tok1 = it.tok0 + a.t.tile_tokens;
+      s.rows0 = it.rows0;
+      s.rows1 = it.rows1;
+      s.kt0 = kt0;
+      s.kt1 = kt1;
+      s.slot = static_cast<int>(blockIdx.x) * 4 + (kt0 == 0 ? 1 : 0);
+      s.flags = (single ? kSegSingle : 0) | (kt0 == 0 && kt1 == kt ? kSegWhole : 0);
+      s.pre_tiles = it.pre_tiles;
+      s.gap = it.gap;
+      s.all_lo = it.all_lo;
+      s.all_hi = it.all_hi;
+      cut.count = 0;
+      if (kt0 == 0 && kt1 < kt) {
+        // The last tile's first unit names the last worker; the workers between each have a tile (a share is
+        // longer than a tile).
+        cut.count = TcShare::owner(U, workers, gbegin + static_cast<int64_t>(kt - 1) * cost) - static_cast<int>(blockIdx.x) + 1;
+        cut.first = s.slot;
+        cut.next = (static_cast<int>(blockIdx.x) + 1) * 4;
+        cut.stride = 4;
+        cut.tok_a = s.tok0;
+        cut.rows_a = s.rows0;
+        cut.tok_b = s.tok1;
+        cut.rows_b = s.rows1;
+        cut.f0 = 0;
+        cut.g = s.g;
+      }
+      return true;
+    }
+  }
+};
+
+// The plan: items and their units before them, by one CTA (a warp an item, whose
+// tokens' spans it reads; their number and total at the end of `cum`).
+constexpr int kPlanThreads = 1024;
+__device__ __forceinline__ int pairs_of(const ScoreReq& q, int tile_tokens) {
+  return (q.n + 2 * tile_tokens - 1) / (2 * tile_tokens);
+}
+// Exclusive scan of x over the block's threads; `carry` is added and becomes the total.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T& carry, T* scratch) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T inc = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  T w = scratch[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += y;
+  }
+  const T all = __shfl_sync(0xffffffffu, w, 31), before = warp ? __shfl_sync(0xffffffffu, w, (warp - 1) & 31) : T(0);
+  __syncthreads();
+  const T r = carry + before + inc - x;
+  carry += all;
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArgs a) {
+  __shared__ int64_t scratch[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tt = a.t.tile_tokens, R = a.t.num_reqs;
+  griddep_wait();
+  griddep_launch();
+  int* const first = a.plan.first;   // items before each request's
+  int n_items = 0;
+  for (int base = 0; base < R; base += kPlanThreads) {
+    int n = 0;
+    if (base + tid < R) {
+      const ScoreReq q = score_req(a, base + tid);
+      n = pairs_of(q, tt);
+      if (q.bad) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
+    }
+    const int f = block_scan(n, n_items, reinterpret_cast<int*>(scratch));
+    if (base + tid < R) first[base + tid] = f;
+  }
+  __syncthreads();
+  n_items = min(n_items, a.plan.most);   // (ranges that overlap could make more)
+  for (int i = warp; i < n_items; i += kPlanThreads / 32) {
+    int lo = 0, n = R;   // the last request with first <= i (those without items share their successor's)
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && first[lo + min(lane * step, n - 1)] <= i);
+      const int k = max(0, __popc(le) - 1);
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+    const ScoreReq q = score_req(a, lo);
+    const int t0 = q.t0 + (i - first[lo]) * 2 * tt, nt = min(2 * tt, q.t0 + q.n - t0);
+    int any_lo = INT_MAX, all_lo = 0, any_hi = -1, all_hi = INT_MAX;
+    bool bad = false;
+    for (int t = t0 + lane; t < t0 + nt; t += 32) {
+      const KeySpan s = key_span(a, t, q.ctx);
+      any_lo = min(any_lo, s.lo);
+      all_lo = max(all_lo, s.lo);
+      any_hi = max(any_hi, s.hi);
+      all_hi = min(all_hi, s.hi);
+      const int p = __ldg(a.t.positions + t);
+      bad |= p < 0 || p >= a.t.max_blocks * kBlockSize;
+    }
+    any_lo = __reduce_min_sync(0xffffffffu, any_lo);
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    any_hi = __reduce_max_sync(0xffffffffu, any_hi);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
+    if (lane == 0) {
+      ScoreItem it;
+      it.req = lo;
+      it.tok0 = t0;
+      it.rows0 = min(tt, nt) * a.t.group;
+      it.rows1 = max(0, nt - tt) * a.t.group;
+      it.pre_tiles = (q.prefix + kNK - 1) / kNK;
+      const int k0 = max(it.pre_tiles, any_lo / kNK);
+      it.gap = k0 - it.pre_tiles;
+      it.ktiles = max(1, it.pre_tiles + max(0, (any_hi + kNK) / kNK - k0));   // (one at least: its rows are written too)
+      it.prefix = q.prefix;
+      it.ctx = q.ctx;
+      it.all_lo = all_lo;
+      it.all_hi = all_hi;
+      it.pad = 0;
+      a.plan.items[i] = it;
+      a.plan.cum[i] = (it.rows1 ? kPairUnits : kSingleUnits) * it.ktiles + kGroupUnits;
+    }
+  }
+  __syncthreads();
+  int64_t total = 0;
+  for (int base = 0; base < n_items; base += kPlanThreads) {
+    const int64_t x = base + tid < n_items ? a.plan.cum[base + tid] : 0;
+    const int64_t c = block_scan(x, total, scratch);
+    if (base + tid < n_items) a.plan.cum[base + tid] = c;
+  }
+  if (tid == 0) {
+    a.plan.cum[a.plan.most] = total;
+    a.plan.cum[a.plan.most + 1] = n_items;
+  }
+}
+
+// V elements that are not finite, added to the stored result of a row that
+// sees them (they were left out of the products).
+template <int D, bool F8>
+__device__ __noinline__ void add_odd(const ScoreArgs& sa, const Seg& s, KeySpan span, uint16_t* o, float* part) {
+  const TreeArgs& a = sa.t;
+  const int64_t Hkv = a.pool.num_kv_heads;
+  const int32_t* bt = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
+  const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
+  for (int j = s.kt0; j < s.kt1; ++j) {
+    const int tile = tile_at(j, s.pre_tiles, s.gap);
+    // (A tile that lacks a block was cleaned too, but its rows are all looked at then: see below.)
+    const bool whole = seen_whole(s, tile * kNK);
+    if (whole && !(s.flags & kSegMissing)) continue;
+    bool lacks = false;
+    if (whole) {
+      for (int b = tile * kBlkPerTile; b < min(nblk, (tile + 1) * kBlkPerTile); ++b) {
+        const int pb = __ldg(bt + b);
+        lacks |= pb < 0 || pb >= a.pool.num_blocks;
+      }
+      if (!lacks) continue;
+    }
+    for (int b = tile * kBlkPerTile; b < min(nblk, (tile + 1) * kBlkPerTile); ++b) {
+      const int pb = __ldg(bt + b);
+      if (pb < 0 || pb >= a.pool.num_blocks) continue;
+      const uint32_t vis = span_bits(s.prefix, span, b * kBlockSize);
+      for (int k = 0; k < kBlockSize; ++k) {
+        if (!((vis >> k) & 1u)) continue;
+        for (int d = 0; d < D; ++d) {
+          const float v = pool_v<D, F8>(a.pool, pb * Hkv + s.g, k, d);
+          if (fabsf(v) < CUDART_INF_F) continue;
+          if (part) part[d] += v;
+          else o[d] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(o[d]) + v, 0.f) & 0xffffu);
+        }
+      }
+    }
+  }
+}
+
+// Int8 pools: a stage's codes, in its upper half, widened in place to bf16 times
+// their block's power of two (lane l holds the exponent of block l % 8); the order
+// of reads and writes is widen_stage's.
+template <int D>
+__device__ __forceinline__ void widen_int8(uint8_t* stage, int lane, int e) {
+  using S = TcSmem<D>;
+  constexpr int kGroups = D / 8;              // 8-code groups per key
+  constexpr int kKeysPerStep = 32 / kGroups;  // keys converted per warp step
+  constexpr int kBatch = 16;                  // steps whose codes are loaded together
+  const uint8_t* codes = stage + S::kKV / 2;
+  const int kk = lane / kGroups, g8 = lane % kGroups;
+  const int hf = (g8 * 8) / 64, cw = g8 % 8;
+#pragma unroll 1
+  for (int b = 0; b < kNK / kKeysPerStep; b += kBatch) {
+    uint2 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      v[u] = *reinterpret_cast<const uint2*>(codes + ((b + u) * kKeysPerStep + kk) * D + g8 * 8);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = (b + u) * kKeysPerStep + kk, r8 = r % 8;
+      const uint32_t f = exp_bf16x2(__shfl_sync(0xffffffffu, e, (b + u) * kKeysPerStep / kBlockSize));
+      uint4 h;
+      int8x4_to_bf16x4(v[u].x, h.x, h.y);
+      int8x4_to_bf16x4(v[u].y, h.z, h.w);
+      h.x = mul_bf16x2(h.x, f);
+      h.y = mul_bf16x2(h.y, f);
+      h.z = mul_bf16x2(h.z, f);
+      h.w = mul_bf16x2(h.w, f);
+      *reinterpret_cast<uint4*>(stage + (r / 8) * S::kGS + hf * S::kHS + r8 * 128 + ((cw ^ r8) * 16)) = h;
+    }
+  }
+}
+
+// (x0, x1) *= Q(x^2) element by element, in paired fp32 operations.
+__device__ __forceinline__ void cap2(float& x0, float& x1, const float (&q)[5]) {
+  asm("{\n\t.reg .b64 p, z, r, k;\n\tmov.b64 p, {%0, %1};\n\tmul.rn.f32x2 z, p, p;\n\tmov.b64 r, {%6, %6};\n\t"
+      "mov.b64 k, {%5, %5};\n\tfma.rn.f32x2 r, r, z, k;\n\tmov.b64 k, {%4, %4};\n\tfma.rn.f32x2 r, r, z, k;\n\t"
+      "mov.b64 k, {%3, %3};\n\tfma.rn.f32x2 r, r, z, k;\n\tmov.b64 k, {%2, %2};\n\tfma.rn.f32x2 r, r, z, k;\n\t"
+      "mul.rn.f32x2 p, p, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x0), "+f"(x1) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]));
+}
+
+// A row's raw products with 128 keys to scores in log2 units; dpos: its position less the first key.
+__device__ __forceinline__ void modify_scores(float (&s)[kNK], const ScoreArgs& a, float slope, int dpos) {
+  if (a.cap_out != 0.f) {
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < kNK; c += 2) top[(c >> 1) & 3] = max3f(top[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    if (!__any_sync(0xffffffffu, !(most < a.cap_small))) {
+#pragma unroll
+      for (int c = 0; c < kNK; c += 2) cap2(s[c], s[c + 1], a.cap_q);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kNK; ++c) {
+        const float y = s[c] * a.base;
+        s[c] = a.cap_out * (fabsf(y) < 0.5f ? tanh_small(y) : tanh_large(y));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kNK; ++c) s[c] *= a.base;
+  }
+  if (a.slopes) {
+    if (__all_sync(0xffffffffu, dpos >= kNK - 1)) {   // every key at or before the position
+      const float b = -slope * static_cast<float>(dpos);
+#pragma unroll
+      for (int c = 0; c < kNK; ++c) s[c] += fmaf(slope, static_cast<float>(c), b);
+    } else {
+      const float d = static_cast<float>(dpos);
+#pragma unroll
+      for (int c = 0; c < kNK; ++c) s[c] = fmaf(-slope, fabsf(d - static_cast<float>(c)), s[c]);
+    }
+  }
+}
+
+template <int D, int KIND, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+               const __grid_constant__ CUtensorMap tmap_q) {
+  constexpr bool F8 = KIND == kPoolFp8;            // f16 operands
+  constexpr bool kCodes = KIND != kPoolBf16;       // stages are widened
+  const TreeArgs& a = sa.t;
+  using S = TcSmem<D>;
+  using M = ScoreSmem<D>;
+  using B = typename M::B;
+  constexpr int kKSt = S::kKSt, kVSt = S::kVSt;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  griddep_wait();
+  griddep_launch();   // the merge may take its place and wait
+  if (threadIdx.x < 2) a.cuts[2 * blockIdx.x + threadIdx.x].count = 0;
+  if ((smem_u32(smem) & 1023u) != 0) {   // swizzle atoms need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_INTERNAL);
+    return;
+  }
+  const unsigned err0 = *reinterpret_cast<volatile unsigned*>(a.pool.err);
+  if (__syncthreads_or((err0 & PKV_DEVERR_TIMEOUT) != 0)) return;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kOffBar);
+  float2* s_ml = reinterpret_cast<float2*>(smem + M::kOffMl);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + M::kOffMisc + 8);
+  volatile int* s_odd = reinterpret_cast<volatile int*>(smem + M::kOffMisc + 16);   // [kSegRing]
+  Seg* s_seg = reinterpret_cast<Seg*>(smem + M::kOffSeg);   // [kSegSlots]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.group, Hkv = a.pool.num_kv_heads;
+  Walk walk;
+  if (!walk.begin(sa)) return;   // block-uniform
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKSt; ++i) {
+      mbar_init(&bars[B::kKFull + i], 1);
+      mbar_init(&bars[B::kKEmpty + i], 1);
+      mbar_init(&bars[B::kKLanded + i], 1);
+    }
+    for (int i = 0; i < kVSt; ++i) {
+      mbar_init(&bars[B::kVFull + i], 1);
+      mbar_init(&bars[B::kVEmpty + i], 1);
+      mbar_init(&bars[B::kVLanded + i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars[B::kS + t], 1);
+      mbar_init(&bars[B::kP + t], 128);
+      mbar_init(&bars[B::kPv + t], 1);
+      mbar_init(&bars[B::kQFull + t], 1);
+      mbar_init(&bars[B::kQEmpty + t], 1);
+      mbar_init(&bars[B::kQc + t], 128);
+    }
+    mbar_init(&bars[B::kMl], 128);
+    mbar_init(&bars[B::kJoined], 128);
+    mbar_init(&bars[B::kDrain], 1);
+    for (int i = 0; i < kSegRing; ++i) mbar_init(&bars[B::kVDone + i], 1);
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(&bars[B::kSegFull + i], 1);
+      mbar_init(&bars[B::kSegEmpty + i], kSegReaders);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  if (warp == 9) {
+    tmem_alloc(s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t sQ = smem_u32(smem + S::kOffQ);
+  const uint32_t sK = smem_u32(smem + S::kOffK);
+  const uint32_t sV = smem_u32(smem + S::kOffV);
+  // The CTA's r-th segment: waits until it is published, reads it and frees its slot.  false: gave up, or no more (`ok`
+  // tells which).
+  Seg sg;
+  bool ok = true;
+  auto take = [&](int r) -> bool {
+    const int slot = r % kSegSlots;
+    if (!(ok = mbar_wait_warp(&bars[B::kSegFull + slot], (r / kSegSlots) & 1, s_abort, a.wait_ns))) return false;
+    sg = s_seg[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[B::kSegEmpty + slot]);
+    return (sg.flags & kSegEnd) == 0;
+  };
+
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------------------------ producers: warp 8 K (and Q), warp 10 V
+    const bool is_k = warp == 8;
+    const int nst = is_k ? kKSt : kVSt;
+    uint8_t* const stages = smem + (is_k ? S::kOffK : S::kOffV);
+    const int bar_full = is_k ? B::kKFull : B::kVFull, bar_empty = is_k ? B::kKEmpty : B::kVEmpty;
+    const int bar_landed = is_k ? B::kKLanded : B::kVLanded;
+    const CUtensorMap* const tm = is_k ? &tmap_k : &tmap_v;
+    int cnt = 0;      // tiles issued in the launch
+    int fin = 0;      // FP8: tiles widened and handed over
+    int nq = 0;       // segments whose query tiles have been issued
+    uint32_t landed_par = 0;
+    for (int r = 0; ok && take(r); ++r) {
+      if (is_k) {
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (!(ok = mbar_wait_warp(&bars[B::kQEmpty + t], (r & 1) ^ 1, s_abort, a.wait_ns))) break;
+          if (lane == 0) {
+            if ((t ? sg.rows1 : sg.rows0) > 0) {
+              mbar_arrive_expect_tx(&bars[B::kQFull + t], static_cast<uint32_t>(D * 2 * G * a.q_box_tokens));
+              uint8_t* qt = smem + S::kOffQ + t * S::kQ;
+#pragma unroll
+              for (int hf = 0; hf < S::kHalves; ++hf)
+                tma_load_3d(qt + hf * (kTcRows * 128), &tmap_q, hf * 64, sg.g * G, t ? sg.tok1 : sg.tok0,
+                            &bars[B::kQFull + t]);
+            } else {
+              mbar_arrive(&bars[B::kQFull + t]);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        nq = r + 1;
+      }
+      const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
+      const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
+      // Lane l holds block 32 w + l of the segment (window w: four key tiles), the next window in flight.
+      auto load_window = [&](int w) -> int {
+        const int j = sg.kt0 + w * 4 + lane / kBlkPerTile;
+        const int b = tile_at(j, sg.pre_tiles, sg.gap) * kBlkPerTile + lane % kBlkPerTile;
+        return j < sg.kt1 && b < nblk ? __ldg(bt_row + b) : -1;
+      };
+      auto check_window = [&](int pb) -> int { return pb >= 0 && pb < a.pool.num_blocks ? pb : -1; };
+      int win = 0;
+      int ids_cur = check_window(load_window(0)), ids_next = load_window(1);
+      // Int8: the window's exponents, asked for a window ahead (the kernel ahead may have written them).
+      auto load_exps = [&](int pb) -> int {
+        if (KIND != kPoolInt8 || pb < 0) return 0;
+        return safe_exp((is_k ? a.pool.k_exps : a.pool.v_exps)[static_cast<int64_t>(pb) * Hkv + sg.g]);
+      };
+      int exps_cur = load_exps(ids_cur), exps_next = 0;
+      if constexpr (KIND == kPoolInt8) {
+        ids_next = check_window(ids_next);
+        exps_next = load_exps(ids_next);
+      }
+      // Lane l < 8: chunk index of key tile j's block l, or -1, and its exponent.
+      int exp_at = 0;
+      auto block_chunk = [&](int j) -> int {
+        const int rel = j - sg.kt0;
+        if ((rel >> 2) != win) {
+          win = rel >> 2;
+          ids_cur = check_window(ids_next);
+          ids_next = load_window(win + 1);
+          if constexpr (KIND == kPoolInt8) {
+            exps_cur = exps_next;
+            ids_next = check_window(ids_next);
+            exps_next = load_exps(ids_next);
+          }
+        }
+        const int src = (rel & 3) * kBlkPerTile + (lane & 7);
+        const int pb = __shfl_sync(0xffffffffu, ids_cur, src);
+        if constexpr (KIND == kPoolInt8) exp_at = __shfl_sync(0xffffffffu, exps_cur, src);
+        return lane < kBlkPerTile && pb >= 0 ? pb * Hkv + sg.g : -1;
+      };
+      int seg_odd = 0;
+      // V tiles that some row does not see whole: clear the rows without a key
+      // (past the context, or of a block that is not there) and elements that are
+      // not finite.  have: blocks that were copied.
+      auto clean_v = [&](uint8_t* stage, int j, uint32_t have) {
+        constexpr int kCh = S::kHalves * 8;   // 16-byte chunks of a key's row
+        const int ch = lane % kCh;
+        uint8_t* col = stage + (ch / 8) * S::kHS;
+        const int live = sg.ctx - tile_at(j, sg.pre_tiles, sg.gap) * kNK;
+        bool odd = false;
+#pragma unroll 4
+        for (int key = lane / kCh; key < kNK; key += 32 / kCh) {
+          uint4* p = reinterpret_cast<uint4*>(col + (key / 8) * S::kGS + (key % 8) * 128 + (((ch % 8) ^ (key % 8)) * 16));
+          if (key >= live || !((have >> (key / kBlockSize)) & 1u)) {
+            *p = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          uint4 v = *p;
+          bool any = false;
+          v.x = finite_pair<F8>(v.x, any);
+          v.y = finite_pair<F8>(v.y, any);
+          v.z = finite_pair<F8>(v.z, any);
+          v.w = finite_pair<F8>(v.w, any);
+          if (any) {
+            *p = v;
+            odd = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, odd)) seg_odd = 1;
+      };
+      // Which tiles need it: those that some row does not see whole, or that lack a block.
+      auto needs_clean = [&](int j, uint32_t have) {
+        const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
+        return have != 0xffu || !seen_whole(sg, key0);
+      };
+      if constexpr (!kCodes) {
+        for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
+          const int y = block_chunk(j);
+          const int st = cnt % nst;
+          const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
+          if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
+          // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
+          if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
+          const bool clean = !is_k && needs_clean(j, have);
+          uint64_t* bar = &bars[(clean ? bar_landed : bar_full) + st];
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (S::kHalves * kBlockSize * 128));
+          __syncwarp();
+          uint8_t* stage = stages + st * S::kKV;
+          if (y >= 0) {
+            if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
+            else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
+          }
+          if (clean) {
+            const uint32_t par = (landed_par >> st) & 1u;
+            landed_par ^= 1u << st;
+            if (!mbar_wait_warp(bar, par, s_abort, a.wait_ns)) {
+              (void)mbar_wait(bar, par, nullptr, a.wait_ns);   // let this tile's copies land
+              ok = false;
+              break;
+            }
+            clean_v(stage, j, have);
+            fence_proxy_async_smem();   // read by the tensor cores
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[bar_full + st]);
+          }
+        }
+        if (!ok) break;
+      } else {
+        // Codes land in the upper half of a stage and are widened in place; a
+        // copy is issued as soon as a stage is free and widened as soon as it
+        // has landed, whichever is ready.
+        int jl = sg.kt0, jw = sg.kt0;
+        uint32_t have_ring = 0;   // blocks copied, 8 bits per stage (at most four stages)
+        uint32_t exp_ring = 0;    // int8, lane l < 8: exponents of block l, likewise
+        uint64_t idle0 = 0;
+        while (jw < sg.kt1) {
+          bool moved = false;
+          if (jl < sg.kt1 && cnt - fin < nst && mbar_test_warp(&bars[bar_empty + cnt % nst], ((cnt / nst) & 1) ^ 1)) {
+            const int y = block_chunk(jl), st = cnt % nst;
+            const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
+            have_ring = (have_ring & ~(0xffu << (8 * st))) | (have << (8 * st));
+            if constexpr (KIND == kPoolInt8)
+              exp_ring = (exp_ring & ~(0xffu << (8 * st))) | ((static_cast<uint32_t>(exp_at) & 0xffu) << (8 * st));
+            uint64_t* bar = &bars[bar_landed + st];
+            const bool withheld = a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0;   // test hook (above)
+            if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D));
+            __syncwarp();
+            if (y >= 0 && !withheld)
+              tma_load_2d(stages + st * S::kKV + S::kKV / 2 + lane * (kBlockSize * D), tm, 0, y * kBlockSize, bar);
+            ++cnt;
+            ++jl;
+            moved = true;
+          }
+          if (fin < cnt && mbar_test_warp(&bars[bar_landed + fin % nst], (fin / nst) & 1)) {
+            const int st = fin % nst;
+            uint8_t* stage = stages + st * S::kKV;
+            const uint32_t have = (have_ring >> (8 * st)) & 0xffu;
+            if constexpr (KIND == kPoolInt8) widen_int8<D>(stage, lane, static_cast<int8_t>((exp_ring >> (8 * st)) & 0xffu));
+            else widen_stage<D>(stage, lane);
+            if (KIND != kPoolInt8 && !is_k && needs_clean(jw, have)) {
+              __syncwarp();
+              clean_v(stage, jw, have);
+            }
+            fence_proxy_async_smem();   // read by the tensor cores
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[bar_full + st]);
+            ++fin;
+            ++jw;
+            moved = true;
+          }
+          if (moved) {
+            idle0 = 0;
+          } else {
+            const uint64_t now = globaltimer_ns();
+            if (idle0 == 0) idle0 = now;
+            if (__any_sync(0xffffffffu, *s_abort != 0 || now - idle0 > a.wait_ns)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+      }
+      if (ok && !is_k && lane == 0) {
+        s_odd[r % kSegRing] = seg_odd;
+        mbar_arrive(&bars[B::kVDone + r % kSegRing]);
+      }
+      __syncwarp();
+    }
+    if (!ok) {   // gave up: flag it and let copies already issued land
+      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+      *s_abort = 1;
+      if constexpr (kCodes) {
+        for (int i = fin; i < cnt; ++i) (void)mbar_wait(&bars[bar_landed + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
+      } else {
+        for (int i = max(0, cnt - nst); i < cnt; ++i)
+          (void)mbar_wait(&bars[bar_full + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
+      }
+      if (is_k && nq > 0) {
+        for (int t = 0; t < 2; ++t) (void)mbar_wait(&bars[B::kQFull + t], (nq - 1) & 1, nullptr, a.wait_ns);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = F8 ? make_idesc_f16(128, kNK, false) : make_idesc_bf16(128, kNK, false);
+    constexpr uint32_t idesc_o = F8 ? make_idesc_f16(128, D, true) : make_idesc_bf16(128, D, true);
+    const uint64_t dk = make_sdesc_sw128(sK, 16, S::kGS);
+    const uint64_t dv = make_sdesc_sw128(sV, S::kHS, S::kGS);
+    const uint64_t dqA = make_sdesc_sw128(sQ, 16, 1024), dqB = make_sdesc_sw128(sQ + S::kQ, 16, 1024);
+    auto k_desc = [&](int gk) { return dk + static_cast<uint64_t>(((gk % kKSt) * S::kKV) >> 4); };
+    auto v_desc = [&](int gv) { return dv + static_cast<uint64_t>(((gv % kVSt) * S::kKV) >> 4); };
+    const uint32_t lead = elect_one();   // every lane runs the issue code, the elected one issues
+    auto release = [&](int bar) { tc_commit_lead(lead, &bars[bar]); };
+    // S of group t = (query tile) K^T
+    auto issue_s = [&](int t, uint64_t dq, uint64_t kd) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int hf = ks / 4, kk = ks % 4;
+        tc_mma_lead(lead, tmem + t * kNK, dq + static_cast<uint64_t>((hf * (kTcRows * 128) + kk * 32) >> 4),
+                    kd + static_cast<uint64_t>((hf * S::kHS + kk * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+      }
+      release(B::kS + t);
+    };
+    // O of group t (+)= P V
+    auto issue_pv = [&](int t, bool acc, uint64_t vd) {
+#pragma unroll
+      for (int ks = 0; ks < kNK / 16; ++ks)
+        tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
+                       vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, (acc || ks > 0) ? 1u : 0u);
+    };
+    constexpr int kQReady = F8 ? B::kQc : B::kQFull;
+    int kc = 0, vc = 0;          // K / V tiles consumed
+    uint32_t pc0 = 0, pc1 = 0;   // P phases of group A / B waited so far
+    auto wait_k = [&] { return mbar_wait_warp(&bars[B::kKFull + kc % kKSt], (kc / kKSt) & 1, s_abort, a.wait_ns); };
+    auto wait_v = [&] { return mbar_wait_warp(&bars[B::kVFull + vc % kVSt], (vc / kVSt) & 1, s_abort, a.wait_ns); };
+    auto wait_p = [&](int t) {
+      const bool o = mbar_wait_warp(&bars[B::kP + t], (t ? pc1 : pc0) & 1, s_abort, a.wait_ns);
+      if (t) ++pc1; else ++pc0;
+      return o;
+    };
+    for (int r = 0; ok && take(r); ++r) {
+      const int n = sg.kt1 - sg.kt0;   // >= 1
+      if (!(ok = mbar_wait_warp(&bars[kQReady], r & 1, s_abort, a.wait_ns) &&
+                 mbar_wait_warp(&bars[kQReady + 1], r & 1, s_abort, a.wait_ns)))
+        break;
+      if (!(sg.flags & kSegSingle)) {
+        // Both groups use every key tile: PV_A(j) S_A(j+1) PV_B(j) S_B(j+1).
+        if (!(ok = wait_k())) break;
+        tc_fence_after();
+        issue_s(0, dqA, k_desc(kc));
+        issue_s(1, dqB, k_desc(kc));
+        if (n == 1) {
+          release(B::kQEmpty);
+          release(B::kQEmpty + 1);
+        }
+        release(B::kKEmpty + kc % kKSt);
+        ++kc;
+        for (int j = 0; ok && j < n; ++j) {
+          if (!(ok = wait_v())) break;
+          const uint64_t vd = v_desc(vc), kd = k_desc(kc);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!(ok = wait_p(t))) break;
+            tc_fence_after();
+            issue_pv(t, j > 0, vd);
+            if (j == n - 1) release(B::kPv + t);
+            if (j + 1 < n) {
+              if (t == 0 && !(ok = wait_k())) break;
+              issue_s(t, t ? dqB : dqA, kd);
+              if (j + 1 == n - 1) release(B::kQEmpty + t);
+            }
+          }
+          if (!ok) break;
+          if (j + 1 < n) {
+            release(B::kKEmpty + kc % kKSt);
+            ++kc;
+          }
+          release(B::kVEmpty + vc % kVSt);
+          ++vc;
+        }
+      } else {
+        // Group j % 2 uses key tile j: S_A(0) S_B(1), then PV(j) S(j+2).
+        release(B::kQEmpty + 1);   // no second query tile
+        for (int j = 0; ok && j < 2 && j < n; ++j) {
+          if (!(ok = wait_k())) break;
+          tc_fence_after();
+          issue_s(j, dqA, k_desc(kc));
+          if (j == n - 1) release(B::kQEmpty);
+          release(B::kKEmpty + kc % kKSt);
+          ++kc;
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int t = j & 1;
+          if (!(ok = wait_v() && wait_p(t))) break;
+          tc_fence_after();
+          if (t) issue_pv(1, j > 1, v_desc(vc)); else issue_pv(0, j > 1, v_desc(vc));
+          if (j + 2 >= n) release(B::kPv + t);
+          release(B::kVEmpty + vc % kVSt);
+          ++vc;
+          if (j + 2 < n) {
+            if (!(ok = wait_k())) break;
+            if (t) issue_s(1, dqA, k_desc(kc)); else issue_s(0, dqA, k_desc(kc));
+            if (j + 2 == n - 1) release(B::kQEmpty);
+            release(B::kKEmpty + kc % kKSt);
+            ++kc;
+          }
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+      *s_abort = 1;
+    }
+    // Drain: every MMA issued has completed before TMEM is released.
+    release(B::kDrain);
+    (void)mbar_wait_warp(&bars[B::kDrain], 0, nullptr, a.wait_ns);
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ scheduler
+    walk.find(sa, lane);
+    for (int r = 0;; ++r) {
+      Seg s;
+      TreeCut cut;
+      const bool more = walk.next(sa, s, cut);
+      if (more) {
+        if (cut.count > 0 && lane == 0) a.cuts[2 * blockIdx.x] = cut;
+        // Blocks that are not there: flagged here, and only then looked for by the softmax warps.
+        const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
+        const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
+        bool gone = false;
+        for (int x = s.kt0 * kBlkPerTile + lane; x < s.kt1 * kBlkPerTile; x += 32) {
+          const int b = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap) * kBlkPerTile + x % kBlkPerTile;
+          if (b >= nblk) continue;
+          const int pb = __ldg(bt_row + b);
+          gone |= pb < 0 || pb >= a.pool.num_blocks;
+        }
+        if (__any_sync(0xffffffffu, gone)) {
+          s.flags |= kSegMissing;
+          if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
+        }
+      } else {
+        s.flags = kSegEnd;
+      }
+      const int slot = r % kSegSlots;
+      if (!(ok = mbar_wait_warp(&bars[B::kSegEmpty + slot], ((r / kSegSlots) & 1) ^ 1, s_abort, a.wait_ns))) break;
+      if (lane == 0) {
+        s_seg[slot] = s;
+        mbar_arrive(&bars[B::kSegFull + slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+      *s_abort = 1;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax / epilogue of group X
+    const int X = (warp >> 2) & 1;
+    const int row = threadIdx.x & 127;        // row within the tile (TMEM lane)
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t colS = X * kNK, colO = kColO + X * 128;
+    const float sl2 = MOD ? 1.f : sa.base;   // what is left to multiply the scores with
+    uint32_t sc = 0, pvc = 0, joins = 0;      // phases waited so far
+    for (int r = 0; ok && take(r); ++r) {
+      const int g = sg.g;
+      const bool single = (sg.flags & kSegSingle) != 0, whole = (sg.flags & kSegWhole) != 0;
+      const bool mine = X == 0 || !single;               // stores its rows
+      const int nrows = X && !single ? sg.rows1 : sg.rows0;
+      const int tok = X && !single ? sg.tok1 : sg.tok0;
+      const bool valid = row < nrows;
+      const int t_row = tok + (valid ? row / G : 0);
+      const KeySpan span = key_span(sa, t_row, sg.ctx);
+      const int pos = MOD ? max(__ldg(a.positions + t_row), -1) : 0;
+      float slope = 0.f;   // log2 units
+      if (MOD && sa.slopes) slope = sa.slopes[g * G + row % G] * 1.4426950408889634f;
+      const int step = single ? 2 : 1;
+      const int n = sg.kt1 - sg.kt0;
+      const int nt = single ? (n + 1 - X) / 2 : n;    // key tiles of this group
+      if constexpr (F8) {
+        // Operands of one MMA share a type: this thread's Q row to f16, in place (exact within f16's range).
+        ok = mbar_wait_warp(&bars[B::kQFull + X], r & 1, s_abort, a.wait_ns);
+        if (ok && mine) {
+          uint8_t* qrow = smem + S::kOffQ + X * S::kQ + row * 128;
+#pragma unroll
+          for (int hf = 0; hf < S::kHalves; ++hf) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint4* q16 = reinterpret_cast<uint4*>(qrow + hf * (kTcRows * 128) + c * 16);
+              uint4 v = *q16;
+              v.x = pack_f16x2(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x));
+              v.y = pack_f16x2(bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
+              v.z = pack_f16x2(bf16lo_to_f32(v.z), bf16hi_to_f32(v.z));
+              v.w = pack_f16x2(bf16lo_to_f32(v.w), bf16hi_to_f32(v.w));
+              *q16 = v;
+            }
+          }
+          fence_proxy_async_smem();   // read by the tensor cores
+        }
+        mbar_arrive(&bars[B::kQc + X]);
+      }
+      // Blocks that are not there, as bits: window of 32 blocks (four key tiles) at a time.
+      const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
+      const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
+      auto missing_of = [&](int w) -> uint32_t {
+        const int j = sg.kt0 + w * 4 + lane / kBlkPerTile;
+        const int b = tile_at(j, sg.pre_tiles, sg.gap) * kBlkPerTile + lane % kBlkPerTile;
+        bool gone = false;
+        if (b < nblk && j < sg.kt1) {
+          const int pb = __ldg(bt_row + b);
+          gone = pb < 0 || pb >= a.pool.num_blocks;
+        }
+        return __ballot_sync(0xffffffffu, gone);
+      };
+      const bool any_missing = (sg.flags & kSegMissing) != 0;
+      uint32_t missing = any_missing ? missing_of(0) : 0u;
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int i = 0; ok && i < nt; ++i) {
+        const int rel = single ? 2 * i + X : i;
+        const int key0 = tile_at(sg.kt0 + rel, sg.pre_tiles, sg.gap) * kNK;
+        if (any_missing && rel > 0 && (rel & 3) < step) missing = missing_of(rel >> 2);
+        const uint32_t gone = (missing >> ((rel & 3) * kBlkPerTile)) & 0xffu;
+        const bool masked = gone != 0 || !seen_whole(sg, key0);
+        uint32_t vis[4];
+        if (masked) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            vis[w] = span_bits(sg.prefix, span, key0 + 32 * w);
+            if ((gone >> (2 * w)) & 1u) vis[w] &= 0xffff0000u;
+            if ((gone >> (2 * w)) & 2u) vis[w] &= 0x0000ffffu;
+          }
+        }
+        if (!(ok = mbar_wait_warp(&bars[B::kS + X], sc & 1, s_abort, a.wait_ns))) break;
+        ++sc;
+        tc_fence_after();
+        float s[kNK];
+#pragma unroll
+        for (int c = 0; c < kNK; c += 16) tmem_ld16(tmem + lane_base + colS + c, s + c);
+        tmem_wait_ld();
+        if constexpr (MOD) modify_scores(s, sa, slope, pos - key0);
+        if (masked) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[32 * w + c] = (vis[w] >> c) & 1u ? s[32 * w + c] : -CUDART_INF_F;
+        }
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+        for (int c = 16; c < kNK; c += 2) mx8[(c >> 1) & 7] = max3f(mx8[(c >> 1) & 7], s[c], s[c + 1]);
+        const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        // Lazy rescaling: a row keeps its reference while the tile's maximum
+        // stays within 2^kRescaleLog2 of it.  (Rows of the tile that are not the
+        // segment's, other requests' or whatever the buffer held, have no say:
+        // they would move the warp's references, and with them roundings.)
+        const float m_tile = valid ? mx * sl2 : -CUDART_INF_F;
+        const bool grow = __any_sync(0xffffffffu, m_tile > m + kRescaleLog2);
+        const float m_new = grow ? fmaxf(m, m_tile) : m;
+        const float neg_m = m_new == -CUDART_INF_F ? 0.f : -m_new;
+        float rs0[4] = {0.f, 0.f, 0.f, 0.f}, rs1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int cc = 0; cc < kNK; cc += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = cc; c < cc + 32; c += 2) {
+            float x0 = s[c], x1 = s[c + 1];
+            fma2(x0, x1, sl2, neg_m);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            add2(rs0[(c >> 1) & 3], rs1[(c >> 1) & 3], p0, p1);
+            pk[(c - cc) / 2] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tmem + lane_base + colS + cc / 2, reinterpret_cast<const float*>(pk));
+        }
+        const float rsum = ((rs0[0] + rs1[0]) + (rs0[1] + rs1[1])) + ((rs0[2] + rs1[2]) + (rs0[3] + rs1[3]));
+        const float alpha = grow && m != -CUDART_INF_F ? fast_exp2(m + neg_m) : 1.f;
+        if (grow && i > 0) {   // O is complete: S was issued after the group's previous PV
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld16(tmem + lane_base + colO + c, o);
+            tmem_ld16(tmem + lane_base + colO + c + 16, o + 16);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st16(tmem + lane_base + colO + c, o);
+            tmem_st16(tmem + lane_base + colO + c + 16, o + 16);
+          }
+        }
+        l = l * alpha + rsum;
+        m = m_new;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars[B::kP + X]);
+      }
+      if (!ok) break;
+      if (nt > 0) {
+        if (!(ok = mbar_wait_warp(&bars[B::kPv + X], pvc & 1, s_abort, a.wait_ns))) break;
+        ++pvc;
+        tc_fence_after();
+      }
+      float wa = 1.f, wb = 0.f;   // weights of A's and B's accumulators
+      bool join = false;
+      if (single) {
+        if (X == 1) {
+          s_ml[row] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(&bars[B::kMl]);
+          ok = mbar_wait_warp(&bars[B::kJoined], joins & 1, s_abort, a.wait_ns);
+          ++joins;
+          tc_fence_after();
+          // Its rows are A's to store; the segment's flag is still to be passed.
+          if (ok) ok = mbar_wait_warp(&bars[B::kVDone + r % kSegRing], (r / kSegRing) & 1, s_abort, a.wait_ns);
+          continue;
+        }
+        if (!(ok = mbar_wait_warp(&bars[B::kMl], joins & 1, s_abort, a.wait_ns))) break;
+        ++joins;
+        tc_fence_after();
+        join = n > 1;
+        const float2 b = s_ml[row];
+        if (join && b.y != 0.f) {   // l = 0: B saw no key of this row
+          if (l == 0.f) {
+            wa = 0.f;
+            wb = 1.f;
+            m = b.x;
+            l = b.y;
+          } else {
+            const float mm = fmaxf(m, b.x);
+            wa = fast_exp2(m - mm);
+            wb = fast_exp2(b.x - mm);
+            l = l * wa + b.y * wb;
+            m = mm;
+          }
+        }
+      }
+      const float inv = l == 0.f ? 0.f : (F8 ? a.pool.v_scale : 1.f) / l;
+      const float lse2 = l == 0.f ? -CUDART_INF_F : m + fast_log2(l);
+      const int h = g * G + row % G;
+      const int64_t prow = static_cast<int64_t>(sg.slot) * 256 + X * 128 + row;
+      const int64_t orow = static_cast<int64_t>(t_row) * a.num_q_heads + h;
+      uint4* dst_o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * D);
+      float4* dst_p = reinterpret_cast<float4*>(a.part_o + prow * D);
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float ob[32];
+        tmem_ld16(tmem + lane_base + colO + c0, ob);
+        tmem_ld16(tmem + lane_base + colO + c0 + 16, ob + 16);
+        if (join) {   // warp-uniform
+          float oc[32];
+          tmem_ld16(tmem + lane_base + kColO + 128 + c0, oc);
+          tmem_ld16(tmem + lane_base + kColO + 128 + c0 + 16, oc + 16);
+          tmem_wait_ld();
+          // (a weight of 0 stands for a state without keys: its columns may hold anything)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            ob[e] = (wa == 0.f ? 0.f : ob[e] * wa) + (wb == 0.f ? 0.f : oc[e] * wb);
+        } else {
+          tmem_wait_ld();
+        }
+        if (valid && l != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ob[e] *= inv;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ob[e] = 0.f;
+        }
+        if (valid) {
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              uint4 w0, w1;
+              w0.x = pack_bf16x2(ob[e], ob[e + 1]);       w0.y = pack_bf16x2(ob[e + 2], ob[e + 3]);
+              w0.z = pack_bf16x2(ob[e + 4], ob[e + 5]);   w0.w = pack_bf16x2(ob[e + 6], ob[e + 7]);
+              w1.x = pack_bf16x2(ob[e + 8], ob[e + 9]);   w1.y = pack_bf16x2(ob[e + 10], ob[e + 11]);
+              w1.z = pack_bf16x2(ob[e + 12], ob[e + 13]); w1.w = pack_bf16x2(ob[e + 14], ob[e + 15]);
+              // A thread writes its own row: 32 bytes a store, a whole sector, where o allows it.
+              if (a.o_align32) {
+                st_global_v8(dst_o + (c0 + e) / 8, w0, w1);
+              } else {
+                dst_o[(c0 + e) / 8] = w0;
+                dst_o[(c0 + e) / 8 + 1] = w1;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(ob + e);
+              st_global_v8(dst_p + (c0 + e) / 4, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+            }
+          }
+        }
+      }
+      if (single) {
+        tc_fence_before();
+        mbar_arrive(&bars[B::kJoined]);   // B's columns have been read
+      }
+      if (valid) {
+        if (whole) {
+          if (a.lse) a.lse[orow] = lse2 * 0.69314718055994530942f;
+        } else {
+          a.part_lse[prow] = lse2;
+        }
+      }
+      if (!(ok = mbar_wait_warp(&bars[B::kVDone + r % kSegRing], (r / kSegRing) & 1, s_abort, a.wait_ns))) break;
+      if (s_odd[r % kSegRing] && valid)
+        add_odd<D, F8>(sa, sg, span, static_cast<uint16_t*>(a.o) + orow * D, whole ? nullptr : a.part_o + prow * D);
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+      *s_abort = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, int KIND, bool MOD>
+int launch_m(const ScoreArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* tq, cudaStream_t s) {
+  const int smem = ScoreSmem<D>::kTotal;
+  const cudaError_t e = smem_attr_once<score_tc_kernel<D, KIND, MOD>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(score_tc_kernel<D, KIND, MOD>, dim3(a.t.ctas), kThreads, smem, s, a, *tk, *tv, *tq);
+}
+template <int D, int KIND>
+int launch_k(const ScoreArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* tq, cudaStream_t s) {
+  return a.cap_out != 0.f || a.slopes ? launch_m<D, KIND, true>(a, tk, tv, tq, s) : launch_m<D, KIND, false>(a, tk, tv, tq, s);
+}
+
+}  // namespace
+
+template <int D>
+int launch_score_tc(const ScoreArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream) {
+  const CUtensorMap* k = static_cast<const CUtensorMap*>(tmk);
+  const CUtensorMap* v = static_cast<const CUtensorMap*>(tmv);
+  const CUtensorMap* q = static_cast<const CUtensorMap*>(tmq);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_dependent(score_plan_kernel, dim3(1), kPlanThreads, 0, s, a);
+  if (e != cudaSuccess) return e;
+  const PoolView& p = a.t.pool;
+  if (p.k_exps) return launch_k<D, kPoolInt8>(a, k, v, q, s);
+  return p.elem_bytes == 1 ? launch_k<D, kPoolFp8>(a, k, v, q, s) : launch_k<D, kPoolBf16>(a, k, v, q, s);
+}
+
+}  // namespace pkv

@@ -5,6 +5,9 @@ Beside the roundings that attn_ref counts (products, sums, exp2, P, O, LSE):
            step of the score; tanh itself is off by 2^-22 of 1 at most, times cap.
   slopes   the distance, its product and the sum are rounded once each: 3 2^-24 slope dist, and 2^-23 |x| for the sums.
   int8     the power of two is exact on scores and P; K and V are bf16 values, P is rounded to bf16.
+  range    p_j relative to the row's maximum is an fp32 number: a weight below 2^-126 (an exponent below -126) is taken as
+           zero, so n keys may lack n 2^-126 max|v|.  (Values of dims whose heavy keys hold zeros are that small: with a
+           weight of 2^-190 the formula gives 6e-59 there, and fp32, whose least number is 1.4e-45, gives 0.)
 """
 import numpy as np
 
@@ -41,6 +44,7 @@ def rows(q, k, v, pos, seen, scale, softcap, slopes, f16_p):
     ds = np.nan_to_num((d + 8) * 2.0 ** -24 * B + 2.0 ** -15 + more)
     up = 2.0 ** -11 if f16_p else 2.0 ** -8
     tol_o = (up + 2 * ds[:, None] + len(j) * 2.0 ** -24) * A + 2.0 ** -8 * np.abs(o)
+    tol_o = tol_o + len(j) * 2.0 ** -126 * np.abs(np.nan_to_num(v, nan=0.0, posinf=0.0, neginf=0.0)).max()
     if f16_p:
         tol_o = tol_o + len(j) * 2.0 ** -25 * np.abs(np.nan_to_num(v, nan=0.0, posinf=0.0, neginf=0.0)).max()
     return o, lse, tol_o, ds + 2.0 ** -23 * np.abs(lse)

@@ -132,10 +132,24 @@ def options(name, batch):
     return o
 
 
+@pytest.fixture(params=[1, 2], ids=["rows", "tiles"])
+def form(request, monkeypatch):
+    """Which kernel takes the batch."""
+    make = make_pool
+
+    def forced(*args):
+        pool = make(*args)
+        pkv.pkv_debug_set(pool, pkv.PKV_DEBUG_TREE_FORM, request.param)
+        return pool
+
+    monkeypatch.setitem(globals(), "make_pool", forced)
+    return request.param
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("opt", list(OPTIONS))
 @pytest.mark.parametrize("batch", list(BATCHES))
-def test_against_the_formulas(batch, opt, dtype):
+def test_against_the_formulas(batch, opt, dtype, form):
     reqs = BATCHES[batch]
     Case(len(reqs) + 11, reqs, 8, 2, 64, dtype, extra=2, **options(opt, reqs)).run()
 
@@ -143,13 +157,13 @@ def test_against_the_formulas(batch, opt, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("hq,hkv,d", [(8, 8, 128), (64, 8, 128), (24, 1, 64), (15, 3, 128), (128, 1, 64), (2, 2, 64), (5, 5, 128)])
 @pytest.mark.parametrize("opt", ["causal", "all"])
-def test_heads(hq, hkv, d, dtype, opt):
+def test_heads(hq, hkv, d, dtype, opt, form):
     reqs = [tail(150, 2), tail(31, 31), tail(500, 1), tail(64, 40)]
     Case(5, reqs, hq, hkv, d, dtype, extra=1, **options(opt, reqs)).run()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_long_contexts_cut_into_shares(dtype):
+def test_long_contexts_cut_into_shares(dtype, form):
     reqs = [tail(30000, 1), tail(17, 1), tail(9001, 2)]
     Case(6, reqs, 8, 2, 128, dtype).run()
     c = Case(7, reqs, 8, 2, 128, dtype, softcap=4.0, slopes=True, window=9000, prefix=[100, 17, 0]).run()
@@ -158,20 +172,28 @@ def test_long_contexts_cut_into_shares(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_many_requests(dtype):
+def test_many_requests(dtype, form):
     rng = np.random.default_rng(4)
     reqs = [tail(int(c), 1) for c in rng.integers(1, 90, 700)]
     Case(8, reqs, 4, 2, 64, dtype, window=20).run()
 
 
-def test_empty_rows_are_zero():
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("opt", ["causal", "cap", "slopes", "all"])
+def test_prompts_of_several_tiles(dtype, opt):
+    """The chosen form (tiles): pairs and single tiles over many key tiles, groups cut into shares."""
+    reqs = [tail(1500, 700), tail(900, 900), tail(40, 1)]
+    Case(19, reqs, 8, 2, 128, dtype, extra=3, **options(opt, reqs)).run()
+
+
+def test_empty_rows_are_zero(form):
     c = Case(9, BATCHES["steps"], 4, 2, 64, docs=5)
     c.run()
     assert c.seen_empty
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
-def test_values_that_are_not_finite(dtype):
+def test_values_that_are_not_finite(dtype, form):
     """Infinite and NaN keys and values reach the rows that see them, and no others."""
     reqs = [tail(70, 40), tail(300, 3)]
     c = Case(10, reqs, 8, 2, 64, dtype, window=30, prefix=[5, 0])
@@ -217,7 +239,7 @@ def test_values_that_are_not_finite(dtype):
     c.check(o, lse, set(clean))
 
 
-def test_exponents_of_int8_pages():
+def test_exponents_of_int8_pages(form):
     """The largest and smallest exponents, and pages whose exponents were never written."""
     reqs = [tail(64, 3), tail(40, 1)]
     c = Case(11, reqs, 4, 2, 64, "int8")
@@ -234,7 +256,7 @@ def test_exponents_of_int8_pages():
     assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
 
 
-def test_extreme_scores():
+def test_extreme_scores(form):
     """Scores far beyond the cap, a large scale, distances past 2^24 steps of a float."""
     reqs = [tail(50, 50)]
     Case(12, reqs, 4, 2, 64, softcap=30.0, scale=50.0).run()
@@ -244,7 +266,7 @@ def test_extreme_scores():
     c.run()
 
 
-def test_bad_blocks_lengths_and_positions():
+def test_bad_blocks_lengths_and_positions(form):
     reqs = [tail(100, 3), tail(40, 2), tail(33, 1)]
     c = Case(15, reqs, 8, 2, 64, prefix=[20, 0, 0], window=30)
     c.bt[0, 5], c.bt[1, 1] = -1, c.pool.num_blocks
@@ -293,7 +315,7 @@ def test_a_step_of_an_8_bit_cache(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_graph_streams_and_devices(dtype):
+def test_graph_streams_and_devices(dtype, form):
     """Captured once, replayed with other lengths, tables, positions and masks; on another stream; bits do not change."""
     reqs = [tail(200, 3), tail(77, 2)]
     a, b = (Case(17 + i, rq, 8, 2, 64, dtype, extra=1, window=40, softcap=8.0, prefix=pre, docs=90)
