@@ -48,7 +48,6 @@ struct Modify {
 template <int D, int KIND>
 struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
   static constexpr bool kCodes = KIND != kPoolBf16;
-  [[maybe_unused]] static constexpr bool kF16 = KIND == kPoolFp8;
   using Base = RowTile<D, kCodes>;
   using Base::kSteps, Base::kTiles, Base::q, Base::o, Base::m, Base::l, Base::odd, Base::ld_codes;
 
@@ -159,7 +158,7 @@ struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
             for (int i = 0; i < 4; ++i) {
               uint32_t b0, b1;
               widen(w[i], b0, b1);
-              mma16<kF16>(s[n][t], q[4 * u + i], b0, b1);
+              mma16<KIND == kPoolFp8>(s[n][t], q[4 * u + i], b0, b1);
             }
           }
       }
@@ -279,7 +278,7 @@ struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
             for (int e = 0; e < 8; ++e) b[e] = finite_pair<true>(b[e], odd);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma16<kF16>(o[4 * i + e], p[n], b[2 * e], b[2 * e + 1]);
+          for (int e = 0; e < 4; ++e) mma16<KIND == kPoolFp8>(o[4 * i + e], p[n], b[2 * e], b[2 * e + 1]);
         }
       }
     }
@@ -343,21 +342,23 @@ template <int D, bool F8>
 __device__ __noinline__ void score_add_odd(const ScoreArgs& a, const RowsReq& q, const int32_t* bt_row, int g,
                                            KeySpan s, KeySpan all, int i0, int i1, uint16_t* o, float* part, int lane) {
   const int64_t Hkv = a.t.pool.num_kv_heads;
-  for (int i = i0; i < i1; ++i) {
-    const int b = i < q.pblk ? i : i + q.gap;
-    const uint32_t vis = b >= a.t.max_blocks ? 0u : span_bits(q.prefix, s, b * kBlockSize);
-    if (!(vis & 0xffffu) || b * kBlockSize + kBlockSize <= q.prefix ||
-        (b * kBlockSize >= all.lo && b * kBlockSize + kBlockSize - 1 <= all.hi))
-      continue;
-    const int pb = __ldg(bt_row + b);
-    if (pb < 0 || pb >= a.t.pool.num_blocks) continue;
-    for (int k = 0; k < kBlockSize; ++k) {
-      if (!((vis >> k) & 1u)) continue;
-      for (int d = lane; d < D; d += 32) {
-        const float v = pool_v<D, F8>(a.t.pool, pb * Hkv + g, k, d);
-        if (fabsf(v) < CUDART_INF_F) continue;
-        if (part) part[d] += v;
-        else o[d] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(o[d]) + v, 0.f) & 0xffffu);
+  for (int i = i0; i < i1; i += 32) {
+    const int b1 = i + lane < q.pblk ? i + lane : i + lane + q.gap, key = b1 * kBlockSize;
+    const bool odd = i + lane < i1 && b1 < a.t.max_blocks && key + kBlockSize > q.prefix &&
+                     !(key >= all.lo && key + kBlockSize - 1 <= all.hi) && (span_bits(q.prefix, s, key) & 0xffffu);
+    for (uint32_t left = __ballot_sync(0xffffffffu, odd); left; left &= left - 1) {
+      const int b = __shfl_sync(0xffffffffu, b1, __ffs(left) - 1);
+      const uint32_t vis = span_bits(q.prefix, s, b * kBlockSize);
+      const int pb = __ldg(bt_row + b);
+      if (pb < 0 || pb >= a.t.pool.num_blocks) continue;
+      for (int k = 0; k < kBlockSize; ++k) {
+        if (!((vis >> k) & 1u)) continue;
+        for (int d = lane; d < D; d += 32) {
+          const float v = pool_v<D, F8>(a.t.pool, pb * Hkv + g, k, d);
+          if (fabsf(v) < CUDART_INF_F) continue;
+          if (part) part[d] += v;
+          else o[d] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(o[d]) + v, 0.f) & 0xffffu);
+        }
       }
     }
   }

@@ -19,13 +19,15 @@ constexpr int kPoolBf16 = 0, kPoolFp8 = 1, kPoolInt8 = 2;
 
 // Two neighbouring query tiles of a request (rows1 = 0: one), of the tiles form's
 // plan: key tiles 0 .. ktiles - 1, of which those below pre_tiles hold the prefix
-// and the others lie `gap` tiles further on; every row sees the keys [all_lo, all_hi].
+// and the others lie `gap` tiles further on.  Every row sees the prefix and the keys
+// [all_lo, all_hi], none sees others than these of [any_lo, any_hi].
 struct alignas(16) ScoreItem {
   int req, tok0, rows0, rows1;
   int pre_tiles, gap, ktiles, prefix;
-  int ctx, all_lo, all_hi, pad;
+  int all_lo, all_hi, any_lo, any_hi;
+  int ctx, pad[3];
 };
-static_assert(sizeof(ScoreItem) == 48, "ScoreItem layout: three 16-byte loads");
+static_assert(sizeof(ScoreItem) == 64, "ScoreItem layout: four 16-byte loads");
 // The plan in the workspace, for `most` items at most.
 struct ScorePlan {
   ScoreItem* items;   // [most]
@@ -39,7 +41,7 @@ struct ScoreArgs {
   TreeArgs t;
   float base;                 // raw products to log2 units, or to the cap's argument (FP8: with k_scale)
   float cap_out;              // cap * log2 e (0: no cap)
-  float cap_small, cap_q[5];  // products below cap_small: x Q(x^2) is the capped score in log2 units
+  float cap_small, cap_q[4];  // products below cap_small: x (q0 + q1 x^2 + ...) is the capped score in log2 units
   const float* slopes;        // [num_q_heads], or nullptr
   int window;                 // 0: none
   const int32_t* first_keys;  // [num_tokens], or nullptr
@@ -50,12 +52,15 @@ struct ScoreArgs {
 struct KeySpan {
   int lo, hi;
 };
-__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int ctx) {
-  const int p = max(__ldg(a.t.positions + t), -1);
-  KeySpan s{a.first_keys ? max(__ldg(a.first_keys + t), 0) : 0, min(p, ctx - 1)};
+__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int pos, int first, int ctx) {
+  const int p = max(pos, -1);
+  KeySpan s{max(first, 0), min(p, ctx - 1)};
   if (a.window > 0) s.lo = max(s.lo, p - a.window + 1);
   s.lo = min(s.lo, ctx);
   return s;
+}
+__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int ctx) {
+  return key_span(a, __ldg(a.t.positions + t), a.first_keys ? __ldg(a.first_keys + t) : 0, ctx);
 }
 // Keys [key0, key0 + 32) that a token sees, as bits.
 __device__ __forceinline__ uint32_t span_bits(int prefix, KeySpan s, int key0) {
@@ -96,5 +101,7 @@ __device__ __forceinline__ float tanh_large(float y) {
   const float e = fast_exp2(fabsf(y) * -2.8853900817779268f);
   return copysignf(__fdividef(1.f - e, 1.f + e), y);
 }
+
+__device__ __forceinline__ float tanh_any(float y) { return fabsf(y) < 0.5f ? tanh_small(y) : tanh_large(y); }
 
 }  // namespace pkv

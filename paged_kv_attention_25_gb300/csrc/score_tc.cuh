@@ -22,12 +22,13 @@
 // reach a row as 0 * inf) and the rows past the context; rows that do see such an
 // element get it added after their result is stored.  Int8 values are finite.
 //
-// Scores: tanh on the FMA pipe, as x Q(x^2) with the polynomial of tanh_small and
-// the scales in its coefficients, five paired operations for two scores, while
-// every |x| of the warp's rows stays below half the cap; tanh_large otherwise.
+// Scores: tanh on the FMA pipe, as a polynomial with the scales in its coefficients,
+// five paired operations for two scores, while every score of the warp's rows stays
+// below half the cap; otherwise by tanh_small and tanh_large.
 //
-// Int8 pools: the producers widen a stage's codes to bf16 times the block's power
-// of two, exactly; the MMAs are those of bf16 pools.
+// Pools of codes: they land in the upper half of a stage, and four more warps widen
+// them in place, two for K and two for V (int8: to bf16 times the block's power of
+// two, exactly, so that the MMAs are those of bf16 pools; FP8: to f16).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -46,11 +47,14 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 384;
+// Warps 0 .. 7 softmax, 8 Q and K producer, 9 MMA issuer, 10 V producer, 11 scheduler; codes: 12 .. 15 widen.
+template <int KIND>
+constexpr int kThreads = KIND == kPoolBf16 ? 384 : 512;
 constexpr int kBlkPerTile = kNK / kBlockSize;   // 8
 constexpr int kSegSlots = 4;                    // segments handed out ahead
 constexpr int kSegRing = 8;                     // V producer's reports (it is at most kSegSlots + 1 ahead)
-constexpr int kSegReaders = 11;                 // warps that read a segment
+template <int KIND>
+constexpr int kSegReaders = KIND == kPoolBf16 ? 11 : 15;   // warps that read a segment
 constexpr int kPairUnits = 3, kSingleUnits = 2, kGroupUnits = 6;
 using TcShare = Share<kPairUnits + kGroupUnits>;
 
@@ -80,10 +84,18 @@ struct alignas(16) Seg {
   int req, g, prefix, ctx;
   int tok0, tok1, rows0, rows1;   // query tiles (rows1 = 0: single)
   int kt0, kt1, slot, flags;
-  int pre_tiles, gap, all_lo, all_hi;   // every row sees the keys [all_lo, all_hi]
+  int pre_tiles, gap, all_lo, all_hi;   // every row sees the keys [all_lo, all_hi],
+  int any_lo, any_hi, pad0, pad1;       // none sees others than these (and the prefix)
 };
-static_assert(sizeof(Seg) == 64, "Seg layout: four 16-byte loads");
+static_assert(sizeof(Seg) == 80, "Seg layout: five 16-byte loads");
 constexpr int kSegSingle = 1, kSegWhole = 2, kSegMissing = 4, kSegEnd = 8;
+
+// A V element that is not finite and was left out of the products of a segment.
+constexpr int kOddMost = 8;   // noted of a segment; all are counted
+struct Odd {
+  int key;
+  uint16_t dim, bits;   // value: bf16, or the f16 of an FP8 code
+};
 
 template <int D>
 struct ScoreSmem {
@@ -92,7 +104,8 @@ struct ScoreSmem {
   static constexpr int kOffBar = S::kOffBar;
   static constexpr int kOffMl = kOffBar + ((B::kCount * 8 + 15) / 16) * 16;   // float2 [128]: B's m, l
   static constexpr int kOffSeg = kOffMl + kTcRows * 8;
-  static constexpr int kOffMisc = kOffSeg + kSegSlots * static_cast<int>(sizeof(Seg));
+  static constexpr int kOffOdd = kOffSeg + kSegSlots * static_cast<int>(sizeof(Seg));   // Odd [kSegRing][kOddMost]
+  static constexpr int kOffMisc = kOffOdd + kSegRing * kOddMost * 8;
   static constexpr int kTotal = kOffMisc + 64;
 };
 static_assert(ScoreSmem<128>::kTotal <= 232448, "shared memory of the D = 128 kernel");
@@ -103,6 +116,17 @@ __device__ __forceinline__ int tile_at(int j, int pre_tiles, int gap) { return j
 // Whether every row of the segment sees the whole key tile that begins at key0.
 __device__ __forceinline__ bool seen_whole(const Seg& s, int key0) {
   return key0 + kNK <= s.prefix || (key0 >= s.all_lo && key0 + kNK - 1 <= s.all_hi);
+}
+
+// The blocks of the key tile at key0 that some row sees a key of, as bits; those that every row sees whole.
+__device__ __forceinline__ uint32_t blocks_below(int keys) { return low_bits(min(max(keys, 0) / kBlockSize, kBlkPerTile)); }
+__device__ __forceinline__ uint32_t blocks_needed(const Seg& s, int key0) {
+  const uint32_t span = s.any_hi < s.any_lo ? 0u : blocks_below(s.any_hi - key0 + kBlockSize) & ~blocks_below(s.any_lo - key0);
+  return blocks_below(s.prefix - key0 + kBlockSize - 1) | span;
+}
+__device__ __forceinline__ uint32_t blocks_whole(const Seg& s, int key0) {
+  return blocks_below(s.prefix - key0) |
+         (blocks_below(s.all_hi - key0 + 1) & ~blocks_below(s.all_lo - key0 + kBlockSize - 1));
 }
 
 // Walks a CTA's share of the line.  Key tile k of a group that begins at unit 0
@@ -149,7 +173,7 @@ struct Walk {
       if (fresh) {
         const int4* p = reinterpret_cast<const int4*>(a.plan.items + idx);
         const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
-        it = ScoreItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+        it = ScoreItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w, __ldcg(&a.plan.items[idx].ctx), {0, 0, 0}};
         at = __ldcg(a.plan.cum + idx);
         fresh = false;
       }
@@ -185,6 +209,8 @@ struct Walk {
       s.gap = it.gap;
       s.all_lo = it.all_lo;
       s.all_hi = it.all_hi;
+      s.any_lo = it.any_lo;
+      s.any_hi = it.any_hi;
       cut.count = 0;
       if (kt0 == 0 && kt1 < kt) {
         // The last tile's first unit names the last worker; the workers between each have a tile (a share is
@@ -236,78 +262,118 @@ __device__ __forceinline__ T block_scan(T x, T& carry, T* scratch) {
   return r;
 }
 
+// Requests' lengths and items' costs are kept in shared memory where they fit (kept
+// requests, kept items), and a warp has the spans of kPlanBatch items under way:
+// what is left is four trips to memory for a small batch.
+constexpr int kPlanReqs = 1024, kPlanItems = 2048, kPlanBatch = 4;
+struct PlanReq {
+  int t0, n, ctx, prefix, first;
+};
 __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArgs a) {
   __shared__ int64_t scratch[32];
+  __shared__ PlanReq s_req[kPlanReqs];
+  __shared__ int s_cost[kPlanItems];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tt = a.t.tile_tokens, R = a.t.num_reqs;
   griddep_wait();
   griddep_launch();
+  const bool kept = R <= kPlanReqs;
   int* const first = a.plan.first;   // items before each request's
   int n_items = 0;
   for (int base = 0; base < R; base += kPlanThreads) {
+    ScoreReq q{0, 0, 0, 0, false};
     int n = 0;
     if (base + tid < R) {
-      const ScoreReq q = score_req(a, base + tid);
+      q = score_req(a, base + tid);
       n = pairs_of(q, tt);
       if (q.bad) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
     }
     const int f = block_scan(n, n_items, reinterpret_cast<int*>(scratch));
-    if (base + tid < R) first[base + tid] = f;
+    if (kept) s_req[tid] = PlanReq{q.t0, q.n, q.ctx, q.prefix, f};
+    else if (base + tid < R) first[base + tid] = f;
   }
   __syncthreads();
   n_items = min(n_items, a.plan.most);   // (ranges that overlap could make more)
-  for (int i = warp; i < n_items; i += kPlanThreads / 32) {
-    int lo = 0, n = R;   // the last request with first <= i (those without items share their successor's)
-    while (n > 1) {
-      const int step = (n + 31) / 32;
-      const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && first[lo + min(lane * step, n - 1)] <= i);
-      const int k = max(0, __popc(le) - 1);
-      n = min(step, n - k * step);
-      lo += k * step;
+  const bool costs = n_items <= kPlanItems;
+  for (int i0 = warp; i0 < n_items; i0 += kPlanBatch * (kPlanThreads / 32)) {
+    PlanReq q[kPlanBatch];
+    int req[kPlanBatch], t0[kPlanBatch], nt[kPlanBatch], any_lo[kPlanBatch], all_lo[kPlanBatch], any_hi[kPlanBatch],
+        all_hi[kPlanBatch];
+#pragma unroll
+    for (int b = 0; b < kPlanBatch; ++b) {
+      const int i = min(i0 + b * (kPlanThreads / 32), n_items - 1);
+      int lo = 0, n = R;   // the last request with first <= i (those without items share their successor's)
+      while (n > 1) {
+        const int step = (n + 31) / 32, x = lo + min(lane * step, n - 1);
+        const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && (kept ? s_req[x].first : first[x]) <= i);
+        const int k = max(0, __popc(le) - 1);
+        n = min(step, n - k * step);
+        lo += k * step;
+      }
+      req[b] = lo;
+      if (kept) {
+        q[b] = s_req[lo];
+      } else {
+        const ScoreReq r = score_req(a, lo);
+        q[b] = PlanReq{r.t0, r.n, r.ctx, r.prefix, first[lo]};
+      }
+      t0[b] = q[b].t0 + (i - q[b].first) * 2 * tt;
+      nt[b] = min(2 * tt, q[b].t0 + q[b].n - t0[b]);
+      any_lo[b] = INT_MAX;
+      all_lo[b] = 0;
+      any_hi[b] = -1;
+      all_hi[b] = INT_MAX;
     }
-    const ScoreReq q = score_req(a, lo);
-    const int t0 = q.t0 + (i - first[lo]) * 2 * tt, nt = min(2 * tt, q.t0 + q.n - t0);
-    int any_lo = INT_MAX, all_lo = 0, any_hi = -1, all_hi = INT_MAX;
     bool bad = false;
-    for (int t = t0 + lane; t < t0 + nt; t += 32) {
-      const KeySpan s = key_span(a, t, q.ctx);
-      any_lo = min(any_lo, s.lo);
-      all_lo = max(all_lo, s.lo);
-      any_hi = max(any_hi, s.hi);
-      all_hi = min(all_hi, s.hi);
-      const int p = __ldg(a.t.positions + t);
-      bad |= p < 0 || p >= a.t.max_blocks * kBlockSize;
+    for (int x = lane; x < 2 * tt; x += 32) {
+#pragma unroll
+      for (int b = 0; b < kPlanBatch; ++b) {
+        if (x >= nt[b]) continue;
+        const KeySpan s = key_span(a, t0[b] + x, q[b].ctx);
+        any_lo[b] = min(any_lo[b], s.lo);
+        all_lo[b] = max(all_lo[b], s.lo);
+        any_hi[b] = max(any_hi[b], s.hi);
+        all_hi[b] = min(all_hi[b], s.hi);
+        const int p = __ldg(a.t.positions + t0[b] + x);
+        bad |= p < 0 || p >= a.t.max_blocks * kBlockSize;
+      }
     }
-    any_lo = __reduce_min_sync(0xffffffffu, any_lo);
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    any_hi = __reduce_max_sync(0xffffffffu, any_hi);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
-    if (lane == 0) {
+#pragma unroll
+    for (int b = 0; b < kPlanBatch; ++b) {
+      const int i = i0 + b * (kPlanThreads / 32);
+      if (i >= n_items) break;
       ScoreItem it;
-      it.req = lo;
-      it.tok0 = t0;
-      it.rows0 = min(tt, nt) * a.t.group;
-      it.rows1 = max(0, nt - tt) * a.t.group;
-      it.pre_tiles = (q.prefix + kNK - 1) / kNK;
-      const int k0 = max(it.pre_tiles, any_lo / kNK);
+      it.any_lo = __reduce_min_sync(0xffffffffu, any_lo[b]);
+      it.all_lo = __reduce_max_sync(0xffffffffu, all_lo[b]);
+      it.any_hi = __reduce_max_sync(0xffffffffu, any_hi[b]);
+      it.all_hi = __reduce_min_sync(0xffffffffu, all_hi[b]);
+      it.req = req[b];
+      it.tok0 = t0[b];
+      it.rows0 = min(tt, nt[b]) * a.t.group;
+      it.rows1 = max(0, nt[b] - tt) * a.t.group;
+      it.prefix = q[b].prefix;
+      it.ctx = q[b].ctx;
+      it.pre_tiles = (it.prefix + kNK - 1) / kNK;
+      const int k0 = max(it.pre_tiles, it.any_lo / kNK);
       it.gap = k0 - it.pre_tiles;
-      it.ktiles = max(1, it.pre_tiles + max(0, (any_hi + kNK) / kNK - k0));   // (one at least: its rows are written too)
-      it.prefix = q.prefix;
-      it.ctx = q.ctx;
-      it.all_lo = all_lo;
-      it.all_hi = all_hi;
-      it.pad = 0;
-      a.plan.items[i] = it;
-      a.plan.cum[i] = (it.rows1 ? kPairUnits : kSingleUnits) * it.ktiles + kGroupUnits;
+      it.ktiles = max(1, it.pre_tiles + max(0, (it.any_hi + kNK) / kNK - k0));   // (one at least: its rows are written too)
+      it.pad[0] = it.pad[1] = it.pad[2] = 0;
+      if (lane == 0) {
+        const int cost = (it.rows1 ? kPairUnits : kSingleUnits) * it.ktiles + kGroupUnits;
+        a.plan.items[i] = it;
+        if (costs) s_cost[i] = cost;
+        else a.plan.cum[i] = cost;
+      }
     }
   }
   __syncthreads();
   int64_t total = 0;
   for (int base = 0; base < n_items; base += kPlanThreads) {
-    const int64_t x = base + tid < n_items ? a.plan.cum[base + tid] : 0;
+    const int i = base + tid;
+    const int64_t x = i < n_items ? (costs ? s_cost[i] : a.plan.cum[i]) : 0;
     const int64_t c = block_scan(x, total, scratch);
-    if (base + tid < n_items) a.plan.cum[base + tid] = c;
+    if (i < n_items) a.plan.cum[i] = c;
   }
   if (tid == 0) {
     a.plan.cum[a.plan.most] = total;
@@ -315,123 +381,296 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
   }
 }
 
-// V elements that are not finite, added to the stored result of a row that
-// sees them (they were left out of the products).
+__device__ __forceinline__ float f16_value(uint32_t bits) {
+  float f;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %1;\n\tcvt.f32.f16 %0, x;\n\t}" : "=f"(f) : "r"(bits));
+  return f;
+}
+// Adds them to the stored result of a row that sees them.
 template <int D, bool F8>
-__device__ __noinline__ void add_odd(const ScoreArgs& sa, const Seg& s, KeySpan span, uint16_t* o, float* part) {
+__device__ __noinline__ void add_odd(const ScoreArgs& sa, const Seg& s, KeySpan span, const Odd* list, int count, uint16_t* o,
+                                     float* part) {
   const TreeArgs& a = sa.t;
+  auto add = [&](int d, float v) {
+    if (part) part[d] += v;
+    else o[d] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(o[d]) + v, 0.f) & 0xffffu);
+  };
+  if (count <= kOddMost) {
+    for (int i = 0; i < count; ++i) {
+      const Odd x = list[i];
+      if (x.key < s.prefix || (x.key >= span.lo && x.key <= span.hi))
+        add(x.dim, F8 ? f16_value(x.bits) : bf16lo_to_f32(x.bits));
+    }
+    return;
+  }
+  // Too many to note: the blocks that were cleaned are looked at again.
   const int64_t Hkv = a.pool.num_kv_heads;
   const int32_t* bt = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
-  const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
   for (int j = s.kt0; j < s.kt1; ++j) {
     const int tile = tile_at(j, s.pre_tiles, s.gap);
-    // (A tile that lacks a block was cleaned too, but its rows are all looked at then: see below.)
-    const bool whole = seen_whole(s, tile * kNK);
-    if (whole && !(s.flags & kSegMissing)) continue;
-    bool lacks = false;
-    if (whole) {
-      for (int b = tile * kBlkPerTile; b < min(nblk, (tile + 1) * kBlkPerTile); ++b) {
-        const int pb = __ldg(bt + b);
-        lacks |= pb < 0 || pb >= a.pool.num_blocks;
-      }
-      if (!lacks) continue;
-    }
-    for (int b = tile * kBlkPerTile; b < min(nblk, (tile + 1) * kBlkPerTile); ++b) {
-      const int pb = __ldg(bt + b);
+    const uint32_t dirty = blocks_needed(s, tile * kNK) & ~blocks_whole(s, tile * kNK);
+    for (int x = 0; x < kBlkPerTile; ++x) {
+      if (!((dirty >> x) & 1u)) continue;
+      const int b = tile * kBlkPerTile + x, pb = __ldg(bt + b);
       if (pb < 0 || pb >= a.pool.num_blocks) continue;
       const uint32_t vis = span_bits(s.prefix, span, b * kBlockSize);
       for (int k = 0; k < kBlockSize; ++k) {
         if (!((vis >> k) & 1u)) continue;
         for (int d = 0; d < D; ++d) {
           const float v = pool_v<D, F8>(a.pool, pb * Hkv + s.g, k, d);
-          if (fabsf(v) < CUDART_INF_F) continue;
-          if (part) part[d] += v;
-          else o[d] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(o[d]) + v, 0.f) & 0xffffu);
+          if (!(fabsf(v) < CUDART_INF_F)) add(d, v);
         }
       }
     }
   }
 }
 
-// Int8 pools: a stage's codes, in its upper half, widened in place to bf16 times
-// their block's power of two (lane l holds the exponent of block l % 8); the order
-// of reads and writes is widen_stage's.
-template <int D>
-__device__ __forceinline__ void widen_int8(uint8_t* stage, int lane, int e) {
+// What the widening warps know of a tile: its first key, its blocks as bits
+// (needed; to be cleaned; copied), and in lane l < 8 the exponent of block l.
+struct CodeTile {
+  int exp, key0, ctx, ring;
+  uint32_t store, dirty, there;
+  bool last;   // of the segment
+};
+
+// Whether `mine` holds for all 64 threads of a team: a hardware barrier.  Every one of them comes to it as often as the
+// other, whatever its own waits found: what they do next hangs on the answer alone.
+__device__ __forceinline__ bool team_all(int team, bool mine) {
+  uint32_t all;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.and.pred q, %1, 64, p;\n\t"
+               "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(all) : "r"(team), "r"(mine ? 1u : 0u) : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ void team_sync(int team) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(team) : "memory"); }
+
+// Widening warps, two (w = 0, 1) for K and two for V: blocks w, w + 2, ... of every
+// tile, one after the other (a loop: short code), exponents asked for a tile ahead.
+// The lines of the tile's second half lie over the codes: before they are written
+// both warps have read all of theirs.
+template <int D, int KIND>
+__device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, uint64_t* bars, const Seg* s_seg, int* s_odd,
+                                            Odd* s_oddl, volatile int* s_abort, bool is_v, int w, int lane) {
   using S = TcSmem<D>;
-  constexpr int kGroups = D / 8;              // 8-code groups per key
-  constexpr int kKeysPerStep = 32 / kGroups;  // keys converted per warp step
-  constexpr int kBatch = 16;                  // steps whose codes are loaded together
-  const uint8_t* codes = stage + S::kKV / 2;
-  const int kk = lane / kGroups, g8 = lane % kGroups;
-  const int hf = (g8 * 8) / 64, cw = g8 % 8;
-#pragma unroll 1
-  for (int b = 0; b < kNK / kKeysPerStep; b += kBatch) {
-    uint2 v[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      v[u] = *reinterpret_cast<const uint2*>(codes + ((b + u) * kKeysPerStep + kk) * D + g8 * 8);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int r = (b + u) * kKeysPerStep + kk, r8 = r % 8;
-      const uint32_t f = exp_bf16x2(__shfl_sync(0xffffffffu, e, (b + u) * kKeysPerStep / kBlockSize));
-      uint4 h;
-      int8x4_to_bf16x4(v[u].x, h.x, h.y);
-      int8x4_to_bf16x4(v[u].y, h.z, h.w);
-      h.x = mul_bf16x2(h.x, f);
-      h.y = mul_bf16x2(h.y, f);
-      h.z = mul_bf16x2(h.z, f);
-      h.w = mul_bf16x2(h.w, f);
-      *reinterpret_cast<uint4*>(stage + (r / 8) * S::kGS + hf * S::kHS + r8 * 128 + ((cw ^ r8) * 16)) = h;
+  using B = typename ScoreSmem<D>::B;
+  constexpr int kPer = D / 32;   // 16-byte pieces that a lane has of a block
+  const TreeArgs& a = sa.t;
+  const int Hkv = a.pool.num_kv_heads;
+  Seg sg{};
+  int r = -1, rel = 0, n = 0;                // segment, its next tile of n
+  int ids_cur = -1, ids_next = -1, win = 0;
+  const int32_t* bt_row = nullptr;
+  bool ok = true;
+  // Lane l holds block l of four key tiles, from tile kt0 + 4 from on.
+  auto load_window = [&](int from) -> int {
+    const int j = sg.kt0 + from * 4 + lane / kBlkPerTile;
+    const int b = tile_at(j, sg.pre_tiles, sg.gap) * kBlkPerTile + lane % kBlkPerTile;
+    return j < sg.kt1 && b < (sg.ctx + kBlockSize - 1) / kBlockSize ? __ldg(bt_row + b) : -1;
+  };
+  auto check_window = [&](int pb) -> int { return pb >= 0 && pb < a.pool.num_blocks ? pb : -1; };
+  // The next tile; false: no more (or gave up).
+  auto fetch = [&](CodeTile& t) -> bool {
+    if (rel == n) {
+      ++r;
+      const int slot = r % kSegSlots;
+      if (!(ok = mbar_wait_warp(&bars[B::kSegFull + slot], (r / kSegSlots) & 1, s_abort, a.wait_ns))) return false;
+      sg = s_seg[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B::kSegEmpty + slot]);
+      if (sg.flags & kSegEnd) return false;
+      rel = 0;
+      n = sg.kt1 - sg.kt0;
+      bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
+      win = 0;
+      ids_cur = check_window(load_window(0));
+      ids_next = load_window(1);
     }
-  }
-}
-
-// (x0, x1) *= Q(x^2) element by element, in paired fp32 operations.
-__device__ __forceinline__ void cap2(float& x0, float& x1, const float (&q)[5]) {
-  asm("{\n\t.reg .b64 p, z, r, k;\n\tmov.b64 p, {%0, %1};\n\tmul.rn.f32x2 z, p, p;\n\tmov.b64 r, {%6, %6};\n\t"
-      "mov.b64 k, {%5, %5};\n\tfma.rn.f32x2 r, r, z, k;\n\tmov.b64 k, {%4, %4};\n\tfma.rn.f32x2 r, r, z, k;\n\t"
-      "mov.b64 k, {%3, %3};\n\tfma.rn.f32x2 r, r, z, k;\n\tmov.b64 k, {%2, %2};\n\tfma.rn.f32x2 r, r, z, k;\n\t"
-      "mul.rn.f32x2 p, p, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "+f"(x0), "+f"(x1) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]));
-}
-
-// A row's raw products with 128 keys to scores in log2 units; dpos: its position less the first key.
-__device__ __forceinline__ void modify_scores(float (&s)[kNK], const ScoreArgs& a, float slope, int dpos) {
-  if (a.cap_out != 0.f) {
-    float top[4] = {0.f, 0.f, 0.f, 0.f};
+    if ((rel >> 2) > win) {
+      ++win;
+      ids_cur = check_window(ids_next);
+      ids_next = load_window(win + 1);
+    }
+    t.key0 = tile_at(sg.kt0 + rel, sg.pre_tiles, sg.gap) * kNK;
+    t.ctx = sg.ctx;
+    t.ring = r % kSegRing;
+    t.store = blocks_needed(sg, t.key0);
+    t.dirty = is_v ? t.store & ~blocks_whole(sg, t.key0) : 0u;
+    const int pb = __shfl_sync(0xffffffffu, ids_cur, (rel & 3) * kBlkPerTile + (lane & 7));
+    const bool has = lane < kBlkPerTile && ((t.store >> lane) & 1u) && pb >= 0;
+    t.there = __ballot_sync(0xffffffffu, has);
+    t.exp = 0;
+    if (KIND == kPoolInt8 && has)   // (the kernel ahead may have written them)
+      t.exp = (is_v ? a.pool.v_exps : a.pool.k_exps)[static_cast<int64_t>(pb) * Hkv + sg.g];
+    t.last = ++rel == n;
+    return true;
+  };
+  const int team = is_v ? 2 : 1, nst = is_v ? S::kVSt : S::kKSt;
+  const int bar_landed = is_v ? B::kVLanded : B::kKLanded, bar_full = is_v ? B::kVFull : B::kKFull;
+  CodeTile next{};
+  bool more = fetch(next);
+  for (int cnt = 0;; ++cnt) {
+    // Once a tile, and once behind the last, both warps come here and leave by what they hold in common: one whose wait
+    // ran out (it may not know whether there is a tile) takes the other along.
+    const CodeTile t = next;
+    const int st = cnt % nst;
+    uint8_t* const stage = smem + (is_v ? S::kOffV : S::kOffK) + st * S::kKV;
+    if (ok && more) ok = mbar_wait_warp(&bars[bar_landed + st], (cnt / nst) & 1, s_abort, a.wait_ns);
+    if (!team_all(team, ok)) return false;
+    if (!more) return true;
+    auto load = [&](int b, uint4 (&v)[kPer]) {
+      const bool there = (t.there >> b) & 1u;
 #pragma unroll
-    for (int c = 0; c < kNK; c += 2) top[(c >> 1) & 3] = max3f(top[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
-    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    if (!__any_sync(0xffffffffu, !(most < a.cap_small))) {
+      for (int u = 0; u < kPer; ++u)    // (a block that is not there becomes zero)
+        v[u] = there ? *reinterpret_cast<const uint4*>(stage + S::kKV / 2 + b * (kBlockSize * D) + (u * 32 + lane) * 16)
+                     : make_uint4(0, 0, 0, 0);
+    };
+    uint4 v[kPer], v4[kPer], v6[kPer];
+    load(w, v);
+    more = fetch(next);
+#pragma unroll 1
+    for (int b = w; b < kBlkPerTile; b += 2) {
+      if (b >= 4) {
+        if (b < 6) team_sync(team);
 #pragma unroll
-      for (int c = 0; c < kNK; c += 2) cap2(s[c], s[c + 1], a.cap_q);
-    } else {
+        for (int u = 0; u < kPer; ++u) v[u] = b < 6 ? v4[u] : v6[u];
+      } else if (b >= 2) {
+        load(w + 2, v);
+        load(w + 4, v4);
+        load(w + 6, v6);
+      }
+      if (!((t.store >> b) & 1u)) continue;
+      const uint32_t f = exp_bf16x2(safe_exp(__shfl_sync(0xffffffffu, t.exp, b)));
+      const bool clean = KIND == kPoolFp8 && ((t.dirty >> b) & 1u);
 #pragma unroll
-      for (int c = 0; c < kNK; ++c) {
-        const float y = s[c] * a.base;
-        s[c] = a.cap_out * (fabsf(y) < 0.5f ? tanh_small(y) : tanh_large(y));
+      for (int u = 0; u < kPer; ++u) {
+        const int at = u * 32 + lane, key = b * kBlockSize + at / (D / 16), c16 = at % (D / 16);
+        const uint32_t c[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (KIND == kPoolInt8) {
+            int8x4_to_bf16x4(c[k], o[2 * k], o[2 * k + 1]);
+            o[2 * k] = mul_bf16x2(o[2 * k], f);
+            o[2 * k + 1] = mul_bf16x2(o[2 * k + 1], f);
+          } else {
+            e4m3x4_to_f16x4(c[k], o[2 * k], o[2 * k + 1]);
+          }
+        }
+        if (clean) {   // codes that are NaN, and what lies behind the context
+          uint32_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) bad |= ((o[k] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+          if (bad) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t h = (o[k] >> (16 * e)) & 0xffffu;
+                if ((h & 0x7c00u) != 0x7c00u) continue;
+                o[k] &= e ? 0x0000ffffu : 0xffff0000u;
+                if (t.key0 + key >= t.ctx) continue;
+                const int nth = atomicAdd(&s_odd[t.ring], 1);
+                if (nth < kOddMost)
+                  s_oddl[t.ring * kOddMost + nth] = Odd{t.key0 + key, static_cast<uint16_t>(c16 * 16 + 2 * k + e), static_cast<uint16_t>(h)};
+              }
+            }
+          }
+        }
+        // Chunks 2 c16 and 2 c16 + 1 of the key's 128-byte lines (swizzled); lanes of the second half of a 256-byte
+        // row store the odd one first, so that eight lanes meet eight banks.
+        const int hf = (2 * c16) / 8, cw = (2 * c16) % 8, r8 = key % 8;
+        uint8_t* line = stage + (key / 8) * S::kGS + hf * S::kHS + r8 * 128;
+        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(line + (((cw + hf) ^ r8) * 16)) = hf ? hi : lo;
+        *reinterpret_cast<uint4*>(line + (((cw + 1 - hf) ^ r8) * 16)) = hf ? lo : hi;
       }
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < kNK; ++c) s[c] *= a.base;
-  }
-  if (a.slopes) {
-    if (__all_sync(0xffffffffu, dpos >= kNK - 1)) {   // every key at or before the position
-      const float b = -slope * static_cast<float>(dpos);
-#pragma unroll
-      for (int c = 0; c < kNK; ++c) s[c] += fmaf(slope, static_cast<float>(c), b);
-    } else {
-      const float d = static_cast<float>(dpos);
-#pragma unroll
-      for (int c = 0; c < kNK; ++c) s[c] = fmaf(-slope, fabsf(d - static_cast<float>(c)), s[c]);
+    fence_proxy_async_smem();   // read by the tensor cores
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bars[bar_full + st]);
+      if (is_v && t.last) mbar_arrive(&bars[B::kVDone + t.ring]);
     }
+    __syncwarp();
   }
+}
+
+// (x0, x1) *= q0 + q1 x^2 + q2 x^4 + q3 x^6 element by element, in paired fp32 operations.
+__device__ __forceinline__ void cap2(float& x0, float& x1, const float (&q)[4]) {
+  asm("{\n\t.reg .b64 p, z, r, k;\n\tmov.b64 p, {%0, %1};\n\tmul.rn.f32x2 z, p, p;\n\tmov.b64 r, {%5, %5};\n\t"
+      "mov.b64 k, {%4, %4};\n\tfma.rn.f32x2 r, r, z, k;\n\tmov.b64 k, {%3, %3};\n\tfma.rn.f32x2 r, r, z, k;\n\t"
+      "mov.b64 k, {%2, %2};\n\tfma.rn.f32x2 r, r, z, k;\n\tmul.rn.f32x2 p, p, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x0), "+f"(x1) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
+}
+// (x0, x1) = (x0, x1) * f + (b0, b1).
+__device__ __forceinline__ void fma2v(float& x0, float& x1, float f, float b0, float b1) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x0), "+f"(x1) : "f"(f), "f"(b0), "f"(b1));
+}
+
+// One row's scores of 32 keys in TMEM, to or from registers (tmem_wait_ld / tmem_wait_st follow).
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+  tmem_ld16(at, v);
+  tmem_ld16(at + 16, v + 16);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
+  tmem_st16(at, v);
+  tmem_st16(at + 16, v + 16);
+}
+
+// Waits for the thread's loads from TMEM; what uses v comes behind it.
+__device__ __forceinline__ void tmem_wait_ld32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :: "memory");
+}
+
+// The general way to a row's scores: 32 keys at a time from TMEM, modified (to log2 units), masked, and back; dpos: the
+// row's position less the tile's first key, vis(c): the keys c .. c + 31 that it sees (none for a row that is not the
+// segment's: what the others take must not hang on it).
+template <bool MOD, class V>
+__device__ __forceinline__ void rewrite_scores(uint32_t at_s, const ScoreArgs& a, float slope, int dpos, bool valid, V&& vis) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < kNK; c0 += 32) {
+    float s[32];
+    tmem_ld32(at_s + c0, s);
+    tmem_wait_ld32(s);
+    const uint32_t v = vis(c0);
+    if constexpr (MOD) {
+      if (a.cap_out != 0.f) {
+        float top[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if ((v >> c) & 1u) top[c & 1] = fmaxf(top[c & 1], fabsf(s[c]));
+        if (__any_sync(0xffffffffu, valid && !(fmaxf(top[0], top[1]) < a.cap_small))) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = a.cap_out * tanh_any(s[c] * a.base);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) cap2(s[c], s[c + 1], a.cap_q);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] *= a.base;
+      }
+      if (a.slopes) {
+        const float d = static_cast<float>(dpos - c0);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(d - static_cast<float>(c)), s[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = (v >> c) & 1u ? s[c] : -CUDART_INF_F;
+    tmem_st32(at_s + c0, s);
+  }
+  tmem_wait_st();
 }
 
 template <int D, int KIND, bool MOD>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<KIND>, 1)
 score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                const __grid_constant__ CUtensorMap tmap_q) {
   constexpr bool F8 = KIND == kPoolFp8;            // f16 operands
@@ -455,7 +694,8 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   float2* s_ml = reinterpret_cast<float2*>(smem + M::kOffMl);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + M::kOffMisc + 8);
-  volatile int* s_odd = reinterpret_cast<volatile int*>(smem + M::kOffMisc + 16);   // [kSegRing]
+  int* s_odd = reinterpret_cast<int*>(smem + M::kOffMisc + 16);   // [kSegRing]: how many of a segment
+  Odd* s_oddl = reinterpret_cast<Odd*>(smem + M::kOffOdd);
   Seg* s_seg = reinterpret_cast<Seg*>(smem + M::kOffSeg);   // [kSegSlots]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -464,12 +704,12 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   if (!walk.begin(sa)) return;   // block-uniform
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKSt; ++i) {
-      mbar_init(&bars[B::kKFull + i], 1);
+      mbar_init(&bars[B::kKFull + i], kCodes ? 2 : 1);
       mbar_init(&bars[B::kKEmpty + i], 1);
       mbar_init(&bars[B::kKLanded + i], 1);
     }
     for (int i = 0; i < kVSt; ++i) {
-      mbar_init(&bars[B::kVFull + i], 1);
+      mbar_init(&bars[B::kVFull + i], kCodes ? 2 : 1);
       mbar_init(&bars[B::kVEmpty + i], 1);
       mbar_init(&bars[B::kVLanded + i], 1);
     }
@@ -484,10 +724,10 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
     mbar_init(&bars[B::kMl], 128);
     mbar_init(&bars[B::kJoined], 128);
     mbar_init(&bars[B::kDrain], 1);
-    for (int i = 0; i < kSegRing; ++i) mbar_init(&bars[B::kVDone + i], 1);
+    for (int i = 0; i < kSegRing; ++i) mbar_init(&bars[B::kVDone + i], kCodes ? 2 : 1);
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&bars[B::kSegFull + i], 1);
-      mbar_init(&bars[B::kSegEmpty + i], kSegReaders);
+      mbar_init(&bars[B::kSegEmpty + i], kSegReaders<KIND>);
     }
     *s_abort = 0;
     fence_mbar_init();
@@ -521,8 +761,22 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
     return (sg.flags & kSegEnd) == 0;
   };
 
+  // Registers: 384 x 168 (codes: 512 x 128) at the launch; the softmax warps' come from the others.
+  if (warp >= 12) {
+    // ------------------------------------------------------------ widening of codes
+    if constexpr (kCodes) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      ok = widen_codes<D, KIND>(sa, smem, bars, s_seg, s_odd, s_oddl, s_abort, warp >= 14, warp & 1, lane);
+      if (!ok) {
+        if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+        *s_abort = 1;
+      }
+    }
+  } else if (warp >= 8) {
+  if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 8 || warp == 10) {
-    // ------------------------------------------------------------ producers: warp 8 K (and Q), warp 10 V
+    // ------------------------------------------------------------ producers: warp 8 Q (and K), warp 10 V
     const bool is_k = warp == 8;
     const int nst = is_k ? kKSt : kVSt;
     uint8_t* const stages = smem + (is_k ? S::kOffK : S::kOffV);
@@ -530,7 +784,6 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
     const int bar_landed = is_k ? B::kKLanded : B::kVLanded;
     const CUtensorMap* const tm = is_k ? &tmap_k : &tmap_v;
     int cnt = 0;      // tiles issued in the launch
-    int fin = 0;      // FP8: tiles widened and handed over
     int nq = 0;       // segments whose query tiles have been issued
     uint32_t landed_par = 0;
     for (int r = 0; ok && take(r); ++r) {
@@ -565,71 +818,67 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       auto check_window = [&](int pb) -> int { return pb >= 0 && pb < a.pool.num_blocks ? pb : -1; };
       int win = 0;
       int ids_cur = check_window(load_window(0)), ids_next = load_window(1);
-      // Int8: the window's exponents, asked for a window ahead (the kernel ahead may have written them).
-      auto load_exps = [&](int pb) -> int {
-        if (KIND != kPoolInt8 || pb < 0) return 0;
-        return safe_exp((is_k ? a.pool.k_exps : a.pool.v_exps)[static_cast<int64_t>(pb) * Hkv + sg.g]);
-      };
-      int exps_cur = load_exps(ids_cur), exps_next = 0;
-      if constexpr (KIND == kPoolInt8) {
-        ids_next = check_window(ids_next);
-        exps_next = load_exps(ids_next);
-      }
-      // Lane l < 8: chunk index of key tile j's block l, or -1, and its exponent.
-      int exp_at = 0;
+      // Lane l < 8: chunk index of key tile j's block l, or -1.
       auto block_chunk = [&](int j) -> int {
         const int rel = j - sg.kt0;
         if ((rel >> 2) != win) {
           win = rel >> 2;
           ids_cur = check_window(ids_next);
           ids_next = load_window(win + 1);
-          if constexpr (KIND == kPoolInt8) {
-            exps_cur = exps_next;
-            ids_next = check_window(ids_next);
-            exps_next = load_exps(ids_next);
-          }
         }
-        const int src = (rel & 3) * kBlkPerTile + (lane & 7);
-        const int pb = __shfl_sync(0xffffffffu, ids_cur, src);
-        if constexpr (KIND == kPoolInt8) exp_at = __shfl_sync(0xffffffffu, exps_cur, src);
-        return lane < kBlkPerTile && pb >= 0 ? pb * Hkv + sg.g : -1;
+        const int pb = __shfl_sync(0xffffffffu, ids_cur, (rel & 3) * kBlkPerTile + (lane & 7));
+        const uint32_t need = blocks_needed(sg, tile_at(j, sg.pre_tiles, sg.gap) * kNK);
+        return lane < kBlkPerTile && ((need >> lane) & 1u) && pb >= 0 ? pb * Hkv + sg.g : -1;
       };
-      int seg_odd = 0;
-      // V tiles that some row does not see whole: clear the rows without a key
-      // (past the context, or of a block that is not there) and elements that are
-      // not finite.  have: blocks that were copied.
-      auto clean_v = [&](uint8_t* stage, int j, uint32_t have) {
-        constexpr int kCh = S::kHalves * 8;   // 16-byte chunks of a key's row
-        const int ch = lane % kCh;
-        uint8_t* col = stage + (ch / 8) * S::kHS;
-        const int live = sg.ctx - tile_at(j, sg.pre_tiles, sg.gap) * kNK;
-        bool odd = false;
-#pragma unroll 4
-        for (int key = lane / kCh; key < kNK; key += 32 / kCh) {
-          uint4* p = reinterpret_cast<uint4*>(col + (key / 8) * S::kGS + (key % 8) * 128 + (((ch % 8) ^ (key % 8)) * 16));
-          if (key >= live || !((have >> (key / kBlockSize)) & 1u)) {
-            *p = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 v = *p;
-          bool any = false;
-          v.x = finite_pair<F8>(v.x, any);
-          v.y = finite_pair<F8>(v.y, any);
-          v.z = finite_pair<F8>(v.z, any);
-          v.w = finite_pair<F8>(v.w, any);
-          if (any) {
-            *p = v;
-            odd = true;
-          }
-        }
-        if (__any_sync(0xffffffffu, odd)) seg_odd = 1;
-      };
-      // Which tiles need it: those that some row does not see whole, or that lack a block.
-      auto needs_clean = [&](int j, uint32_t have) {
+      // V blocks that some row does not see whole: cleared of what they hold behind
+      // the context, and of elements that are not finite, which are noted; blocks that
+      // are not there (copied: have) become zero.  A lane has the 16-byte pieces
+      // lane, lane + 32, ... of a block's rows, eight (four) loads under way.
+      auto dirty_blocks = [&](int j, uint32_t have) -> uint32_t {
         const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
-        return have != 0xffu || !seen_whole(sg, key0);
+        return blocks_needed(sg, key0) & ~(blocks_whole(sg, key0) & have);
       };
-      if constexpr (!kCodes) {
+      auto clean_v = [&](uint8_t* stage, int j, uint32_t have) {
+        constexpr int kCh = S::kHalves * 8;   // 16-byte pieces of a key's row
+        constexpr int kIt = kBlockSize * kCh / 32;
+        const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
+        const int ch = lane % kCh;
+        for (uint32_t left = dirty_blocks(j, have); left; left &= left - 1) {
+          const int b = __ffs(left) - 1;
+          const bool there = (have >> b) & 1u;
+          uint4* p[kIt];
+          uint4 v[kIt];
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) {
+            const int key = b * kBlockSize + (lane + 32 * i) / kCh;
+            p[i] = reinterpret_cast<uint4*>(stage + (key / 8) * S::kGS + (ch / 8) * S::kHS + (key % 8) * 128 +
+                                            (((ch % 8) ^ (key % 8)) * 16));
+            v[i] = there ? *p[i] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) {
+            const int key = key0 + b * kBlockSize + (lane + 32 * i) / kCh;
+            if (!there || key >= sg.ctx) {
+              *p[i] = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            // An exponent of ones carries into the sign's place.
+            constexpr uint32_t kExp = F8 ? 0x7c007c00u : 0x7f807f80u, kOne = F8 ? 0x04000400u : 0x00800080u;
+            const uint32_t bad = (((v[i].x & kExp) + kOne) | ((v[i].y & kExp) + kOne) | ((v[i].z & kExp) + kOne) |
+                                  ((v[i].w & kExp) + kOne)) & 0x80008000u;
+            if (!bad) continue;
+            uint16_t h[8];
+            *reinterpret_cast<uint4*>(h) = v[i];
+            for (int e = 0; e < 8; ++e) {
+              if ((h[e] & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
+              const int n = atomicAdd(&s_odd[r % kSegRing], 1);
+              if (n < kOddMost) s_oddl[(r % kSegRing) * kOddMost + n] = Odd{key, static_cast<uint16_t>(ch * 8 + e), h[e]};
+              h[e] = 0;
+            }
+            *p[i] = *reinterpret_cast<uint4*>(h);
+          }
+        }
+      };
         for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
           const int y = block_chunk(j);
           const int st = cnt % nst;
@@ -637,14 +886,14 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
           // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
           if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
-          const bool clean = !is_k && needs_clean(j, have);
-          uint64_t* bar = &bars[(clean ? bar_landed : bar_full) + st];
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (S::kHalves * kBlockSize * 128));
+          const bool clean = !kCodes && !is_k && dirty_blocks(j, have) != 0;
+          uint64_t* bar = &bars[(clean || kCodes ? bar_landed : bar_full) + st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D * (kCodes ? 1 : 2)));
           __syncwarp();
           uint8_t* stage = stages + st * S::kKV;
           if (y >= 0) {
-            if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
+            if constexpr (kCodes) tma_load_2d(stage + S::kKV / 2 + lane * (kBlockSize * D), tm, 0, y * kBlockSize, bar);
+            else if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
             else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
           }
           if (clean) {
@@ -662,76 +911,17 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           }
         }
         if (!ok) break;
-      } else {
-        // Codes land in the upper half of a stage and are widened in place; a
-        // copy is issued as soon as a stage is free and widened as soon as it
-        // has landed, whichever is ready.
-        int jl = sg.kt0, jw = sg.kt0;
-        uint32_t have_ring = 0;   // blocks copied, 8 bits per stage (at most four stages)
-        uint32_t exp_ring = 0;    // int8, lane l < 8: exponents of block l, likewise
-        uint64_t idle0 = 0;
-        while (jw < sg.kt1) {
-          bool moved = false;
-          if (jl < sg.kt1 && cnt - fin < nst && mbar_test_warp(&bars[bar_empty + cnt % nst], ((cnt / nst) & 1) ^ 1)) {
-            const int y = block_chunk(jl), st = cnt % nst;
-            const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
-            have_ring = (have_ring & ~(0xffu << (8 * st))) | (have << (8 * st));
-            if constexpr (KIND == kPoolInt8)
-              exp_ring = (exp_ring & ~(0xffu << (8 * st))) | ((static_cast<uint32_t>(exp_at) & 0xffu) << (8 * st));
-            uint64_t* bar = &bars[bar_landed + st];
-            const bool withheld = a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0;   // test hook (above)
-            if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D));
-            __syncwarp();
-            if (y >= 0 && !withheld)
-              tma_load_2d(stages + st * S::kKV + S::kKV / 2 + lane * (kBlockSize * D), tm, 0, y * kBlockSize, bar);
-            ++cnt;
-            ++jl;
-            moved = true;
-          }
-          if (fin < cnt && mbar_test_warp(&bars[bar_landed + fin % nst], (fin / nst) & 1)) {
-            const int st = fin % nst;
-            uint8_t* stage = stages + st * S::kKV;
-            const uint32_t have = (have_ring >> (8 * st)) & 0xffu;
-            if constexpr (KIND == kPoolInt8) widen_int8<D>(stage, lane, static_cast<int8_t>((exp_ring >> (8 * st)) & 0xffu));
-            else widen_stage<D>(stage, lane);
-            if (KIND != kPoolInt8 && !is_k && needs_clean(jw, have)) {
-              __syncwarp();
-              clean_v(stage, jw, have);
-            }
-            fence_proxy_async_smem();   // read by the tensor cores
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[bar_full + st]);
-            ++fin;
-            ++jw;
-            moved = true;
-          }
-          if (moved) {
-            idle0 = 0;
-          } else {
-            const uint64_t now = globaltimer_ns();
-            if (idle0 == 0) idle0 = now;
-            if (__any_sync(0xffffffffu, *s_abort != 0 || now - idle0 > a.wait_ns)) {
-              ok = false;
-              break;
-            }
-          }
-        }
+      if constexpr (!kCodes) {
+        __syncwarp();   // the notes are written
+        if (!is_k && lane == 0) mbar_arrive(&bars[B::kVDone + r % kSegRing]);
+        __syncwarp();
       }
-      if (ok && !is_k && lane == 0) {
-        s_odd[r % kSegRing] = seg_odd;
-        mbar_arrive(&bars[B::kVDone + r % kSegRing]);
-      }
-      __syncwarp();
     }
     if (!ok) {   // gave up: flag it and let copies already issued land
       if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
       *s_abort = 1;
-      if constexpr (kCodes) {
-        for (int i = fin; i < cnt; ++i) (void)mbar_wait(&bars[bar_landed + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
-      } else {
-        for (int i = max(0, cnt - nst); i < cnt; ++i)
-          (void)mbar_wait(&bars[bar_full + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
-      }
+      for (int i = max(0, cnt - nst); i < cnt; ++i)
+        (void)mbar_wait(&bars[(kCodes ? bar_landed : bar_full) + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
       if (is_k && nq > 0) {
         for (int t = 0; t < 2; ++t) (void)mbar_wait(&bars[B::kQFull + t], (nq - 1) & 1, nullptr, a.wait_ns);
       }
@@ -758,11 +948,26 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       release(B::kS + t);
     };
     // O of group t (+)= P V
-    auto issue_pv = [&](int t, bool acc, uint64_t vd) {
+    // (of the tile's blocks that some row sees; acc: O has products of the segment)
+    bool acc0 = false, acc1 = false;
+    auto issue_pv = [&](int t, int j, uint64_t vd) {
+      const uint32_t need = blocks_needed(sg, tile_at(sg.kt0 + j, sg.pre_tiles, sg.gap) * kNK);
+      bool acc = t ? acc1 : acc0;
+      if (need == 0xffu) {
 #pragma unroll
-      for (int ks = 0; ks < kNK / 16; ++ks)
-        tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
-                       vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, (acc || ks > 0) ? 1u : 0u);
+        for (int ks = 0; ks < kNK / 16; ++ks)
+          tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
+                         vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, (acc || ks > 0) ? 1u : 0u);
+        acc = true;
+      } else {
+        for (int ks = 0; ks < kNK / 16; ++ks) {
+          if (!((need >> ks) & 1u)) continue;
+          tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
+                         vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, acc ? 1u : 0u);
+          acc = true;
+        }
+      }
+      if (t) acc1 = acc; else acc0 = acc;
     };
     constexpr int kQReady = F8 ? B::kQc : B::kQFull;
     int kc = 0, vc = 0;          // K / V tiles consumed
@@ -776,6 +981,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
     };
     for (int r = 0; ok && take(r); ++r) {
       const int n = sg.kt1 - sg.kt0;   // >= 1
+      acc0 = acc1 = false;
       if (!(ok = mbar_wait_warp(&bars[kQReady], r & 1, s_abort, a.wait_ns) &&
                  mbar_wait_warp(&bars[kQReady + 1], r & 1, s_abort, a.wait_ns)))
         break;
@@ -798,7 +1004,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           for (int t = 0; t < 2; ++t) {
             if (!(ok = wait_p(t))) break;
             tc_fence_after();
-            issue_pv(t, j > 0, vd);
+            issue_pv(t, j, vd);
             if (j == n - 1) release(B::kPv + t);
             if (j + 1 < n) {
               if (t == 0 && !(ok = wait_k())) break;
@@ -829,7 +1035,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           const int t = j & 1;
           if (!(ok = wait_v() && wait_p(t))) break;
           tc_fence_after();
-          if (t) issue_pv(1, j > 1, v_desc(vc)); else issue_pv(0, j > 1, v_desc(vc));
+          if (t) issue_pv(1, j, v_desc(vc)); else issue_pv(0, j, v_desc(vc));
           if (j + 2 >= n) release(B::kPv + t);
           release(B::kVEmpty + vc % kVSt);
           ++vc;
@@ -879,6 +1085,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       const int slot = r % kSegSlots;
       if (!(ok = mbar_wait_warp(&bars[B::kSegEmpty + slot], ((r / kSegSlots) & 1) ^ 1, s_abort, a.wait_ns))) break;
       if (lane == 0) {
+        s_odd[r % kSegRing] = 0;   // (segment r - kSegRing is long done)
         s_seg[slot] = s;
         mbar_arrive(&bars[B::kSegFull + slot]);
       }
@@ -889,8 +1096,11 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
       *s_abort = 1;
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax / epilogue of group X
+    if constexpr (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int X = (warp >> 2) & 1;
     const int row = threadIdx.x & 127;        // row within the tile (TMEM lane)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -905,8 +1115,9 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       const int tok = X && !single ? sg.tok1 : sg.tok0;
       const bool valid = row < nrows;
       const int t_row = tok + (valid ? row / G : 0);
-      const KeySpan span = key_span(sa, t_row, sg.ctx);
-      const int pos = MOD ? max(__ldg(a.positions + t_row), -1) : 0;
+      // (asked for here, waited for where a tile is not seen whole)
+      const int raw_pos = __ldg(a.positions + t_row), raw_first = sa.first_keys ? __ldg(sa.first_keys + t_row) : 0;
+      const int pos = max(raw_pos, -1);
       float slope = 0.f;   // log2 units
       if (MOD && sa.slopes) slope = sa.slopes[g * G + row % G] * 1.4426950408889634f;
       const int step = single ? 2 : 1;
@@ -956,28 +1167,55 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         if (any_missing && rel > 0 && (rel & 3) < step) missing = missing_of(rel >> 2);
         const uint32_t gone = (missing >> ((rel & 3) * kBlkPerTile)) & 0xffu;
         const bool masked = gone != 0 || !seen_whole(sg, key0);
-        uint32_t vis[4];
-        if (masked) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            vis[w] = span_bits(sg.prefix, span, key0 + 32 * w);
-            if ((gone >> (2 * w)) & 1u) vis[w] &= 0xffff0000u;
-            if ((gone >> (2 * w)) & 2u) vis[w] &= 0x0000ffffu;
-          }
-        }
+        const KeySpan span = masked ? key_span(sa, raw_pos, raw_first, sg.ctx) : KeySpan{0, -1};
         if (!(ok = mbar_wait_warp(&bars[B::kS + X], sc & 1, s_abort, a.wait_ns))) break;
         ++sc;
         tc_fence_after();
+        // A tile that every row sees whole, and whose scores take the short way, is done in registers.  The others
+        // are first rewritten in TMEM by a loop: unrolled for 128 keys its code would drive the rest out of the
+        // instruction cache (warps, the neighbouring SM's too, then waited two steps' time at each such tile).
+        const uint32_t at_s = tmem + lane_base + colS;
+        const int dpos = pos - key0;
+        const bool sloped = MOD && sa.slopes != nullptr;
+        bool general = masked || (sloped && !__all_sync(0xffffffffu, dpos >= kNK - 1));
         float s[kNK];
+        auto load = [&] {
 #pragma unroll
-        for (int c = 0; c < kNK; c += 16) tmem_ld16(tmem + lane_base + colS + c, s + c);
-        tmem_wait_ld();
-        if constexpr (MOD) modify_scores(s, sa, slope, pos - key0);
-        if (masked) {
+          for (int c = 0; c < kNK; c += 16) tmem_ld16(at_s + c, s + c);
+          tmem_wait_ld();
+        };
+        if (!general) {
+          load();
+          if (MOD && sa.cap_out != 0.f) {
+            // (rows that are not the segment's have no say)
+            float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
+            for (int c = 0; c < kNK; c += 2) top[(c >> 1) & 3] = max3f(top[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
+            const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            general = __any_sync(0xffffffffu, valid && !(most < sa.cap_small));
+          }
+        }
+        if (general) {
+          rewrite_scores<MOD>(at_s, sa, slope, dpos, valid, [&](int c0) {
+            if (!masked) return 0xffffffffu;
+            uint32_t v = span_bits(sg.prefix, span, key0 + c0);
+            const uint32_t lost = gone >> (c0 / kBlockSize);
+            if (lost & 1u) v &= 0xffff0000u;
+            if (lost & 2u) v &= 0x0000ffffu;
+            return v;
+          });
+          load();
+        } else if constexpr (MOD) {
+          if (sa.cap_out != 0.f) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[32 * w + c] = (vis[w] >> c) & 1u ? s[32 * w + c] : -CUDART_INF_F;
+            for (int c = 0; c < kNK; c += 2) cap2(s[c], s[c + 1], sa.cap_q);
+          }
+          if (sloped) {   // - slope (dpos - c), every key at or before the position
+            const float b = -slope * static_cast<float>(dpos), f = sa.cap_out != 0.f ? 1.f : sa.base;
+#pragma unroll
+            for (int c = 0; c < kNK; c += 2)
+              fma2v(s[c], s[c + 1], f, fmaf(slope, static_cast<float>(c), b), fmaf(slope, static_cast<float>(c + 1), b));
+          }
         }
         float mx8[8];
 #pragma unroll
@@ -1005,21 +1243,19 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
             add2(rs0[(c >> 1) & 3], rs1[(c >> 1) & 3], p0, p1);
             pk[(c - cc) / 2] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
-          tmem_st16(tmem + lane_base + colS + cc / 2, reinterpret_cast<const float*>(pk));
+          tmem_st16(at_s + cc / 2, reinterpret_cast<const float*>(pk));
         }
         const float rsum = ((rs0[0] + rs1[0]) + (rs0[1] + rs1[1])) + ((rs0[2] + rs1[2]) + (rs0[3] + rs1[3]));
         const float alpha = grow && m != -CUDART_INF_F ? fast_exp2(m + neg_m) : 1.f;
         if (grow && i > 0) {   // O is complete: S was issued after the group's previous PV
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
-            tmem_ld16(tmem + lane_base + colO + c, o);
-            tmem_ld16(tmem + lane_base + colO + c + 16, o + 16);
-            tmem_wait_ld();
+            tmem_ld32(tmem + lane_base + colO + c, o);
+            tmem_wait_ld32(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tmem_st16(tmem + lane_base + colO + c, o);
-            tmem_st16(tmem + lane_base + colO + c + 16, o + 16);
+            tmem_st32(tmem + lane_base + colO + c, o);
           }
         }
         l = l * alpha + rsum;
@@ -1075,11 +1311,10 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       const int64_t orow = static_cast<int64_t>(t_row) * a.num_q_heads + h;
       uint4* dst_o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * D);
       float4* dst_p = reinterpret_cast<float4*>(a.part_o + prow * D);
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float ob[32];
-        tmem_ld16(tmem + lane_base + colO + c0, ob);
-        tmem_ld16(tmem + lane_base + colO + c0 + 16, ob + 16);
+        tmem_ld32(tmem + lane_base + colO + c0, ob);
         if (join) {   // warp-uniform
           float oc[32];
           tmem_ld16(tmem + lane_base + kColO + 128 + c0, oc);
@@ -1137,8 +1372,10 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         }
       }
       if (!(ok = mbar_wait_warp(&bars[B::kVDone + r % kSegRing], (r / kSegRing) & 1, s_abort, a.wait_ns))) break;
-      if (s_odd[r % kSegRing] && valid)
-        add_odd<D, F8>(sa, sg, span, static_cast<uint16_t*>(a.o) + orow * D, whole ? nullptr : a.part_o + prow * D);
+      const int odd = s_odd[r % kSegRing];
+      if (odd && valid)
+        add_odd<D, F8>(sa, sg, key_span(sa, raw_pos, raw_first, sg.ctx), s_oddl + (r % kSegRing) * kOddMost, odd,
+                       static_cast<uint16_t*>(a.o) + orow * D, whole ? nullptr : a.part_o + prow * D);
     }
     if (!ok) {
       if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
@@ -1158,7 +1395,7 @@ int launch_m(const ScoreArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, c
   const int smem = ScoreSmem<D>::kTotal;
   const cudaError_t e = smem_attr_once<score_tc_kernel<D, KIND, MOD>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(score_tc_kernel<D, KIND, MOD>, dim3(a.t.ctas), kThreads, smem, s, a, *tk, *tv, *tq);
+  return launch_dependent(score_tc_kernel<D, KIND, MOD>, dim3(a.t.ctas), kThreads<KIND>, smem, s, a, *tk, *tv, *tq);
 }
 template <int D, int KIND>
 int launch_k(const ScoreArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* tq, cudaStream_t s) {
