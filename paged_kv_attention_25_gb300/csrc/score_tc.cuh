@@ -594,13 +594,24 @@ __device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, 
   }
 }
 
-// (x0, x1) *= q0 + q1 x^2 + q2 x^4 + q3 x^6 element by element, in paired fp32 operations.
-__device__ __forceinline__ void cap2(float& x0, float& x1, const float (&q)[4]) {
-  asm("{\n\t.reg .b64 p, z, r, k;\n\tmov.b64 p, {%0, %1};\n\tmul.rn.f32x2 z, p, p;\n\tmov.b64 r, {%5, %5};\n\t"
-      "mov.b64 k, {%4, %4};\n\tfma.rn.f32x2 r, r, z, k;\n\tmov.b64 k, {%3, %3};\n\tfma.rn.f32x2 r, r, z, k;\n\t"
-      "mov.b64 k, {%2, %2};\n\tfma.rn.f32x2 r, r, z, k;\n\tmul.rn.f32x2 p, p, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "+f"(x0), "+f"(x1) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
 }
+// (x0, x1) *= q0 + q1 x^2 + q2 x^4 + q3 x^6 element by element, in paired fp32 operations (q: each coefficient twice).
+__device__ __forceinline__ void cap2(float& x0, float& x1, const uint64_t (&q)[4]) {
+  asm("{\n\t.reg .b64 p, z, r;\n\tmov.b64 p, {%0, %1};\n\tmul.rn.f32x2 z, p, p;\n\tfma.rn.f32x2 r, %5, z, %4;\n\t"
+      "fma.rn.f32x2 r, r, z, %3;\n\tfma.rn.f32x2 r, r, z, %2;\n\tmul.rn.f32x2 p, p, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x0), "+f"(x1) : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
+}
+struct CapPairs {
+  uint64_t q[4];
+  __device__ __forceinline__ explicit CapPairs(const ScoreArgs& a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = pair_of(a.cap_q[i], a.cap_q[i]);
+  }
+};
 // (x0, x1) = (x0, x1) * f + (b0, b1).
 __device__ __forceinline__ void fma2v(float& x0, float& x1, float f, float b0, float b1) {
   asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
@@ -628,42 +639,65 @@ __device__ __forceinline__ void tmem_wait_ld32(float (&v)[32]) {
                :: "memory");
 }
 
-// The general way to a row's scores: 32 keys at a time from TMEM, modified (to log2 units), masked, and back; dpos: the
-// row's position less the tile's first key, vis(c): the keys c .. c + 31 that it sees (none for a row that is not the
-// segment's: what the others take must not hang on it).
+// A row's raw products with N keys (at `at` in TMEM; masked ones zero) to scores in log2 units; dpos: its position less
+// the first of the keys; valid: the row is the segment's (others have no say in what the warp does).
+template <int N>
+__device__ __forceinline__ void modify(float (&s)[N], uint32_t at, const ScoreArgs& a, float slope, int dpos, bool valid) {
+  if (a.cap_out != 0.f) {
+    const CapPairs k(a);
+    float top[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < N; c += 2) top[(c >> 1) & 1] = max3f(top[(c >> 1) & 1], fabsf(s[c]), fabsf(s[c + 1]));
+    if (__any_sync(0xffffffffu, valid && !(fmaxf(top[0], top[1]) < a.cap_small))) {
+      // (rarely taken: short code, by way of TMEM)
+#pragma unroll
+      for (int c = 0; c < N; c += 16) tmem_st16(at + c, s + c);
+      tmem_wait_st();
+#pragma unroll 1
+      for (int c0 = 0; c0 < N; c0 += 16) {
+        float x[16];
+        tmem_ld16(at + c0, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) x[c] = a.cap_out * tanh_any(x[c] * a.base);
+        tmem_st16(at + c0, x);
+      }
+      tmem_wait_st();
+#pragma unroll
+      for (int c = 0; c < N; c += 16) tmem_ld16(at + c, s + c);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; c += 2) cap2(s[c], s[c + 1], k.q);
+    }
+  }
+  const float f = a.cap_out != 0.f ? 1.f : a.base;
+  if (a.slopes) {
+    if (__all_sync(0xffffffffu, dpos >= N - 1)) {   // every key at or before the position: - slope (dpos - c)
+      const float b = -slope * static_cast<float>(dpos);
+#pragma unroll
+      for (int c = 0; c < N; c += 2)
+        fma2v(s[c], s[c + 1], f, fmaf(slope, static_cast<float>(c), b), fmaf(slope, static_cast<float>(c + 1), b));
+    } else {
+      const float d = static_cast<float>(dpos);
+#pragma unroll
+      for (int c = 0; c < N; ++c) s[c] = fmaf(-slope, fabsf(d - static_cast<float>(c)), s[c] * f);
+    }
+  }
+}
+
+// A row's masked scores, 32 keys at a time from TMEM and back; vis(c): the keys c .. c + 31 that it sees.  (Modified
+// scores: masked ones become zero.)
 template <bool MOD, class V>
-__device__ __forceinline__ void rewrite_scores(uint32_t at_s, const ScoreArgs& a, float slope, int dpos, bool valid, V&& vis) {
+__device__ __forceinline__ void mask_scores(uint32_t at_s, V&& vis) {
 #pragma unroll 1
   for (int c0 = 0; c0 < kNK; c0 += 32) {
     float s[32];
     tmem_ld32(at_s + c0, s);
     tmem_wait_ld32(s);
     const uint32_t v = vis(c0);
-    if constexpr (MOD) {
-      if (a.cap_out != 0.f) {
-        float top[2] = {0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if ((v >> c) & 1u) top[c & 1] = fmaxf(top[c & 1], fabsf(s[c]));
-        if (__any_sync(0xffffffffu, valid && !(fmaxf(top[0], top[1]) < a.cap_small))) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] = a.cap_out * tanh_any(s[c] * a.base);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) cap2(s[c], s[c + 1], a.cap_q);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] *= a.base;
-      }
-      if (a.slopes) {
-        const float d = static_cast<float>(dpos - c0);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(d - static_cast<float>(c)), s[c]);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = (v >> c) & 1u ? s[c] : -CUDART_INF_F;
+    for (int c = 0; c < 32; ++c) s[c] = (v >> c) & 1u ? s[c] : MOD ? 0.f : -CUDART_INF_F;
     tmem_st32(at_s + c0, s);
   }
   tmem_wait_st();
@@ -1171,58 +1205,49 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         if (!(ok = mbar_wait_warp(&bars[B::kS + X], sc & 1, s_abort, a.wait_ns))) break;
         ++sc;
         tc_fence_after();
-        // A tile that every row sees whole, and whose scores take the short way, is done in registers.  The others
-        // are first rewritten in TMEM by a loop: unrolled for 128 keys its code would drive the rest out of the
-        // instruction cache (warps, the neighbouring SM's too, then waited two steps' time at each such tile).
+        // The code is kept short: what is unrolled for 128 keys and more drives the rest out of the instruction cache
+        // (the neighbouring SM's, too: its warps then waited two steps' time at each masked tile).  Masked scores are
+        // rewritten in TMEM by a loop; modified ones are so 64 keys at a time, and P is made from there.
         const uint32_t at_s = tmem + lane_base + colS;
-        const int dpos = pos - key0;
-        const bool sloped = MOD && sa.slopes != nullptr;
-        bool general = masked || (sloped && !__all_sync(0xffffffffu, dpos >= kNK - 1));
-        float s[kNK];
-        auto load = [&] {
+        auto vis = [&](int c0) {
+          uint32_t v = span_bits(sg.prefix, span, key0 + c0);
+          const uint32_t lost = gone >> (c0 / kBlockSize);
+          if (lost & 1u) v &= 0xffff0000u;
+          if (lost & 2u) v &= 0x0000ffffu;
+          return v;
+        };
+        if (masked) mask_scores<MOD>(at_s, vis);
+        constexpr int kAtOnce = MOD ? 64 : kNK;
+        float s[kAtOnce], mx = -CUDART_INF_F;
+        auto load = [&](int c0) {
 #pragma unroll
-          for (int c = 0; c < kNK; c += 16) tmem_ld16(at_s + c, s + c);
+          for (int c = 0; c < kAtOnce; c += 16) tmem_ld16(at_s + c0 + c, s + c);
           tmem_wait_ld();
         };
-        if (!general) {
-          load();
-          if (MOD && sa.cap_out != 0.f) {
-            // (rows that are not the segment's have no say)
-            float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c0 = 0; c0 < kNK; c0 += kAtOnce) {
+          load(c0);
+          if constexpr (MOD) {
+            modify<kAtOnce>(s, at_s + c0, sa, slope, pos - key0 - c0, valid);
+            if (masked) {   // (in words of 32)
 #pragma unroll
-            for (int c = 0; c < kNK; c += 2) top[(c >> 1) & 3] = max3f(top[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
-            const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            general = __any_sync(0xffffffffu, valid && !(most < sa.cap_small));
+              for (int w = 0; w < kAtOnce; w += 32) {
+                const uint32_t v = vis(c0 + w);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[w + c] = (v >> c) & 1u ? s[w + c] : -CUDART_INF_F;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < kAtOnce; c += 16) tmem_st16(at_s + c0 + c, s + c);
           }
+          float mx8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+          for (int c = 16; c < kAtOnce; c += 2) mx8[(c >> 1) & 7] = max3f(mx8[(c >> 1) & 7], s[c], s[c + 1]);
+          mx = max3f(mx, max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])), mx);
         }
-        if (general) {
-          rewrite_scores<MOD>(at_s, sa, slope, dpos, valid, [&](int c0) {
-            if (!masked) return 0xffffffffu;
-            uint32_t v = span_bits(sg.prefix, span, key0 + c0);
-            const uint32_t lost = gone >> (c0 / kBlockSize);
-            if (lost & 1u) v &= 0xffff0000u;
-            if (lost & 2u) v &= 0x0000ffffu;
-            return v;
-          });
-          load();
-        } else if constexpr (MOD) {
-          if (sa.cap_out != 0.f) {
-#pragma unroll
-            for (int c = 0; c < kNK; c += 2) cap2(s[c], s[c + 1], sa.cap_q);
-          }
-          if (sloped) {   // - slope (dpos - c), every key at or before the position
-            const float b = -slope * static_cast<float>(dpos), f = sa.cap_out != 0.f ? 1.f : sa.base;
-#pragma unroll
-            for (int c = 0; c < kNK; c += 2)
-              fma2v(s[c], s[c + 1], f, fmaf(slope, static_cast<float>(c), b), fmaf(slope, static_cast<float>(c + 1), b));
-          }
-        }
-        float mx8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(s[2 * k], s[2 * k + 1]);
-#pragma unroll
-        for (int c = 16; c < kNK; c += 2) mx8[(c >> 1) & 7] = max3f(mx8[(c >> 1) & 7], s[c], s[c + 1]);
-        const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        if constexpr (MOD) tmem_wait_st();
         // Lazy rescaling: a row keeps its reference while the tile's maximum
         // stays within 2^kRescaleLog2 of it.  (Rows of the tile that are not the
         // segment's, other requests' or whatever the buffer held, have no say:
@@ -1232,18 +1257,22 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         const float m_new = grow ? fmaxf(m, m_tile) : m;
         const float neg_m = m_new == -CUDART_INF_F ? 0.f : -m_new;
         float rs0[4] = {0.f, 0.f, 0.f, 0.f}, rs1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c0 = 0; c0 < kNK; c0 += kAtOnce) {
+          if constexpr (MOD) load(c0);
 #pragma unroll
-        for (int cc = 0; cc < kNK; cc += 32) {
-          uint32_t pk[16];
+          for (int cc = 0; cc < kAtOnce; cc += 32) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = cc; c < cc + 32; c += 2) {
-            float x0 = s[c], x1 = s[c + 1];
-            fma2(x0, x1, sl2, neg_m);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            add2(rs0[(c >> 1) & 3], rs1[(c >> 1) & 3], p0, p1);
-            pk[(c - cc) / 2] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            for (int c = cc; c < cc + 32; c += 2) {
+              float x0 = s[c], x1 = s[c + 1];
+              fma2(x0, x1, sl2, neg_m);
+              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+              add2(rs0[(c >> 1) & 3], rs1[(c >> 1) & 3], p0, p1);
+              pk[(c - cc) / 2] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            }
+            tmem_st16(at_s + (c0 + cc) / 2, reinterpret_cast<const float*>(pk));
           }
-          tmem_st16(at_s + cc / 2, reinterpret_cast<const float*>(pk));
         }
         const float rsum = ((rs0[0] + rs1[0]) + (rs0[1] + rs1[1])) + ((rs0[2] + rs1[2]) + (rs0[3] + rs1[3]));
         const float alpha = grow && m != -CUDART_INF_F ? fast_exp2(m + neg_m) : 1.f;
