@@ -154,6 +154,16 @@ bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_to
   return rows > most * num_reqs && work > 16ll * 3 * pool->num_sms;
 }
 
+// The form of a call of pkv_score_attn.  (Its tiles form has one line of work: a cut and two partials a CTA.)
+TreeForm score_form(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks) {
+  TreeForm f = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
+  if (f.tensor) {
+    f.cuts = f.ctas;
+    f.slots = 2 * f.cuts;
+  }
+  return f;
+}
+
 // The plan of pkv_score_attn's tiles form, behind the workspace of the form itself.
 struct ScoreWs {
   TreeWs tree;
@@ -470,7 +480,7 @@ int pkv_score_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_block
   const int rc = check_heads(pool, num_q_heads);
   if (rc) return rc;
   if (num_reqs < 0 || num_tokens < 0 || max_blocks < 0) return fail(PKV_EINVAL, "negative size");
-  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
+  const TreeForm form = score_form(pool, num_q_heads, num_reqs, num_tokens, max_blocks);
   *bytes = score_ws(pool, form, num_q_heads, num_reqs, num_tokens).total;
   return PKV_OK;
 }
@@ -492,7 +502,7 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   if (!q || !q_positions || !block_tables || !ctx_lens || !cu_q_lens || !o) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
-  const TreeForm form = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
+  const TreeForm form = score_form(pool, num_q_heads, num_reqs, num_tokens, max_blocks);
   const ScoreWs w = score_ws(pool, form, num_q_heads, num_reqs, num_tokens);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_score_attn_workspace_size()"))) return rc;
   DeviceGuard guard(pool->device);
@@ -533,7 +543,8 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   s.window = d.window;
   s.first_keys = d.first_keys;
   a.tile_tokens = kTcRows / a.group;
-  const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / (form.tensor ? kTcRows : 16) + num_reqs) *
+  s.row_tile = static_cast<int64_t>(num_tokens) * a.group <= 8ll * num_reqs ? 8 : 16;
+  const int64_t groups = (static_cast<int64_t>(num_tokens) * a.group / (form.tensor ? kTcRows : s.row_tile) + num_reqs) *
                          pool->num_kv_heads;
   // (A window alone bounds what a single token reads, whatever the table's width.)
   int blocks = max_blocks;

@@ -47,8 +47,26 @@ struct Modify {
 
 template <int D, int KIND>
 struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
+  using Base = RowTile<D, KIND != kPoolBf16>;
+  static constexpr int kRows = kRowTile;
+  // The rows whose queries, and whose state, a thread holds.
+  __device__ __forceinline__ static int row_a(int lane) { return lane >> 2; }
+  __device__ __forceinline__ static int row_b(int lane) { return (lane >> 2) + 8; }
+  template <class Q>
+  __device__ __forceinline__ void ask(Q&& q_row, int lane) { Base::load(q_row(row_a(lane)), q_row(row_b(lane)), lane); }
+  // The rows times f0 (f1), to where o_row says (nullptr: nowhere).
+  template <class R>
+  __device__ __forceinline__ void put_bf16(R&& o_row, float f0, float f1, int lane) const {
+    if (uint16_t* p = o_row(row_a(lane))) Base::put_bf16(p, 0, f0, lane);
+    if (uint16_t* p = o_row(row_b(lane))) Base::put_bf16(p, 1, f1, lane);
+  }
+  template <class R>
+  __device__ __forceinline__ void put_f32(R&& o_row, float f0, float f1, int lane) const {
+    if (float* p = o_row(row_a(lane))) Base::put_f32(p, 0, f0, lane);
+    if (float* p = o_row(row_b(lane))) Base::put_f32(p, 1, f1, lane);
+  }
+  __device__ __forceinline__ static bool first_of_row(int lane) { return (lane & 3) == 0; }
   static constexpr bool kCodes = KIND != kPoolBf16;
-  using Base = RowTile<D, kCodes>;
   using Base::kSteps, Base::kTiles, Base::q, Base::o, Base::m, Base::l, Base::odd, Base::ld_codes;
 
   // The loaded queries as operands (int8: bf16 as they are), and an empty state.
@@ -285,6 +303,316 @@ struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
   }
 };
 
+__device__ __forceinline__ uint32_t movm_t(uint32_t a) {   // an 8 x 8 matrix of 16 bits, transposed
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// The same for up to 8 rows, keys and dims as the MMA's rows instead:
+//   S^T = K Q^T    16 keys x 8 rows, D / 16 k-steps
+//   O^T += V^T P^T   D / 16 m-tiles of 16 dims x 8 rows, one k-step of 16 keys
+// half the products, scores and registers of a tile of 16 rows of which half are
+// not there.  Thread t = 4g + c holds the state of rows 2c and 2c + 1, the scores of
+// keys g and g + 8.  Codes: k-step s holds dims (D/4) c + 4 s .. + 3, m-tile j's rows
+// g and g + 8 are dims (D/8) g + 2 j and + 1: a thread reads whole 16-byte pieces.
+template <int D, int KIND>
+struct ScoreCol {
+  static constexpr bool kCodes = KIND != kPoolBf16, kF16 = KIND == kPoolFp8;
+  static constexpr int kRows = 8, kSteps = D / 16, kTiles = D / 16;
+  using Row = ScoreTile<D, KIND>;
+  uint32_t q[kSteps][2];
+  float o[kTiles][4];   // (dim, row 2c), (dim, row 2c + 1), (dim', row 2c), (dim', row 2c + 1)
+  float m[2], l[2];     // rows 2c and 2c + 1; l is this thread's share of the sum
+  bool odd;
+
+  __device__ __forceinline__ static int row_a(int lane) { return 2 * (lane & 3); }
+  __device__ __forceinline__ static int row_b(int lane) { return 2 * (lane & 3) + 1; }
+  __device__ __forceinline__ static bool first_of_row(int lane) { return lane < 4; }
+  template <class Q>
+  __device__ __forceinline__ void ask(Q&& q_row, int lane) {
+    const int c = lane & 3;
+    const uint16_t* p = q_row(lane >> 2);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int d0 = kCodes ? (D / 4) * c + 4 * s : 16 * s + 2 * c;
+      q[s][0] = p ? *reinterpret_cast<const uint32_t*>(p + d0) : 0u;
+      q[s][1] = p ? *reinterpret_cast<const uint32_t*>(p + d0 + (kCodes ? 2 : 8)) : 0u;
+    }
+  }
+  __device__ __forceinline__ void begin() {
+    if constexpr (kF16) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) q[s][i] = pack_f16x2(bf16lo_to_f32(q[s][i]), bf16hi_to_f32(q[s][i]));
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m[0] = m[1] = -CUDART_INF_F;
+    l[0] = l[1] = 0.f;
+    odd = false;
+  }
+
+  // As ScoreTile::block; vis0 / vis1: the keys that rows 2c and 2c + 1 see.
+  template <int MASK, int NB>
+  __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, const BlockFactor (&f)[NB], const int (&key0)[NB],
+                                        const Modify& mod, uint32_t vis0, uint32_t vis1, int lane, uint32_t kb1 = 0,
+                                        uint32_t vb1 = 0) {
+    static_assert(NB == 1 || MASK == kMaskNone, "masks are those of one block");
+    const int g = lane >> 2, c = lane & 3;
+    float s[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    if constexpr (!kCodes) {
+      // Lane l addresses line ((l / 8) % 2) * 8 + l % 8, 16-byte chunk 2 s + l / 16.
+      const int r8 = lane & 7, key8 = (lane >> 3) & 1, cx = lane >> 4;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const uint32_t base = (n ? kb1 : kb) + key8 * (D / 64) * 1024 + r8 * 128;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          const int ch = 2 * st + cx;
+          uint32_t a[4];
+          ldsm4(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), a[0], a[1], a[2], a[3]);
+          mma16<false>(s[n], a, q[st][0], q[st][1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          uint4 x, y;
+          Row::ld_codes(n ? kb1 : kb, g, (D / 64) * c + u, x);
+          Row::ld_codes(n ? kb1 : kb, g + 8, (D / 64) * c + u, y);
+          const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a[4];
+            Row::widen(wx[i], a[0], a[2]);
+            Row::widen(wy[i], a[1], a[3]);
+            mma16<kF16>(s[n], a, q[4 * u + i][0], q[4 * u + i][1]);
+          }
+        }
+      }
+    }
+    float sl = f[0].score;   // what is left to multiply the scores with
+    if (KIND == kPoolInt8 || mod.on) {
+      modify<NB>(s, f, mod, key0, g);
+      sl = 1.f;
+    }
+    if constexpr (MASK != kMaskNone) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!(((e & 1 ? vis1 : vis0) >> (g + 8 * (e >> 1))) & 1u)) s[0][e] = -CUDART_INF_F;
+    }
+    float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][2]));
+      mx1 = fmaxf(mx1, fmaxf(s[n][1], s[n][3]));
+    }
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+    }
+    const float n0 = fmaxf(m[0], mx0 * sl), n1 = fmaxf(m[1], mx1 * sl);   // sl > 0
+    if (__any_sync(0xffffffffu, n0 > m[0] || n1 > m[1])) {
+      const float a0 = n0 == -CUDART_INF_F ? 1.f : fast_exp2(m[0] - n0);
+      const float a1 = n1 == -CUDART_INF_F ? 1.f : fast_exp2(m[1] - n1);
+      l[0] *= a0;
+      l[1] *= a1;
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        o[j][0] *= a0; o[j][1] *= a1;
+        o[j][2] *= a0; o[j][3] *= a1;
+      }
+      m[0] = n0;
+      m[1] = n1;
+    }
+    const float u0 = m[0] == -CUDART_INF_F ? 0.f : -m[0], u1 = m[1] == -CUDART_INF_F ? 0.f : -m[1];
+    uint32_t p[NB][2];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = fast_exp2(fmaf(s[n][e], sl, e & 1 ? u1 : u0));
+      l[0] += s[n][0] + s[n][2];
+      l[1] += s[n][1] + s[n][3];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = s[n][2 * h], p1 = s[n][2 * h + 1];
+        if constexpr (kF16) p[n][h] = movm_t(pack_f16x2(p0, p1));
+        else if constexpr (KIND == kPoolInt8) p[n][h] = movm_t(pack_bf16x2(p0 * f[n].value, p1 * f[n].value));
+        else p[n][h] = movm_t(pack_bf16x2(p0, p1));
+      }
+    }
+    if constexpr (!kCodes) {
+      // Lane l addresses line (l / 16) * 8 + l % 8, chunk 2 j + (l / 8) % 2; transposed on the way.
+      const int r8 = lane & 7, key8 = lane >> 4, cx = (lane >> 3) & 1;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const uint32_t base = (n ? vb1 : vb) + key8 * (D / 64) * 1024 + r8 * 128;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          const int ch = 2 * j + cx;
+          uint32_t a[4];
+          ldsm4_t(base + (ch >> 3) * 1024 + (((ch & 7) ^ r8) << 4), a[0], a[1], a[2], a[3]);
+          if constexpr (MASK == kMaskRows) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = finite_pair<false>(a[e], odd);
+          }
+          mma16<false>(o[j], a, p[n][0], p[n][1]);
+        }
+      }
+    } else {
+      // Keys 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 codes from dim (D / 8) g; a byte
+      // permute pairs two keys' codes of one dim before the conversion.
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 2 * c + (k & 1) + 8 * (k >> 1);
+          if constexpr (D == 128) {
+            uint4 x;
+            Row::ld_codes(n ? vb1 : vb, key, g, x);
+            v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+          } else {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1])
+                         : "r"((n ? vb1 : vb) + key * D + 8 * g) : "memory");
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {   // word i: m-tiles 2 i and 2 i + 1
+          uint32_t a[2][4];
+          Row::widen(__byte_perm(v[0][i], v[1][i], 0x5140), a[0][0], a[0][1]);
+          Row::widen(__byte_perm(v[2][i], v[3][i], 0x5140), a[0][2], a[0][3]);
+          Row::widen(__byte_perm(v[0][i], v[1][i], 0x7362), a[1][0], a[1][1]);
+          Row::widen(__byte_perm(v[2][i], v[3][i], 0x7362), a[1][2], a[1][3]);
+          if constexpr (MASK == kMaskRows && KIND == kPoolFp8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e >> 2][e & 3] = finite_pair<true>(a[e >> 2][e & 3], odd);
+          }
+          mma16<kF16>(o[2 * i], a[0], p[n][0], p[n][1]);
+          mma16<kF16>(o[2 * i + 1], a[1], p[n][0], p[n][1]);
+        }
+      }
+    }
+  }
+
+  // Raw products to scores in log2 units.
+  template <int NB>
+  __device__ __forceinline__ static void modify(float (&s)[NB][4], const BlockFactor (&f)[NB], const Modify& mod,
+                                                const int (&key0)[NB], int g) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] *= f[n].score;
+    if (!mod.on) return;
+    if (mod.cap_out != 0.f) {
+      float top = 0.f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(s[n][e]));
+      const bool small = !__any_sync(0xffffffffu, top >= 0.5f);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = s[n][e];
+          float r = tanh_small(y);
+          if (!small && !(fabsf(y) < 0.5f)) r = tanh_large(y);
+          s[n][e] = mod.cap_out * r;
+        }
+    }
+    if (mod.slopes) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const float d0 = static_cast<float>(mod.p0 - key0[n] - g), d1 = static_cast<float>(mod.p1 - key0[n] - g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[n][e] = fmaf(-(e & 1 ? mod.slope1 : mod.slope0), fabsf((e & 1 ? d1 : d0) - (e < 2 ? 0.f : 8.f)), s[n][e]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void total_l(float& l0, float& l1) const {
+    l0 = l[0];
+    l1 = l[1];
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+  }
+  // The rows times f0 (rows 2c), f1 (2c + 1), to where o_row says (nullptr: nowhere).
+  template <class R>
+  __device__ __forceinline__ void put_bf16(R&& o_row, float f0, float f1, int lane) const {
+    const int g = lane >> 2, c = lane & 3;
+    if constexpr (kCodes) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint16_t* row = o_row(2 * c + i);
+        if (!row) continue;
+        const float f = i ? f1 : f0;
+        uint32_t w[kTiles];
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) w[j] = pack_bf16x2(o[j][i] * f, o[j][2 + i] * f);
+#pragma unroll
+        for (int j = 0; j < kTiles; j += 4)
+          *reinterpret_cast<uint4*>(row + (D / 8) * g + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+      }
+    } else {
+      uint16_t* row = o_row(g);
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        const uint32_t lo = movm_t(pack_bf16x2(o[j][0] * f0, o[j][1] * f1));
+        const uint32_t hi = movm_t(pack_bf16x2(o[j][2] * f0, o[j][3] * f1));
+        if (row) {
+          *reinterpret_cast<uint32_t*>(row + 16 * j + 2 * c) = lo;
+          *reinterpret_cast<uint32_t*>(row + 16 * j + 8 + 2 * c) = hi;
+        }
+      }
+    }
+  }
+  // Dim of o[j][0] (o[j][1]); o[j][2] (o[j][3]) is dim_step further on.
+  __device__ __forceinline__ static int dim(int j, int lane) { return kCodes ? (D / 8) * (lane >> 2) + 2 * j : 16 * j + (lane >> 2); }
+  static constexpr int kDimStep = kCodes ? 1 : 8;
+  template <class R>
+  __device__ __forceinline__ void put_f32(R&& o_row, float f0, float f1, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float* row = o_row(2 * (lane & 3) + i);
+      if (!row) continue;
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        row[dim(j, lane)] = o[j][i] * (i ? f1 : f0);
+        row[dim(j, lane) + kDimStep] = o[j][2 + i] * (i ? f1 : f0);
+      }
+    }
+  }
+  // Writes the warp's state to `buf` ([8][D + 4] floats: o unnormalised, m in log2 units, l).
+  __device__ __forceinline__ void store(float* buf, int lane) const {
+    float l0, l1;
+    total_l(l0, l1);
+    float* r0 = buf + 2 * (lane & 3) * (D + 4);
+    float* r1 = r0 + (D + 4);
+    if (lane < 4) {
+      r0[D] = m[0]; r0[D + 1] = l0;
+      r1[D] = m[1]; r1[D + 1] = l1;
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      const int d = dim(j, lane);
+      r0[d] = o[j][0]; r0[d + kDimStep] = o[j][2];
+      r1[d] = o[j][1]; r1[d + kDimStep] = o[j][3];
+    }
+  }
+};
+
 // A request as the rows form plans it: the blocks that hold its prefix, then
 // those from `gap` blocks further on up to the last that a token sees.
 struct RowsReq : ScoreReq {
@@ -331,8 +659,9 @@ __device__ __forceinline__ RowsReq rows_req_warp(const ScoreArgs& a, int r, int 
   plan_blocks(q, lo, hi);
   return q;
 }
+template <int RT>
 __device__ __forceinline__ int rows_tiles(const ScoreReq& q, int group) {
-  return static_cast<int>((static_cast<int64_t>(q.n) * group + kRowTile - 1) / kRowTile);
+  return static_cast<int>((static_cast<int64_t>(q.n) * group + RT - 1) / RT);
 }
 
 // V elements that are not finite, added to a stored row that sees them (they
@@ -365,13 +694,14 @@ __device__ __noinline__ void score_add_odd(const ScoreArgs& a, const RowsReq& q,
 }
 
 // A worker walks its share of the line of all groups' blocks, segment by
-// segment (blocks [b0, b1) of one group: 16 query rows, one KV head), as in the
+// segment (blocks [b0, b1) of one group: a tile of 16 or 8 query rows, one KV head), as in the
 // tree attention: shares of single warps where there are many groups, of CTAs of
 // four warps where there are few, whole groups where they are short.
-template <int D, int KIND, int W>
+template <int D, int KIND, int W, class Tile>
 __global__ void __launch_bounds__(32 * W, 12 / W)
 score_rows_kernel(const ScoreArgs a) {
   constexpr bool kCodes = KIND != kPoolBf16;
+  constexpr int kRT = Tile::kRows;
   using S = RowsSmem<D, kCodes, W>;
   constexpr bool kAlways = W != kRowWarps;   // always whole groups
   extern __shared__ uint8_t raw[];
@@ -385,7 +715,7 @@ score_rows_kernel(const ScoreArgs a) {
   griddep_launch();   // the merge may take its place and wait
   if (!kAlways && tid < W) t.cuts[cut_record(blockIdx.x, W, true, tid)].count = 0;
   if (tid == 0) s_odd = 0;
-  auto groups = [&](const ScoreReq& q) { return static_cast<int64_t>(rows_tiles(q, G)) * Hkv; };
+  auto groups = [&](const ScoreReq& q) { return static_cast<int64_t>(rows_tiles<kRT>(q, G)) * Hkv; };
   auto flag = [&](const ScoreReq& q) {
     if (q.bad && blockIdx.x == 0) atomicOr(t.pool.err, PKV_DEVERR_POSITION);
   };
@@ -476,18 +806,18 @@ score_rows_kernel(const ScoreArgs a) {
     const int kblk = rq.blocks, glen = kblk + kGroupUnits;
     const int grp = static_cast<int>(sh.off / glen);
     const int x = static_cast<int>(sh.off - static_cast<int64_t>(grp) * glen);
-    const int ntile = rows_tiles(rq, G);
+    const int ntile = rows_tiles<kRT>(rq, G);
     const int g = grp / ntile;
-    const int row0 = (grp - g * ntile) * kRowTile;
-    const int nrows = static_cast<int>(min(static_cast<int64_t>(kRowTile), static_cast<int64_t>(rq.n) * G - row0));
+    const int row0 = (grp - g * ntile) * kRT;
+    const int nrows = static_cast<int>(min(static_cast<int64_t>(kRT), static_cast<int64_t>(rq.n) * G - row0));
     const int len = static_cast<int>(min(static_cast<int64_t>(glen - x), sh.end - sh.u));
     const int64_t gbegin = sh.u - x;
     sh.u += len;
     sh.off += len;
     const int b0 = x, b1 = min(x + len, kblk);
     if (b0 >= b1) continue;   // the group's fixed units only
-    // Rows g' and g' + 8 of this thread.
-    const int ra = lane >> 2, rb = ra + 8;
+    // The rows whose state this thread holds.
+    const int ra = Tile::row_a(lane), rb = Tile::row_b(lane);
     auto tok_of = [&](int rr) { return rq.t0 + (row0 + min(rr, nrows - 1)) / G; };
     auto q_row = [&](int rr) -> const uint16_t* {
       if (rr >= nrows) return nullptr;
@@ -503,7 +833,7 @@ score_rows_kernel(const ScoreArgs a) {
       mod.slope0 = a.slopes[g * G + (row0 + min(ra, nrows - 1)) % G] * 1.4426950408889634f;
       mod.slope1 = a.slopes[g * G + (row0 + min(rb, nrows - 1)) % G] * 1.4426950408889634f;
     }
-    if (b0 == 0 && wi == 0 && (lane & 3) == 0) {
+    if (b0 == 0 && wi == 0 && Tile::first_of_row(lane)) {
       const int most = t.max_blocks * kBlockSize;
       if (mod.p0 < 0 || mod.p0 >= most || mod.p1 < 0 || mod.p1 >= most) atomicOr(t.pool.err, PKV_DEVERR_POSITION);
     }
@@ -547,8 +877,8 @@ score_rows_kernel(const ScoreArgs a) {
                                                   (key0 >= lo_all && key0 + kBlockSize - 1 <= hi_all)));
     };
     look();
-    ScoreTile<D, KIND> rt;
-    rt.load(q_row(ra), q_row(rb), lane);   // asked for before the first blocks
+    Tile rt;
+    rt.ask(q_row, lane);   // asked for before the first blocks
     // One group of copies an iteration (an empty one for a block that is not there, and behind the last).
     auto copy = [&](int j) {
       const int chunk = __shfl_sync(0xffffffffu, (j >> 5) == win ? chunk_cur : chunk_next, j & 31);
@@ -617,21 +947,20 @@ score_rows_kernel(const ScoreArgs a) {
     if (solo) {
       float l0, l1;
       rt.total_l(l0, l1);
+      const float f0 = l0 == 0.f ? 0.f : v_scale / l0, f1 = l1 == 0.f ? 0.f : v_scale / l1;
+      if (whole)
+        rt.put_bf16([&](int rr) { return rr < nrows ? static_cast<uint16_t*>(t.o) + out_row(rr) * D : nullptr; }, f0, f1, lane);
+      else
+        rt.put_f32([&](int rr) { return rr < nrows ? t.part_o + (slot + rr) * D : nullptr; }, f0, f1, lane);
+      if (Tile::first_of_row(lane)) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = i ? rb : ra;
-        const float L = i ? l1 : l0;
-        const float f = L == 0.f ? 0.f : v_scale / L;
-        const float lse2 = L == 0.f ? -CUDART_INF_F : rt.m[i] + fast_log2(L);
-        if (rr < nrows) {
-          if (whole) {
-            const int64_t at = out_row(rr);
-            rt.put_bf16(static_cast<uint16_t*>(t.o) + at * D, i, f, lane);
-            if ((lane & 3) == 0 && t.lse) t.lse[at] = lse2 * 0.69314718055994530942f;
-          } else {
-            rt.put_f32(t.part_o + (slot + rr) * D, i, f, lane);
-            if ((lane & 3) == 0) t.part_lse[slot + rr] = lse2;
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int rr = i ? rb : ra;
+          const float L = i ? l1 : l0;
+          const float lse2 = L == 0.f ? -CUDART_INF_F : rt.m[i] + fast_log2(L);
+          if (rr >= nrows) continue;
+          if (!whole) t.part_lse[slot + rr] = lse2;
+          else if (t.lse) t.lse[out_row(rr)] = lse2 * 0.69314718055994530942f;
         }
       }
       if (KIND != kPoolInt8 && __any_sync(0xffffffffu, rt.odd)) {
@@ -643,7 +972,7 @@ score_rows_kernel(const ScoreArgs a) {
       __syncthreads();   // every warp's ring has drained
       // Merge the warps' states: [warp][16][D + 4] floats over the ring.
       float* mbuf = reinterpret_cast<float*>(ring);
-      rt.store(mbuf + warp * kRowTile * S::kMergeRow, lane);
+      rt.store(mbuf + warp * kRT * S::kMergeRow, lane);
       __syncthreads();
       constexpr int kDims = D / 8;   // dims of a thread's part of a row
       const int rr = tid >> 3, d0 = (tid & 7) * kDims;
@@ -652,10 +981,10 @@ score_rows_kernel(const ScoreArgs a) {
 #pragma unroll
         for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, mbuf[(w * kRowTile + rr) * S::kMergeRow + D]);
+        for (int w = 0; w < W; ++w) M = fmaxf(M, mbuf[(w * kRT + rr) * S::kMergeRow + D]);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float* src = mbuf + (w * kRowTile + rr) * S::kMergeRow;
+          const float* src = mbuf + (w * kRT + rr) * S::kMergeRow;
           if (src[D + 1] == 0.f) continue;   // the warp saw no key of this row (a NaN score leaves m, not l, as it was)
           const float f = fast_exp2(src[D] - M);
           L = fmaf(f, src[D + 1], L);
@@ -708,17 +1037,21 @@ score_rows_kernel(const ScoreArgs a) {
   }
 }
 
-template <int D, int KIND, int W>
+template <int D, int KIND, int W, class Tile>
 int launch_w(const ScoreArgs& a, cudaStream_t s) {
   constexpr int smem = RowsSmem<D, KIND != kPoolBf16, W>::kTotal;
   static_assert(smem <= 232448, "shared memory of a CTA");
-  const cudaError_t e = smem_attr_once<score_rows_kernel<D, KIND, W>>(smem);
+  const cudaError_t e = smem_attr_once<score_rows_kernel<D, KIND, W, Tile>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(score_rows_kernel<D, KIND, W>, dim3(a.t.ctas), 32 * W, smem, s, a);
+  return launch_dependent(score_rows_kernel<D, KIND, W, Tile>, dim3(a.t.ctas), 32 * W, smem, s, a);
+}
+template <int D, int KIND, class Tile>
+int launch_r(const ScoreArgs& a, cudaStream_t s) {
+  return a.t.form.warps == 12 ? launch_w<D, KIND, 12, Tile>(a, s) : launch_w<D, KIND, kRowWarps, Tile>(a, s);
 }
 template <int D, int KIND>
 int launch_k(const ScoreArgs& a, cudaStream_t s) {
-  return a.t.form.warps == 12 ? launch_w<D, KIND, 12>(a, s) : launch_w<D, KIND, kRowWarps>(a, s);
+  return a.row_tile == 8 ? launch_r<D, KIND, ScoreCol<D, KIND>>(a, s) : launch_r<D, KIND, ScoreTile<D, KIND>>(a, s);
 }
 
 }  // namespace

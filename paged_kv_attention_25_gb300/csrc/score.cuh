@@ -45,6 +45,7 @@ struct ScoreArgs {
   const float* slopes;        // [num_q_heads], or nullptr
   int window;                 // 0: none
   const int32_t* first_keys;  // [num_tokens], or nullptr
+  int row_tile;               // rows form: 16 or 8 rows a tile
   ScorePlan plan;             // tiles form
 };
 

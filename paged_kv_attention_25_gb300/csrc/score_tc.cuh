@@ -203,7 +203,7 @@ struct Walk {
       s.rows1 = it.rows1;
       s.kt0 = kt0;
       s.kt1 = kt1;
-      s.slot = static_cast<int>(blockIdx.x) * 4 + (kt0 == 0 ? 1 : 0);
+      s.slot = static_cast<int>(blockIdx.x) * 2 + (kt0 == 0 ? 1 : 0);
       s.flags = (single ? kSegSingle : 0) | (kt0 == 0 && kt1 == kt ? kSegWhole : 0);
       s.pre_tiles = it.pre_tiles;
       s.gap = it.gap;
@@ -217,8 +217,8 @@ struct Walk {
         // longer than a tile).
         cut.count = TcShare::owner(U, workers, gbegin + static_cast<int64_t>(kt - 1) * cost) - static_cast<int>(blockIdx.x) + 1;
         cut.first = s.slot;
-        cut.next = (static_cast<int>(blockIdx.x) + 1) * 4;
-        cut.stride = 4;
+        cut.next = (static_cast<int>(blockIdx.x) + 1) * 2;
+        cut.stride = 2;
         cut.tok_a = s.tok0;
         cut.rows_a = s.rows0;
         cut.tok_b = s.tok1;
@@ -263,9 +263,10 @@ __device__ __forceinline__ T block_scan(T x, T& carry, T* scratch) {
 }
 
 // Requests' lengths and items' costs are kept in shared memory where they fit (kept
-// requests, kept items), and a warp has the spans of kPlanBatch items under way:
-// what is left is four trips to memory for a small batch.
-constexpr int kPlanReqs = 1024, kPlanItems = 2048, kPlanBatch = 4;
+// requests, kept items).  Eight lanes take an item, and the code is short: it runs
+// once, and much of its time is its first reading (382 items of 32 tokens: 17 us with
+// a warp an item, four unrolled).
+constexpr int kPlanReqs = 1024, kPlanItems = 2048, kPlanLanes = 8;
 struct PlanReq {
   int t0, n, ctx, prefix, first;
 };
@@ -273,13 +274,14 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
   __shared__ int64_t scratch[32];
   __shared__ PlanReq s_req[kPlanReqs];
   __shared__ int s_cost[kPlanItems];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, sub = tid % kPlanLanes;
   const int tt = a.t.tile_tokens, R = a.t.num_reqs;
   griddep_wait();
   griddep_launch();
   const bool kept = R <= kPlanReqs;
   int* const first = a.plan.first;   // items before each request's
   int n_items = 0;
+#pragma unroll 1
   for (int base = 0; base < R; base += kPlanThreads) {
     ScoreReq q{0, 0, 0, 0, false};
     int n = 0;
@@ -295,76 +297,68 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
   __syncthreads();
   n_items = min(n_items, a.plan.most);   // (ranges that overlap could make more)
   const bool costs = n_items <= kPlanItems;
-  for (int i0 = warp; i0 < n_items; i0 += kPlanBatch * (kPlanThreads / 32)) {
-    PlanReq q[kPlanBatch];
-    int req[kPlanBatch], t0[kPlanBatch], nt[kPlanBatch], any_lo[kPlanBatch], all_lo[kPlanBatch], any_hi[kPlanBatch],
-        all_hi[kPlanBatch];
-#pragma unroll
-    for (int b = 0; b < kPlanBatch; ++b) {
-      const int i = min(i0 + b * (kPlanThreads / 32), n_items - 1);
-      int lo = 0, n = R;   // the last request with first <= i (those without items share their successor's)
-      while (n > 1) {
-        const int step = (n + 31) / 32, x = lo + min(lane * step, n - 1);
-        const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && (kept ? s_req[x].first : first[x]) <= i);
-        const int k = max(0, __popc(le) - 1);
-        n = min(step, n - k * step);
-        lo += k * step;
+  const int rounds = (n_items + kPlanThreads / kPlanLanes - 1) / (kPlanThreads / kPlanLanes);
+#pragma unroll 1
+  for (int round = 0; round < rounds; ++round) {
+    const int i = round * (kPlanThreads / kPlanLanes) + tid / kPlanLanes;
+    const bool live = i < n_items;
+    PlanReq q{0, 0, 0, 0, 0};
+    int lo = 0;
+    if (live) {
+      int hi = R - 1;   // the last request with first <= i (those without items share their successor's)
+#pragma unroll 1
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((kept ? s_req[mid].first : first[mid]) <= i) lo = mid; else hi = mid - 1;
       }
-      req[b] = lo;
       if (kept) {
-        q[b] = s_req[lo];
+        q = s_req[lo];
       } else {
         const ScoreReq r = score_req(a, lo);
-        q[b] = PlanReq{r.t0, r.n, r.ctx, r.prefix, first[lo]};
+        q = PlanReq{r.t0, r.n, r.ctx, r.prefix, first[lo]};
       }
-      t0[b] = q[b].t0 + (i - q[b].first) * 2 * tt;
-      nt[b] = min(2 * tt, q[b].t0 + q[b].n - t0[b]);
-      any_lo[b] = INT_MAX;
-      all_lo[b] = 0;
-      any_hi[b] = -1;
-      all_hi[b] = INT_MAX;
     }
+    ScoreItem it;
+    it.tok0 = q.t0 + (i - q.first) * 2 * tt;
+    const int nt = live ? min(2 * tt, q.t0 + q.n - it.tok0) : 0;
+    it.any_lo = INT_MAX;
+    it.all_lo = 0;
+    it.any_hi = -1;
+    it.all_hi = INT_MAX;
     bool bad = false;
-    for (int x = lane; x < 2 * tt; x += 32) {
-#pragma unroll
-      for (int b = 0; b < kPlanBatch; ++b) {
-        if (x >= nt[b]) continue;
-        const KeySpan s = key_span(a, t0[b] + x, q[b].ctx);
-        any_lo[b] = min(any_lo[b], s.lo);
-        all_lo[b] = max(all_lo[b], s.lo);
-        any_hi[b] = max(any_hi[b], s.hi);
-        all_hi[b] = min(all_hi[b], s.hi);
-        const int p = __ldg(a.t.positions + t0[b] + x);
-        bad |= p < 0 || p >= a.t.max_blocks * kBlockSize;
-      }
+#pragma unroll 4
+    for (int x = sub; x < nt; x += kPlanLanes) {
+      const int p = __ldg(a.t.positions + it.tok0 + x);
+      const KeySpan s = key_span(a, p, a.first_keys ? __ldg(a.first_keys + it.tok0 + x) : 0, q.ctx);
+      it.any_lo = min(it.any_lo, s.lo);
+      it.all_lo = max(it.all_lo, s.lo);
+      it.any_hi = max(it.any_hi, s.hi);
+      it.all_hi = min(it.all_hi, s.hi);
+      bad |= p < 0 || p >= a.t.max_blocks * kBlockSize;
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
+    if (bad) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
 #pragma unroll
-    for (int b = 0; b < kPlanBatch; ++b) {
-      const int i = i0 + b * (kPlanThreads / 32);
-      if (i >= n_items) break;
-      ScoreItem it;
-      it.any_lo = __reduce_min_sync(0xffffffffu, any_lo[b]);
-      it.all_lo = __reduce_max_sync(0xffffffffu, all_lo[b]);
-      it.any_hi = __reduce_max_sync(0xffffffffu, any_hi[b]);
-      it.all_hi = __reduce_min_sync(0xffffffffu, all_hi[b]);
-      it.req = req[b];
-      it.tok0 = t0[b];
-      it.rows0 = min(tt, nt[b]) * a.t.group;
-      it.rows1 = max(0, nt[b] - tt) * a.t.group;
-      it.prefix = q[b].prefix;
-      it.ctx = q[b].ctx;
+    for (int d = 1; d < kPlanLanes; d <<= 1) {
+      it.any_lo = min(it.any_lo, __shfl_xor_sync(0xffffffffu, it.any_lo, d));
+      it.all_lo = max(it.all_lo, __shfl_xor_sync(0xffffffffu, it.all_lo, d));
+      it.any_hi = max(it.any_hi, __shfl_xor_sync(0xffffffffu, it.any_hi, d));
+      it.all_hi = min(it.all_hi, __shfl_xor_sync(0xffffffffu, it.all_hi, d));
+    }
+    if (live && sub == 0) {
+      it.req = lo;
+      it.rows0 = min(tt, nt) * a.t.group;
+      it.rows1 = max(0, nt - tt) * a.t.group;
+      it.prefix = q.prefix;
+      it.ctx = q.ctx;
       it.pre_tiles = (it.prefix + kNK - 1) / kNK;
       const int k0 = max(it.pre_tiles, it.any_lo / kNK);
       it.gap = k0 - it.pre_tiles;
       it.ktiles = max(1, it.pre_tiles + max(0, (it.any_hi + kNK) / kNK - k0));   // (one at least: its rows are written too)
       it.pad[0] = it.pad[1] = it.pad[2] = 0;
-      if (lane == 0) {
-        const int cost = (it.rows1 ? kPairUnits : kSingleUnits) * it.ktiles + kGroupUnits;
-        a.plan.items[i] = it;
-        if (costs) s_cost[i] = cost;
-        else a.plan.cum[i] = cost;
-      }
+      const int cost = (it.rows1 ? kPairUnits : kSingleUnits) * it.ktiles + kGroupUnits;
+      a.plan.items[i] = it;
+      if (costs) s_cost[i] = cost;
+      else a.plan.cum[i] = cost;
     }
   }
   __syncthreads();
@@ -717,7 +711,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   extern __shared__ __align__(1024) uint8_t smem[];
   griddep_wait();
   griddep_launch();   // the merge may take its place and wait
-  if (threadIdx.x < 2) a.cuts[2 * blockIdx.x + threadIdx.x].count = 0;
+  if (threadIdx.x == 0) a.cuts[blockIdx.x].count = 0;
   if ((smem_u32(smem) & 1023u) != 0) {   // swizzle atoms need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(a.pool.err, PKV_DEVERR_INTERNAL);
     return;
@@ -1098,7 +1092,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       TreeCut cut;
       const bool more = walk.next(sa, s, cut);
       if (more) {
-        if (cut.count > 0 && lane == 0) a.cuts[2 * blockIdx.x] = cut;
+        if (cut.count > 0 && lane == 0) a.cuts[blockIdx.x] = cut;
         // Blocks that are not there: flagged here, and only then looked for by the softmax warps.
         const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
         const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
