@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const PoolView pool
         const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
         uint32_t o[8];
         if constexpr (KIND == 2) {
-          const uint32_t f = exp_bf16x2(ex[b]);
+          const uint32_t f = exp_bf16x2(ex[b] + kWidenShift);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             int8x4_to_bf16x4(w[k], o[2 * k], o[2 * k + 1]);

@@ -36,6 +36,9 @@ using WarpShare = Share<4>;
 struct BlockFactor {
   float score, value;
 };
+// Raw products of widened codes are in units of 2^-kWidenShift (by itself: the factor of
+// the largest exponent would leave fp32's range).
+template <int KIND> constexpr float kRawUnit = KIND == kPoolInt8 ? static_cast<float>(1 << kWidenShift) : 1.f;
 // What becomes of the scores of rows g and g + 8 of a thread.
 struct Modify {
   bool on;             // cap or slopes
@@ -95,7 +98,7 @@ struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][t][e] *= f[n].score;
+        for (int e = 0; e < 4; ++e) s[n][t][e] = s[n][t][e] * kRawUnit<KIND> * f[n].score;
     if (!mod.on) return;
     if (mod.cap_out != 0.f) {
       float top = 0.f;
@@ -509,7 +512,7 @@ struct ScoreCol {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] *= f[n].score;
+      for (int e = 0; e < 4; ++e) s[n][e] = s[n][e] * kRawUnit<KIND> * f[n].score;
     if (!mod.on) return;
     if (mod.cap_out != 0.f) {
       float top = 0.f;
@@ -893,7 +896,7 @@ score_rows_kernel(const ScoreArgs a) {
       if constexpr (KIND == kPoolInt8) {
         const int e = __shfl_sync(0xffffffffu, exps_cur, i & 31);
         f.score *= exp_f32(static_cast<int16_t>(e & 0xffff));
-        f.value = exp_f32(e >> 16);
+        f.value = exp_f32((e >> 16) + kWidenShift);
       }
       return f;
     };

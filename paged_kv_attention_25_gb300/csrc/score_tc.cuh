@@ -532,7 +532,7 @@ __device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, 
         load(w + 6, v6);
       }
       if (!((t.store >> b) & 1u)) continue;
-      const uint32_t f = exp_bf16x2(safe_exp(__shfl_sync(0xffffffffu, t.exp, b)));
+      const uint32_t f = exp_bf16x2(safe_exp(__shfl_sync(0xffffffffu, t.exp, b)) + kWidenShift);
       const bool clean = KIND == kPoolFp8 && ((t.dirty >> b) & 1u);
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
