@@ -145,18 +145,25 @@ int check_workspace(const void* workspace, size_t have, size_t need, const char*
 // A batch that gives every CTA of the rows form 16 blocks at most stays there
 // (one request of 240 tokens, 2 KV heads, D = 64, 128 rows: 8.9 / 13.8).  The table's
 // width stands for the contexts' lengths, which only the device knows.
-bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks) {
+bool takes_tiles(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks, int64_t most) {
   if (pool->tree_form != 0) return pool->tree_form == 2;
   if (num_reqs < 1) return false;
   const int64_t rows = static_cast<int64_t>(num_tokens) * (num_q_heads / pool->num_kv_heads);
-  const int64_t most = pool->elem_bytes == 1 ? 44 : pool->head_dim == 64 ? 40 : 20;
   const int64_t work = (rows / 16 + num_reqs) * pool->num_kv_heads * max_blocks;   // at most
   return rows > most * num_reqs && work > 16ll * 3 * pool->num_sms;
 }
+bool tree_tensor(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks) {
+  return takes_tiles(pool, num_q_heads, num_reqs, num_tokens, max_blocks,
+                     pool->elem_bytes == 1 ? 44 : pool->head_dim == 64 ? 40 : 20);
+}
 
-// The form of a call of pkv_score_attn.  (Its tiles form has one line of work: a cut and two partials a CTA.)
+// The form of a call of pkv_score_attn.  (Its tiles form has one line of work: a cut and two partials a CTA.)  Measured
+// (rows / tiles, us), 48 requests that read 4100 tokens, 64 / 8 heads: bf16, D = 128: 16 rows 162 / 172, 24 rows 278 / 175,
+// 8 to 32 rows (20 in the mean) 195 / 175; D = 64: 16 rows 95 / 117, 24 rows 158 / 118; int8 40 rows 242 / 240, 64 rows
+// 316 / 243; FP8 48 rows 236 / 256, 64 rows 310 / 255.
 TreeForm score_form(const pkv_pool* pool, int num_q_heads, int num_reqs, int num_tokens, int max_blocks) {
-  TreeForm f = tree_form(tree_tensor(pool, num_q_heads, num_reqs, num_tokens, max_blocks), pool->num_sms);
+  const bool tiles = takes_tiles(pool, num_q_heads, num_reqs, num_tokens, max_blocks, pool->elem_bytes == 1 ? 44 : 16);
+  TreeForm f = tree_form(tiles, pool->num_sms);
   if (f.tensor) {
     f.cuts = f.ctas;
     f.slots = 2 * f.cuts;
