@@ -62,9 +62,11 @@ __device__ __forceinline__ uint32_t rescale_int8x4(uint32_t c, float f) {
 // order of the batch) is among them; a warp takes the rows of one of these blocks,
 // one KV head, K or V: up to 16 x D values in registers, their maximum, the codes.
 // The y grid shares out (head, K or V).  Bound by HBM for prompts, by the chain of
-// dependent loads (request, table, exponent) for a decode step.
+// dependent loads (request, table, exponent) for a decode step.  28,870 tokens of 8
+// heads, D = 128: 40 us (4.5 TB/s); four CTAs an SM spill a few registers, but two
+// took 47, and reading the rows twice (the second time out of L1) with six 43.
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_int8_kernel(
+__global__ void __launch_bounds__(kThreads, 4) append_int8_kernel(
     const PoolView pool, uint8_t* kp, uint8_t* vp, const int32_t* __restrict__ bt, int max_blocks, int num_reqs,
     const int32_t* __restrict__ cu, const int32_t* __restrict__ pos, const int32_t* __restrict__ held_lens,
     const uint8_t* k_new, const uint8_t* v_new, int num_tokens) {
@@ -197,23 +199,26 @@ __global__ void __launch_bounds__(kThreads) append_int8_kernel(
 }
 
 // Rows of a cache as bf16: a thread takes 16 values of a token's K or V row at a
-// time, kBatch loads under way.  Bound by HBM (a row's codes are a whole line).
-constexpr int kBatch = 4;
+// time, kBatch loads under way.  Bound by HBM (a row's codes are a whole line): 52
+// thousand int8 tokens of 8 heads, D = 128, 58 us.  Small CTAs and few loads a
+// thread, so that an SM has 16 CTAs at different stages: with 256 threads, 16 tokens
+// and 4 loads it was 68 us.  A row's 32 bytes go out as one store: as two, 74 us.
+constexpr int kBatch = 2, kReadTokens = 8, kReadThreads = 128;
 template <int KIND>   // 0: bf16, 1: e4m3, 2: int8
-__global__ void __launch_bounds__(kThreads) read_rows_kernel(const PoolView pool, const int32_t* __restrict__ bt,
+__global__ void __launch_bounds__(kReadThreads, 2048 / kReadThreads) read_rows_kernel(const PoolView pool, const int32_t* __restrict__ bt,
                                                              int max_blocks, int num_reqs,
                                                              const int32_t* __restrict__ cu,
                                                              const int32_t* __restrict__ pos, int num_tokens,
-                                                             uint8_t* k_out, uint8_t* v_out) {
-  __shared__ int s_pb[kTokens], s_slot[kTokens];   // block (-1: a slot that is not there, -2: no request)
+                                                             uint8_t* k_out, uint8_t* v_out, bool align32) {
+  __shared__ int s_pb[kReadTokens], s_slot[kReadTokens];   // block (-1: a slot that is not there, -2: no request)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hkv = pool.num_kv_heads, D = pool.head_dim;
   griddep_wait();
   griddep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) check_cu(cu, num_reqs, num_tokens, pool.err);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
-  const int here = static_cast<int>(min(static_cast<int64_t>(kTokens), num_tokens - t0));
-  for (int i = warp; i < here; i += kWarps) {
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTokens;
+  const int here = static_cast<int>(min(static_cast<int64_t>(kReadTokens), num_tokens - t0));
+  for (int i = warp; i < here; i += (kReadThreads / 32)) {
     const int t = static_cast<int>(t0) + i;
     const int p = __ldg(pos + t);
     const int r = req_of_warp(cu, num_reqs, t, lane);
@@ -236,26 +241,33 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const PoolView pool
     }
   }
   __syncthreads();
-  const int per = D / 16;                     // pieces of a head's row
-  const int row = Hkv * per;                  // ... of a token's K (or V)
-  const int pieces = here * row;              // of K; V's follow
-  const int step = kThreads * static_cast<int>(gridDim.y);
-  for (int e0 = static_cast<int>(blockIdx.y) * kThreads + tid; e0 < 2 * pieces; e0 += kBatch * step) {
+  const int lg = D == 128 ? 3 : 2, per = 1 << lg;   // pieces of a head's row
+  const int row = Hkv << lg;                        // ... of a token's K (or V)
+  const int step = kReadThreads * static_cast<int>(gridDim.y);
+  // Line i of 2 * here (K's tokens, then V's), piece x of its row; a step on without a division.
+  const int first = static_cast<int>(blockIdx.y) * kReadThreads + tid, di = step / row, dx = step - di * row;
+  int i = first / row, x = first - i * row;
+  auto on = [&](int& i, int& x) {
+    i += di;
+    x += dx;
+    if (x >= row) {
+      x -= row;
+      ++i;
+    }
+  };
+  while (i < 2 * here) {
     uint4 c[kBatch], c2[kBatch];
     int ex[kBatch];
+    int li = i, lx = x;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int e = e0 + b * step;
+    for (int b = 0; b < kBatch; ++b, on(li, lx)) {
       c[b] = c2[b] = make_uint4(0, 0, 0, 0);
       ex[b] = 0;
-      if (e >= 2 * pieces) continue;
-      const bool is_v = e >= pieces;
-      const int x = is_v ? e - pieces : e;
-      const int i = x / row, rest = x - i * row, g = rest / per, pc = rest - g * per;
-      const int pb = s_pb[i];
-      if (pb < 0) continue;
-      const int64_t chunk = static_cast<int64_t>(pb) * Hkv + g;
-      const int64_t at = (chunk * kBlockSize + s_slot[i]) * per + pc;   // in pieces of 16 values
+      const bool is_v = li >= here;
+      const int tok = is_v ? li - here : li;
+      if (li >= 2 * here || s_pb[tok] < 0) continue;
+      const int64_t chunk = static_cast<int64_t>(s_pb[tok]) * Hkv + (lx >> lg);
+      const int64_t at = (((chunk << 4) + s_slot[tok]) << lg) + (lx & (per - 1));   // in pieces of 16 values
       const uint4* src = static_cast<const uint4*>(is_v ? pool.v : pool.k);
       if constexpr (KIND == 0) {
         c[b] = __ldcg(src + 2 * at);
@@ -266,19 +278,16 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const PoolView pool
       }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int e = e0 + b * step;
-      if (e >= 2 * pieces) continue;
-      const bool is_v = e >= pieces;
-      const int x = is_v ? e - pieces : e;
-      const int i = x / row;
-      if (s_pb[i] == -2) continue;
+    for (int b = 0; b < kBatch; ++b, on(i, x)) {
+      const bool is_v = i >= here;
+      const int tok = is_v ? i - here : i;
+      if (i >= 2 * here || s_pb[tok] == -2) continue;
       uint4 lo = c[b], hi = c2[b];
       if constexpr (KIND != 0) {
         const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
         uint32_t o[8];
         if constexpr (KIND == 2) {
-          const uint32_t f = exp_bf16x2(ex[b] + kWidenShift);
+          const uint32_t f = exp_bf16x2(ex[b] + kWidenShift);   // (codes of a slot that is not there are zero)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             int8x4_to_bf16x4(w[k], o[2 * k], o[2 * k + 1]);
@@ -302,11 +311,14 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const PoolView pool
         }
         lo = make_uint4(o[0], o[1], o[2], o[3]);
         hi = make_uint4(o[4], o[5], o[6], o[7]);
-        if (s_pb[i] < 0) lo = hi = make_uint4(0, 0, 0, 0);
       }
-      uint4* dst = reinterpret_cast<uint4*>(is_v ? v_out : k_out) + 2 * (t0 * row + x);
-      dst[0] = lo;
-      dst[1] = hi;
+      uint4* dst = reinterpret_cast<uint4*>(is_v ? v_out : k_out) + 2 * ((t0 + tok) * row + x);
+      if (align32) {
+        st_global_v8(dst, lo, hi);
+      } else {
+        dst[0] = lo;
+        dst[1] = hi;
+      }
     }
   }
 }
@@ -334,12 +346,13 @@ int launch_append_int8(const PoolView& pool, void* kp, void* vp, const int32_t* 
 
 int launch_read_rows(const PoolView& pool, const int32_t* bt, int max_blocks, int num_reqs, const int32_t* cu,
                      const int32_t* pos, int num_tokens, void* k_out, void* v_out, int num_sms, void* stream) {
-  const int ctas = (num_tokens + kTokens - 1) / kTokens;
-  const int64_t pieces = 2ll * kTokens * pool.num_kv_heads * (pool.head_dim / 16);
-  const dim3 grid(ctas, spread(ctas, static_cast<int>((pieces + kThreads - 1) / kThreads), num_sms));
+  const int ctas = (num_tokens + kReadTokens - 1) / kReadTokens;
+  const int64_t pieces = 2ll * kReadTokens * pool.num_kv_heads * (pool.head_dim / 16);
+  const bool align32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
+  const dim3 grid(ctas, spread(ctas, static_cast<int>((pieces + kReadThreads - 1) / kReadThreads), num_sms));
   auto go = [&](auto kernel) {
-    return launch_dependent(kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), pool, bt, max_blocks, num_reqs,
-                            cu, pos, num_tokens, static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out));
+    return launch_dependent(kernel, grid, kReadThreads, 0, static_cast<cudaStream_t>(stream), pool, bt, max_blocks, num_reqs,
+                            cu, pos, num_tokens, static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out), align32);
   };
   return pool.k_exps ? go(read_rows_kernel<2>) : pool.elem_bytes == 1 ? go(read_rows_kernel<1>) : go(read_rows_kernel<0>);
 }
