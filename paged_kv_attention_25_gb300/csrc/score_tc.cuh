@@ -12,7 +12,8 @@
 //           joins B's state at the end); the key tiles that hold the prefix, then
 //           those from the first key that any row sees to the last;
 //   line    the items of one KV head after another's, a key tile of a pair three
-//           units, of a single tile two, and kGroupUnits for start and epilogue.
+//           units, of a single tile two (codes: three), and kGroupUnits for start
+//           and epilogue.
 // A CTA takes an equal share of the line; a group that several share is merged by
 // log-sum-exp.
 //
@@ -26,7 +27,7 @@
 // five paired operations for two scores, while every score of the warp's rows stays
 // below half the cap; otherwise by tanh_small and tanh_large.
 //
-// Pools of codes: they land in the upper half of a stage, and four more warps widen
+// Pools of codes: they land in the upper half of each block's lines, and four more warps widen
 // them in place, two for K and two for V (int8: to bf16 times the block's power of
 // two, exactly, so that the MMAs are those of bf16 pools; FP8: to f16).
 #pragma once
@@ -47,15 +48,26 @@
 namespace pkv {
 namespace {
 
+constexpr int kTeam = 2;   // codes: warps that widen K, and V
+// Registers of a CTA for codes, of 128 each at the launch.  Widening wants more (104: 5 % slower, 88: 20 %), and four
+// warps a team would leave it 48 (80 % slower).
+constexpr int kRegsWiden = 120, kRegsCodes = 56, kRegsSoft = 168;
+static_assert(kRegsCodes <= 128 && kRegsWiden <= 128 && kRegsSoft >= 128 && 2 * kRegsSoft + kRegsWiden + kRegsCodes <= 4 * 128,
+              "setmaxnreg.dec goes down, .inc up, within the launch's registers");
 // Warps 0 .. 7 softmax, 8 Q and K producer, 9 MMA issuer, 10 V producer, 11 scheduler; codes: 12 .. 15 widen.
 template <int KIND>
-constexpr int kThreads = KIND == kPoolBf16 ? 384 : 512;
+constexpr int kThreads = KIND == kPoolBf16 ? 384 : 384 + 64 * kTeam;
 constexpr int kBlkPerTile = kNK / kBlockSize;   // 8
 constexpr int kSegSlots = 4;                    // segments handed out ahead
 constexpr int kSegRing = 8;                     // V producer's reports (it is at most kSegSlots + 1 ahead)
 template <int KIND>
-constexpr int kSegReaders = KIND == kPoolBf16 ? 11 : 15;   // warps that read a segment
-constexpr int kPairUnits = 3, kSingleUnits = 2, kGroupUnits = 6;
+constexpr int kSegReaders = KIND == kPoolBf16 ? 11 : 11 + 2 * kTeam;   // warps that read a segment
+// (Codes: a single tile waits for the widening as a pair does; as two units it made 10 requests of 1 to 733 new tokens
+// 10 % slower.)
+constexpr int kPairUnits = 3, kSingleUnits = 2, kCodeSingleUnits = 3, kGroupUnits = 6;
+__device__ __forceinline__ int tile_cost(const PoolView& pool, bool single) {
+  return !single ? kPairUnits : pool.elem_bytes == 1 ? kCodeSingleUnits : kSingleUnits;
+}
 using TcShare = Share<kPairUnits + kGroupUnits>;
 
 template <int KS, int VS>
@@ -178,7 +190,7 @@ struct Walk {
         fresh = false;
       }
       const bool single = it.rows1 == 0;
-      const int cost = single ? kSingleUnits : kPairUnits;
+      const int cost = tile_cost(a.t.pool, single);
       glen = cost * it.ktiles + kGroupUnits;
       const int x = static_cast<int>(u - g * total - at);
       const int len = static_cast<int>(min(static_cast<int64_t>(glen - x), end - u));
@@ -355,7 +367,7 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
       it.gap = k0 - it.pre_tiles;
       it.ktiles = max(1, it.pre_tiles + max(0, (it.any_hi + kNK) / kNK - k0));   // (one at least: its rows are written too)
       it.pad[0] = it.pad[1] = it.pad[2] = 0;
-      const int cost = (it.rows1 ? kPairUnits : kSingleUnits) * it.ktiles + kGroupUnits;
+      const int cost = tile_cost(a.t.pool, it.rows1 == 0) * it.ktiles + kGroupUnits;
       a.plan.items[i] = it;
       if (costs) s_cost[i] = cost;
       else a.plan.cum[i] = cost;
@@ -427,20 +439,12 @@ struct CodeTile {
   bool last;   // of the segment
 };
 
-// Whether `mine` holds for all 64 threads of a team: a hardware barrier.  Every one of them comes to it as often as the
-// other, whatever its own waits found: what they do next hangs on the answer alone.
-__device__ __forceinline__ bool team_all(int team, bool mine) {
-  uint32_t all;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.and.pred q, %1, 64, p;\n\t"
-               "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(all) : "r"(team), "r"(mine ? 1u : 0u) : "memory");
-  return all != 0;
-}
-__device__ __forceinline__ void team_sync(int team) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(team) : "memory"); }
-
 // Widening warps, two (w = 0, 1) for K and two for V: blocks w, w + 2, ... of every
-// tile, one after the other (a loop: short code), exponents asked for a tile ahead.
-// The lines of the tile's second half lie over the codes: before they are written
-// both warps have read all of theirs.
+// tile, exponents asked for a tile ahead, the next block's codes while one is widened.
+// A block's codes land on the second half of its own lines: the warp that has read
+// them all may write.  Bound by one warp's chain of instructions; short code matters
+// more than overlap (two blocks at once: 18 % slower, all four 45 %; piece by piece,
+// 512 bytes each: 19 to 50 %).
 template <int D, int KIND>
 __device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, uint64_t* bars, const Seg* s_seg, int* s_odd,
                                             Odd* s_oddl, volatile int* s_abort, bool is_v, int w, int lane) {
@@ -497,86 +501,78 @@ __device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, 
     t.last = ++rel == n;
     return true;
   };
-  const int team = is_v ? 2 : 1, nst = is_v ? S::kVSt : S::kKSt;
+  const int nst = is_v ? S::kVSt : S::kKSt;
   const int bar_landed = is_v ? B::kVLanded : B::kKLanded, bar_full = is_v ? B::kVFull : B::kKFull;
   CodeTile next{};
   bool more = fetch(next);
-  for (int cnt = 0;; ++cnt) {
-    // Once a tile, and once behind the last, both warps come here and leave by what they hold in common: one whose wait
-    // ran out (it may not know whether there is a tile) takes the other along.
+  for (int cnt = 0; more; ++cnt) {
     const CodeTile t = next;
     const int st = cnt % nst;
     uint8_t* const stage = smem + (is_v ? S::kOffV : S::kOffK) + st * S::kKV;
-    if (ok && more) ok = mbar_wait_warp(&bars[bar_landed + st], (cnt / nst) & 1, s_abort, a.wait_ns);
-    if (!team_all(team, ok)) return false;
-    if (!more) return true;
+    if (!(ok = mbar_wait_warp(&bars[bar_landed + st], (cnt / nst) & 1, s_abort, a.wait_ns))) return false;
     auto load = [&](int b, uint4 (&v)[kPer]) {
       const bool there = (t.there >> b) & 1u;
 #pragma unroll
       for (int u = 0; u < kPer; ++u)    // (a block that is not there becomes zero)
-        v[u] = there ? *reinterpret_cast<const uint4*>(stage + S::kKV / 2 + b * (kBlockSize * D) + (u * 32 + lane) * 16)
+        v[u] = there ? *reinterpret_cast<const uint4*>(stage + b * S::kBlkBytes + S::kBlkBytes / 2 + (u * 32 + lane) * 16)
                      : make_uint4(0, 0, 0, 0);
     };
-    uint4 v[kPer], v4[kPer], v6[kPer];
+    uint4 v[kPer], ahead[kPer];
     load(w, v);
     more = fetch(next);
 #pragma unroll 1
-    for (int b = w; b < kBlkPerTile; b += 2) {
-      if (b >= 4) {
-        if (b < 6) team_sync(team);
+    for (int b = w; b < kBlkPerTile; b += kTeam) {
+      if (b + kTeam < kBlkPerTile) load(b + kTeam, ahead);
+      __syncwarp();   // block b's codes have been read
+      if ((t.store >> b) & 1u) {
+        const uint32_t f = exp_bf16x2(safe_exp(__shfl_sync(0xffffffffu, t.exp, b)) + kWidenShift);
+        const bool clean = KIND == kPoolFp8 && ((t.dirty >> b) & 1u);
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) v[u] = b < 6 ? v4[u] : v6[u];
-      } else if (b >= 2) {
-        load(w + 2, v);
-        load(w + 4, v4);
-        load(w + 6, v6);
-      }
-      if (!((t.store >> b) & 1u)) continue;
-      const uint32_t f = exp_bf16x2(safe_exp(__shfl_sync(0xffffffffu, t.exp, b)) + kWidenShift);
-      const bool clean = KIND == kPoolFp8 && ((t.dirty >> b) & 1u);
+        for (int u = 0; u < kPer; ++u) {
+          const int at = u * 32 + lane, key = b * kBlockSize + at / (D / 16), c16 = at % (D / 16);
+          const uint32_t c[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          uint32_t o[8];
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int at = u * 32 + lane, key = b * kBlockSize + at / (D / 16), c16 = at % (D / 16);
-        const uint32_t c[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (KIND == kPoolInt8) {
-            int8x4_to_bf16x4(c[k], o[2 * k], o[2 * k + 1]);
-            o[2 * k] = mul_bf16x2(o[2 * k], f);
-            o[2 * k + 1] = mul_bf16x2(o[2 * k + 1], f);
-          } else {
-            e4m3x4_to_f16x4(c[k], o[2 * k], o[2 * k + 1]);
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (KIND == kPoolInt8) {
+              int8x4_to_bf16x4(c[k], o[2 * k], o[2 * k + 1]);
+              o[2 * k] = mul_bf16x2(o[2 * k], f);
+              o[2 * k + 1] = mul_bf16x2(o[2 * k + 1], f);
+            } else {
+              e4m3x4_to_f16x4(c[k], o[2 * k], o[2 * k + 1]);
+            }
           }
-        }
-        if (clean) {   // codes that are NaN, and what lies behind the context
-          uint32_t bad = 0;
+          if (clean) {   // codes that are NaN, and what lies behind the context
+            uint32_t bad = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) bad |= ((o[k] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-          if (bad) {
+            for (int k = 0; k < 8; ++k) bad |= ((o[k] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+            if (bad) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+              for (int k = 0; k < 8; ++k) {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t h = (o[k] >> (16 * e)) & 0xffffu;
-                if ((h & 0x7c00u) != 0x7c00u) continue;
-                o[k] &= e ? 0x0000ffffu : 0xffff0000u;
-                if (t.key0 + key >= t.ctx) continue;
-                const int nth = atomicAdd(&s_odd[t.ring], 1);
-                if (nth < kOddMost)
-                  s_oddl[t.ring * kOddMost + nth] = Odd{t.key0 + key, static_cast<uint16_t>(c16 * 16 + 2 * k + e), static_cast<uint16_t>(h)};
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t h = (o[k] >> (16 * e)) & 0xffffu;
+                  if ((h & 0x7c00u) != 0x7c00u) continue;
+                  o[k] &= e ? 0x0000ffffu : 0xffff0000u;
+                  if (t.key0 + key >= t.ctx) continue;
+                  const int nth = atomicAdd(&s_odd[t.ring], 1);
+                  if (nth < kOddMost)
+                    s_oddl[t.ring * kOddMost + nth] = Odd{t.key0 + key, static_cast<uint16_t>(c16 * 16 + 2 * k + e), static_cast<uint16_t>(h)};
+                }
               }
             }
           }
+          // Chunks 2 c16 and 2 c16 + 1 of the key's 128-byte lines (swizzled); lanes of the second half of a 256-byte
+          // row store the odd one first, so that eight lanes meet eight banks.
+          const int hf = (2 * c16) / 8, cw = (2 * c16) % 8, r8 = key % 8;
+          uint8_t* line = stage + (key / 8) * S::kGS + hf * S::kHS + r8 * 128;
+          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(line + (((cw + hf) ^ r8) * 16)) = hf ? hi : lo;
+          *reinterpret_cast<uint4*>(line + (((cw + 1 - hf) ^ r8) * 16)) = hf ? lo : hi;
         }
-        // Chunks 2 c16 and 2 c16 + 1 of the key's 128-byte lines (swizzled); lanes of the second half of a 256-byte
-        // row store the odd one first, so that eight lanes meet eight banks.
-        const int hf = (2 * c16) / 8, cw = (2 * c16) % 8, r8 = key % 8;
-        uint8_t* line = stage + (key / 8) * S::kGS + hf * S::kHS + r8 * 128;
-        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint4*>(line + (((cw + hf) ^ r8) * 16)) = hf ? hi : lo;
-        *reinterpret_cast<uint4*>(line + (((cw + 1 - hf) ^ r8) * 16)) = hf ? lo : hi;
       }
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) v[u] = ahead[u];
     }
     fence_proxy_async_smem();   // read by the tensor cores
     __syncwarp();
@@ -586,6 +582,7 @@ __device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, 
     }
     __syncwarp();
   }
+  return ok;
 }
 
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
@@ -732,12 +729,12 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   if (!walk.begin(sa)) return;   // block-uniform
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKSt; ++i) {
-      mbar_init(&bars[B::kKFull + i], kCodes ? 2 : 1);
+      mbar_init(&bars[B::kKFull + i], kCodes ? kTeam : 1);
       mbar_init(&bars[B::kKEmpty + i], 1);
       mbar_init(&bars[B::kKLanded + i], 1);
     }
     for (int i = 0; i < kVSt; ++i) {
-      mbar_init(&bars[B::kVFull + i], kCodes ? 2 : 1);
+      mbar_init(&bars[B::kVFull + i], kCodes ? kTeam : 1);
       mbar_init(&bars[B::kVEmpty + i], 1);
       mbar_init(&bars[B::kVLanded + i], 1);
     }
@@ -752,7 +749,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
     mbar_init(&bars[B::kMl], 128);
     mbar_init(&bars[B::kJoined], 128);
     mbar_init(&bars[B::kDrain], 1);
-    for (int i = 0; i < kSegRing; ++i) mbar_init(&bars[B::kVDone + i], kCodes ? 2 : 1);
+    for (int i = 0; i < kSegRing; ++i) mbar_init(&bars[B::kVDone + i], kCodes ? kTeam : 1);
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&bars[B::kSegFull + i], 1);
       mbar_init(&bars[B::kSegEmpty + i], kSegReaders<KIND>);
@@ -793,15 +790,15 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   if (warp >= 12) {
     // ------------------------------------------------------------ widening of codes
     if constexpr (kCodes) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-      ok = widen_codes<D, KIND>(sa, smem, bars, s_seg, s_odd, s_oddl, s_abort, warp >= 14, warp & 1, lane);
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+      ok = widen_codes<D, KIND>(sa, smem, bars, s_seg, s_odd, s_oddl, s_abort, warp >= 12 + kTeam, warp % kTeam, lane);
       if (!ok) {
         if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
         *s_abort = 1;
       }
     }
   } else if (warp >= 8) {
-  if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCodes));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------ producers: warp 8 Q (and K), warp 10 V
@@ -920,7 +917,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           __syncwarp();
           uint8_t* stage = stages + st * S::kKV;
           if (y >= 0) {
-            if constexpr (kCodes) tma_load_2d(stage + S::kKV / 2 + lane * (kBlockSize * D), tm, 0, y * kBlockSize, bar);
+            if constexpr (kCodes) tma_load_2d(stage + lane * S::kBlkBytes + S::kBlkBytes / 2, tm, 0, y * kBlockSize, bar);
             else if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
             else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
           }
@@ -1127,7 +1124,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   }
   } else {
     // ------------------------------------------------------------ softmax / epilogue of group X
-    if constexpr (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if constexpr (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int X = (warp >> 2) & 1;
     const int row = threadIdx.x & 127;        // row within the tile (TMEM lane)
