@@ -155,8 +155,9 @@ typedef struct {
 } pkv_plan_stats;
 
 /* Accumulated device time per kernel family while profiling is on.  The tree
- * attention of few rows and the attention over selected blocks count as split-KV, the tree
- * attention over tiles of 128 rows as tensor-core, its merge as merge; bounds, selection and pages count as append. */
+ * attention of few rows, the attention over selected blocks and the rows form of pkv_score_attn count as split-KV, the
+ * tiles forms of pkv_tree_attn and pkv_score_attn (its plan with it) as tensor-core, their merges as merge; bounds,
+ * selection, pages, pkv_append_int8 and pkv_read_rows count as append. */
 typedef struct {
   int launches[5];          /* 0 append, 1 split-KV, 2 tensor-core, 3 merge, 4 swap */
   double total_ms[5];

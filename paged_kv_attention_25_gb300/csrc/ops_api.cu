@@ -1,5 +1,6 @@
 // C entry points of the operators beside the causal paged attention: tree
-// attention, block-selected attention, pages.  Their lengths, tables and masks
+// attention, block-selected attention, attention with modified scores, the int8
+// cache's writing and reading, pages.  Their lengths, tables and masks
 // are read on the device alone, so that the calls can be captured in a graph;
 // they keep nothing from one call for the next and run on the caller's stream.
 // A call of several kernels holds the pool's lock while it launches them, so that
@@ -9,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "internal.h"
@@ -171,6 +173,11 @@ TreeForm score_form(const pkv_pool* pool, int num_q_heads, int num_reqs, int num
   return f;
 }
 
+// (The plan counts items in 32 bits: one a request, and two tiles each.)
+int check_items(int num_reqs, int num_tokens) {
+  if (static_cast<int64_t>(num_reqs) + num_tokens > INT_MAX) return fail(PKV_EUNSUPPORTED, "too many requests and tokens");
+  return PKV_OK;
+}
 // The plan of pkv_score_attn's tiles form, behind the workspace of the form itself.
 struct ScoreWs {
   TreeWs tree;
@@ -487,6 +494,7 @@ int pkv_score_attn_workspace_size(pkv_pool* pool, int num_q_heads, int max_block
   const int rc = check_heads(pool, num_q_heads);
   if (rc) return rc;
   if (num_reqs < 0 || num_tokens < 0 || max_blocks < 0) return fail(PKV_EINVAL, "negative size");
+  if (const int big = check_items(num_reqs, num_tokens)) return big;
   const TreeForm form = score_form(pool, num_q_heads, num_reqs, num_tokens, max_blocks);
   *bytes = score_ws(pool, form, num_q_heads, num_reqs, num_tokens).total;
   return PKV_OK;
@@ -509,6 +517,7 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   if (!q || !q_positions || !block_tables || !ctx_lens || !cu_q_lens || !o) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
+  if ((rc = check_items(num_reqs, num_tokens))) return rc;
   const TreeForm form = score_form(pool, num_q_heads, num_reqs, num_tokens, max_blocks);
   const ScoreWs w = score_ws(pool, form, num_q_heads, num_reqs, num_tokens);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total, "pkv_score_attn_workspace_size()"))) return rc;

@@ -582,7 +582,9 @@ struct ScoreCol {
     }
   }
   // Dim of o[j][0] (o[j][1]); o[j][2] (o[j][3]) is dim_step further on.
-  __device__ __forceinline__ static int dim(int j, int lane) { return kCodes ? (D / 8) * (lane >> 2) + 2 * j : 16 * j + (lane >> 2); }
+  __device__ __forceinline__ static int dim(int j, int lane) {
+    return kCodes ? (D / 8) * (lane >> 2) + 2 * j : 16 * j + (lane >> 2);
+  }
   static constexpr int kDimStep = kCodes ? 1 : 8;
   template <class R>
   __device__ __forceinline__ void put_f32(R&& o_row, float f0, float f1, int lane) const {
@@ -702,6 +704,12 @@ __device__ __noinline__ void score_add_odd(const ScoreArgs& a, const RowsReq& q,
 // segment (blocks [b0, b1) of one group: a tile of 16 or 8 query rows, one KV head), as in the
 // tree attention: shares of single warps where there are many groups, of CTAs of
 // four warps where there are few, whole groups where they are short.
+//
+// Bound by HBM for bf16 (64 conversations of 0.6 to 30 thousand tokens, 64 / 8 heads,
+// D = 128: 6.1 TB/s), by a warp's chain of copies, conversions and products for codes
+// (the same in int8: 5.6 TB/s, issue slots 46 % busy, 167 us with the merge;
+// e4m3 162).  12 warps an SM: with 16, and rings of three or two blocks, it took 169 to
+// 179 us.  On tiles of 16 rows, half of them empty, the int8 case took 187.
 template <int D, int KIND, int W, class Tile>
 __global__ void __launch_bounds__(32 * W, 12 / W)
 score_rows_kernel(const ScoreArgs a) {
@@ -843,8 +851,10 @@ score_rows_kernel(const ScoreArgs a) {
       if (mod.p0 < 0 || mod.p0 >= most || mod.p1 < 0 || mod.p1 >= most) atomicOr(t.pool.err, PKV_DEVERR_POSITION);
     }
     // What the tile's rows see in common, and what any of them sees.
-    const int lo_all = __reduce_max_sync(0xffffffffu, max(sa.lo, sb.lo)), hi_all = __reduce_min_sync(0xffffffffu, min(sa.hi, sb.hi));
-    const int lo_any = __reduce_min_sync(0xffffffffu, min(sa.lo, sb.lo)), hi_any = __reduce_max_sync(0xffffffffu, max(sa.hi, sb.hi));
+    const int lo_all = __reduce_max_sync(0xffffffffu, max(sa.lo, sb.lo));
+    const int hi_all = __reduce_min_sync(0xffffffffu, min(sa.hi, sb.hi));
+    const int lo_any = __reduce_min_sync(0xffffffffu, min(sa.lo, sb.lo));
+    const int hi_any = __reduce_max_sync(0xffffffffu, max(sa.hi, sb.hi));
     const int live = b1 - b0;
     const int nb_w = live > wi ? (live - wi + wn - 1) / wn : 0;
     const int32_t* bt_row = t.block_tables + static_cast<int64_t>(req) * t.max_blocks;

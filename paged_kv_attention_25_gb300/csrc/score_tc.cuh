@@ -557,7 +557,8 @@ __device__ __forceinline__ bool widen_codes(const ScoreArgs& sa, uint8_t* smem, 
                   if (t.key0 + key >= t.ctx) continue;
                   const int nth = atomicAdd(&s_odd[t.ring], 1);
                   if (nth < kOddMost)
-                    s_oddl[t.ring * kOddMost + nth] = Odd{t.key0 + key, static_cast<uint16_t>(c16 * 16 + 2 * k + e), static_cast<uint16_t>(h)};
+                    s_oddl[t.ring * kOddMost + nth] =
+                      Odd{t.key0 + key, static_cast<uint16_t>(c16 * 16 + 2 * k + e), static_cast<uint16_t>(h)};
                 }
               }
             }
@@ -798,330 +799,330 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       }
     }
   } else if (warp >= 8) {
-  if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCodes));
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-  if (warp == 8 || warp == 10) {
-    // ------------------------------------------------------------ producers: warp 8 Q (and K), warp 10 V
-    const bool is_k = warp == 8;
-    const int nst = is_k ? kKSt : kVSt;
-    uint8_t* const stages = smem + (is_k ? S::kOffK : S::kOffV);
-    const int bar_full = is_k ? B::kKFull : B::kVFull, bar_empty = is_k ? B::kKEmpty : B::kVEmpty;
-    const int bar_landed = is_k ? B::kKLanded : B::kVLanded;
-    const CUtensorMap* const tm = is_k ? &tmap_k : &tmap_v;
-    int cnt = 0;      // tiles issued in the launch
-    int nq = 0;       // segments whose query tiles have been issued
-    uint32_t landed_par = 0;
-    for (int r = 0; ok && take(r); ++r) {
-      if (is_k) {
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (!(ok = mbar_wait_warp(&bars[B::kQEmpty + t], (r & 1) ^ 1, s_abort, a.wait_ns))) break;
-          if (lane == 0) {
-            if ((t ? sg.rows1 : sg.rows0) > 0) {
-              mbar_arrive_expect_tx(&bars[B::kQFull + t], static_cast<uint32_t>(D * 2 * G * a.q_box_tokens));
-              uint8_t* qt = smem + S::kOffQ + t * S::kQ;
+    if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCodes));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8 || warp == 10) {
+      // ------------------------------------------------------------ producers: warp 8 Q (and K), warp 10 V
+      const bool is_k = warp == 8;
+      const int nst = is_k ? kKSt : kVSt;
+      uint8_t* const stages = smem + (is_k ? S::kOffK : S::kOffV);
+      const int bar_full = is_k ? B::kKFull : B::kVFull, bar_empty = is_k ? B::kKEmpty : B::kVEmpty;
+      const int bar_landed = is_k ? B::kKLanded : B::kVLanded;
+      const CUtensorMap* const tm = is_k ? &tmap_k : &tmap_v;
+      int cnt = 0;      // tiles issued in the launch
+      int nq = 0;       // segments whose query tiles have been issued
+      uint32_t landed_par = 0;
+      for (int r = 0; ok && take(r); ++r) {
+        if (is_k) {
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!(ok = mbar_wait_warp(&bars[B::kQEmpty + t], (r & 1) ^ 1, s_abort, a.wait_ns))) break;
+            if (lane == 0) {
+              if ((t ? sg.rows1 : sg.rows0) > 0) {
+                mbar_arrive_expect_tx(&bars[B::kQFull + t], static_cast<uint32_t>(D * 2 * G * a.q_box_tokens));
+                uint8_t* qt = smem + S::kOffQ + t * S::kQ;
 #pragma unroll
-              for (int hf = 0; hf < S::kHalves; ++hf)
-                tma_load_3d(qt + hf * (kTcRows * 128), &tmap_q, hf * 64, sg.g * G, t ? sg.tok1 : sg.tok0,
-                            &bars[B::kQFull + t]);
-            } else {
-              mbar_arrive(&bars[B::kQFull + t]);
+                for (int hf = 0; hf < S::kHalves; ++hf)
+                  tma_load_3d(qt + hf * (kTcRows * 128), &tmap_q, hf * 64, sg.g * G, t ? sg.tok1 : sg.tok0,
+                              &bars[B::kQFull + t]);
+              } else {
+                mbar_arrive(&bars[B::kQFull + t]);
+              }
             }
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        nq = r + 1;
-      }
-      const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
-      const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
-      // Lane l holds block 32 w + l of the segment (window w: four key tiles), the next window in flight.
-      auto load_window = [&](int w) -> int {
-        const int j = sg.kt0 + w * 4 + lane / kBlkPerTile;
-        const int b = tile_at(j, sg.pre_tiles, sg.gap) * kBlkPerTile + lane % kBlkPerTile;
-        return j < sg.kt1 && b < nblk ? __ldg(bt_row + b) : -1;
-      };
-      auto check_window = [&](int pb) -> int { return pb >= 0 && pb < a.pool.num_blocks ? pb : -1; };
-      int win = 0;
-      int ids_cur = check_window(load_window(0)), ids_next = load_window(1);
-      // Lane l < 8: chunk index of key tile j's block l, or -1.
-      auto block_chunk = [&](int j) -> int {
-        const int rel = j - sg.kt0;
-        if ((rel >> 2) != win) {
-          win = rel >> 2;
-          ids_cur = check_window(ids_next);
-          ids_next = load_window(win + 1);
-        }
-        const int pb = __shfl_sync(0xffffffffu, ids_cur, (rel & 3) * kBlkPerTile + (lane & 7));
-        const uint32_t need = blocks_needed(sg, tile_at(j, sg.pre_tiles, sg.gap) * kNK);
-        return lane < kBlkPerTile && ((need >> lane) & 1u) && pb >= 0 ? pb * Hkv + sg.g : -1;
-      };
-      // V blocks that some row does not see whole: cleared of what they hold behind
-      // the context, and of elements that are not finite, which are noted; blocks that
-      // are not there (copied: have) become zero.  A lane has the 16-byte pieces
-      // lane, lane + 32, ... of a block's rows, eight (four) loads under way.
-      auto dirty_blocks = [&](int j, uint32_t have) -> uint32_t {
-        const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
-        return blocks_needed(sg, key0) & ~(blocks_whole(sg, key0) & have);
-      };
-      auto clean_v = [&](uint8_t* stage, int j, uint32_t have) {
-        constexpr int kCh = S::kHalves * 8;   // 16-byte pieces of a key's row
-        constexpr int kIt = kBlockSize * kCh / 32;
-        const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
-        const int ch = lane % kCh;
-        for (uint32_t left = dirty_blocks(j, have); left; left &= left - 1) {
-          const int b = __ffs(left) - 1;
-          const bool there = (have >> b) & 1u;
-          uint4* p[kIt];
-          uint4 v[kIt];
-#pragma unroll
-          for (int i = 0; i < kIt; ++i) {
-            const int key = b * kBlockSize + (lane + 32 * i) / kCh;
-            p[i] = reinterpret_cast<uint4*>(stage + (key / 8) * S::kGS + (ch / 8) * S::kHS + (key % 8) * 128 +
-                                            (((ch % 8) ^ (key % 8)) * 16));
-            v[i] = there ? *p[i] : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < kIt; ++i) {
-            const int key = key0 + b * kBlockSize + (lane + 32 * i) / kCh;
-            if (!there || key >= sg.ctx) {
-              *p[i] = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            // An exponent of ones carries into the sign's place.
-            constexpr uint32_t kExp = F8 ? 0x7c007c00u : 0x7f807f80u, kOne = F8 ? 0x04000400u : 0x00800080u;
-            const uint32_t bad = (((v[i].x & kExp) + kOne) | ((v[i].y & kExp) + kOne) | ((v[i].z & kExp) + kOne) |
-                                  ((v[i].w & kExp) + kOne)) & 0x80008000u;
-            if (!bad) continue;
-            uint16_t h[8];
-            *reinterpret_cast<uint4*>(h) = v[i];
-            for (int e = 0; e < 8; ++e) {
-              if ((h[e] & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
-              const int n = atomicAdd(&s_odd[r % kSegRing], 1);
-              if (n < kOddMost) s_oddl[(r % kSegRing) * kOddMost + n] = Odd{key, static_cast<uint16_t>(ch * 8 + e), h[e]};
-              h[e] = 0;
-            }
-            *p[i] = *reinterpret_cast<uint4*>(h);
-          }
-        }
-      };
-        for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
-          const int y = block_chunk(j);
-          const int st = cnt % nst;
-          const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
-          if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
-          // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
-          if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
-          const bool clean = !kCodes && !is_k && dirty_blocks(j, have) != 0;
-          uint64_t* bar = &bars[(clean || kCodes ? bar_landed : bar_full) + st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D * (kCodes ? 1 : 2)));
-          __syncwarp();
-          uint8_t* stage = stages + st * S::kKV;
-          if (y >= 0) {
-            if constexpr (kCodes) tma_load_2d(stage + lane * S::kBlkBytes + S::kBlkBytes / 2, tm, 0, y * kBlockSize, bar);
-            else if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
-            else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
-          }
-          if (clean) {
-            const uint32_t par = (landed_par >> st) & 1u;
-            landed_par ^= 1u << st;
-            if (!mbar_wait_warp(bar, par, s_abort, a.wait_ns)) {
-              (void)mbar_wait(bar, par, nullptr, a.wait_ns);   // let this tile's copies land
-              ok = false;
-              break;
-            }
-            clean_v(stage, j, have);
-            fence_proxy_async_smem();   // read by the tensor cores
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[bar_full + st]);
           }
+          if (!ok) break;
+          nq = r + 1;
         }
-        if (!ok) break;
-      if constexpr (!kCodes) {
-        __syncwarp();   // the notes are written
-        if (!is_k && lane == 0) mbar_arrive(&bars[B::kVDone + r % kSegRing]);
-        __syncwarp();
-      }
-    }
-    if (!ok) {   // gave up: flag it and let copies already issued land
-      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
-      *s_abort = 1;
-      for (int i = max(0, cnt - nst); i < cnt; ++i)
-        (void)mbar_wait(&bars[(kCodes ? bar_landed : bar_full) + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
-      if (is_k && nq > 0) {
-        for (int t = 0; t < 2; ++t) (void)mbar_wait(&bars[B::kQFull + t], (nq - 1) & 1, nullptr, a.wait_ns);
-      }
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_s = F8 ? make_idesc_f16(128, kNK, false) : make_idesc_bf16(128, kNK, false);
-    constexpr uint32_t idesc_o = F8 ? make_idesc_f16(128, D, true) : make_idesc_bf16(128, D, true);
-    const uint64_t dk = make_sdesc_sw128(sK, 16, S::kGS);
-    const uint64_t dv = make_sdesc_sw128(sV, S::kHS, S::kGS);
-    const uint64_t dqA = make_sdesc_sw128(sQ, 16, 1024), dqB = make_sdesc_sw128(sQ + S::kQ, 16, 1024);
-    auto k_desc = [&](int gk) { return dk + static_cast<uint64_t>(((gk % kKSt) * S::kKV) >> 4); };
-    auto v_desc = [&](int gv) { return dv + static_cast<uint64_t>(((gv % kVSt) * S::kKV) >> 4); };
-    const uint32_t lead = elect_one();   // every lane runs the issue code, the elected one issues
-    auto release = [&](int bar) { tc_commit_lead(lead, &bars[bar]); };
-    // S of group t = (query tile) K^T
-    auto issue_s = [&](int t, uint64_t dq, uint64_t kd) {
+        const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
+        const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
+        // Lane l holds block 32 w + l of the segment (window w: four key tiles), the next window in flight.
+        auto load_window = [&](int w) -> int {
+          const int j = sg.kt0 + w * 4 + lane / kBlkPerTile;
+          const int b = tile_at(j, sg.pre_tiles, sg.gap) * kBlkPerTile + lane % kBlkPerTile;
+          return j < sg.kt1 && b < nblk ? __ldg(bt_row + b) : -1;
+        };
+        auto check_window = [&](int pb) -> int { return pb >= 0 && pb < a.pool.num_blocks ? pb : -1; };
+        int win = 0;
+        int ids_cur = check_window(load_window(0)), ids_next = load_window(1);
+        // Lane l < 8: chunk index of key tile j's block l, or -1.
+        auto block_chunk = [&](int j) -> int {
+          const int rel = j - sg.kt0;
+          if ((rel >> 2) != win) {
+            win = rel >> 2;
+            ids_cur = check_window(ids_next);
+            ids_next = load_window(win + 1);
+          }
+          const int pb = __shfl_sync(0xffffffffu, ids_cur, (rel & 3) * kBlkPerTile + (lane & 7));
+          const uint32_t need = blocks_needed(sg, tile_at(j, sg.pre_tiles, sg.gap) * kNK);
+          return lane < kBlkPerTile && ((need >> lane) & 1u) && pb >= 0 ? pb * Hkv + sg.g : -1;
+        };
+        // V blocks that some row does not see whole: cleared of what they hold behind
+        // the context, and of elements that are not finite, which are noted; blocks that
+        // are not there (copied: have) become zero.  A lane has the 16-byte pieces
+        // lane, lane + 32, ... of a block's rows, eight (four) loads under way.
+        auto dirty_blocks = [&](int j, uint32_t have) -> uint32_t {
+          const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
+          return blocks_needed(sg, key0) & ~(blocks_whole(sg, key0) & have);
+        };
+        auto clean_v = [&](uint8_t* stage, int j, uint32_t have) {
+          constexpr int kCh = S::kHalves * 8;   // 16-byte pieces of a key's row
+          constexpr int kIt = kBlockSize * kCh / 32;
+          const int key0 = tile_at(j, sg.pre_tiles, sg.gap) * kNK;
+          const int ch = lane % kCh;
+          for (uint32_t left = dirty_blocks(j, have); left; left &= left - 1) {
+            const int b = __ffs(left) - 1;
+            const bool there = (have >> b) & 1u;
+            uint4* p[kIt];
+            uint4 v[kIt];
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int hf = ks / 4, kk = ks % 4;
-        tc_mma_lead(lead, tmem + t * kNK, dq + static_cast<uint64_t>((hf * (kTcRows * 128) + kk * 32) >> 4),
-                    kd + static_cast<uint64_t>((hf * S::kHS + kk * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
-      }
-      release(B::kS + t);
-    };
-    // O of group t (+)= P V
-    // (of the tile's blocks that some row sees; acc: O has products of the segment)
-    bool acc0 = false, acc1 = false;
-    auto issue_pv = [&](int t, int j, uint64_t vd) {
-      const uint32_t need = blocks_needed(sg, tile_at(sg.kt0 + j, sg.pre_tiles, sg.gap) * kNK);
-      bool acc = t ? acc1 : acc0;
-      if (need == 0xffu) {
+            for (int i = 0; i < kIt; ++i) {
+              const int key = b * kBlockSize + (lane + 32 * i) / kCh;
+              p[i] = reinterpret_cast<uint4*>(stage + (key / 8) * S::kGS + (ch / 8) * S::kHS + (key % 8) * 128 +
+                                              (((ch % 8) ^ (key % 8)) * 16));
+              v[i] = there ? *p[i] : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-        for (int ks = 0; ks < kNK / 16; ++ks)
-          tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
-                         vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, (acc || ks > 0) ? 1u : 0u);
-        acc = true;
-      } else {
-        for (int ks = 0; ks < kNK / 16; ++ks) {
-          if (!((need >> ks) & 1u)) continue;
-          tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
-                         vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, acc ? 1u : 0u);
-          acc = true;
-        }
-      }
-      if (t) acc1 = acc; else acc0 = acc;
-    };
-    constexpr int kQReady = F8 ? B::kQc : B::kQFull;
-    int kc = 0, vc = 0;          // K / V tiles consumed
-    uint32_t pc0 = 0, pc1 = 0;   // P phases of group A / B waited so far
-    auto wait_k = [&] { return mbar_wait_warp(&bars[B::kKFull + kc % kKSt], (kc / kKSt) & 1, s_abort, a.wait_ns); };
-    auto wait_v = [&] { return mbar_wait_warp(&bars[B::kVFull + vc % kVSt], (vc / kVSt) & 1, s_abort, a.wait_ns); };
-    auto wait_p = [&](int t) {
-      const bool o = mbar_wait_warp(&bars[B::kP + t], (t ? pc1 : pc0) & 1, s_abort, a.wait_ns);
-      if (t) ++pc1; else ++pc0;
-      return o;
-    };
-    for (int r = 0; ok && take(r); ++r) {
-      const int n = sg.kt1 - sg.kt0;   // >= 1
-      acc0 = acc1 = false;
-      if (!(ok = mbar_wait_warp(&bars[kQReady], r & 1, s_abort, a.wait_ns) &&
-                 mbar_wait_warp(&bars[kQReady + 1], r & 1, s_abort, a.wait_ns)))
-        break;
-      if (!(sg.flags & kSegSingle)) {
-        // Both groups use every key tile: PV_A(j) S_A(j+1) PV_B(j) S_B(j+1).
-        if (!(ok = wait_k())) break;
-        tc_fence_after();
-        issue_s(0, dqA, k_desc(kc));
-        issue_s(1, dqB, k_desc(kc));
-        if (n == 1) {
-          release(B::kQEmpty);
-          release(B::kQEmpty + 1);
-        }
-        release(B::kKEmpty + kc % kKSt);
-        ++kc;
-        for (int j = 0; ok && j < n; ++j) {
-          if (!(ok = wait_v())) break;
-          const uint64_t vd = v_desc(vc), kd = k_desc(kc);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!(ok = wait_p(t))) break;
-            tc_fence_after();
-            issue_pv(t, j, vd);
-            if (j == n - 1) release(B::kPv + t);
-            if (j + 1 < n) {
-              if (t == 0 && !(ok = wait_k())) break;
-              issue_s(t, t ? dqB : dqA, kd);
-              if (j + 1 == n - 1) release(B::kQEmpty + t);
+            for (int i = 0; i < kIt; ++i) {
+              const int key = key0 + b * kBlockSize + (lane + 32 * i) / kCh;
+              if (!there || key >= sg.ctx) {
+                *p[i] = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              // An exponent of ones carries into the sign's place.
+              constexpr uint32_t kExp = F8 ? 0x7c007c00u : 0x7f807f80u, kOne = F8 ? 0x04000400u : 0x00800080u;
+              const uint32_t bad = (((v[i].x & kExp) + kOne) | ((v[i].y & kExp) + kOne) | ((v[i].z & kExp) + kOne) |
+                                    ((v[i].w & kExp) + kOne)) & 0x80008000u;
+              if (!bad) continue;
+              uint16_t h[8];
+              *reinterpret_cast<uint4*>(h) = v[i];
+              for (int e = 0; e < 8; ++e) {
+                if ((h[e] & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
+                const int n = atomicAdd(&s_odd[r % kSegRing], 1);
+                if (n < kOddMost) s_oddl[(r % kSegRing) * kOddMost + n] = Odd{key, static_cast<uint16_t>(ch * 8 + e), h[e]};
+                h[e] = 0;
+              }
+              *p[i] = *reinterpret_cast<uint4*>(h);
+            }
+          }
+        };
+          for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
+            const int y = block_chunk(j);
+            const int st = cnt % nst;
+            const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
+            if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
+            // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
+            if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
+            const bool clean = !kCodes && !is_k && dirty_blocks(j, have) != 0;
+            uint64_t* bar = &bars[(clean || kCodes ? bar_landed : bar_full) + st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D * (kCodes ? 1 : 2)));
+            __syncwarp();
+            uint8_t* stage = stages + st * S::kKV;
+            if (y >= 0) {
+              if constexpr (kCodes) tma_load_2d(stage + lane * S::kBlkBytes + S::kBlkBytes / 2, tm, 0, y * kBlockSize, bar);
+              else if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
+              else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
+            }
+            if (clean) {
+              const uint32_t par = (landed_par >> st) & 1u;
+              landed_par ^= 1u << st;
+              if (!mbar_wait_warp(bar, par, s_abort, a.wait_ns)) {
+                (void)mbar_wait(bar, par, nullptr, a.wait_ns);   // let this tile's copies land
+                ok = false;
+                break;
+              }
+              clean_v(stage, j, have);
+              fence_proxy_async_smem();   // read by the tensor cores
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[bar_full + st]);
             }
           }
           if (!ok) break;
-          if (j + 1 < n) {
-            release(B::kKEmpty + kc % kKSt);
-            ++kc;
-          }
-          release(B::kVEmpty + vc % kVSt);
-          ++vc;
+        if constexpr (!kCodes) {
+          __syncwarp();   // the notes are written
+          if (!is_k && lane == 0) mbar_arrive(&bars[B::kVDone + r % kSegRing]);
+          __syncwarp();
         }
-      } else {
-        // Group j % 2 uses key tile j: S_A(0) S_B(1), then PV(j) S(j+2).
-        release(B::kQEmpty + 1);   // no second query tile
-        for (int j = 0; ok && j < 2 && j < n; ++j) {
+      }
+      if (!ok) {   // gave up: flag it and let copies already issued land
+        if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+        *s_abort = 1;
+        for (int i = max(0, cnt - nst); i < cnt; ++i)
+          (void)mbar_wait(&bars[(kCodes ? bar_landed : bar_full) + i % nst], (i / nst) & 1, nullptr, a.wait_ns);
+        if (is_k && nq > 0) {
+          for (int t = 0; t < 2; ++t) (void)mbar_wait(&bars[B::kQFull + t], (nq - 1) & 1, nullptr, a.wait_ns);
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc_s = F8 ? make_idesc_f16(128, kNK, false) : make_idesc_bf16(128, kNK, false);
+      constexpr uint32_t idesc_o = F8 ? make_idesc_f16(128, D, true) : make_idesc_bf16(128, D, true);
+      const uint64_t dk = make_sdesc_sw128(sK, 16, S::kGS);
+      const uint64_t dv = make_sdesc_sw128(sV, S::kHS, S::kGS);
+      const uint64_t dqA = make_sdesc_sw128(sQ, 16, 1024), dqB = make_sdesc_sw128(sQ + S::kQ, 16, 1024);
+      auto k_desc = [&](int gk) { return dk + static_cast<uint64_t>(((gk % kKSt) * S::kKV) >> 4); };
+      auto v_desc = [&](int gv) { return dv + static_cast<uint64_t>(((gv % kVSt) * S::kKV) >> 4); };
+      const uint32_t lead = elect_one();   // every lane runs the issue code, the elected one issues
+      auto release = [&](int bar) { tc_commit_lead(lead, &bars[bar]); };
+      // S of group t = (query tile) K^T
+      auto issue_s = [&](int t, uint64_t dq, uint64_t kd) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int hf = ks / 4, kk = ks % 4;
+          tc_mma_lead(lead, tmem + t * kNK, dq + static_cast<uint64_t>((hf * (kTcRows * 128) + kk * 32) >> 4),
+                      kd + static_cast<uint64_t>((hf * S::kHS + kk * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+        }
+        release(B::kS + t);
+      };
+      // O of group t (+)= P V
+      // (of the tile's blocks that some row sees; acc: O has products of the segment)
+      bool acc0 = false, acc1 = false;
+      auto issue_pv = [&](int t, int j, uint64_t vd) {
+        const uint32_t need = blocks_needed(sg, tile_at(sg.kt0 + j, sg.pre_tiles, sg.gap) * kNK);
+        bool acc = t ? acc1 : acc0;
+        if (need == 0xffu) {
+#pragma unroll
+          for (int ks = 0; ks < kNK / 16; ++ks)
+            tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
+                           vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, (acc || ks > 0) ? 1u : 0u);
+          acc = true;
+        } else {
+          for (int ks = 0; ks < kNK / 16; ++ks) {
+            if (!((need >> ks) & 1u)) continue;
+            tc_mma_ts_lead(lead, tmem + kColO + t * 128, tmem + t * kNK + ks * 8,
+                           vd + static_cast<uint64_t>((ks * 2 * S::kGS) >> 4), idesc_o, acc ? 1u : 0u);
+            acc = true;
+          }
+        }
+        if (t) acc1 = acc; else acc0 = acc;
+      };
+      constexpr int kQReady = F8 ? B::kQc : B::kQFull;
+      int kc = 0, vc = 0;          // K / V tiles consumed
+      uint32_t pc0 = 0, pc1 = 0;   // P phases of group A / B waited so far
+      auto wait_k = [&] { return mbar_wait_warp(&bars[B::kKFull + kc % kKSt], (kc / kKSt) & 1, s_abort, a.wait_ns); };
+      auto wait_v = [&] { return mbar_wait_warp(&bars[B::kVFull + vc % kVSt], (vc / kVSt) & 1, s_abort, a.wait_ns); };
+      auto wait_p = [&](int t) {
+        const bool o = mbar_wait_warp(&bars[B::kP + t], (t ? pc1 : pc0) & 1, s_abort, a.wait_ns);
+        if (t) ++pc1; else ++pc0;
+        return o;
+      };
+      for (int r = 0; ok && take(r); ++r) {
+        const int n = sg.kt1 - sg.kt0;   // >= 1
+        acc0 = acc1 = false;
+        if (!(ok = mbar_wait_warp(&bars[kQReady], r & 1, s_abort, a.wait_ns) &&
+                   mbar_wait_warp(&bars[kQReady + 1], r & 1, s_abort, a.wait_ns)))
+          break;
+        if (!(sg.flags & kSegSingle)) {
+          // Both groups use every key tile: PV_A(j) S_A(j+1) PV_B(j) S_B(j+1).
           if (!(ok = wait_k())) break;
           tc_fence_after();
-          issue_s(j, dqA, k_desc(kc));
-          if (j == n - 1) release(B::kQEmpty);
+          issue_s(0, dqA, k_desc(kc));
+          issue_s(1, dqB, k_desc(kc));
+          if (n == 1) {
+            release(B::kQEmpty);
+            release(B::kQEmpty + 1);
+          }
           release(B::kKEmpty + kc % kKSt);
           ++kc;
-        }
-        for (int j = 0; ok && j < n; ++j) {
-          const int t = j & 1;
-          if (!(ok = wait_v() && wait_p(t))) break;
-          tc_fence_after();
-          if (t) issue_pv(1, j, v_desc(vc)); else issue_pv(0, j, v_desc(vc));
-          if (j + 2 >= n) release(B::kPv + t);
-          release(B::kVEmpty + vc % kVSt);
-          ++vc;
-          if (j + 2 < n) {
+          for (int j = 0; ok && j < n; ++j) {
+            if (!(ok = wait_v())) break;
+            const uint64_t vd = v_desc(vc), kd = k_desc(kc);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!(ok = wait_p(t))) break;
+              tc_fence_after();
+              issue_pv(t, j, vd);
+              if (j == n - 1) release(B::kPv + t);
+              if (j + 1 < n) {
+                if (t == 0 && !(ok = wait_k())) break;
+                issue_s(t, t ? dqB : dqA, kd);
+                if (j + 1 == n - 1) release(B::kQEmpty + t);
+              }
+            }
+            if (!ok) break;
+            if (j + 1 < n) {
+              release(B::kKEmpty + kc % kKSt);
+              ++kc;
+            }
+            release(B::kVEmpty + vc % kVSt);
+            ++vc;
+          }
+        } else {
+          // Group j % 2 uses key tile j: S_A(0) S_B(1), then PV(j) S(j+2).
+          release(B::kQEmpty + 1);   // no second query tile
+          for (int j = 0; ok && j < 2 && j < n; ++j) {
             if (!(ok = wait_k())) break;
-            if (t) issue_s(1, dqA, k_desc(kc)); else issue_s(0, dqA, k_desc(kc));
-            if (j + 2 == n - 1) release(B::kQEmpty);
+            tc_fence_after();
+            issue_s(j, dqA, k_desc(kc));
+            if (j == n - 1) release(B::kQEmpty);
             release(B::kKEmpty + kc % kKSt);
             ++kc;
           }
+          for (int j = 0; ok && j < n; ++j) {
+            const int t = j & 1;
+            if (!(ok = wait_v() && wait_p(t))) break;
+            tc_fence_after();
+            if (t) issue_pv(1, j, v_desc(vc)); else issue_pv(0, j, v_desc(vc));
+            if (j + 2 >= n) release(B::kPv + t);
+            release(B::kVEmpty + vc % kVSt);
+            ++vc;
+            if (j + 2 < n) {
+              if (!(ok = wait_k())) break;
+              if (t) issue_s(1, dqA, k_desc(kc)); else issue_s(0, dqA, k_desc(kc));
+              if (j + 2 == n - 1) release(B::kQEmpty);
+              release(B::kKEmpty + kc % kKSt);
+              ++kc;
+            }
+          }
         }
       }
-    }
-    if (!ok) {
-      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
-      *s_abort = 1;
-    }
-    // Drain: every MMA issued has completed before TMEM is released.
-    release(B::kDrain);
-    (void)mbar_wait_warp(&bars[B::kDrain], 0, nullptr, a.wait_ns);
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ scheduler
-    walk.find(sa, lane);
-    for (int r = 0;; ++r) {
-      Seg s;
-      TreeCut cut;
-      const bool more = walk.next(sa, s, cut);
-      if (more) {
-        if (cut.count > 0 && lane == 0) a.cuts[blockIdx.x] = cut;
-        // Blocks that are not there: flagged here, and only then looked for by the softmax warps.
-        const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
-        const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
-        bool gone = false;
-        for (int x = s.kt0 * kBlkPerTile + lane; x < s.kt1 * kBlkPerTile; x += 32) {
-          const int b = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap) * kBlkPerTile + x % kBlkPerTile;
-          if (b >= nblk) continue;
-          const int pb = __ldg(bt_row + b);
-          gone |= pb < 0 || pb >= a.pool.num_blocks;
-        }
-        if (__any_sync(0xffffffffu, gone)) {
-          s.flags |= kSegMissing;
-          if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
-        }
-      } else {
-        s.flags = kSegEnd;
+      if (!ok) {
+        if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+        *s_abort = 1;
       }
-      const int slot = r % kSegSlots;
-      if (!(ok = mbar_wait_warp(&bars[B::kSegEmpty + slot], ((r / kSegSlots) & 1) ^ 1, s_abort, a.wait_ns))) break;
-      if (lane == 0) {
-        s_odd[r % kSegRing] = 0;   // (segment r - kSegRing is long done)
-        s_seg[slot] = s;
-        mbar_arrive(&bars[B::kSegFull + slot]);
+      // Drain: every MMA issued has completed before TMEM is released.
+      release(B::kDrain);
+      (void)mbar_wait_warp(&bars[B::kDrain], 0, nullptr, a.wait_ns);
+    } else if (warp == 11) {
+      // ------------------------------------------------------------ scheduler
+      walk.find(sa, lane);
+      for (int r = 0;; ++r) {
+        Seg s;
+        TreeCut cut;
+        const bool more = walk.next(sa, s, cut);
+        if (more) {
+          if (cut.count > 0 && lane == 0) a.cuts[blockIdx.x] = cut;
+          // Blocks that are not there: flagged here, and only then looked for by the softmax warps.
+          const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
+          const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
+          bool gone = false;
+          for (int x = s.kt0 * kBlkPerTile + lane; x < s.kt1 * kBlkPerTile; x += 32) {
+            const int b = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap) * kBlkPerTile + x % kBlkPerTile;
+            if (b >= nblk) continue;
+            const int pb = __ldg(bt_row + b);
+            gone |= pb < 0 || pb >= a.pool.num_blocks;
+          }
+          if (__any_sync(0xffffffffu, gone)) {
+            s.flags |= kSegMissing;
+            if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
+          }
+        } else {
+          s.flags = kSegEnd;
+        }
+        const int slot = r % kSegSlots;
+        if (!(ok = mbar_wait_warp(&bars[B::kSegEmpty + slot], ((r / kSegSlots) & 1) ^ 1, s_abort, a.wait_ns))) break;
+        if (lane == 0) {
+          s_odd[r % kSegRing] = 0;   // (segment r - kSegRing is long done)
+          s_seg[slot] = s;
+          mbar_arrive(&bars[B::kSegFull + slot]);
+        }
+        __syncwarp();
+        if (!more) break;
       }
-      __syncwarp();
-      if (!more) break;
+      if (!ok) {
+        if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
+        *s_abort = 1;
+      }
     }
-    if (!ok) {
-      if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_TIMEOUT);
-      *s_abort = 1;
-    }
-  }
   } else {
     // ------------------------------------------------------------ softmax / epilogue of group X
     if constexpr (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));

@@ -167,3 +167,12 @@ def test_rows_read_back_to_any_16_byte_boundary(dtype):
         row = exact[blk[0 if t < 4 else 1][p // 16], :, p % 16]
         if dtype != "fp8_e4m3":                                   # (codes times a scale are rounded)
             assert np.array_equal(want[0][t].double().cpu().numpy(), row)
+
+
+def test_more_items_than_are_counted_are_refused():
+    pool = pkv.Pool(4, 2, 64)
+    for reqs, tokens in ((2 ** 31 - 1, 1), (2 ** 30, 2 ** 30)):
+        with pytest.raises(pkv.PkvError) as e:
+            pkv.pkv_score_attn_workspace_size(pool, 8, 4, reqs, tokens)
+        assert e.value.code == pkv.PKV_EUNSUPPORTED
+    assert pkv.pkv_score_attn_workspace_size(pool, 8, 4, 1000, 1000) > 0
