@@ -176,3 +176,40 @@ def test_more_items_than_are_counted_are_refused():
             pkv.pkv_score_attn_workspace_size(pool, 8, 4, reqs, tokens)
         assert e.value.code == pkv.PKV_EUNSUPPORTED
     assert pkv.pkv_score_attn_workspace_size(pool, 8, 4, 1000, 1000) > 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_pools_whose_offsets_pass_32_bits(dtype):
+    """Blocks at both ends of a pool whose K and V take more than 2^32 bytes each."""
+    hkv, d = 2, 64
+    nb = (2 ** 32 + 2 ** 28) // (hkv * 16 * d) // (2 if dtype == "bf16" else 1)
+    pool = pkv.Pool(nb, hkv, d, dtype=dtype, **(dict(k_scale=0.03, v_scale=0.5) if dtype == "fp8_e4m3" else {}))
+    ends = [nb - 1, 0, nb - 2, 1, nb - 3]
+    ctx = 16 * len(ends) - 5
+    rng = np.random.default_rng(90)
+    bt = np.array([ends], np.int32)
+    pos = np.arange(ctx, dtype=np.int32)
+    rows = [torch.tensor(rng.standard_normal((ctx, hkv, d)), dtype=torch.float32).to(torch.bfloat16).cuda() for _ in range(2)]
+    i = lambda x: ref.dev(np.asarray(x, np.int32))
+    if dtype == "int8":
+        pkv.pkv_append_int8(pool, i(bt), i([0, ctx]), i(pos), i([0]), *rows)
+    else:
+        pkv.pkv_append(pool, i(bt), i([0, ctx]), i(pos), *rows)
+    small = pkv.Pool(len(ends), hkv, d, dtype=dtype, **(dict(k_scale=0.03, v_scale=0.5) if dtype == "fp8_e4m3" else {}))
+    near = np.arange(len(ends), dtype=np.int32)[None]
+    if dtype == "int8":
+        pkv.pkv_append_int8(small, i(near), i([0, ctx]), i(pos), i([0]), *rows)
+    else:
+        pkv.pkv_append(small, i(near), i([0, ctx]), i(pos), *rows)
+    q = torch.randn((ctx, 4, d), generator=torch.Generator().manual_seed(91)).to(torch.bfloat16).cuda()
+    for form in (1, 2):
+        got = []
+        for p, table in ((pool, bt), (small, near)):
+            pkv.pkv_debug_set(p, pkv.PKV_DEBUG_TREE_FORM, form)
+            got.append((pkv.pkv_read_rows(p, i(table), i([0, ctx]), i(pos)),
+                        pkv.pkv_score_attn(p, q, i(pos), i(table), i([ctx]), i([0, ctx]), 0.125, softcap=3.0, window=50)))
+            assert pkv.pkv_check_device_errors(p) == 0
+        for a, b in zip(got[0][0] + got[0][1], got[1][0] + got[1][1]):
+            assert torch.equal(a, b)
+    if dtype == "bf16":
+        assert torch.equal(got[0][0][0], rows[0]) and torch.equal(got[0][0][1], rows[1])
