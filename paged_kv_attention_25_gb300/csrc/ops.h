@@ -61,6 +61,7 @@ inline int cut_record(int block, int W, bool solo, int warp) { return block * W 
 int launch_tree_rows(const TreeArgs& a, void* stream);
 int launch_tree_tc(const TreeArgs& a, const void* tmk, const void* tmv, const void* tmq, void* stream);
 int launch_tree_merge(const TreeArgs& a, void* stream);
+int launch_score_merge(const TreeArgs& a, int row_tile, int64_t groups, void* stream);   // groups: at most, of the call
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
                      unsigned* err, void* stream);
 

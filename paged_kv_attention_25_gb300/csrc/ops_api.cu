@@ -583,7 +583,7 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   }
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "score attention launch");
   if (a.form.whole) return PKV_OK;
-  rc = timed_launch(pool, 3, stream, [&] { return launch_tree_merge(a, stream); });
+  rc = timed_launch(pool, 3, stream, [&] { return launch_score_merge(a, s.row_tile, groups, stream); });
   if (rc != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(rc), "score attention merge launch");
   return PKV_OK;
 }

@@ -433,11 +433,9 @@ rows_kernel(const TreeArgs a) {
 //   M = max LSE_c, LSE = M + log2 sum 2^(LSE_c - M), O = sum 2^(LSE_c - LSE) O_c
 // Bound by the latency of its loads (the record, then the partials): 304 cuts of up
 // to 512 rows in 19 us by itself, most of them read from L2; 1824 of 16 rows in 10.
-template <int D, int SlotRows>
+template <int D, int SlotRows, int kRows, int kBatch>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kDPL = D / 32;
-  constexpr int kRows = SlotRows >= 128 ? 4 : 2;
-  constexpr int kBatch = SlotRows >= 128 ? 2 : 4;
   griddep_wait();   // the attention kernel's writes
   const int lane = threadIdx.x & 31;
   const int row0 = (static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5)) * kRows;
@@ -464,9 +462,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     float e[kBatch][kRows], v[kBatch][kRows][kDPL];
 #pragma unroll
     for (int c = 0; c < kBatch; ++c) {
-      const int64_t at = slot_row(min(c0 + c, s.x - 1));
+      const int64_t at = slot_row(c0 + c);
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
+        e[c][k] = -CUDART_INF_F;
+        if (c0 + c >= s.x) continue;
         const int64_t r = at + (i0 + k < rows ? k : 0);
         e[c][k] = __ldcg(a.part_lse + r);
         const float* src = a.part_o + r * D + lane * kDPL;
@@ -483,10 +483,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     for (int k = 0; k < kRows; ++k) {
       float m = M[k];
 #pragma unroll
-      for (int c = 0; c < kBatch; ++c) {
-        if (c0 + c >= s.x) e[c][k] = -CUDART_INF_F;
-        m = fmaxf(m, e[c][k]);
-      }
+      for (int c = 0; c < kBatch; ++c) m = fmaxf(m, e[c][k]);
       if (m > M[k]) {
         const float f = M[k] == -CUDART_INF_F ? 1.f : fast_exp2(M[k] - m);   // (nothing, or NaN, summed so far)
         sum[k] *= f;
@@ -575,9 +572,9 @@ int launch_rows(const TreeArgs& a, cudaStream_t s) {
   return a.sel ? launch_rows_l<D, F8, true>(a, s) : launch_rows_l<D, F8, false>(a, s);
 }
 
-template <int D, int SlotRows>
-int launch_merge_t(const TreeArgs& a, int cuts, cudaStream_t s) {
-  return launch_dependent(tree_merge_kernel<D, SlotRows>, dim3(cuts, SlotRows >= 128 ? SlotRows / 32 : 1), 256, 0, s, a);
+template <int D, int SlotRows, int kRows, int kBatch>
+int launch_merge_t(const TreeArgs& a, int rows, cudaStream_t s) {
+  return launch_dependent(tree_merge_kernel<D, SlotRows, kRows, kBatch>, dim3(a.form.cuts, rows / (8 * kRows)), 256, 0, s, a);
 }
 
 }  // namespace
@@ -604,10 +601,25 @@ int launch_tree_rows(const TreeArgs& a, void* stream) {
 
 int launch_tree_merge(const TreeArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int n = a.form.cuts;
   if (a.form.tensor)
-    return a.pool.head_dim == 128 ? launch_merge_t<128, 256>(a, n, s) : launch_merge_t<64, 256>(a, n, s);
-  return a.pool.head_dim == 128 ? launch_merge_t<128, kRowTile>(a, n, s) : launch_merge_t<64, kRowTile>(a, n, s);
+    return a.pool.head_dim == 128 ? launch_merge_t<128, 256, 4, 2>(a, 256, s) : launch_merge_t<64, 256, 4, 2>(a, 256, s);
+  return a.pool.head_dim == 128 ? launch_merge_t<128, kRowTile, 2, 4>(a, kRowTile, s)
+                                : launch_merge_t<64, kRowTile, 2, 4>(a, kRowTile, s);
+}
+
+// (The scored attention's: tiles of 8 rows leave a warp one row, and one user's long context is cut into hundreds of
+// parts.  Rows, a warp a row with 32 registers of partials under way: 16 thousand tokens of 2 KV heads, D = 64, 12.6 us
+// with the attention, as above 17.0.  Tiles, fewer rows and more parts a warp where a group has many parts, from eight
+// CTAs a group on: 32 tokens on 100 thousand, 2 KV heads, 37 us, as above 50; 3 prompts of packed documents 43 and 40.)
+template <int D>
+int launch_score_merge_d(const TreeArgs& a, int row_tile, int64_t groups, cudaStream_t s) {
+  if (!a.form.tensor) return launch_merge_t<D, kRowTile, 1, 1024 / D>(a, row_tile, s);
+  return a.ctas >= 8 * groups ? launch_merge_t<D, 256, 2, 8>(a, 256, s) : launch_merge_t<D, 256, 4, 2>(a, 256, s);
+}
+int launch_score_merge(const TreeArgs& a, int row_tile, int64_t groups, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a.pool.head_dim == 128 ? launch_score_merge_d<128>(a, row_tile, groups, s)
+                                : launch_score_merge_d<64>(a, row_tile, groups, s);
 }
 
 int launch_tree_mask(const int32_t* parents, const int32_t* cu, int num_reqs, int num_tokens, uint32_t* mask, int words,
