@@ -27,8 +27,8 @@
 // five paired operations for two scores, while every score of the warp's rows stays
 // below half the cap; otherwise by tanh_small and tanh_large.  It is monotonic:
 // without a bias the raw products' maximum gives the scores', and the last operation
-// subtracts it (4 prompts of 1.8 to 5 thousand tokens 912 -> 791 us; scores written back
-// to TMEM before their maximum is known, as masked or biased ones still are).
+// subtracts it (4 prompts of 1.8 to 5 thousand tokens, 64 / 8 heads, D = 128: 778 us;
+// 912 with scores written back to TMEM first, as masked or biased ones still are).
 //
 // Pools of codes: they land in the upper half of each block's lines, and four more warps widen
 // them in place, two for K and two for V (int8: to bf16 times the block's power of
@@ -52,6 +52,9 @@
 namespace pkv {
 namespace {
 
+// What becomes of scores: a kernel for each, as code that does not run takes room in the instruction cache, too (the
+// capped prompts of the header 791 us with the code for a bias beside theirs, biased ones 900 us, now 823).
+enum { kPlain, kCapped, kBiased };   // kBiased: capped or not
 constexpr int kTeam = 2;   // codes: warps that widen K, and V
 // Registers of a CTA for codes, of 128 each at the launch.  Widening wants more (104: 5 % slower, 88: 20 %), and four
 // warps a team would leave it 48 (80 % slower).
@@ -648,9 +651,9 @@ __device__ __forceinline__ void tmem_wait_ld32(float (&v)[32]) {
 
 // A row's raw products with N keys (at `at` in TMEM; masked ones zero) to scores in log2 units; dpos: its position less
 // the first of the keys; valid: the row is the segment's (others have no say in what the warp does).
-template <int N>
+template <bool BIAS, int N>
 __device__ __forceinline__ void modify(float (&s)[N], uint32_t at, const ScoreArgs& a, float slope, int dpos, bool valid) {
-  if (a.cap_out != 0.f) {
+  if (!BIAS || a.cap_out != 0.f) {
     const CapPairs k(a);
     float top[2] = {0.f, 0.f};
 #pragma unroll
@@ -678,8 +681,8 @@ __device__ __forceinline__ void modify(float (&s)[N], uint32_t at, const ScoreAr
       for (int c = 0; c < N; c += 2) cap2(s[c], s[c + 1], k.q);
     }
   }
-  const float f = a.cap_out != 0.f ? 1.f : a.base;
-  if (a.slopes) {
+  if constexpr (BIAS) {
+    const float f = a.cap_out != 0.f ? 1.f : a.base;
     if (__all_sync(0xffffffffu, dpos >= N - 1)) {   // every key at or before the position: - slope (dpos - c)
       const float b = -slope * static_cast<float>(dpos);
 #pragma unroll
@@ -710,11 +713,12 @@ __device__ __forceinline__ void mask_scores(uint32_t at_s, V&& vis) {
   tmem_wait_st();
 }
 
-template <int D, int KIND, bool MOD>
+template <int D, int KIND, int HOW>
 __global__ void __launch_bounds__(kThreads<KIND>, 1)
 score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                const __grid_constant__ CUtensorMap tmap_q) {
   constexpr bool F8 = KIND == kPoolFp8;            // f16 operands
+  constexpr bool MOD = HOW != kPlain, BIAS = HOW == kBiased;
   constexpr bool kCodes = KIND != kPoolBf16;       // stages are widened
   const TreeArgs& a = sa.t;
   using S = TcSmem<D>;
@@ -1160,7 +1164,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       const int raw_pos = __ldg(a.positions + t_row), raw_first = sa.first_keys ? __ldg(sa.first_keys + t_row) : 0;
       const int pos = max(raw_pos, -1);
       float slope = 0.f;   // log2 units
-      if (MOD && sa.slopes) slope = sa.slopes[g * G + row % G] * 1.4426950408889634f;
+      if (BIAS) slope = sa.slopes[g * G + row % G] * 1.4426950408889634f;
       const int step = single ? 2 : 1;
       const int n = sg.kt1 - sg.kt0;
       const int nt = single ? (n + 1 - X) / 2 : n;    // key tiles of this group
@@ -1234,8 +1238,8 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         // Small capped scores (no bias, seen whole): the cap is monotonic, so that the largest raw product names the
         // largest score, and the raw products become P in one go.
         bool straight = false;
-        if constexpr (MOD) {
-          if (!masked && !sa.slopes) {
+        if constexpr (MOD && !BIAS) {
+          if (!masked) {
             float hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -1263,27 +1267,32 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           }
         }
         if (!straight) {
+          // (Short code again: 32 keys at a time where it is a detour.)
+          constexpr int kStep = MOD && !BIAS ? 32 : kAtOnce;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kNK; c0 += kAtOnce) {
-            load(c0);
+          for (int c0 = 0; c0 < kNK; c0 += kStep) {
+            float (&y)[kStep] = reinterpret_cast<float (&)[kStep]>(s);
+#pragma unroll
+            for (int c = 0; c < kStep; c += 16) tmem_ld16(at_s + c0 + c, y + c);
+            tmem_wait_ld();
             if constexpr (MOD) {
-              modify<kAtOnce>(s, at_s + c0, sa, slope, pos - key0 - c0, valid);
+              modify<BIAS, kStep>(y, at_s + c0, sa, slope, pos - key0 - c0, valid);
               if (masked) {   // (in words of 32)
 #pragma unroll
-                for (int w = 0; w < kAtOnce; w += 32) {
+                for (int w = 0; w < kStep; w += 32) {
                   const uint32_t v = vis(c0 + w);
 #pragma unroll
-                  for (int c = 0; c < 32; ++c) s[w + c] = (v >> c) & 1u ? s[w + c] : -CUDART_INF_F;
+                  for (int c = 0; c < 32; ++c) y[w + c] = (v >> c) & 1u ? y[w + c] : -CUDART_INF_F;
                 }
               }
 #pragma unroll
-              for (int c = 0; c < kAtOnce; c += 16) tmem_st16(at_s + c0 + c, s + c);
+              for (int c = 0; c < kStep; c += 16) tmem_st16(at_s + c0 + c, y + c);
             }
             float mx8[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+            for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(y[2 * k], y[2 * k + 1]);
 #pragma unroll
-            for (int c = 16; c < kAtOnce; c += 2) mx8[(c >> 1) & 7] = max3f(mx8[(c >> 1) & 7], s[c], s[c + 1]);
+            for (int c = 16; c < kStep; c += 2) mx8[(c >> 1) & 7] = max3f(mx8[(c >> 1) & 7], y[c], y[c + 1]);
             mx = max3f(mx, max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])), mx);
           }
         }
@@ -1319,7 +1328,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
             }
           }
         };
-        if constexpr (MOD) {
+        if constexpr (MOD && !BIAS) {
           if (straight) to_p(std::true_type{});
           else to_p(std::false_type{});
         } else {
@@ -1470,16 +1479,17 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
   }
 }
 
-template <int D, int KIND, bool MOD>
+template <int D, int KIND, int HOW>
 int launch_m(const ScoreArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* tq, cudaStream_t s) {
   const int smem = ScoreSmem<D>::kTotal;
-  const cudaError_t e = smem_attr_once<score_tc_kernel<D, KIND, MOD>>(smem);
+  const cudaError_t e = smem_attr_once<score_tc_kernel<D, KIND, HOW>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(score_tc_kernel<D, KIND, MOD>, dim3(a.t.ctas), kThreads<KIND>, smem, s, a, *tk, *tv, *tq);
+  return launch_dependent(score_tc_kernel<D, KIND, HOW>, dim3(a.t.ctas), kThreads<KIND>, smem, s, a, *tk, *tv, *tq);
 }
 template <int D, int KIND>
 int launch_k(const ScoreArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* tq, cudaStream_t s) {
-  return a.cap_out != 0.f || a.slopes ? launch_m<D, KIND, true>(a, tk, tv, tq, s) : launch_m<D, KIND, false>(a, tk, tv, tq, s);
+  if (a.slopes) return launch_m<D, KIND, kBiased>(a, tk, tv, tq, s);
+  return a.cap_out != 0.f ? launch_m<D, KIND, kCapped>(a, tk, tv, tq, s) : launch_m<D, KIND, kPlain>(a, tk, tv, tq, s);
 }
 
 }  // namespace
