@@ -1110,15 +1110,16 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         const bool more = walk.next(sa, s, cut);
         if (more) {
           if (cut.count > 0 && lane == 0) a.cuts[blockIdx.x] = cut;
-          // Blocks that are not there: flagged here, and only then looked for by the softmax warps.
+          // Blocks that some row sees and that are not there: flagged here, and only then looked for by the softmax warps.
+          // (The table may hold anything for the others, pages freed behind a window for instance.)
           const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
           const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
           bool gone = false;
           for (int x = s.kt0 * kBlkPerTile + lane; x < s.kt1 * kBlkPerTile; x += 32) {
-            const int b = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap) * kBlkPerTile + x % kBlkPerTile;
+            const int tile = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap), b = tile * kBlkPerTile + x % kBlkPerTile;
             if (b >= nblk) continue;
             const int pb = __ldg(bt_row + b);
-            gone |= pb < 0 || pb >= a.pool.num_blocks;
+            if (pb < 0 || pb >= a.pool.num_blocks) gone |= (blocks_needed(s, tile * kNK) >> (x % kBlkPerTile)) & 1u;
           }
           if (__any_sync(0xffffffffu, gone)) {
             s.flags |= kSegMissing;
@@ -1190,7 +1191,8 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         }
         mbar_arrive(&bars[B::kQc + X]);
       }
-      // Blocks that are not there, as bits: window of 32 blocks (four key tiles) at a time.
+      // Blocks that are not there, as bits: window of 32 blocks (four key tiles) at a time.  (Where no row sees such a
+      // block its keys are masked anyway.)
       const int32_t* bt_row = a.block_tables + static_cast<int64_t>(sg.req) * a.max_blocks;
       const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize;
       auto missing_of = [&](int w) -> uint32_t {

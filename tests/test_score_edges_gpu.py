@@ -1,0 +1,76 @@
+"""Attention with modified scores at the edges of what its documentation allows: tables with invalid ids where nobody looks,
+tokens that see nothing, the corners of the cap's range, batches of more requests and items than the plan keeps at hand."""
+import numpy as np
+import pytest
+import torch
+
+import attn_ref as ref
+import score_ref
+from paged_kv_attention_25_gb300 import pkv
+from test_score_gpu import DTYPES, Case, built, tail  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+FORMS = pytest.mark.parametrize("form", [1, 2], ids=["rows", "tiles"])
+TYPES = pytest.mark.parametrize("dtype", DTYPES)
+
+
+def forced(case, form):
+    pkv.pkv_debug_set(case.pool, pkv.PKV_DEBUG_TREE_FORM, form)
+    return case
+
+
+def unseen_blocks(c):
+    """(request, block) pairs of the table of which no token of the request sees a key, beyond the context among them."""
+    out = []
+    for r in range(len(c.ctx)):
+        ctx = int(c.ctx[r])
+        seen = np.zeros(c.bt.shape[1] * 16, bool)
+        for t in range(c.cu[r], c.cu[r + 1]):
+            seen[:ctx] |= score_ref.sees(int(c.pos[t]), ctx, 0 if c.prefix is None else int(c.prefix[r]),
+                                         0 if c.first is None else int(c.first[t]), c.window)
+        out += [(r, b) for b in np.nonzero(~seen.reshape(-1, 16).any(1))[0]]
+    return out
+
+
+def check_unseen_ids(c, inside):
+    """Bad ids in the blocks that nobody sees, `inside` of them within the contexts at least, change nothing and are no error."""
+    want = c.call()
+    c.check(*want)
+    assert pkv.pkv_check_device_errors(c.pool) == 0
+    gone = unseen_blocks(c)
+    assert sum(b * 16 < c.ctx[r] for r, b in gone) >= inside
+    for i, (r, b) in enumerate(gone):
+        c.bt[r, b] = (-1, c.pool.num_blocks, -2 ** 31, 2 ** 31 - 1)[i % 4]
+    got = c.call()
+    assert pkv.pkv_check_device_errors(c.pool) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+UNSEEN = {
+    # windows that begin anywhere in a tile of 128 keys, with and without a few leading tokens
+    "window": ([tail(700, 3), tail(391, 9), tail(200, 1), tail(129, 2)], dict(window=100), 60),
+    "window_prefix": ([tail(700, 3), tail(391, 9), tail(200, 1)], dict(window=45, prefix=[5, 17, 0]), 60),
+    "window_cap_slopes": ([tail(523, 40), tail(260, 2)], dict(window=33, softcap=4.0, slopes=True), 40),
+    # positions well below the contexts' ends
+    "behind": ([(400, [100, 101, 102, 103]), (300, [0]), (150, list(range(20, 60)))], {}, 35),
+    # prompts of several tiles whose first tokens have left the window of the last
+    "prompts": ([tail(1500, 300), tail(900, 150)], dict(window=70), 100),
+}
+
+
+@FORMS
+@TYPES
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", list(UNSEEN))
+def test_block_ids_that_nobody_sees_are_not_looked_at(what, d, dtype, form):
+    reqs, opts, inside = UNSEEN[what]
+    check_unseen_ids(forced(Case(100, reqs, 8, 2, d, dtype, **opts), form), inside)
+
+
+@FORMS
+@TYPES
+def test_block_ids_before_a_document(dtype, form):
+    c = forced(Case(101, [tail(600, 50), tail(333, 3)], 8, 2, 64, dtype), form)
+    c.first = np.concatenate([np.full(50, 505), np.full(3, 300)]).astype(np.int32)
+    check_unseen_ids(c, 45)
