@@ -24,7 +24,7 @@ LIB = os.path.join(BUILD, "libpkv.so")
 SOURCES = ["api.cu", "plan.cpp", "cache.cpp", "decode.cu", "attn_tc.cu", "merge_append.cu", "attn_static.cu", "swap.cu",
            "ops_api.cu", "tree.cu", "tree_tc.cu", "sparse.cu", "pages.cu", "int8.cu", "score.cu", "score_tc64.cu", "score_tc128.cu"]
 HEADERS = ["internal.h", "pool.h", "ptx.cuh", "append.cuh", "merge.cuh", "ops.h", "rows.cuh", "sched.cuh",
-           "tc.cuh", "int8.cuh", "score.cuh", "score_tc.cuh"]
+           "tc.cuh", "int8.cuh", "score.cuh", "score_cap.h", "score_tc.cuh"]
 BINDING = os.path.join(BUILD, "pkv_binding.so")
 BINDING_STAMP = os.path.join(BUILD, "pkv_binding.stamp")   # binding_key(), and "built" or "left out"
 BINDING_SOURCE = "binding.cpp"

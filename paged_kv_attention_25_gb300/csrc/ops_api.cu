@@ -18,6 +18,7 @@
 #include "pool.h"
 #include "sched.cuh"
 #include "score.cuh"
+#include "score_cap.h"
 
 using namespace pkv;
 
@@ -544,14 +545,9 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   if (d.softcap > 0.f) {
     s.base /= d.softcap;
     s.cap_out = d.softcap * 1.4426950408889634f;
-    // cap_out tanh(base x) for |base x| < 1/2 as x (q0 + q1 x^2 + q2 x^4 + q3 x^6): tanh(y) / y interpolated at Chebyshev
-    // nodes of y^2 in [0, 1/4], off by 6e-7 of it.  (Where the powers of base leave fp32's range nothing counts as small.)
-    if (s.base >= 0x1p-15f && s.base <= 0x1p15f) {
-      s.cap_small = 0.5f / s.base;
-      const double c[4] = {0.9999994510270872, -0.3332628423141671, 0.13189939425594752, -0.04439273843261177};
-      double f = static_cast<double>(s.base) * s.cap_out;
-      for (int i = 0; i < 4; ++i, f *= static_cast<double>(s.base) * s.base) s.cap_q[i] = static_cast<float>(c[i] * f);
-    }
+    const CapPoly poly = cap_poly(s.base, s.cap_out);
+    s.cap_small = poly.small;
+    std::copy(poly.q, poly.q + 4, s.cap_q);
   } else {
     s.base *= 1.4426950408889634f;
   }

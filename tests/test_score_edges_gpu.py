@@ -74,3 +74,21 @@ def test_block_ids_before_a_document(dtype, form):
     c = forced(Case(101, [tail(600, 50), tail(333, 3)], 8, 2, 64, dtype), form)
     c.first = np.concatenate([np.full(50, 505), np.full(3, 300)]).astype(np.int32)
     check_unseen_ids(c, 45)
+
+
+@FORMS
+@pytest.mark.parametrize("scale,softcap", [(2.0 ** 44, 2.0 ** 29), (2.0 ** 10, 2.0 ** -9), (2.0 ** -40, 2.0 ** -18), (2.0 ** 30, 2.0 ** 30)])
+def test_caps_and_scales_far_from_one(scale, softcap, form):
+    """Queries as small as the scale is large (and the reverse), so that scores lie on both sides of half the cap, where that
+    is anything: products of powers of two, exact in every step before the cap."""
+    c = forced(Case(110, [tail(200, 20)], 4, 2, 64, scale=scale, softcap=softcap), form)
+    size = min(softcap, 8.0) / scale / 8
+    c.q = (c.q.float() * 2.0 ** round(np.log2(size))).to(torch.bfloat16)
+    o, lse = c.call()
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    if softcap >= 2.0 ** 20:      # scores below 2^-17 of the cap: the formula without it is off by 2^-35 of them, and its bounds
+        c.cap = 0.0               # hold, as the polynomial's 6e-7 of a score below 32 is less than their 2^-15
+    c.check(o, lse)
+    c.q = torch.zeros_like(c.q)
+    c.check(*c.call())
+    assert pkv.pkv_check_device_errors(c.pool) == 0
