@@ -531,7 +531,9 @@ int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int
  * bytes for the same sizes, 256-byte aligned, used by one call at a time as for
  * pkv_tree_attn.  num_tokens == 0 is a no-op.
  * Errors: PKV_EINVAL (softcap neither 0 nor in 2^-30 .. 2^30, window < 0, bad shapes, a
- * workspace that is too small), PKV_EUNSUPPORTED, PKV_ECUDA.
+ * workspace that is too small, a scale (FP8: times k_scale) that is no normal number of
+ * fp32 when divided by softcap or, without one, multiplied by log2 e), PKV_EUNSUPPORTED,
+ * PKV_ECUDA.
  */
 typedef struct {
   float softcap;              /* 0: none */

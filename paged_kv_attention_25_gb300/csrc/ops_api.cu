@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <mutex>
 
 #include "internal.h"
@@ -509,12 +510,17 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   int rc = check_tables(max_blocks, num_reqs, num_tokens);
   if (rc) return rc;
   const pkv_score_desc d = score ? *score : pkv_score_desc{};
-  // (So that scale / softcap times a product of q and K stays in fp32's range.)
   if (!(d.softcap == 0.f || (d.softcap >= 0x1p-30f && d.softcap <= 0x1p30f)))
     return fail(PKV_EINVAL, "softcap must be 0 or in 2^-30 .. 2^30");
   if (d.window < 0) return fail(PKV_EINVAL, "window must be >= 0");
   if (num_tokens == 0) return PKV_OK;
   if ((rc = check_heads(pool, num_q_heads)) || (rc = check_scale(scale))) return rc;
+  // What raw products are multiplied with: infinite it would make NaN of a product of 0, as 0 of a masked key's -inf;
+  // between 0 and the normal numbers it would lack bits of scores that large products bring back into range.
+  float base = scale * (pool->k_exps || pool->elem_bytes == 2 ? 1.f : pool->k_scale);
+  base = d.softcap > 0.f ? base / d.softcap : base * 1.4426950408889634f;
+  if (!std::isnormal(base))
+    return fail(PKV_EINVAL, "scale (FP8 pools: times k_scale), over softcap if there is one, is out of fp32's range");
   if (!q || !q_positions || !block_tables || !ctx_lens || !cu_q_lens || !o) return fail(PKV_EINVAL, "NULL device pointer");
   if (!aligned16(q) || !aligned16(o)) return fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (static_cast<int64_t>(num_tokens) * num_q_heads >= (1ll << 31)) return fail(PKV_EUNSUPPORTED, "too many query rows");
@@ -541,15 +547,12 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
   a.positions = q_positions;
   a.o = o;
   a.lse = lse;
-  s.base = scale * (pool->k_exps || pool->elem_bytes == 2 ? 1.f : pool->k_scale);
+  s.base = base;
   if (d.softcap > 0.f) {
-    s.base /= d.softcap;
     s.cap_out = d.softcap * 1.4426950408889634f;
     const CapPoly poly = cap_poly(s.base, s.cap_out);
     s.cap_small = poly.small;
     std::copy(poly.q, poly.q + 4, s.cap_q);
-  } else {
-    s.base *= 1.4426950408889634f;
   }
   s.slopes = d.slopes;
   s.window = d.window;

@@ -92,3 +92,26 @@ def test_caps_and_scales_far_from_one(scale, softcap, form):
     c.q = torch.zeros_like(c.q)
     c.check(*c.call())
     assert pkv.pkv_check_device_errors(c.pool) == 0
+
+
+@FORMS
+def test_scales_whose_products_leave_fp32_are_refused(form):
+    """scale, scale * k_scale or their quotient by softcap, as the scores are made with them, have to be normal numbers."""
+    f32 = lambda x: float(np.float32(x))
+    ok = [("bf16", 2.0 ** 126, 0.0, 1.0), ("fp8_e4m3", 2.0 ** 96, 0.0, 2.0 ** 30), ("fp8_e4m3", 2.0 ** -63, 0.0, 2.0 ** -63),
+          ("bf16", 2.0 ** 97, 2.0 ** -30, 1.0), ("bf16", 2.0 ** -96, 2.0 ** 30, 1.0)]
+    bad = [("bf16", f32(3e38), 0.0, 1.0), ("fp8_e4m3", 2.0 ** 98, 0.0, 2.0 ** 30), ("bf16", 2.0 ** 98, 2.0 ** -30, 1.0),
+           ("bf16", 2.0 ** -97, 2.0 ** 30, 1.0), ("fp8_e4m3", 2.0 ** -40, 2.0, 2.0 ** -100), ("int8", f32(3e38), 0.0, 1.0),
+           ("fp8_e4m3", f32(1e-30), 0.0, f32(1e-30)), ("bf16", 2.0 ** -128, 0.0, 1.0)]
+    for i, (dtype, scale, softcap, k_scale) in enumerate(ok + bad):
+        c = Case(120, [tail(20, 2)], 4, 2, 64, dtype, scale=scale, softcap=softcap)
+        if dtype == "fp8_e4m3":
+            c.pool = pkv.Pool(c.pool.num_blocks, 2, 64, dtype=dtype, k_scale=k_scale, v_scale=0.5)
+        forced(c, form)
+        c.q = torch.zeros_like(c.q)          # (scores of zero whatever the scale)
+        if i < len(ok):
+            c.check(*c.call())
+            continue
+        with pytest.raises(pkv.PkvError) as e:
+            c.call()
+        assert e.value.code == pkv.PKV_EINVAL
