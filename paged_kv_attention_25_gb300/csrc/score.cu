@@ -32,21 +32,24 @@ constexpr int kManyTokens = 64;   // a request of more tokens is planned as if t
 using RowsShare = Share<4 * kRowWarps>;   // few groups: four blocks a warp at least
 using WarpShare = Share<4>;
 
-// Factors of one block: of its scores (raw products to log2 units, or to the cap's argument), of P.
+// Factors of one block: of its scores (raw products to log2 units, or to the cap's argument; int8: the block's power of
+// two alone, which with Modify::base in one factor could leave fp32's range), of P.
 struct BlockFactor {
   float score, value;
 };
-// Raw products of widened codes are in units of 2^-kWidenShift (by itself: the factor of
-// the largest exponent would leave fp32's range).
-template <int KIND> constexpr float kRawUnit = KIND == kPoolInt8 ? static_cast<float>(1 << kWidenShift) : 1.f;
 // What becomes of the scores of rows g and g + 8 of a thread.
 struct Modify {
+  float base;          // int8: what products are multiplied with, beside the block's power
   bool on;             // cap or slopes
   float cap_out;       // 0: no cap
   bool slopes;
   float slope0, slope1;   // log2 units
   int p0, p1;          // positions
 };
+template <int KIND>
+__device__ __forceinline__ float raw_score(float s, const BlockFactor& f, const Modify& mod) {
+  return (KIND == kPoolInt8 ? s * mod.base : s) * f.score;
+}
 
 template <int D, int KIND>
 struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
@@ -98,7 +101,7 @@ struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][t][e] = s[n][t][e] * kRawUnit<KIND> * f[n].score;
+        for (int e = 0; e < 4; ++e) s[n][t][e] = raw_score<KIND>(s[n][t][e], f[n], mod);
     if (!mod.on) return;
     if (mod.cap_out != 0.f) {
       float top = 0.f;
@@ -512,7 +515,7 @@ struct ScoreCol {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = s[n][e] * kRawUnit<KIND> * f[n].score;
+      for (int e = 0; e < 4; ++e) s[n][e] = raw_score<KIND>(s[n][e], f[n], mod);
     if (!mod.on) return;
     if (mod.cap_out != 0.f) {
       float top = 0.f;
@@ -840,7 +843,7 @@ score_rows_kernel(const ScoreArgs a) {
     };
     const int ta = tok_of(ra), tb = tok_of(rb);
     const KeySpan sa = key_span(a, ta, rq.ctx), sb = key_span(a, tb, rq.ctx);
-    Modify mod{cap || a.slopes != nullptr, a.cap_out, a.slopes != nullptr, 0.f, 0.f,
+    Modify mod{a.base, cap || a.slopes != nullptr, a.cap_out, a.slopes != nullptr, 0.f, 0.f,
                max(__ldg(t.positions + ta), -1), max(__ldg(t.positions + tb), -1)};
     if (mod.slopes) {
       mod.slope0 = a.slopes[g * G + (row0 + min(ra, nrows - 1)) % G] * 1.4426950408889634f;
@@ -907,7 +910,7 @@ score_rows_kernel(const ScoreArgs a) {
       BlockFactor f{a.base, 1.f};
       if constexpr (KIND == kPoolInt8) {
         const int e = __shfl_sync(0xffffffffu, exps_cur, i & 31);
-        f.score *= exp_f32(static_cast<int16_t>(e & 0xffff));
+        f.score = exp_f32(static_cast<int16_t>(e & 0xffff) + kWidenShift);
         f.value = exp_f32((e >> 16) + kWidenShift);
       }
       return f;

@@ -115,3 +115,14 @@ def test_scales_whose_products_leave_fp32_are_refused(form):
         with pytest.raises(pkv.PkvError) as e:
             c.call()
         assert e.value.code == pkv.PKV_EINVAL
+
+
+@FORMS
+def test_int8_keys_of_the_largest_exponent(form):
+    """Products that are zero give scores of zero whatever the exponent and the scale; those that are not are fp32 numbers."""
+    c = forced(Case(121, [tail(80, 3), tail(33, 1)], 4, 2, 64, "int8", scale=200.0), form)
+    c.pool.k_exps.fill_(121)
+    c.q = torch.zeros_like(c.q)
+    c.q[1, 2, 5] = 2.0 ** -120
+    c.check(*c.call())
+    assert pkv.pkv_check_device_errors(c.pool) == 0
