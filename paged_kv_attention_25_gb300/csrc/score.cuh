@@ -49,7 +49,8 @@ struct ScoreArgs {
   ScorePlan plan;             // tiles form
 };
 
-// The keys behind the prefix that a token sees: [lo, hi] (hi < lo: none).
+// The keys behind the prefix that a token sees: [lo, hi].  None: [ctx, -1], so that a token without keys (a document that
+// begins behind it, a position in front of the sequence) does not widen what the others of its tile see.
 struct KeySpan {
   int lo, hi;
 };
@@ -57,8 +58,7 @@ __device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int pos, int fir
   const int p = max(pos, -1);
   KeySpan s{max(first, 0), min(p, ctx - 1)};
   if (a.window > 0) s.lo = max(s.lo, p - a.window + 1);
-  s.lo = min(s.lo, ctx);
-  return s;
+  return s.hi < s.lo ? KeySpan{ctx, -1} : s;
 }
 __device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int ctx) {
   return key_span(a, __ldg(a.t.positions + t), a.first_keys ? __ldg(a.first_keys + t) : 0, ctx);

@@ -126,3 +126,19 @@ def test_int8_keys_of_the_largest_exponent(form):
     c.q[1, 2, 5] = 2.0 ** -120
     c.check(*c.call())
     assert pkv.pkv_check_device_errors(c.pool) == 0
+
+
+@FORMS
+@TYPES
+def test_tokens_that_see_nothing_do_not_widen_what_is_read(dtype, form):
+    """A document that begins behind its token, a token in front of the sequence: the blocks between are still nobody's."""
+    c = forced(Case(122, [(700, [20, 690, 21, 691]), (512, [100, 500])], 8, 2, 64, dtype, window=30), form)
+    c.first = np.array([300, 600, 22, 0, 400, 0], np.int32)
+    c.pos[2] = 21
+    check_unseen_ids(c, 60)
+    c = forced(Case(123, [(700, [3, 690, 691])], 8, 2, 64, dtype, window=30, prefix=[7]), form)
+    c.pos[0] = -5
+    for r, b in unseen_blocks(c):
+        c.bt[r, b] = -1
+    c.check(*c.call())
+    assert pkv.pkv_check_device_errors(c.pool) == pkv.PKV_DEVERR_POSITION
