@@ -271,26 +271,25 @@ __device__ __forceinline__ int pairs_of(const ScoreReq& q, int tile_tokens) {
   return (q.n + 2 * tile_tokens - 1) / (2 * tile_tokens);
 }
 // Exclusive scan of x over the block's threads; `carry` is added and becomes the total.
-template <class T>
-__device__ __forceinline__ T block_scan(T x, T& carry, T* scratch) {
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t& carry, int64_t* scratch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  T inc = x;
+  int64_t inc = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, inc, d);
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += y;
   }
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
-  T w = scratch[lane];
+  int64_t w = scratch[lane];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, w, d);
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, d);
     if (lane >= d) w += y;
   }
-  const T all = __shfl_sync(0xffffffffu, w, 31), before = warp ? __shfl_sync(0xffffffffu, w, (warp - 1) & 31) : T(0);
+  const int64_t all = __shfl_sync(0xffffffffu, w, 31), before = warp ? __shfl_sync(0xffffffffu, w, (warp - 1) & 31) : 0;
   __syncthreads();
-  const T r = carry + before + inc - x;
+  const int64_t r = carry + before + inc - x;
   carry += all;
   return r;
 }
@@ -313,7 +312,10 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
   griddep_launch();
   const bool kept = R <= kPlanReqs;
   int* const first = a.plan.first;   // items before each request's
-  int n_items = 0;
+  // (Counted in 64 bits and cut: ranges of tokens that overlap could make more items than there is room for, or than 32
+  // bits hold.  An item looked for below lies before the cut, where the sums are whole.)
+  const int64_t most = a.plan.most;
+  int64_t count = 0;
 #pragma unroll 1
   for (int base = 0; base < R; base += kPlanThreads) {
     ScoreReq q{0, 0, 0, 0, false};
@@ -323,12 +325,12 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
       n = pairs_of(q, tt);
       if (q.bad) atomicOr(a.t.pool.err, PKV_DEVERR_POSITION);
     }
-    const int f = block_scan(n, n_items, reinterpret_cast<int*>(scratch));
+    const int f = static_cast<int>(min(block_scan(static_cast<int64_t>(n), count, scratch), most));
     if (kept) s_req[tid] = PlanReq{q.t0, q.n, q.ctx, q.prefix, f};
     else if (base + tid < R) first[base + tid] = f;
   }
   __syncthreads();
-  n_items = min(n_items, a.plan.most);   // (ranges that overlap could make more)
+  const int n_items = static_cast<int>(min(count, most));
   const bool costs = n_items <= kPlanItems;
   const int rounds = (n_items + kPlanThreads / kPlanLanes - 1) / (kPlanThreads / kPlanLanes);
 #pragma unroll 1

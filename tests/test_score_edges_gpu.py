@@ -7,7 +7,7 @@ import torch
 import attn_ref as ref
 import score_ref
 from paged_kv_attention_25_gb300 import pkv
-from test_score_gpu import DTYPES, Case, built, tail  # noqa: F401
+from test_score_gpu import DTYPES, Case, built, make_pool, tail, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +142,22 @@ def test_tokens_that_see_nothing_do_not_widen_what_is_read(dtype, form):
         c.bt[r, b] = -1
     c.check(*c.call())
     assert pkv.pkv_check_device_errors(c.pool) == pkv.PKV_DEVERR_POSITION
+
+
+def test_token_ranges_that_overlap_beyond_32_bits():
+    """Half of 180 thousand requests claim all of 100 thousand tokens each: 4.5e9 pairs of tiles, cut to what the plan has
+    room for and flagged.  All requests have the same page, so that whoever writes a row writes the same."""
+    tokens, reqs, hq, d = 100_000, 180_000, 128, 64
+    pool = make_pool(3, 1, d, "bf16", 130)
+    pkv.pkv_debug_set(pool, pkv.PKV_DEBUG_TREE_FORM, 2)
+    q = torch.randn((tokens, hq, d), generator=torch.Generator("cuda").manual_seed(131), device="cuda").to(torch.bfloat16)
+    i32 = lambda n, x: torch.full((n,), x, dtype=torch.int32, device="cuda")
+    cu = i32(reqs + 1, 0)
+    cu[1::2] = tokens
+    o, lse = pkv.pkv_score_attn(pool, q, i32(tokens, 5), i32(reqs, 1).view(-1, 1), i32(reqs, 16), cu, 0.125)
+    assert pkv.pkv_check_device_errors(pool) == pkv.PKV_DEVERR_POSITION
+    k, v = (values(pool, w)[1, 0] for w in "kv")
+    for t in (0, 1, 49_999, 77_776, tokens - 1):
+        want, wl, tol, tl = score_ref.rows(q[t].double().cpu().numpy(), k, v, 5, np.arange(16) <= 5, 0.125, 0.0, None, False)
+        ref.assert_close(o[t].double().cpu().numpy(), want, tol, f"O of token {t}")
+        ref.assert_close(lse[t].double().cpu().numpy(), wl, tl, f"LSE of token {t}")
