@@ -161,3 +161,108 @@ def test_token_ranges_that_overlap_beyond_32_bits():
         want, wl, tol, tl = score_ref.rows(q[t].double().cpu().numpy(), k, v, 5, np.arange(16) <= 5, 0.125, 0.0, None, False)
         ref.assert_close(o[t].double().cpu().numpy(), want, tol, f"O of token {t}")
         ref.assert_close(lse[t].double().cpu().numpy(), wl, tl, f"LSE of token {t}")
+
+
+@TYPES
+@pytest.mark.parametrize("reqs,toks,hq", [(1100, 1, 8), (5, 900, 128), (1500, 3, 128)],
+                         ids=["many_requests", "many_items", "both"])
+def test_plans_beyond_what_is_kept_at_hand(reqs, toks, hq, dtype):
+    """More than 1,024 requests, more than 2,048 items of two tiles (tiles of one token with 128 rows), and both."""
+    rng = np.random.default_rng(132)
+    ctxs = rng.integers(toks, toks + 40, reqs)
+    c = forced(Case(133, [tail(int(x), toks) for x in ctxs], hq, 1, 64, dtype, extra=2, window=30, softcap=6.0), 2)
+    o, lse = c.call()
+    last = len(c.pos) - 3
+    c.check(o, lse, {0, 1, 2, last // 2, last - 1, last} | set(rng.integers(0, last, 40).tolist()))
+    assert torch.isfinite(o[:last + 1]).all() and torch.isfinite(lse[:last + 1]).all()
+    assert pkv.pkv_check_device_errors(c.pool) == 0
+    # Every request and tile is served: as in the rows form.  Each is off by 2^-8 A for P and 2^-8 |O| for O, A and |O| at
+    # most the largest |v|, and by half as much again for everything else.
+    pkv.pkv_debug_set(c.pool, pkv.PKV_DEBUG_TREE_FORM, 1)
+    p, m = c.call()
+    most = np.abs(values(c.pool, "v")).max()
+    assert (o[:last + 1].float() - p[:last + 1].float()).abs().max() <= 2 * 2.5 * 2.0 ** -8 * most
+    assert (lse[:last + 1] - m[:last + 1]).abs().max() <= 1e-3
+
+
+@TYPES
+@pytest.mark.parametrize("form", [1, 2], ids=["rows", "tiles"])
+def test_rows_without_a_key_in_every_type(dtype, form):
+    """(And documents that leave some tokens nothing, and requests without a context.)"""
+    c = forced(Case(134, [tail(40, 3), tail(300, 7), tail(16, 2), (0, []), tail(129, 5), tail(2, 2)], 8, 2, 128, dtype, docs=5), form)
+    c.run()
+    assert c.seen_empty
+
+
+@TYPES
+@pytest.mark.parametrize("form", [1, 2], ids=["rows", "tiles"])
+def test_scores_beyond_the_cap_in_every_type(dtype, form):
+    reqs = [tail(50, 50), tail(200, 3)]
+    forced(Case(135, reqs, 8, 2, 64, dtype, softcap=30.0, scale=40.0), form).run()
+    forced(Case(136, reqs, 8, 2, 128, dtype, softcap=5.0, slopes=True, scale=3.0), form).run()
+    c = forced(Case(137, reqs, 4, 2, 64, dtype, slopes=True), form)
+    c.slopes = np.array([100.0, -0.25, 0.0, 1e-3], np.float32)
+    c.run()
+
+
+@FORMS
+def test_exponents_outside_their_range_are_read_as_the_nearest(form):
+    """Pages that the table names, with exponents that no append writes.  K: large ones, under queries small enough; V: one page
+    of large ones (codes of at most 1: 16 of them stay in fp32's range), then small ones alone, and zeros under any."""
+    c = forced(Case(140, [tail(90, 4), tail(33, 2)], 4, 2, 64, "int8"), form)
+    gen = torch.Generator("cuda").manual_seed(141)
+    sign = torch.where(torch.rand(c.q.shape) < 0.5, -1.0, 1.0)
+    big, tiny, zero = (c.bt[0][1], c.bt[1][0]), (c.bt[0][0], c.bt[1][1]), c.bt[0][3]
+    for i, e in zip(big, (127, 122)):
+        c.pool.k[i] = torch.randint(-3, 4, c.pool.k[i].shape, generator=gen, device="cuda")
+        c.pool.k_exps[i] = e
+    for i, e in zip(tiny, (-128, -127)):
+        c.pool.k_exps[i] = e
+    c.pool.k[zero], c.pool.k_exps[zero] = 0, 127
+    c.q = (sign * (0.5 + torch.rand(c.q.shape))).mul(2.0 ** -119).to(torch.bfloat16)
+    c.check(*c.call())
+    c.q = (sign * torch.rand(c.q.shape)).to(torch.bfloat16)
+    for i in big:
+        c.pool.k_exps[i] = -7
+    c.pool.v[big[0]] = torch.randint(-1, 2, c.pool.v[big[0]].shape, generator=gen, device="cuda")
+    c.pool.v_exps[big[0]] = 127
+    c.pool.v[zero], c.pool.v_exps[zero] = 0, 122
+    c.check(*c.call())
+    assert pkv.pkv_check_device_errors(c.pool) == 0
+
+
+@FORMS
+def test_int8_values_below_bf16s_weights(form):
+    """Exponents of -126 and below everywhere.  The rows form's weights times 2^e (times 2^6, the widening's) are bf16
+    numbers below its normal ones: each is off by 2^-134 at most, times a code of 127 / 64 at most, 2^-133 a key; O is
+    off by 2^-134 where it has no normal bf16 number."""
+    c = forced(Case(142, [tail(150, 4), tail(33, 2), tail(600, 1)], 8, 2, 64, "int8"), form)
+    for e in (-126, -128):
+        c.pool.v_exps.fill_(e)
+        o, lse = c.call()
+        o, lse = o.cpu().double().numpy(), lse.cpu().double().numpy()
+        k, v, q = values(c.pool, "k"), values(c.pool, "v"), c.q.double().numpy()
+        for r in range(3):
+            ctx = int(c.ctx[r])
+            for g in range(2):
+                kk, vv = (ref.gather(x, c.bt[r], ctx, g)[0] for x in (k, v))
+                hs = slice(4 * g, 4 * g + 4)
+                for t in range(c.cu[r], c.cu[r + 1]):
+                    seen = np.arange(ctx) <= c.pos[t]
+                    want, wl, tol, tl = score_ref.rows(q[t, hs], kk, vv, int(c.pos[t]), seen, c.scale, 0.0, None, False)
+                    ref.assert_close(o[t, hs], want, tol + seen.sum() * 2.0 ** -133 + 2.0 ** -134, f"O of token {t}")
+                    ref.assert_close(lse[t, hs], wl, tl, f"LSE of token {t}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_read_back_with_exponents_outside_their_range(d):
+    pool = make_pool(5, 3, d, "int8", 143)
+    exps = [-128, -127, -126, 121, 122]
+    for i, e in enumerate(exps):
+        pool.k_exps[i], pool.v_exps[i] = e, (127 if e == 122 else e)
+    pos = np.arange(80, dtype=np.int32)
+    k, v = pkv.pkv_read_rows(pool, ref.dev(np.arange(5, dtype=np.int32)[None]), ref.dev(np.array([0, 80], np.int32)), ref.dev(pos))
+    for got, which in ((k, "k"), (v, "v")):
+        want = values(pool, which).transpose(0, 2, 1, 3).reshape(80, 3, d)
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    assert pkv.pkv_check_device_errors(pool) == 0
