@@ -558,14 +558,15 @@ int pkv_score_attn(pkv_pool* pool, const void* q, int num_q_heads, const int32_t
  * x of the call that fall into one block (positions as for pkv_append) set, for
  * each KV head, for K and for V by itself:
  *   e  = max(e_old, the smallest e' in [-126, 121] with |x| <= 127 * 2^e' for all of them),
- *        without e_old if the block holds no tokens;
+ *        without e_old if the block keeps no tokens;
  *   c  = round-to-even(x / 2^e) for the new rows,
- *   c' = round-to-even(c * 2^(e_old - e)) for the codes of the tokens it holds.
+ *   c' = round-to-even(c * 2^(e_old - e)) for the codes of the tokens it keeps.
  * held_lens[r]: the tokens that request r holds before the call: slots at
  * positions below it keep their values (but for that rounding) unless the call
- * writes them, and a block with such slots holds tokens.  What other slots of a
- * written block hold is not kept.  A new conversation, or a page taken anew, has
- * held_lens 0 there: what an earlier owner left has no say.
+ * writes them, and a block with a slot that does keeps tokens.  What other slots of
+ * a written block hold is not kept.  What an earlier owner of a page left has no say
+ * where the request holds nothing there, nor where the call writes all that it holds
+ * there (dropped blocks that a step recomputes on fresh pages).
  * Magnitudes above 127 * 2^121 count as that, infinities among them; NaN counts
  * as 0; infinities and NaN set PKV_DEVERR_VALUE.
  * Precondition: tokens of one block follow one another in the batch (as ascending

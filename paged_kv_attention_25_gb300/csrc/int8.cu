@@ -1,7 +1,7 @@
 // The 8-bit cache with a power of two for each (block, KV head): the quantising
 // write, and the reading back of rows (of pools of any type).
 //
-//   e  = max(e_old if the block holds tokens, the smallest e' >= -126 with max |x| <= 127 2^e')
+//   e  = max(e_old if the block keeps tokens, the smallest e' >= -126 with max |x| <= 127 2^e')
 //   c  = rne(x / 2^e) for new rows x,   rne(c 2^(e_old - e)) for held codes
 //
 // A power of two instead of max|x| / 127: codes use six to seven bits, but x / 2^e
@@ -28,7 +28,7 @@ constexpr uint32_t kTop = 0x7f7eu;   // bf16 bits of 127 * 2^121
 
 // The new tokens of one block: those that follow one another in the batch.
 struct Run {
-  int pb, held;         // block; the slots that held tokens before the call, as bits
+  int pb, held;         // block; the slots that held tokens before the call and keep them, as bits
   int tok[kBlockSize];  // the new row of each slot (the last of several), -1: none
 };
 
@@ -107,17 +107,19 @@ __global__ void __launch_bounds__(kThreads, 4) append_int8_kernel(
     Run& run = s_run[at];
     if (lane < kBlockSize) run.tok[lane] = -1;
     __syncwarp();
+    uint32_t written = 0;
     for (int base = t;;) {
       const uint32_t out = __ballot_sync(0xffffffffu, base + lane >= end || (p >> 4) != (p0 >> 4));
       const int n = out ? __ffs(out) - 1 : 32;
       if (lane < n) atomicMax(&run.tok[p & 15], base + lane);
+      written |= __reduce_or_sync(0xffffffffu, lane < n ? 1u << (p & 15) : 0u);
       if (n < 32) break;
       base += 32;
       p = lane < num_tokens - base ? __ldg(pos + base + lane) : -1;
     }
     if (lane == 0) {
       run.pb = pb;
-      run.held = static_cast<int>(low_bits(min(held, kBlockSize)));
+      run.held = static_cast<int>(low_bits(min(held, kBlockSize)) & ~written);
     }
   }
   __syncthreads();
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_int8_kernel(
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int slot = s * kSlots + sub;
-        if (((held >> slot) & 1u) && run.tok[slot] < 0) {
+        if ((held >> slot) & 1u) {
           uint4* c = reinterpret_cast<uint4*>(codes + slot * D);
           const uint4 v = *c;
           *c = make_uint4(rescale_int8x4(v.x, down), rescale_int8x4(v.y, down), rescale_int8x4(v.z, down),
