@@ -515,9 +515,9 @@ int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int
  * Scores are fp32 as for pkv_tree_attn (int8 pools: bf16 operands), tanh and the
  * bias are taken in fp32; P is rounded to bf16 (f16 for FP8 pools), O once.  Results
  * do not depend on timing.  Keys that a token does not see do not reach it, be
- * their values infinite or NaN.  Blocks behind the prefix and before the first key
- * that a token of the request sees, or behind the last one, are not read, and their
- * table entries may hold anything (pages freed behind a window; blocks between the
+ * their values infinite or NaN.  Of the blocks behind the prefix those before the
+ * first and behind the last key that a token of the request sees there are not read, and
+ * their table entries may hold anything (pages freed behind a window; blocks between the
  * keys of tokens that lie far apart may be read).  A request of many tokens and
  * others of few may share a call.
  * Invalid block ids are flagged where they would be read and their keys seen by

@@ -641,7 +641,7 @@ __device__ __forceinline__ RowsReq rows_req(const ScoreArgs& a, int r) {
     lo = q.ctx;
     hi = -1;
     for (int t = q.t0; t < q.t0 + q.n; ++t) {
-      const KeySpan s = key_span(a, t, q.ctx);
+      const KeySpan s = key_span(a, t, q.prefix, q.ctx);
       lo = min(lo, s.lo);
       hi = max(hi, s.hi);
     }
@@ -657,7 +657,7 @@ __device__ __forceinline__ RowsReq rows_req_warp(const ScoreArgs& a, int r, int 
     lo = q.ctx;
     hi = -1;
     for (int t = lane; t < q.n; t += 32) {
-      const KeySpan s = key_span(a, q.t0 + t, q.ctx);
+      const KeySpan s = key_span(a, q.t0 + t, q.prefix, q.ctx);
       lo = min(lo, s.lo);
       hi = max(hi, s.hi);
     }
@@ -842,7 +842,7 @@ score_rows_kernel(const ScoreArgs a) {
              (static_cast<int64_t>(rq.t0 + f / G) * t.num_q_heads + g * G + f % G) * D;
     };
     const int ta = tok_of(ra), tb = tok_of(rb);
-    const KeySpan sa = key_span(a, ta, rq.ctx), sb = key_span(a, tb, rq.ctx);
+    const KeySpan sa = key_span(a, ta, rq.prefix, rq.ctx), sb = key_span(a, tb, rq.prefix, rq.ctx);
     Modify mod{a.base, cap || a.slopes != nullptr, a.cap_out, a.slopes != nullptr, 0.f, 0.f,
                max(__ldg(t.positions + ta), -1), max(__ldg(t.positions + tb), -1)};
     if (mod.slopes) {
@@ -958,7 +958,7 @@ score_rows_kernel(const ScoreArgs a) {
       return static_cast<int64_t>(rq.t0 + f / G) * t.num_q_heads + g * G + f % G;
     };
     auto add_odd = [&](int rr) {
-      score_add_odd<D, KIND == kPoolFp8>(a, rq, bt_row, g, key_span(a, tok_of(rr), rq.ctx), KeySpan{lo_all, hi_all}, b0, b1,
+      score_add_odd<D, KIND == kPoolFp8>(a, rq, bt_row, g, key_span(a, tok_of(rr), rq.prefix, rq.ctx), KeySpan{lo_all, hi_all}, b0, b1,
                                          static_cast<uint16_t*>(t.o) + out_row(rr) * D,
                                          whole ? nullptr : t.part_o + (slot + rr) * D, lane);
     };

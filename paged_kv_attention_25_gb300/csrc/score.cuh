@@ -49,19 +49,20 @@ struct ScoreArgs {
   ScorePlan plan;             // tiles form
 };
 
-// The keys behind the prefix that a token sees: [lo, hi].  None: [ctx, -1], so that a token without keys (a document that
-// begins behind it, a position in front of the sequence) does not widen what the others of its tile see.
+// The keys [lo, hi] that a token sees beside the prefix (they may begin inside it).  None behind it: [ctx, -1], so that a
+// token without such keys (a document that begins behind it, a position in the prefix or in front of the sequence) does
+// not widen what the others of its tile see.
 struct KeySpan {
   int lo, hi;
 };
-__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int pos, int first, int ctx) {
+__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int pos, int first, int prefix, int ctx) {
   const int p = max(pos, -1);
   KeySpan s{max(first, 0), min(p, ctx - 1)};
   if (a.window > 0) s.lo = max(s.lo, p - a.window + 1);
-  return s.hi < s.lo ? KeySpan{ctx, -1} : s;
+  return s.hi < max(s.lo, prefix) ? KeySpan{ctx, -1} : s;
 }
-__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int ctx) {
-  return key_span(a, __ldg(a.t.positions + t), a.first_keys ? __ldg(a.first_keys + t) : 0, ctx);
+__device__ __forceinline__ KeySpan key_span(const ScoreArgs& a, int t, int prefix, int ctx) {
+  return key_span(a, __ldg(a.t.positions + t), a.first_keys ? __ldg(a.first_keys + t) : 0, prefix, ctx);
 }
 // Keys [key0, key0 + 32) that a token sees, as bits.
 __device__ __forceinline__ uint32_t span_bits(int prefix, KeySpan s, int key0) {

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kPlanThreads) score_plan_kernel(const ScoreArg
 #pragma unroll 4
     for (int x = sub; x < nt; x += kPlanLanes) {
       const int p = __ldg(a.t.positions + it.tok0 + x);
-      const KeySpan s = key_span(a, p, a.first_keys ? __ldg(a.first_keys + it.tok0 + x) : 0, q.ctx);
+      const KeySpan s = key_span(a, p, a.first_keys ? __ldg(a.first_keys + it.tok0 + x) : 0, q.prefix, q.ctx);
       it.any_lo = min(it.any_lo, s.lo);
       it.all_lo = max(it.all_lo, s.lo);
       it.any_hi = max(it.any_hi, s.hi);
@@ -1231,7 +1231,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         if (any_missing && rel > 0 && (rel & 3) < step) missing = missing_of(rel >> 2);
         const uint32_t gone = (missing >> ((rel & 3) * kBlkPerTile)) & 0xffu;
         const bool masked = gone != 0 || !seen_whole(sg, key0);
-        const KeySpan span = masked ? key_span(sa, raw_pos, raw_first, sg.ctx) : KeySpan{0, -1};
+        const KeySpan span = masked ? key_span(sa, raw_pos, raw_first, sg.prefix, sg.ctx) : KeySpan{0, -1};
         if (!(ok = mbar_wait_warp(&bars[B::kS + X], sc & 1, s_abort, a.wait_ns))) break;
         ++sc;
         tc_fence_after();
@@ -1482,7 +1482,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
       if (!(ok = mbar_wait_warp(&bars[B::kVDone + r % kSegRing], (r / kSegRing) & 1, s_abort, a.wait_ns))) break;
       const int odd = s_odd[r % kSegRing];
       if (odd && valid)
-        add_odd<D, F8>(sa, sg, key_span(sa, raw_pos, raw_first, sg.ctx), s_oddl + (r % kSegRing) * kOddMost, odd,
+        add_odd<D, F8>(sa, sg, key_span(sa, raw_pos, raw_first, sg.prefix, sg.ctx), s_oddl + (r % kSegRing) * kOddMost, odd,
                        static_cast<uint16_t*>(a.o) + orow * D, whole ? nullptr : a.part_o + prow * D);
     }
     if (!ok) {

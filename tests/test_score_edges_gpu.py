@@ -266,3 +266,12 @@ def test_rows_read_back_with_exponents_outside_their_range(d):
         want = values(pool, which).transpose(0, 2, 1, 3).reshape(80, 3, d)
         assert np.array_equal(got.double().cpu().numpy(), want)
     assert pkv.pkv_check_device_errors(pool) == 0
+
+
+@FORMS
+@TYPES
+def test_tokens_inside_the_prefix_do_not_widen_what_is_read(dtype, form):
+    """A window or document that lies inside the prefix adds nothing to it, and no blocks between it and the others' keys."""
+    c = forced(Case(124, [(900, [200, 880, 299, 881]), (700, [690, 30]), (400, [150, 100])], 8, 2, 64, dtype, window=30,
+                    prefix=[300, 45, 200]), form)
+    check_unseen_ids(c, 70)
