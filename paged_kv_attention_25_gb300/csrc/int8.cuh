@@ -22,7 +22,8 @@ __device__ __forceinline__ uint32_t exp_bf16x2(int e) { return static_cast<uint3
 // 2^-133 for all eight bits (subnormal to 127, then the first binade, whose step is
 // the same).  With uu = c + 128 the fused uu * 2^-133 * 2^127 - 128 * 2^-6 is exact.
 // Three integer instructions a word; taking 128 + (low bits) and the sign apart, as
-// exponents in place, takes six and decoded 32 x 48k tokens in 167 us, not %s.
+// exponents in place, takes six: 10 requests of 1 to 733 new tokens over int8, 64 / 8 heads,
+// on tiles 294 us against 280 (both before the widening's later steps); decoding took the same time.
 constexpr int kWidenShift = 6;
 __device__ __forceinline__ void int8x4_to_bf16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   const uint32_t x = codes ^ 0x80808080u;

@@ -11,7 +11,9 @@
 // Int8 pools: codes are widened to bf16 (exact, seven bits), and the block's
 // powers of two go to the scores and to P: 2^e_K on 16 x 16 scores and 2^e_V on
 // as many p are a sixteenth of the products that scaling the operands would take,
-// and neither rounds.  P is rounded to bf16 (8 bits, as for bf16 pools).
+// and neither rounds while p 2^(e_V + 6) is a normal bf16 number (below, values of V
+// under 2^-100 or so, a key's share of O is off by 2^-133 at most).  P is rounded to
+// bf16 (8 bits, as for bf16 pools).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -240,7 +242,7 @@ struct ScoreTile : RowTile<D, KIND != kPoolBf16> {
         if constexpr (KIND == kPoolFp8) {
           p[n][2 * t] = pack_f16x2(s[n][t][0], s[n][t][1]);
           p[n][2 * t + 1] = pack_f16x2(s[n][t][2], s[n][t][3]);
-        } else if constexpr (KIND == kPoolInt8) {   // (a power of two: P is rounded as without it)
+        } else if constexpr (KIND == kPoolInt8) {   // (a power of two: P is rounded as without it, see above)
           p[n][2 * t] = pack_bf16x2(s[n][t][0] * f[n].value, s[n][t][1] * f[n].value);
           p[n][2 * t + 1] = pack_bf16x2(s[n][t][2] * f[n].value, s[n][t][3] * f[n].value);
         } else {

@@ -891,7 +891,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
           const uint32_t need = blocks_needed(sg, tile_at(j, sg.pre_tiles, sg.gap) * kNK);
           return lane < kBlkPerTile && ((need >> lane) & 1u) && pb >= 0 ? pb * Hkv + sg.g : -1;
         };
-        // V blocks that some row does not see whole: cleared of what they hold behind
+        // bf16 V blocks that some row does not see whole: cleared of what they hold behind
         // the context, and of elements that are not finite, which are noted; blocks that
         // are not there (copied: have) become zero.  A lane has the 16-byte pieces
         // lane, lane + 32, ... of a block's rows, eight (four) loads under way.
@@ -924,7 +924,7 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
                 continue;
               }
               // An exponent of ones carries into the sign's place.
-              constexpr uint32_t kExp = F8 ? 0x7c007c00u : 0x7f807f80u, kOne = F8 ? 0x04000400u : 0x00800080u;
+              constexpr uint32_t kExp = 0x7f807f80u, kOne = 0x00800080u;
               const uint32_t bad = (((v[i].x & kExp) + kOne) | ((v[i].y & kExp) + kOne) | ((v[i].z & kExp) + kOne) |
                                     ((v[i].w & kExp) + kOne)) & 0x80008000u;
               if (!bad) continue;
@@ -940,38 +940,38 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
             }
           }
         };
-          for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
-            const int y = block_chunk(j);
-            const int st = cnt % nst;
-            const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
-            if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
-            // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
-            if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
-            const bool clean = !kCodes && !is_k && dirty_blocks(j, have) != 0;
-            uint64_t* bar = &bars[(clean || kCodes ? bar_landed : bar_full) + st];
-            if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D * (kCodes ? 1 : 2)));
-            __syncwarp();
-            uint8_t* stage = stages + st * S::kKV;
-            if (y >= 0) {
-              if constexpr (kCodes) tma_load_2d(stage + lane * S::kBlkBytes + S::kBlkBytes / 2, tm, 0, y * kBlockSize, bar);
-              else if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
-              else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
-            }
-            if (clean) {
-              const uint32_t par = (landed_par >> st) & 1u;
-              landed_par ^= 1u << st;
-              if (!mbar_wait_warp(bar, par, s_abort, a.wait_ns)) {
-                (void)mbar_wait(bar, par, nullptr, a.wait_ns);   // let this tile's copies land
-                ok = false;
-                break;
-              }
-              clean_v(stage, j, have);
-              fence_proxy_async_smem();   // read by the tensor cores
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars[bar_full + st]);
-            }
+        for (int j = sg.kt0; j < sg.kt1; ++j, ++cnt) {
+          const int y = block_chunk(j);
+          const int st = cnt % nst;
+          const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
+          if (!(ok = mbar_wait_warp(&bars[bar_empty + st], ((cnt / nst) & 1) ^ 1, s_abort, a.wait_ns))) break;
+          // Test hook: CTA 0 never issues its first K tile, so that the issuer's bounded wait for it runs out.
+          if (a.withhold == 2 && is_k && cnt == 0 && blockIdx.x == 0) continue;
+          const bool clean = !kCodes && !is_k && dirty_blocks(j, have) != 0;
+          uint64_t* bar = &bars[(clean || kCodes ? bar_landed : bar_full) + st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(have)) * (kBlockSize * D * (kCodes ? 1 : 2)));
+          __syncwarp();
+          uint8_t* stage = stages + st * S::kKV;
+          if (y >= 0) {
+            if constexpr (kCodes) tma_load_2d(stage + lane * S::kBlkBytes + S::kBlkBytes / 2, tm, 0, y * kBlockSize, bar);
+            else if constexpr (D == 128) tma_load_4d(stage + lane * S::kBlkBytes, tm, 0, 0, 0, 2 * y, bar);
+            else tma_load_2d(stage + lane * S::kBlkBytes, tm, 0, y * kBlockSize, bar);
           }
-          if (!ok) break;
+          if (clean) {
+            const uint32_t par = (landed_par >> st) & 1u;
+            landed_par ^= 1u << st;
+            if (!mbar_wait_warp(bar, par, s_abort, a.wait_ns)) {
+              (void)mbar_wait(bar, par, nullptr, a.wait_ns);   // let this tile's copies land
+              ok = false;
+              break;
+            }
+            clean_v(stage, j, have);
+            fence_proxy_async_smem();   // read by the tensor cores
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[bar_full + st]);
+          }
+        }
+        if (!ok) break;
         if constexpr (!kCodes) {
           __syncwarp();   // the notes are written
           if (!is_k && lane == 0) mbar_arrive(&bars[B::kVDone + r % kSegRing]);
