@@ -148,20 +148,6 @@ __device__ __forceinline__ uint32_t blocks_whole(const Seg& s, int key0) {
          (blocks_below(s.all_hi - key0 + 1) & ~blocks_below(s.all_lo - key0 + kBlockSize - 1));
 }
 
-// Whether a block of the segment's key tiles that some row sees is not there.
-__device__ __noinline__ bool any_seen_missing(const TreeArgs& a, const Seg& s, int lane) {
-  const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
-  const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
-  bool gone = false;
-  for (int x = s.kt0 * kBlkPerTile + lane; x < s.kt1 * kBlkPerTile; x += 32) {
-    const int tile = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap), b = tile * kBlkPerTile + x % kBlkPerTile;
-    if (b >= nblk || !((blocks_needed(s, tile * kNK) >> (x % kBlkPerTile)) & 1u)) continue;
-    const int pb = __ldg(bt_row + b);
-    gone |= pb < 0 || pb >= a.pool.num_blocks;
-  }
-  return __any_sync(0xffffffffu, gone);
-}
-
 // Walks a CTA's share of the line.  Key tile k of a group that begins at unit 0
 // belongs to the worker that holds unit k * cost; the group's fixed units follow
 // its last tile.
@@ -1127,18 +1113,22 @@ score_tc_kernel(const ScoreArgs sa, const __grid_constant__ CUtensorMap tmap_k, 
         if (more) {
           if (cut.count > 0 && lane == 0) a.cuts[blockIdx.x] = cut;
           // Blocks that some row sees and that are not there: flagged here, and only then looked for by the softmax warps.
-          // (The table may hold anything for the others, pages freed behind a window for instance.  A first look at all
-          // ids, many loads under way, keeps what rows see out of its loop, which took 10 of 221 us of the int8 new turns.)
+          // The segment's blocks of the prefix, and those behind it between the first and the last key seen: the table may
+          // hold anything for the others, pages freed behind a window for instance.  (No branch on what a load brings, so
+          // that several are under way: with one the int8 new turns took 221 us, not 212.)
           const int32_t* bt_row = a.block_tables + static_cast<int64_t>(s.req) * a.max_blocks;
-          const int nblk = (s.ctx + kBlockSize - 1) / kBlockSize;
           bool gone = false;
-          for (int x = s.kt0 * kBlkPerTile + lane; x < s.kt1 * kBlkPerTile; x += 32) {
-            const int b = tile_at(x / kBlkPerTile, s.pre_tiles, s.gap) * kBlkPerTile + x % kBlkPerTile;
-            if (b >= nblk) continue;
-            const int pb = __ldg(bt_row + b);
-            gone |= pb < 0 || pb >= a.pool.num_blocks;
-          }
-          if (__any_sync(0xffffffffu, gone) && any_seen_missing(a, s, lane)) {
+          auto look = [&](int b0, int b1) {
+            for (int b = b0 + lane; b < b1; b += 32) {
+              const int pb = __ldg(bt_row + b);
+              gone |= pb < 0 || pb >= a.pool.num_blocks;
+            }
+          };
+          const int pblk = (s.prefix + kBlockSize - 1) / kBlockSize, t0 = s.kt0 * kBlkPerTile, t1 = s.kt1 * kBlkPerTile;
+          const int skip = s.gap * kBlkPerTile;   // (0 if the prefix's last tile holds keys seen behind it)
+          look(t0, min(t1, pblk));
+          look(max(max(t0 + skip, pblk), s.any_lo / kBlockSize), min(t1 + skip, (s.any_hi + kBlockSize) / kBlockSize));
+          if (__any_sync(0xffffffffu, gone)) {
             s.flags |= kSegMissing;
             if (lane == 0) atomicOr(a.pool.err, PKV_DEVERR_BLOCK_ID);
           }
