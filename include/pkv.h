@@ -513,13 +513,14 @@ int pkv_compact(pkv_pool* pool, const int32_t* block_tables, int max_blocks, int
  *   arrays, or NULL (0; 0; none).  0 <= prefix <= ctx <= max_blocks * 16; negative
  *   first_keys count as 0.  Positions and first_keys of a request in any order.
  * Scores are fp32 as for pkv_tree_attn (int8 pools: bf16 operands), tanh and the
- * bias are taken in fp32; P is rounded to bf16 (f16 for FP8 pools), O once.  Results
- * do not depend on timing.  Keys that a token does not see do not reach it, be
- * their values infinite or NaN.  Of the blocks behind the prefix those before the
- * first and behind the last key that a token of the request sees there are not read, and
- * their table entries may hold anything (pages freed behind a window; blocks between the
- * keys of tokens that lie far apart may be read).  A request of many tokens and
- * others of few may share a call.
+ * bias are taken in fp32; P is rounded to bf16 (f16 for FP8 pools), O once.  (Int8
+ * pools: where values are as small as 2^-100, a key's share of O may be off by 2^-133
+ * besides.)  Results do not depend on timing.  Keys that a token does not see do
+ * not reach it, be their values infinite or NaN.  Of the blocks behind the prefix
+ * those before the first and behind the last key that a token of the request sees
+ * there are not read, and their table entries may hold anything (pages freed behind
+ * a window; blocks between the keys of tokens that lie far apart may be read).  A
+ * request of many tokens and others of few may share a call.
  * Invalid block ids are flagged where they would be read and their keys seen by
  * nobody; lengths out of range are flagged and cut; positions outside the table
  * are flagged (below 0: the prefix is seen; beyond: all keys that the masks leave).
@@ -585,7 +586,7 @@ int pkv_append_int8(pkv_pool* pool, const int32_t* block_tables, int max_blocks,
  * [cu_lens[r], cu_lens[r + 1])) the K and V rows at positions[t], all KV heads, as
  *   k_out, v_out [num_tokens][num_kv_heads][head_dim] bf16 (16-byte aligned)
  * from a pool of any type: bf16 rows as they are, int8 values exactly, FP8 codes
- * times their scale, rounded once.  Positions in any order, repeated or not.  A
+ * times their scale in fp32, then rounded to bf16.  Positions in any order, repeated or not.  A
  * position or block id out of range is flagged and its rows are zero; rows of
  * tokens that belong to no request are left as they are.  All arrays device; can
  * be captured, runs on `stream` alone.
@@ -625,8 +626,9 @@ int pkv_swap_in(pkv_pool* pool, const int32_t* block_ids, int n, const void* hos
  * host_buf), so it takes no SMs and overlaps whatever the caller queues next.
  * The blocks land in the pool at the start of the pool's next call that reads
  * or writes it (pkv_append, pkv_paged_attn, pkv_tree_attn, pkv_sparse_attn,
- * pkv_summarize, pkv_fork, pkv_copy_blocks, pkv_compact, pkv_swap_out,
- * pkv_swap_in, another pkv_swap_in_ahead) or at pkv_swap_in_finish: that
+ * pkv_score_attn, pkv_read_rows, pkv_summarize, pkv_fork, pkv_copy_blocks,
+ * pkv_compact, pkv_swap_out, pkv_swap_in, another pkv_swap_in_ahead) or at
+ * pkv_swap_in_finish: that
  * call's stream waits for the transfer, and a kernel scatters the staged
  * blocks into block_ids.  A replayed graph lands nothing but what was both
  * started and landed in its capture, and a call that is being captured is
@@ -700,6 +702,8 @@ int pkv_copy_to_host(void* host_dst, const void* src, size_t bytes, void* stream
  * PKV_ENOMEM if the step's conversations cannot fit in the pool even after
  * evicting every other conversation; on an error the manager is unchanged.
  * pkv_cache_release forgets a conversation and frees its blocks and slots.
+ * Int8 pools refuse swaps: over such a pool use cpu_blocks = 0 (blocks are dropped
+ * and recomputed, nothing is swapped).
  */
 typedef struct pkv_cache pkv_cache;
 int pkv_cache_create(int gpu_blocks, int cpu_blocks, float token_cost, pkv_cache** out);

@@ -63,8 +63,9 @@ __device__ __forceinline__ uint32_t rescale_int8x4(uint32_t c, float f) {
 // one KV head, K or V: up to 16 x D values in registers, their maximum, the codes.
 // The y grid shares out (head, K or V).  Bound by HBM for prompts, by the chain of
 // dependent loads (request, table, exponent) for a decode step.  28,870 tokens of 8
-// heads, D = 128: 40 us (4.5 TB/s); four CTAs an SM spill a few registers, but two
-// took 47, and reading the rows twice (the second time out of L1) with six 43.
+// heads, D = 128: 31.7 us in a row of such launches (5.6 TB/s); by itself, L2 flushed, from
+// event to event, 40; four CTAs an SM spill a few registers, but two took 47 so, and
+// reading the rows twice (the second time out of L1) with six 43.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) append_int8_kernel(
     const PoolView pool, uint8_t* kp, uint8_t* vp, const int32_t* __restrict__ bt, int max_blocks, int num_reqs,
@@ -202,9 +203,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_int8_kernel(
 
 // Rows of a cache as bf16: a thread takes 16 values of a token's K or V row at a
 // time, kBatch loads under way.  Bound by HBM (a row's codes are a whole line): 52
-// thousand int8 tokens of 8 heads, D = 128, 58 us.  Small CTAs and few loads a
+// thousand int8 tokens of 8 heads, D = 128, 54 us in a row of such launches (6.0 TB/s); by
+// itself, L2 flushed, from event to event, 58 to 60.  Small CTAs and few loads a
 // thread, so that an SM has 16 CTAs at different stages: with 256 threads, 16 tokens
-// and 4 loads it was 68 us.  A row's 32 bytes go out as one store: as two, 74 us.
+// and 4 loads it was 68 us so.  A row's 32 bytes go out as one store: as two, 74 us.
 constexpr int kBatch = 2, kReadTokens = 8, kReadThreads = 128;
 template <int KIND>   // 0: bf16, 1: e4m3, 2: int8
 __global__ void __launch_bounds__(kReadThreads, 2048 / kReadThreads) read_rows_kernel(const PoolView pool, const int32_t* __restrict__ bt,

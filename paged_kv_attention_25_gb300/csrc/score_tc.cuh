@@ -27,8 +27,9 @@
 // five paired operations for two scores, while every score of the warp's rows stays
 // below half the cap; otherwise by tanh_small and tanh_large.  It is monotonic:
 // without a bias the raw products' maximum gives the scores', and the last operation
-// subtracts it (4 prompts of 1.8 to 5 thousand tokens, 64 / 8 heads, D = 128: 778 us;
-// 912 with scores written back to TMEM first, as masked or biased ones still are).
+// subtracts it (4 prompts of 1.8 to 5 thousand tokens, 64 / 8 heads, D = 128: 769 us;
+// 912 with scores written back to TMEM first, as masked or biased ones still are; scores on
+// both sides of half the cap 1,700).
 //
 // Pools of codes: they land in the upper half of each block's lines, and four more warps widen
 // them in place, two for K and two for V (int8: to bf16 times the block's power of
@@ -53,7 +54,7 @@ namespace pkv {
 namespace {
 
 // What becomes of scores: a kernel for each, as code that does not run takes room in the instruction cache, too (the
-// capped prompts of the header 791 us with the code for a bias beside theirs, biased ones 900 us, now 823).
+// capped prompts of the header 791 us with the code for a bias beside theirs, biased ones 900 us, 823 by itself).
 enum { kPlain, kCapped, kBiased };   // kBiased: capped or not
 constexpr int kTeam = 2;   // codes: warps that widen K, and V
 // Registers of a CTA for codes, of 128 each at the launch.  Widening wants more (104: 5 % slower, 88: 20 %), and four
